@@ -76,8 +76,13 @@ const char *moe_last_cuda_error(void);
 /* Quantisation formats of expert weights (canonical block layouts). */
 enum moe_qtype {
     MOE_Q8_0 = 0,  /* 34 B per 32 weights: fp16 d (little-endian), int8 q[32]; w = d*q */
-    MOE_Q4_SM = 1  /* 20 B per 32 weights: fp16 d, fp16 m, 16 B codes (byte i: q[2i] low
+    MOE_Q4_SM = 1, /* 20 B per 32 weights: fp16 d, fp16 m, 16 B codes (byte i: q[2i] low
                       nibble, q[2i+1] high nibble); w = d*q + m */
+    MOE_MXFP4 = 2  /* microscaled 4-bit floating point, 17 B per 32 weights: E8M0 scale byte s,
+                      16 B of E2M1 codes (nibbles as above; bit 3 sign, magnitudes 0, 0.5, 1,
+                      1.5, 2, 3, 4, 6); w = 2^(s-127) * e2m1(q), s = 255: NaN.  Served by slot
+                      images, host-managed pools and the moe_mx4_* calls below; moe_expert_ffn*
+                      and the stacks refuse it */
 };
 /* Activation element types. */
 enum moe_xtype { MOE_F32 = 0, MOE_BF16 = 1 };
@@ -124,6 +129,8 @@ int moe_router_topk_threshold(const void *x, int xtype, int T, int H, const uint
 /*
  * moe_slot_image_bytes — size of one expert's slot image (gate + up + down).
  * It equals the canonical size: 2*F*H/32*B + H*F/32*B with B = 34 (q8_0) or 20 (4-bit).
+ * MOE_MXFP4: (ceil(F/64) * ceil(H/128) + ceil(H/128) * ceil(F/128)) * 8704 bytes, the
+ * canonical size (B = 17) when H and F are multiples of 128.
  * H and F must be multiples of 32.
  */
 int moe_slot_image_bytes(int qtype, int H, int F, size_t *bytes_out);
@@ -141,6 +148,12 @@ int moe_slot_image_bytes(int qtype, int H, int F, size_t *bytes_out);
  * scale entries (fp16 d, or fp16 d and m), row l's entry at position 4 (l % 8) + l / 8.
  * So any K range of a tile is one contiguous run of bytes.  The image has the canonical
  * size and holds the same values; moe_unpack_expert inverts it exactly.
+ * MOE_MXFP4 images hold two matrices, gate/up then down, as 128-row tiles, each a run of
+ * 8704-byte tile blocks, one per 128 columns along K: 128 rows of 64 code bytes, row r's 16-byte
+ * piece c (columns 32c .. 32c+31 of the block) at 64 r + 16 (c ^ ((r / 2) % 4)), then 512 scale
+ * bytes, the scale of (r, piece c) at 8192 + 16 (r % 32) + 4 (r / 32) + c.  Tile g of gate/up
+ * holds gate rows 64g .. 64g+63 and then up rows 64g .. 64g+63; rows past F or H and columns past
+ * K are zero (codes and scales).  This is the order in which the tensor cores read both.
  */
 int moe_pack_expert(int qtype, int H, int F, const void *gate_aos, const void *up_aos,
                     const void *down_aos, void *slot_image_dst, size_t *slot_bytes_out);
@@ -404,6 +417,97 @@ int moe_combine(const float *partial, int T, int k, int H, const float *extra, f
  */
 int moe_combine_rmsnorm(const float *partial, int T, int k, int H, const float *extra, float *y,
                         float *xn, float eps, moe_stream_t s);
+
+/* ------------------------------------------ microscaled 4-bit experts (MXFP4) */
+
+/*
+ * The MXFP4 operators: activations and weights to 4 bits, the routed experts' products with
+ * both sides in 4 bits (prompts), and a whole MoE layer over 4-bit experts with activations kept
+ * at fp32 accuracy (decode).  Page 5, section 1.2, keeps quantised blocks as they are on the GPU
+ * and multiplies them there; the format is the Open Compute microscaling one (32 elements of E2M1
+ * under one E8M0 scale).
+ *
+ * moe_mx4_quantize — rows of x to MXFP4.  Per 32 columns: s = max(0, floor(log2 max|x|) - 2 + 127),
+ * codes = x / 2^(s-127) rounded to the nearest E2M1 value (ties to the even code, beyond 6 to 6);
+ * a block of zeros has s = 0; a block with an infinity or a NaN has s = 255 (NaN) and codes 0.
+ *   x      device [rows][ld], xtype MOE_F32 or MOE_BF16, ld >= cols elements between rows
+ *          (element-aligned; 16-byte aligned rows take wide loads).
+ *   codes  device [rows][cols/2] out, byte i of a row: column 2i low nibble, 2i+1 high nibble.
+ *   scales device [rows][cols/32] out.
+ * cols a positive multiple of 32; rows >= 0 (0: no-op); codes 16-byte aligned.
+ *
+ * moe_mx4_dequantize — the inverse: y[r][c] = 2^(s-127) * e2m1 (device [rows][ld], ytype; exact in
+ * both types).  Columns cols .. ld-1 of y are left as they were.
+ */
+int moe_mx4_quantize(const void *x, int xtype, int rows, int cols, size_t ld, uint8_t *codes,
+                     uint8_t *scales, moe_stream_t s);
+int moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int rows, int cols, void *y, int ytype,
+                       size_t ld, moe_stream_t s);
+
+/*
+ * moe_mx4_quantize_experts — n experts' weights (device gate, up [n][F][H] and down [n][H][F],
+ * contiguous, wtype MOE_F32 or MOE_BF16) to MOE_MXFP4 slot images by the rule of moe_mx4_quantize:
+ * expert i to slot slots[i] of pool (device int32 [n], each in [0, n_slots), no slot twice; NULL:
+ * slot i).  A slot out of range is recorded in the device status word and skipped.  pool and
+ * slot_bytes are 256-byte aligned, slot_bytes >= moe_slot_image_bytes; every byte of an image is
+ * written, bytes between images are left.
+ * moe_mx4_dequantize_experts — the inverse, of n slots into gate, up, down (wtype).
+ */
+int moe_mx4_quantize_experts(const void *gate, const void *up, const void *down, int wtype, int n, int H, int F,
+                             void *pool, size_t slot_bytes, const int32_t *slots, int n_slots, moe_stream_t s);
+int moe_mx4_dequantize_experts(const void *pool, size_t slot_bytes, const int32_t *slots, int n_slots, int n,
+                               int H, int F, void *gate, void *up, void *down, int wtype, moe_stream_t s);
+
+/*
+ * moe_mx4_expert_gateup — the routed experts' first product on 4-bit tokens: for each route
+ *   (t, j), e = ids[t][j]:   h[t*k + j][:] = silu(Wg_e x_t) * (Wu_e x_t)
+ * moe_mx4_expert_down — their second one, on 4-bit h rows:
+ *   partial[t][j][:] = weights[t][j] * (Wd_e h[t*k + j])
+ * Between them a caller quantises h (moe_mx4_quantize, T*k rows of F); moe_combine sums partial.
+ * Products of 4-bit operands are exact, sums are fp32, h is rounded once to htype.
+ *   x_codes, x_scales  device, moe_mx4_quantize output of T rows of H; h_codes, h_scales: T*k rows
+ *                      of F.  Both code arrays 16-byte aligned.
+ *   ids                device [T][k]; any expert any number of times; -1: no route, its row of h or
+ *                      partial is left untouched; other ids outside [0, E), and slots outside
+ *                      [0, n_slots), are recorded in the device status word and skipped.
+ *   weights            device [T][k].
+ *   d_slot_table, n_slots, pool, slot_bytes  as in moe_expert_ffn, MOE_MXFP4 images, pool and
+ *                      slot_bytes 256-byte aligned.
+ *   h                  device [T*k][F] out, htype MOE_F32 or MOE_BF16; partial device [T][k][H] fp32.
+ *   workspace          device, moe_mx4_expert_workspace() bytes, 256-byte aligned; needs no
+ *                      initial contents; one per call in flight.
+ * H, F multiples of 32; T >= 0 (0: no-op), E <= MOE_MAX_E, k <= MOE_MAX_K, T*k <= 2^24.
+ */
+int moe_mx4_expert_workspace(int T, int H, int F, int E, int k, size_t *bytes);
+int moe_mx4_expert_gateup(const uint8_t *x_codes, const uint8_t *x_scales, int T, int H, int F, int E, int k,
+                          const int32_t *ids, const int32_t *d_slot_table, int n_slots, const void *pool,
+                          size_t slot_bytes, void *h, int htype, void *workspace, size_t ws_bytes,
+                          moe_stream_t s);
+int moe_mx4_expert_down(const uint8_t *h_codes, const uint8_t *h_scales, int T, int H, int F, int E, int k,
+                        const int32_t *ids, const float *weights, const int32_t *d_slot_table, int n_slots,
+                        const void *pool, size_t slot_bytes, float *partial, void *workspace,
+                        size_t ws_bytes, moe_stream_t s);
+
+/*
+ * moe_mx4_layer — a whole MoE layer for a few tokens (T <= MOE_DECODE_MAX_T) over resident MXFP4
+ * experts: moe_router_topk's routing, the routed FFNs and the combine,
+ *   y[t] = extra[t] + sum_{j=0..k-1} weights[t][j] * Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),
+ * with x and h kept at fp32 accuracy (24-bit fixed point under one scale per token, per 32
+ * columns of h), summed over j in the order 0..k-1 after extra.  The same bits for the same input.
+ *   x, w_router, bias  as in moe_router_topk; extra device [T][H] fp32 or NULL; y device [T][H]
+ *                      fp32 out, may alias extra.
+ *   ids, weights       device [T][k] out, or NULL.
+ *   d_slot_table .. slot_bytes  as in moe_mx4_expert_gateup; an expert whose slot is outside
+ *                      [0, n_slots) is recorded in the device status word and its routes add nothing.
+ *   workspace          device, moe_mx4_layer_workspace() bytes, 256-byte aligned; needs no initial
+ *                      contents; one per call in flight.
+ * A token with an infinity or a NaN has NaN outputs, as has one whose h overflows.
+ */
+int moe_mx4_layer_workspace(int T, int H, int F, int E, int k, size_t *bytes);
+int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int E, int k, const uint16_t *w_router,
+                  const float *bias, const int32_t *d_slot_table, int n_slots, const void *pool,
+                  size_t slot_bytes, const float *extra, float *y, int32_t *ids, float *weights,
+                  void *workspace, size_t ws_bytes, moe_stream_t s);
 
 /* ------------------------------------------------------------ device status */
 

@@ -23,6 +23,7 @@ MOE_ERR_TIMEOUT = -5
 MOE_ERR_UNSUPPORTED = -6
 MOE_Q8_0 = 0
 MOE_Q4_SM = 1
+MOE_MXFP4 = 2
 MOE_F32 = 0
 MOE_BF16 = 1
 MOE_MAX_K = 8
@@ -41,6 +42,9 @@ EXPORTED = [
     "moe_expert_ffn_noalloc", "moe_combine_rmsnorm", "moe_cache_state_bytes", "moe_cache_plan",
     "moe_expert_ffn_fill", "moe_last_cuda_error", "moe_router_topk_threshold",
     "moe_cache_prefetch_plan", "moe_cache_prefetch_fill",
+    "moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_quantize_experts", "moe_mx4_dequantize_experts",
+    "moe_mx4_expert_workspace", "moe_mx4_expert_gateup", "moe_mx4_expert_down",
+    "moe_mx4_layer_workspace", "moe_mx4_layer",
 ]
 MOE_NOALLOC_SCRATCH_MAX = 8 << 20
 
@@ -173,6 +177,18 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "moe_set_decode_fused": ([_i], _i),
         "moe_get_decode_fused": ([], _i),
         "moe_debug_inject_fault": ([_i, _i], _i),
+        "moe_mx4_quantize": ([_vp, _i, _i, _i, _sz, _vp, _vp, _vp], _i),
+        "moe_mx4_dequantize": ([_vp, _vp, _i, _i, _vp, _i, _sz, _vp], _i),
+        "moe_mx4_quantize_experts": ([_vp, _vp, _vp, _i, _i, _i, _i, _vp, _sz, _vp, _i, _vp], _i),
+        "moe_mx4_dequantize_experts": ([_vp, _sz, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp], _i),
+        "moe_mx4_expert_workspace": ([_i, _i, _i, _i, _i, P(_sz)], _i),
+        "moe_mx4_expert_gateup": ([_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _sz, _vp, _i, _vp, _sz, _vp],
+                                  _i),
+        "moe_mx4_expert_down": ([_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _sz, _vp, _vp, _sz, _vp],
+                                _i),
+        "moe_mx4_layer_workspace": ([_i, _i, _i, _i, _i, P(_sz)], _i),
+        "moe_mx4_layer": ([_vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _sz,
+                           _vp], _i),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -431,3 +447,63 @@ def moe_stack_destroy(stack: int) -> None:
 
 def moe_debug_inject_fault(kind: int, countdown: int = 0) -> None:
     _ck("moe_debug_inject_fault", load().moe_debug_inject_fault(kind, countdown))
+
+
+def moe_mx4_quantize(x, xtype: int, rows: int, cols: int, ld: int, codes, scales, stream=None) -> None:
+    _ck("moe_mx4_quantize", load().moe_mx4_quantize(_ptr(x), xtype, rows, cols, ld, _ptr(codes), _ptr(scales),
+                                                    _stream(stream)))
+
+
+def moe_mx4_dequantize(codes, scales, rows: int, cols: int, y, ytype: int, ld: int, stream=None) -> None:
+    _ck("moe_mx4_dequantize", load().moe_mx4_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(y), ytype, ld,
+                                                        _stream(stream)))
+
+
+def moe_mx4_quantize_experts(gate, up, down, wtype: int, n: int, H: int, F: int, pool, slot_bytes: int, slots,
+                             n_slots: int, stream=None) -> None:
+    _ck("moe_mx4_quantize_experts",
+        load().moe_mx4_quantize_experts(_ptr(gate), _ptr(up), _ptr(down), wtype, n, H, F, _ptr(pool), slot_bytes,
+                                        _ptr(slots), n_slots, _stream(stream)))
+
+
+def moe_mx4_dequantize_experts(pool, slot_bytes: int, slots, n_slots: int, n: int, H: int, F: int, gate, up, down,
+                               wtype: int, stream=None) -> None:
+    _ck("moe_mx4_dequantize_experts",
+        load().moe_mx4_dequantize_experts(_ptr(pool), slot_bytes, _ptr(slots), n_slots, n, H, F, _ptr(gate),
+                                          _ptr(up), _ptr(down), wtype, _stream(stream)))
+
+
+def moe_mx4_expert_workspace(T: int, H: int, F: int, E: int, k: int) -> int:
+    out = _sz()
+    _ck("moe_mx4_expert_workspace", load().moe_mx4_expert_workspace(T, H, F, E, k, ctypes.byref(out)))
+    return out.value
+
+
+def moe_mx4_expert_gateup(x_codes, x_scales, T: int, H: int, F: int, E: int, k: int, ids, d_slot_table, n_slots: int,
+                          pool, slot_bytes: int, h, htype: int, workspace, ws_bytes: int, stream=None) -> None:
+    _ck("moe_mx4_expert_gateup",
+        load().moe_mx4_expert_gateup(_ptr(x_codes), _ptr(x_scales), T, H, F, E, k, _ptr(ids), _ptr(d_slot_table),
+                                     n_slots, _ptr(pool), slot_bytes, _ptr(h), htype, _ptr(workspace), ws_bytes,
+                                     _stream(stream)))
+
+
+def moe_mx4_expert_down(h_codes, h_scales, T: int, H: int, F: int, E: int, k: int, ids, weights, d_slot_table,
+                        n_slots: int, pool, slot_bytes: int, partial, workspace, ws_bytes: int, stream=None) -> None:
+    _ck("moe_mx4_expert_down",
+        load().moe_mx4_expert_down(_ptr(h_codes), _ptr(h_scales), T, H, F, E, k, _ptr(ids), _ptr(weights),
+                                   _ptr(d_slot_table), n_slots, _ptr(pool), slot_bytes, _ptr(partial),
+                                   _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def moe_mx4_layer_workspace(T: int, H: int, F: int, E: int, k: int) -> int:
+    out = _sz()
+    _ck("moe_mx4_layer_workspace", load().moe_mx4_layer_workspace(T, H, F, E, k, ctypes.byref(out)))
+    return out.value
+
+
+def moe_mx4_layer(x, xtype: int, T: int, H: int, F: int, E: int, k: int, w_router, bias, d_slot_table, n_slots: int,
+                  pool, slot_bytes: int, extra, y, ids, weights, workspace, ws_bytes: int, stream=None) -> None:
+    _ck("moe_mx4_layer",
+        load().moe_mx4_layer(_ptr(x), xtype, T, H, F, E, k, _ptr(w_router), _ptr(bias), _ptr(d_slot_table), n_slots,
+                             _ptr(pool), slot_bytes, _ptr(extra), _ptr(y), _ptr(ids), _ptr(weights),
+                             _ptr(workspace), ws_bytes, _stream(stream)))

@@ -513,12 +513,14 @@ extern "C" int moe_cache_create(const moe_cache_desc *desc, moe_cache **out) {
     MOE_CHECK(desc && out);
     *out = nullptr;
     const moe_cache_desc &d = *desc;
-    MOE_CHECK(d.qtype == MOE_Q8_0 || d.qtype == MOE_Q4_SM);
+    MOE_CHECK(d.qtype == MOE_Q8_0 || d.qtype == MOE_Q4_SM || d.qtype == MOE_MXFP4);
     MOE_CHECK(d.H > 0 && d.F > 0 && d.H % 32 == 0 && d.F % 32 == 0);
     MOE_CHECK(d.n_layers >= 1 && d.n_experts >= 1 && d.n_experts <= MOE_MAX_E && d.first_layer >= 0);
     MOE_CHECK(d.n_slots >= 1);
     MOE_CHECK(d.admit_after >= 0 && d.lru_window >= 0);
     if (d.device_managed && d.lru_window > 0) return MOE_ERR_UNSUPPORTED;
+    // the kernels that fill a device-managed pool read q8_0 and 4-bit images only
+    if (d.device_managed && d.qtype == MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
     const size_t img = moe_expert_image_bytes(d.qtype, d.H, d.F);
     MOE_CHECK(d.slot_bytes >= img && d.slot_bytes % 256 == 0);
     MOE_CHECK(d.device_pool && ((uintptr_t)d.device_pool % 256) == 0);
@@ -849,6 +851,7 @@ const void *moe_cache_pool(const moe_cache *c, int *n_slots) {
     return c ? c->d.device_pool : nullptr;
 }
 
+int moe_cache_qtype(const moe_cache *c) { return c->d.qtype; }
 bool moe_cache_is_device_managed(const moe_cache *c) { return c && c->d.device_managed; }
 
 int moe_cache_layer_range(const moe_cache *c, int *first_layer, int *n_layers) {

@@ -72,7 +72,31 @@ __host__ __device__ static inline int moe_piece_in_block(int p, int lane) { retu
 __host__ __device__ static inline int moe_scale_in_block(int qtype, int lane) {
     return MOE_TILE_ROWS * (qtype == MOE_Q8_0 ? 32 : 16) + moe_scale_pos(lane) * moe_scale_entry_bytes(qtype);
 }
+// MOE_MXFP4 images are laid out for the tensor cores instead: two matrices (gate/up interleaved by
+// 64 rows, then down) of 128-row tiles, each a run of MX4_TB-byte tile blocks, one per 128 columns
+// (see moe_pack_expert in moe.h).
+#define MX4_TB 8704
+__host__ __device__ static inline size_t mx4_gu_bytes(int H, int F) {
+    return (size_t)((F + 63) / 64) * ((H + 127) / 128) * MX4_TB;
+}
+__host__ __device__ static inline size_t mx4_down_bytes(int H, int F) {
+    return (size_t)((H + 127) / 128) * ((F + 127) / 128) * MX4_TB;
+}
+// byte offsets in a matrix of B column blocks: the code byte of (tile row, column), and its scale
+__host__ __device__ static inline size_t mx4_tile_offset(int B, int row, int col) {
+    return ((size_t)(row >> 7) * B + (col >> 7)) * MX4_TB;
+}
+__host__ __device__ static inline size_t mx4_code_offset(int B, int row, int col) {
+    const int r = row & 127, c = (col >> 5) & 3;
+    return mx4_tile_offset(B, row, col) + r * 64 + ((c ^ ((r >> 1) & 3)) << 4) + ((col & 31) >> 1);
+}
+__host__ __device__ static inline size_t mx4_scale_offset(int B, int row, int col) {
+    return mx4_tile_offset(B, row, col) + 8192 + 16 * (row & 31) + 4 * ((row >> 5) & 3) + ((col >> 5) & 3);
+}
+// tile row of gate row f in the gate/up matrix (up row f: 64 further)
+__host__ __device__ static inline int mx4_gate_row(int f) { return (f >> 6) * 128 + (f & 63); }
 __host__ __device__ static inline size_t moe_expert_image_bytes(int qtype, int H, int F) {
+    if (qtype == MOE_MXFP4) return mx4_gu_bytes(H, F) + mx4_down_bytes(H, F);
     return 2 * moe_matrix_bytes(qtype, F, H) + moe_matrix_bytes(qtype, H, F);
 }
 // matrix m of an expert image: 0 gate, 1 up, 2 down
@@ -168,6 +192,7 @@ const void *moe_cache_image(const moe_cache *c, int layer, int expert);
 const void *moe_cache_pool(const moe_cache *c, int *n_slots);
 int moe_cache_layer_range(const moe_cache *c, int *first_layer, int *n_layers);
 bool moe_cache_is_device_managed(const moe_cache *c);
+int moe_cache_qtype(const moe_cache *c);
 
 size_t moe_decode_workspace_bytes(int T, int H, int F, int qtype, int E, int k);
 // moe_combine_rmsnorm skipping the routes whose id is -1 (ids [T][k] device, or NULL).

@@ -53,8 +53,38 @@ void unpack_matrix(int qtype, int R, int K, const uint8_t *src, uint8_t *aos) {
     }
 }
 
+// MXFP4: canonical block (E8M0 scale byte, 16 code bytes) of (row r of a matrix of RT tile rows,
+// 32-column block b) <-> its place in the tile blocks (layout in moe.h).
+template <bool PACK>
+void mx4_rows(uint8_t *tiles, int B, int tile_row, int NB, uint8_t *aos_row) {
+    for (int b = 0; b < NB; ++b) {
+        uint8_t *blk = aos_row + (size_t)b * 17;
+        uint8_t *code = tiles + mx4_code_offset(B, tile_row, 32 * b), *sc = tiles + mx4_scale_offset(B, tile_row, 32 * b);
+        if (PACK) {
+            *sc = blk[0];
+            memcpy(code, blk + 1, 16);
+        } else {
+            blk[0] = *sc;
+            memcpy(blk + 1, code, 16);
+        }
+    }
+}
+
+template <bool PACK>
+void mx4_expert(int H, int F, uint8_t *image, uint8_t *gate, uint8_t *up, uint8_t *down) {
+    const int HB = (H + 127) / 128, FB = (F + 127) / 128;
+    const size_t gu_row = (size_t)H / 32 * 17, down_row = (size_t)F / 32 * 17;
+    if (PACK) memset(image, 0, moe_expert_image_bytes(MOE_MXFP4, H, F));
+    for (int f = 0; f < F; ++f) {
+        mx4_rows<PACK>(image, HB, mx4_gate_row(f), H / 32, gate + f * gu_row);
+        mx4_rows<PACK>(image, HB, mx4_gate_row(f) + 64, H / 32, up + f * gu_row);
+    }
+    for (int h = 0; h < H; ++h)
+        mx4_rows<PACK>(image + mx4_gu_bytes(H, F), FB, h, F / 32, down + h * down_row);
+}
+
 bool shape_ok(int qtype, int H, int F) {
-    return (qtype == MOE_Q8_0 || qtype == MOE_Q4_SM) && H > 0 && F > 0 && H % 32 == 0 &&
+    return (qtype == MOE_Q8_0 || qtype == MOE_Q4_SM || qtype == MOE_MXFP4) && H > 0 && F > 0 && H % 32 == 0 &&
            F % 32 == 0;
 }
 
@@ -75,6 +105,10 @@ extern "C" int moe_pack_expert(int qtype, int H, int F, const void *gate_aos, co
     MOE_CHECK(gate_aos && up_aos && down_aos);
     MOE_CHECK(((uintptr_t)slot_image_dst & 15) == 0);
     uint8_t *dst = (uint8_t *)slot_image_dst;
+    if (qtype == MOE_MXFP4) {
+        mx4_expert<true>(H, F, dst, (uint8_t *)gate_aos, (uint8_t *)up_aos, (uint8_t *)down_aos);
+        return MOE_OK;
+    }
     pack_matrix(qtype, F, H, (const uint8_t *)gate_aos, dst + moe_expert_matrix_offset(qtype, H, F, 0));
     pack_matrix(qtype, F, H, (const uint8_t *)up_aos, dst + moe_expert_matrix_offset(qtype, H, F, 1));
     pack_matrix(qtype, H, F, (const uint8_t *)down_aos, dst + moe_expert_matrix_offset(qtype, H, F, 2));
@@ -86,6 +120,10 @@ extern "C" int moe_unpack_expert(int qtype, int H, int F, const void *slot_image
     MOE_CHECK(shape_ok(qtype, H, F));
     MOE_CHECK(slot_image && gate_aos && up_aos && down_aos);
     const uint8_t *src = (const uint8_t *)slot_image;
+    if (qtype == MOE_MXFP4) {
+        mx4_expert<false>(H, F, (uint8_t *)src, (uint8_t *)gate_aos, (uint8_t *)up_aos, (uint8_t *)down_aos);
+        return MOE_OK;
+    }
     unpack_matrix(qtype, F, H, src + moe_expert_matrix_offset(qtype, H, F, 0), (uint8_t *)gate_aos);
     unpack_matrix(qtype, F, H, src + moe_expert_matrix_offset(qtype, H, F, 1), (uint8_t *)up_aos);
     unpack_matrix(qtype, H, F, src + moe_expert_matrix_offset(qtype, H, F, 2), (uint8_t *)down_aos);

@@ -466,6 +466,10 @@ extern "C" int moe_stack_create(const moe_stack_desc *desc, moe_stack **out) {
             delete st;
             return MOE_ERR_INVALID;  // the caches' kind must match the stack's
         }
+        if (moe_cache_qtype(c) == MOE_MXFP4) {
+            delete st;
+            return MOE_ERR_UNSUPPORTED;  // the stacks' kernels read q8_0 and 4-bit images
+        }
         st->caches.push_back(c);
         for (int l = first; l < first + n; ++l) st->group_of_layer[l] = g;
     }
