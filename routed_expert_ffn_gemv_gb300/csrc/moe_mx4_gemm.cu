@@ -1,100 +1,563 @@
-// The routed experts' products over MXFP4 weights (moe_mx4_expert_gateup, moe_mx4_expert_down).
+// The routed experts' products over MXFP4 weights and MXFP4 activations
+// (moe_mx4_expert_gateup, moe_mx4_expert_down) on the block-scaled tensor cores.
+//
+//   D[128 weight rows][N routes] += (A . SFA)[rows][64] * (B . SFB)[routes][64]^T,
+//   tcgen05.mma kind::mxf4: E2M1 operands read from shared memory, one E8M0 scale per 32 columns
+//   read from tensor memory, exact products, fp32 sums in tensor memory.
+// The weights are the M side, so that an expert's few routes cost only as wide an MMA as they are.
+//
+//  * mx4_route_kernel: the routes sorted by expert (one cluster of up to 8 CTAs: shared-memory
+//    histograms joined over distributed shared memory, positions by a shared cursor) and cut into
+//    chunks of at most NT routes of one expert, experts with the most routes first.  The order of
+//    the routes inside an expert is not fixed; a route's result does not depend on it.
+//  * mx4_gemm_kernel: persistent, one CTA per SM; a work item is (chunk, 128-row weight tile).
+//    Warp roles, mbarrier rings that run on across items:
+//      warps 0, 1  a stage of 256 columns: the tile's two 8704-byte blocks (codes and scales, one
+//                  bulk copy: the slot image is in operand order) and the chunk's code rows,
+//                  four rows to a TMA gather, straight into the 128-byte-swizzled operand layout;
+//      warp 2      one thread issues the four MMAs of a stage and one commit;
+//      warps 4-7   the stage's scales into tensor memory: the weights' from the landed blocks, the
+//                  routes' from global memory (loaded a stage ahead).  Each warp writes its own
+//                  lane quarter (the tensor core reads a copy in each);
+//      warps 8-11  the epilogue of the previous item from the other accumulator: gate/up tiles hold
+//                  64 gate rows in lanes 0-63 and the same up rows in 64-127, the up quarters hand
+//                  their values over through shared memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
 #include "moe_mx4_gemm.cuh"
+#include "moe_tc.cuh"
+
+#define MXG_THREADS 384
+#define MXG_CTRL 13312
+#define MXG_WBYTES (2 * MX4_TB)  // weights of a stage: two tile blocks
+#define MXG_ROUTE_THREADS 1024
+#define MXG_ROUTE_CLUSTER 8
 
 namespace {
 
-// One warp per output element pair: lanes walk the 32-column blocks of K.
-template <int IN>  // MOE_MXFP4: codes + scales rows; MOE_F32 + 16 / MOE_BF16 + 16: plain rows
-struct Act {
-    const void *p;
-    const uint8_t *scales;
-    int K;
-    __device__ void block(size_t row, int b, float (&v)[32]) const {
-        if (IN == MOE_MXFP4) {
-            const uint8_t *c = (const uint8_t *)p + row * (K / 2) + 16 * b;
-            const float m = e8m0_value(scales[row * (K / 32) + b]);
-            for (int i = 0; i < 16; ++i) {
-                v[2 * i] = e2m1_value(c[i] & 15) * m;
-                v[2 * i + 1] = e2m1_value(c[i] >> 4) * m;
-            }
-        } else if (IN == MOE_BF16 + 16) {
-            for (int i = 0; i < 32; ++i) v[i] = __bfloat162float(((const __nv_bfloat16 *)p)[row * K + 32 * b + i]);
-        } else {
-            for (int i = 0; i < 32; ++i) v[i] = ((const float *)p)[row * K + 32 * b + i];
-        }
-    }
+// ------------------------------------------------------------------ workspace
+
+struct GemmWs {
+    int max_chunks;
+    size_t o_rows, o_slot, o_pos, o_n, ints;  // in ints; [0] is the number of chunks
 };
 
-__device__ float weight_dot(const uint8_t *m, int B, int row, int b, const float (&v)[32]) {
-    const uint8_t *c = m + mx4_code_offset(B, row, 32 * b);
-    float s = 0.f;
-    for (int i = 0; i < 16; ++i)
-        s += e2m1_value(c[i] & 15) * v[2 * i] + e2m1_value(c[i] >> 4) * v[2 * i + 1];
-    return s * e8m0_value(m[mx4_scale_offset(B, row, 32 * b)]);
+GemmWs gemm_ws(int T, int E, int k, int NT) {
+    GemmWs L;
+    const long R = (long)T * k;
+    L.max_chunks = (int)(R / NT + std::min<long>(E, R));
+    size_t o = 16;
+    L.o_rows = o; o += R;
+    L.o_slot = o; o += L.max_chunks;
+    L.o_pos = o;  o += L.max_chunks;
+    L.o_n = o;    o += L.max_chunks;
+    L.ints = o;
+    return L;
 }
 
-__device__ float warp_sum(float v) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// Most routes of a chunk.
+#define MXG_NT_SMALL 32
+#define MXG_NT_LARGE 224
+int chunk_routes(int T, int E, int k) { return (long)T * k <= 16L * E ? MXG_NT_SMALL : MXG_NT_LARGE; }
+
+// ------------------------------------------------------------------ routes by expert
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
 
-__device__ const uint8_t *image_of(int e, int E, const int32_t *table, int n_slots, const void *pool,
-                                   size_t slot_bytes, int *status) {
-    if (e == -1) return nullptr;
-    int slot = -1;
-    if (e >= 0 && e < E) slot = table ? table[e] : e;
-    if (slot < 0 || slot >= n_slots) {
-        moe_set_status(status, MOE_ERR_INVALID);
-        return nullptr;
+__global__ void __launch_bounds__(MXG_ROUTE_THREADS)
+mx4_route_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *__restrict__ table, int n_slots, int NT,
+                 int32_t *__restrict__ ints, int32_t *__restrict__ rows, int32_t *__restrict__ c_slot,
+                 int32_t *__restrict__ c_pos, int32_t *__restrict__ c_n, int *status) {
+    __shared__ int hist[MOE_MAX_E], cnt[MOE_MAX_E], cur[MOE_MAX_E], off[MOE_MAX_E];
+    __shared__ int order[MOE_MAX_E], first[MOE_MAX_E];
+    const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), tid = threadIdx.x;
+    const int seg = (R + C - 1) / C, r0 = rank * seg, r1 = min(R, r0 + seg);
+    if (tid < MOE_MAX_E) hist[tid] = 0;
+    pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+    for (int r = r0 + tid; r < r1; r += MXG_ROUTE_THREADS) {
+        const int e = ids[r];
+        if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+        else if (e != -1) moe_set_status(status, MOE_ERR_INVALID);
     }
-    return (const uint8_t *)pool + (size_t)slot * slot_bytes;
+    cluster_sync_all();
+    int before = 0;
+    if (tid < MOE_MAX_E) {
+        int total = 0;
+        for (int c = 0; c < C; ++c) {
+            if (c == rank) before = total;
+            total += (int)ld_cluster_u32(cluster_map(&hist[tid], c));
+        }
+        cnt[tid] = total;
+        off[tid] = total;
+    }
+    __syncthreads();
+    // exclusive sums over the experts: offsets of the routes
+    if (tid < 32) {
+        int v[MOE_MAX_E / 32], s = 0;
+        for (int i = 0; i < MOE_MAX_E / 32; ++i) {
+            v[i] = s;
+            s += cnt[tid * (MOE_MAX_E / 32) + i];
+        }
+        int x = s;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (tid >= o) x += y;
+        }
+        for (int i = 0; i < MOE_MAX_E / 32; ++i) off[tid * (MOE_MAX_E / 32) + i] = x - s + v[i];
+    }
+    __syncthreads();
+    if (tid < MOE_MAX_E) cur[tid] = off[tid] + before;
+    __syncthreads();
+    for (int r = r0 + tid; r < r1; r += MXG_ROUTE_THREADS) {
+        const int e = ids[r];
+        if (e >= 0 && e < E) rows[atomicAdd(&cur[e], 1)] = r;
+    }
+    if (rank == 0) {
+        // chunks, the experts with the most routes first
+        if (tid < MOE_MAX_E) {
+            int o = 0;
+            for (int j = 0; j < MOE_MAX_E; ++j) o += cnt[j] > cnt[tid] || (cnt[j] == cnt[tid] && j < tid);
+            order[o] = tid;
+        }
+        __syncthreads();
+        if (tid < 32) {
+            int v[MOE_MAX_E / 32], s = 0;
+            for (int i = 0; i < MOE_MAX_E / 32; ++i) {
+                v[i] = s;
+                s += (cnt[order[tid * (MOE_MAX_E / 32) + i]] + NT - 1) / NT;
+            }
+            int x = s;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (tid >= o) x += y;
+            }
+            for (int i = 0; i < MOE_MAX_E / 32; ++i) first[tid * (MOE_MAX_E / 32) + i] = x - s + v[i];
+            if (tid == 31) ints[0] = x;
+        }
+        __syncthreads();
+        if (tid < MOE_MAX_E) {
+            const int e = order[tid], n = cnt[e], nc = (n + NT - 1) / NT;
+            int slot = -1;
+            if (n > 0) {
+                slot = table ? table[e] : e;
+                if (slot < 0 || slot >= n_slots) {
+                    moe_set_status(status, MOE_ERR_INVALID);
+                    slot = -1;
+                }
+            }
+            for (int c = 0; c < nc; ++c) {  // near-equal chunks
+                const int a = (int)((long)n * c / nc), b = (int)((long)n * (c + 1) / nc);
+                c_slot[first[tid] + c] = slot;
+                c_pos[first[tid] + c] = off[e] + a;
+                c_n[first[tid] + c] = b - a;
+            }
+        }
+    }
+    cluster_sync_all();  // the histograms stay until every CTA has read them
 }
 
-template <int IN, int OUT>
-__global__ void gateup_simple(Act<IN> x, int k, int H, int F, int E, const int32_t *ids, const int32_t *table,
-                              int n_slots, const void *pool, size_t slot_bytes, void *h, int *status) {
-    const int r = blockIdx.x, lane = threadIdx.x & 31;
-    const uint8_t *m = image_of(ids[r], E, table, n_slots, pool, slot_bytes, status);
-    if (!m) return;
-    const int B = (H + 127) / 128;
-    for (int f = blockIdx.y * 8 + threadIdx.x / 32; f < F; f += gridDim.y * 8) {
-        float g = 0.f, u = 0.f;
-        for (int b = lane; b < H / 32; b += 32) {
-            float v[32];
-            x.block(r / k, b, v);
-            g += weight_dot(m, B, mx4_gate_row(f), b, v);
-            u += weight_dot(m, B, mx4_gate_row(f) + 64, b, v);
+// ------------------------------------------------------------------ the products
+
+struct GemmParams {
+    CUtensorMap map;         // the code rows, boxes of 128 bytes of one row
+    const uint8_t *scales;   // [rows][K / 32]
+    const uint8_t *pool;
+    size_t slot_bytes;
+    const int32_t *ints, *rows, *c_slot, *c_pos, *c_n;
+    const float *weights;    // down
+    void *out;
+    int K, R_out, div;       // columns, output row length, routes per code row
+    int MT;                  // weight tiles of an item list
+    size_t mat;              // byte offset of the matrix in an image
+    int *status;
+};
+
+template <int NT>
+struct GemmGeom {
+    static constexpr int STAGE = MXG_WBYTES + NT * 128;
+    static constexpr int S = NT == MXG_NT_LARGE ? 4 : 9;     // ring stages
+    static constexpr int SFS = NT == MXG_NT_LARGE ? 2 : 8;   // scale slots in tensor memory, 24 columns each
+    static constexpr int SFCOL = 2 * NT;                     // after the two accumulators
+    static constexpr size_t SMEM = 1024 + MXG_CTRL + (size_t)S * STAGE;
+    static_assert(SFCOL + SFS * 24 <= 512 && S > SFS && STAGE % 1024 == 0 && SMEM <= 227 * 1024, "budget");
+};
+
+// Four rows of the map's box width to 4 x 128 bytes of shared memory.  x is a multiple of 128.
+__device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, int x, const int (&r)[4], uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The eight scale bytes of a row from block 8q on (fewer at the row's end: zeros).
+__device__ __forceinline__ uint2 scale8(const uint8_t *row, int q, int KS) {
+    if ((KS & 7) == 0 && ((uintptr_t)row & 7) == 0) return *(const uint2 *)(row + 8 * q);
+    uint32_t v[2] = {0u, 0u};
+    const int n = min(8, KS - 8 * q);
+    for (int i = 0; i < n; ++i) v[i >> 2] |= (uint32_t)row[8 * q + i] << (8 * (i & 3));
+    return make_uint2(v[0], v[1]);
+}
+
+template <int NT, bool DOWN, int OT>
+__global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_constant__ GemmParams p) {
+    using G = GemmGeom<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_smem_1024(smem_raw);
+    uint64_t *s_full = (uint64_t *)smem;
+    uint64_t *s_empty = s_full + G::S;
+    uint64_t *sf_full = s_empty + G::S;
+    uint64_t *acc_full = sf_full + G::SFS;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *mma_done = acc_empty + 2;
+    uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
+    volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
+    static_assert((2 * G::S + G::SFS + 6) * 8 <= 1024, "barriers");
+    float *xch = (float *)(smem + 1024);         // [2 pairs][2 slots][16 columns][32 lanes]
+    int *e_route = (int *)(smem + 1024 + 8192);  // [2 accumulators][NT]
+    float *e_w = (float *)(e_route + 2 * NT);
+    static_assert(1024 + 8192 + 4 * NT * 4 <= MXG_CTRL, "control block");
+    uint8_t *ring = smem + MXG_CTRL;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::S; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&s_empty[s], 1);
         }
-        g = warp_sum(g);
-        u = warp_sum(u);
-        const float y = g / (1.0f + expf(-g)) * u;
+        for (int s = 0; s < G::SFS; ++s) mbar_init(&sf_full[s], 4);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 4);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+    const int MT = p.MT, n_items = p.ints[0] * MT;
+    const int KB = (p.K + 127) / 128, NKS = (KB + 1) / 2, KS = p.K / 32;
+
+    if (warp < 2) {
+        // ---------------- producers: warp 0 the stage's expected bytes, its weights and the even
+        // groups of four rows, warp 1 the odd groups
+        int g = 0;
+        bool ok = true;
+        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
+            const int c = j / MT, m = j % MT;
+            const int slot = p.c_slot[c];
+            if (slot < 0) continue;
+            const int pos0 = p.c_pos[c], n = p.c_n[c];
+            const int npad = (n + 7) & ~7, q = 2 * lane + warp;  // this lane's group of four rows
+            int r4[4];
+            for (int i = 0; i < 4; ++i) {
+                const int at = 4 * q + i;
+                r4[i] = p.rows[pos0 + (at < n ? at : 0)] / p.div;  // rows past the chunk: unused columns
+            }
+            const uint8_t *w = p.pool + (size_t)slot * p.slot_bytes + p.mat + (size_t)m * KB * MX4_TB;
+            for (int kc = 0; kc < NKS; ++kc, ++g) {
+                const int s = g % G::S;
+                if (g >= G::S) {
+                    ok = mbar_wait_role(&s_empty[s], ((g / G::S) & 1) ^ 1, p.status, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                }
+                uint8_t *st = ring + (size_t)s * G::STAGE;
+                if (warp == 0 && lane == 0) {
+                    const uint32_t wb = 2 * kc + 1 < KB ? MXG_WBYTES : MX4_TB;
+                    mbar_arrive_expect_tx(&s_full[s], wb + (uint32_t)npad * 128u);
+                    bulk_g2s(st, w + (size_t)kc * MXG_WBYTES, wb, &s_full[s]);
+                }
+                if (4 * q < npad) tma_gather4(st + MXG_WBYTES + q * 512, &p.map, kc * 128, r4, &s_full[s]);
+                __syncwarp();
+            }
+        }
+        // never leave with copies in flight
+        if (warp == 0 && lane == 0)
+            for (int s = 0; s < G::S && s < g; ++s) {
+                const int last = s + ((g - 1 - s) / G::S) * G::S;
+                mbar_wait_bounded(&s_full[s], (last / G::S) & 1, p.status);
+            }
+        if (!ok) settle_after_abort();
+    } else if (warp == 2) {
+        // ---------------- MMA issuer
         if (lane == 0) {
-            if (OUT == MOE_BF16) ((__nv_bfloat16 *)h)[(size_t)r * F + f] = __float2bfloat16(y);
-            else ((float *)h)[(size_t)r * F + f] = y;
+            int g = 0, jl = 0;
+            bool ok = true;
+            for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
+                const int c = j / MT;
+                if (p.c_slot[c] < 0) continue;
+                const int npad = (p.c_n[c] + 7) & ~7;
+                const uint32_t id0 = umma_idesc_mxf4(128, npad, 0), id2 = umma_idesc_mxf4(128, npad, 2);
+                const int buf = jl & 1;
+                if (jl >= 2 && !(ok = mbar_wait_role(&acc_empty[buf], ((jl / 2) - 1) & 1, p.status, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * NT;
+                for (int kc = 0; kc < NKS; ++kc, ++g) {
+                    const int s = g % G::S, f = g % G::SFS;
+                    if (!(ok = mbar_wait_role(&sf_full[f], (g / G::SFS) & 1, p.status, abort_flag))) break;
+                    if (!(ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
+                    tc_fence_after();
+                    uint8_t *st = ring + (size_t)s * G::STAGE;
+                    const uint64_t a = umma_desc_sw64(smem_u32(st)), b = umma_desc_sw128(smem_u32(st + MXG_WBYTES));
+                    const uint32_t sf = tmem + G::SFCOL + 24 * f;
+                    const int steps = min(4, (p.K - 256 * kc + 63) / 64);
+                    umma_mxf4(d, a, b, id0, sf, sf + 8, kc > 0);
+                    if (steps > 1) umma_mxf4(d, a + 2, b + 2, id2, sf, sf + 8, 1);
+                    if (steps > 2) umma_mxf4(d, a + (MX4_TB >> 4), b + 4, id0, sf + 4, sf + 16, 1);
+                    if (steps > 3) umma_mxf4(d, a + (MX4_TB >> 4) + 2, b + 6, id2, sf + 4, sf + 16, 1);
+                    umma_commit(&s_empty[s]);
+                }
+                if (ok) umma_commit(&acc_full[buf]);
+                ++jl;
+            }
+            umma_commit(mma_done);  // every MMA has completed before tensor memory is released
+            mbar_wait_bounded(mma_done, 0, p.status);
         }
+    } else if (warp >= 4 && warp < 8) {
+        // ---------------- scales
+        const uint32_t t0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::SFCOL;
+        constexpr int NI = NT / 32;
+        int g = 0;
+        bool ok = true;
+        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
+            const int c = j / MT;
+            if (p.c_slot[c] < 0) continue;
+            const int pos0 = p.c_pos[c], n = p.c_n[c];
+            const uint8_t *row[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int at = 32 * i + lane;
+                row[i] = at < n ? p.scales + (size_t)(p.rows[pos0 + at] / p.div) * KS : nullptr;
+            }
+            uint2 nxt[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) nxt[i] = row[i] ? scale8(row[i], 0, KS) : make_uint2(0, 0);
+            for (int kc = 0; kc < NKS; ++kc, ++g) {
+                const int s = g % G::S, f = g % G::SFS;
+                uint32_t v[24];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[8 + i] = i < NI ? nxt[i < NI ? i : 0].x : 0u;
+                    v[16 + i] = i < NI ? nxt[i < NI ? i : 0].y : 0u;
+                }
+                if (kc + 1 < NKS)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        if (row[i]) nxt[i] = scale8(row[i], kc + 1, KS);
+                // the slot's last reader: the MMAs of stage g - SFS, whose commit released that ring stage
+                if (g >= G::SFS)
+                    ok = mbar_wait_role(&s_empty[(g - G::SFS) % G::S], ((g - G::SFS) / G::S) & 1, p.status, abort_flag);
+                if (ok) ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                const uint8_t *st = ring + (size_t)s * G::STAGE;
+                const uint4 a = *(const uint4 *)(st + 8192 + 16 * lane);
+                uint4 b = make_uint4(0, 0, 0, 0);
+                if (2 * kc + 1 < KB) b = *(const uint4 *)(st + MX4_TB + 8192 + 16 * lane);
+                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) tmem_st8(t0 + 24 * f + 8 * i, *reinterpret_cast<uint32_t(*)[8]>(&v[8 * i]));
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&sf_full[f]);
+            }
+        }
+    } else if (warp >= 8) {
+        // ---------------- epilogue: lane quarter q, lane = weight row 32 q + lane of the tile
+        const int q = warp & 3, ew = warp - 8;
+        int jl = 0, xs = 0;
+        bool ok = true;
+        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
+            const int c = j / MT, m = j % MT;
+            if (p.c_slot[c] < 0) continue;
+            const int pos0 = p.c_pos[c], n = p.c_n[c], buf = jl & 1;
+            for (int i = ew * 32 + lane; i < n; i += 128) {
+                const int r = p.rows[pos0 + i];
+                e_route[buf * NT + i] = r;
+                if (DOWN) e_w[buf * NT + i] = p.weights[r];
+            }
+            const bool w = mbar_wait_role(&acc_full[buf], (jl / 2) & 1, p.status, abort_flag);
+            if (!(ok = bar_and_n(1, 128, w))) break;
+            tc_fence_after();
+            const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * NT;
+            for (int c0 = 0; c0 < n; c0 += 16, ++xs) {
+                uint32_t v[16];
+                tmem_ld16(tb + c0, v);
+                tmem_ld_wait();
+                const int nn = min(16, n - c0);
+                const int *rt = e_route + buf * NT + c0;
+                if (!DOWN) {
+                    float *xb = xch + (size_t)((q & 1) * 2 + (xs & 1)) * 512 + lane;
+                    if (q >= 2)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) xb[32 * i] = __uint_as_float(v[i]);
+                    bar_sync_n(2 + (q & 1), 64);
+                    const int f = 64 * m + 32 * q + lane;
+                    if (q < 2 && f < p.R_out) {
+                        float h[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float gv = __uint_as_float(v[i]);
+                            h[i] = gv / (1.0f + __expf(-gv)) * xb[32 * i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < nn) {
+                                const size_t at = (size_t)rt[i] * p.R_out + f;
+                                if (OT == MOE_BF16) ((__nv_bfloat16 *)p.out)[at] = __float2bfloat16(h[i]);
+                                else ((float *)p.out)[at] = h[i];
+                            }
+                    }
+                } else {
+                    const int o = 128 * m + 32 * q + lane;
+                    const float *wt = e_w + buf * NT + c0;
+                    if (o < p.R_out)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < nn) ((float *)p.out)[(size_t)rt[i] * p.R_out + o] = wt[i] * __uint_as_float(v[i]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(&acc_empty[buf]);
+            ++jl;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
-template <int IN>
-__global__ void down_simple(Act<IN> hq, int H, int F, int E, const int32_t *ids, const float *weights,
-                            const int32_t *table, int n_slots, const void *pool, size_t slot_bytes, float *partial,
-                            int *status) {
-    const int r = blockIdx.x, lane = threadIdx.x & 31;
-    const uint8_t *m = image_of(ids[r], E, table, n_slots, pool, slot_bytes, status);
-    if (!m) return;
-    m += mx4_gu_bytes(H, F);
-    const int B = (F + 127) / 128;
-    const float w = weights[r];
-    for (int o = blockIdx.y * 8 + threadIdx.x / 32; o < H; o += gridDim.y * 8) {
-        float y = 0.f;
-        for (int b = lane; b < F / 32; b += 32) {
-            float v[32];
-            hq.block(r, b, v);
-            y += weight_dot(m, B, o, b, v);
+// ------------------------------------------------------------------ host
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
+    });
+    return fn;
+}
+
+// Code rows [rows][K/2] as boxes of 128 bytes of one row (TMA gathers), 128-byte swizzle; columns
+// past the row's end read 0.
+int encode_codes_map(const uint8_t *codes, long rows, int K, CUtensorMap *map) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return MOE_ERR_UNSUPPORTED;
+    const cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)K / 2};
+    const cuuint32_t box[2] = {128, 1};
+    const cuuint32_t es[2] = {1, 1};
+    if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)codes, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+        CUDA_SUCCESS)
+        return MOE_ERR_CUDA;
+    return MOE_OK;
+}
+
+template <int NT, bool DOWN, int OT>
+int launch_gemm_t(const GemmParams &p, int max_chunks, cudaStream_t s) {
+    using G = GemmGeom<NT>;
+    static std::mutex mu;
+    static int sms[64] = {0};
+    int dev = -1;
+    MOE_TRY_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    int n = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!sms[dev]) {
+            MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_gemm_kernel<NT, DOWN, OT>,
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::SMEM));
+            MOE_TRY_CUDA(cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev));
         }
-        y = warp_sum(y);
-        if (lane == 0) partial[(size_t)r * H + o] = w * y;
+        n = sms[dev];
     }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    const long items = (long)max_chunks * p.MT;
+    moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<long>(items, n)), dim3(MXG_THREADS), G::SMEM, s);
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<NT, DOWN, OT>, p));
+    return MOE_OK;
+}
+
+template <bool DOWN, int OT>
+int launch_gemm(const GemmParams &p, int NT, int max_chunks, cudaStream_t s) {
+    return NT == MXG_NT_SMALL ? launch_gemm_t<MXG_NT_SMALL, DOWN, OT>(p, max_chunks, s)
+                              : launch_gemm_t<MXG_NT_LARGE, DOWN, OT>(p, max_chunks, s);
+}
+
+int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, int H, int F, int E, int k,
+                const int32_t *ids, const float *weights, const int32_t *table, int n_slots, const void *pool,
+                size_t slot_bytes, void *out, int otype, void *workspace, cudaStream_t s) {
+    const int NT = chunk_routes(T, E, k);
+    const GemmWs L = gemm_ws(T, E, k, NT);
+    int32_t *w = (int32_t *)workspace;
+    GemmParams p;
+    p.K = down ? F : H;
+    p.R_out = down ? H : F;
+    p.div = down ? 1 : k;
+    const int rc = encode_codes_map(codes, down ? (long)T * k : T, p.K, &p.map);
+    if (rc != MOE_OK) return rc;
+    p.scales = scales;
+    p.pool = (const uint8_t *)pool;
+    p.slot_bytes = slot_bytes;
+    p.ints = w;
+    p.rows = w + L.o_rows;
+    p.c_slot = w + L.o_slot;
+    p.c_pos = w + L.o_pos;
+    p.c_n = w + L.o_n;
+    p.weights = weights;
+    p.out = out;
+    p.MT = down ? (H + 127) / 128 : (F + 63) / 64;
+    p.mat = down ? mx4_gu_bytes(H, F) : 0;
+    p.status = moe_status_word_device_ptr();
+
+    const int R = T * k;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    const int C = R <= 2 * MXG_ROUTE_THREADS ? 1 : MXG_ROUTE_CLUSTER;
+    moe_pdl_config(&cfg, attr, dim3(C), dim3(MXG_ROUTE_THREADS), 0, s);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_route_kernel, ids, R, E, table, n_slots, NT, w, w + L.o_rows,
+                                    w + L.o_slot, w + L.o_pos, w + L.o_n, p.status));
+    if (down) return launch_gemm<true, MOE_F32>(p, NT, L.max_chunks, s);
+    return otype == MOE_BF16 ? launch_gemm<false, MOE_BF16>(p, NT, L.max_chunks, s)
+                             : launch_gemm<false, MOE_F32>(p, NT, L.max_chunks, s);
 }
 
 }  // namespace
@@ -112,36 +575,11 @@ int mx4_pool_check(int H, int F, int n_slots, const void *pool, size_t slot_byte
     return MOE_OK;
 }
 
-int mx4_simple_gateup_plain(const void *x, int xtype, int T, int H, int F, int E, int k, const int32_t *ids,
-                            const int32_t *table, int n_slots, const void *pool, size_t slot_bytes, float *h,
-                            cudaStream_t s) {
-    int *status = moe_status_word_device_ptr();
-    const dim3 g(T * k, (F + 7) / 8);
-    if (xtype == MOE_BF16)
-        gateup_simple<MOE_BF16 + 16, MOE_F32><<<g, 256, 0, s>>>({x, nullptr, H}, k, H, F, E, ids, table, n_slots, pool,
-                                                                slot_bytes, h, status);
-    else
-        gateup_simple<MOE_F32 + 16, MOE_F32><<<g, 256, 0, s>>>({x, nullptr, H}, k, H, F, E, ids, table, n_slots, pool,
-                                                               slot_bytes, h, status);
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
-}
-
-int mx4_simple_down_plain(const float *h, int T, int H, int F, int E, int k, const int32_t *ids, const float *weights,
-                          const int32_t *table, int n_slots, const void *pool, size_t slot_bytes, float *partial,
-                          cudaStream_t s) {
-    down_simple<MOE_F32 + 16><<<dim3(T * k, (H + 7) / 8), 256, 0, s>>>({h, nullptr, F}, H, F, E, ids, weights, table,
-                                                                       n_slots, pool, slot_bytes, partial,
-                                                                       moe_status_word_device_ptr());
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
-}
-
 extern "C" int moe_mx4_expert_workspace(int T, int H, int F, int E, int k, size_t *bytes) {
     MOE_CHECK(bytes);
     const int rc = mx4_ffn_check(T, H, F, E, k);
     if (rc != MOE_OK) return rc;
-    *bytes = 256;
+    *bytes = (gemm_ws(T, E, k, chunk_routes(T, E, k)).ints * 4 + 255) / 256 * 256;
     return MOE_OK;
 }
 
@@ -157,17 +595,8 @@ extern "C" int moe_mx4_expert_gateup(const uint8_t *x_codes, const uint8_t *x_sc
     MOE_CHECK(x_codes && x_scales && ids && h && workspace && ws_bytes >= need);
     MOE_CHECK(((uintptr_t)x_codes & 15) == 0 && ((uintptr_t)workspace & 255) == 0);
     if ((rc = mx4_pool_check(H, F, n_slots, pool, slot_bytes)) != MOE_OK) return rc;
-    cudaStream_t st = moe_cuda_stream(s);
-    int *status = moe_status_word_device_ptr();
-    const dim3 g(T * k, (F + 7) / 8);
-    if (htype == MOE_BF16)
-        gateup_simple<MOE_MXFP4, MOE_BF16><<<g, 256, 0, st>>>({x_codes, x_scales, H}, k, H, F, E, ids, d_slot_table,
-                                                              n_slots, pool, slot_bytes, h, status);
-    else
-        gateup_simple<MOE_MXFP4, MOE_F32><<<g, 256, 0, st>>>({x_codes, x_scales, H}, k, H, F, E, ids, d_slot_table,
-                                                             n_slots, pool, slot_bytes, h, status);
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
+    return run_product(false, x_codes, x_scales, T, H, F, E, k, ids, nullptr, d_slot_table, n_slots, pool, slot_bytes,
+                       h, htype, workspace, moe_cuda_stream(s));
 }
 
 extern "C" int moe_mx4_expert_down(const uint8_t *h_codes, const uint8_t *h_scales, int T, int H, int F, int E, int k,
@@ -181,9 +610,6 @@ extern "C" int moe_mx4_expert_down(const uint8_t *h_codes, const uint8_t *h_scal
     MOE_CHECK(h_codes && h_scales && ids && weights && partial && workspace && ws_bytes >= need);
     MOE_CHECK(((uintptr_t)h_codes & 15) == 0 && ((uintptr_t)workspace & 255) == 0);
     if ((rc = mx4_pool_check(H, F, n_slots, pool, slot_bytes)) != MOE_OK) return rc;
-    down_simple<MOE_MXFP4><<<dim3(T * k, (H + 7) / 8), 256, 0, moe_cuda_stream(s)>>>(
-        {h_codes, h_scales, F}, H, F, E, ids, weights, d_slot_table, n_slots, pool, slot_bytes, partial,
-        moe_status_word_device_ptr());
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
+    return run_product(true, h_codes, h_scales, T, H, F, E, k, ids, weights, d_slot_table, n_slots, pool, slot_bytes,
+                       partial, MOE_F32, workspace, moe_cuda_stream(s));
 }

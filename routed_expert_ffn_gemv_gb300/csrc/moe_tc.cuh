@@ -115,3 +115,84 @@ __host__ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t
     const uint32_t chunk = (k >> 3) ^ (row & 7);
     return (row >> 3) * 1024 + (row & 7) * 128 + chunk * 16 + (k & 7) * 2;
 }
+
+// ------------------------------------------------------------------ block-scaled 4-bit MMA
+
+// Shared-memory matrix descriptor for a K-major operand tile stored with the 64-byte swizzle:
+// rows of 64 bytes (128 E2M1), 8-row atoms of 512 bytes, 16-byte chunk j of row r stored at
+// j ^ ((r / 2) % 4).  The tile base must be 512-byte aligned; 64 elements along K add 32 bytes.
+__device__ __forceinline__ uint64_t umma_desc_sw64(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFF) >> 4);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)(512 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)4 << 61;  // layout: 64-byte swizzle
+    return d;
+}
+
+// Instruction descriptor of kind::mxf4: E2M1 A and B with E8M0 scales (two per 64 columns), both
+// K-major, fp32 accumulator.  sf_id (0 or 2): which half of each 32-bit scale word this K = 64 step
+// takes, for A and B alike.
+__host__ __device__ constexpr uint32_t umma_idesc_mxf4(int M, int N, int sf_id) {
+    return ((uint32_t)sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(M >> 4) << 24) | ((uint32_t)sf_id << 29);
+}
+
+// D[tmem] (+)= (A . SFA)[smem] * (B . SFB)[smem]^T over K = 64, issued by one thread.  The scales of
+// row m of A (n of B) are the bytes of one 32-bit word in tensor memory: lane m % 32 of every lane
+// quarter, column m / 32 from sfa (sfb).
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ uint8_t *align_smem_1024(uint8_t *p) {
+    const uint32_t a = smem_u32(p);
+    return p + ((1024 - (a & 1023)) & 1023);
+}
+
+__device__ __forceinline__ void mbar_arrive1(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Bounded wait for an mbarrier phase (polling): false when another role of the CTA has aborted, or
+// when the limit ran out (MOE_ERR_TIMEOUT recorded, the CTA's roles abort).
+__device__ __forceinline__ bool mbar_wait_role(uint64_t *bar, uint32_t parity, int *status, volatile int *abort_flag) {
+    for (uint32_t i = 0; i < MOE_TEST_SPIN_LIMIT; ++i) {
+        if (mbar_test_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+    }
+    moe_set_status(status, MOE_ERR_TIMEOUT);
+    *abort_flag = 1;
+    return false;
+}
+
+// Named barriers (ids 1..15) over `count` threads; the second ANDs a predicate.
+__device__ __forceinline__ void bar_sync_n(int id, int count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_and_n(int id, int count, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id), "r"(count)
+        : "memory");
+    return r != 0;
+}
+
+// For a role that leaves after an abort with copies whose barrier may never complete: time enough
+// for them to land (a copy takes microseconds; this waits about a millisecond, once, on an error).
+__device__ __forceinline__ void settle_after_abort() {
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+}
