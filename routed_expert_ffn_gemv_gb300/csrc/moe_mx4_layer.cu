@@ -1,151 +1,809 @@
-// A whole MoE layer for a few tokens over resident MXFP4 experts (moe_mx4_layer).
+// A whole MoE layer for a few tokens over resident MXFP4 experts (moe_mx4_layer): two kernels.
+//
+// The 4-bit tensor cores multiply E2M1 by E2M1.  To keep the activations at fp32 accuracy they are
+// written in radix 8: an activation is a 24-bit fixed-point number under a common scale, and its
+// eight digits -4 .. 3 are all E2M1 values, so a token becomes eight exact 4-bit columns and
+//     w . x = scale * sum_p 8^p (w . digit_p),
+// each term an exact product of 4-bit operands summed in fp32 by the MMA.  Eight columns are the
+// narrowest MMA there is, so one token's digits cost nothing over a single 4-bit column, the weights
+// go from HBM through shared memory to the tensor core untouched, and no thread dequantises.
+//   x: one scale per token (largest magnitude to 7190000, the largest symmetric 8-digit number);
+//   h: one power of two per 32 columns, the MMA's own E8M0 scale (largest magnitude below 2^22).
+//
+//  * mx4_prep_kernel, one 8-CTA cluster per 8 tokens: the router (a CTA sums its eighth of H, the
+//    partial logits meet over distributed shared memory, one warp selects), the tokens' digits in
+//    operand order, and the counters of the second kernel.
+//  * mx4_layer_kernel: persistent.  Units: (chunk of at most NR routes of one expert, 128-row weight
+//    tile) of gate/up, then of down.  CTAs take units in order from a counter, so a down unit only
+//    ever waits for gate/up units that running CTAs hold: no co-residency is needed, and other work
+//    on the GPU cannot deadlock it.  Roles as in the grouped product, with
+//      warp 0      claims units, copies the weights (17 KB a stage: bound by HBM),
+//      warp 1      copies the digits (gate/up: 512 bytes per token and 128 columns; down: once the
+//                  chunk's gate/up units are all done),
+//      warp 2      the MMAs, warps 4-7 the scales,
+//      warps 8-11  gate/up: sum_p, SwiGLU, the digits and scales of h (a block of 32 columns is a
+//                  warp: one reduction; an 8x8 nibble transpose by three shuffles); down: sum_p, the
+//                  router weight, partial rows; the CTA that completes a tile of H adds the partial
+//                  rows in route order onto extra.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <mutex>
+
 #include "moe_mx4_gemm.cuh"
+#include "moe_select.cuh"
+#include "moe_tc.cuh"
 
-namespace {
+#define MXL_CLUSTER 8
+#define MXL_TOKENS 8          // tokens per cluster
+#define MXL_PREP_THREADS 256
+#define MXL_THREADS 384
+#define MXL_SFS 4             // scale slots in tensor memory, 16 columns each
+#define MXL_Q 4               // claimed units in flight in a CTA
+#define MXL_MAX_R (MOE_DECODE_MAX_T * MOE_MAX_K)
+#define MXL_XMAX 7190000.0f   // <= 3 (8^8 - 1) / 7
+#define MXL_BIAS 9586980u     // 4 (8^8 - 1) / 7: turns digits -4 .. 3 into 0 .. 7
+#define MXL_WBYTES (2 * MX4_TB)
 
-// One warp per output element pair: lanes walk the 32-column blocks of K.
-template <int IN>  // MOE_MXFP4: codes + scales rows; MOE_F32 + 16 / MOE_BF16 + 16: plain rows
-struct Act {
-    const void *p;
-    const uint8_t *scales;
-    int K;
-    __device__ void block(size_t row, int b, float (&v)[32]) const {
-        if (IN == MOE_MXFP4) {
-            const uint8_t *c = (const uint8_t *)p + row * (K / 2) + 16 * b;
-            const float m = e8m0_value(scales[row * (K / 32) + b]);
-            for (int i = 0; i < 16; ++i) {
-                v[2 * i] = e2m1_value(c[i] & 15) * m;
-                v[2 * i + 1] = e2m1_value(c[i] >> 4) * m;
-            }
-        } else if (IN == MOE_BF16 + 16) {
-            for (int i = 0; i < 32; ++i) v[i] = __bfloat162float(((const __nv_bfloat16 *)p)[row * K + 32 * b + i]);
-        } else {
-            for (int i = 0; i < 32; ++i) v[i] = ((const float *)p)[row * K + 32 * b + i];
-        }
-    }
-};
-
-__device__ float weight_dot(const uint8_t *m, int B, int row, int b, const float (&v)[32]) {
-    const uint8_t *c = m + mx4_code_offset(B, row, 32 * b);
-    float s = 0.f;
-    for (int i = 0; i < 16; ++i)
-        s += e2m1_value(c[i] & 15) * v[2 * i] + e2m1_value(c[i] >> 4) * v[2 * i + 1];
-    return s * e8m0_value(m[mx4_scale_offset(B, row, 32 * b)]);
-}
-
-__device__ float warp_sum(float v) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-__device__ const uint8_t *image_of(int e, int E, const int32_t *table, int n_slots, const void *pool,
-                                   size_t slot_bytes, int *status) {
-    if (e == -1) return nullptr;
-    int slot = -1;
-    if (e >= 0 && e < E) slot = table ? table[e] : e;
-    if (slot < 0 || slot >= n_slots) {
-        moe_set_status(status, MOE_ERR_INVALID);
-        return nullptr;
-    }
-    return (const uint8_t *)pool + (size_t)slot * slot_bytes;
-}
-
-template <int IN, int OUT>
-__global__ void gateup_simple(Act<IN> x, int k, int H, int F, int E, const int32_t *ids, const int32_t *table,
-                              int n_slots, const void *pool, size_t slot_bytes, void *h, int *status) {
-    const int r = blockIdx.x, lane = threadIdx.x & 31;
-    const uint8_t *m = image_of(ids[r], E, table, n_slots, pool, slot_bytes, status);
-    if (!m) return;
-    const int B = (H + 127) / 128;
-    for (int f = blockIdx.y * 8 + threadIdx.x / 32; f < F; f += gridDim.y * 8) {
-        float g = 0.f, u = 0.f;
-        for (int b = lane; b < H / 32; b += 32) {
-            float v[32];
-            x.block(r / k, b, v);
-            g += weight_dot(m, B, mx4_gate_row(f), b, v);
-            u += weight_dot(m, B, mx4_gate_row(f) + 64, b, v);
-        }
-        g = warp_sum(g);
-        u = warp_sum(u);
-        const float y = g / (1.0f + expf(-g)) * u;
-        if (lane == 0) {
-            if (OUT == MOE_BF16) ((__nv_bfloat16 *)h)[(size_t)r * F + f] = __float2bfloat16(y);
-            else ((float *)h)[(size_t)r * F + f] = y;
-        }
-    }
-}
-
-template <int IN>
-__global__ void down_simple(Act<IN> hq, int H, int F, int E, const int32_t *ids, const float *weights,
-                            const int32_t *table, int n_slots, const void *pool, size_t slot_bytes, float *partial,
-                            int *status) {
-    const int r = blockIdx.x, lane = threadIdx.x & 31;
-    const uint8_t *m = image_of(ids[r], E, table, n_slots, pool, slot_bytes, status);
-    if (!m) return;
-    m += mx4_gu_bytes(H, F);
-    const int B = (F + 127) / 128;
-    const float w = weights[r];
-    for (int o = blockIdx.y * 8 + threadIdx.x / 32; o < H; o += gridDim.y * 8) {
-        float y = 0.f;
-        for (int b = lane; b < F / 32; b += 32) {
-            float v[32];
-            hq.block(r, b, v);
-            y += weight_dot(m, B, o, b, v);
-        }
-        y = warp_sum(y);
-        if (lane == 0) partial[(size_t)r * H + o] = w * y;
-    }
-}
-
-}  // namespace
-
-static int mx4_simple_gateup_plain(const void *x, int xtype, int T, int H, int F, int E, int k, const int32_t *ids,
-                            const int32_t *table, int n_slots, const void *pool, size_t slot_bytes, float *h,
-                            cudaStream_t s) {
-    int *status = moe_status_word_device_ptr();
-    const dim3 g(T * k, (F + 7) / 8);
-    if (xtype == MOE_BF16)
-        gateup_simple<MOE_BF16 + 16, MOE_F32><<<g, 256, 0, s>>>({x, nullptr, H}, k, H, F, E, ids, table, n_slots, pool,
-                                                                slot_bytes, h, status);
-    else
-        gateup_simple<MOE_F32 + 16, MOE_F32><<<g, 256, 0, s>>>({x, nullptr, H}, k, H, F, E, ids, table, n_slots, pool,
-                                                               slot_bytes, h, status);
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
-}
-
-static int mx4_simple_down_plain(const float *h, int T, int H, int F, int E, int k, const int32_t *ids, const float *weights,
-                          const int32_t *table, int n_slots, const void *pool, size_t slot_bytes, float *partial,
-                          cudaStream_t s) {
-    down_simple<MOE_F32 + 16><<<dim3(T * k, (H + 7) / 8), 256, 0, s>>>({h, nullptr, F}, H, F, E, ids, weights, table,
-                                                                       n_slots, pool, slot_bytes, partial,
-                                                                       moe_status_word_device_ptr());
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
-}
-
+static_assert(MXL_MAX_R <= MOE_MAX_E, "one thread per route and per expert");
 
 namespace {
 
 struct LayerWs {
-    size_t ids, weights, h, partial, total;
+    size_t ctr, ids, weights, xscale, xq, hq, hs, partial, total;
+    size_t ctr_ints;
 };
 
 LayerWs layer_ws(int T, int H, int F, int k) {
     LayerWs L;
-    const size_t R = (size_t)T * k;
+    const size_t R = (size_t)T * k, HB = (H + 127) / 128, FB = (F + 127) / 128;
     size_t o = 0;
     auto take = [&](size_t n) {
         const size_t at = o;
-        o += (n + 255) / 256 * 256;
+        o += (n + 511) / 512 * 512;
         return at;
     };
+    L.ctr_ints = 4 + R + HB;  // ticket, (pad), ready[chunk], done[tile of H]
+    L.ctr = take(L.ctr_ints * 4);
     L.ids = take(R * 4);
     L.weights = take(R * 4);
-    L.h = take(R * F * 4);
+    L.xscale = take((size_t)T * 8);
+    L.xq = take(HB * T * 512);
+    L.hq = take(R * FB * 512);
+    L.hs = take(R * FB * 64);
     L.partial = take(R * H * 4);
     L.total = o;
     return L;
+}
+
+// Code of the radix-8 digit d (0 .. 7 for -4 .. 3).
+__device__ __forceinline__ uint32_t digit_code(uint32_t d) { return (0x5420ACDEu >> (4 * d)) & 15u; }
+
+// ------------------------------------------------------------------ router, digits of x
+
+struct PrepParams {
+    const void *x;
+    const uint16_t *w_router;
+    const float *bias;
+    int T, H, E, k, wide_w, wide_x;
+    int32_t *ids;
+    float *weights;
+    float2 *xscale;
+    uint8_t *xq;
+    int *ctr;
+    int n_ctr;
+};
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+size_t prep_smem(int H, int E, int TT) {
+    const int E8 = (E + 7) / 8 * 8;
+    return ((size_t)H / MXL_CLUSTER * TT + (size_t)(MXL_PREP_THREADS / 32 + 1) * TT * E8 + 16) * 4;
+}
+
+// TT: tokens of a cluster (1, 2, 4 or 8; the last cluster may hold fewer).
+template <int XT, int TT>
+__global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr int NW = MXL_PREP_THREADS / 32;
+    const int rank = (int)cluster_ctarank(), tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    const int HS = p.H / MXL_CLUSTER, h0 = rank * HS, E8 = (p.E + 7) & ~7;
+    const int t0 = blockIdx.y * TT, nt = min(TT, p.T - t0);
+    float *xs = sm;                   // [HS][TT]
+    float *red = xs + HS * TT;        // [NW][TT][E8]
+    float *part = red + NW * TT * E8; // [TT][E8]
+    uint32_t *mx = (uint32_t *)(part + TT * E8);
+    pdl_trigger();
+    pdl_wait();
+    if (blockIdx.y == 0)
+        for (int i = rank * MXL_PREP_THREADS + tid; i < p.n_ctr; i += MXL_CLUSTER * MXL_PREP_THREADS) p.ctr[i] = 0;
+    if (warp < TT) {
+        // this CTA's eighth of token `warp`, and its largest magnitude (as bits: NaN sorts above all)
+        uint32_t m = 0;
+        for (int h = lane; h < HS; h += 32) {
+            float v = 0.f;
+            if (warp < nt) {
+                const size_t at = (size_t)(t0 + warp) * p.H + h0 + h;
+                v = XT == MOE_BF16 ? __bfloat162float(((const __nv_bfloat16 *)p.x)[at]) : ((const float *)p.x)[at];
+            }
+            xs[h * TT + warp] = v;
+            m = max(m, __float_as_uint(v) & 0x7FFFFFFFu);
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) mx[warp] = m;
+    }
+    __syncthreads();
+    // logits: thread (cg, hsub) takes experts 8 cg .. 8 cg + 7 of rows hsub, hsub + NH, ...
+    int ncl = 0;  // log2 of the column groups, a power of two of them
+    while ((8 << ncl) < E8) ++ncl;
+    const int cg = tid & ((1 << ncl) - 1), hsub = tid >> ncl, NH = MXL_PREP_THREADS >> ncl;
+    float acc[TT][8];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[t][j] = 0.f;
+    if (8 * cg < p.E) {
+        const uint16_t *wr = p.w_router + (size_t)h0 * p.E + 8 * cg;
+        const int ne = min(8, p.E - 8 * cg);
+#pragma unroll 4
+        for (int h = hsub; h < HS; h += NH) {
+            float w[8];
+            if (p.wide_w) {
+                const uint4 u = *(const uint4 *)(wr + (size_t)h * p.E);
+                const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = __half22float2(*(const __half2 *)&q[j]);
+                    w[2 * j] = f.x;
+                    w[2 * j + 1] = f.y;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = j < ne ? __half2float(__ushort_as_half(wr[(size_t)h * p.E + j])) : 0.f;
+            }
+            const float *xh = xs + h * TT;
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const float xv = xh[t];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(xv, w[j], acc[t][j]);
+            }
+        }
+    }
+    for (int o = 1 << ncl; o < 32; o <<= 1)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[t][j] += __shfl_xor_sync(0xffffffffu, acc[t][j], o);
+    if (lane < (1 << ncl) && 8 * cg < p.E)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) red[(warp * TT + t) * E8 + 8 * cg + j] = acc[t][j];
+    __syncthreads();
+    for (int i = tid; i < TT * E8; i += MXL_PREP_THREADS) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) s += red[w * TT * E8 + i];
+        part[i] = s;
+    }
+    cluster_sync_all();
+    // token t0 + rank is selected by this CTA's first warp
+    if (warp == 0 && rank < nt) {
+        float v[MOE_MAX_E / 32];
+#pragma unroll
+        for (int i = 0; i < MOE_MAX_E / 32; ++i) {
+            const int e = lane + 32 * i;
+            v[i] = -INFINITY;
+            if (e < p.E) {
+                float s = 0.f;
+#pragma unroll
+                for (int r = 0; r < MXL_CLUSTER; ++r) s += ld_cluster_f32(cluster_map(&part[rank * E8 + e], r));
+                if (p.bias) s += p.bias[e];
+                v[i] = (s != s) ? -INFINITY : s;  // NaN never wins
+            }
+        }
+        select_topk_softmax(v, p.E, p.k, lane, (size_t)(t0 + rank), p.ids, p.weights, 0.f);
+    }
+    // digits: eight columns of one token per thread
+    float m_norm[TT], m_pow[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < MXL_CLUSTER; ++r) m = max(m, ld_cluster_u32(cluster_map(&mx[t], r)));
+        // largest magnitude = norm * pow, norm in [1, 2), pow a power of two (possibly subnormal)
+        const int e = (int)(m >> 23);
+        float norm = __uint_as_float((m & 0x7FFFFFu) | 0x3F800000u), pw = __uint_as_float((uint32_t)e << 23);
+        if (m == 0 || e == 255) {
+            norm = m == 0 ? 1.f : __uint_as_float(0x7FC00000u);
+            pw = 1.f;
+        } else if (e == 0) {
+            const int top = 31 - __clz(m);
+            norm = (float)m / (float)(1u << top);
+            pw = __uint_as_float(1u << top);
+        }
+        m_norm[t] = norm;
+        m_pow[t] = pw;
+        if (rank == 0 && tid == t && t < nt) p.xscale[t0 + t] = make_float2(norm / MXL_XMAX, pw);
+    }
+    const int per = p.H / 8;
+    for (int i = rank * MXL_PREP_THREADS + tid; i < nt * per; i += MXL_CLUSTER * MXL_PREP_THREADS) {
+        const int t = i / per, col = (i - t * per) * 8;
+        float v[8];
+        load8<XT>(p.x, (size_t)(t0 + t) * p.H + col, p.wide_x, v);
+        float norm = m_norm[0], pw = m_pow[0];
+#pragma unroll
+        for (int q = 1; q < TT; ++q)
+            if (t == q) {
+                norm = m_norm[q];
+                pw = m_pow[q];
+            }
+        // x / pow in (-2, 2): by two exact factors where 1 / pow would overflow
+        const float f = MXL_XMAX / norm, i1 = pw < 1e-30f ? 1.2676506e30f : 1.f, i2 = 1.f / (pw * i1);
+        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t u = (uint32_t)(__float2int_rn(v[j] * i1 * i2 * f)) + MXL_BIAS;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] |= digit_code((u >> (3 * q)) & 7u) << (4 * j);
+        }
+        uint8_t *atom = p.xq + ((size_t)(col >> 7) * p.T + t0 + t) * 512;
+        const int c = (col >> 5) & 3, o = 4 * ((col >> 3) & 3);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) *(uint32_t *)(atom + q * 64 + ((c ^ ((q >> 1) & 3)) << 4) + o) = w[q];
+    }
+    cluster_sync_all();  // partial logits and maxima stay until every CTA has read them
+}
+
+// ------------------------------------------------------------------ experts and combine
+
+struct FfnParams {
+    int T, H, F, E, k;
+    const int32_t *ids, *table;
+    const float *weights, *extra;
+    int n_slots;
+    const uint8_t *pool;
+    size_t slot_bytes;
+    const float2 *xscale;
+    const uint8_t *xq;
+    uint8_t *hq;
+    uint32_t *hs;
+    float *partial, *y;
+    int *ticket, *ready, *done;
+    int *status;
+};
+
+template <int NR>
+struct LayerGeom {
+    static constexpr int S = NR == 8 ? 7 : 5;
+    static constexpr int BOFF = MXL_WBYTES, HSOFF = BOFF + 2 * NR * 512;
+    static constexpr int STAGE = HSOFF + 512;
+    static constexpr int N = NR * 8;
+    static constexpr int SFCOL = 2 * N;
+    static constexpr int CTRL = 1024 + 2 * 4 * NR / 2 * 32 * 4 + 5 * MXL_MAX_R * 4 + 1024;
+    static constexpr size_t SMEM = 1024 + (CTRL + 1023) / 1024 * 1024 + (size_t)S * STAGE;
+    static_assert(SFCOL + MXL_SFS * 16 <= 512 && S > MXL_SFS && STAGE % 512 == 0 && SMEM <= 227 * 1024, "budget");
+};
+
+__device__ __forceinline__ int ld_acquire_gpu(const int *a) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// A unit's place: chunk, weight tile, and which product.
+struct Unit {
+    int chunk, m;
+    bool down;
+};
+__device__ __forceinline__ Unit unit_of(int u, int nch, int FT, int HT) {
+    Unit r;
+    r.down = u >= nch * FT;
+    const int v = r.down ? u - nch * FT : u, per = r.down ? HT : FT;
+    r.chunk = v / per;
+    r.m = v - r.chunk * per;
+    return r;
+}
+
+// y[t][rows of tile m] = extra + the partial rows of token t's routes, in route order (`ok`: routes
+// that were computed), by 128 threads.
+__device__ __forceinline__ void combine_tile(const FfnParams &p, int m, int thr, const int *ok) {
+    const int o = 128 * m + thr;
+    if (o >= p.H) return;
+    for (int t = 0; t < p.T; ++t) {
+        float v[MOE_MAX_K];
+#pragma unroll
+        for (int j = 0; j < MOE_MAX_K; ++j)
+            v[j] = j < p.k && ok[t * p.k + j] ? __ldcg(p.partial + (size_t)(t * p.k + j) * p.H + o) : 0.f;
+        float s = p.extra ? p.extra[(size_t)t * p.H + o] : 0.f;
+#pragma unroll
+        for (int j = 0; j < MOE_MAX_K; ++j)
+            if (j < p.k) s += v[j];
+        p.y[(size_t)t * p.H + o] = s;
+    }
+}
+
+template <int NR>
+__global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnParams p) {
+    using G = LayerGeom<NR>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_smem_1024(smem_raw);
+    uint64_t *s_full = (uint64_t *)smem;       // weights and digits of a stage
+    uint64_t *s_empty = s_full + G::S;
+    uint64_t *sf_full = s_empty + G::S;
+    uint64_t *acc_full = sf_full + MXL_SFS;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *q_full = acc_empty + 2;
+    uint64_t *q_empty = q_full + MXL_Q;
+    uint64_t *mma_done = q_empty + MXL_Q;
+    uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
+    volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
+    volatile int *q_unit = (volatile int *)(tmem_slot + 2);  // [MXL_Q]
+    int *s_nch = (int *)(tmem_slot + 2 + MXL_Q);
+    int *s_last = s_nch + 1;
+    int *s_scan = s_nch + 2;                                 // [8]
+    static_assert((2 * G::S + MXL_SFS + 4 + 2 * MXL_Q + 1) * 8 + (2 + MXL_Q + 10) * 4 <= 1024, "barriers");
+    float *xch = (float *)(smem + 1024);                     // [2 buffers][2 pairs][2 ways][NR / 2][32]
+    int *c_slot = (int *)(xch + 2 * 4 * (NR / 2) * 32);      // [MXL_MAX_R] each
+    int *c_pos = c_slot + MXL_MAX_R;
+    int *c_n = c_pos + MXL_MAX_R;
+    int *rows = c_n + MXL_MAX_R;
+    int *r_ok = rows + MXL_MAX_R;                            // ids first, then whether a route is computed
+    uint8_t *ring = smem + (G::CTRL + 1023) / 1024 * 1024;
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid == 0) {
+        for (int s = 0; s < G::S; ++s) {
+            mbar_init(&s_full[s], 2);
+            mbar_init(&s_empty[s], 1);
+        }
+        for (int s = 0; s < MXL_SFS; ++s) mbar_init(&sf_full[s], 4);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 4);
+        }
+        for (int q = 0; q < MXL_Q; ++q) {
+            mbar_init(&q_full[q], 1);
+            mbar_init(&q_empty[q], 10);  // warps 1, 2, 4-7, 8-11
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    // the first unit is claimed while the chunks are put together
+    int claim = 0;
+    if (tid == 0) claim = atomicAdd(p.ticket, 1);
+    const int R = p.T * p.k;
+    int *s_ids = c_slot;  // until the chunks are written
+    if (tid < MXL_MAX_R) s_ids[tid] = tid < R ? p.ids[tid] : -1;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // chunks: thread e counts expert e's routes; exclusive sums give its chunks and positions
+    int cnt = 0, slot = -1, pk = 0, incl = 0;
+    if (tid < MOE_MAX_E) {
+        for (int r = 0; r < R; ++r) cnt += s_ids[r] == tid;
+        if (cnt > 0) {
+            slot = p.table ? p.table[tid] : tid;
+            if (slot < 0 || slot >= p.n_slots) {
+                moe_set_status(p.status, MOE_ERR_INVALID);
+                cnt = 0;
+            }
+        }
+        pk = cnt | ((cnt + NR - 1) / NR) << 16;
+        incl = pk;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        r_ok[tid] = 0;
+    }
+    const int my_ids = tid < MXL_MAX_R ? s_ids[tid] : -1;
+    __syncthreads();
+    if (tid < MOE_MAX_E) {
+        int before = incl - pk;
+        for (int w = 0; w < warp; ++w) before += s_scan[w];
+        if (tid == MOE_MAX_E - 1) *s_nch = (before + pk) >> 16;
+        // route ids move out of the chunk table's space
+        c_n[tid] = my_ids;
+        incl = before;
+    }
+    __syncthreads();
+    if (tid < MOE_MAX_E && cnt > 0) {
+        int at = incl & 0xFFFF;
+        for (int r = 0; r < R; ++r)
+            if (c_n[r] == tid) {
+                rows[at++] = r;
+                r_ok[r] = 1;
+            }
+    }
+    __syncthreads();
+    if (tid < MOE_MAX_E && cnt > 0) {
+        const int c0 = incl >> 16, pos = incl & 0xFFFF, nc = (cnt + NR - 1) / NR;
+        for (int c = 0; c < nc; ++c) {
+            const int a = cnt * c / nc, b = cnt * (c + 1) / nc;
+            c_slot[c0 + c] = slot;
+            c_pos[c0 + c] = pos + a;
+            c_n[c0 + c] = b - a;
+        }
+    }
+    __syncthreads();
+    const int nch = *s_nch;
+    const int HB = (p.H + 127) / 128, FB = (p.F + 127) / 128, FT = (p.F + 63) / 64, HT = HB;
+    const int n_units = nch * (FT + HT);
+    const size_t down_off = mx4_gu_bytes(p.H, p.F);
+
+    // a consumer's next unit (-1: none left; -2: abort)
+    auto next_unit = [&](int i) -> int {
+        const int q = i % MXL_Q;
+        bool ok = mbar_wait_role(&q_full[q], (i / MXL_Q) & 1, p.status, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return -2;
+        const int u = q_unit[q];
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&q_empty[q]);
+        return u;
+    };
+
+    if (nch == 0) {
+        // no expert is resident: the layer is its extra
+        for (int m = blockIdx.x; m < HT; m += gridDim.x)
+            if (tid < 128) combine_tile(p, m, tid, r_ok);
+    } else if (warp == 0) {
+        // ---------------- claims and weights
+        if (lane == 0) {
+            int g = 0;
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                const int q = i % MXL_Q, u = claim < n_units ? claim : -1;
+                if (i >= MXL_Q && !(ok = mbar_wait_role(&q_empty[q], ((i / MXL_Q) & 1) ^ 1, p.status, abort_flag))) break;
+                q_unit[q] = u;
+                mbar_arrive1(&q_full[q]);
+                if (u < 0) break;
+                claim = atomicAdd(p.ticket, 1);
+                const Unit un = unit_of(u, nch, FT, HT);
+                const int KB = un.down ? FB : HB, NKS = (KB + 1) / 2;
+                const uint8_t *w = p.pool + (size_t)c_slot[un.chunk] * p.slot_bytes + (un.down ? down_off : 0) +
+                                   (size_t)un.m * KB * MX4_TB;
+                for (int kc = 0; kc < NKS; ++kc, ++g) {
+                    const int s = g % G::S;
+                    if (g >= G::S && !(ok = mbar_wait_role(&s_empty[s], ((g / G::S) & 1) ^ 1, p.status, abort_flag)))
+                        break;
+                    const uint32_t wb = 2 * kc + 1 < KB ? MXL_WBYTES : MX4_TB;
+                    mbar_arrive_expect_tx(&s_full[s], wb);
+                    bulk_g2s(ring + (size_t)s * G::STAGE, w + (size_t)kc * MXL_WBYTES, wb, &s_full[s]);
+                }
+            }
+            if (!ok) {
+                settle_after_abort();
+            } else {
+                for (int s = 0; s < G::S && s < g; ++s) {
+                    const int last = s + ((g - 1 - s) / G::S) * G::S;
+                    mbar_wait_role(&s_full[s], (last / G::S) & 1, p.status, abort_flag);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- digits
+        int g = 0;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int u = next_unit(i);
+            if (u < 0) {
+                ok = u != -2;
+                break;
+            }
+            const Unit un = unit_of(u, nch, FT, HT);
+            const int KB = un.down ? FB : HB, NKS = (KB + 1) / 2, n = c_n[un.chunk], pos = c_pos[un.chunk];
+            if (un.down) {
+                // every gate/up unit of the chunk is done, its digits and scales written
+                bool rdy = false;
+                for (uint32_t it = 0; it < MOE_SPIN_LIMIT; ++it) {
+                    if (ld_acquire_gpu(&p.ready[un.chunk]) >= FT) {
+                        rdy = true;
+                        break;
+                    }
+                    if (*abort_flag) break;
+                }
+                if (!rdy && !*abort_flag) {
+                    moe_set_status(p.status, MOE_ERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                if (!(ok = __all_sync(0xffffffffu, rdy))) break;
+                fence_proxy_async_all();
+            }
+            // gate/up: lane b n + i copies token i's digits of block b
+            const int tok = !un.down && lane < n ? rows[pos + lane] / p.k : 0;
+            for (int kc = 0; kc < NKS; ++kc, ++g) {
+                const int s = g % G::S;
+                if (g >= G::S) ok = mbar_wait_role(&s_empty[s], ((g / G::S) & 1) ^ 1, p.status, abort_flag);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                uint8_t *st = ring + (size_t)s * G::STAGE;
+                const int nb = min(2, KB - 2 * kc);
+                if (lane == 0) mbar_arrive_expect_tx(&s_full[s], (uint32_t)(nb * (n * 512 + (un.down ? 64 : 0))));
+                __syncwarp();
+                if (!un.down) {
+                    if (lane < n)
+                        for (int b = 0; b < nb; ++b)
+                            bulk_g2s(st + G::BOFF + b * NR * 512 + lane * 512,
+                                     p.xq + ((size_t)(2 * kc + b) * p.T + tok) * 512, 512, &s_full[s]);
+                } else if (lane < nb) {
+                    const int kb = 2 * kc + lane;
+                    bulk_g2s(st + G::BOFF + lane * NR * 512, p.hq + ((size_t)pos * FB + (size_t)kb * n) * 512,
+                             (uint32_t)n * 512u, &s_full[s]);
+                    bulk_g2s(st + G::HSOFF + lane * 64, p.hs + ((size_t)un.chunk * FB + kb) * 16, 64, &s_full[s]);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) settle_after_abort();
+    } else if (warp == 2) {
+        // ---------------- MMA issuer
+        int g = 0;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int u = next_unit(i);
+            if (u < 0) break;
+            if (lane == 0) {
+                const Unit un = unit_of(u, nch, FT, HT);
+                const int K = un.down ? p.F : p.H, NKS = (K + 255) / 256, N = 8 * c_n[un.chunk];
+                const uint32_t id0 = umma_idesc_mxf4(128, N, 0), id2 = umma_idesc_mxf4(128, N, 2);
+                const int buf = i & 1;
+                if (i >= 2) ok = mbar_wait_role(&acc_empty[buf], ((i / 2) - 1) & 1, p.status, abort_flag);
+                tc_fence_after();
+                const uint32_t d = tmem + buf * G::N;
+                for (int kc = 0; kc < NKS && ok; ++kc, ++g) {
+                    const int s = g % G::S, f = g % MXL_SFS;
+                    if (!(ok = mbar_wait_role(&sf_full[f], (g / MXL_SFS) & 1, p.status, abort_flag))) break;
+                    if (!(ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(ring + (size_t)s * G::STAGE);
+                    const uint64_t a = umma_desc_sw64(st), b = umma_desc_sw64(st + G::BOFF);
+                    const uint32_t sf = tmem + G::SFCOL + 16 * f;
+                    const int steps = min(4, (K - 256 * kc + 63) / 64);
+                    constexpr int A1 = MX4_TB >> 4, B1 = NR * 512 >> 4;
+                    umma_mxf4(d, a, b, id0, sf, sf + 8, kc > 0);
+                    if (steps > 1) umma_mxf4(d, a + 2, b + 2, id2, sf, sf + 8, 1);
+                    if (steps > 2) umma_mxf4(d, a + A1, b + B1, id0, sf + 4, sf + 12, 1);
+                    if (steps > 3) umma_mxf4(d, a + A1 + 2, b + B1 + 2, id2, sf + 4, sf + 12, 1);
+                    umma_commit(&s_empty[s]);
+                }
+                if (ok) umma_commit(&acc_full[buf]);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);  // the warp waits for its issuing thread
+        }
+        __syncwarp();
+        if (lane == 0) {
+            umma_commit(mma_done);
+            mbar_wait_bounded(mma_done, 0, p.status);
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ---------------- scales: the weights' rows lane, lane + 32, ..; a route's for its 8 columns
+        const uint32_t t0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::SFCOL;
+        int g = 0;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int u = next_unit(i);
+            if (u < 0) break;
+            const Unit un = unit_of(u, nch, FT, HT);
+            const int KB = un.down ? FB : HB, NKS = (KB + 1) / 2;
+            for (int kc = 0; kc < NKS; ++kc, ++g) {
+                const int s = g % G::S, f = g % MXL_SFS;
+                if (g >= MXL_SFS)
+                    ok = mbar_wait_role(&s_empty[(g - MXL_SFS) % G::S], ((g - MXL_SFS) / G::S) & 1, p.status, abort_flag);
+                if (ok) ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                const uint8_t *st = ring + (size_t)s * G::STAGE;
+                const bool two = 2 * kc + 1 < KB;
+                const uint4 a = *(const uint4 *)(st + 8192 + 16 * lane);
+                uint4 b = make_uint4(0, 0, 0, 0);
+                if (two) b = *(const uint4 *)(st + MX4_TB + 8192 + 16 * lane);
+                uint32_t va[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, vb[8];
+                const uint32_t *hs = (const uint32_t *)(st + G::HSOFF) + (lane >> 3);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    vb[c] = un.down ? hs[4 * c] : 0x7F7F7F7Fu;
+                    vb[4 + c] = un.down ? (two ? hs[16 + 4 * c] : 0u) : 0x7F7F7F7Fu;
+                }
+                tmem_st8(t0 + 16 * f, va);
+                tmem_st8(t0 + 16 * f + 8, vb);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&sf_full[f]);
+            }
+        }
+    } else if (warp >= 8) {
+        // ---------------- epilogue
+        const int q = warp & 3, ew = tid - 256;
+        const float pow8[8] = {1.f, 8.f, 64.f, 512.f, 4096.f, 32768.f, 262144.f, 2097152.f};
+        for (int i = 0;; ++i) {
+            const int u = next_unit(i);
+            bool ok = u != -2;
+            Unit un = {0, 0, false};
+            if (u >= 0) {
+                un = unit_of(u, nch, FT, HT);
+                ok = mbar_wait_role(&acc_full[i & 1], (i / 2) & 1, p.status, abort_flag);
+            }
+            if (!bar_and_n(1, 128, ok) || u < 0) break;
+            tc_fence_after();
+            const int buf = i & 1, n = c_n[un.chunk], pos = c_pos[un.chunk];
+            const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * G::N;
+            if (!un.down) {
+                // route i's gate (lane quarters 0, 1) and up (2, 3) values; the gate warps finish the even
+                // routes, the up warps the odd ones
+                float mine[NR / 2];
+                float *xb = xch + (size_t)((buf * 2 + (q & 1)) * 2) * (NR / 2) * 32 + lane;
+                float *out = xb + (q < 2 ? 1 : 0) * (NR / 2) * 32, *in = xb + (q < 2 ? 0 : 1) * (NR / 2) * 32;
+#pragma unroll
+                for (int c = 0; c < NR / 2; ++c) {
+                    if (2 * c < n) {
+                        uint32_t v[16];
+                        tmem_ld16(tb + 16 * c, v);
+                        tmem_ld_wait();
+                        float a = __uint_as_float(v[0]), b = __uint_as_float(v[8]);
+#pragma unroll
+                        for (int d = 1; d < 8; ++d) {
+                            a = fmaf(__uint_as_float(v[d]), pow8[d], a);
+                            b = fmaf(__uint_as_float(v[8 + d]), pow8[d], b);
+                        }
+                        mine[c] = q < 2 ? a : b;
+                        out[32 * c] = q < 2 ? b : a;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&acc_empty[buf]);
+                bar_sync_n(2 + (q & 1), 64);
+                const int f0 = 64 * un.m + 32 * (q & 1), kb = f0 >> 7, cb = (f0 >> 5) & 3;
+#pragma unroll
+                for (int c = 0; c < NR / 2; ++c) {
+                    const int r = 2 * c + (q >> 1);
+                    if (r < n) {
+                        const float2 xs = p.xscale[rows[pos + r] / p.k];
+                        const float other = in[32 * c];
+                        const float gv = (q < 2 ? mine[c] : other) * xs.x * xs.y;
+                        const float uv = (q < 2 ? other : mine[c]) * xs.x * xs.y;
+                        const float h = gv / (1.0f + expf(-gv)) * uv;
+                        const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23);
+                        const int sc = e == 255 ? 255 : max(0, e - 21);
+                        uint32_t dg = MXL_BIAS;
+                        if (e != 255) dg += (uint32_t)__float2int_rn(h * e8m0_inverse(sc));
+                        uint32_t w = 0;
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) w |= digit_code((dg >> (3 * d)) & 7u) << (4 * d);
+                        // lane 8a + b: digit b of columns 8a .. 8a + 7
+                        uint32_t y = __shfl_xor_sync(0xffffffffu, w, 4);
+                        w = lane & 4 ? (w & 0xFFFF0000u) | (y >> 16) : (w & 0x0000FFFFu) | (y << 16);
+                        y = __shfl_xor_sync(0xffffffffu, w, 2);
+                        w = lane & 2 ? (w & 0xFF00FF00u) | ((y >> 8) & 0x00FF00FFu) : (w & 0x00FF00FFu) | ((y & 0x00FF00FFu) << 8);
+                        y = __shfl_xor_sync(0xffffffffu, w, 1);
+                        w = lane & 1 ? (w & 0xF0F0F0F0u) | ((y >> 4) & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | ((y & 0x0F0F0F0Fu) << 4);
+                        const int d = lane & 7;
+                        uint8_t *atom = p.hq + ((size_t)pos * FB + (size_t)kb * n + r) * 512;
+                        *(uint32_t *)(atom + d * 64 + ((cb ^ ((d >> 1) & 3)) << 4) + 4 * (lane >> 3)) = w;
+                        if (lane == 0) ((uint8_t *)(p.hs + ((size_t)un.chunk * FB + kb) * 16 + r))[cb] = (uint8_t)sc;
+                    }
+                }
+                fence_proxy_async_all();
+                bar_sync_n(1, 128);
+                if (ew == 0) {
+                    __threadfence();
+                    atomicAdd(&p.ready[un.chunk], 1);
+                }
+            } else {
+                const int o = 128 * un.m + 32 * q + lane;
+#pragma unroll
+                for (int c = 0; c < NR / 2; ++c) {
+                    if (2 * c < n) {
+                        uint32_t v[16];
+                        tmem_ld16(tb + 16 * c, v);
+                        tmem_ld_wait();
+                        float a[2] = {__uint_as_float(v[0]), __uint_as_float(v[8])};
+#pragma unroll
+                        for (int d = 1; d < 8; ++d) {
+                            a[0] = fmaf(__uint_as_float(v[d]), pow8[d], a[0]);
+                            a[1] = fmaf(__uint_as_float(v[8 + d]), pow8[d], a[1]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (2 * c + j < n && o < p.H) {
+                                const int r = rows[pos + 2 * c + j];
+                                p.partial[(size_t)r * p.H + o] = p.weights[r] * a[j];
+                            }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&acc_empty[buf]);
+                bar_sync_n(1, 128);
+                if (ew == 0) {
+                    __threadfence();
+                    *s_last = atomicAdd(&p.done[un.m], 1) == nch - 1;
+                    __threadfence();
+                }
+                bar_sync_n(1, 128);
+                if (*(volatile int *)s_last) combine_tile(p, un.m, ew, r_ok);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+template <int XT, int TT>
+int launch_prep_t(const PrepParams &p, cudaStream_t s) {
+    const size_t smem = prep_smem(p.H, p.E, TT);
+    if (smem > 200 * 1024) return MOE_ERR_UNSUPPORTED;
+    if (smem > 48 * 1024)
+        MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_prep_kernel<XT, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          (int)smem));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    moe_pdl_config(&cfg, attr, dim3(MXL_CLUSTER, (p.T + TT - 1) / TT), dim3(MXL_PREP_THREADS), smem, s);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = MXL_CLUSTER;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_prep_kernel<XT, TT>, p));
+    return MOE_OK;
+}
+
+template <int XT>
+int launch_prep(const PrepParams &p, cudaStream_t s) {
+    if (p.T == 1) return launch_prep_t<XT, 1>(p, s);
+    if (p.T == 2) return launch_prep_t<XT, 2>(p, s);
+    if (p.T <= 4) return launch_prep_t<XT, 4>(p, s);
+    return launch_prep_t<XT, MXL_TOKENS>(p, s);
+}
+
+template <int NR>
+int launch_layer_t(const FfnParams &p, cudaStream_t s) {
+    using G = LayerGeom<NR>;
+    static std::mutex mu;
+    static int sms[64] = {0};
+    int dev = -1, n = 0;
+    MOE_TRY_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!sms[dev]) {
+            MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_layer_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              (int)G::SMEM));
+            MOE_TRY_CUDA(cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev));
+        }
+        n = sms[dev];
+    }
+    const long chunks = (long)p.T * p.k;
+    const long units = chunks * ((p.F + 63) / 64 + (p.H + 127) / 128);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<long>(units, n)), dim3(MXL_THREADS), G::SMEM, s);
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_layer_kernel<NR>, p));
+    return MOE_OK;
 }
 
 }  // namespace
@@ -172,17 +830,40 @@ extern "C" int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int 
     if ((rc = mx4_pool_check(H, F, n_slots, pool, slot_bytes)) != MOE_OK) return rc;
     const LayerWs L = layer_ws(T, H, F, k);
     uint8_t *w = (uint8_t *)workspace;
-    if (!ids) ids = (int32_t *)(w + L.ids);
-    if (!weights) weights = (float *)(w + L.weights);
-    float *h = (float *)(w + L.h), *partial = (float *)(w + L.partial);
     cudaStream_t st = moe_cuda_stream(s);
-    if ((rc = moe_router_topk(x, xtype, T, H, w_router, bias, E, k, ids, weights, nullptr, s)) != MOE_OK) return rc;
-    MOE_TRY_CUDA(cudaMemsetAsync(partial, 0, (size_t)T * k * H * 4, st));
-    if ((rc = mx4_simple_gateup_plain(x, xtype, T, H, F, E, k, ids, d_slot_table, n_slots, pool, slot_bytes, h, st)) !=
-        MOE_OK)
-        return rc;
-    if ((rc = mx4_simple_down_plain(h, T, H, F, E, k, ids, weights, d_slot_table, n_slots, pool, slot_bytes, partial,
-                                    st)) != MOE_OK)
-        return rc;
-    return moe_combine(partial, T, k, H, extra, y, s);
+    PrepParams a;
+    a.x = x;
+    a.w_router = w_router;
+    a.bias = bias;
+    a.T = T; a.H = H; a.E = E; a.k = k;
+    a.wide_w = E % 8 == 0 && ((uintptr_t)w_router & 15) == 0;
+    a.wide_x = ((uintptr_t)x & 15) == 0;
+    a.ids = ids ? ids : (int32_t *)(w + L.ids);
+    a.weights = weights ? weights : (float *)(w + L.weights);
+    a.xscale = (float2 *)(w + L.xscale);
+    a.xq = w + L.xq;
+    a.ctr = (int *)(w + L.ctr);
+    a.n_ctr = (int)L.ctr_ints;
+    FfnParams b;
+    b.T = T; b.H = H; b.F = F; b.E = E; b.k = k;
+    b.ids = a.ids;
+    b.table = d_slot_table;
+    b.weights = a.weights;
+    b.extra = extra;
+    b.n_slots = n_slots;
+    b.pool = (const uint8_t *)pool;
+    b.slot_bytes = slot_bytes;
+    b.xscale = a.xscale;
+    b.xq = a.xq;
+    b.hq = w + L.hq;
+    b.hs = (uint32_t *)(w + L.hs);
+    b.partial = (float *)(w + L.partial);
+    b.y = y;
+    b.ticket = a.ctr;
+    b.ready = a.ctr + 4;
+    b.done = b.ready + (size_t)T * k;
+    b.status = moe_status_word_device_ptr();
+    rc = xtype == MOE_BF16 ? launch_prep<MOE_BF16>(a, st) : launch_prep<MOE_F32>(a, st);
+    if (rc != MOE_OK) return rc;
+    return T <= 8 ? launch_layer_t<8>(b, st) : launch_layer_t<16>(b, st);
 }
