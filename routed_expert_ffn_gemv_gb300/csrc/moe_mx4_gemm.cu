@@ -19,9 +19,7 @@
 //      warps 4-7   the stage's scales into tensor memory: the weights' from the landed blocks, the
 //                  routes' from global memory (loaded a stage ahead).  Each warp writes its own
 //                  lane quarter (the tensor core reads a copy in each);
-//      warps 8-11  the epilogue of the previous item from the other accumulator: gate/up tiles hold
-//                  64 gate rows in lanes 0-63 and the same up rows in 64-127, the up quarters hand
-//                  their values over through shared memory.
+//      warps 8-15  the epilogue of the previous item from the other accumulator.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -31,8 +29,8 @@
 #include "moe_mx4_gemm.cuh"
 #include "moe_tc.cuh"
 
-#define MXG_THREADS 384
-#define MXG_CTRL 13312
+#define MXG_THREADS 512
+#define MXG_CTRL 23552
 #define MXG_WBYTES (2 * MX4_TB)  // weights of a stage: two tile blocks
 #define MXG_ROUTE_THREADS 1024
 #define MXG_ROUTE_CLUSTER 8
@@ -224,10 +222,10 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     static_assert((2 * G::S + G::SFS + 6) * 8 <= 1024, "barriers");
-    float *xch = (float *)(smem + 1024);         // [2 pairs][2 slots][16 columns][32 lanes]
-    int *e_route = (int *)(smem + 1024 + 8192);  // [2 accumulators][NT]
-    float *e_w = (float *)(e_route + 2 * NT);
-    static_assert(1024 + 8192 + 4 * NT * 4 <= MXG_CTRL, "control block");
+    float *xch = (float *)(smem + 1024);             // [4 pairs][2 slots][2 ways][8 columns][32 lanes]
+    uint8_t **e_row = (uint8_t **)(smem + 1024 + 16384);  // [2 accumulators][NT] output rows
+    float *e_w = (float *)(e_row + 2 * NT);          // [2 accumulators][NT]
+    static_assert(1024 + 16384 + 2 * NT * 12 <= MXG_CTRL && MXG_CTRL % 1024 == 0, "control block");
     uint8_t *ring = smem + MXG_CTRL;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -239,7 +237,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
         for (int s = 0; s < G::SFS; ++s) mbar_init(&sf_full[s], 4);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 4);
+            mbar_init(&acc_empty[b], 8);
         }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
@@ -385,58 +383,63 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
             }
         }
     } else if (warp >= 8) {
-        // ---------------- epilogue: lane quarter q, lane = weight row 32 q + lane of the tile
-        const int q = warp & 3, ew = warp - 8;
+        // ---------------- epilogue: lane quarter q, lane = weight row 32 q + lane of the tile; the two
+        // warps of a quarter take alternate groups of 16 routes.  Every output row's address is looked
+        // up once per item.  Gate/up: lanes 0-63 hold gate rows, 64-127 the same up rows; a gate warp
+        // and its up warp trade halves of the 16 routes, so that both work on SwiGLU.
+        const int q = warp & 3, ew = warp - 8, half = ew >> 2;
+        constexpr int ES = OT == MOE_BF16 ? 2 : 4;
         int jl = 0, xs = 0;
         bool ok = true;
         for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
             const int c = j / MT, m = j % MT;
             if (p.c_slot[c] < 0) continue;
             const int pos0 = p.c_pos[c], n = p.c_n[c], buf = jl & 1;
-            for (int i = ew * 32 + lane; i < n; i += 128) {
+            for (int i = ew * 32 + lane; i < n; i += 256) {
                 const int r = p.rows[pos0 + i];
-                e_route[buf * NT + i] = r;
+                e_row[buf * NT + i] = (uint8_t *)p.out + (size_t)r * p.R_out * ES;
                 if (DOWN) e_w[buf * NT + i] = p.weights[r];
             }
             const bool w = mbar_wait_role(&acc_full[buf], (jl / 2) & 1, p.status, abort_flag);
-            if (!(ok = bar_and_n(1, 128, w))) break;
+            if (!(ok = bar_and_n(1, 256, w))) break;
             tc_fence_after();
             const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * NT;
-            for (int c0 = 0; c0 < n; c0 += 16, ++xs) {
+            for (int c0 = 16 * half; c0 < n; c0 += 32, ++xs) {
                 uint32_t v[16];
                 tmem_ld16(tb + c0, v);
                 tmem_ld_wait();
-                const int nn = min(16, n - c0);
-                const int *rt = e_route + buf * NT + c0;
+                uint8_t *const *row = e_row + buf * NT + c0;
                 if (!DOWN) {
-                    float *xb = xch + (size_t)((q & 1) * 2 + (xs & 1)) * 512 + lane;
-                    if (q >= 2)
+                    // the gate warp keeps routes 0-7 of the group and hands over 8-15, the up warp the
+                    // other way round
+                    const int pair = (q & 1) + 2 * half, up = q >> 1;
+                    float *xb = xch + (size_t)(pair * 2 + (xs & 1)) * 512 + lane;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) xb[32 * i] = __uint_as_float(v[i]);
-                    bar_sync_n(2 + (q & 1), 64);
-                    const int f = 64 * m + 32 * q + lane;
-                    if (q < 2 && f < p.R_out) {
-                        float h[16];
+                    for (int i = 0; i < 8; ++i) xb[256 * up + 32 * i] = __uint_as_float(up ? v[i] : v[8 + i]);
+                    bar_sync_n(2 + pair, 64);
+                    const int f = 64 * m + 32 * (q & 1) + lane, nn = min(8, n - c0 - 8 * up);
+                    float h[8];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float gv = __uint_as_float(v[i]);
-                            h[i] = gv / (1.0f + __expf(-gv)) * xb[32 * i];
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i < nn) {
-                                const size_t at = (size_t)rt[i] * p.R_out + f;
-                                if (OT == MOE_BF16) ((__nv_bfloat16 *)p.out)[at] = __float2bfloat16(h[i]);
-                                else ((float *)p.out)[at] = h[i];
-                            }
+                    for (int i = 0; i < 8; ++i) {
+                        const float other = xb[256 * (1 - up) + 32 * i];
+                        const float gv = up ? other : __uint_as_float(v[i]);
+                        const float uv = up ? __uint_as_float(v[8 + i]) : other;
+                        h[i] = __fdividef(gv, 1.0f + expf(-gv)) * uv;
                     }
+                    if (f < p.R_out)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i < nn) {
+                                if (OT == MOE_BF16) ((__nv_bfloat16 *)row[8 * up + i])[f] = __float2bfloat16(h[i]);
+                                else ((float *)row[8 * up + i])[f] = h[i];
+                            }
                 } else {
-                    const int o = 128 * m + 32 * q + lane;
+                    const int o = 128 * m + 32 * q + lane, nn = min(16, n - c0);
                     const float *wt = e_w + buf * NT + c0;
                     if (o < p.R_out)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (i < nn) ((float *)p.out)[(size_t)rt[i] * p.R_out + o] = wt[i] * __uint_as_float(v[i]);
+                            if (i < nn) ((float *)row[i])[o] = wt[i] * __uint_as_float(v[i]);
                 }
             }
             tc_fence_before();

@@ -14,7 +14,7 @@
 //    partial logits meet over distributed shared memory, one warp selects), the tokens' digits in
 //    operand order, and the counters of the second kernel.
 //  * mx4_layer_kernel: persistent.  Units: (chunk of at most NR routes of one expert, 128-row weight
-//    tile) of gate/up, then of down.  CTAs take units in order from a counter, so a down unit only
+//    tile) of gate/up, then of down, then (tile of H, eight tokens) of the combine.  CTAs take units in order from a counter, so a down unit only
 //    ever waits for gate/up units that running CTAs hold: no co-residency is needed, and other work
 //    on the GPU cannot deadlock it.  Roles as in the grouped product, with
 //      warp 0      claims units, copies the weights (17 KB a stage: bound by HBM),
@@ -23,8 +23,9 @@
 //      warp 2      the MMAs, warps 4-7 the scales,
 //      warps 8-11  gate/up: sum_p, SwiGLU, the digits and scales of h (a block of 32 columns is a
 //                  warp: one reduction; an 8x8 nibble transpose by three shuffles); down: sum_p, the
-//                  router weight, partial rows; the CTA that completes a tile of H adds the partial
-//                  rows in route order onto extra.
+//                  router weight, partial rows.  Units after the last down unit add the partial rows of
+//                  a tile of H in route order onto extra;
+//      warp 3      publishes finished units to the other CTAs.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -40,6 +41,7 @@
 #define MXL_THREADS 384
 #define MXL_SFS 4             // scale slots in tensor memory, 16 columns each
 #define MXL_Q 4               // claimed units in flight in a CTA
+#define MXL_PUB (2 * MXL_Q)   // the epilogue may be MXL_Q units ahead of warp 3 and of a queue slot's reuse
 #define MXL_MAX_R (MOE_DECODE_MAX_T * MOE_MAX_K)
 #define MXL_XMAX 7190000.0f   // <= 3 (8^8 - 1) / 7
 #define MXL_BIAS 9586980u     // 4 (8^8 - 1) / 7: turns digits -4 .. 3 into 0 .. 7
@@ -296,38 +298,69 @@ __device__ __forceinline__ int ld_acquire_gpu(const int *a) {
     asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ void red_release_gpu(int *a) {
+    asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.s32 [%0], 1;" ::"l"(a) : "memory");
+}
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// A unit's place: chunk, weight tile, and which product.
+// A unit: gate/up or down tile m of a chunk, or (last) tile m of y for tokens 8 c .. 8 c + 7.
+enum { MXL_UP = 0, MXL_DOWN = 1, MXL_COMBINE = 2 };
 struct Unit {
-    int chunk, m;
-    bool down;
+    int kind, c, m;
 };
 __device__ __forceinline__ Unit unit_of(int u, int nch, int FT, int HT) {
     Unit r;
-    r.down = u >= nch * FT;
-    const int v = r.down ? u - nch * FT : u, per = r.down ? HT : FT;
-    r.chunk = v / per;
-    r.m = v - r.chunk * per;
+    r.kind = u < nch * FT ? MXL_UP : u < nch * (FT + HT) ? MXL_DOWN : MXL_COMBINE;
+    const int v = r.kind == MXL_UP ? u : r.kind == MXL_DOWN ? u - nch * FT : u - nch * (FT + HT);
+    const int per = r.kind == MXL_UP ? FT : HT;
+    r.c = v / per;
+    r.m = v - r.c * per;
     return r;
 }
 
-// y[t][rows of tile m] = extra + the partial rows of token t's routes, in route order (`ok`: routes
-// that were computed), by 128 threads.
-__device__ __forceinline__ void combine_tile(const FfnParams &p, int m, int thr, const int *ok) {
-    const int o = 128 * m + thr;
+// y[t][columns of tile m] = extra + the partial rows of token t's routes, in route order (`ok`: routes
+// that were computed), for eight tokens by 128 threads: four columns of a token to a thread.
+__device__ __forceinline__ void combine_tile(const FfnParams &p, int m, int t0, int thr, const int *ok) {
+    const int o = 128 * m + 4 * (thr & 31);
     if (o >= p.H) return;
-    for (int t = 0; t < p.T; ++t) {
-        float v[MOE_MAX_K];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = t0 + (thr >> 5) + 4 * i;
+        if (t >= p.T) break;
+        float4 v[MOE_MAX_K];
 #pragma unroll
         for (int j = 0; j < MOE_MAX_K; ++j)
-            v[j] = j < p.k && ok[t * p.k + j] ? __ldcg(p.partial + (size_t)(t * p.k + j) * p.H + o) : 0.f;
-        float s = p.extra ? p.extra[(size_t)t * p.H + o] : 0.f;
+            v[j] = j < p.k && ok[t * p.k + j] ? __ldcg((const float4 *)(p.partial + (size_t)(t * p.k + j) * p.H + o))
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        const size_t at = (size_t)t * p.H + o;
+        if (p.extra)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s[q] = p.extra[at + q];
 #pragma unroll
         for (int j = 0; j < MOE_MAX_K; ++j)
-            if (j < p.k) s += v[j];
-        p.y[(size_t)t * p.H + o] = s;
+            if (j < p.k) {
+                s[0] += v[j].x;
+                s[1] += v[j].y;
+                s[2] += v[j].z;
+                s[3] += v[j].w;
+            }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p.y[at + q] = s[q];
     }
+}
+
+// Bounded wait of a warp until *a >= want (counted up by other CTAs that are running).
+__device__ __forceinline__ bool wait_count(const int *a, int want, int *status, volatile int *abort_flag) {
+    bool ok = false;
+    for (uint32_t it = 0; it < MOE_SPIN_LIMIT; ++it) {
+        if ((ok = ld_acquire_gpu(a) >= want) || *abort_flag) break;
+    }
+    if (!ok && !*abort_flag) {
+        moe_set_status(status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
 template <int NR>
@@ -342,14 +375,14 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
     uint64_t *acc_empty = acc_full + 2;
     uint64_t *q_full = acc_empty + 2;
     uint64_t *q_empty = q_full + MXL_Q;
-    uint64_t *mma_done = q_empty + MXL_Q;
+    uint64_t *pub = q_empty + MXL_Q;           // a unit's outputs are written (4 epilogue warps)
+    uint64_t *mma_done = pub + MXL_PUB;
     uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *q_unit = (volatile int *)(tmem_slot + 2);  // [MXL_Q]
     int *s_nch = (int *)(tmem_slot + 2 + MXL_Q);
-    int *s_last = s_nch + 1;
-    int *s_scan = s_nch + 2;                                 // [8]
-    static_assert((2 * G::S + MXL_SFS + 4 + 2 * MXL_Q + 1) * 8 + (2 + MXL_Q + 10) * 4 <= 1024, "barriers");
+    int *s_scan = s_nch + 1;                                 // [8]
+    static_assert((2 * G::S + MXL_SFS + 4 + 2 * MXL_Q + MXL_PUB + 1) * 8 + (2 + MXL_Q + 9) * 4 <= 1024, "barriers");
     float *xch = (float *)(smem + 1024);                     // [2 buffers][2 pairs][2 ways][NR / 2][32]
     int *c_slot = (int *)(xch + 2 * 4 * (NR / 2) * 32);      // [MXL_MAX_R] each
     int *c_pos = c_slot + MXL_MAX_R;
@@ -371,8 +404,9 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
         }
         for (int q = 0; q < MXL_Q; ++q) {
             mbar_init(&q_full[q], 1);
-            mbar_init(&q_empty[q], 10);  // warps 1, 2, 4-7, 8-11
+            mbar_init(&q_empty[q], 11);  // every warp but warp 0
         }
+        for (int q = 0; q < MXL_PUB; ++q) mbar_init(&pub[q], 4);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -445,7 +479,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
     __syncthreads();
     const int nch = *s_nch;
     const int HB = (p.H + 127) / 128, FB = (p.F + 127) / 128, FT = (p.F + 63) / 64, HT = HB;
-    const int n_units = nch * (FT + HT);
+    const int n_units = nch * (FT + HT) + HT * ((p.T + 7) / 8);
     const size_t down_off = mx4_gu_bytes(p.H, p.F);
 
     // a consumer's next unit (-1: none left; -2: abort)
@@ -463,7 +497,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
     if (nch == 0) {
         // no expert is resident: the layer is its extra
         for (int m = blockIdx.x; m < HT; m += gridDim.x)
-            if (tid < 128) combine_tile(p, m, tid, r_ok);
+            if (tid < 128)
+                for (int t = 0; t < p.T; t += 8) combine_tile(p, m, t, tid, r_ok);
     } else if (warp == 0) {
         // ---------------- claims and weights
         if (lane == 0) {
@@ -477,8 +512,10 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
                 if (u < 0) break;
                 claim = atomicAdd(p.ticket, 1);
                 const Unit un = unit_of(u, nch, FT, HT);
-                const int KB = un.down ? FB : HB, NKS = (KB + 1) / 2;
-                const uint8_t *w = p.pool + (size_t)c_slot[un.chunk] * p.slot_bytes + (un.down ? down_off : 0) +
+                if (un.kind == MXL_COMBINE) continue;
+                const bool down = un.kind == MXL_DOWN;
+                const int KB = down ? FB : HB, NKS = (KB + 1) / 2;
+                const uint8_t *w = p.pool + (size_t)c_slot[un.c] * p.slot_bytes + (down ? down_off : 0) +
                                    (size_t)un.m * KB * MX4_TB;
                 for (int kc = 0; kc < NKS; ++kc, ++g) {
                     const int s = g % G::S;
@@ -509,35 +546,25 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
                 break;
             }
             const Unit un = unit_of(u, nch, FT, HT);
-            const int KB = un.down ? FB : HB, NKS = (KB + 1) / 2, n = c_n[un.chunk], pos = c_pos[un.chunk];
-            if (un.down) {
+            if (un.kind == MXL_COMBINE) continue;
+            const bool down = un.kind == MXL_DOWN;
+            const int KB = down ? FB : HB, NKS = (KB + 1) / 2, n = c_n[un.c], pos = c_pos[un.c];
+            if (down) {
                 // every gate/up unit of the chunk is done, its digits and scales written
-                bool rdy = false;
-                for (uint32_t it = 0; it < MOE_SPIN_LIMIT; ++it) {
-                    if (ld_acquire_gpu(&p.ready[un.chunk]) >= FT) {
-                        rdy = true;
-                        break;
-                    }
-                    if (*abort_flag) break;
-                }
-                if (!rdy && !*abort_flag) {
-                    moe_set_status(p.status, MOE_ERR_TIMEOUT);
-                    *abort_flag = 1;
-                }
-                if (!(ok = __all_sync(0xffffffffu, rdy))) break;
+                if (!(ok = wait_count(&p.ready[un.c], FT, p.status, abort_flag))) break;
                 fence_proxy_async_all();
             }
-            // gate/up: lane b n + i copies token i's digits of block b
-            const int tok = !un.down && lane < n ? rows[pos + lane] / p.k : 0;
+            // gate/up: lane i copies the digits of the chunk's token i
+            const int tok = !down && lane < n ? rows[pos + lane] / p.k : 0;
             for (int kc = 0; kc < NKS; ++kc, ++g) {
                 const int s = g % G::S;
                 if (g >= G::S) ok = mbar_wait_role(&s_empty[s], ((g / G::S) & 1) ^ 1, p.status, abort_flag);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 uint8_t *st = ring + (size_t)s * G::STAGE;
                 const int nb = min(2, KB - 2 * kc);
-                if (lane == 0) mbar_arrive_expect_tx(&s_full[s], (uint32_t)(nb * (n * 512 + (un.down ? 64 : 0))));
+                if (lane == 0) mbar_arrive_expect_tx(&s_full[s], (uint32_t)(nb * (n * 512 + (down ? 64 : 0))));
                 __syncwarp();
-                if (!un.down) {
+                if (!down) {
                     if (lane < n)
                         for (int b = 0; b < nb; ++b)
                             bulk_g2s(st + G::BOFF + b * NR * 512 + lane * 512,
@@ -546,7 +573,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
                     const int kb = 2 * kc + lane;
                     bulk_g2s(st + G::BOFF + lane * NR * 512, p.hq + ((size_t)pos * FB + (size_t)kb * n) * 512,
                              (uint32_t)n * 512u, &s_full[s]);
-                    bulk_g2s(st + G::HSOFF + lane * 64, p.hs + ((size_t)un.chunk * FB + kb) * 16, 64, &s_full[s]);
+                    bulk_g2s(st + G::HSOFF + lane * 64, p.hs + ((size_t)un.c * FB + kb) * 16, 64, &s_full[s]);
                 }
                 __syncwarp();
             }
@@ -559,9 +586,10 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
         for (int i = 0; ok; ++i) {
             const int u = next_unit(i);
             if (u < 0) break;
+            const Unit un = unit_of(u, nch, FT, HT);
+            if (un.kind == MXL_COMBINE) continue;  // these come last: units before them keep their numbering
             if (lane == 0) {
-                const Unit un = unit_of(u, nch, FT, HT);
-                const int K = un.down ? p.F : p.H, NKS = (K + 255) / 256, N = 8 * c_n[un.chunk];
+                const int K = un.kind == MXL_DOWN ? p.F : p.H, NKS = (K + 255) / 256, N = 8 * c_n[un.c];
                 const uint32_t id0 = umma_idesc_mxf4(128, N, 0), id2 = umma_idesc_mxf4(128, N, 2);
                 const int buf = i & 1;
                 if (i >= 2) ok = mbar_wait_role(&acc_empty[buf], ((i / 2) - 1) & 1, p.status, abort_flag);
@@ -592,6 +620,23 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
             umma_commit(mma_done);
             mbar_wait_bounded(mma_done, 0, p.status);
         }
+    } else if (warp == 3) {
+        // ---------------- publishes finished units: rows of h for the chunk's down units, partial rows
+        // for the tile's combine
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int u = next_unit(i);
+            if (u < 0) break;
+            const Unit un = unit_of(u, nch, FT, HT);
+            if (un.kind == MXL_COMBINE) continue;
+            ok = mbar_wait_role(&pub[i % MXL_PUB], (i / MXL_PUB) & 1, p.status, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (lane == 0) {
+                fence_proxy_async_all();
+                red_release_gpu(un.kind == MXL_UP ? &p.ready[un.c] : &p.done[un.m]);
+            }
+            __syncwarp();
+        }
     } else if (warp >= 4 && warp < 8) {
         // ---------------- scales: the weights' rows lane, lane + 32, ..; a route's for its 8 columns
         const uint32_t t0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::SFCOL;
@@ -601,7 +646,9 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
             const int u = next_unit(i);
             if (u < 0) break;
             const Unit un = unit_of(u, nch, FT, HT);
-            const int KB = un.down ? FB : HB, NKS = (KB + 1) / 2;
+            if (un.kind == MXL_COMBINE) continue;
+            const bool down = un.kind == MXL_DOWN;
+            const int KB = down ? FB : HB, NKS = (KB + 1) / 2;
             for (int kc = 0; kc < NKS; ++kc, ++g) {
                 const int s = g % G::S, f = g % MXL_SFS;
                 if (g >= MXL_SFS)
@@ -618,8 +665,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
                 const uint32_t *hs = (const uint32_t *)(st + G::HSOFF) + (lane >> 3);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    vb[c] = un.down ? hs[4 * c] : 0x7F7F7F7Fu;
-                    vb[4 + c] = un.down ? (two ? hs[16 + 4 * c] : 0u) : 0x7F7F7F7Fu;
+                    vb[c] = down ? hs[4 * c] : 0x7F7F7F7Fu;
+                    vb[4 + c] = down ? (two ? hs[16 + 4 * c] : 0u) : 0x7F7F7F7Fu;
                 }
                 tmem_st8(t0 + 16 * f, va);
                 tmem_st8(t0 + 16 * f + 8, vb);
@@ -636,16 +683,21 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
         for (int i = 0;; ++i) {
             const int u = next_unit(i);
             bool ok = u != -2;
-            Unit un = {0, 0, false};
+            Unit un = {MXL_COMBINE, 0, 0};
             if (u >= 0) {
                 un = unit_of(u, nch, FT, HT);
-                ok = mbar_wait_role(&acc_full[i & 1], (i / 2) & 1, p.status, abort_flag);
+                ok = un.kind == MXL_COMBINE ? wait_count(&p.done[un.m], nch, p.status, abort_flag)
+                                            : mbar_wait_role(&acc_full[i & 1], (i / 2) & 1, p.status, abort_flag);
             }
             if (!bar_and_n(1, 128, ok) || u < 0) break;
+            if (un.kind == MXL_COMBINE) {
+                combine_tile(p, un.m, 8 * un.c, ew, r_ok);
+                continue;
+            }
             tc_fence_after();
-            const int buf = i & 1, n = c_n[un.chunk], pos = c_pos[un.chunk];
+            const int buf = i & 1, n = c_n[un.c], pos = c_pos[un.c];
             const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * G::N;
-            if (!un.down) {
+            if (un.kind == MXL_UP) {
                 // route i's gate (lane quarters 0, 1) and up (2, 3) values; the gate warps finish the even
                 // routes, the up warps the odd ones
                 float mine[NR / 2];
@@ -698,14 +750,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
                         const int d = lane & 7;
                         uint8_t *atom = p.hq + ((size_t)pos * FB + (size_t)kb * n + r) * 512;
                         *(uint32_t *)(atom + d * 64 + ((cb ^ ((d >> 1) & 3)) << 4) + 4 * (lane >> 3)) = w;
-                        if (lane == 0) ((uint8_t *)(p.hs + ((size_t)un.chunk * FB + kb) * 16 + r))[cb] = (uint8_t)sc;
+                        if (lane == 0) ((uint8_t *)(p.hs + ((size_t)un.c * FB + kb) * 16 + r))[cb] = (uint8_t)sc;
                     }
-                }
-                fence_proxy_async_all();
-                bar_sync_n(1, 128);
-                if (ew == 0) {
-                    __threadfence();
-                    atomicAdd(&p.ready[un.chunk], 1);
                 }
             } else {
                 const int o = 128 * un.m + 32 * q + lane;
@@ -732,15 +778,10 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(&acc_empty[buf]);
-                bar_sync_n(1, 128);
-                if (ew == 0) {
-                    __threadfence();
-                    *s_last = atomicAdd(&p.done[un.m], 1) == nch - 1;
-                    __threadfence();
-                }
-                bar_sync_n(1, 128);
-                if (*(volatile int *)s_last) combine_tile(p, un.m, ew, r_ok);
             }
+            // warp 3 publishes the unit (its fence does not hold the epilogue up)
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(&pub[i % MXL_PUB]);
         }
     }
     tc_fence_before();
