@@ -6,7 +6,8 @@
 //   read from tensor memory, exact products, fp32 sums in tensor memory.
 // The weights are the M side, so that an expert's few routes cost only as wide an MMA as they are.
 //
-//  * mx4_route_kernel: the routes sorted by expert (one cluster of up to 8 CTAs: shared-memory
+//  * few routes (MX4_LOCAL_R): each CTA groups them by expert itself;
+//    otherwise mx4_route_kernel: the routes sorted by expert (one cluster of up to 8 CTAs: shared-memory
 //    histograms joined over distributed shared memory, positions by a shared cursor) and cut into
 //    chunks of at most NT routes of one expert, experts with the most routes first.  The order of
 //    the routes inside an expert is not fixed; a route's result does not depend on it.
@@ -17,7 +18,7 @@
 //                  four rows to a TMA gather, straight into the 128-byte-swizzled operand layout;
 //      warp 2      one thread issues the four MMAs of a stage and one commit;
 //      warps 4-7   the stage's scales into tensor memory: the weights' from the landed blocks, the
-//                  routes' from global memory (loaded a stage ahead).  Each warp writes its own
+//                  routes' from global memory (loaded two stages ahead).  Each warp writes its own
 //                  lane quarter (the tensor core reads a copy in each);
 //      warps 8-15  the epilogue of the previous item from the other accumulator.
 #include <cuda.h>
@@ -30,7 +31,7 @@
 #include "moe_tc.cuh"
 
 #define MXG_THREADS 512
-#define MXG_CTRL 23552
+#define MXG_CTRL 28672
 #define MXG_WBYTES (2 * MX4_TB)  // weights of a stage: two tile blocks
 #define MXG_ROUTE_THREADS 1024
 #define MXG_ROUTE_CLUSTER 8
@@ -59,22 +60,17 @@ GemmWs gemm_ws(int T, int E, int k, int NT) {
 
 // Most routes of a chunk.
 #define MXG_NT_SMALL 32
-#define MXG_NT_LARGE 224
+#define MXG_NT_LARGE 192
 int chunk_routes(int T, int E, int k) { return (long)T * k <= 16L * E ? MXG_NT_SMALL : MXG_NT_LARGE; }
 
 // ------------------------------------------------------------------ routes by expert
-
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
 
 __global__ void __launch_bounds__(MXG_ROUTE_THREADS)
 mx4_route_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *__restrict__ table, int n_slots, int NT,
                  int32_t *__restrict__ ints, int32_t *__restrict__ rows, int32_t *__restrict__ c_slot,
                  int32_t *__restrict__ c_pos, int32_t *__restrict__ c_n, int *status) {
-    __shared__ int hist[MOE_MAX_E], cnt[MOE_MAX_E], cur[MOE_MAX_E], off[MOE_MAX_E];
+    __shared__ __align__(16) int cnt[MOE_MAX_E];
+    __shared__ int hist[MOE_MAX_E], cur[MOE_MAX_E], off[MOE_MAX_E];
     __shared__ int order[MOE_MAX_E], first[MOE_MAX_E];
     const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), tid = threadIdx.x;
     const int seg = (R + C - 1) / C, r0 = rank * seg, r1 = min(R, r0 + seg);
@@ -116,15 +112,29 @@ mx4_route_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *_
     __syncthreads();
     if (tid < MOE_MAX_E) cur[tid] = off[tid] + before;
     __syncthreads();
-    for (int r = r0 + tid; r < r1; r += MXG_ROUTE_THREADS) {
-        const int e = ids[r];
-        if (e >= 0 && e < E) rows[atomicAdd(&cur[e], 1)] = r;
+    for (int rb = r0; rb < r1; rb += MXG_ROUTE_THREADS) {
+        // the lanes of one expert reserve their positions together
+        const int r = rb + tid, e = r < r1 ? ids[r] : -1;
+        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && e < E) {
+            const int lead = __ffs(peers) - 1;
+            int at = 0;
+            if ((tid & 31) == lead) at = atomicAdd(&cur[e], __popc(peers));
+            at = __shfl_sync(peers, at, lead);
+            rows[at + __popc(peers & ((1u << (tid & 31)) - 1))] = r;
+        }
     }
     if (rank == 0) {
         // chunks, the experts with the most routes first
         if (tid < MOE_MAX_E) {
+            const int mine = cnt[tid];
             int o = 0;
-            for (int j = 0; j < MOE_MAX_E; ++j) o += cnt[j] > cnt[tid] || (cnt[j] == cnt[tid] && j < tid);
+#pragma unroll 4
+            for (int j = 0; j < MOE_MAX_E; j += 4) {
+                const int4 v = *(const int4 *)&cnt[j];
+                o += (v.x > mine || (v.x == mine && j < tid)) + (v.y > mine || (v.y == mine && j + 1 < tid)) +
+                     (v.z > mine || (v.z == mine && j + 2 < tid)) + (v.w > mine || (v.w == mine && j + 3 < tid));
+            }
             order[o] = tid;
         }
         __syncthreads();
@@ -171,7 +181,9 @@ struct GemmParams {
     const uint8_t *scales;   // [rows][K / 32]
     const uint8_t *pool;
     size_t slot_bytes;
-    const int32_t *ints, *rows, *c_slot, *c_pos, *c_n;
+    const int32_t *ints, *rows, *c_slot, *c_pos, *c_n;  // mx4_route_kernel's tables
+    const int32_t *ids, *table;                         // LOCAL
+    int R, E, n_slots;
     const float *weights;    // down
     void *out;
     int K, R_out, div;       // columns, output row length, routes per code row
@@ -180,14 +192,15 @@ struct GemmParams {
     int *status;
 };
 
+// A ring stage and its scales in tensor memory share their index: a landed stage means that the MMAs
+// that read the scales' previous contents are done, so the scale slots need no wait of their own.
 template <int NT>
 struct GemmGeom {
     static constexpr int STAGE = MXG_WBYTES + NT * 128;
-    static constexpr int S = NT == MXG_NT_LARGE ? 4 : 9;     // ring stages
-    static constexpr int SFS = NT == MXG_NT_LARGE ? 2 : 8;   // scale slots in tensor memory, 24 columns each
-    static constexpr int SFCOL = 2 * NT;                     // after the two accumulators
+    static constexpr int S = NT == MXG_NT_LARGE ? 4 : 8;     // ring stages
+    static constexpr int SFCOL = 2 * NT;                     // scales after the two accumulators, 24 columns a stage
     static constexpr size_t SMEM = 1024 + MXG_CTRL + (size_t)S * STAGE;
-    static_assert(SFCOL + SFS * 24 <= 512 && S > SFS && STAGE % 1024 == 0 && SMEM <= 227 * 1024, "budget");
+    static_assert(SFCOL + S * 24 <= 512 && STAGE % 1024 == 0 && SMEM <= 227 * 1024, "budget");
 };
 
 // Four rows of the map's box width to 4 x 128 bytes of shared memory.  x is a multiple of 128.
@@ -208,7 +221,8 @@ __device__ __forceinline__ uint2 scale8(const uint8_t *row, int q, int KS) {
     return make_uint2(v[0], v[1]);
 }
 
-template <int NT, bool DOWN, int OT>
+// LOCAL: few routes, grouped by the CTA itself; otherwise mx4_route_kernel's tables.
+template <int NT, bool DOWN, int OT, bool LOCAL>
 __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_constant__ GemmParams p) {
     using G = GemmGeom<NT>;
     extern __shared__ uint8_t smem_raw[];
@@ -216,16 +230,18 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     uint64_t *s_full = (uint64_t *)smem;
     uint64_t *s_empty = s_full + G::S;
     uint64_t *sf_full = s_empty + G::S;
-    uint64_t *acc_full = sf_full + G::SFS;
+    uint64_t *acc_full = sf_full + G::S;
     uint64_t *acc_empty = acc_full + 2;
     uint64_t *mma_done = acc_empty + 2;
     uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
-    static_assert((2 * G::S + G::SFS + 6) * 8 <= 1024, "barriers");
+    static_assert((3 * G::S + 6) * 8 <= 1024, "barriers");
     float *xch = (float *)(smem + 1024);             // [4 pairs][2 slots][2 ways][8 columns][32 lanes]
     uint8_t **e_row = (uint8_t **)(smem + 1024 + 16384);  // [2 accumulators][NT] output rows
     float *e_w = (float *)(e_row + 2 * NT);          // [2 accumulators][NT]
-    static_assert(1024 + 16384 + 2 * NT * 12 <= MXG_CTRL && MXG_CTRL % 1024 == 0, "control block");
+    Mx4Chunks &loc = *(Mx4Chunks *)(e_w + 2 * NT);   // LOCAL
+    static_assert(1024 + 16384 + 2 * NT * 12 + (LOCAL ? sizeof(Mx4Chunks) : 0) <= MXG_CTRL && MXG_CTRL % 1024 == 0,
+                  "control block");
     uint8_t *ring = smem + MXG_CTRL;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -233,8 +249,8 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
         for (int s = 0; s < G::S; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&s_empty[s], 1);
+            mbar_init(&sf_full[s], 4);
         }
-        for (int s = 0; s < G::SFS; ++s) mbar_init(&sf_full[s], 4);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 8);
@@ -253,7 +269,10 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_trigger();
-    const int MT = p.MT, n_items = p.ints[0] * MT;
+    if (LOCAL) mx4_local_chunks(loc, p.ids, p.R, p.E, p.table, p.n_slots, NT, p.status);
+    const int *c_slots = LOCAL ? loc.slot : p.c_slot, *c_poss = LOCAL ? loc.pos : p.c_pos, *c_ns = LOCAL ? loc.n : p.c_n;
+    const int *rows = LOCAL ? loc.rows : p.rows;
+    const int MT = p.MT, n_items = (LOCAL ? loc.nch : p.ints[0]) * MT;
     const int KB = (p.K + 127) / 128, NKS = (KB + 1) / 2, KS = p.K / 32;
 
     if (warp < 2) {
@@ -263,14 +282,14 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
         bool ok = true;
         for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
             const int c = j / MT, m = j % MT;
-            const int slot = p.c_slot[c];
+            const int slot = c_slots[c];
             if (slot < 0) continue;
-            const int pos0 = p.c_pos[c], n = p.c_n[c];
+            const int pos0 = c_poss[c], n = c_ns[c];
             const int npad = (n + 7) & ~7, q = 2 * lane + warp;  // this lane's group of four rows
             int r4[4];
             for (int i = 0; i < 4; ++i) {
                 const int at = 4 * q + i;
-                r4[i] = p.rows[pos0 + (at < n ? at : 0)] / p.div;  // rows past the chunk: unused columns
+                r4[i] = rows[pos0 + (at < n ? at : 0)] / p.div;  // rows past the chunk: unused columns
             }
             const uint8_t *w = p.pool + (size_t)slot * p.slot_bytes + p.mat + (size_t)m * KB * MX4_TB;
             for (int kc = 0; kc < NKS; ++kc, ++g) {
@@ -303,21 +322,21 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
             bool ok = true;
             for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
                 const int c = j / MT;
-                if (p.c_slot[c] < 0) continue;
-                const int npad = (p.c_n[c] + 7) & ~7;
+                if (c_slots[c] < 0) continue;
+                const int npad = (c_ns[c] + 7) & ~7;
                 const uint32_t id0 = umma_idesc_mxf4(128, npad, 0), id2 = umma_idesc_mxf4(128, npad, 2);
                 const int buf = jl & 1;
                 if (jl >= 2 && !(ok = mbar_wait_role(&acc_empty[buf], ((jl / 2) - 1) & 1, p.status, abort_flag))) break;
                 tc_fence_after();
                 const uint32_t d = tmem + buf * NT;
                 for (int kc = 0; kc < NKS; ++kc, ++g) {
-                    const int s = g % G::S, f = g % G::SFS;
-                    if (!(ok = mbar_wait_role(&sf_full[f], (g / G::SFS) & 1, p.status, abort_flag))) break;
+                    const int s = g % G::S;
+                    if (!(ok = mbar_wait_role(&sf_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
                     if (!(ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
                     tc_fence_after();
                     uint8_t *st = ring + (size_t)s * G::STAGE;
                     const uint64_t a = umma_desc_sw64(smem_u32(st)), b = umma_desc_sw128(smem_u32(st + MXG_WBYTES));
-                    const uint32_t sf = tmem + G::SFCOL + 24 * f;
+                    const uint32_t sf = tmem + G::SFCOL + 24 * s;
                     const int steps = min(4, (p.K - 256 * kc + 63) / 64);
                     umma_mxf4(d, a, b, id0, sf, sf + 8, kc > 0);
                     if (steps > 1) umma_mxf4(d, a + 2, b + 2, id2, sf, sf + 8, 1);
@@ -339,33 +358,35 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
         bool ok = true;
         for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
             const int c = j / MT;
-            if (p.c_slot[c] < 0) continue;
-            const int pos0 = p.c_pos[c], n = p.c_n[c];
+            if (c_slots[c] < 0) continue;
+            const int pos0 = c_poss[c], n = c_ns[c];
             const uint8_t *row[NI];
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int at = 32 * i + lane;
-                row[i] = at < n ? p.scales + (size_t)(p.rows[pos0 + at] / p.div) * KS : nullptr;
+                row[i] = at < n ? p.scales + (size_t)(rows[pos0 + at] / p.div) * KS : nullptr;
             }
-            uint2 nxt[NI];
+            // scales are loaded two stages ahead (a load takes about as long as a stage)
+            uint2 n0[NI], n1[NI];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) nxt[i] = row[i] ? scale8(row[i], 0, KS) : make_uint2(0, 0);
+            for (int i = 0; i < NI; ++i) {
+                n0[i] = row[i] ? scale8(row[i], 0, KS) : make_uint2(0, 0);
+                n1[i] = row[i] && NKS > 1 ? scale8(row[i], 1, KS) : make_uint2(0, 0);
+            }
             for (int kc = 0; kc < NKS; ++kc, ++g) {
-                const int s = g % G::S, f = g % G::SFS;
+                const int s = g % G::S;
                 uint32_t v[24];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    v[8 + i] = i < NI ? nxt[i < NI ? i : 0].x : 0u;
-                    v[16 + i] = i < NI ? nxt[i < NI ? i : 0].y : 0u;
+                    v[8 + i] = i < NI ? n0[i < NI ? i : 0].x : 0u;
+                    v[16 + i] = i < NI ? n0[i < NI ? i : 0].y : 0u;
                 }
-                if (kc + 1 < NKS)
 #pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        if (row[i]) nxt[i] = scale8(row[i], kc + 1, KS);
-                // the slot's last reader: the MMAs of stage g - SFS, whose commit released that ring stage
-                if (g >= G::SFS)
-                    ok = mbar_wait_role(&s_empty[(g - G::SFS) % G::S], ((g - G::SFS) / G::S) & 1, p.status, abort_flag);
-                if (ok) ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag);
+                for (int i = 0; i < NI; ++i) {
+                    n0[i] = n1[i];
+                    if (row[i] && kc + 2 < NKS) n1[i] = scale8(row[i], kc + 2, KS);
+                }
+                ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
                 const uint8_t *st = ring + (size_t)s * G::STAGE;
@@ -375,11 +396,11 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                 v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
                 v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 #pragma unroll
-                for (int i = 0; i < 3; ++i) tmem_st8(t0 + 24 * f + 8 * i, *reinterpret_cast<uint32_t(*)[8]>(&v[8 * i]));
+                for (int i = 0; i < 3; ++i) tmem_st8(t0 + 24 * s + 8 * i, *reinterpret_cast<uint32_t(*)[8]>(&v[8 * i]));
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive1(&sf_full[f]);
+                if (lane == 0) mbar_arrive1(&sf_full[s]);
             }
         }
     } else if (warp >= 8) {
@@ -393,10 +414,10 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
         bool ok = true;
         for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
             const int c = j / MT, m = j % MT;
-            if (p.c_slot[c] < 0) continue;
-            const int pos0 = p.c_pos[c], n = p.c_n[c], buf = jl & 1;
+            if (c_slots[c] < 0) continue;
+            const int pos0 = c_poss[c], n = c_ns[c], buf = jl & 1;
             for (int i = ew * 32 + lane; i < n; i += 256) {
-                const int r = p.rows[pos0 + i];
+                const int r = rows[pos0 + i];
                 e_row[buf * NT + i] = (uint8_t *)p.out + (size_t)r * p.R_out * ES;
                 if (DOWN) e_w[buf * NT + i] = p.weights[r];
             }
@@ -489,7 +510,7 @@ int encode_codes_map(const uint8_t *codes, long rows, int K, CUtensorMap *map) {
     return MOE_OK;
 }
 
-template <int NT, bool DOWN, int OT>
+template <int NT, bool DOWN, int OT, bool LOCAL>
 int launch_gemm_t(const GemmParams &p, int max_chunks, cudaStream_t s) {
     using G = GemmGeom<NT>;
     static std::mutex mu;
@@ -501,7 +522,7 @@ int launch_gemm_t(const GemmParams &p, int max_chunks, cudaStream_t s) {
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!sms[dev]) {
-            MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_gemm_kernel<NT, DOWN, OT>,
+            MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_gemm_kernel<NT, DOWN, OT, LOCAL>,
                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::SMEM));
             MOE_TRY_CUDA(cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev));
         }
@@ -511,14 +532,17 @@ int launch_gemm_t(const GemmParams &p, int max_chunks, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     const long items = (long)max_chunks * p.MT;
     moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<long>(items, n)), dim3(MXG_THREADS), G::SMEM, s);
-    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<NT, DOWN, OT>, p));
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<NT, DOWN, OT, LOCAL>, p));
     return MOE_OK;
 }
 
 template <bool DOWN, int OT>
 int launch_gemm(const GemmParams &p, int NT, int max_chunks, cudaStream_t s) {
-    return NT == MXG_NT_SMALL ? launch_gemm_t<MXG_NT_SMALL, DOWN, OT>(p, max_chunks, s)
-                              : launch_gemm_t<MXG_NT_LARGE, DOWN, OT>(p, max_chunks, s);
+    if (p.R <= MX4_LOCAL_R)
+        return NT == MXG_NT_LARGE ? launch_gemm_t<MXG_NT_LARGE, DOWN, OT, true>(p, max_chunks, s)
+                                  : launch_gemm_t<MXG_NT_SMALL, DOWN, OT, true>(p, max_chunks, s);
+    return NT == MXG_NT_LARGE ? launch_gemm_t<MXG_NT_LARGE, DOWN, OT, false>(p, max_chunks, s)
+                              : launch_gemm_t<MXG_NT_SMALL, DOWN, OT, false>(p, max_chunks, s);
 }
 
 int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, int H, int F, int E, int k,
@@ -541,23 +565,30 @@ int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, i
     p.c_slot = w + L.o_slot;
     p.c_pos = w + L.o_pos;
     p.c_n = w + L.o_n;
+    p.ids = ids;
+    p.table = table;
+    p.R = T * k;
+    p.E = E;
+    p.n_slots = n_slots;
     p.weights = weights;
     p.out = out;
     p.MT = down ? (H + 127) / 128 : (F + 63) / 64;
     p.mat = down ? mx4_gu_bytes(H, F) : 0;
     p.status = moe_status_word_device_ptr();
 
-    const int R = T * k;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    const int C = R <= 2 * MXG_ROUTE_THREADS ? 1 : MXG_ROUTE_CLUSTER;
-    moe_pdl_config(&cfg, attr, dim3(C), dim3(MXG_ROUTE_THREADS), 0, s);
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_route_kernel, ids, R, E, table, n_slots, NT, w, w + L.o_rows,
-                                    w + L.o_slot, w + L.o_pos, w + L.o_n, p.status));
+    if (p.R > MX4_LOCAL_R) {
+        const int R = p.R;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        const int C = R <= 2 * MXG_ROUTE_THREADS ? 1 : MXG_ROUTE_CLUSTER;
+        moe_pdl_config(&cfg, attr, dim3(C), dim3(MXG_ROUTE_THREADS), 0, s);
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = C;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+        MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_route_kernel, ids, R, E, table, n_slots, NT, w, w + L.o_rows,
+                                        w + L.o_slot, w + L.o_pos, w + L.o_n, p.status));
+    }
     if (down) return launch_gemm<true, MOE_F32>(p, NT, L.max_chunks, s);
     return otype == MOE_BF16 ? launch_gemm<false, MOE_BF16>(p, NT, L.max_chunks, s)
                              : launch_gemm<false, MOE_F32>(p, NT, L.max_chunks, s);
