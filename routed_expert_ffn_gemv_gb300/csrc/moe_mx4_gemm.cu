@@ -14,11 +14,11 @@
 //  * mx4_gemm_kernel: persistent, one CTA per SM; a work item is (chunk, 128-row weight tile).
 //    Warp roles, mbarrier rings that run on across items:
 //      warps 0, 1  a stage of 256 columns: the tile's two 8704-byte blocks (codes and scales, one
-//                  bulk copy: the slot image is in operand order) and the chunk's code rows,
-//                  four rows to a TMA gather, straight into the 128-byte-swizzled operand layout;
+//                  bulk copy: the slot image is in operand order) and the chunk's code rows, as runs
+//                  of mx4_gather_kernel's output, or, for few routes, four rows to a TMA gather
+//                  straight into the 128-byte-swizzled operand layout;
 //      warp 2      one thread issues the four MMAs of a stage and one commit;
-//      warps 4-7   the stage's scales into tensor memory: the weights' from the landed blocks, the
-//                  routes' from global memory (loaded two stages ahead).  Each warp writes its own
+//      warps 4-7   the stage's scales into tensor memory.  Each warp writes its own
 //                  lane quarter (the tensor core reads a copy in each);
 //      warps 8-15  the epilogue of the previous item from the other accumulator.
 #include <cuda.h>
@@ -43,18 +43,25 @@ namespace {
 struct GemmWs {
     int max_chunks;
     size_t o_rows, o_slot, o_pos, o_n, ints;  // in ints; [0] is the number of chunks
+    size_t Rp;                                // positions: every expert's start at a multiple of 8
+    size_t codes, scales, total;              // in bytes
 };
 
-GemmWs gemm_ws(int T, int E, int k, int NT) {
+GemmWs gemm_ws(int T, int H, int F, int E, int k, int NT) {
     GemmWs L;
     const long R = (long)T * k;
     L.max_chunks = (int)(R / NT + std::min<long>(E, R));
+    L.Rp = (size_t)(R + 7 * std::min<long>(E, R) + 7) / 8 * 8;
     size_t o = 16;
-    L.o_rows = o; o += R;
+    L.o_rows = o; o += L.Rp;
     L.o_slot = o; o += L.max_chunks;
     L.o_pos = o;  o += L.max_chunks;
     L.o_n = o;    o += L.max_chunks;
     L.ints = o;
+    L.codes = (o * 4 + 1023) / 1024 * 1024;
+    const size_t stages = (std::max(H, F) + 255) / 256, rows = R > MX4_LOCAL_R ? stages * L.Rp : 0;
+    L.scales = L.codes + rows * 128;
+    L.total = L.scales + rows * 8;
     return L;
 }
 
@@ -100,7 +107,7 @@ mx4_route_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *_
         int v[MOE_MAX_E / 32], s = 0;
         for (int i = 0; i < MOE_MAX_E / 32; ++i) {
             v[i] = s;
-            s += cnt[tid * (MOE_MAX_E / 32) + i];
+            s += (cnt[tid * (MOE_MAX_E / 32) + i] + 7) & ~7;
         }
         int x = s;
         for (int o = 1; o < 32; o <<= 1) {
@@ -163,22 +170,79 @@ mx4_route_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *_
                     slot = -1;
                 }
             }
-            for (int c = 0; c < nc; ++c) {  // near-equal chunks
-                const int a = (int)((long)n * c / nc), b = (int)((long)n * (c + 1) / nc);
+            // near-equal chunks that start at multiples of 8 (NT is one: no chunk is empty)
+            const int size = nc ? ((n + nc - 1) / nc + 7) & ~7 : 0;
+            for (int c = 0; c < nc; ++c) {
                 c_slot[first[tid] + c] = slot;
-                c_pos[first[tid] + c] = off[e] + a;
-                c_n[first[tid] + c] = b - a;
+                c_pos[first[tid] + c] = off[e] + c * size;
+                c_n[first[tid] + c] = min(size, n - c * size);
             }
         }
     }
     cluster_sync_all();  // the histograms stay until every CTA has read them
 }
 
+// The eight scale bytes of a row from block 8q on (fewer at the row's end: zeros).
+__device__ __forceinline__ uint2 scale8(const uint8_t *row, int q, int KS) {
+    if ((KS & 7) == 0 && ((uintptr_t)row & 7) == 0) return *(const uint2 *)(row + 8 * q);
+    uint32_t v[2] = {0u, 0u};
+    const int n = min(8, KS - 8 * q);
+    for (int i = 0; i < n; ++i) v[i >> 2] |= (uint32_t)row[8 * q + i] << (8 * (i & 3));
+    return make_uint2(v[0], v[1]);
+}
+
+// ------------------------------------------------------------------ code rows in operand order
+//
+// Rows of codes and scales from their places to the chunks' positions, by stages of 256 columns:
+// codes [stage][position][128 bytes], 16-byte piece j at j ^ (position % 8) (the 128-byte swizzle; chunks
+// start at multiples of 8), scales [stage][position][8 bytes], zeros past K.  So a stage of a chunk is
+// two runs of bytes.  Measured: gathering by TMA inside the product kernel (four rows a copy, 48 copies
+// a stage) kept two warps busy all the time, about 80 clocks a copy, and bound it.
+// A warp takes eight positions; Rp positions in all.
+#define MXG_GATHER_THREADS 256
+__global__ void __launch_bounds__(MXG_GATHER_THREADS)
+mx4_gather_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int K, int div, int per_chunk,
+                  size_t Rp, const int32_t *__restrict__ ints, const int32_t *__restrict__ rows,
+                  const int32_t *__restrict__ c_pos, const int32_t *__restrict__ c_n, uint8_t *__restrict__ xg,
+                  uint8_t *__restrict__ sg) {
+    const int lane = threadIdx.x & 31, KS = K / 32, NKS = (K + 255) / 256;
+    pdl_wait();
+    pdl_trigger();
+    const int items = ints[0] * per_chunk, warps = gridDim.x * (MXG_GATHER_THREADS / 32);
+    for (int it = blockIdx.x * (MXG_GATHER_THREADS / 32) + threadIdx.x / 32; it < items; it += warps) {
+        const int c = it / per_chunk, i0 = (it - c * per_chunk) * 8, n = min(8, c_n[c] - i0);
+        if (n <= 0) continue;
+        const int pos = c_pos[c] + i0;
+        // lane l: piece l % 8 of a stage, row l / 8 (and + 4)
+        const int j = lane & 7, r0 = lane >> 3;
+        const int src0 = r0 < n ? rows[pos + r0] / div : -1, src1 = r0 + 4 < n ? rows[pos + r0 + 4] / div : -1;
+        uint8_t *d0 = xg + (size_t)(pos + r0) * 128 + ((j ^ r0) << 4), *d1 = xg + (size_t)(pos + r0 + 4) * 128 + ((j ^ (r0 + 4)) << 4);
+#pragma unroll 4
+        for (int q = 0; q < NKS; ++q) {
+            const int col = 128 * q + 16 * j;  // bytes into the code row
+            uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
+            if (col < K / 2) {
+                if (src0 >= 0) a = *(const uint4 *)(codes + (size_t)src0 * (K / 2) + col);
+                if (src1 >= 0) b = *(const uint4 *)(codes + (size_t)src1 * (K / 2) + col);
+            }
+            if (src0 >= 0) *(uint4 *)(d0 + (size_t)q * Rp * 128) = a;
+            if (src1 >= 0) *(uint4 *)(d1 + (size_t)q * Rp * 128) = b;
+        }
+        // scales: lane l takes row l / 4 and stages l % 4, + 4, ..
+        const int rs = lane >> 2, src = rs < n ? rows[pos + rs] / div : -1;
+        if (src >= 0)
+            for (int q = lane & 3; q < NKS; q += 4)
+                *(uint2 *)(sg + ((size_t)q * Rp + pos + rs) * 8) = scale8(scales + (size_t)src * KS, q, KS);
+    }
+}
+
 // ------------------------------------------------------------------ the products
 
 struct GemmParams {
-    CUtensorMap map;         // the code rows, boxes of 128 bytes of one row
-    const uint8_t *scales;   // [rows][K / 32]
+    CUtensorMap map;         // LOCAL: the code rows, boxes of 128 bytes of one row
+    const uint8_t *scales;   // LOCAL: [rows][K / 32]
+    const uint8_t *xg, *sg;  // otherwise mx4_gather_kernel's rows
+    size_t Rp;
     const uint8_t *pool;
     size_t slot_bytes;
     const int32_t *ints, *rows, *c_slot, *c_pos, *c_n;  // mx4_route_kernel's tables
@@ -196,7 +260,8 @@ struct GemmParams {
 // that read the scales' previous contents are done, so the scale slots need no wait of their own.
 template <int NT>
 struct GemmGeom {
-    static constexpr int STAGE = MXG_WBYTES + NT * 128;
+    static constexpr int SOFF = MXG_WBYTES + NT * 128;       // weights, code rows, scales
+    static constexpr int STAGE = (SOFF + NT * 8 + 1023) / 1024 * 1024;
     static constexpr int S = NT == MXG_NT_LARGE ? 4 : 8;     // ring stages
     static constexpr int SFCOL = 2 * NT;                     // scales after the two accumulators, 24 columns a stage
     static constexpr size_t SMEM = 1024 + MXG_CTRL + (size_t)S * STAGE;
@@ -210,15 +275,6 @@ __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, i
         "%5, %6}], [%7];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(smem_u32(bar))
         : "memory");
-}
-
-// The eight scale bytes of a row from block 8q on (fewer at the row's end: zeros).
-__device__ __forceinline__ uint2 scale8(const uint8_t *row, int q, int KS) {
-    if ((KS & 7) == 0 && ((uintptr_t)row & 7) == 0) return *(const uint2 *)(row + 8 * q);
-    uint32_t v[2] = {0u, 0u};
-    const int n = min(8, KS - 8 * q);
-    for (int i = 0; i < n; ++i) v[i >> 2] |= (uint32_t)row[8 * q + i] << (8 * (i & 3));
-    return make_uint2(v[0], v[1]);
 }
 
 // LOCAL: few routes, grouped by the CTA itself; otherwise mx4_route_kernel's tables.
@@ -276,40 +332,51 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     const int KB = (p.K + 127) / 128, NKS = (KB + 1) / 2, KS = p.K / 32;
 
     if (warp < 2) {
-        // ---------------- producers: warp 0 the stage's expected bytes, its weights and the even
-        // groups of four rows, warp 1 the odd groups
+        // ---------------- producers.  LOCAL: warp 0 the stage's expected bytes, its weights and the even
+        // groups of four code rows, warp 1 the odd groups.  Otherwise warp 0's first lane: the
+        // weights, the chunk's rows and their scales, three runs of bytes.
         int g = 0;
         bool ok = true;
-        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
+        for (int j = blockIdx.x; j < n_items && ok && (LOCAL || threadIdx.x == 0); j += gridDim.x) {
             const int c = j / MT, m = j % MT;
             const int slot = c_slots[c];
             if (slot < 0) continue;
             const int pos0 = c_poss[c], n = c_ns[c];
             const int npad = (n + 7) & ~7, q = 2 * lane + warp;  // this lane's group of four rows
             int r4[4];
-            for (int i = 0; i < 4; ++i) {
-                const int at = 4 * q + i;
-                r4[i] = rows[pos0 + (at < n ? at : 0)] / p.div;  // rows past the chunk: unused columns
-            }
+            if (LOCAL)
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 4 * q + i;
+                    r4[i] = rows[pos0 + (at < n ? at : 0)] / p.div;  // rows past the chunk: unused columns
+                }
             const uint8_t *w = p.pool + (size_t)slot * p.slot_bytes + p.mat + (size_t)m * KB * MX4_TB;
             for (int kc = 0; kc < NKS; ++kc, ++g) {
                 const int s = g % G::S;
                 if (g >= G::S) {
                     ok = mbar_wait_role(&s_empty[s], ((g / G::S) & 1) ^ 1, p.status, abort_flag);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (LOCAL) ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                 }
                 uint8_t *st = ring + (size_t)s * G::STAGE;
-                if (warp == 0 && lane == 0) {
-                    const uint32_t wb = 2 * kc + 1 < KB ? MXG_WBYTES : MX4_TB;
-                    mbar_arrive_expect_tx(&s_full[s], wb + (uint32_t)npad * 128u);
+                const uint32_t wb = 2 * kc + 1 < KB ? MXG_WBYTES : MX4_TB;
+                if (LOCAL) {
+                    if (threadIdx.x == 0) {
+                        mbar_arrive_expect_tx(&s_full[s], wb + (uint32_t)npad * 128u);
+                        bulk_g2s(st, w + (size_t)kc * MXG_WBYTES, wb, &s_full[s]);
+                    }
+                    if (4 * q < npad) tma_gather4(st + MXG_WBYTES + q * 512, &p.map, kc * 128, r4, &s_full[s]);
+                    __syncwarp();
+                } else {
+                    const uint32_t sb = (uint32_t)((n + 1) & ~1) * 8u;
+                    mbar_arrive_expect_tx(&s_full[s], wb + (uint32_t)n * 128u + sb);
                     bulk_g2s(st, w + (size_t)kc * MXG_WBYTES, wb, &s_full[s]);
+                    bulk_g2s(st + MXG_WBYTES, p.xg + ((size_t)kc * p.Rp + pos0) * 128, (uint32_t)n * 128u, &s_full[s]);
+                    bulk_g2s(st + G::SOFF, p.sg + ((size_t)kc * p.Rp + pos0) * 8, sb, &s_full[s]);
                 }
-                if (4 * q < npad) tma_gather4(st + MXG_WBYTES + q * 512, &p.map, kc * 128, r4, &s_full[s]);
-                __syncwarp();
             }
         }
         // never leave with copies in flight
-        if (warp == 0 && lane == 0)
+        if (threadIdx.x == 0)
             for (int s = 0; s < G::S && s < g; ++s) {
                 const int last = s + ((g - 1 - s) / G::S) * G::S;
                 mbar_wait_bounded(&s_full[s], (last / G::S) & 1, p.status);
@@ -360,36 +427,39 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
             const int c = j / MT;
             if (c_slots[c] < 0) continue;
             const int pos0 = c_poss[c], n = c_ns[c];
+            // LOCAL: the routes' scales from their rows, loaded two stages ahead (a load takes about as long
+            // as a stage); otherwise they landed with the stage
             const uint8_t *row[NI];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int at = 32 * i + lane;
-                row[i] = at < n ? p.scales + (size_t)(rows[pos0 + at] / p.div) * KS : nullptr;
-            }
-            // scales are loaded two stages ahead (a load takes about as long as a stage)
             uint2 n0[NI], n1[NI];
+            if (LOCAL)
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                n0[i] = row[i] ? scale8(row[i], 0, KS) : make_uint2(0, 0);
-                n1[i] = row[i] && NKS > 1 ? scale8(row[i], 1, KS) : make_uint2(0, 0);
-            }
+                for (int i = 0; i < NI; ++i) {
+                    const int at = 32 * i + lane;
+                    row[i] = at < n ? p.scales + (size_t)(rows[pos0 + at] / p.div) * KS : nullptr;
+                    n0[i] = row[i] ? scale8(row[i], 0, KS) : make_uint2(0, 0);
+                    n1[i] = row[i] && NKS > 1 ? scale8(row[i], 1, KS) : make_uint2(0, 0);
+                }
             for (int kc = 0; kc < NKS; ++kc, ++g) {
                 const int s = g % G::S;
                 uint32_t v[24];
+                ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                const uint8_t *st = ring + (size_t)s * G::STAGE;
+                if (!LOCAL)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) n0[i] = *(const uint2 *)(st + G::SOFF + 8 * (32 * i + lane));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     v[8 + i] = i < NI ? n0[i < NI ? i : 0].x : 0u;
                     v[16 + i] = i < NI ? n0[i < NI ? i : 0].y : 0u;
                 }
+                if (LOCAL)
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    n0[i] = n1[i];
-                    if (row[i] && kc + 2 < NKS) n1[i] = scale8(row[i], kc + 2, KS);
-                }
-                ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                tc_fence_after();
-                const uint8_t *st = ring + (size_t)s * G::STAGE;
+                    for (int i = 0; i < NI; ++i) {
+                        n0[i] = n1[i];
+                        if (row[i] && kc + 2 < NKS) n1[i] = scale8(row[i], kc + 2, KS);
+                    }
                 const uint4 a = *(const uint4 *)(st + 8192 + 16 * lane);
                 uint4 b = make_uint4(0, 0, 0, 0);
                 if (2 * kc + 1 < KB) b = *(const uint4 *)(st + MX4_TB + 8192 + 16 * lane);
@@ -549,15 +619,22 @@ int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, i
                 const int32_t *ids, const float *weights, const int32_t *table, int n_slots, const void *pool,
                 size_t slot_bytes, void *out, int otype, void *workspace, cudaStream_t s) {
     const int NT = chunk_routes(T, E, k);
-    const GemmWs L = gemm_ws(T, E, k, NT);
+    const GemmWs L = gemm_ws(T, H, F, E, k, NT);
     int32_t *w = (int32_t *)workspace;
     GemmParams p;
     p.K = down ? F : H;
     p.R_out = down ? H : F;
     p.div = down ? 1 : k;
-    const int rc = encode_codes_map(codes, down ? (long)T * k : T, p.K, &p.map);
-    if (rc != MOE_OK) return rc;
+    p.R = T * k;
+    if (p.R <= MX4_LOCAL_R) {
+        const int rc = encode_codes_map(codes, down ? (long)T * k : T, p.K, &p.map);
+        if (rc != MOE_OK) return rc;
+    }
     p.scales = scales;
+    uint8_t *xg = (uint8_t *)workspace + L.codes, *sg = (uint8_t *)workspace + L.scales;
+    p.xg = xg;
+    p.sg = sg;
+    p.Rp = L.Rp;
     p.pool = (const uint8_t *)pool;
     p.slot_bytes = slot_bytes;
     p.ints = w;
@@ -567,7 +644,6 @@ int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, i
     p.c_n = w + L.o_n;
     p.ids = ids;
     p.table = table;
-    p.R = T * k;
     p.E = E;
     p.n_slots = n_slots;
     p.weights = weights;
@@ -588,6 +664,12 @@ int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, i
         cfg.numAttrs = 2;
         MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_route_kernel, ids, R, E, table, n_slots, NT, w, w + L.o_rows,
                                         w + L.o_slot, w + L.o_pos, w + L.o_n, p.status));
+        const int per_chunk = NT / 8;
+        const long warps = (long)L.max_chunks * per_chunk;
+        moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<long>((warps + 7) / 8, 8 * 152)), dim3(MXG_GATHER_THREADS), 0,
+                       s);
+        MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_gather_kernel, codes, scales, p.K, p.div, per_chunk, L.Rp,
+                                        (const int32_t *)w, p.rows, p.c_pos, p.c_n, xg, sg));
     }
     if (down) return launch_gemm<true, MOE_F32>(p, NT, L.max_chunks, s);
     return otype == MOE_BF16 ? launch_gemm<false, MOE_BF16>(p, NT, L.max_chunks, s)
@@ -613,7 +695,7 @@ extern "C" int moe_mx4_expert_workspace(int T, int H, int F, int E, int k, size_
     MOE_CHECK(bytes);
     const int rc = mx4_ffn_check(T, H, F, E, k);
     if (rc != MOE_OK) return rc;
-    *bytes = (gemm_ws(T, E, k, chunk_routes(T, E, k)).ints * 4 + 255) / 256 * 256;
+    *bytes = (gemm_ws(T, H, F, E, k, chunk_routes(T, E, k)).total + 255) / 256 * 256;
     return MOE_OK;
 }
 
