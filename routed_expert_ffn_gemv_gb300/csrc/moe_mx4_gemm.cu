@@ -31,9 +31,10 @@
 #include "moe_tc.cuh"
 
 #define MXG_THREADS 512
-#define MXG_CTRL 28672
+#define MXG_CTRL 30720
 #define MXG_WBYTES (2 * MX4_TB)  // weights of a stage: two tile blocks
 #define MXG_ROUTE_THREADS 1024
+#define MXG_TABLE 512             // chunks whose table entries are kept in shared memory
 #define MXG_ROUTE_CLUSTER 8
 
 namespace {
@@ -268,6 +269,12 @@ struct GemmGeom {
     static_assert(SFCOL + S * 24 <= 512 && STAGE % 1024 == 0 && SMEM <= 227 * 1024, "budget");
 };
 
+// Where a route's outputs go, and the router weight on them (down).
+struct alignas(16) OutRow {
+    uint8_t *p;
+    float w;
+};
+
 // Four rows of the map's box width to 4 x 128 bytes of shared memory.  x is a multiple of 128.
 __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, int x, const int (&r)[4], uint64_t *bar) {
     asm volatile(
@@ -293,17 +300,18 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     static_assert((3 * G::S + 6) * 8 <= 1024, "barriers");
     float *xch = (float *)(smem + 1024);             // [4 pairs][2 slots][2 ways][8 columns][32 lanes]
-    uint8_t **e_row = (uint8_t **)(smem + 1024 + 16384);  // [2 accumulators][NT] output rows
-    float *e_w = (float *)(e_row + 2 * NT);          // [2 accumulators][NT]
-    Mx4Chunks &loc = *(Mx4Chunks *)(e_w + 2 * NT);   // LOCAL
-    static_assert(1024 + 16384 + 2 * NT * 12 + (LOCAL ? sizeof(Mx4Chunks) : 0) <= MXG_CTRL && MXG_CTRL % 1024 == 0,
+    OutRow *e_out = (OutRow *)(smem + 1024 + 16384);      // [2 accumulators][NT]
+    Mx4Chunks &loc = *(Mx4Chunks *)(e_out + 2 * NT);      // LOCAL
+    int *tab = (int *)(e_out + 2 * NT);                   // otherwise [3][MXG_TABLE]: the chunk table's start
+    static_assert(1024 + 16384 + 2 * NT * 16 + sizeof(Mx4Chunks) <= MXG_CTRL && MXG_CTRL % 1024 == 0 &&
+                      3 * MXG_TABLE * 4 <= sizeof(Mx4Chunks),
                   "control block");
     uint8_t *ring = smem + MXG_CTRL;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::S; ++s) {
-            mbar_init(&s_full[s], 1);
+            mbar_init(&s_full[s], LOCAL ? 1 : 2);
             mbar_init(&s_empty[s], 1);
             mbar_init(&sf_full[s], 4);
         }
@@ -327,17 +335,29 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     pdl_trigger();
     if (LOCAL) mx4_local_chunks(loc, p.ids, p.R, p.E, p.table, p.n_slots, NT, p.status);
     const int *c_slots = LOCAL ? loc.slot : p.c_slot, *c_poss = LOCAL ? loc.pos : p.c_pos, *c_ns = LOCAL ? loc.n : p.c_n;
+    if (!LOCAL && p.ints[0] <= MXG_TABLE) {
+        // every role looks its items up; from global memory each look costs an L2 round trip
+        for (int i = threadIdx.x; i < p.ints[0]; i += MXG_THREADS) {
+            tab[i] = p.c_slot[i];
+            tab[MXG_TABLE + i] = p.c_pos[i];
+            tab[2 * MXG_TABLE + i] = p.c_n[i];
+        }
+        c_slots = tab;
+        c_poss = tab + MXG_TABLE;
+        c_ns = tab + 2 * MXG_TABLE;
+        __syncthreads();
+    }
     const int *rows = LOCAL ? loc.rows : p.rows;
     const int MT = p.MT, n_items = (LOCAL ? loc.nch : p.ints[0]) * MT;
     const int KB = (p.K + 127) / 128, NKS = (KB + 1) / 2, KS = p.K / 32;
 
     if (warp < 2) {
         // ---------------- producers.  LOCAL: warp 0 the stage's expected bytes, its weights and the even
-        // groups of four code rows, warp 1 the odd groups.  Otherwise warp 0's first lane: the
-        // weights, the chunk's rows and their scales, three runs of bytes.
+        // groups of four code rows, warp 1 the odd groups.  Otherwise their first lanes: warp 0
+        // the weights, warp 1 the chunk's rows and scales, runs of bytes.
         int g = 0;
         bool ok = true;
-        for (int j = blockIdx.x; j < n_items && ok && (LOCAL || threadIdx.x == 0); j += gridDim.x) {
+        for (int j = blockIdx.x; j < n_items && ok && (LOCAL || lane == 0); j += gridDim.x) {
             const int c = j / MT, m = j % MT;
             const int slot = c_slots[c];
             if (slot < 0) continue;
@@ -367,11 +387,17 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                     if (4 * q < npad) tma_gather4(st + MXG_WBYTES + q * 512, &p.map, kc * 128, r4, &s_full[s]);
                     __syncwarp();
                 } else {
-                    const uint32_t sb = (uint32_t)((n + 1) & ~1) * 8u;
-                    mbar_arrive_expect_tx(&s_full[s], wb + (uint32_t)n * 128u + sb);
-                    bulk_g2s(st, w + (size_t)kc * MXG_WBYTES, wb, &s_full[s]);
-                    bulk_g2s(st + MXG_WBYTES, p.xg + ((size_t)kc * p.Rp + pos0) * 128, (uint32_t)n * 128u, &s_full[s]);
-                    bulk_g2s(st + G::SOFF, p.sg + ((size_t)kc * p.Rp + pos0) * 8, sb, &s_full[s]);
+                    // two threads, an arrival each: a copy takes its thread about 100 clocks
+                    if (warp == 0) {
+                        mbar_arrive_expect_tx(&s_full[s], wb);
+                        bulk_g2s(st, w + (size_t)kc * MXG_WBYTES, wb, &s_full[s]);
+                    } else {
+                        const uint32_t sb = (uint32_t)((n + 1) & ~1) * 8u;
+                        mbar_arrive_expect_tx(&s_full[s], (uint32_t)n * 128u + sb);
+                        bulk_g2s(st + MXG_WBYTES, p.xg + ((size_t)kc * p.Rp + pos0) * 128, (uint32_t)n * 128u,
+                                 &s_full[s]);
+                        bulk_g2s(st + G::SOFF, p.sg + ((size_t)kc * p.Rp + pos0) * 8, sb, &s_full[s]);
+                    }
                 }
             }
         }
@@ -399,6 +425,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                 for (int kc = 0; kc < NKS; ++kc, ++g) {
                     const int s = g % G::S;
                     if (!(ok = mbar_wait_role(&sf_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
+                    // the scale warps saw the stage land; this thread observes it too (at once)
                     if (!(ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
                     tc_fence_after();
                     uint8_t *st = ring + (size_t)s * G::STAGE;
@@ -488,8 +515,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
             const int pos0 = c_poss[c], n = c_ns[c], buf = jl & 1;
             for (int i = ew * 32 + lane; i < n; i += 256) {
                 const int r = rows[pos0 + i];
-                e_row[buf * NT + i] = (uint8_t *)p.out + (size_t)r * p.R_out * ES;
-                if (DOWN) e_w[buf * NT + i] = p.weights[r];
+                e_out[buf * NT + i] = {(uint8_t *)p.out + (size_t)r * p.R_out * ES, DOWN ? p.weights[r] : 0.f};
             }
             const bool w = mbar_wait_role(&acc_full[buf], (jl / 2) & 1, p.status, abort_flag);
             if (!(ok = bar_and_n(1, 256, w))) break;
@@ -498,17 +524,20 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
             for (int c0 = 16 * half; c0 < n; c0 += 32, ++xs) {
                 uint32_t v[16];
                 tmem_ld16(tb + c0, v);
-                tmem_ld_wait();
-                uint8_t *const *row = e_row + buf * NT + c0;
+                const OutRow *row = e_out + buf * NT + c0;
                 if (!DOWN) {
                     // the gate warp keeps routes 0-7 of the group and hands over 8-15, the up warp the
                     // other way round
                     const int pair = (q & 1) + 2 * half, up = q >> 1;
                     float *xb = xch + (size_t)(pair * 2 + (xs & 1)) * 512 + lane;
+                    uint8_t *o[8];
+                    const int f = 64 * m + 32 * (q & 1) + lane, nn = f < p.R_out ? min(8, n - c0 - 8 * up) : 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = row[8 * up + i].p + (size_t)f * ES;
+                    tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) xb[256 * up + 32 * i] = __uint_as_float(up ? v[i] : v[8 + i]);
                     bar_sync_n(2 + pair, 64);
-                    const int f = 64 * m + 32 * (q & 1) + lane, nn = min(8, n - c0 - 8 * up);
                     float h[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -517,20 +546,32 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                         const float uv = up ? __uint_as_float(v[8 + i]) : other;
                         h[i] = __fdividef(gv, 1.0f + expf(-gv)) * uv;
                     }
-                    if (f < p.R_out)
+                    auto put = [&](int i) {
+                        if (OT == MOE_BF16) *(__nv_bfloat16 *)o[i] = __float2bfloat16(h[i]);
+                        else *(float *)o[i] = h[i];
+                    };
+                    if (nn == 8) {  // no branch between the stores
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) put(i);
+                    } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (i < nn) {
-                                if (OT == MOE_BF16) ((__nv_bfloat16 *)row[8 * up + i])[f] = __float2bfloat16(h[i]);
-                                else ((float *)row[8 * up + i])[f] = h[i];
-                            }
+                            if (i < nn) put(i);
+                    }
                 } else {
-                    const int o = 128 * m + 32 * q + lane, nn = min(16, n - c0);
-                    const float *wt = e_w + buf * NT + c0;
-                    if (o < p.R_out)
+                    const int o = 128 * m + 32 * q + lane, nn = o < p.R_out ? min(16, n - c0) : 0;
+                    OutRow r[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = row[i];
+                    tmem_ld_wait();
+                    if (nn == 16) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) ((float *)r[i].p)[o] = r[i].w * __uint_as_float(v[i]);
+                    } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (i < nn) ((float *)row[i])[o] = wt[i] * __uint_as_float(v[i]);
+                            if (i < nn) ((float *)r[i].p)[o] = r[i].w * __uint_as_float(v[i]);
+                    }
                 }
             }
             tc_fence_before();
