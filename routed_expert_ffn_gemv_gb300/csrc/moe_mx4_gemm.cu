@@ -425,8 +425,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                 for (int kc = 0; kc < NKS; ++kc, ++g) {
                     const int s = g % G::S;
                     if (!(ok = mbar_wait_role(&sf_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
-                    // the scale warps saw the stage land; this thread observes it too (at once)
-                    if (!(ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
+                    // (the scale warps saw the stage land before they arrived)
                     tc_fence_after();
                     uint8_t *st = ring + (size_t)s * G::STAGE;
                     const uint64_t a = umma_desc_sw64(smem_u32(st)), b = umma_desc_sw128(smem_u32(st + MXG_WBYTES));

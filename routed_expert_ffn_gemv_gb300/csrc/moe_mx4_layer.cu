@@ -10,7 +10,7 @@
 //   x: one scale per token (largest magnitude to 7190000, the largest symmetric 8-digit number);
 //   h: one power of two per 32 columns, the MMA's own E8M0 scale (largest magnitude below 2^22).
 //
-//  * mx4_prep_kernel, one 8-CTA cluster per 8 tokens: the router (a CTA sums its eighth of H, the
+//  * mx4_prep_kernel, 8-CTA clusters of 1 to 4 tokens: the router (a CTA sums its eighth of H, the
 //    partial logits meet over distributed shared memory, one warp selects), the tokens' digits in
 //    operand order, and the counters of the second kernel.
 //  * mx4_layer_kernel: persistent.  Units: (chunk of at most NR routes of one expert, 128-row weight
@@ -18,8 +18,8 @@
 //    ever waits for gate/up units that running CTAs hold: no co-residency is needed, and other work
 //    on the GPU cannot deadlock it.  Roles as in the grouped product, with
 //      warp 0      claims units, copies the weights (17 KB a stage: bound by HBM),
-//      warp 1      copies the digits (gate/up: 512 bytes per token and 128 columns; down: once the
-//                  chunk's gate/up units are all done),
+//      warp 1      copies the digits of h once the chunk's gate/up units are all done (and x's, where
+//                  they do not stay in shared memory),
 //      warp 2      the MMAs, warps 4-7 the scales,
 //      warps 8-11  gate/up: sum_p, SwiGLU, the digits and scales of h (a block of 32 columns is a
 //                  warp: one reduction; an 8x8 nibble transpose by three shuffles); down: sum_p, the
@@ -36,10 +36,9 @@
 #include "moe_tc.cuh"
 
 #define MXL_CLUSTER 8
-#define MXL_TOKENS 8          // tokens per cluster
+#define MXL_MAX_CLUSTERS 8    // of the first kernel, 1 to 4 tokens each
 #define MXL_PREP_THREADS 256
 #define MXL_THREADS 384
-#define MXL_SFS 4             // scale slots in tensor memory, 16 columns each
 #define MXL_Q 4               // claimed units in flight in a CTA
 #define MXL_PUB (2 * MXL_Q)   // the epilogue may be MXL_Q units ahead of warp 3 and of a queue slot's reuse
 #define MXL_MAX_R (MOE_DECODE_MAX_T * MOE_MAX_K)
@@ -47,7 +46,7 @@
 #define MXL_BIAS 9586980u     // 4 (8^8 - 1) / 7: turns digits -4 .. 3 into 0 .. 7
 #define MXL_WBYTES (2 * MX4_TB)
 
-static_assert(MXL_MAX_R <= MOE_MAX_E, "one thread per route and per expert");
+static_assert(MXL_MAX_R <= MX4_LOCAL_R, "a CTA groups the routes itself");
 
 namespace {
 
@@ -70,9 +69,9 @@ LayerWs layer_ws(int T, int H, int F, int k) {
     L.ids = take(R * 4);
     L.weights = take(R * 4);
     L.xscale = take((size_t)T * 8);
-    L.xq = take(HB * T * 512);
-    L.hq = take(R * FB * 512);
-    L.hs = take(R * FB * 64);
+    L.xq = take((HB + 1) / 2 * T * 1024);
+    L.hq = take(R * ((FB + 1) / 2) * 1024);
+    L.hs = take(R * ((FB + 1) / 2) * 128);
     L.partial = take(R * H * 4);
     L.total = o;
     return L;
@@ -96,84 +95,106 @@ struct PrepParams {
     int n_ctr;
 };
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 size_t prep_smem(int H, int E, int TT) {
     const int E8 = (E + 7) / 8 * 8;
-    return ((size_t)H / MXL_CLUSTER * TT + (size_t)(MXL_PREP_THREADS / 32 + 1) * TT * E8 + 16) * 4;
+    return ((size_t)H / MXL_CLUSTER * TT + (size_t)(MXL_PREP_THREADS / 32 + 1) * TT * E8) * 4;
 }
 
-// TT: tokens of a cluster (1, 2, 4 or 8; the last cluster may hold fewer).
+__device__ __forceinline__ void half8(const uint4 &u, float (&w)[8]) {
+    const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*(const __half2 *)&q[j]);
+        w[2 * j] = f.x;
+        w[2 * j + 1] = f.y;
+    }
+}
+
+// TT: tokens of a cluster (the last one may hold fewer).  Few tokens to a cluster and up to eight
+// clusters: the router's sums, not its reads of w_router from L2, take the time.
 template <int XT, int TT>
 __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int NW = MXL_PREP_THREADS / 32;
+    __shared__ uint32_t mx_w[TT][MXL_PREP_THREADS / 32], mx[TT], gmx[TT];
+    constexpr int NW = MXL_PREP_THREADS / 32, PRE = 16;  // rows of w_router a thread reads ahead
     const int rank = (int)cluster_ctarank(), tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int HS = p.H / MXL_CLUSTER, h0 = rank * HS, E8 = (p.E + 7) & ~7;
     const int t0 = blockIdx.y * TT, nt = min(TT, p.T - t0);
     float *xs = sm;                   // [HS][TT]
     float *red = xs + HS * TT;        // [NW][TT][E8]
     float *part = red + NW * TT * E8; // [TT][E8]
-    uint32_t *mx = (uint32_t *)(part + TT * E8);
-    pdl_trigger();
-    pdl_wait();
-    if (blockIdx.y == 0)
-        for (int i = rank * MXL_PREP_THREADS + tid; i < p.n_ctr; i += MXL_CLUSTER * MXL_PREP_THREADS) p.ctr[i] = 0;
-    if (warp < TT) {
-        // this CTA's eighth of token `warp`, and its largest magnitude (as bits: NaN sorts above all)
-        uint32_t m = 0;
-        for (int h = lane; h < HS; h += 32) {
-            float v = 0.f;
-            if (warp < nt) {
-                const size_t at = (size_t)(t0 + warp) * p.H + h0 + h;
-                v = XT == MOE_BF16 ? __bfloat162float(((const __nv_bfloat16 *)p.x)[at]) : ((const float *)p.x)[at];
-            }
-            xs[h * TT + warp] = v;
-            m = max(m, __float_as_uint(v) & 0x7FFFFFFFu);
-        }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) mx[warp] = m;
-    }
-    __syncthreads();
     // logits: thread (cg, hsub) takes experts 8 cg .. 8 cg + 7 of rows hsub, hsub + NH, ...
     int ncl = 0;  // log2 of the column groups, a power of two of them
     while ((8 << ncl) < E8) ++ncl;
     const int cg = tid & ((1 << ncl) - 1), hsub = tid >> ncl, NH = MXL_PREP_THREADS >> ncl;
+    const bool has = 8 * cg < p.E;
+    const uint16_t *wr = p.w_router + (size_t)h0 * p.E + 8 * cg;
+    uint4 pre[PRE];
+    pdl_trigger();
+    if (p.wide_w && has)  // the router's weights do not come from the kernel before
+#pragma unroll
+        for (int i = 0; i < PRE; ++i) {
+            const int h = hsub + i * NH;
+            pre[i] = h < HS ? *(const uint4 *)(wr + (size_t)h * p.E) : make_uint4(0, 0, 0, 0);
+        }
+    pdl_wait();
+    if (blockIdx.y == 0)
+        for (int i = rank * MXL_PREP_THREADS + tid; i < p.n_ctr; i += MXL_CLUSTER * MXL_PREP_THREADS) p.ctr[i] = 0;
+    // this CTA's eighth of the tokens, and their largest magnitudes (as bits: NaN sorts above all)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        uint32_t m = 0;
+        for (int h = tid; h < HS; h += MXL_PREP_THREADS) {
+            float v = 0.f;
+            if (t < nt) {
+                const size_t at = (size_t)(t0 + t) * p.H + h0 + h;
+                v = XT == MOE_BF16 ? __bfloat162float(((const __nv_bfloat16 *)p.x)[at]) : ((const float *)p.x)[at];
+            }
+            xs[h * TT + t] = v;
+            m = max(m, __float_as_uint(v) & 0x7FFFFFFFu);
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) mx_w[t][warp] = m;
+    }
+    __syncthreads();
+    if (tid < TT) {
+        uint32_t m = 0;
+        for (int w = 0; w < NW; ++w) m = max(m, mx_w[tid][w]);
+        mx[tid] = m;
+    }
     float acc[TT][8];
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[t][j] = 0.f;
-    if (8 * cg < p.E) {
-        const uint16_t *wr = p.w_router + (size_t)h0 * p.E + 8 * cg;
-        const int ne = min(8, p.E - 8 * cg);
-#pragma unroll 4
-        for (int h = hsub; h < HS; h += NH) {
-            float w[8];
-            if (p.wide_w) {
-                const uint4 u = *(const uint4 *)(wr + (size_t)h * p.E);
-                const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+    auto add_row = [&](int h, const float (&w)[8]) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = __half22float2(*(const __half2 *)&q[j]);
-                    w[2 * j] = f.x;
-                    w[2 * j + 1] = f.y;
+        for (int t = 0; t < TT; ++t) {
+            const float xv = xs[h * TT + t];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(xv, w[j], acc[t][j]);
+        }
+    };
+    if (has) {
+        float w[8];
+        if (p.wide_w) {
+#pragma unroll
+            for (int i = 0; i < PRE; ++i)
+                if (hsub + i * NH < HS) {
+                    half8(pre[i], w);
+                    add_row(hsub + i * NH, w);
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j] = j < ne ? __half2float(__ushort_as_half(wr[(size_t)h * p.E + j])) : 0.f;
+#pragma unroll 4
+            for (int h = hsub + PRE * NH; h < HS; h += NH) {
+                half8(*(const uint4 *)(wr + (size_t)h * p.E), w);
+                add_row(h, w);
             }
-            const float *xh = xs + h * TT;
+        } else {
+            const int ne = min(8, p.E - 8 * cg);
+            for (int h = hsub; h < HS; h += NH) {
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const float xv = xh[t];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(xv, w[j], acc[t][j]);
+                for (int j = 0; j < 8; ++j) w[j] = j < ne ? __half2float(__ushort_as_half(wr[(size_t)h * p.E + j])) : 0.f;
+                add_row(h, w);
             }
         }
     }
@@ -182,7 +203,7 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p
         for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[t][j] += __shfl_xor_sync(0xffffffffu, acc[t][j], o);
-    if (lane < (1 << ncl) && 8 * cg < p.E)
+    if (lane < (1 << ncl) && has)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -195,70 +216,65 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p
         part[i] = s;
     }
     cluster_sync_all();
-    // token t0 + rank is selected by this CTA's first warp
-    if (warp == 0 && rank < nt) {
-        float v[MOE_MAX_E / 32];
+    if (warp == 0) {
+        // token t0 + rank is selected by this CTA's first warp
+        if (rank < nt) {
+            float v[MOE_MAX_E / 32];
 #pragma unroll
-        for (int i = 0; i < MOE_MAX_E / 32; ++i) {
-            const int e = lane + 32 * i;
-            v[i] = -INFINITY;
-            if (e < p.E) {
-                float s = 0.f;
+            for (int i = 0; i < MOE_MAX_E / 32; ++i) {
+                const int e = lane + 32 * i;
+                v[i] = -INFINITY;
+                if (e < p.E) {
+                    float s = 0.f;
 #pragma unroll
-                for (int r = 0; r < MXL_CLUSTER; ++r) s += ld_cluster_f32(cluster_map(&part[rank * E8 + e], r));
-                if (p.bias) s += p.bias[e];
-                v[i] = (s != s) ? -INFINITY : s;  // NaN never wins
+                    for (int r = 0; r < MXL_CLUSTER; ++r) s += ld_cluster_f32(cluster_map(&part[rank * E8 + e], r));
+                    if (p.bias) s += p.bias[e];
+                    v[i] = (s != s) ? -INFINITY : s;  // NaN never wins
+                }
             }
+            select_topk_softmax(v, p.E, p.k, lane, (size_t)(t0 + rank), p.ids, p.weights, 0.f);
         }
-        select_topk_softmax(v, p.E, p.k, lane, (size_t)(t0 + rank), p.ids, p.weights, 0.f);
-    }
-    // digits: eight columns of one token per thread
-    float m_norm[TT], m_pow[TT];
+    } else {
+        // digits, by the other warps: eight columns of one token per thread
+        if (warp == 1) {
+            uint32_t m = lane < TT * MXL_CLUSTER ? ld_cluster_u32(cluster_map(&mx[lane / MXL_CLUSTER], lane % MXL_CLUSTER)) : 0;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int r = 0; r < MXL_CLUSTER; ++r) m = max(m, ld_cluster_u32(cluster_map(&mx[t], r)));
-        // largest magnitude = norm * pow, norm in [1, 2), pow a power of two (possibly subnormal)
-        const int e = (int)(m >> 23);
-        float norm = __uint_as_float((m & 0x7FFFFFu) | 0x3F800000u), pw = __uint_as_float((uint32_t)e << 23);
-        if (m == 0 || e == 255) {
-            norm = m == 0 ? 1.f : __uint_as_float(0x7FC00000u);
-            pw = 1.f;
-        } else if (e == 0) {
-            const int top = 31 - __clz(m);
-            norm = (float)m / (float)(1u << top);
-            pw = __uint_as_float(1u << top);
+            for (int o = 1; o < MXL_CLUSTER; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane < TT * MXL_CLUSTER && lane % MXL_CLUSTER == 0) gmx[lane / MXL_CLUSTER] = m;
         }
-        m_norm[t] = norm;
-        m_pow[t] = pw;
-        if (rank == 0 && tid == t && t < nt) p.xscale[t0 + t] = make_float2(norm / MXL_XMAX, pw);
-    }
-    const int per = p.H / 8;
-    for (int i = rank * MXL_PREP_THREADS + tid; i < nt * per; i += MXL_CLUSTER * MXL_PREP_THREADS) {
-        const int t = i / per, col = (i - t * per) * 8;
-        float v[8];
-        load8<XT>(p.x, (size_t)(t0 + t) * p.H + col, p.wide_x, v);
-        float norm = m_norm[0], pw = m_pow[0];
-#pragma unroll
-        for (int q = 1; q < TT; ++q)
-            if (t == q) {
-                norm = m_norm[q];
-                pw = m_pow[q];
+        bar_sync_n(1, MXL_PREP_THREADS - 32);
+        const int per = p.H / 8;
+        for (int i = rank * (MXL_PREP_THREADS - 32) + tid - 32; i < nt * per; i += MXL_CLUSTER * (MXL_PREP_THREADS - 32)) {
+            const int t = i / per, col = (i - t * per) * 8;
+            float v[8];
+            load8<XT>(p.x, (size_t)(t0 + t) * p.H + col, p.wide_x, v);
+            // largest magnitude = norm * pw, norm in [1, 2), pw a power of two (possibly subnormal)
+            const uint32_t m = gmx[t];
+            const int e = (int)(m >> 23);
+            float norm = __uint_as_float((m & 0x7FFFFFu) | 0x3F800000u), pw = __uint_as_float((uint32_t)e << 23);
+            if (m == 0 || e == 255) {
+                norm = m == 0 ? 1.f : __uint_as_float(0x7FC00000u);
+                pw = 1.f;
+            } else if (e == 0) {
+                const int top = 31 - __clz(m);
+                norm = (float)m / (float)(1u << top);
+                pw = __uint_as_float(1u << top);
             }
-        // x / pow in (-2, 2): by two exact factors where 1 / pow would overflow
-        const float f = MXL_XMAX / norm, i1 = pw < 1e-30f ? 1.2676506e30f : 1.f, i2 = 1.f / (pw * i1);
-        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (col == 0) p.xscale[t0 + t] = make_float2(norm / MXL_XMAX, pw);
+            // x / pw in (-2, 2): by two exact factors where 1 / pw would overflow
+            const float f = MXL_XMAX / norm, i1 = pw < 1e-30f ? 1.2676506e30f : 1.f, i2 = 1.f / (pw * i1);
+            uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t u = (uint32_t)(__float2int_rn(v[j] * i1 * i2 * f)) + MXL_BIAS;
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t u = (uint32_t)(__float2int_rn(v[j] * i1 * i2 * f)) + MXL_BIAS;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] |= digit_code((u >> (3 * q)) & 7u) << (4 * j);
+                for (int q = 0; q < 8; ++q) w[q] |= digit_code((u >> (3 * q)) & 7u) << (4 * j);
+            }
+            uint8_t *atom = p.xq + ((size_t)(col >> 8) * p.T + t0 + t) * 1024 + ((col >> 7) & 1) * 512;
+            const int c = (col >> 5) & 3, o = 4 * ((col >> 3) & 3);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) *(uint32_t *)(atom + q * 64 + ((c ^ ((q >> 1) & 3)) << 4) + o) = w[q];
         }
-        uint8_t *atom = p.xq + ((size_t)(col >> 7) * p.T + t0 + t) * 512;
-        const int c = (col >> 5) & 3, o = 4 * ((col >> 3) & 3);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) *(uint32_t *)(atom + q * 64 + ((c ^ ((q >> 1) & 3)) << 4) + o) = w[q];
     }
     cluster_sync_all();  // partial logits and maxima stay until every CTA has read them
 }
@@ -279,18 +295,21 @@ struct FfnParams {
     float *partial, *y;
     int *ticket, *ready, *done;
     int *status;
+    int res;      // bytes of resident digits (0: copied by stage)
+    int S, stage; // ring stages, bytes of one
 };
 
+// Shared memory: control, the tokens' digits (resident: T <= NR = 8, and enough of the ring left),
+// then S stages of two weight blocks, `cap` routes' digits (1024 bytes each: two 512-byte atoms of 8
+// rows x 128 columns) and 128 bytes of h scales.
 template <int NR>
 struct LayerGeom {
-    static constexpr int S = NR == 8 ? 7 : 5;
-    static constexpr int BOFF = MXL_WBYTES, HSOFF = BOFF + 2 * NR * 512;
-    static constexpr int STAGE = HSOFF + 512;
     static constexpr int N = NR * 8;
-    static constexpr int SFCOL = 2 * N;
-    static constexpr int CTRL = 1024 + 2 * 4 * NR / 2 * 32 * 4 + 5 * MXL_MAX_R * 4 + 1024;
-    static constexpr size_t SMEM = 1024 + (CTRL + 1023) / 1024 * 1024 + (size_t)S * STAGE;
-    static_assert(SFCOL + MXL_SFS * 16 <= 512 && S > MXL_SFS && STAGE % 512 == 0 && SMEM <= 227 * 1024, "budget");
+    static constexpr int SFCOL = 2 * N;      // scales after the two accumulators, 16 columns a stage
+    static constexpr int MAXS = 10;
+    static constexpr int CTRL = (1024 + 2 * 4 * NR / 2 * 32 * 4 + (int)sizeof(Mx4Chunks) + MXL_MAX_R * 4 +
+                                 MOE_DECODE_MAX_T * 8 + 1023) / 1024 * 1024;
+    static_assert(SFCOL + MAXS * 16 <= 512, "tensor memory");
 };
 
 __device__ __forceinline__ int ld_acquire_gpu(const int *a) {
@@ -299,7 +318,7 @@ __device__ __forceinline__ int ld_acquire_gpu(const int *a) {
     return v;
 }
 __device__ __forceinline__ void red_release_gpu(int *a) {
-    asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.s32 [%0], 1;" ::"l"(a) : "memory");
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(a) : "memory");
 }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
@@ -318,9 +337,9 @@ __device__ __forceinline__ Unit unit_of(int u, int nch, int FT, int HT) {
     return r;
 }
 
-// y[t][columns of tile m] = extra + the partial rows of token t's routes, in route order (`ok`: routes
-// that were computed), for eight tokens by 128 threads: four columns of a token to a thread.
-__device__ __forceinline__ void combine_tile(const FfnParams &p, int m, int t0, int thr, const int *ok) {
+// y[t][columns of tile m] = extra + the partial rows of token t's routes, in route order (`id` -1: not
+// computed), for eight tokens by 128 threads: four columns of a token to a thread.
+__device__ __forceinline__ void combine_tile(const FfnParams &p, int m, int t0, int thr, const int *id) {
     const int o = 128 * m + 4 * (thr & 31);
     if (o >= p.H) return;
 #pragma unroll
@@ -330,7 +349,7 @@ __device__ __forceinline__ void combine_tile(const FfnParams &p, int m, int t0, 
         float4 v[MOE_MAX_K];
 #pragma unroll
         for (int j = 0; j < MOE_MAX_K; ++j)
-            v[j] = j < p.k && ok[t * p.k + j] ? __ldcg((const float4 *)(p.partial + (size_t)(t * p.k + j) * p.H + o))
+            v[j] = j < p.k && id[t * p.k + j] >= 0 ? __ldcg((const float4 *)(p.partial + (size_t)(t * p.k + j) * p.H + o))
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         const size_t at = (size_t)t * p.H + o;
@@ -364,40 +383,40 @@ __device__ __forceinline__ bool wait_count(const int *a, int want, int *status, 
 }
 
 template <int NR>
-__global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnParams p) {
+__global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_constant__ FfnParams p) {
     using G = LayerGeom<NR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     uint64_t *s_full = (uint64_t *)smem;       // weights and digits of a stage
-    uint64_t *s_empty = s_full + G::S;
-    uint64_t *sf_full = s_empty + G::S;
-    uint64_t *acc_full = sf_full + MXL_SFS;
+    uint64_t *s_empty = s_full + G::MAXS;
+    uint64_t *sf_full = s_empty + G::MAXS;
+    uint64_t *acc_full = sf_full + G::MAXS;
     uint64_t *acc_empty = acc_full + 2;
     uint64_t *q_full = acc_empty + 2;
     uint64_t *q_empty = q_full + MXL_Q;
     uint64_t *pub = q_empty + MXL_Q;           // a unit's outputs are written (4 epilogue warps)
-    uint64_t *mma_done = pub + MXL_PUB;
+    uint64_t *x_full = pub + MXL_PUB;          // resident digits
+    uint64_t *mma_done = x_full + 1;
     uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *q_unit = (volatile int *)(tmem_slot + 2);  // [MXL_Q]
-    int *s_nch = (int *)(tmem_slot + 2 + MXL_Q);
-    int *s_scan = s_nch + 1;                                 // [8]
-    static_assert((2 * G::S + MXL_SFS + 4 + 2 * MXL_Q + MXL_PUB + 1) * 8 + (2 + MXL_Q + 9) * 4 <= 1024, "barriers");
+    static_assert((3 * G::MAXS + 4 + 2 * MXL_Q + MXL_PUB + 2) * 8 + (2 + MXL_Q) * 4 <= 1024, "barriers");
     float *xch = (float *)(smem + 1024);                     // [2 buffers][2 pairs][2 ways][NR / 2][32]
-    int *c_slot = (int *)(xch + 2 * 4 * (NR / 2) * 32);      // [MXL_MAX_R] each
-    int *c_pos = c_slot + MXL_MAX_R;
-    int *c_n = c_pos + MXL_MAX_R;
-    int *rows = c_n + MXL_MAX_R;
-    int *r_ok = rows + MXL_MAX_R;                            // ids first, then whether a route is computed
-    uint8_t *ring = smem + (G::CTRL + 1023) / 1024 * 1024;
+    Mx4Chunks &ch = *(Mx4Chunks *)(xch + 2 * 4 * (NR / 2) * 32);
+    float *s_w = (float *)(&ch + 1);                         // [MXL_MAX_R] router weights
+    float2 *s_xs = (float2 *)(s_w + MXL_MAX_R);              // [MOE_DECODE_MAX_T]
+    uint8_t *xres = smem + G::CTRL;
+    uint8_t *ring = xres + p.res;
+    const int S = p.S, STAGE = p.stage;
+    const int hs_off = STAGE - 128;                          // h scales at a stage's end
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
-        for (int s = 0; s < G::S; ++s) {
-            mbar_init(&s_full[s], 2);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&s_full[s], 1);
             mbar_init(&s_empty[s], 1);
+            mbar_init(&sf_full[s], 4);
         }
-        for (int s = 0; s < MXL_SFS; ++s) mbar_init(&sf_full[s], 4);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 4);
@@ -407,6 +426,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
             mbar_init(&q_empty[q], 11);  // every warp but warp 0
         }
         for (int q = 0; q < MXL_PUB; ++q) mbar_init(&pub[q], 4);
+        mbar_init(x_full, 1);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -417,67 +437,23 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
     }
     pdl_wait();
     pdl_trigger();
-    // the first unit is claimed while the chunks are put together
+    // the first unit is claimed, and the resident digits are fetched, while the chunks are put together
     int claim = 0;
-    if (tid == 0) claim = atomicAdd(p.ticket, 1);
+    if (tid == 0) {
+        claim = atomicAdd(p.ticket, 1);
+        if (p.res) {
+            mbar_arrive_expect_tx(x_full, (uint32_t)p.res);
+            bulk_g2s(xres, p.xq, (uint32_t)p.res, x_full);
+        }
+    }
     const int R = p.T * p.k;
-    int *s_ids = c_slot;  // until the chunks are written
-    if (tid < MXL_MAX_R) s_ids[tid] = tid < R ? p.ids[tid] : -1;
+    if (tid < R) s_w[tid] = p.weights[tid];
+    if (tid < p.T) s_xs[tid] = p.xscale[tid];
     tc_fence_before();
-    __syncthreads();
+    mx4_local_chunks(ch, p.ids, R, p.E, p.table, p.n_slots, NR, p.status);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // chunks: thread e counts expert e's routes; exclusive sums give its chunks and positions
-    int cnt = 0, slot = -1, pk = 0, incl = 0;
-    if (tid < MOE_MAX_E) {
-        for (int r = 0; r < R; ++r) cnt += s_ids[r] == tid;
-        if (cnt > 0) {
-            slot = p.table ? p.table[tid] : tid;
-            if (slot < 0 || slot >= p.n_slots) {
-                moe_set_status(p.status, MOE_ERR_INVALID);
-                cnt = 0;
-            }
-        }
-        pk = cnt | ((cnt + NR - 1) / NR) << 16;
-        incl = pk;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) s_scan[warp] = incl;
-        r_ok[tid] = 0;
-    }
-    const int my_ids = tid < MXL_MAX_R ? s_ids[tid] : -1;
-    __syncthreads();
-    if (tid < MOE_MAX_E) {
-        int before = incl - pk;
-        for (int w = 0; w < warp; ++w) before += s_scan[w];
-        if (tid == MOE_MAX_E - 1) *s_nch = (before + pk) >> 16;
-        // route ids move out of the chunk table's space
-        c_n[tid] = my_ids;
-        incl = before;
-    }
-    __syncthreads();
-    if (tid < MOE_MAX_E && cnt > 0) {
-        int at = incl & 0xFFFF;
-        for (int r = 0; r < R; ++r)
-            if (c_n[r] == tid) {
-                rows[at++] = r;
-                r_ok[r] = 1;
-            }
-    }
-    __syncthreads();
-    if (tid < MOE_MAX_E && cnt > 0) {
-        const int c0 = incl >> 16, pos = incl & 0xFFFF, nc = (cnt + NR - 1) / NR;
-        for (int c = 0; c < nc; ++c) {
-            const int a = cnt * c / nc, b = cnt * (c + 1) / nc;
-            c_slot[c0 + c] = slot;
-            c_pos[c0 + c] = pos + a;
-            c_n[c0 + c] = b - a;
-        }
-    }
-    __syncthreads();
-    const int nch = *s_nch;
+    const int nch = ch.nch;
     const int HB = (p.H + 127) / 128, FB = (p.F + 127) / 128, FT = (p.F + 63) / 64, HT = HB;
     const int n_units = nch * (FT + HT) + HT * ((p.T + 7) / 8);
     const size_t down_off = mx4_gu_bytes(p.H, p.F);
@@ -493,17 +469,27 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
         if (lane == 0) mbar_arrive1(&q_empty[q]);
         return u;
     };
+    // ring position: stage index and the parity of its current fill
+    int s = 0;
+    uint32_t ph = 0;
+    auto advance = [&]() {
+        if (++s == S) {
+            s = 0;
+            ph ^= 1u;
+        }
+    };
 
     if (nch == 0) {
         // no expert is resident: the layer is its extra
+        if (tid == 0 && p.res) mbar_wait_role(x_full, 0, p.status, abort_flag);
         for (int m = blockIdx.x; m < HT; m += gridDim.x)
             if (tid < 128)
-                for (int t = 0; t < p.T; t += 8) combine_tile(p, m, t, tid, r_ok);
+                for (int t = 0; t < p.T; t += 8) combine_tile(p, m, t, tid, ch.id);
     } else if (warp == 0) {
-        // ---------------- claims and weights
+        // ---------------- claims and weights; a stage's barrier expects its digits' bytes too
         if (lane == 0) {
-            int g = 0;
             bool ok = true;
+            int fills = 0;
             for (int i = 0; ok; ++i) {
                 const int q = i % MXL_Q, u = claim < n_units ? claim : -1;
                 if (i >= MXL_Q && !(ok = mbar_wait_role(&q_empty[q], ((i / MXL_Q) & 1) ^ 1, p.status, abort_flag))) break;
@@ -515,30 +501,32 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
                 if (un.kind == MXL_COMBINE) continue;
                 const bool down = un.kind == MXL_DOWN;
                 const int KB = down ? FB : HB, NKS = (KB + 1) / 2;
-                const uint8_t *w = p.pool + (size_t)c_slot[un.c] * p.slot_bytes + (down ? down_off : 0) +
+                const uint32_t nb = down ? (uint32_t)ch.n[un.c] * 1024u + 128u : p.res ? 0u : (uint32_t)ch.n[un.c] * 1024u;
+                const uint8_t *w = p.pool + (size_t)ch.slot[un.c] * p.slot_bytes + (down ? down_off : 0) +
                                    (size_t)un.m * KB * MX4_TB;
-                for (int kc = 0; kc < NKS; ++kc, ++g) {
-                    const int s = g % G::S;
-                    if (g >= G::S && !(ok = mbar_wait_role(&s_empty[s], ((g / G::S) & 1) ^ 1, p.status, abort_flag)))
-                        break;
+                for (int kc = 0; kc < NKS; ++kc, advance(), ++fills) {
+                    if (fills >= S && !(ok = mbar_wait_role(&s_empty[s], ph ^ 1u, p.status, abort_flag))) break;
                     const uint32_t wb = 2 * kc + 1 < KB ? MXL_WBYTES : MX4_TB;
-                    mbar_arrive_expect_tx(&s_full[s], wb);
-                    bulk_g2s(ring + (size_t)s * G::STAGE, w + (size_t)kc * MXL_WBYTES, wb, &s_full[s]);
+                    mbar_arrive_expect_tx(&s_full[s], wb + nb);
+                    bulk_g2s(ring + (size_t)s * STAGE, w + (size_t)kc * MXL_WBYTES, wb, &s_full[s]);
                 }
             }
-            if (!ok) {
-                settle_after_abort();
-            } else {
-                for (int s = 0; s < G::S && s < g; ++s) {
-                    const int last = s + ((g - 1 - s) / G::S) * G::S;
-                    mbar_wait_role(&s_full[s], (last / G::S) & 1, p.status, abort_flag);
+            // never leave with copies in flight: the last fill of every stage
+            if (ok && p.res) ok = mbar_wait_role(x_full, 0, p.status, abort_flag);
+            for (int i = 0; ok && i < S && i < fills; ++i) {
+                if (--s < 0) {
+                    s = S - 1;
+                    ph ^= 1u;
                 }
+                ok = mbar_wait_role(&s_full[s], ph, p.status, abort_flag);
             }
+            if (!ok) settle_after_abort();
         }
     } else if (warp == 1) {
-        // ---------------- digits
-        int g = 0;
+        // ---------------- digits (it keeps step with the ring through the units that need none)
         bool ok = true;
+        int fills = 0;
+        uint32_t ready = 0;  // bit b: chunk 32 b + lane has all its rows of h
         for (int i = 0; ok; ++i) {
             const int u = next_unit(i);
             if (u < 0) {
@@ -548,63 +536,69 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
             const Unit un = unit_of(u, nch, FT, HT);
             if (un.kind == MXL_COMBINE) continue;
             const bool down = un.kind == MXL_DOWN;
-            const int KB = down ? FB : HB, NKS = (KB + 1) / 2, n = c_n[un.c], pos = c_pos[un.c];
+            const int NKS = ((down ? FB : HB) + 1) / 2, n = ch.n[un.c], pos = ch.pos[un.c];
             if (down) {
-                // every gate/up unit of the chunk is done, its digits and scales written
-                if (!(ok = wait_count(&p.ready[un.c], FT, p.status, abort_flag))) break;
+                // every gate/up unit of the chunk is done, its digits and scales written.  One look covers 32
+                // chunks, so a chunk seen ready costs no more looks.
+                const int b = un.c >> 5, mine = 32 * b + lane;
+                for (uint32_t it = 0; !(__shfl_sync(0xffffffffu, ready, un.c & 31) >> b & 1u); ++it) {
+                    if (mine < nch && ld_acquire_gpu(&p.ready[mine]) >= FT) ready |= 1u << b;
+                    if (it >= MOE_SPIN_LIMIT && lane == 0) {
+                        moe_set_status(p.status, MOE_ERR_TIMEOUT);
+                        *abort_flag = 1;
+                    }
+                    if (!(ok = __all_sync(0xffffffffu, !*abort_flag))) break;
+                }
+                if (!ok) break;
+                __syncwarp();
                 fence_proxy_async_all();
             }
-            // gate/up: lane i copies the digits of the chunk's token i
-            const int tok = !down && lane < n ? rows[pos + lane] / p.k : 0;
-            for (int kc = 0; kc < NKS; ++kc, ++g) {
-                const int s = g % G::S;
-                if (g >= G::S) ok = mbar_wait_role(&s_empty[s], ((g / G::S) & 1) ^ 1, p.status, abort_flag);
+            const int tok = !down && lane < n ? ch.rows[pos + lane] / p.k : 0;
+            for (int kc = 0; kc < NKS; ++kc, advance(), ++fills) {
+                if (fills >= S) ok = mbar_wait_role(&s_empty[s], ph ^ 1u, p.status, abort_flag);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                uint8_t *st = ring + (size_t)s * G::STAGE;
-                const int nb = min(2, KB - 2 * kc);
-                if (lane == 0) mbar_arrive_expect_tx(&s_full[s], (uint32_t)(nb * (n * 512 + (down ? 64 : 0))));
-                __syncwarp();
-                if (!down) {
-                    if (lane < n)
-                        for (int b = 0; b < nb; ++b)
-                            bulk_g2s(st + G::BOFF + b * NR * 512 + lane * 512,
-                                     p.xq + ((size_t)(2 * kc + b) * p.T + tok) * 512, 512, &s_full[s]);
-                } else if (lane < nb) {
-                    const int kb = 2 * kc + lane;
-                    bulk_g2s(st + G::BOFF + lane * NR * 512, p.hq + ((size_t)pos * FB + (size_t)kb * n) * 512,
-                             (uint32_t)n * 512u, &s_full[s]);
-                    bulk_g2s(st + G::HSOFF + lane * 64, p.hs + ((size_t)un.c * FB + kb) * 16, 64, &s_full[s]);
+                uint8_t *st = ring + (size_t)s * STAGE;
+                if (down) {
+                    if (lane == 0) {
+                        bulk_g2s(st + MXL_WBYTES, p.hq + ((size_t)pos * ((FB + 1) / 2) + (size_t)kc * n) * 1024,
+                                 (uint32_t)n * 1024u, &s_full[s]);
+                        bulk_g2s(st + hs_off, p.hs + ((size_t)un.c * ((FB + 1) / 2) + kc) * 32, 128, &s_full[s]);
+                    }
+                } else if (!p.res && lane < n) {
+                    bulk_g2s(st + MXL_WBYTES + lane * 1024, p.xq + ((size_t)kc * p.T + tok) * 1024, 1024, &s_full[s]);
                 }
                 __syncwarp();
             }
         }
         if (!ok) settle_after_abort();
     } else if (warp == 2) {
-        // ---------------- MMA issuer
-        int g = 0;
-        bool ok = true;
+        // ---------------- MMA issuer.  Resident digits: gate/up multiplies every token's (the width is
+        // free, and the chunk's tokens need not be adjacent)
+        bool ok = true, xok = !p.res;
         for (int i = 0; ok; ++i) {
             const int u = next_unit(i);
             if (u < 0) break;
             const Unit un = unit_of(u, nch, FT, HT);
             if (un.kind == MXL_COMBINE) continue;  // these come last: units before them keep their numbering
             if (lane == 0) {
-                const int K = un.kind == MXL_DOWN ? p.F : p.H, NKS = (K + 255) / 256, N = 8 * c_n[un.c];
+                const bool down = un.kind == MXL_DOWN, all = !down && p.res;
+                if (all && !xok) ok = xok = mbar_wait_role(x_full, 0, p.status, abort_flag);
+                const int K = down ? p.F : p.H, NKS = (K + 255) / 256, N = 8 * (all ? p.T : ch.n[un.c]);
                 const uint32_t id0 = umma_idesc_mxf4(128, N, 0), id2 = umma_idesc_mxf4(128, N, 2);
                 const int buf = i & 1;
-                if (i >= 2) ok = mbar_wait_role(&acc_empty[buf], ((i / 2) - 1) & 1, p.status, abort_flag);
+                if (ok && i >= 2) ok = mbar_wait_role(&acc_empty[buf], ((i / 2) - 1) & 1, p.status, abort_flag);
                 tc_fence_after();
                 const uint32_t d = tmem + buf * G::N;
-                for (int kc = 0; kc < NKS && ok; ++kc, ++g) {
-                    const int s = g % G::S, f = g % MXL_SFS;
-                    if (!(ok = mbar_wait_role(&sf_full[f], (g / MXL_SFS) & 1, p.status, abort_flag))) break;
-                    if (!(ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
+                for (int kc = 0; kc < NKS && ok; ++kc, advance()) {
+                    // (the scale warps saw the stage land before they arrived)
+                    if (!(ok = mbar_wait_role(&sf_full[s], ph, p.status, abort_flag))) break;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(ring + (size_t)s * G::STAGE);
-                    const uint64_t a = umma_desc_sw64(st), b = umma_desc_sw64(st + G::BOFF);
-                    const uint32_t sf = tmem + G::SFCOL + 16 * f;
+                    const uint32_t st = smem_u32(ring + (size_t)s * STAGE);
+                    const uint64_t a = umma_desc_sw64(st);
+                    const uint64_t b = umma_desc_sw64_rows1024(all ? smem_u32(xres) + kc * p.T * 1024 : st + MXL_WBYTES);
+                    const uint32_t sf = tmem + G::SFCOL + 16 * s;
                     const int steps = min(4, (K - 256 * kc + 63) / 64);
-                    constexpr int A1 = MX4_TB >> 4, B1 = NR * 512 >> 4;
+                    constexpr int A1 = MX4_TB >> 4, B1 = 512 >> 4;
                     umma_mxf4(d, a, b, id0, sf, sf + 8, kc > 0);
                     if (steps > 1) umma_mxf4(d, a + 2, b + 2, id2, sf, sf + 8, 1);
                     if (steps > 2) umma_mxf4(d, a + A1, b + B1, id0, sf + 4, sf + 12, 1);
@@ -632,15 +626,15 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
             ok = mbar_wait_role(&pub[i % MXL_PUB], (i / MXL_PUB) & 1, p.status, abort_flag);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             if (lane == 0) {
-                fence_proxy_async_all();
+                if (un.kind == MXL_UP) fence_proxy_async_all();
                 red_release_gpu(un.kind == MXL_UP ? &p.ready[un.c] : &p.done[un.m]);
             }
             __syncwarp();
         }
     } else if (warp >= 4 && warp < 8) {
-        // ---------------- scales: the weights' rows lane, lane + 32, ..; a route's for its 8 columns
+        // ---------------- scales: the weights' rows lane, lane + 32, ..; a route's for its 8 columns (1 for
+        // x, whose scale is applied at the end)
         const uint32_t t0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::SFCOL;
-        int g = 0;
         bool ok = true;
         for (int i = 0; ok; ++i) {
             const int u = next_unit(i);
@@ -649,37 +643,42 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
             if (un.kind == MXL_COMBINE) continue;
             const bool down = un.kind == MXL_DOWN;
             const int KB = down ? FB : HB, NKS = (KB + 1) / 2;
-            for (int kc = 0; kc < NKS; ++kc, ++g) {
-                const int s = g % G::S, f = g % MXL_SFS;
-                if (g >= MXL_SFS)
-                    ok = mbar_wait_role(&s_empty[(g - MXL_SFS) % G::S], ((g - MXL_SFS) / G::S) & 1, p.status, abort_flag);
-                if (ok) ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag);
+            for (int kc = 0; kc < NKS; ++kc, advance()) {
+                ok = mbar_wait_role(&s_full[s], ph, p.status, abort_flag);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
-                const uint8_t *st = ring + (size_t)s * G::STAGE;
+                const uint8_t *st = ring + (size_t)s * STAGE;
                 const bool two = 2 * kc + 1 < KB;
                 const uint4 a = *(const uint4 *)(st + 8192 + 16 * lane);
                 uint4 b = make_uint4(0, 0, 0, 0);
                 if (two) b = *(const uint4 *)(st + MX4_TB + 8192 + 16 * lane);
-                uint32_t va[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, vb[8];
-                const uint32_t *hs = (const uint32_t *)(st + G::HSOFF) + (lane >> 3);
+                const uint32_t va[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                uint32_t vb[8];
+                const uint32_t *hs = (const uint32_t *)(st + hs_off) + (lane >> 3);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     vb[c] = down ? hs[4 * c] : 0x7F7F7F7Fu;
-                    vb[4 + c] = down ? (two ? hs[16 + 4 * c] : 0u) : 0x7F7F7F7Fu;
+                    vb[4 + c] = down ? hs[16 + 4 * c] : 0x7F7F7F7Fu;
                 }
-                tmem_st8(t0 + 16 * f, va);
-                tmem_st8(t0 + 16 * f + 8, vb);
+                tmem_st8(t0 + 16 * s, va);
+                tmem_st8(t0 + 16 * s + 8, vb);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive1(&sf_full[f]);
+                if (lane == 0) mbar_arrive1(&sf_full[s]);
             }
         }
     } else if (warp >= 8) {
         // ---------------- epilogue
         const int q = warp & 3, ew = tid - 256;
         const float pow8[8] = {1.f, 8.f, 64.f, 512.f, 4096.f, 32768.f, 262144.f, 2097152.f};
+        // sum_p 8^p (eight columns), smallest first
+        auto digit_sum = [&](const uint32_t (&v)[8]) {
+            float a = __uint_as_float(v[0]);
+#pragma unroll
+            for (int d = 1; d < 8; ++d) a = fmaf(__uint_as_float(v[d]), pow8[d], a);
+            return a;
+        };
         for (int i = 0;; ++i) {
             const int u = next_unit(i);
             bool ok = u != -2;
@@ -691,11 +690,11 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
             }
             if (!bar_and_n(1, 128, ok) || u < 0) break;
             if (un.kind == MXL_COMBINE) {
-                combine_tile(p, un.m, 8 * un.c, ew, r_ok);
+                combine_tile(p, un.m, 8 * un.c, ew, ch.id);
                 continue;
             }
             tc_fence_after();
-            const int buf = i & 1, n = c_n[un.c], pos = c_pos[un.c];
+            const int buf = i & 1, n = ch.n[un.c], pos = ch.pos[un.c];
             const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * G::N;
             if (un.kind == MXL_UP) {
                 // route i's gate (lane quarters 0, 1) and up (2, 3) values; the gate warps finish the even
@@ -706,15 +705,12 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
 #pragma unroll
                 for (int c = 0; c < NR / 2; ++c) {
                     if (2 * c < n) {
-                        uint32_t v[16];
-                        tmem_ld16(tb + 16 * c, v);
+                        const int r1 = min(2 * c + 1, n - 1);
+                        uint32_t v0[8], v1[8];
+                        tmem_ld8(tb + 8 * (p.res ? ch.rows[pos + 2 * c] / p.k : 2 * c), v0);
+                        tmem_ld8(tb + 8 * (p.res ? ch.rows[pos + r1] / p.k : r1), v1);
                         tmem_ld_wait();
-                        float a = __uint_as_float(v[0]), b = __uint_as_float(v[8]);
-#pragma unroll
-                        for (int d = 1; d < 8; ++d) {
-                            a = fmaf(__uint_as_float(v[d]), pow8[d], a);
-                            b = fmaf(__uint_as_float(v[8 + d]), pow8[d], b);
-                        }
+                        const float a = digit_sum(v0), b = digit_sum(v1);
                         mine[c] = q < 2 ? a : b;
                         out[32 * c] = q < 2 ? b : a;
                     }
@@ -723,16 +719,16 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(&acc_empty[buf]);
                 bar_sync_n(2 + (q & 1), 64);
-                const int f0 = 64 * un.m + 32 * (q & 1), kb = f0 >> 7, cb = (f0 >> 5) & 3;
+                const int f0 = 64 * un.m + 32 * (q & 1), kb = f0 >> 7, cb = (f0 >> 5) & 3, HK = (FB + 1) / 2;
 #pragma unroll
                 for (int c = 0; c < NR / 2; ++c) {
                     const int r = 2 * c + (q >> 1);
                     if (r < n) {
-                        const float2 xs = p.xscale[rows[pos + r] / p.k];
+                        const float2 xs = s_xs[ch.rows[pos + r] / p.k];
                         const float other = in[32 * c];
                         const float gv = (q < 2 ? mine[c] : other) * xs.x * xs.y;
                         const float uv = (q < 2 ? other : mine[c]) * xs.x * xs.y;
-                        const float h = gv / (1.0f + expf(-gv)) * uv;
+                        const float h = __fdividef(gv, 1.0f + expf(-gv)) * uv;
                         const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23);
                         const int sc = e == 255 ? 255 : max(0, e - 21);
                         uint32_t dg = MXL_BIAS;
@@ -748,9 +744,10 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
                         y = __shfl_xor_sync(0xffffffffu, w, 1);
                         w = lane & 1 ? (w & 0xF0F0F0F0u) | ((y >> 4) & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | ((y & 0x0F0F0F0Fu) << 4);
                         const int d = lane & 7;
-                        uint8_t *atom = p.hq + ((size_t)pos * FB + (size_t)kb * n + r) * 512;
+                        uint8_t *atom = p.hq + ((size_t)pos * HK + (size_t)(kb >> 1) * n + r) * 1024 + (kb & 1) * 512;
                         *(uint32_t *)(atom + d * 64 + ((cb ^ ((d >> 1) & 3)) << 4) + 4 * (lane >> 3)) = w;
-                        if (lane == 0) ((uint8_t *)(p.hs + ((size_t)un.c * FB + kb) * 16 + r))[cb] = (uint8_t)sc;
+                        if (lane == 0)
+                            ((uint8_t *)(p.hs + ((size_t)un.c * HK + (kb >> 1)) * 32 + (kb & 1) * 16 + r))[cb] = (uint8_t)sc;
                     }
                 }
             } else {
@@ -758,20 +755,16 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const FfnPara
 #pragma unroll
                 for (int c = 0; c < NR / 2; ++c) {
                     if (2 * c < n) {
-                        uint32_t v[16];
-                        tmem_ld16(tb + 16 * c, v);
+                        uint32_t v0[8], v1[8];
+                        tmem_ld8(tb + 16 * c, v0);
+                        tmem_ld8(tb + 16 * c + 8, v1);
                         tmem_ld_wait();
-                        float a[2] = {__uint_as_float(v[0]), __uint_as_float(v[8])};
-#pragma unroll
-                        for (int d = 1; d < 8; ++d) {
-                            a[0] = fmaf(__uint_as_float(v[d]), pow8[d], a[0]);
-                            a[1] = fmaf(__uint_as_float(v[8 + d]), pow8[d], a[1]);
-                        }
+                        const float a[2] = {digit_sum(v0), digit_sum(v1)};
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             if (2 * c + j < n && o < p.H) {
-                                const int r = rows[pos + 2 * c + j];
-                                p.partial[(size_t)r * p.H + o] = p.weights[r] * a[j];
+                                const int r = ch.rows[pos + 2 * c + j];
+                                p.partial[(size_t)r * p.H + o] = s_w[r] * a[j];
                             }
                     }
                 }
@@ -815,15 +808,24 @@ int launch_prep_t(const PrepParams &p, cudaStream_t s) {
 
 template <int XT>
 int launch_prep(const PrepParams &p, cudaStream_t s) {
-    if (p.T == 1) return launch_prep_t<XT, 1>(p, s);
-    if (p.T == 2) return launch_prep_t<XT, 2>(p, s);
-    if (p.T <= 4) return launch_prep_t<XT, 4>(p, s);
-    return launch_prep_t<XT, MXL_TOKENS>(p, s);
+    if (p.T <= MXL_MAX_CLUSTERS) return launch_prep_t<XT, 1>(p, s);
+    if (p.T <= 2 * MXL_MAX_CLUSTERS) return launch_prep_t<XT, 2>(p, s);
+    return launch_prep_t<XT, 4>(p, s);
 }
 
+// Shared memory of a block, less the alignment of its start.
+#define MXL_SMEM (227 * 1024 - 1024)
+
 template <int NR>
-int launch_layer_t(const FfnParams &p, cudaStream_t s) {
+int launch_layer_t(FfnParams &p, cudaStream_t s) {
     using G = LayerGeom<NR>;
+    // digits stay resident where four ring stages remain beside them
+    const int HK = ((p.H + 127) / 128 + 1) / 2, cap = std::min(p.T, NR);
+    p.stage = (MXL_WBYTES + cap * 1024 + 128 + 511) / 512 * 512;
+    p.res = p.T <= 8 ? HK * p.T * 1024 : 0;
+    if (p.res && G::CTRL + p.res + 4 * p.stage > MXL_SMEM) p.res = 0;
+    p.S = std::min<int>(G::MAXS, (MXL_SMEM - G::CTRL - p.res) / p.stage);
+    if (p.S < 2) return MOE_ERR_UNSUPPORTED;
     static std::mutex mu;
     static int sms[64] = {0};
     int dev = -1, n = 0;
@@ -833,7 +835,7 @@ int launch_layer_t(const FfnParams &p, cudaStream_t s) {
         std::lock_guard<std::mutex> lock(mu);
         if (!sms[dev]) {
             MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_layer_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              (int)G::SMEM));
+                                              MXL_SMEM + 1024));
             MOE_TRY_CUDA(cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev));
         }
         n = sms[dev];
@@ -842,7 +844,8 @@ int launch_layer_t(const FfnParams &p, cudaStream_t s) {
     const long units = chunks * ((p.F + 63) / 64 + (p.H + 127) / 128);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<long>(units, n)), dim3(MXL_THREADS), G::SMEM, s);
+    moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<long>(units, n)), dim3(MXL_THREADS),
+                   1024 + G::CTRL + p.res + (size_t)p.S * p.stage, s);
     MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_layer_kernel<NR>, p));
     return MOE_OK;
 }

@@ -138,6 +138,11 @@ __device__ __forceinline__ uint64_t umma_desc_sw64(uint32_t smem_addr) {
     return d;
 }
 
+// The same with 1024 bytes from one 8-row atom to the next.
+__device__ __forceinline__ uint64_t umma_desc_sw64_rows1024(uint32_t smem_addr) {
+    return umma_desc_sw64(smem_addr) + ((uint64_t)(512 >> 4) << 32);
+}
+
 // Instruction descriptor of kind::mxf4: E2M1 A and B with E8M0 scales (two per 64 columns), both
 // K-major, fp32 accumulator.  sf_id (0 or 2): which half of each 32-bit scale word this K = 64 step
 // takes, for A and B alike.
