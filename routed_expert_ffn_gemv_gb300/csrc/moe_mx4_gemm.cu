@@ -349,19 +349,20 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     }
     const int *rows = LOCAL ? loc.rows : p.rows;
     const int MT = p.MT, n_items = (LOCAL ? loc.nch : p.ints[0]) * MT;
-    const int KB = (p.K + 127) / 128, NKS = (KB + 1) / 2, KS = p.K / 32;
+    const int K = p.K, KB = (K + 127) / 128, NKS = (KB + 1) / 2, KS = K / 32;
 
     if (warp < 2) {
         // ---------------- producers.  LOCAL: warp 0 the stage's expected bytes, its weights and the even
-        // groups of four code rows, warp 1 the odd groups.  Otherwise their first lanes: warp 0
-        // the weights, warp 1 the chunk's rows and scales, runs of bytes.
-        int g = 0;
+        // groups of four code rows, warp 1 the odd groups.  Otherwise warp 0 the weights, warp 1
+        // the chunk's rows and scales, runs of bytes.
+        int g = 0, st_i = 0;
+        uint32_t ph = 1;
         bool ok = true;
-        for (int j = blockIdx.x; j < n_items && ok && (LOCAL || lane == 0); j += gridDim.x) {
+        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
             const int c = j / MT, m = j % MT;
-            const int slot = c_slots[c];
+            const int slot = __shfl_sync(0xffffffffu, c_slots[c], 0);
             if (slot < 0) continue;
-            const int pos0 = c_poss[c], n = c_ns[c];
+            const int pos0 = __shfl_sync(0xffffffffu, c_poss[c], 0), n = __shfl_sync(0xffffffffu, c_ns[c], 0);
             const int npad = (n + 7) & ~7, q = 2 * lane + warp;  // this lane's group of four rows
             int r4[4];
             if (LOCAL)
@@ -370,34 +371,32 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                     r4[i] = rows[pos0 + (at < n ? at : 0)] / p.div;  // rows past the chunk: unused columns
                 }
             const uint8_t *w = p.pool + (size_t)slot * p.slot_bytes + p.mat + (size_t)m * KB * MX4_TB;
+            const uint8_t *xrow = p.xg + (size_t)pos0 * 128, *srow = p.sg + (size_t)pos0 * 8;
             for (int kc = 0; kc < NKS; ++kc, ++g) {
-                const int s = g % G::S;
-                if (g >= G::S) {
-                    ok = mbar_wait_role(&s_empty[s], ((g / G::S) & 1) ^ 1, p.status, abort_flag);
-                    if (LOCAL) ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                if (g >= G::S && !(ok = mbar_wait_warp(&s_empty[st_i], ph, p.status, abort_flag))) break;
+                uint8_t *st = ring + (size_t)st_i * G::STAGE;
+                uint64_t *full = &s_full[st_i];
+                if (warp == 0) {
+                    const uint32_t wb = 2 * kc + 1 < KB ? MXG_WBYTES : MX4_TB;
+                    mbar_arrive_expect_tx_elect(full, LOCAL ? wb + (uint32_t)npad * 128u : wb);
+                    bulk_g2s_elect(st, w, wb, full);
+                    w += MXG_WBYTES;
+                } else if (!LOCAL) {
+                    // (an arrival of its own: a copy takes its thread about 100 clocks)
+                    const uint32_t sb = (uint32_t)((n + 1) & ~1) * 8u;
+                    mbar_arrive_expect_tx_elect(full, (uint32_t)n * 128u + sb);
+                    bulk_g2s_elect(st + MXG_WBYTES, xrow, (uint32_t)n * 128u, full);
+                    bulk_g2s_elect(st + G::SOFF, srow, sb, full);
+                    xrow += p.Rp * 128;
+                    srow += p.Rp * 8;
                 }
-                uint8_t *st = ring + (size_t)s * G::STAGE;
-                const uint32_t wb = 2 * kc + 1 < KB ? MXG_WBYTES : MX4_TB;
                 if (LOCAL) {
-                    if (threadIdx.x == 0) {
-                        mbar_arrive_expect_tx(&s_full[s], wb + (uint32_t)npad * 128u);
-                        bulk_g2s(st, w + (size_t)kc * MXG_WBYTES, wb, &s_full[s]);
-                    }
-                    if (4 * q < npad) tma_gather4(st + MXG_WBYTES + q * 512, &p.map, kc * 128, r4, &s_full[s]);
+                    if (4 * q < npad) tma_gather4(st + MXG_WBYTES + q * 512, &p.map, kc * 128, r4, full);
                     __syncwarp();
-                } else {
-                    // two threads, an arrival each: a copy takes its thread about 100 clocks
-                    if (warp == 0) {
-                        mbar_arrive_expect_tx(&s_full[s], wb);
-                        bulk_g2s(st, w + (size_t)kc * MXG_WBYTES, wb, &s_full[s]);
-                    } else {
-                        const uint32_t sb = (uint32_t)((n + 1) & ~1) * 8u;
-                        mbar_arrive_expect_tx(&s_full[s], (uint32_t)n * 128u + sb);
-                        bulk_g2s(st + MXG_WBYTES, p.xg + ((size_t)kc * p.Rp + pos0) * 128, (uint32_t)n * 128u,
-                                 &s_full[s]);
-                        bulk_g2s(st + G::SOFF, p.sg + ((size_t)kc * p.Rp + pos0) * 8, sb, &s_full[s]);
-                    }
+                }
+                if (++st_i == G::S) {
+                    st_i = 0;
+                    ph ^= 1u;
                 }
             }
         }
@@ -409,40 +408,42 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
             }
         if (!ok) settle_after_abort();
     } else if (warp == 2) {
-        // ---------------- MMA issuer
-        if (lane == 0) {
-            int g = 0, jl = 0;
-            bool ok = true;
-            for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
-                const int c = j / MT;
-                if (c_slots[c] < 0) continue;
-                const int npad = (c_ns[c] + 7) & ~7;
-                const uint32_t id0 = umma_idesc_mxf4(128, npad, 0), id2 = umma_idesc_mxf4(128, npad, 2);
-                const int buf = jl & 1;
-                if (jl >= 2 && !(ok = mbar_wait_role(&acc_empty[buf], ((jl / 2) - 1) & 1, p.status, abort_flag))) break;
+        // ---------------- MMA issuer: the whole warp, one elected thread inside each instruction
+        int jl = 0, st_i = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
+            const int c = __shfl_sync(0xffffffffu, j / MT, 0);
+            if (c_slots[c] < 0) continue;
+            const int npad = __shfl_sync(0xffffffffu, (c_ns[c] + 7) & ~7, 0);
+            const uint32_t id0 = umma_idesc_mxf4(128, npad, 0), id2 = umma_idesc_mxf4(128, npad, 2);
+            const int buf = jl & 1;
+            if (jl >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((jl / 2) - 1) & 1, p.status, abort_flag))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + buf * NT;
+            for (int kc = 0; kc < NKS; ++kc) {
+                // (the scale warps saw the stage land before they arrived)
+                if (!(ok = mbar_wait_warp(&sf_full[st_i], ph, p.status, abort_flag))) break;
                 tc_fence_after();
-                const uint32_t d = tmem + buf * NT;
-                for (int kc = 0; kc < NKS; ++kc, ++g) {
-                    const int s = g % G::S;
-                    if (!(ok = mbar_wait_role(&sf_full[s], (g / G::S) & 1, p.status, abort_flag))) break;
-                    // (the scale warps saw the stage land before they arrived)
-                    tc_fence_after();
-                    uint8_t *st = ring + (size_t)s * G::STAGE;
-                    const uint64_t a = umma_desc_sw64(smem_u32(st)), b = umma_desc_sw128(smem_u32(st + MXG_WBYTES));
-                    const uint32_t sf = tmem + G::SFCOL + 24 * s;
-                    const int steps = min(4, (p.K - 256 * kc + 63) / 64);
-                    umma_mxf4(d, a, b, id0, sf, sf + 8, kc > 0);
-                    if (steps > 1) umma_mxf4(d, a + 2, b + 2, id2, sf, sf + 8, 1);
-                    if (steps > 2) umma_mxf4(d, a + (MX4_TB >> 4), b + 4, id0, sf + 4, sf + 16, 1);
-                    if (steps > 3) umma_mxf4(d, a + (MX4_TB >> 4) + 2, b + 6, id2, sf + 4, sf + 16, 1);
-                    umma_commit(&s_empty[s]);
+                const uint32_t st = smem_u32(ring) + (uint32_t)st_i * G::STAGE;
+                const uint64_t a = umma_desc_sw64(st), b = umma_desc_sw128(st + MXG_WBYTES);
+                const uint32_t sf = tmem + G::SFCOL + 24 * st_i;
+                const int steps = (K - 256 * kc + 63) / 64;
+                umma_mxf4(d, a, b, id0, sf, sf + 8, kc > 0);
+                if (steps > 1) umma_mxf4(d, a + 2, b + 2, id2, sf, sf + 8, 1);
+                if (steps > 2) umma_mxf4(d, a + (MX4_TB >> 4), b + 4, id0, sf + 4, sf + 16, 1);
+                if (steps > 3) umma_mxf4(d, a + (MX4_TB >> 4) + 2, b + 6, id2, sf + 4, sf + 16, 1);
+                umma_commit_elect(&s_empty[st_i]);
+                if (++st_i == G::S) {
+                    st_i = 0;
+                    ph ^= 1u;
                 }
-                if (ok) umma_commit(&acc_full[buf]);
-                ++jl;
             }
-            umma_commit(mma_done);  // every MMA has completed before tensor memory is released
-            mbar_wait_bounded(mma_done, 0, p.status);
+            if (ok) umma_commit_elect(&acc_full[buf]);
+            ++jl;
         }
+        umma_commit_elect(mma_done);  // every MMA has completed before tensor memory is released
+        mbar_wait_bounded(mma_done, 0, p.status);
     } else if (warp >= 4 && warp < 8) {
         // ---------------- scales
         const uint32_t t0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::SFCOL;

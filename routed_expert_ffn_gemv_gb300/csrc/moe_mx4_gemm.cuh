@@ -32,7 +32,7 @@ struct Mx4Chunks {
 
 // Called by every thread of a block of at least MX4_LOCAL_R; syncs the block.  Routes of -1 are not
 // served; ids outside [0, E) and slots outside [0, n_slots) are recorded and not served either.
-// Chunks of at most NR routes.
+// Chunks of at most NR routes.  `table`: global or shared memory, or NULL.
 __device__ __forceinline__ void mx4_local_chunks(Mx4Chunks &c, const int32_t *ids, int R, int E, const int32_t *table,
                                                  int n_slots, int NR, int *status) {
     const int r = threadIdx.x, lane = r & 31, warp = r >> 5;
@@ -56,6 +56,7 @@ __device__ __forceinline__ void mx4_local_chunks(Mx4Chunks &c, const int32_t *id
     int cnt = 0, rank = 0, first = MX4_LOCAL_R, pk = 0, incl = 0;
     if (r < MX4_LOCAL_R) {
         if (id >= 0)
+#pragma unroll 4
             for (int q = 0; q < R; q += 4) {
                 const int4 v = *(const int4 *)&c.id[q];
                 const int w[4] = {v.x, v.y, v.z, v.w};

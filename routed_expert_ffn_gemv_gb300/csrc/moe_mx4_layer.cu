@@ -51,7 +51,7 @@ static_assert(MXL_MAX_R <= MX4_LOCAL_R, "a CTA groups the routes itself");
 namespace {
 
 struct LayerWs {
-    size_t ctr, ids, weights, xscale, xq, hq, hs, partial, total;
+    size_t ctr, ids, weights, xscale, xq, hq, partial, total;
     size_t ctr_ints;
 };
 
@@ -70,8 +70,7 @@ LayerWs layer_ws(int T, int H, int F, int k) {
     L.weights = take(R * 4);
     L.xscale = take((size_t)T * 8);
     L.xq = take((HB + 1) / 2 * T * 1024);
-    L.hq = take(R * ((FB + 1) / 2) * 1024);
-    L.hs = take(R * ((FB + 1) / 2) * 128);
+    L.hq = take(R * ((FB + 1) / 2) * (1024 + 128));  // (at most a chunk per route)
     L.partial = take(R * H * 4);
     L.total = o;
     return L;
@@ -130,7 +129,6 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p
     const bool has = 8 * cg < p.E;
     const uint16_t *wr = p.w_router + (size_t)h0 * p.E + 8 * cg;
     uint4 pre[PRE];
-    pdl_trigger();
     if (p.wide_w && has)  // the router's weights do not come from the kernel before
 #pragma unroll
         for (int i = 0; i < PRE; ++i) {
@@ -138,6 +136,11 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p
             pre[i] = h < HS ? *(const uint4 *)(wr + (size_t)h * p.E) : make_uint4(0, 0, 0, 0);
         }
     pdl_wait();
+    pdl_trigger();  // not before: the next kernel reads its slot table before its own wait
+    float bias[MOE_MAX_E / 32];
+    if (warp == 0)
+#pragma unroll
+        for (int i = 0; i < MOE_MAX_E / 32; ++i) bias[i] = p.bias && lane + 32 * i < p.E ? p.bias[lane + 32 * i] : 0.f;
     if (blockIdx.y == 0)
         for (int i = rank * MXL_PREP_THREADS + tid; i < p.n_ctr; i += MXL_CLUSTER * MXL_PREP_THREADS) p.ctr[i] = 0;
     // this CTA's eighth of the tokens, and their largest magnitudes (as bits: NaN sorts above all)
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p
                     float s = 0.f;
 #pragma unroll
                     for (int r = 0; r < MXL_CLUSTER; ++r) s += ld_cluster_f32(cluster_map(&part[rank * E8 + e], r));
-                    if (p.bias) s += p.bias[e];
+                    s += bias[i];
                     v[i] = (s != s) ? -INFINITY : s;  // NaN never wins
                 }
             }
@@ -291,7 +294,6 @@ struct FfnParams {
     const float2 *xscale;
     const uint8_t *xq;
     uint8_t *hq;
-    uint32_t *hs;
     float *partial, *y;
     int *ticket, *ready, *done;
     int *status;
@@ -300,15 +302,15 @@ struct FfnParams {
 };
 
 // Shared memory: control, the tokens' digits (resident: T <= NR = 8, and enough of the ring left),
-// then S stages of two weight blocks, `cap` routes' digits (1024 bytes each: two 512-byte atoms of 8
-// rows x 128 columns) and 128 bytes of h scales.
+// then S stages of two weight blocks and `cap` routes' digits (1024 bytes each: two 512-byte atoms of 8
+// rows x 128 columns), for down followed by 128 bytes of h scales ([2 blocks][16 routes] words).
 template <int NR>
 struct LayerGeom {
     static constexpr int N = NR * 8;
     static constexpr int SFCOL = 2 * N;      // scales after the two accumulators, 16 columns a stage
     static constexpr int MAXS = 10;
-    static constexpr int CTRL = (1024 + 2 * 4 * NR / 2 * 32 * 4 + (int)sizeof(Mx4Chunks) + MXL_MAX_R * 4 +
-                                 MOE_DECODE_MAX_T * 8 + 1023) / 1024 * 1024;
+    static constexpr int CTRL = (1024 + 2 * 4 * NR * 32 * 4 + (int)sizeof(Mx4Chunks) + MXL_MAX_R * 4 +
+                                 MOE_DECODE_MAX_T * 8 + MOE_MAX_E * 4 + 1023) / 1024 * 1024;
     static_assert(SFCOL + MAXS * 16 <= 512, "tensor memory");
 };
 
@@ -322,8 +324,13 @@ __device__ __forceinline__ void red_release_gpu(int *a) {
 }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
+// Digits of h of stage kc of a chunk of n routes (n * 1024 bytes, then its scales).
+__device__ __forceinline__ size_t hq_offset(int chunk, int pos, int n, int stages, int kc) {
+    return (size_t)stages * (pos * 1024 + chunk * 128) + (size_t)kc * (n * 1024 + 128);
+}
+
 // A unit: gate/up or down tile m of a chunk, or (last) tile m of y for tokens 8 c .. 8 c + 7.
-enum { MXL_UP = 0, MXL_DOWN = 1, MXL_COMBINE = 2 };
+enum { MXL_UP = 0, MXL_DOWN = 1, MXL_COMBINE = 2, MXL_NONE = 3, MXL_ABORT = 4 };
 struct Unit {
     int kind, c, m;
 };
@@ -335,6 +342,12 @@ __device__ __forceinline__ Unit unit_of(int u, int nch, int FT, int HT) {
     r.c = v / per;
     r.m = v - r.c * per;
     return r;
+}
+
+// A unit in one word (chunks: 8 bits, tiles: 20), as it travels to the CTA's roles; -1: none left.
+__device__ __forceinline__ int unit_pack(const Unit &u) { return u.kind << 28 | u.c << 20 | u.m; }
+__device__ __forceinline__ Unit unit_unpack(int v) {
+    return v < 0 ? Unit{MXL_NONE, 0, 0} : Unit{v >> 28, (v >> 20) & 0xFF, v & 0xFFFFF};
 }
 
 // y[t][columns of tile m] = extra + the partial rows of token t's routes, in route order (`id` -1: not
@@ -401,14 +414,14 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *q_unit = (volatile int *)(tmem_slot + 2);  // [MXL_Q]
     static_assert((3 * G::MAXS + 4 + 2 * MXL_Q + MXL_PUB + 2) * 8 + (2 + MXL_Q) * 4 <= 1024, "barriers");
-    float *xch = (float *)(smem + 1024);                     // [2 buffers][2 pairs][2 ways][NR / 2][32]
-    Mx4Chunks &ch = *(Mx4Chunks *)(xch + 2 * 4 * (NR / 2) * 32);
+    float *xch = (float *)(smem + 1024);                     // [2 buffers][2 pairs][gate, up][NR][32]
+    Mx4Chunks &ch = *(Mx4Chunks *)(xch + 2 * 4 * NR * 32);
     float *s_w = (float *)(&ch + 1);                         // [MXL_MAX_R] router weights
     float2 *s_xs = (float2 *)(s_w + MXL_MAX_R);              // [MOE_DECODE_MAX_T]
+    int *s_table = (int *)(s_xs + MOE_DECODE_MAX_T);         // [MOE_MAX_E]
     uint8_t *xres = smem + G::CTRL;
     uint8_t *ring = xres + p.res;
     const int S = p.S, STAGE = p.stage;
-    const int hs_off = STAGE - 128;                          // h scales at a stage's end
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
@@ -435,8 +448,11 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    // (the first kernel lets this one start after everything before it is complete)
+    if (p.table && tid < p.E) s_table[tid] = p.table[tid];
     pdl_wait();
     pdl_trigger();
+    __syncthreads();
     // the first unit is claimed, and the resident digits are fetched, while the chunks are put together
     int claim = 0;
     if (tid == 0) {
@@ -450,7 +466,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
     if (tid < R) s_w[tid] = p.weights[tid];
     if (tid < p.T) s_xs[tid] = p.xscale[tid];
     tc_fence_before();
-    mx4_local_chunks(ch, p.ids, R, p.E, p.table, p.n_slots, NR, p.status);
+    mx4_local_chunks(ch, p.ids, R, p.E, p.table ? s_table : nullptr, p.n_slots, NR, p.status);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int nch = ch.nch;
@@ -458,16 +474,13 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
     const int n_units = nch * (FT + HT) + HT * ((p.T + 7) / 8);
     const size_t down_off = mx4_gu_bytes(p.H, p.F);
 
-    // a consumer's next unit (-1: none left; -2: abort)
-    auto next_unit = [&](int i) -> int {
+    // a consumer's next unit
+    auto next_unit = [&](int i) -> Unit {
         const int q = i % MXL_Q;
-        bool ok = mbar_wait_role(&q_full[q], (i / MXL_Q) & 1, p.status, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return -2;
-        const int u = q_unit[q];
-        __syncwarp();
+        if (!mbar_wait_warp(&q_full[q], (i / MXL_Q) & 1, p.status, abort_flag)) return Unit{MXL_ABORT, 0, 0};
+        const int v = __shfl_sync(0xffffffffu, q_unit[q], 0);
         if (lane == 0) mbar_arrive1(&q_empty[q]);
-        return u;
+        return unit_unpack(v);
     };
     // ring position: stage index and the parity of its current fill
     int s = 0;
@@ -487,28 +500,30 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                 for (int t = 0; t < p.T; t += 8) combine_tile(p, m, t, tid, ch.id);
     } else if (warp == 0) {
         // ---------------- claims and weights; a stage's barrier expects its digits' bytes too
-        if (lane == 0) {
+        {
             bool ok = true;
             int fills = 0;
             for (int i = 0; ok; ++i) {
-                const int q = i % MXL_Q, u = claim < n_units ? claim : -1;
-                if (i >= MXL_Q && !(ok = mbar_wait_role(&q_empty[q], ((i / MXL_Q) & 1) ^ 1, p.status, abort_flag))) break;
-                q_unit[q] = u;
-                mbar_arrive1(&q_full[q]);
-                if (u < 0) break;
-                claim = atomicAdd(p.ticket, 1);
+                const int q = i % MXL_Q, u = __shfl_sync(0xffffffffu, claim, 0);
+                if (i >= MXL_Q && !(ok = mbar_wait_warp(&q_empty[q], ((i / MXL_Q) & 1) ^ 1, p.status, abort_flag))) break;
                 const Unit un = unit_of(u, nch, FT, HT);
+                if (lane == 0) {
+                    q_unit[q] = u < n_units ? unit_pack(un) : -1;
+                    mbar_arrive1(&q_full[q]);
+                    if (u < n_units) claim = atomicAdd(p.ticket, 1);
+                }
+                if (u >= n_units) break;
                 if (un.kind == MXL_COMBINE) continue;
                 const bool down = un.kind == MXL_DOWN;
-                const int KB = down ? FB : HB, NKS = (KB + 1) / 2;
-                const uint32_t nb = down ? (uint32_t)ch.n[un.c] * 1024u + 128u : p.res ? 0u : (uint32_t)ch.n[un.c] * 1024u;
-                const uint8_t *w = p.pool + (size_t)ch.slot[un.c] * p.slot_bytes + (down ? down_off : 0) +
-                                   (size_t)un.m * KB * MX4_TB;
-                for (int kc = 0; kc < NKS; ++kc, advance(), ++fills) {
-                    if (fills >= S && !(ok = mbar_wait_role(&s_empty[s], ph ^ 1u, p.status, abort_flag))) break;
+                const int KB = down ? FB : HB, NKS = (KB + 1) / 2, n = __shfl_sync(0xffffffffu, ch.n[un.c], 0);
+                const uint32_t nb = down ? (uint32_t)n * 1024u + 128u : p.res ? 0u : (uint32_t)n * 1024u;
+                const uint8_t *w = p.pool + (size_t)__shfl_sync(0xffffffffu, ch.slot[un.c], 0) * p.slot_bytes +
+                                   (down ? down_off : 0) + (size_t)un.m * KB * MX4_TB;
+                for (int kc = 0; kc < NKS; ++kc, advance(), ++fills, w += MXL_WBYTES) {
+                    if (fills >= S && !(ok = mbar_wait_warp(&s_empty[s], ph ^ 1u, p.status, abort_flag))) break;
                     const uint32_t wb = 2 * kc + 1 < KB ? MXL_WBYTES : MX4_TB;
-                    mbar_arrive_expect_tx(&s_full[s], wb + nb);
-                    bulk_g2s(ring + (size_t)s * STAGE, w + (size_t)kc * MXL_WBYTES, wb, &s_full[s]);
+                    mbar_arrive_expect_tx_elect(&s_full[s], wb + nb);
+                    bulk_g2s_elect(ring + (size_t)s * STAGE, w, wb, &s_full[s]);
                 }
             }
             // never leave with copies in flight: the last fill of every stage
@@ -528,20 +543,22 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
         int fills = 0;
         uint32_t ready = 0;  // bit b: chunk 32 b + lane has all its rows of h
         for (int i = 0; ok; ++i) {
-            const int u = next_unit(i);
-            if (u < 0) {
-                ok = u != -2;
+            const Unit un = next_unit(i);
+            if (un.kind >= MXL_COMBINE) {
+                if (un.kind == MXL_COMBINE) continue;
+                ok = un.kind != MXL_ABORT;
                 break;
             }
-            const Unit un = unit_of(u, nch, FT, HT);
-            if (un.kind == MXL_COMBINE) continue;
             const bool down = un.kind == MXL_DOWN;
-            const int NKS = ((down ? FB : HB) + 1) / 2, n = ch.n[un.c], pos = ch.pos[un.c];
+            const int NKS = ((down ? FB : HB) + 1) / 2;
+            const int n = __shfl_sync(0xffffffffu, ch.n[un.c], 0), pos = __shfl_sync(0xffffffffu, ch.pos[un.c], 0);
             if (down) {
                 // every gate/up unit of the chunk is done, its digits and scales written.  One look covers 32
                 // chunks, so a chunk seen ready costs no more looks.
                 const int b = un.c >> 5, mine = 32 * b + lane;
+                bool looked = false;
                 for (uint32_t it = 0; !(__shfl_sync(0xffffffffu, ready, un.c & 31) >> b & 1u); ++it) {
+                    looked = true;
                     if (mine < nch && ld_acquire_gpu(&p.ready[mine]) >= FT) ready |= 1u << b;
                     if (it >= MOE_SPIN_LIMIT && lane == 0) {
                         moe_set_status(p.status, MOE_ERR_TIMEOUT);
@@ -550,20 +567,16 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                     if (!(ok = __all_sync(0xffffffffu, !*abort_flag))) break;
                 }
                 if (!ok) break;
-                __syncwarp();
-                fence_proxy_async_all();
+                // the rows were written as ordinary stores; from here on they are read by bulk copies
+                if (looked) fence_proxy_async_all();
             }
             const int tok = !down && lane < n ? ch.rows[pos + lane] / p.k : 0;
             for (int kc = 0; kc < NKS; ++kc, advance(), ++fills) {
-                if (fills >= S) ok = mbar_wait_role(&s_empty[s], ph ^ 1u, p.status, abort_flag);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (fills >= S && !(ok = mbar_wait_warp(&s_empty[s], ph ^ 1u, p.status, abort_flag))) break;
                 uint8_t *st = ring + (size_t)s * STAGE;
                 if (down) {
-                    if (lane == 0) {
-                        bulk_g2s(st + MXL_WBYTES, p.hq + ((size_t)pos * ((FB + 1) / 2) + (size_t)kc * n) * 1024,
-                                 (uint32_t)n * 1024u, &s_full[s]);
-                        bulk_g2s(st + hs_off, p.hs + ((size_t)un.c * ((FB + 1) / 2) + kc) * 32, 128, &s_full[s]);
-                    }
+                    bulk_g2s_elect(st + MXL_WBYTES, p.hq + hq_offset(un.c, pos, n, NKS, kc),
+                                   (uint32_t)n * 1024u + 128u, &s_full[s]);
                 } else if (!p.res && lane < n) {
                     bulk_g2s(st + MXL_WBYTES + lane * 1024, p.xq + ((size_t)kc * p.T + tok) * 1024, 1024, &s_full[s]);
                 }
@@ -576,57 +589,50 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
         // free, and the chunk's tokens need not be adjacent)
         bool ok = true, xok = !p.res;
         for (int i = 0; ok; ++i) {
-            const int u = next_unit(i);
-            if (u < 0) break;
-            const Unit un = unit_of(u, nch, FT, HT);
-            if (un.kind == MXL_COMBINE) continue;  // these come last: units before them keep their numbering
-            if (lane == 0) {
-                const bool down = un.kind == MXL_DOWN, all = !down && p.res;
-                if (all && !xok) ok = xok = mbar_wait_role(x_full, 0, p.status, abort_flag);
-                const int K = down ? p.F : p.H, NKS = (K + 255) / 256, N = 8 * (all ? p.T : ch.n[un.c]);
-                const uint32_t id0 = umma_idesc_mxf4(128, N, 0), id2 = umma_idesc_mxf4(128, N, 2);
-                const int buf = i & 1;
-                if (ok && i >= 2) ok = mbar_wait_role(&acc_empty[buf], ((i / 2) - 1) & 1, p.status, abort_flag);
-                tc_fence_after();
-                const uint32_t d = tmem + buf * G::N;
-                for (int kc = 0; kc < NKS && ok; ++kc, advance()) {
-                    // (the scale warps saw the stage land before they arrived)
-                    if (!(ok = mbar_wait_role(&sf_full[s], ph, p.status, abort_flag))) break;
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(ring + (size_t)s * STAGE);
-                    const uint64_t a = umma_desc_sw64(st);
-                    const uint64_t b = umma_desc_sw64_rows1024(all ? smem_u32(xres) + kc * p.T * 1024 : st + MXL_WBYTES);
-                    const uint32_t sf = tmem + G::SFCOL + 16 * s;
-                    const int steps = min(4, (K - 256 * kc + 63) / 64);
-                    constexpr int A1 = MX4_TB >> 4, B1 = 512 >> 4;
-                    umma_mxf4(d, a, b, id0, sf, sf + 8, kc > 0);
-                    if (steps > 1) umma_mxf4(d, a + 2, b + 2, id2, sf, sf + 8, 1);
-                    if (steps > 2) umma_mxf4(d, a + A1, b + B1, id0, sf + 4, sf + 12, 1);
-                    if (steps > 3) umma_mxf4(d, a + A1 + 2, b + B1 + 2, id2, sf + 4, sf + 12, 1);
-                    umma_commit(&s_empty[s]);
-                }
-                if (ok) umma_commit(&acc_full[buf]);
+            const Unit un = next_unit(i);
+            if (un.kind >= MXL_COMBINE) {  // combines come last: units before them keep their numbering
+                if (un.kind == MXL_COMBINE) continue;
+                break;
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);  // the warp waits for its issuing thread
+            const bool down = un.kind == MXL_DOWN, all = !down && p.res;
+            if (all && !xok) ok = xok = mbar_wait_warp(x_full, 0, p.status, abort_flag);
+            const int K = down ? p.F : p.H, NKS = (K + 255) / 256;
+            const int N = 8 * (all ? p.T : __shfl_sync(0xffffffffu, ch.n[un.c], 0));
+            const uint32_t id0 = umma_idesc_mxf4(128, N, 0), id2 = umma_idesc_mxf4(128, N, 2);
+            const int buf = i & 1;
+            if (ok && i >= 2) ok = mbar_wait_warp(&acc_empty[buf], ((i / 2) - 1) & 1, p.status, abort_flag);
+            tc_fence_after();
+            const uint32_t d = tmem + buf * G::N;
+            for (int kc = 0; kc < NKS && ok; ++kc, advance()) {
+                // (the scale warps saw the stage land before they arrived)
+                if (!(ok = mbar_wait_warp(&sf_full[s], ph, p.status, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(ring) + (uint32_t)(s * STAGE);
+                const uint64_t a = umma_desc_sw64(st);
+                const uint64_t b = umma_desc_sw64_rows1024(all ? smem_u32(xres) + kc * p.T * 1024 : st + MXL_WBYTES);
+                const uint32_t sf = tmem + G::SFCOL + 16 * s;
+                const int steps = (K - 256 * kc + 63) / 64;
+                constexpr int A1 = MX4_TB >> 4, B1 = 512 >> 4;
+                umma_mxf4(d, a, b, id0, sf, sf + 8, kc > 0);
+                if (steps > 1) umma_mxf4(d, a + 2, b + 2, id2, sf, sf + 8, 1);
+                if (steps > 2) umma_mxf4(d, a + A1, b + B1, id0, sf + 4, sf + 12, 1);
+                if (steps > 3) umma_mxf4(d, a + A1 + 2, b + B1 + 2, id2, sf + 4, sf + 12, 1);
+                umma_commit_elect(&s_empty[s]);
+            }
+            if (ok) umma_commit_elect(&acc_full[buf]);
         }
-        __syncwarp();
-        if (lane == 0) {
-            umma_commit(mma_done);
-            mbar_wait_bounded(mma_done, 0, p.status);
-        }
+        umma_commit_elect(mma_done);
+        mbar_wait_bounded(mma_done, 0, p.status);
     } else if (warp == 3) {
         // ---------------- publishes finished units: rows of h for the chunk's down units, partial rows
         // for the tile's combine
         bool ok = true;
         for (int i = 0; ok; ++i) {
-            const int u = next_unit(i);
-            if (u < 0) break;
-            const Unit un = unit_of(u, nch, FT, HT);
+            const Unit un = next_unit(i);
             if (un.kind == MXL_COMBINE) continue;
-            ok = mbar_wait_role(&pub[i % MXL_PUB], (i / MXL_PUB) & 1, p.status, abort_flag);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (un.kind > MXL_COMBINE) break;
+            if (!(ok = mbar_wait_warp(&pub[i % MXL_PUB], (i / MXL_PUB) & 1, p.status, abort_flag))) break;
             if (lane == 0) {
-                if (un.kind == MXL_UP) fence_proxy_async_all();
                 red_release_gpu(un.kind == MXL_UP ? &p.ready[un.c] : &p.done[un.m]);
             }
             __syncwarp();
@@ -637,15 +643,13 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
         const uint32_t t0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::SFCOL;
         bool ok = true;
         for (int i = 0; ok; ++i) {
-            const int u = next_unit(i);
-            if (u < 0) break;
-            const Unit un = unit_of(u, nch, FT, HT);
+            const Unit un = next_unit(i);
             if (un.kind == MXL_COMBINE) continue;
+            if (un.kind > MXL_COMBINE) break;
             const bool down = un.kind == MXL_DOWN;
-            const int KB = down ? FB : HB, NKS = (KB + 1) / 2;
+            const int KB = down ? FB : HB, NKS = (KB + 1) / 2, hs_off = MXL_WBYTES + ch.n[un.c] * 1024;
             for (int kc = 0; kc < NKS; ++kc, advance()) {
-                ok = mbar_wait_role(&s_full[s], ph, p.status, abort_flag);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (!(ok = mbar_wait_warp(&s_full[s], ph, p.status, abort_flag))) break;
                 tc_fence_after();
                 const uint8_t *st = ring + (size_t)s * STAGE;
                 const bool two = 2 * kc + 1 < KB;
@@ -680,15 +684,11 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
             return a;
         };
         for (int i = 0;; ++i) {
-            const int u = next_unit(i);
-            bool ok = u != -2;
-            Unit un = {MXL_COMBINE, 0, 0};
-            if (u >= 0) {
-                un = unit_of(u, nch, FT, HT);
-                ok = un.kind == MXL_COMBINE ? wait_count(&p.done[un.m], nch, p.status, abort_flag)
-                                            : mbar_wait_role(&acc_full[i & 1], (i / 2) & 1, p.status, abort_flag);
-            }
-            if (!bar_and_n(1, 128, ok) || u < 0) break;
+            const Unit un = next_unit(i);
+            bool ok = un.kind != MXL_ABORT;
+            if (un.kind == MXL_COMBINE) ok = wait_count(&p.done[un.m], nch, p.status, abort_flag);
+            else if (un.kind < MXL_COMBINE) ok = mbar_wait_role(&acc_full[i & 1], (i / 2) & 1, p.status, abort_flag);
+            if (!bar_and_n(1, 128, ok) || un.kind == MXL_NONE) break;
             if (un.kind == MXL_COMBINE) {
                 combine_tile(p, un.m, 8 * un.c, ew, ch.id);
                 continue;
@@ -697,76 +697,58 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
             const int buf = i & 1, n = ch.n[un.c], pos = ch.pos[un.c];
             const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * G::N;
             if (un.kind == MXL_UP) {
-                // route i's gate (lane quarters 0, 1) and up (2, 3) values; the gate warps finish the even
-                // routes, the up warps the odd ones
-                float mine[NR / 2];
-                float *xb = xch + (size_t)((buf * 2 + (q & 1)) * 2) * (NR / 2) * 32 + lane;
-                float *out = xb + (q < 2 ? 1 : 0) * (NR / 2) * 32, *in = xb + (q < 2 ? 0 : 1) * (NR / 2) * 32;
-#pragma unroll
-                for (int c = 0; c < NR / 2; ++c) {
-                    if (2 * c < n) {
-                        const int r1 = min(2 * c + 1, n - 1);
-                        uint32_t v0[8], v1[8];
-                        tmem_ld8(tb + 8 * (p.res ? ch.rows[pos + 2 * c] / p.k : 2 * c), v0);
-                        tmem_ld8(tb + 8 * (p.res ? ch.rows[pos + r1] / p.k : r1), v1);
-                        tmem_ld_wait();
-                        const float a = digit_sum(v0), b = digit_sum(v1);
-                        mine[c] = q < 2 ? a : b;
-                        out[32 * c] = q < 2 ? b : a;
-                    }
+                // route r's gate (lane quarters 0, 1) and up (2, 3) values meet in shared memory; the gate warps
+                // finish the even routes, the up warps the odd ones.  (Loops, not unrolled code: the first
+                // unit of a CTA runs at the speed of instruction fetches from memory.)
+                float *xg = xch + (size_t)(buf * 2 + (q & 1)) * 2 * NR * 32 + lane, *xu = xg + NR * 32;
+                float *own = q < 2 ? xg : xu;
+#pragma unroll 1
+                for (int r = 0; r < n; ++r) {
+                    uint32_t v[8];
+                    tmem_ld8(tb + 8 * (p.res ? ch.rows[pos + r] / p.k : r), v);
+                    tmem_ld_wait();
+                    own[32 * r] = digit_sum(v);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive1(&acc_empty[buf]);
                 bar_sync_n(2 + (q & 1), 64);
-                const int f0 = 64 * un.m + 32 * (q & 1), kb = f0 >> 7, cb = (f0 >> 5) & 3, HK = (FB + 1) / 2;
+                const int f0 = 64 * un.m + 32 * (q & 1), kb = f0 >> 7, cb = (f0 >> 5) & 3;
+                uint8_t *hq = p.hq + hq_offset(un.c, pos, n, (FB + 1) / 2, kb >> 1);
+                const int d = lane & 7;  // this lane's digit after the transpose
+                uint8_t *dst = hq + (kb & 1) * 512 + d * 64 + ((cb ^ ((d >> 1) & 3)) << 4) + 4 * (lane >> 3);
+#pragma unroll 1
+                for (int r = q >> 1; r < n; r += 2) {
+                    const float2 xs = s_xs[ch.rows[pos + r] / p.k];
+                    const float gv = xg[32 * r] * xs.x * xs.y, uv = xu[32 * r] * xs.x * xs.y;
+                    const float h = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
+                    const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23);
+                    const int sc = e == 255 ? 255 : max(0, e - 21);
+                    uint32_t dg = MXL_BIAS;
+                    if (e != 255) dg += (uint32_t)__float2int_rn(h * e8m0_inverse(sc));
+                    uint32_t w = 0;
 #pragma unroll
-                for (int c = 0; c < NR / 2; ++c) {
-                    const int r = 2 * c + (q >> 1);
-                    if (r < n) {
-                        const float2 xs = s_xs[ch.rows[pos + r] / p.k];
-                        const float other = in[32 * c];
-                        const float gv = (q < 2 ? mine[c] : other) * xs.x * xs.y;
-                        const float uv = (q < 2 ? other : mine[c]) * xs.x * xs.y;
-                        const float h = __fdividef(gv, 1.0f + expf(-gv)) * uv;
-                        const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23);
-                        const int sc = e == 255 ? 255 : max(0, e - 21);
-                        uint32_t dg = MXL_BIAS;
-                        if (e != 255) dg += (uint32_t)__float2int_rn(h * e8m0_inverse(sc));
-                        uint32_t w = 0;
-#pragma unroll
-                        for (int d = 0; d < 8; ++d) w |= digit_code((dg >> (3 * d)) & 7u) << (4 * d);
-                        // lane 8a + b: digit b of columns 8a .. 8a + 7
-                        uint32_t y = __shfl_xor_sync(0xffffffffu, w, 4);
-                        w = lane & 4 ? (w & 0xFFFF0000u) | (y >> 16) : (w & 0x0000FFFFu) | (y << 16);
-                        y = __shfl_xor_sync(0xffffffffu, w, 2);
-                        w = lane & 2 ? (w & 0xFF00FF00u) | ((y >> 8) & 0x00FF00FFu) : (w & 0x00FF00FFu) | ((y & 0x00FF00FFu) << 8);
-                        y = __shfl_xor_sync(0xffffffffu, w, 1);
-                        w = lane & 1 ? (w & 0xF0F0F0F0u) | ((y >> 4) & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | ((y & 0x0F0F0F0Fu) << 4);
-                        const int d = lane & 7;
-                        uint8_t *atom = p.hq + ((size_t)pos * HK + (size_t)(kb >> 1) * n + r) * 1024 + (kb & 1) * 512;
-                        *(uint32_t *)(atom + d * 64 + ((cb ^ ((d >> 1) & 3)) << 4) + 4 * (lane >> 3)) = w;
-                        if (lane == 0)
-                            ((uint8_t *)(p.hs + ((size_t)un.c * HK + (kb >> 1)) * 32 + (kb & 1) * 16 + r))[cb] = (uint8_t)sc;
-                    }
+                    for (int i8 = 0; i8 < 8; ++i8) w |= digit_code((dg >> (3 * i8)) & 7u) << (4 * i8);
+                    // lane 8a + b: digit b of columns 8a .. 8a + 7
+                    uint32_t y = __shfl_xor_sync(0xffffffffu, w, 4);
+                    w = lane & 4 ? (w & 0xFFFF0000u) | (y >> 16) : (w & 0x0000FFFFu) | (y << 16);
+                    y = __shfl_xor_sync(0xffffffffu, w, 2);
+                    w = lane & 2 ? (w & 0xFF00FF00u) | ((y >> 8) & 0x00FF00FFu) : (w & 0x00FF00FFu) | ((y & 0x00FF00FFu) << 8);
+                    y = __shfl_xor_sync(0xffffffffu, w, 1);
+                    w = lane & 1 ? (w & 0xF0F0F0F0u) | ((y >> 4) & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | ((y & 0x0F0F0F0Fu) << 4);
+                    *(uint32_t *)(dst + r * 1024) = w;
+                    if (lane == 0) hq[n * 1024 + (kb & 1) * 64 + 4 * r + cb] = (uint8_t)sc;
                 }
             } else {
                 const int o = 128 * un.m + 32 * q + lane;
-#pragma unroll
-                for (int c = 0; c < NR / 2; ++c) {
-                    if (2 * c < n) {
-                        uint32_t v0[8], v1[8];
-                        tmem_ld8(tb + 16 * c, v0);
-                        tmem_ld8(tb + 16 * c + 8, v1);
-                        tmem_ld_wait();
-                        const float a[2] = {digit_sum(v0), digit_sum(v1)};
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            if (2 * c + j < n && o < p.H) {
-                                const int r = ch.rows[pos + 2 * c + j];
-                                p.partial[(size_t)r * p.H + o] = s_w[r] * a[j];
-                            }
-                    }
+#pragma unroll 1
+                for (int i2 = 0; i2 < n; ++i2) {
+                    uint32_t v[8];
+                    tmem_ld8(tb + 8 * i2, v);
+                    tmem_ld_wait();
+                    const int r = ch.rows[pos + i2];
+                    const float a = s_w[r] * digit_sum(v);
+                    if (o < p.H) p.partial[(size_t)r * p.H + o] = a;
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -900,7 +882,6 @@ extern "C" int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int 
     b.xscale = a.xscale;
     b.xq = a.xq;
     b.hq = w + L.hq;
-    b.hs = (uint32_t *)(w + L.hs);
     b.partial = (float *)(w + L.partial);
     b.y = y;
     b.ticket = a.ctr;

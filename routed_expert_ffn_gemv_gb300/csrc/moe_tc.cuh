@@ -151,17 +151,43 @@ __host__ __device__ constexpr uint32_t umma_idesc_mxf4(int M, int N, int sf_id) 
            ((uint32_t)(M >> 4) << 24) | ((uint32_t)sf_id << 29);
 }
 
-// D[tmem] (+)= (A . SFA)[smem] * (B . SFB)[smem]^T over K = 64, issued by one thread.  The scales of
-// row m of A (n of B) are the bytes of one 32-bit word in tensor memory: lane m % 32 of every lane
-// quarter, column m / 32 from sfa (sfb).
+// D[tmem] (+)= (A . SFA)[smem] * (B . SFB)[smem]^T over K = 64, issued by one elected thread of a
+// converged warp.  The scales of row m of A (n of B) are the bytes of one 32-bit word in tensor memory:
+// lane m % 32 of every lane quarter, column m / 32 from sfa (sfb).  Called by the whole warp, the election
+// inside: the operands stay in uniform registers (behind an `if (lane == 0)` every operand is moved
+// there first, about 80 clocks an MMA).
 __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
             d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// The same election for a commit, a bulk copy and an expecting arrival.
+__device__ __forceinline__ void umma_commit_elect(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void bulk_g2s_elect(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_elect(uint64_t *bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes)
         : "memory");
 }
 
@@ -179,7 +205,8 @@ __device__ __forceinline__ void mbar_arrive1(uint64_t *bar) {
 // complete costs a few tens of clocks that way, about 190 by try_wait.  Then try_wait, which lets the
 // hardware suspend the thread: with a dozen warps waiting, polling by test_wait took the shared-memory
 // pipe from the working roles (MXFP4 layer, 8 tokens, Qwen-shaped: 76 us against 67 us).
-__device__ __forceinline__ bool mbar_wait_role(uint64_t *bar, uint32_t parity, int *status, volatile int *abort_flag) {
+static __device__ __forceinline__ bool mbar_wait_role(uint64_t *bar, uint32_t parity, int *status,
+                                                      volatile int *abort_flag) {
     if (mbar_test_wait(bar, parity)) return true;
     for (uint32_t i = 0; i < MOE_SPIN_LIMIT; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -188,6 +215,10 @@ __device__ __forceinline__ bool mbar_wait_role(uint64_t *bar, uint32_t parity, i
     moe_set_status(status, MOE_ERR_TIMEOUT);
     *abort_flag = 1;
     return false;
+}
+// The same for a whole warp: every lane waits, all agree.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, int *status, volatile int *abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait_role(bar, parity, status, abort_flag));
 }
 
 // Named barriers (ids 1..15) over `count` threads; the second ANDs a predicate.
