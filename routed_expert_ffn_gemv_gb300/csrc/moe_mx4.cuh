@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "moe_ptx.cuh"
 
@@ -12,11 +13,11 @@ __device__ __forceinline__ float e8m0_value(int s) {
     return __uint_as_float(bits);
 }
 
-// The scale byte of a block whose largest magnitude is amax: floor(log2 amax) - 2, biased and
+// The scale byte of a block whose largest magnitude has these bits: floor(log2 amax) - 2, biased and
 // clamped at 0, straight from the exponent field (a subnormal or zero amax gives 0); an infinity
-// or a NaN gives 255.
-__device__ __forceinline__ int e8m0_of_amax(float amax) {
-    const int e = (int)(__float_as_uint(amax) >> 23);
+// or a NaN gives 255.  Magnitudes compare as integers, NaN above all.
+__device__ __forceinline__ int e8m0_of_amax(uint32_t amax_bits) {
+    const int e = (int)(amax_bits >> 23);
     return e == 255 ? 255 : max(0, e - 2);
 }
 // 2^(127 - s), the multiplier that brings a block of scale s into the E2M1 range (s <= 252: a
@@ -29,40 +30,73 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
     asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Value of a 4-bit code: doubled magnitudes 0 1 2 3 4 6 8 12 as nibbles of a constant.
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-    const float m = 0.5f * (float)((0xC8643210u >> (4 * (code & 7))) & 15);
-    return code & 8 ? -m : m;
+// Values of the two codes of a byte.
+__device__ __forceinline__ float2 e2m1x2_value(uint32_t codes) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(codes));
+    return __half22float2(*(const __half2 *)&h);
 }
 
-// Eight consecutive elements as floats (wide loads where `wide`).
+// Eight consecutive elements as they are stored (wide loads where `wide`), as floats, and back.
 template <int XT>
-__device__ __forceinline__ void load8(const void *p, size_t i, bool wide, float (&v)[8]) {
+struct Raw8 {
+    uint32_t w[XT == MOE_BF16 ? 4 : 8];
+};
+template <int XT>
+__device__ __forceinline__ Raw8<XT> load_raw8(const void *p, size_t i, bool wide) {
+    Raw8<XT> r;
     if (XT == MOE_BF16) {
-        const __nv_bfloat16 *b = (const __nv_bfloat16 *)p + i;
+        const uint16_t *b = (const uint16_t *)p + i;
         if (wide) {
             const uint4 u = *(const uint4 *)b;
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = __uint_as_float(w[j] << 16);
-                v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-            }
+            r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __bfloat162float(b[j]);
+            for (int j = 0; j < 4; ++j) r.w[j] = (uint32_t)b[2 * j] | (uint32_t)b[2 * j + 1] << 16;
         }
     } else {
-        const float *f = (const float *)p + i;
+        const uint32_t *f = (const uint32_t *)p + i;
         if (wide) {
-            const float4 a = *(const float4 *)f, b = *(const float4 *)(f + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            const uint4 a = *(const uint4 *)f, b = *(const uint4 *)(f + 4);
+            r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
+            r.w[XT == MOE_BF16 ? 0 : 4] = b.x; r.w[XT == MOE_BF16 ? 0 : 5] = b.y;
+            r.w[XT == MOE_BF16 ? 0 : 6] = b.z; r.w[XT == MOE_BF16 ? 0 : 7] = b.w;
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = f[j];
+            for (int j = 0; j < (XT == MOE_BF16 ? 4 : 8); ++j) r.w[j] = f[j];
         }
     }
+    return r;
+}
+template <int XT>
+__device__ __forceinline__ void raw8_floats(const Raw8<XT> &r, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (XT == MOE_BF16) {
+            v[2 * j] = __uint_as_float(r.w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(r.w[j] & 0xFFFF0000u);
+        } else {
+            v[2 * j] = __uint_as_float(r.w[XT == MOE_BF16 ? 0 : 2 * j]);
+            v[2 * j + 1] = __uint_as_float(r.w[XT == MOE_BF16 ? 0 : 2 * j + 1]);
+        }
+    }
+}
+// Bits of the largest magnitude of the eight (as fp32).
+template <int XT>
+__device__ __forceinline__ uint32_t raw8_amax(const Raw8<XT> &r) {
+    if (XT == MOE_BF16) {
+        const uint32_t m = 0x7FFF7FFFu;
+        const uint32_t a = __vmaxu2(__vmaxu2(r.w[0] & m, r.w[1] & m), __vmaxu2(r.w[2] & m, r.w[3] & m));
+        return max(a << 16, a & 0xFFFF0000u);
+    }
+    uint32_t a = 0;
+#pragma unroll
+    for (int j = 0; j < (XT == MOE_BF16 ? 4 : 8); ++j) a = max(a, r.w[j] & 0x7FFFFFFFu);
+    return a;
+}
+template <int XT>
+__device__ __forceinline__ void load8(const void *p, size_t i, bool wide, float (&v)[8]) {
+    raw8_floats<XT>(load_raw8<XT>(p, i, wide), v);
 }
 template <int XT>
 __device__ __forceinline__ void store8(void *p, size_t i, bool wide, const float (&v)[8]) {
@@ -94,27 +128,27 @@ __device__ __forceinline__ void store8(void *p, size_t i, bool wide, const float
 
 // One thread's eight elements of a 32-column block shared by four neighbouring lanes: the block's
 // scale byte and the eight codes (element i at bits 4i).  All 32 lanes must call it.
-__device__ __forceinline__ uint32_t mx4_quant8(const float (&v)[8], int &scale) {
-    float amax = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        amax = fmaxf(amax, fabsf(v[j]));
-        bad |= !(fabsf(v[j]) <= 3.402823466e38f);  // fmaxf drops a NaN
-    }
-    if (bad) amax = __uint_as_float(0x7F800000u);
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+template <int XT>
+__device__ __forceinline__ uint32_t mx4_quant8(const Raw8<XT> &r, int &scale) {
+    uint32_t amax = raw8_amax<XT>(r);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     scale = e8m0_of_amax(amax);
     if (scale == 255) return 0;
     const float inv = e8m0_inverse(scale);
-    uint32_t c = 0;
+    float v[8];
+    raw8_floats<XT>(r, v);
+    uint32_t c[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c |= e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv) << (8 * j);
-    return c;
+    for (int j = 0; j < 4; ++j) c[j] = e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv);
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 __device__ __forceinline__ void mx4_dequant8(uint32_t codes, int scale, float (&v)[8]) {
     const float m = e8m0_value(scale);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = e2m1_value((codes >> (4 * j)) & 15) * m;
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = e2m1x2_value(codes >> (8 * j));
+        v[2 * j] = f.x * m;
+        v[2 * j + 1] = f.y * m;
+    }
 }

@@ -6,16 +6,15 @@
 //   read from tensor memory, exact products, fp32 sums in tensor memory.
 // The weights are the M side, so that an expert's few routes cost only as wide an MMA as they are.
 //
-//  * few routes (MX4_LOCAL_R): each CTA groups them by expert itself;
-//    otherwise mx4_route_kernel: the routes sorted by expert (one cluster of up to 8 CTAs: shared-memory
-//    histograms joined over distributed shared memory, positions by a shared cursor) and cut into
-//    chunks of at most NT routes of one expert, experts with the most routes first.  The order of
-//    the routes inside an expert is not fixed; a route's result does not depend on it.
+//  * few routes (MX4_LOCAL_R): each CTA groups them by expert itself; otherwise mx4_count_kernel and
+//    mx4_place_kernel sort them and lay their rows out.  Chunks are at most NT routes of one expert,
+//    experts with the most routes first.  The order of the routes inside an expert is not fixed; a
+//    route's result does not depend on it.
 //  * mx4_gemm_kernel: persistent, one CTA per SM; a work item is (chunk, 128-row weight tile).
 //    Warp roles, mbarrier rings that run on across items:
 //      warps 0, 1  a stage of 256 columns: the tile's two 8704-byte blocks (codes and scales, one
 //                  bulk copy: the slot image is in operand order) and the chunk's code rows, as runs
-//                  of mx4_gather_kernel's output, or, for few routes, four rows to a TMA gather
+//                  of mx4_place_kernel's output, or, for few routes, four rows to a TMA gather
 //                  straight into the 128-byte-swizzled operand layout;
 //      warp 2      one thread issues the four MMAs of a stage and one commit;
 //      warps 4-7   the stage's scales into tensor memory.  Each warp writes its own
@@ -31,11 +30,11 @@
 #include "moe_tc.cuh"
 
 #define MXG_THREADS 512
-#define MXG_CTRL 30720
+#define MXG_CTRL 32768
 #define MXG_WBYTES (2 * MX4_TB)  // weights of a stage: two tile blocks
-#define MXG_ROUTE_THREADS 1024
 #define MXG_TABLE 512             // chunks whose table entries are kept in shared memory
-#define MXG_ROUTE_CLUSTER 8
+
+#define MXG_ROUTE_BLOCKS 256
 
 namespace {
 
@@ -43,7 +42,7 @@ namespace {
 
 struct GemmWs {
     int max_chunks;
-    size_t o_rows, o_slot, o_pos, o_n, ints;  // in ints; [0] is the number of chunks
+    size_t o_rows, o_slot, o_pos, o_n, o_hist, ints;  // in ints; [0] is the number of chunks
     size_t Rp;                                // positions: every expert's start at a multiple of 8
     size_t codes, scales, total;              // in bytes
 };
@@ -58,6 +57,7 @@ GemmWs gemm_ws(int T, int H, int F, int E, int k, int NT) {
     L.o_slot = o; o += L.max_chunks;
     L.o_pos = o;  o += L.max_chunks;
     L.o_n = o;    o += L.max_chunks;
+    L.o_hist = o; o += (size_t)MXG_ROUTE_BLOCKS * E;
     L.ints = o;
     L.codes = (o * 4 + 1023) / 1024 * 1024;
     const size_t stages = (std::max(H, F) + 255) / 256, rows = R > MX4_LOCAL_R ? stages * L.Rp : 0;
@@ -73,116 +73,6 @@ int chunk_routes(int T, int E, int k) { return (long)T * k <= 16L * E ? MXG_NT_S
 
 // ------------------------------------------------------------------ routes by expert
 
-__global__ void __launch_bounds__(MXG_ROUTE_THREADS)
-mx4_route_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *__restrict__ table, int n_slots, int NT,
-                 int32_t *__restrict__ ints, int32_t *__restrict__ rows, int32_t *__restrict__ c_slot,
-                 int32_t *__restrict__ c_pos, int32_t *__restrict__ c_n, int *status) {
-    __shared__ __align__(16) int cnt[MOE_MAX_E];
-    __shared__ int hist[MOE_MAX_E], cur[MOE_MAX_E], off[MOE_MAX_E];
-    __shared__ int order[MOE_MAX_E], first[MOE_MAX_E];
-    const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), tid = threadIdx.x;
-    const int seg = (R + C - 1) / C, r0 = rank * seg, r1 = min(R, r0 + seg);
-    if (tid < MOE_MAX_E) hist[tid] = 0;
-    pdl_wait();
-    pdl_trigger();
-    __syncthreads();
-    for (int r = r0 + tid; r < r1; r += MXG_ROUTE_THREADS) {
-        const int e = ids[r];
-        if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-        else if (e != -1) moe_set_status(status, MOE_ERR_INVALID);
-    }
-    cluster_sync_all();
-    int before = 0;
-    if (tid < MOE_MAX_E) {
-        int total = 0;
-        for (int c = 0; c < C; ++c) {
-            if (c == rank) before = total;
-            total += (int)ld_cluster_u32(cluster_map(&hist[tid], c));
-        }
-        cnt[tid] = total;
-        off[tid] = total;
-    }
-    __syncthreads();
-    // exclusive sums over the experts: offsets of the routes
-    if (tid < 32) {
-        int v[MOE_MAX_E / 32], s = 0;
-        for (int i = 0; i < MOE_MAX_E / 32; ++i) {
-            v[i] = s;
-            s += (cnt[tid * (MOE_MAX_E / 32) + i] + 7) & ~7;
-        }
-        int x = s;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (tid >= o) x += y;
-        }
-        for (int i = 0; i < MOE_MAX_E / 32; ++i) off[tid * (MOE_MAX_E / 32) + i] = x - s + v[i];
-    }
-    __syncthreads();
-    if (tid < MOE_MAX_E) cur[tid] = off[tid] + before;
-    __syncthreads();
-    for (int rb = r0; rb < r1; rb += MXG_ROUTE_THREADS) {
-        // the lanes of one expert reserve their positions together
-        const int r = rb + tid, e = r < r1 ? ids[r] : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && e < E) {
-            const int lead = __ffs(peers) - 1;
-            int at = 0;
-            if ((tid & 31) == lead) at = atomicAdd(&cur[e], __popc(peers));
-            at = __shfl_sync(peers, at, lead);
-            rows[at + __popc(peers & ((1u << (tid & 31)) - 1))] = r;
-        }
-    }
-    if (rank == 0) {
-        // chunks, the experts with the most routes first
-        if (tid < MOE_MAX_E) {
-            const int mine = cnt[tid];
-            int o = 0;
-#pragma unroll 4
-            for (int j = 0; j < MOE_MAX_E; j += 4) {
-                const int4 v = *(const int4 *)&cnt[j];
-                o += (v.x > mine || (v.x == mine && j < tid)) + (v.y > mine || (v.y == mine && j + 1 < tid)) +
-                     (v.z > mine || (v.z == mine && j + 2 < tid)) + (v.w > mine || (v.w == mine && j + 3 < tid));
-            }
-            order[o] = tid;
-        }
-        __syncthreads();
-        if (tid < 32) {
-            int v[MOE_MAX_E / 32], s = 0;
-            for (int i = 0; i < MOE_MAX_E / 32; ++i) {
-                v[i] = s;
-                s += (cnt[order[tid * (MOE_MAX_E / 32) + i]] + NT - 1) / NT;
-            }
-            int x = s;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (tid >= o) x += y;
-            }
-            for (int i = 0; i < MOE_MAX_E / 32; ++i) first[tid * (MOE_MAX_E / 32) + i] = x - s + v[i];
-            if (tid == 31) ints[0] = x;
-        }
-        __syncthreads();
-        if (tid < MOE_MAX_E) {
-            const int e = order[tid], n = cnt[e], nc = (n + NT - 1) / NT;
-            int slot = -1;
-            if (n > 0) {
-                slot = table ? table[e] : e;
-                if (slot < 0 || slot >= n_slots) {
-                    moe_set_status(status, MOE_ERR_INVALID);
-                    slot = -1;
-                }
-            }
-            // near-equal chunks that start at multiples of 8 (NT is one: no chunk is empty)
-            const int size = nc ? ((n + nc - 1) / nc + 7) & ~7 : 0;
-            for (int c = 0; c < nc; ++c) {
-                c_slot[first[tid] + c] = slot;
-                c_pos[first[tid] + c] = off[e] + c * size;
-                c_n[first[tid] + c] = min(size, n - c * size);
-            }
-        }
-    }
-    cluster_sync_all();  // the histograms stay until every CTA has read them
-}
-
 // The eight scale bytes of a row from block 8q on (fewer at the row's end: zeros).
 __device__ __forceinline__ uint2 scale8(const uint8_t *row, int q, int KS) {
     if ((KS & 7) == 0 && ((uintptr_t)row & 7) == 0) return *(const uint2 *)(row + 8 * q);
@@ -192,61 +82,158 @@ __device__ __forceinline__ uint2 scale8(const uint8_t *row, int q, int KS) {
     return make_uint2(v[0], v[1]);
 }
 
-// ------------------------------------------------------------------ code rows in operand order
-//
-// Rows of codes and scales from their places to the chunks' positions, by stages of 256 columns:
-// codes [stage][position][128 bytes], 16-byte piece j at j ^ (position % 8) (the 128-byte swizzle; chunks
-// start at multiples of 8), scales [stage][position][8 bytes], zeros past K.  So a stage of a chunk is
-// two runs of bytes.  Measured: gathering by TMA inside the product kernel (four rows a copy, 48 copies
-// a stage) kept two warps busy all the time, about 80 clocks a copy, and bound it.
-// A warp takes eight positions; Rp positions in all.
-#define MXG_GATHER_THREADS 256
-__global__ void __launch_bounds__(MXG_GATHER_THREADS)
-mx4_gather_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int K, int div, int per_chunk,
-                  size_t Rp, const int32_t *__restrict__ ints, const int32_t *__restrict__ rows,
-                  const int32_t *__restrict__ c_pos, const int32_t *__restrict__ c_n, uint8_t *__restrict__ xg,
-                  uint8_t *__restrict__ sg) {
-    const int lane = threadIdx.x & 31, KS = K / 32, NKS = (K + 255) / 256;
+// Two kernels of the same blocks of consecutive routes.  The first counts each block's routes per expert.
+// In the second every block adds the counts up (all blocks: the experts' starts, at multiples of 8; the
+// blocks before: its own cursors), gives its routes their positions and takes their rows there, in
+// operand order by stages of 256 columns: codes [stage][position][128 bytes], 16-byte piece j at
+// j ^ (position % 8) (the 128-byte swizzle; chunks start at multiples of 8), scales [stage][position][8
+// bytes], zeros past K.  So a stage of a chunk is two runs of bytes.  Its first block writes the chunk
+// table.  Measured, 32768 routes: one cluster of 8 CTAs for the positions and a gather kernel took
+// 17 + 8 us; gathering by TMA inside the product kernel (four rows a copy, 48 copies a stage) kept two
+// warps busy all the time, about 80 clocks a copy, and bound it.
+#define MXG_ROUTE_THREADS 256
+
+__global__ void __launch_bounds__(MXG_ROUTE_THREADS)
+mx4_count_kernel(const int32_t *__restrict__ ids, int R, int E, int32_t *__restrict__ hist, int *status) {
+    __shared__ int h[MOE_MAX_E];
+    const int tid = threadIdx.x, seg = (R + gridDim.x - 1) / gridDim.x, r0 = blockIdx.x * seg, r1 = min(R, r0 + seg);
+    for (int e = tid; e < E; e += MXG_ROUTE_THREADS) h[e] = 0;
     pdl_wait();
     pdl_trigger();
-    const int items = ints[0] * per_chunk, warps = gridDim.x * (MXG_GATHER_THREADS / 32);
-    for (int it = blockIdx.x * (MXG_GATHER_THREADS / 32) + threadIdx.x / 32; it < items; it += warps) {
-        const int c = it / per_chunk, i0 = (it - c * per_chunk) * 8, n = min(8, c_n[c] - i0);
-        if (n <= 0) continue;
-        const int pos = c_pos[c] + i0;
-        // lane l: piece l % 8 of a stage, row l / 8 (and + 4)
-        const int j = lane & 7, r0 = lane >> 3;
-        const int src0 = r0 < n ? rows[pos + r0] / div : -1, src1 = r0 + 4 < n ? rows[pos + r0 + 4] / div : -1;
-        uint8_t *d0 = xg + (size_t)(pos + r0) * 128 + ((j ^ r0) << 4), *d1 = xg + (size_t)(pos + r0 + 4) * 128 + ((j ^ (r0 + 4)) << 4);
-#pragma unroll 4
-        for (int q = 0; q < NKS; ++q) {
-            const int col = 128 * q + 16 * j;  // bytes into the code row
-            uint4 a = make_uint4(0, 0, 0, 0), b = make_uint4(0, 0, 0, 0);
-            if (col < K / 2) {
-                if (src0 >= 0) a = *(const uint4 *)(codes + (size_t)src0 * (K / 2) + col);
-                if (src1 >= 0) b = *(const uint4 *)(codes + (size_t)src1 * (K / 2) + col);
-            }
-            if (src0 >= 0) *(uint4 *)(d0 + (size_t)q * Rp * 128) = a;
-            if (src1 >= 0) *(uint4 *)(d1 + (size_t)q * Rp * 128) = b;
+    __syncthreads();
+    for (int r = r0 + tid; r < r1; r += MXG_ROUTE_THREADS) {
+        const int e = ids[r];
+        if (e >= 0 && e < E) atomicAdd(&h[e], 1);
+        else if (e != -1) moe_set_status(status, MOE_ERR_INVALID);
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += MXG_ROUTE_THREADS) hist[blockIdx.x * E + e] = h[e];
+}
+
+// Exclusive sums of v over the block's 256 threads.
+__device__ __forceinline__ int block_exclusive(int v, int *warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) x += warp_sums[w];
+    return x - v;
+}
+
+__global__ void __launch_bounds__(MXG_ROUTE_THREADS)
+mx4_place_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *__restrict__ table, int n_slots, int NT,
+                 const int32_t *__restrict__ hist, const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
+                 int K, int div, size_t Rp, int32_t *__restrict__ ints, int32_t *__restrict__ rows,
+                 int32_t *__restrict__ c_slot, int32_t *__restrict__ c_pos, int32_t *__restrict__ c_n,
+                 uint8_t *__restrict__ xg, uint8_t *__restrict__ sg, int *status) {
+    __shared__ __align__(16) int cnt[MOE_MAX_E];
+    __shared__ int cur[MOE_MAX_E], order[MOE_MAX_E], sums[MXG_ROUTE_THREADS / 32];
+    __shared__ int s_pos[MXG_ROUTE_THREADS], s_src[MXG_ROUTE_THREADS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int seg = (R + gridDim.x - 1) / gridDim.x, r0 = blockIdx.x * seg, r1 = min(R, r0 + seg);
+    const int KS = K / 32, NKS = (K + 255) / 256;
+    pdl_wait();
+    pdl_trigger();
+    int total = 0, before = 0;
+    if (tid < E)
+#pragma unroll 16
+        for (int b = 0; b < (int)gridDim.x; ++b) {
+            const int v = hist[b * E + tid];
+            before += b < (int)blockIdx.x ? v : 0;
+            total += v;
         }
-        // scales: lane l takes row l / 4 and stages l % 4, + 4, ..
-        const int rs = lane >> 2, src = rs < n ? rows[pos + rs] / div : -1;
-        if (src >= 0)
+    const int off = block_exclusive((total + 7) & ~7, sums);
+    cnt[tid] = total;
+    cur[tid] = off + before;
+    __syncthreads();
+    for (int rb = r0; rb < r1; rb += MXG_ROUTE_THREADS) {
+        // the lanes of one expert reserve their positions together
+        const int r = rb + tid, id = r < r1 ? ids[r] : -1, e = id >= 0 && id < E ? id : -1;
+        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        int pos = -1;
+        if (e >= 0) {
+            const int lead = __ffs(peers) - 1;
+            int at = 0;
+            if (lane == lead) at = atomicAdd(&cur[e], __popc(peers));
+            at = __shfl_sync(peers, at, lead);
+            pos = at + __popc(peers & ((1u << lane) - 1));
+            rows[pos] = r;
+        }
+        s_pos[tid] = pos;
+        s_src[tid] = r / div;
+        __syncthreads();
+        // codes: lane l takes piece l % 8 of a stage of row l / 8 (of four rows at a time)
+        const int j = lane & 7;
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+            const int k = 32 * warp + 4 * i + (lane >> 3), at = s_pos[k];
+            if (at < 0) continue;
+            const uint8_t *src = codes + (size_t)s_src[k] * (K / 2);
+            uint8_t *dst = xg + (size_t)at * 128 + ((j ^ (at & 7)) << 4);
+#pragma unroll 4
+            for (int q = 0; q < NKS; ++q) {
+                const int col = 128 * q + 16 * j;  // bytes into the code row
+                *(uint4 *)(dst + (size_t)q * Rp * 128) = col < K / 2 ? *(const uint4 *)(src + col) : make_uint4(0, 0, 0, 0);
+            }
+        }
+        // scales: lane l takes row l / 4 (of eight at a time) and stages l % 4, + 4, ..
+        for (int i = 0; i < 4; ++i) {
+            const int k = 32 * warp + 8 * i + (lane >> 2), at = s_pos[k];
+            if (at < 0) continue;
             for (int q = lane & 3; q < NKS; q += 4)
-                *(uint2 *)(sg + ((size_t)q * Rp + pos + rs) * 8) = scale8(scales + (size_t)src * KS, q, KS);
+                *(uint2 *)(sg + ((size_t)q * Rp + at) * 8) = scale8(scales + (size_t)s_src[k] * KS, q, KS);
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0) {
+        // chunks, the experts with the most routes first
+        int o = 0;
+#pragma unroll 4
+        for (int j = 0; j < MOE_MAX_E; j += 4) {
+            const int4 v = *(const int4 *)&cnt[j];
+            o += (v.x > total || (v.x == total && j < tid)) + (v.y > total || (v.y == total && j + 1 < tid)) +
+                 (v.z > total || (v.z == total && j + 2 < tid)) + (v.w > total || (v.w == total && j + 3 < tid));
+        }
+        order[o] = tid;
+        cur[tid] = off;
+        __syncthreads();
+        const int e = order[tid], n = cnt[e], nc = (n + NT - 1) / NT;
+        const int first = block_exclusive(nc, sums);
+        if (tid == MXG_ROUTE_THREADS - 1) ints[0] = first + nc;
+        if (n > 0) {
+            int slot = table ? table[e] : e;
+            if (slot < 0 || slot >= n_slots) {
+                moe_set_status(status, MOE_ERR_INVALID);
+                slot = -1;
+            }
+            // near-equal chunks that start at multiples of 8 (NT is one: no chunk is empty)
+            const int size = ((n + nc - 1) / nc + 7) & ~7;
+            for (int c = 0; c < nc; ++c) {
+                c_slot[first + c] = slot;
+                c_pos[first + c] = cur[e] + c * size;
+                c_n[first + c] = min(size, n - c * size);
+            }
+        }
     }
 }
+static_assert(MXG_ROUTE_THREADS == MOE_MAX_E, "a thread per expert");
 
 // ------------------------------------------------------------------ the products
 
 struct GemmParams {
     CUtensorMap map;         // LOCAL: the code rows, boxes of 128 bytes of one row
     const uint8_t *scales;   // LOCAL: [rows][K / 32]
-    const uint8_t *xg, *sg;  // otherwise mx4_gather_kernel's rows
+    const uint8_t *xg, *sg;  // otherwise mx4_place_kernel's rows
     size_t Rp;
     const uint8_t *pool;
     size_t slot_bytes;
-    const int32_t *ints, *rows, *c_slot, *c_pos, *c_n;  // mx4_route_kernel's tables
+    const int32_t *ints, *rows, *c_slot, *c_pos, *c_n;  // mx4_place_kernel's tables
     const int32_t *ids, *table;                         // LOCAL
     int R, E, n_slots;
     const float *weights;    // down
@@ -284,7 +271,7 @@ __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// LOCAL: few routes, grouped by the CTA itself; otherwise mx4_route_kernel's tables.
+// LOCAL: few routes, grouped by the CTA itself; otherwise mx4_place_kernel's tables.
 template <int NT, bool DOWN, int OT, bool LOCAL>
 __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_constant__ GemmParams p) {
     using G = GemmGeom<NT>;
@@ -299,11 +286,11 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     static_assert((3 * G::S + 6) * 8 <= 1024, "barriers");
-    float *xch = (float *)(smem + 1024);             // [4 pairs][2 slots][2 ways][8 columns][32 lanes]
-    OutRow *e_out = (OutRow *)(smem + 1024 + 16384);      // [2 accumulators][NT]
+    float *xch = (float *)(smem + 1024);             // [4 pairs][2 slots][2 ways][8 columns][32 lanes]; down: [8][16][36]
+    OutRow *e_out = (OutRow *)(smem + 1024 + 18432);      // [2 accumulators][NT]
     Mx4Chunks &loc = *(Mx4Chunks *)(e_out + 2 * NT);      // LOCAL
     int *tab = (int *)(e_out + 2 * NT);                   // otherwise [3][MXG_TABLE]: the chunk table's start
-    static_assert(1024 + 16384 + 2 * NT * 16 + sizeof(Mx4Chunks) <= MXG_CTRL && MXG_CTRL % 1024 == 0 &&
+    static_assert(1024 + 18432 + 2 * NT * 16 + sizeof(Mx4Chunks) <= MXG_CTRL && MXG_CTRL % 1024 == 0 &&
                       3 * MXG_TABLE * 4 <= sizeof(Mx4Chunks),
                   "control block");
     uint8_t *ring = smem + MXG_CTRL;
@@ -559,19 +546,23 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                             if (i < nn) put(i);
                     }
                 } else {
-                    const int o = 128 * m + 32 * q + lane, nn = o < p.R_out ? min(16, n - c0) : 0;
-                    OutRow r[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) r[i] = row[i];
+                    // 32 rows x 16 routes by way of shared memory (padded: no bank conflicts), so that a store
+                    // covers four rows of four routes: a quarter of the store instructions
+                    float *xb = xch + ew * 576;
                     tmem_ld_wait();
-                    if (nn == 16) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) ((float *)r[i].p)[o] = r[i].w * __uint_as_float(v[i]);
-                    } else {
+                    for (int i = 0; i < 16; ++i) xb[36 * i + lane] = __uint_as_float(v[i]);
+                    __syncwarp();
+                    const int o = 128 * m + 32 * q + 4 * (lane & 7), nn = o < p.R_out ? n - c0 : 0;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i < nn) ((float *)r[i].p)[o] = r[i].w * __uint_as_float(v[i]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 4 * i + (lane >> 3);
+                        const OutRow d = row[r];
+                        const float4 a = *(const float4 *)(xb + 36 * r + 4 * (lane & 7));
+                        if (r < nn)
+                            *(float4 *)((float *)d.p + o) = make_float4(d.w * a.x, d.w * a.y, d.w * a.z, d.w * a.w);
                     }
+                    __syncwarp();
                 }
             }
             tc_fence_before();
@@ -694,23 +685,14 @@ int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, i
     p.status = moe_status_word_device_ptr();
 
     if (p.R > MX4_LOCAL_R) {
-        const int R = p.R;
         cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[2];
-        const int C = R <= 2 * MXG_ROUTE_THREADS ? 1 : MXG_ROUTE_CLUSTER;
-        moe_pdl_config(&cfg, attr, dim3(C), dim3(MXG_ROUTE_THREADS), 0, s);
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = C;
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.numAttrs = 2;
-        MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_route_kernel, ids, R, E, table, n_slots, NT, w, w + L.o_rows,
-                                        w + L.o_slot, w + L.o_pos, w + L.o_n, p.status));
-        const int per_chunk = NT / 8;
-        const long warps = (long)L.max_chunks * per_chunk;
-        moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<long>((warps + 7) / 8, 8 * 152)), dim3(MXG_GATHER_THREADS), 0,
-                       s);
-        MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_gather_kernel, codes, scales, p.K, p.div, per_chunk, L.Rp,
-                                        (const int32_t *)w, p.rows, p.c_pos, p.c_n, xg, sg));
+        cudaLaunchAttribute attr[1];
+        const int blocks = std::min(MXG_ROUTE_BLOCKS, (p.R + MXG_ROUTE_THREADS - 1) / MXG_ROUTE_THREADS);
+        moe_pdl_config(&cfg, attr, dim3(blocks), dim3(MXG_ROUTE_THREADS), 0, s);
+        MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_count_kernel, ids, p.R, E, w + L.o_hist, p.status));
+        MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_place_kernel, ids, p.R, E, table, n_slots, NT,
+                                        (const int32_t *)(w + L.o_hist), codes, scales, p.K, p.div, L.Rp, w,
+                                        w + L.o_rows, w + L.o_slot, w + L.o_pos, w + L.o_n, xg, sg, p.status));
     }
     if (down) return launch_gemm<true, MOE_F32>(p, NT, L.max_chunks, s);
     return otype == MOE_BF16 ? launch_gemm<false, MOE_BF16>(p, NT, L.max_chunks, s)
@@ -765,7 +747,7 @@ extern "C" int moe_mx4_expert_down(const uint8_t *h_codes, const uint8_t *h_scal
     if (rc != MOE_OK) return rc;
     if (T == 0) return MOE_OK;
     MOE_CHECK(h_codes && h_scales && ids && weights && partial && workspace && ws_bytes >= need);
-    MOE_CHECK(((uintptr_t)h_codes & 15) == 0 && ((uintptr_t)workspace & 255) == 0);
+    MOE_CHECK(((uintptr_t)h_codes & 15) == 0 && ((uintptr_t)workspace & 255) == 0 && ((uintptr_t)partial & 15) == 0);
     if ((rc = mx4_pool_check(H, F, n_slots, pool, slot_bytes)) != MOE_OK) return rc;
     return run_product(true, h_codes, h_scales, T, H, F, E, k, ids, weights, d_slot_table, n_slots, pool, slot_bytes,
                        partial, MOE_F32, workspace, moe_cuda_stream(s));

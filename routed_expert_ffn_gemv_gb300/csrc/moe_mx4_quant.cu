@@ -12,19 +12,21 @@
 namespace {
 
 // Rows: a thread takes eight consecutive columns (one 16-byte load of bf16, two of fp32) and
-// writes their four code bytes; the four threads of a block share its scale by two shuffles.
-template <int XT>
+// writes their four code bytes; the four threads of a block share its scale by two shuffles.  I: the
+// index type (32 bits wherever the rows have fewer than 2^31 groups: the division by the row length is
+// what an element costs most).
+template <int XT, typename I>
 __global__ void __launch_bounds__(MXQ_THREADS)
-mx4_rows_kernel(const void *__restrict__ x, int rows, int cols, size_t ld, int wide, uint8_t *__restrict__ codes,
+mx4_rows_kernel(const void *__restrict__ x, I n, I per, size_t ld, int wide, uint8_t *__restrict__ codes,
                 uint8_t *__restrict__ scales) {
-    const size_t per = (size_t)cols / 8, n = per * rows;
-    for (size_t i0 = (size_t)blockIdx.x * MXQ_THREADS; i0 < n; i0 += (size_t)gridDim.x * MXQ_THREADS) {
-        const size_t i = i0 + threadIdx.x;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        const size_t r = i / per, c = i - r * per;
-        if (i < n) load8<XT>(x, r * ld + c * 8, wide, v);
+    pdl_wait();
+    pdl_trigger();
+    for (I i0 = (I)blockIdx.x * MXQ_THREADS; i0 < n; i0 += (I)gridDim.x * MXQ_THREADS) {
+        const I i = i0 + threadIdx.x, r = i / per, c = i - r * per;
+        Raw8<XT> v = {};
+        if (i < n) v = load_raw8<XT>(x, (size_t)r * ld + (size_t)c * 8, wide);
         int s;
-        const uint32_t q = mx4_quant8(v, s);
+        const uint32_t q = mx4_quant8<XT>(v, s);
         if (i < n) {
             ((uint32_t *)codes)[i] = q;
             if ((c & 3) == 0) scales[i >> 2] = (uint8_t)s;
@@ -32,16 +34,17 @@ mx4_rows_kernel(const void *__restrict__ x, int rows, int cols, size_t ld, int w
     }
 }
 
-template <int YT>
+template <int YT, typename I>
 __global__ void __launch_bounds__(MXQ_THREADS)
-mx4_rows_back_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int rows, int cols,
-                     size_t ld, int wide, void *__restrict__ y) {
-    const size_t per = (size_t)cols / 8, n = per * rows;
-    for (size_t i = (size_t)blockIdx.x * MXQ_THREADS + threadIdx.x; i < n; i += (size_t)gridDim.x * MXQ_THREADS) {
-        const size_t r = i / per, c = i - r * per;
+mx4_rows_back_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, I n, I per, size_t ld,
+                     int wide, void *__restrict__ y) {
+    pdl_wait();
+    pdl_trigger();
+    for (I i = (I)blockIdx.x * MXQ_THREADS + threadIdx.x; i < n; i += (I)gridDim.x * MXQ_THREADS) {
+        const I r = i / per, c = i - r * per;
         float v[8];
         mx4_dequant8(((const uint32_t *)codes)[i], scales[i >> 2], v);
-        store8<YT>(y, r * ld + c * 8, wide, v);
+        store8<YT>(y, (size_t)r * ld + (size_t)c * 8, wide, v);
     }
 }
 
@@ -89,6 +92,8 @@ mx4_experts_kernel(const void *__restrict__ gate, const void *__restrict__ up, c
                    int F, int wide, int tiles, uint8_t *__restrict__ pool, size_t slot_bytes,
                    const int32_t *__restrict__ slots, int n_slots, int *status) {
     __shared__ __align__(16) uint8_t tb[MX4_TB];
+    pdl_wait();
+    pdl_trigger();
     const int i = blockIdx.x / tiles, tile = blockIdx.x % tiles;
     const int slot = slots ? slots[i] : i;
     if (slot < 0 || slot >= n_slots) {
@@ -97,14 +102,19 @@ mx4_experts_kernel(const void *__restrict__ gate, const void *__restrict__ up, c
     }
     const Mx4Tile t = mx4_tile_of<XT>(gate, up, down, i, H, F, tile);
     const int c = (threadIdx.x & 15) * 8;  // the half-warp's row takes 16 threads of 8 columns
+    Raw8<XT> v[8];  // every load first
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int row = threadIdx.x / 16 + 16 * j, h = row >> 6, r = row & 63;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const int row = threadIdx.x / 16 + 16 * j, h = j >> 2, r = row & 63;
+        v[j] = {};
         if (r < t.nrow[h] && t.col0 + c < t.K)
-            load8<XT>(t.src[h], (size_t)(t.row0[h] + r) * t.K + t.col0 + c, wide, v);
+            v[j] = load_raw8<XT>(t.src[h], (size_t)(t.row0[h] + r) * t.K + t.col0 + c, wide);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int row = threadIdx.x / 16 + 16 * j;
         int s;
-        const uint32_t q = mx4_quant8(v, s);
+        const uint32_t q = mx4_quant8<XT>(v[j], s);
         *(uint32_t *)(tb + mx4_code_offset(1, row, c)) = q;
         if ((c & 31) == 0) tb[mx4_scale_offset(1, row, c)] = (uint8_t)s;
     }
@@ -119,6 +129,8 @@ mx4_experts_back_kernel(const uint8_t *__restrict__ pool, size_t slot_bytes, con
                         int n_slots, int H, int F, int wide, int tiles, void *gate, void *up, void *down,
                         int *status) {
     __shared__ __align__(16) uint8_t tb[MX4_TB];
+    pdl_wait();
+    pdl_trigger();
     const int i = blockIdx.x / tiles, tile = blockIdx.x % tiles;
     const int slot = slots ? slots[i] : i;
     if (slot < 0 || slot >= n_slots) {
@@ -132,7 +144,7 @@ mx4_experts_back_kernel(const uint8_t *__restrict__ pool, size_t slot_bytes, con
     const int c = (threadIdx.x & 15) * 8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int row = threadIdx.x / 16 + 16 * j, h = row >> 6, r = row & 63;
+        const int row = threadIdx.x / 16 + 16 * j, h = j >> 2, r = row & 63;
         if (r >= t.nrow[h] || t.col0 + c >= t.K) continue;
         float v[8];
         mx4_dequant8(*(const uint32_t *)(tb + mx4_code_offset(1, row, c)), tb[mx4_scale_offset(1, row, c)], v);
@@ -148,9 +160,30 @@ int wide_rows(const void *p, size_t ld, int type) {
     return ((uintptr_t)p & 15) == 0 && (ld * es & 15) == 0;
 }
 
-unsigned rows_grid(int rows, int cols) {
-    const size_t b = ((size_t)rows * (cols / 8) + MXQ_THREADS - 1) / MXQ_THREADS;
-    return (unsigned)std::min<size_t>(b, 1u << 20);
+// A launch with the programmatic dependency on the stream's previous kernel.
+template <typename... K, typename... A>
+int launch(void (*kernel)(K...), size_t blocks, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<size_t>(blocks, 0x7FFFFFFFu)), dim3(MXQ_THREADS), 0, s);
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, (K)args...));
+    return MOE_OK;
+}
+
+template <int XT>
+int launch_rows(const void *x, int rows, int cols, size_t ld, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
+    const size_t per = (size_t)cols / 8, n = per * rows, g = (n + MXQ_THREADS - 1) / MXQ_THREADS;
+    const int wide = wide_rows(x, ld, XT);
+    return n < (1u << 31) ? launch(mx4_rows_kernel<XT, uint32_t>, g, s, x, n, per, ld, wide, codes, scales)
+                          : launch(mx4_rows_kernel<XT, size_t>, 1u << 20, s, x, n, per, ld, wide, codes, scales);
+}
+
+template <int YT>
+int launch_rows_back(const uint8_t *codes, const uint8_t *scales, int rows, int cols, void *y, size_t ld, cudaStream_t s) {
+    const size_t per = (size_t)cols / 8, n = per * rows, g = (n + MXQ_THREADS - 1) / MXQ_THREADS;
+    const int wide = wide_rows(y, ld, YT);
+    return n < (1u << 31) ? launch(mx4_rows_back_kernel<YT, uint32_t>, g, s, codes, scales, n, per, ld, wide, y)
+                          : launch(mx4_rows_back_kernel<YT, size_t>, 1u << 20, s, codes, scales, n, per, ld, wide, y);
 }
 
 // Checks of the expert calls; tiles of one image.
@@ -172,15 +205,9 @@ extern "C" int moe_mx4_quantize(const void *x, int xtype, int rows, int cols, si
     if (rows == 0) return MOE_OK;
     MOE_CHECK(x && codes && scales);
     MOE_CHECK(((uintptr_t)x & (xtype == MOE_BF16 ? 1 : 3)) == 0 && ((uintptr_t)codes & 15) == 0);
-    const int wide = wide_rows(x, ld, xtype);
-    const unsigned g = rows_grid(rows, cols);
     cudaStream_t st = moe_cuda_stream(s);
-    if (xtype == MOE_BF16)
-        mx4_rows_kernel<MOE_BF16><<<g, MXQ_THREADS, 0, st>>>(x, rows, cols, ld, wide, codes, scales);
-    else
-        mx4_rows_kernel<MOE_F32><<<g, MXQ_THREADS, 0, st>>>(x, rows, cols, ld, wide, codes, scales);
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
+    return xtype == MOE_BF16 ? launch_rows<MOE_BF16>(x, rows, cols, ld, codes, scales, st)
+                             : launch_rows<MOE_F32>(x, rows, cols, ld, codes, scales, st);
 }
 
 extern "C" int moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int rows, int cols, void *y, int ytype,
@@ -189,15 +216,9 @@ extern "C" int moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
     if (rows == 0) return MOE_OK;
     MOE_CHECK(y && codes && scales);
     MOE_CHECK(((uintptr_t)y & (ytype == MOE_BF16 ? 1 : 3)) == 0 && ((uintptr_t)codes & 15) == 0);
-    const int wide = wide_rows(y, ld, ytype);
-    const unsigned g = rows_grid(rows, cols);
     cudaStream_t st = moe_cuda_stream(s);
-    if (ytype == MOE_BF16)
-        mx4_rows_back_kernel<MOE_BF16><<<g, MXQ_THREADS, 0, st>>>(codes, scales, rows, cols, ld, wide, y);
-    else
-        mx4_rows_back_kernel<MOE_F32><<<g, MXQ_THREADS, 0, st>>>(codes, scales, rows, cols, ld, wide, y);
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
+    return ytype == MOE_BF16 ? launch_rows_back<MOE_BF16>(codes, scales, rows, cols, y, ld, st)
+                             : launch_rows_back<MOE_F32>(codes, scales, rows, cols, y, ld, st);
 }
 
 extern "C" int moe_mx4_quantize_experts(const void *gate, const void *up, const void *down, int wtype, int n, int H,
@@ -212,15 +233,11 @@ extern "C" int moe_mx4_quantize_experts(const void *gate, const void *up, const 
     const int wide = (any & 15) == 0;
     int *status = moe_status_word_device_ptr();
     cudaStream_t st = moe_cuda_stream(s);
-    const unsigned g = (unsigned)tiles * n;
-    if (wtype == MOE_BF16)
-        mx4_experts_kernel<MOE_BF16><<<g, MXQ_THREADS, 0, st>>>(gate, up, down, H, F, wide, tiles, (uint8_t *)pool,
-                                                               slot_bytes, slots, n_slots, status);
-    else
-        mx4_experts_kernel<MOE_F32><<<g, MXQ_THREADS, 0, st>>>(gate, up, down, H, F, wide, tiles, (uint8_t *)pool,
-                                                              slot_bytes, slots, n_slots, status);
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
+    const size_t g = (size_t)tiles * n;
+    return wtype == MOE_BF16 ? launch(mx4_experts_kernel<MOE_BF16>, g, st, gate, up, down, H, F, wide, tiles,
+                                      (uint8_t *)pool, slot_bytes, slots, n_slots, status)
+                             : launch(mx4_experts_kernel<MOE_F32>, g, st, gate, up, down, H, F, wide, tiles,
+                                      (uint8_t *)pool, slot_bytes, slots, n_slots, status);
 }
 
 extern "C" int moe_mx4_dequantize_experts(const void *pool, size_t slot_bytes, const int32_t *slots, int n_slots,
@@ -235,13 +252,9 @@ extern "C" int moe_mx4_dequantize_experts(const void *pool, size_t slot_bytes, c
     const int wide = (any & 15) == 0;
     int *status = moe_status_word_device_ptr();
     cudaStream_t st = moe_cuda_stream(s);
-    const unsigned g = (unsigned)tiles * n;
-    if (wtype == MOE_BF16)
-        mx4_experts_back_kernel<MOE_BF16><<<g, MXQ_THREADS, 0, st>>>((const uint8_t *)pool, slot_bytes, slots, n_slots,
-                                                                    H, F, wide, tiles, gate, up, down, status);
-    else
-        mx4_experts_back_kernel<MOE_F32><<<g, MXQ_THREADS, 0, st>>>((const uint8_t *)pool, slot_bytes, slots, n_slots,
-                                                                   H, F, wide, tiles, gate, up, down, status);
-    MOE_TRY_CUDA(cudaGetLastError());
-    return MOE_OK;
+    const size_t g = (size_t)tiles * n;
+    return wtype == MOE_BF16 ? launch(mx4_experts_back_kernel<MOE_BF16>, g, st, (const uint8_t *)pool, slot_bytes, slots,
+                                      n_slots, H, F, wide, tiles, gate, up, down, status)
+                             : launch(mx4_experts_back_kernel<MOE_F32>, g, st, (const uint8_t *)pool, slot_bytes, slots,
+                                      n_slots, H, F, wide, tiles, gate, up, down, status);
 }
