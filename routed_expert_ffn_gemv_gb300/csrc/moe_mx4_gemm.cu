@@ -30,9 +30,8 @@
 #include "moe_tc.cuh"
 
 #define MXG_THREADS 512
-#define MXG_CTRL 32768
 #define MXG_WBYTES (2 * MX4_TB)  // weights of a stage: two tile blocks
-#define MXG_TABLE 512             // chunks whose table entries are kept in shared memory
+#define MXG_ITEMS 64              // items of a CTA that are looked up ahead, in shared memory
 
 #define MXG_ROUTE_BLOCKS 256
 
@@ -68,7 +67,7 @@ GemmWs gemm_ws(int T, int H, int F, int E, int k, int NT) {
 
 // Most routes of a chunk.
 #define MXG_NT_SMALL 32
-#define MXG_NT_LARGE 192
+#define MXG_NT_LARGE 176
 int chunk_routes(int T, int E, int k) { return (long)T * k <= 16L * E ? MXG_NT_SMALL : MXG_NT_LARGE; }
 
 // ------------------------------------------------------------------ routes by expert
@@ -87,11 +86,13 @@ __device__ __forceinline__ uint2 scale8(const uint8_t *row, int q, int KS) {
 // blocks before: its own cursors), gives its routes their positions and takes their rows there, in
 // operand order by stages of 256 columns: codes [stage][position][128 bytes], 16-byte piece j at
 // j ^ (position % 8) (the 128-byte swizzle; chunks start at multiples of 8), scales [stage][position][8
-// bytes], zeros past K.  So a stage of a chunk is two runs of bytes.  Its first block writes the chunk
-// table.  Measured, 32768 routes: one cluster of 8 CTAs for the positions and a gather kernel took
-// 17 + 8 us; gathering by TMA inside the product kernel (four rows a copy, 48 copies a stage) kept two
+// bytes], zeros past K.  So a stage of a chunk is two runs of bytes.  One more block writes the chunk
+// table.  Bound by the latency of its row copies, hence 1024 threads a block.  Measured, 32768 routes:
+// one cluster of 8 CTAs for the positions and a gather kernel took 17 + 8 us, this kernel with 256
+// threads a block 27 us; gathering by TMA inside the product kernel (four rows a copy, 48 copies a stage) kept two
 // warps busy all the time, about 80 clocks a copy, and bound it.
-#define MXG_ROUTE_THREADS 256
+#define MXG_ROUTE_THREADS 256  // routes of a block at a time
+#define MXG_PLACE_THREADS 1024
 
 __global__ void __launch_bounds__(MXG_ROUTE_THREADS)
 mx4_count_kernel(const int32_t *__restrict__ ids, int R, int E, int32_t *__restrict__ hist, int *status) {
@@ -110,7 +111,7 @@ mx4_count_kernel(const int32_t *__restrict__ ids, int R, int E, int32_t *__restr
     for (int e = tid; e < E; e += MXG_ROUTE_THREADS) hist[blockIdx.x * E + e] = h[e];
 }
 
-// Exclusive sums of v over the block's 256 threads.
+// Exclusive sums of v over the block's threads.
 __device__ __forceinline__ int block_exclusive(int v, int *warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
@@ -126,86 +127,66 @@ __device__ __forceinline__ int block_exclusive(int v, int *warp_sums) {
     return x - v;
 }
 
-__global__ void __launch_bounds__(MXG_ROUTE_THREADS)
+__global__ void __launch_bounds__(MXG_PLACE_THREADS)
 mx4_place_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *__restrict__ table, int n_slots, int NT,
                  const int32_t *__restrict__ hist, const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                  int K, int div, size_t Rp, int32_t *__restrict__ ints, int32_t *__restrict__ rows,
                  int32_t *__restrict__ c_slot, int32_t *__restrict__ c_pos, int32_t *__restrict__ c_n,
                  uint8_t *__restrict__ xg, uint8_t *__restrict__ sg, int *status) {
+    constexpr int PARTS = MXG_PLACE_THREADS / MOE_MAX_E;
     __shared__ __align__(16) int cnt[MOE_MAX_E];
-    __shared__ int cur[MOE_MAX_E], order[MOE_MAX_E], sums[MXG_ROUTE_THREADS / 32];
+    __shared__ int cur[MOE_MAX_E], order[MOE_MAX_E], sums[MXG_PLACE_THREADS / 32], part[2][PARTS][MOE_MAX_E];
     __shared__ int s_pos[MXG_ROUTE_THREADS], s_src[MXG_ROUTE_THREADS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int seg = (R + gridDim.x - 1) / gridDim.x, r0 = blockIdx.x * seg, r1 = min(R, r0 + seg);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, blocks = gridDim.x - 1;
+    const int seg = (R + blocks - 1) / blocks, r0 = blockIdx.x * seg, r1 = min(R, r0 + seg);
     const int KS = K / 32, NKS = (K + 255) / 256;
+    // (the count kernel lets this one start after everything before it is complete: ids may be read)
+    const int first_id = tid < MXG_ROUTE_THREADS && r0 + tid < r1 ? ids[r0 + tid] : -1;
     pdl_wait();
     pdl_trigger();
-    int total = 0, before = 0;
-    if (tid < E)
+    {
+        const int e = tid % MOE_MAX_E, q = tid / MOE_MAX_E;
+        int t = 0, before = 0;
+        if (e < E)
 #pragma unroll 16
-        for (int b = 0; b < (int)gridDim.x; ++b) {
-            const int v = hist[b * E + tid];
-            before += b < (int)blockIdx.x ? v : 0;
-            total += v;
+            for (int b = q; b < blocks; b += PARTS) {
+                const int v = hist[b * E + e];
+                before += b < (int)blockIdx.x ? v : 0;
+                t += v;
+            }
+        part[0][q][e] = t;
+        part[1][q][e] = before;
+    }
+    __syncthreads();
+    int total = 0, before = 0;
+    if (tid < MOE_MAX_E)
+        for (int q = 0; q < PARTS; ++q) {
+            total += part[0][q][tid];
+            before += part[1][q][tid];
         }
     const int off = block_exclusive((total + 7) & ~7, sums);
-    cnt[tid] = total;
-    cur[tid] = off + before;
-    __syncthreads();
-    for (int rb = r0; rb < r1; rb += MXG_ROUTE_THREADS) {
-        // the lanes of one expert reserve their positions together
-        const int r = rb + tid, id = r < r1 ? ids[r] : -1, e = id >= 0 && id < E ? id : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        int pos = -1;
-        if (e >= 0) {
-            const int lead = __ffs(peers) - 1;
-            int at = 0;
-            if (lane == lead) at = atomicAdd(&cur[e], __popc(peers));
-            at = __shfl_sync(peers, at, lead);
-            pos = at + __popc(peers & ((1u << lane) - 1));
-            rows[pos] = r;
-        }
-        s_pos[tid] = pos;
-        s_src[tid] = r / div;
-        __syncthreads();
-        // codes: lane l takes piece l % 8 of a stage of row l / 8 (of four rows at a time)
-        const int j = lane & 7;
-#pragma unroll 2
-        for (int i = 0; i < 8; ++i) {
-            const int k = 32 * warp + 4 * i + (lane >> 3), at = s_pos[k];
-            if (at < 0) continue;
-            const uint8_t *src = codes + (size_t)s_src[k] * (K / 2);
-            uint8_t *dst = xg + (size_t)at * 128 + ((j ^ (at & 7)) << 4);
-#pragma unroll 4
-            for (int q = 0; q < NKS; ++q) {
-                const int col = 128 * q + 16 * j;  // bytes into the code row
-                *(uint4 *)(dst + (size_t)q * Rp * 128) = col < K / 2 ? *(const uint4 *)(src + col) : make_uint4(0, 0, 0, 0);
-            }
-        }
-        // scales: lane l takes row l / 4 (of eight at a time) and stages l % 4, + 4, ..
-        for (int i = 0; i < 4; ++i) {
-            const int k = 32 * warp + 8 * i + (lane >> 2), at = s_pos[k];
-            if (at < 0) continue;
-            for (int q = lane & 3; q < NKS; q += 4)
-                *(uint2 *)(sg + ((size_t)q * Rp + at) * 8) = scale8(scales + (size_t)s_src[k] * KS, q, KS);
-        }
-        __syncthreads();
+    if (tid < MOE_MAX_E) {
+        cnt[tid] = total;
+        cur[tid] = off + before;
     }
-    if (blockIdx.x == 0) {
+    __syncthreads();
+    if ((int)blockIdx.x == blocks) {
         // chunks, the experts with the most routes first
-        int o = 0;
+        if (tid < MOE_MAX_E) {
+            int o = 0;
 #pragma unroll 4
-        for (int j = 0; j < MOE_MAX_E; j += 4) {
-            const int4 v = *(const int4 *)&cnt[j];
-            o += (v.x > total || (v.x == total && j < tid)) + (v.y > total || (v.y == total && j + 1 < tid)) +
-                 (v.z > total || (v.z == total && j + 2 < tid)) + (v.w > total || (v.w == total && j + 3 < tid));
+            for (int j = 0; j < MOE_MAX_E; j += 4) {
+                const int4 v = *(const int4 *)&cnt[j];
+                o += (v.x > total || (v.x == total && j < tid)) + (v.y > total || (v.y == total && j + 1 < tid)) +
+                     (v.z > total || (v.z == total && j + 2 < tid)) + (v.w > total || (v.w == total && j + 3 < tid));
+            }
+            order[o] = tid;
+            cur[tid] = off;
         }
-        order[o] = tid;
-        cur[tid] = off;
         __syncthreads();
-        const int e = order[tid], n = cnt[e], nc = (n + NT - 1) / NT;
+        const int e = tid < MOE_MAX_E ? order[tid] : 0, n = tid < MOE_MAX_E ? cnt[e] : 0, nc = (n + NT - 1) / NT;
         const int first = block_exclusive(nc, sums);
-        if (tid == MXG_ROUTE_THREADS - 1) ints[0] = first + nc;
+        if (tid == MXG_PLACE_THREADS - 1) ints[0] = first;
         if (n > 0) {
             int slot = table ? table[e] : e;
             if (slot < 0 || slot >= n_slots) {
@@ -220,8 +201,50 @@ mx4_place_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *_
                 c_n[first + c] = min(size, n - c * size);
             }
         }
+        return;
+    }
+    for (int rb = r0; rb < r1; rb += MXG_ROUTE_THREADS) {
+        if (tid < MXG_ROUTE_THREADS) {
+            // the lanes of one expert reserve their positions together
+            const int r = rb + tid, id = rb == r0 ? first_id : r < r1 ? ids[r] : -1, e = id >= 0 && id < E ? id : -1;
+            const unsigned peers = __match_any_sync(0xffffffffu, e);
+            int pos = -1;
+            if (e >= 0) {
+                const int lead = __ffs(peers) - 1;
+                int at = 0;
+                if (lane == lead) at = atomicAdd(&cur[e], __popc(peers));
+                at = __shfl_sync(peers, at, lead);
+                pos = at + __popc(peers & ((1u << lane) - 1));
+                rows[pos] = r;
+            }
+            s_pos[tid] = pos;
+            s_src[tid] = r / div;
+        }
+        __syncthreads();
+        // a warp takes eight rows.  Codes: lane l piece l % 8 of a stage of row l / 8 (and + 4)
+        const int j = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = 8 * warp + 4 * i + (lane >> 3), at = s_pos[k];
+            if (at >= 0) {
+                const uint8_t *src = codes + (size_t)s_src[k] * (K / 2);
+                uint8_t *dst = xg + (size_t)at * 128 + ((j ^ (at & 7)) << 4);
+#pragma unroll 8
+                for (int q = 0; q < NKS; ++q) {
+                    const int col = 128 * q + 16 * j;  // bytes into the code row
+                    *(uint4 *)(dst + (size_t)q * Rp * 128) = col < K / 2 ? *(const uint4 *)(src + col) : make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+        // scales: lane l stages l % 4, + 4, .. of row l / 4
+        const int k = 8 * warp + (lane >> 2), at = s_pos[k];
+        if (at >= 0)
+            for (int q = lane & 3; q < NKS; q += 4)
+                *(uint2 *)(sg + ((size_t)q * Rp + at) * 8) = scale8(scales + (size_t)s_src[k] * KS, q, KS);
+        __syncthreads();
     }
 }
+static_assert(MXG_PLACE_THREADS == 4 * MXG_ROUTE_THREADS, "eight rows a warp");
 static_assert(MXG_ROUTE_THREADS == MOE_MAX_E, "a thread per expert");
 
 // ------------------------------------------------------------------ the products
@@ -246,21 +269,25 @@ struct GemmParams {
 
 // A ring stage and its scales in tensor memory share their index: a landed stage means that the MMAs
 // that read the scales' previous contents are done, so the scale slots need no wait of their own.
-template <int NT>
+// A stage lives about 3000 clocks (its copies, its scales, its MMAs): as many stages as fit.  Gate/up
+// exchanges eight routes at a time, down (three stages an item, its epilogue the longer part) 16.
+template <int NT, bool DOWN>
 struct GemmGeom {
-    static constexpr int SOFF = MXG_WBYTES + NT * 128;       // weights, code rows, scales
-    static constexpr int STAGE = (SOFF + NT * 8 + 1023) / 1024 * 1024;
-    static constexpr int S = NT == MXG_NT_LARGE ? 4 : 8;     // ring stages
+    static constexpr int NI = (NT + 31) / 32;                // 32-route groups
+    static constexpr int STAGE = MXG_WBYTES + NT * 128;      // weights, code rows
+    static constexpr int SSTAGE = NI * 256;                  // scales of the rows
+    static constexpr int S = NT == MXG_NT_LARGE ? (DOWN ? 4 : 5) : (DOWN ? 8 : 9);  // ring stages
     static constexpr int SFCOL = 2 * NT;                     // scales after the two accumulators, 24 columns a stage
-    static constexpr size_t SMEM = 1024 + MXG_CTRL + (size_t)S * STAGE;
-    static_assert(SFCOL + S * 24 <= 512 && STAGE % 1024 == 0 && SMEM <= 227 * 1024, "budget");
+    static constexpr int XCH = DOWN ? 8 * 16 * 36 * 4 : 4 * 2 * 2 * 4 * 32 * 4;
+    static constexpr int O_XCH = 1024 + MXG_ITEMS * 16, O_ROWS = O_XCH + XCH, O_LOC = O_ROWS + 2 * NT * 8;
+    static constexpr int O_SC = (O_LOC + (int)sizeof(Mx4Chunks) + 15) / 16 * 16;
+    static constexpr int O_RING = (O_SC + S * SSTAGE + 1023) / 1024 * 1024;
+    static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
+    static_assert(SFCOL + S * 24 <= 512 && STAGE % 1024 == 0 && O_LOC % 16 == 0 && SMEM <= 227 * 1024, "budget");
 };
 
-// Where a route's outputs go, and the router weight on them (down).
-struct alignas(16) OutRow {
-    uint8_t *p;
-    float w;
-};
+// A work item: slot (-1: none), first position and number of its routes, weight tile.
+typedef int4 Item;
 
 // Four rows of the map's box width to 4 x 128 bytes of shared memory.  x is a multiple of 128.
 __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, int x, const int (&r)[4], uint64_t *bar) {
@@ -274,7 +301,7 @@ __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, i
 // LOCAL: few routes, grouped by the CTA itself; otherwise mx4_place_kernel's tables.
 template <int NT, bool DOWN, int OT, bool LOCAL>
 __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_constant__ GemmParams p) {
-    using G = GemmGeom<NT>;
+    using G = GemmGeom<NT, DOWN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     uint64_t *s_full = (uint64_t *)smem;
@@ -286,14 +313,11 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     static_assert((3 * G::S + 6) * 8 <= 1024, "barriers");
-    float *xch = (float *)(smem + 1024);             // [4 pairs][2 slots][2 ways][8 columns][32 lanes]; down: [8][16][36]
-    OutRow *e_out = (OutRow *)(smem + 1024 + 18432);      // [2 accumulators][NT]
-    Mx4Chunks &loc = *(Mx4Chunks *)(e_out + 2 * NT);      // LOCAL
-    int *tab = (int *)(e_out + 2 * NT);                   // otherwise [3][MXG_TABLE]: the chunk table's start
-    static_assert(1024 + 18432 + 2 * NT * 16 + sizeof(Mx4Chunks) <= MXG_CTRL && MXG_CTRL % 1024 == 0 &&
-                      3 * MXG_TABLE * 4 <= sizeof(Mx4Chunks),
-                  "control block");
-    uint8_t *ring = smem + MXG_CTRL;
+    Item *items = (Item *)(smem + 1024);                  // [MXG_ITEMS]
+    float *xch = (float *)(smem + G::O_XCH);              // gate/up [4 pairs][2][2 ways][4 routes][32], down [8][16][36]
+    int2 *e_rows = (int2 *)(smem + G::O_ROWS);            // [2 accumulators][NT]: route, its weight's bits
+    Mx4Chunks &loc = *(Mx4Chunks *)(smem + G::O_LOC);     // LOCAL
+    uint8_t *ring = smem + G::O_RING, *sring = smem + G::O_SC;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
@@ -321,21 +345,19 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     pdl_wait();
     pdl_trigger();
     if (LOCAL) mx4_local_chunks(loc, p.ids, p.R, p.E, p.table, p.n_slots, NT, p.status);
-    const int *c_slots = LOCAL ? loc.slot : p.c_slot, *c_poss = LOCAL ? loc.pos : p.c_pos, *c_ns = LOCAL ? loc.n : p.c_n;
-    if (!LOCAL && p.ints[0] <= MXG_TABLE) {
-        // every role looks its items up; from global memory each look costs an L2 round trip
-        for (int i = threadIdx.x; i < p.ints[0]; i += MXG_THREADS) {
-            tab[i] = p.c_slot[i];
-            tab[MXG_TABLE + i] = p.c_pos[i];
-            tab[2 * MXG_TABLE + i] = p.c_n[i];
-        }
-        c_slots = tab;
-        c_poss = tab + MXG_TABLE;
-        c_ns = tab + 2 * MXG_TABLE;
-        __syncthreads();
-    }
     const int *rows = LOCAL ? loc.rows : p.rows;
     const int MT = p.MT, n_items = (LOCAL ? loc.nch : p.ints[0]) * MT;
+    // this CTA's items are blockIdx.x, + gridDim.x, ..; every role looks them up, and from global memory
+    // each look costs an L2 round trip
+    const int n_mine = (int)blockIdx.x < n_items ? (n_items - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0;
+    auto look_up = [&](int i) -> Item {
+        const int j = blockIdx.x + i * gridDim.x, c = j / MT;
+        return LOCAL ? make_int4(loc.slot[c], loc.pos[c], loc.n[c], j - c * MT)
+                     : make_int4(p.c_slot[c], p.c_pos[c], p.c_n[c], j - c * MT);
+    };
+    for (int i = threadIdx.x; i < min(n_mine, MXG_ITEMS); i += MXG_THREADS) items[i] = look_up(i);
+    __syncthreads();
+    auto item_at = [&](int i) -> Item { return i < MXG_ITEMS ? items[i] : look_up(i); };
     const int K = p.K, KB = (K + 127) / 128, NKS = (KB + 1) / 2, KS = K / 32;
 
     if (warp < 2) {
@@ -345,17 +367,17 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
         int g = 0, st_i = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
-            const int c = j / MT, m = j % MT;
-            const int slot = __shfl_sync(0xffffffffu, c_slots[c], 0);
+        for (int i = 0; i < n_mine && ok; ++i) {
+            const Item it = item_at(i);
+            const int slot = __shfl_sync(0xffffffffu, it.x, 0), m = __shfl_sync(0xffffffffu, it.w, 0);
             if (slot < 0) continue;
-            const int pos0 = __shfl_sync(0xffffffffu, c_poss[c], 0), n = __shfl_sync(0xffffffffu, c_ns[c], 0);
+            const int pos0 = __shfl_sync(0xffffffffu, it.y, 0), n = __shfl_sync(0xffffffffu, it.z, 0);
             const int npad = (n + 7) & ~7, q = 2 * lane + warp;  // this lane's group of four rows
             int r4[4];
             if (LOCAL)
-                for (int i = 0; i < 4; ++i) {
-                    const int at = 4 * q + i;
-                    r4[i] = rows[pos0 + (at < n ? at : 0)] / p.div;  // rows past the chunk: unused columns
+                for (int k = 0; k < 4; ++k) {
+                    const int at = 4 * q + k;
+                    r4[k] = rows[pos0 + (at < n ? at : 0)] / p.div;  // rows past the chunk: unused columns
                 }
             const uint8_t *w = p.pool + (size_t)slot * p.slot_bytes + p.mat + (size_t)m * KB * MX4_TB;
             const uint8_t *xrow = p.xg + (size_t)pos0 * 128, *srow = p.sg + (size_t)pos0 * 8;
@@ -373,7 +395,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                     const uint32_t sb = (uint32_t)((n + 1) & ~1) * 8u;
                     mbar_arrive_expect_tx_elect(full, (uint32_t)n * 128u + sb);
                     bulk_g2s_elect(st + MXG_WBYTES, xrow, (uint32_t)n * 128u, full);
-                    bulk_g2s_elect(st + G::SOFF, srow, sb, full);
+                    bulk_g2s_elect(sring + st_i * G::SSTAGE, srow, sb, full);
                     xrow += p.Rp * 128;
                     srow += p.Rp * 8;
                 }
@@ -399,10 +421,10 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
         int jl = 0, st_i = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
-            const int c = __shfl_sync(0xffffffffu, j / MT, 0);
-            if (c_slots[c] < 0) continue;
-            const int npad = __shfl_sync(0xffffffffu, (c_ns[c] + 7) & ~7, 0);
+        for (int i = 0; i < n_mine && ok; ++i) {
+            const Item it = item_at(i);
+            if (it.x < 0) continue;
+            const int npad = __shfl_sync(0xffffffffu, (it.z + 7) & ~7, 0);
             const uint32_t id0 = umma_idesc_mxf4(128, npad, 0), id2 = umma_idesc_mxf4(128, npad, 2);
             const int buf = jl & 1;
             if (jl >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((jl / 2) - 1) & 1, p.status, abort_flag))) break;
@@ -434,13 +456,14 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     } else if (warp >= 4 && warp < 8) {
         // ---------------- scales
         const uint32_t t0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::SFCOL;
-        constexpr int NI = NT / 32;
-        int g = 0;
+        constexpr int NI = G::NI;
+        int st_i = 0;
+        uint32_t ph = 0;
         bool ok = true;
-        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
-            const int c = j / MT;
-            if (c_slots[c] < 0) continue;
-            const int pos0 = c_poss[c], n = c_ns[c];
+        for (int j = 0; j < n_mine && ok; ++j) {
+            const Item it = item_at(j);
+            if (it.x < 0) continue;
+            const int pos0 = it.y, n = it.z;
             // LOCAL: the routes' scales from their rows, loaded two stages ahead (a load takes about as long
             // as a stage); otherwise they landed with the stage
             const uint8_t *row[NI];
@@ -453,16 +476,14 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                     n0[i] = row[i] ? scale8(row[i], 0, KS) : make_uint2(0, 0);
                     n1[i] = row[i] && NKS > 1 ? scale8(row[i], 1, KS) : make_uint2(0, 0);
                 }
-            for (int kc = 0; kc < NKS; ++kc, ++g) {
-                const int s = g % G::S;
+            for (int kc = 0; kc < NKS; ++kc) {
                 uint32_t v[24];
-                ok = mbar_wait_role(&s_full[s], (g / G::S) & 1, p.status, abort_flag);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (!(ok = mbar_wait_warp(&s_full[st_i], ph, p.status, abort_flag))) break;
                 tc_fence_after();
-                const uint8_t *st = ring + (size_t)s * G::STAGE;
+                const uint8_t *st = ring + (size_t)st_i * G::STAGE;
                 if (!LOCAL)
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) n0[i] = *(const uint2 *)(st + G::SOFF + 8 * (32 * i + lane));
+                    for (int i = 0; i < NI; ++i) n0[i] = *(const uint2 *)(sring + st_i * G::SSTAGE + 8 * (32 * i + lane));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     v[8 + i] = i < NI ? n0[i < NI ? i : 0].x : 0u;
@@ -480,87 +501,109 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                 v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
                 v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 #pragma unroll
-                for (int i = 0; i < 3; ++i) tmem_st8(t0 + 24 * s + 8 * i, *reinterpret_cast<uint32_t(*)[8]>(&v[8 * i]));
+                for (int i = 0; i < 3; ++i) tmem_st8(t0 + 24 * st_i + 8 * i, *reinterpret_cast<uint32_t(*)[8]>(&v[8 * i]));
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive1(&sf_full[s]);
+                if (lane == 0) mbar_arrive1(&sf_full[st_i]);
+                if (++st_i == G::S) {
+                    st_i = 0;
+                    ph ^= 1u;
+                }
             }
         }
     } else if (warp >= 8) {
         // ---------------- epilogue: lane quarter q, lane = weight row 32 q + lane of the tile; the two
-        // warps of a quarter take alternate groups of 16 routes.  Every output row's address is looked
-        // up once per item.  Gate/up: lanes 0-63 hold gate rows, 64-127 the same up rows; a gate warp
-        // and its up warp trade halves of the 16 routes, so that both work on SwiGLU.
-        const int q = warp & 3, ew = warp - 8, half = ew >> 2;
-        constexpr int ES = OT == MOE_BF16 ? 2 : 4;
+        // warps of a quarter take alternate groups of routes.  The next item's routes and weights are
+        // read while this one is worked on.  Gate/up: lanes 0-63 hold gate rows, 64-127 the same up
+        // rows; a gate warp and its up warp trade halves of the group, so that both work on SwiGLU.
+        const int q = warp & 3, ew = warp - 8, half = ew >> 2, et = ew * 32 + lane;
         int jl = 0, xs = 0;
-        bool ok = true;
-        for (int j = blockIdx.x; j < n_items && ok; j += gridDim.x) {
-            const int c = j / MT, m = j % MT;
-            if (c_slots[c] < 0) continue;
-            const int pos0 = c_poss[c], n = c_ns[c], buf = jl & 1;
-            for (int i = ew * 32 + lane; i < n; i += 256) {
-                const int r = rows[pos0 + i];
-                e_out[buf * NT + i] = {(uint8_t *)p.out + (size_t)r * p.R_out * ES, DOWN ? p.weights[r] : 0.f};
-            }
+        auto next_item = [&](int i, Item &it) {  // the first item from i on that has a slot
+            for (; i < n_mine; ++i)
+                if ((it = item_at(i)).x >= 0) break;
+            return i;
+        };
+        Item it = make_int4(-1, 0, 0, 0);
+        int i = next_item(0, it);
+        int route = i < n_mine && et < it.z ? rows[it.y + et] : 0;
+        float weight = DOWN && i < n_mine && et < it.z ? p.weights[route] : 0.f;
+        while (i < n_mine) {
+            const int n = it.z, m = it.w, buf = jl & 1;
+            if (et < n) e_rows[buf * NT + et] = make_int2(route, __float_as_int(weight));
+            Item nx = it;
+            i = next_item(i + 1, nx);
+            const bool more = i < n_mine && et < nx.z;
+            if (more) route = rows[nx.y + et];
             const bool w = mbar_wait_role(&acc_full[buf], (jl / 2) & 1, p.status, abort_flag);
-            if (!(ok = bar_and_n(1, 256, w))) break;
+            if (!bar_and_n(1, 256, w)) break;
+            if (DOWN && more) weight = p.weights[route];
             tc_fence_after();
             const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * NT;
-            for (int c0 = 16 * half; c0 < n; c0 += 32, ++xs) {
-                uint32_t v[16];
-                tmem_ld16(tb + c0, v);
-                const OutRow *row = e_out + buf * NT + c0;
-                if (!DOWN) {
-                    // the gate warp keeps routes 0-7 of the group and hands over 8-15, the up warp the
-                    // other way round
-                    const int pair = (q & 1) + 2 * half, up = q >> 1;
-                    float *xb = xch + (size_t)(pair * 2 + (xs & 1)) * 512 + lane;
-                    uint8_t *o[8];
-                    const int f = 64 * m + 32 * (q & 1) + lane, nn = f < p.R_out ? min(8, n - c0 - 8 * up) : 0;
+            if (!DOWN) {
+                constexpr int ES = OT == MOE_BF16 ? 2 : 4;
+                const int pair = (q & 1) + 2 * half, up = q >> 1, f = 64 * m + 32 * (q & 1) + lane;
+                uint8_t *out = (uint8_t *)p.out + (size_t)f * ES;
+                for (int c0 = 8 * half; c0 < n; c0 += 16, ++xs) {
+                    uint32_t v[8];
+                    tmem_ld8(tb + c0, v);
+                    // the gate warp keeps routes 0-3 of the group and hands over 4-7, the up warp the other
+                    // way round
+                    float *xb = xch + (size_t)(pair * 2 + (xs & 1)) * 256 + lane;
+                    const int2 *row = e_rows + buf * NT + c0 + 4 * up;
+                    uint8_t *o[4];
+                    const int nn = f < p.R_out ? min(4, n - c0 - 4 * up) : 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = row[8 * up + i].p + (size_t)f * ES;
+                    for (int k = 0; k < 4; ++k) o[k] = out + (size_t)row[k].x * (p.R_out * ES);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) xb[256 * up + 32 * i] = __uint_as_float(up ? v[i] : v[8 + i]);
+                    for (int k = 0; k < 4; ++k) xb[128 * up + 32 * k] = __uint_as_float(up ? v[k] : v[4 + k]);
                     bar_sync_n(2 + pair, 64);
-                    float h[8];
+                    float h[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float other = xb[256 * (1 - up) + 32 * i];
-                        const float gv = up ? other : __uint_as_float(v[i]);
-                        const float uv = up ? __uint_as_float(v[8 + i]) : other;
-                        h[i] = __fdividef(gv, 1.0f + expf(-gv)) * uv;
+                    for (int k = 0; k < 4; ++k) {
+                        const float other = xb[128 * (1 - up) + 32 * k];
+                        const float gv = up ? other : __uint_as_float(v[k]);
+                        const float uv = up ? __uint_as_float(v[4 + k]) : other;
+                        h[k] = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
                     }
-                    auto put = [&](int i) {
-                        if (OT == MOE_BF16) *(__nv_bfloat16 *)o[i] = __float2bfloat16(h[i]);
-                        else *(float *)o[i] = h[i];
+                    auto put = [&](int k) {
+                        if (OT == MOE_BF16) *(__nv_bfloat16 *)o[k] = __float2bfloat16(h[k]);
+                        else *(float *)o[k] = h[k];
                     };
-                    if (nn == 8) {  // no branch between the stores
+                    if (nn == 4) {  // no branch between the stores
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) put(i);
+                        for (int k = 0; k < 4; ++k) put(k);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i < nn) put(i);
+                        for (int k = 0; k < 4; ++k)
+                            if (k < nn) put(k);
                     }
-                } else {
-                    // 32 rows x 16 routes by way of shared memory (padded: no bank conflicts), so that a store
-                    // covers four rows of four routes: a quarter of the store instructions
-                    float *xb = xch + ew * 576;
+                }
+            } else {
+                // 32 rows x 16 routes by way of shared memory (padded: no bank conflicts), so that a store
+                // covers four rows of four routes: a quarter of the store instructions
+                float *xb = xch + ew * 576;
+                const int o = 128 * m + 32 * q + 4 * (lane & 7);
+                float *out = (float *)p.out + o;
+                for (int c0 = 16 * half; c0 < n; c0 += 32) {
+                    uint32_t v[16];
+                    tmem_ld16(tb + c0, v);
+                    const int nn = o < p.R_out ? n - c0 : 0;
+                    int2 d[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) d[k] = e_rows[buf * NT + c0 + 4 * k + (lane >> 3)];
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) xb[36 * i + lane] = __uint_as_float(v[i]);
+                    for (int k = 0; k < 16; ++k) xb[36 * k + lane] = __uint_as_float(v[k]);
                     __syncwarp();
-                    const int o = 128 * m + 32 * q + 4 * (lane & 7), nn = o < p.R_out ? n - c0 : 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 4 * i + (lane >> 3);
-                        const OutRow d = row[r];
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 4 * k + (lane >> 3);
                         const float4 a = *(const float4 *)(xb + 36 * r + 4 * (lane & 7));
+                        const float wt = __int_as_float(d[k].y);
                         if (r < nn)
-                            *(float4 *)((float *)d.p + o) = make_float4(d.w * a.x, d.w * a.y, d.w * a.z, d.w * a.w);
+                            *(float4 *)(out + (size_t)d[k].x * p.R_out) = make_float4(wt * a.x, wt * a.y, wt * a.z, wt * a.w);
                     }
                     __syncwarp();
                 }
@@ -569,6 +612,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive1(&acc_empty[buf]);
             ++jl;
+            it = nx;
         }
     }
     tc_fence_before();
@@ -614,7 +658,7 @@ int encode_codes_map(const uint8_t *codes, long rows, int K, CUtensorMap *map) {
 
 template <int NT, bool DOWN, int OT, bool LOCAL>
 int launch_gemm_t(const GemmParams &p, int max_chunks, cudaStream_t s) {
-    using G = GemmGeom<NT>;
+    using G = GemmGeom<NT, DOWN>;
     static std::mutex mu;
     static int sms[64] = {0};
     int dev = -1;
@@ -690,6 +734,7 @@ int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, i
         const int blocks = std::min(MXG_ROUTE_BLOCKS, (p.R + MXG_ROUTE_THREADS - 1) / MXG_ROUTE_THREADS);
         moe_pdl_config(&cfg, attr, dim3(blocks), dim3(MXG_ROUTE_THREADS), 0, s);
         MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_count_kernel, ids, p.R, E, w + L.o_hist, p.status));
+        moe_pdl_config(&cfg, attr, dim3(blocks + 1), dim3(MXG_PLACE_THREADS), 0, s);
         MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_place_kernel, ids, p.R, E, table, n_slots, NT,
                                         (const int32_t *)(w + L.o_hist), codes, scales, p.K, p.div, L.Rp, w,
                                         w + L.o_rows, w + L.o_slot, w + L.o_pos, w + L.o_n, xg, sg, p.status));
