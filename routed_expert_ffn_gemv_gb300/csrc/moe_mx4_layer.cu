@@ -10,7 +10,7 @@
 //   x: one scale per token (largest magnitude to 7190000, the largest symmetric 8-digit number);
 //   h: one power of two per 32 columns, the MMA's own E8M0 scale (largest magnitude below 2^22).
 //
-//  * mx4_prep_kernel, 8-CTA clusters of 1 to 4 tokens: the router (a CTA sums its eighth of H, the
+//  * mx4_prep_kernel, 8-CTA clusters of 1 or 2 tokens: the router (a CTA sums its eighth of H, the
 //    partial logits meet over distributed shared memory, one warp selects), the tokens' digits in
 //    operand order, and the counters of the second kernel.
 //  * mx4_layer_kernel: persistent.  Units: (chunk of at most NR routes of one expert, 128-row weight
@@ -36,7 +36,7 @@
 #include "moe_tc.cuh"
 
 #define MXL_CLUSTER 8
-#define MXL_MAX_CLUSTERS 8    // of the first kernel, 1 to 4 tokens each
+#define MXL_MAX_CLUSTERS 16   // of the first kernel, 1 or 2 tokens each
 #define MXL_PREP_THREADS 256
 #define MXL_THREADS 384
 #define MXL_Q 4               // claimed units in flight in a CTA
@@ -109,13 +109,15 @@ __device__ __forceinline__ void half8(const uint4 &u, float (&w)[8]) {
     }
 }
 
-// TT: tokens of a cluster (the last one may hold fewer).  Few tokens to a cluster and up to eight
-// clusters: the router's sums, not its reads of w_router from L2, take the time.
+// TT: tokens of a cluster (the last one may hold fewer).  Few tokens to a cluster and up to 16 clusters:
+// the router's sums, not its reads of w_router from L2, take the time.  The kernel is a chain of
+// latencies, instruction fetches among them: loops are kept rolled.
 template <int XT, int TT>
-__global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p) {
+__global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid_constant__ PrepParams p) {
     extern __shared__ __align__(16) float sm[];
     __shared__ uint32_t mx_w[TT][MXL_PREP_THREADS / 32], mx[TT], gmx[TT];
-    constexpr int NW = MXL_PREP_THREADS / 32, PRE = 16;  // rows of w_router a thread reads ahead
+    __shared__ float lg[MOE_MAX_E];
+    constexpr int NW = MXL_PREP_THREADS / 32, PRE = 8;  // rows of w_router a thread reads at a time
     const int rank = (int)cluster_ctarank(), tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int HS = p.H / MXL_CLUSTER, h0 = rank * HS, E8 = (p.E + 7) & ~7;
     const int t0 = blockIdx.y * TT, nt = min(TT, p.T - t0);
@@ -126,39 +128,59 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p
     int ncl = 0;  // log2 of the column groups, a power of two of them
     while ((8 << ncl) < E8) ++ncl;
     const int cg = tid & ((1 << ncl) - 1), hsub = tid >> ncl, NH = MXL_PREP_THREADS >> ncl;
-    const bool has = 8 * cg < p.E;
     const uint16_t *wr = p.w_router + (size_t)h0 * p.E + 8 * cg;
-    uint4 pre[PRE];
-    if (p.wide_w && has)  // the router's weights do not come from the kernel before
+    const int ne = p.E - 8 * cg;
+    auto load_rows = [&](int h, uint4 (&a)[PRE]) {
 #pragma unroll
-        for (int i = 0; i < PRE; ++i) {
-            const int h = hsub + i * NH;
-            pre[i] = h < HS ? *(const uint4 *)(wr + (size_t)h * p.E) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < PRE; ++i, h += NH) {
+            a[i] = make_uint4(0, 0, 0, 0);
+            if (h < HS && ne > 0) {
+                const uint16_t *src = wr + (size_t)h * p.E;
+                if (p.wide_w) {
+                    a[i] = *(const uint4 *)src;
+                } else {
+                    uint32_t q[4] = {0, 0, 0, 0};
+#pragma unroll 1
+                    for (int j = 0; j < min(8, ne); ++j) {
+                        const uint32_t v = (uint32_t)src[j] << (16 * (j & 1));
+                        if (j < 2) q[0] |= v;
+                        else if (j < 4) q[1] |= v;
+                        else if (j < 6) q[2] |= v;
+                        else q[3] |= v;
+                    }
+                    a[i] = make_uint4(q[0], q[1], q[2], q[3]);
+                }
+            }
         }
+    };
+    uint4 wa[PRE], wb[PRE];
+    load_rows(hsub, wa);  // the router's weights do not come from the kernel before
+    load_rows(hsub + PRE * NH, wb);
     pdl_wait();
     pdl_trigger();  // not before: the next kernel reads its slot table before its own wait
-    float bias[MOE_MAX_E / 32];
-    if (warp == 0)
+    // this CTA's eighth of the tokens, and their largest magnitudes (as bits: NaN sorts above all)
+    {
+        uint32_t m[TT] = {};
+        for (int h = tid; h < HS; h += MXL_PREP_THREADS)
 #pragma unroll
-        for (int i = 0; i < MOE_MAX_E / 32; ++i) bias[i] = p.bias && lane + 32 * i < p.E ? p.bias[lane + 32 * i] : 0.f;
+            for (int t = 0; t < TT; ++t) {
+                float v = 0.f;
+                if (t < nt) {
+                    const size_t at = (size_t)(t0 + t) * p.H + h0 + h;
+                    v = XT == MOE_BF16 ? __bfloat162float(((const __nv_bfloat16 *)p.x)[at]) : ((const float *)p.x)[at];
+                }
+                xs[h * TT + t] = v;
+                m[t] = max(m[t], __float_as_uint(v) & 0x7FFFFFFFu);
+            }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            m[t] = __reduce_max_sync(0xffffffffu, m[t]);
+            if (lane == 0) mx_w[t][warp] = m[t];
+        }
+    }
+    const float bias = p.bias && tid < p.E ? p.bias[tid] : 0.f;
     if (blockIdx.y == 0)
         for (int i = rank * MXL_PREP_THREADS + tid; i < p.n_ctr; i += MXL_CLUSTER * MXL_PREP_THREADS) p.ctr[i] = 0;
-    // this CTA's eighth of the tokens, and their largest magnitudes (as bits: NaN sorts above all)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        uint32_t m = 0;
-        for (int h = tid; h < HS; h += MXL_PREP_THREADS) {
-            float v = 0.f;
-            if (t < nt) {
-                const size_t at = (size_t)(t0 + t) * p.H + h0 + h;
-                v = XT == MOE_BF16 ? __bfloat162float(((const __nv_bfloat16 *)p.x)[at]) : ((const float *)p.x)[at];
-            }
-            xs[h * TT + t] = v;
-            m = max(m, __float_as_uint(v) & 0x7FFFFFFFu);
-        }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) mx_w[t][warp] = m;
-    }
     __syncthreads();
     if (tid < TT) {
         uint32_t m = 0;
@@ -170,43 +192,30 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p
     for (int t = 0; t < TT; ++t)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[t][j] = 0.f;
-    auto add_row = [&](int h, const float (&w)[8]) {
+#pragma unroll 1
+    for (int h = hsub; h < HS; h += PRE * NH) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const float xv = xs[h * TT + t];
+        for (int i = 0; i < PRE; ++i) {
+            float w[8];
+            half8(wa[i], w);
+            const float *xh = xs + min(h + i * NH, HS - 1) * TT;  // (rows past the slice are zeros)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(xv, w[j], acc[t][j]);
-        }
-    };
-    if (has) {
-        float w[8];
-        if (p.wide_w) {
+            for (int t = 0; t < TT; ++t) {
+                const float xv = xh[t];
 #pragma unroll
-            for (int i = 0; i < PRE; ++i)
-                if (hsub + i * NH < HS) {
-                    half8(pre[i], w);
-                    add_row(hsub + i * NH, w);
-                }
-#pragma unroll 4
-            for (int h = hsub + PRE * NH; h < HS; h += NH) {
-                half8(*(const uint4 *)(wr + (size_t)h * p.E), w);
-                add_row(h, w);
+                for (int j = 0; j < 8; ++j) acc[t][j] = fmaf(xv, w[j], acc[t][j]);
             }
-        } else {
-            const int ne = min(8, p.E - 8 * cg);
-            for (int h = hsub; h < HS; h += NH) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = j < ne ? __half2float(__ushort_as_half(wr[(size_t)h * p.E + j])) : 0.f;
-                add_row(h, w);
-            }
+            wa[i] = wb[i];
         }
+        if (h + 2 * PRE * NH < HS) load_rows(h + 2 * PRE * NH, wb);
     }
+#pragma unroll 1
     for (int o = 1 << ncl; o < 32; o <<= 1)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[t][j] += __shfl_xor_sync(0xffffffffu, acc[t][j], o);
-    if (lane < (1 << ncl) && has)
+    if (lane < (1 << ncl) && ne > 0)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -219,34 +228,29 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p
         part[i] = s;
     }
     cluster_sync_all();
+    // a thread per expert sums token t0 + rank's logit; the last warp fetches the tokens' maxima
+    if (rank < nt && tid < p.E) {
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < MXL_CLUSTER; ++r) s += ld_cluster_f32(cluster_map(&part[rank * E8 + tid], r));
+        s += bias;
+        lg[tid] = (s != s) ? -INFINITY : s;  // NaN never wins
+    }
+    if (warp == NW - 1) {
+        uint32_t m = lane < TT * MXL_CLUSTER ? ld_cluster_u32(cluster_map(&mx[lane / MXL_CLUSTER], lane % MXL_CLUSTER)) : 0;
+#pragma unroll
+        for (int o = 1; o < MXL_CLUSTER; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane < TT * MXL_CLUSTER && lane % MXL_CLUSTER == 0) gmx[lane / MXL_CLUSTER] = m;
+    }
+    __syncthreads();
+    // nothing of another CTA is read after this; a CTA's own shared memory stays until all have come here
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (warp == 0) {
-        // token t0 + rank is selected by this CTA's first warp
-        if (rank < nt) {
-            float v[MOE_MAX_E / 32];
-#pragma unroll
-            for (int i = 0; i < MOE_MAX_E / 32; ++i) {
-                const int e = lane + 32 * i;
-                v[i] = -INFINITY;
-                if (e < p.E) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int r = 0; r < MXL_CLUSTER; ++r) s += ld_cluster_f32(cluster_map(&part[rank * E8 + e], r));
-                    s += bias[i];
-                    v[i] = (s != s) ? -INFINITY : s;  // NaN never wins
-                }
-            }
-            select_topk_softmax(v, p.E, p.k, lane, (size_t)(t0 + rank), p.ids, p.weights, 0.f);
-        }
+        if (rank < nt) select_topk_keys(lg, p.E, p.k, lane, (size_t)(t0 + rank), p.ids, p.weights);
     } else {
         // digits, by the other warps: eight columns of one token per thread
-        if (warp == 1) {
-            uint32_t m = lane < TT * MXL_CLUSTER ? ld_cluster_u32(cluster_map(&mx[lane / MXL_CLUSTER], lane % MXL_CLUSTER)) : 0;
-#pragma unroll
-            for (int o = 1; o < MXL_CLUSTER; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane < TT * MXL_CLUSTER && lane % MXL_CLUSTER == 0) gmx[lane / MXL_CLUSTER] = m;
-        }
-        bar_sync_n(1, MXL_PREP_THREADS - 32);
         const int per = p.H / 8;
+#pragma unroll 1
         for (int i = rank * (MXL_PREP_THREADS - 32) + tid - 32; i < nt * per; i += MXL_CLUSTER * (MXL_PREP_THREADS - 32)) {
             const int t = i / per, col = (i - t * per) * 8;
             float v[8];
@@ -279,7 +283,8 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(PrepParams p
             for (int q = 0; q < 8; ++q) *(uint32_t *)(atom + q * 64 + ((c ^ ((q >> 1) & 3)) << 4) + o) = w[q];
         }
     }
-    cluster_sync_all();  // partial logits and maxima stay until every CTA has read them
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ experts and combine
@@ -788,11 +793,12 @@ int launch_prep_t(const PrepParams &p, cudaStream_t s) {
     return MOE_OK;
 }
 
+static_assert(MOE_DECODE_MAX_T <= 2 * MXL_MAX_CLUSTERS, "two tokens a cluster at most");
+
 template <int XT>
 int launch_prep(const PrepParams &p, cudaStream_t s) {
     if (p.T <= MXL_MAX_CLUSTERS) return launch_prep_t<XT, 1>(p, s);
-    if (p.T <= 2 * MXL_MAX_CLUSTERS) return launch_prep_t<XT, 2>(p, s);
-    return launch_prep_t<XT, 4>(p, s);
+    return launch_prep_t<XT, 2>(p, s);
 }
 
 // Shared memory of a block, less the alignment of its start.
