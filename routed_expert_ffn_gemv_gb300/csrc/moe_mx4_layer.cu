@@ -46,6 +46,7 @@
 #define MXL_BIAS 9586980u     // 4 (8^8 - 1) / 7: turns digits -4 .. 3 into 0 .. 7
 #define MXL_WBYTES (2 * MX4_TB)
 
+static_assert(MXL_PREP_THREADS == MOE_MAX_E, "a thread per expert");
 static_assert(MXL_MAX_R <= MX4_LOCAL_R, "a CTA groups the routes itself");
 
 namespace {
@@ -116,7 +117,8 @@ template <int XT, int TT>
 __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid_constant__ PrepParams p) {
     extern __shared__ __align__(16) float sm[];
     __shared__ uint32_t mx_w[TT][MXL_PREP_THREADS / 32], mx[TT], gmx[TT];
-    __shared__ float lg[MOE_MAX_E];
+    __shared__ __align__(16) uint32_t key[MOE_MAX_E];
+    __shared__ uint32_t sel[2 * MOE_MAX_K];
     constexpr int NW = MXL_PREP_THREADS / 32, PRE = 8;  // rows of w_router a thread reads at a time
     const int rank = (int)cluster_ctarank(), tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int HS = p.H / MXL_CLUSTER, h0 = rank * HS, E8 = (p.E + 7) & ~7;
@@ -233,8 +235,9 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid
         float s = 0.f;
 #pragma unroll
         for (int r = 0; r < MXL_CLUSTER; ++r) s += ld_cluster_f32(cluster_map(&part[rank * E8 + tid], r));
-        s += bias;
-        lg[tid] = (s != s) ? -INFINITY : s;  // NaN never wins
+        key[tid] = select_key(s + bias);
+    } else {
+        key[tid] = 0;
     }
     if (warp == NW - 1) {
         uint32_t m = lane < TT * MXL_CLUSTER ? ld_cluster_u32(cluster_map(&mx[lane / MXL_CLUSTER], lane % MXL_CLUSTER)) : 0;
@@ -245,16 +248,22 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid
     __syncthreads();
     // nothing of another CTA is read after this; a CTA's own shared memory stays until all have come here
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    if (warp == 0) {
-        if (rank < nt) select_topk_keys(lg, p.E, p.k, lane, (size_t)(t0 + rank), p.ids, p.weights);
-    } else {
-        // digits, by the other warps: eight columns of one token per thread
-        const int per = p.H / 8;
+    if (rank < nt) select_topk_block(key, p.E, p.k, sel, (size_t)(t0 + rank), p.ids, p.weights);
+    if (warp > 0) {
+        // digits, by the other warps: eight columns of one token per thread, of this CTA's eighth of H where
+        // it is whole groups of eight columns, else of the tokens' groups in turn
+        const bool own = HS % 8 == 0;
+        const int per = own ? HS / 8 : p.H / 8, step = (MXL_PREP_THREADS - 32) * (own ? 1 : MXL_CLUSTER);
 #pragma unroll 1
-        for (int i = rank * (MXL_PREP_THREADS - 32) + tid - 32; i < nt * per; i += MXL_CLUSTER * (MXL_PREP_THREADS - 32)) {
-            const int t = i / per, col = (i - t * per) * 8;
+        for (int i = own ? tid - 32 : (tid - 32) * MXL_CLUSTER + rank; i < nt * per; i += step) {
+            const int t = i / per, col = (i - t * per) * 8 + (own ? h0 : 0);
             float v[8];
-            load8<XT>(p.x, (size_t)(t0 + t) * p.H + col, p.wide_x, v);
+            if (own) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = xs[(col - h0 + j) * TT + t];
+            } else {
+                load8<XT>(p.x, (size_t)(t0 + t) * p.H + col, p.wide_x, v);
+            }
             // largest magnitude = norm * pw, norm in [1, 2), pw a power of two (possibly subnormal)
             const uint32_t m = gmx[t];
             const int e = (int)(m >> 23);

@@ -64,60 +64,50 @@ __device__ __forceinline__ void select_topk_softmax(const float (&v)[MOE_MAX_E /
 }
 
 #ifdef __CUDACC__
-// The same selection where its latency counts: logits lg[0 .. E) in shared memory (no NaN: those are
-// -inf), one warp.  A logit is an unsigned key that orders like it; each step is one warp maximum of the
-// keys and one warp minimum of the ids that hold it, and only the lane that lost its best looks for
-// another.  Lanes 0 .. k-1 write ids / weights of row `row`.  (Measured on the decode layer: 0.6 us for 8
-// of 128 where the shuffle selection took 3 to 5 us.)
-__device__ __forceinline__ void select_topk_keys(const float *lg, int E, int k, int lane, size_t row,
-                                                 int32_t *__restrict__ ids, float *__restrict__ weights) {
-    auto key_of = [](float v) {
-        const uint32_t b = __float_as_uint(v + 0.0f);  // -0 and 0 are equal logits
-        return b & 0x80000000u ? ~b : b | 0x80000000u;
-    };
-    unsigned taken = 0;
-    uint32_t best = 0;
-    int best_e = 0x7FFFFFFF;
-    auto look = [&]() {
-        best = 0;
-        best_e = 0x7FFFFFFF;
-#pragma unroll 1
-        for (int e = lane; e < E; e += 32)
-            if (!(taken >> (e >> 5) & 1u)) {
-                const uint32_t q = key_of(lg[e]);
-                if (best_e == 0x7FFFFFFF || q > best) {
-                    best = q;
-                    best_e = e;
-                }
-            }
-    };
-    look();
-    int my_id = 0;
-    float my_v = 0.f, top = 0.f;
-#pragma unroll 1
-    for (int j = 0; j < k; ++j) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == m ? (unsigned)best_e : 0x7FFFFFFFu);
-        const float v = lg[e];
-        if (j == 0) top = v;
-        if (lane == j) {
-            my_id = e;
-            my_v = v;
-        }
-        if ((e & 31) == lane) {
-            taken |= 1u << (e >> 5);
-            look();
-        }
-        __syncwarp();
+// The same selection where its latency counts, by a block of 256 threads: key[0 .. E) in shared memory
+// (16-byte aligned, zeros up to a multiple of 4) holds select_key of the logits.  An expert's rank is the
+// number of experts before it, counted by all threads at once, several to an expert; no step waits for
+// another.  `sel`: 2 * MOE_MAX_K words.  Syncs the block once; after that the first warp writes ids /
+// weights of row `row` and the others return.  (Measured on the decode layer, 8 of 128: the shuffle
+// selection took 3 to 5 us.)
+__device__ __forceinline__ uint32_t select_key(float v) {
+    const uint32_t b = __float_as_uint((v != v ? -INFINITY : v) + 0.0f);  // NaN never wins; -0 equals 0
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float select_value(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+__device__ __forceinline__ void select_topk_block(const uint32_t *key, int E, int k, uint32_t *sel, size_t row,
+                                                  int32_t *__restrict__ ids, float *__restrict__ weights) {
+    const int tid = threadIdx.x;
+    int lg = 0;  // log2 of the experts' power of two: 256 >> lg threads (1 to 32) to an expert
+    while ((1 << lg) < E) ++lg;
+    const int lp = min(5, 8 - lg), part = tid & ((1 << lp) - 1), e = tid >> lp;
+    const uint32_t mine = e < E ? key[e] : 0;
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 4 * part; j < E; j += 4 << lp) {
+        const uint4 v = *(const uint4 *)(key + j);
+        rank += (v.x > mine || (v.x == mine && j < e)) + (v.y > mine || (v.y == mine && j + 1 < e)) +
+                (v.z > mine || (v.z == mine && j + 2 < e)) + (v.w > mine || (v.w == mine && j + 3 < e));
     }
-    const float x = lane < k ? expf(my_v - top) : 0.f;
-    float sum = x;
+    for (int o = 1; o < 1 << lp; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (e < E && part == 0 && rank < k) {
+        sel[2 * rank] = (uint32_t)e;
+        sel[2 * rank + 1] = mine;
+    }
+    __syncthreads();
+    if (tid < 32) {
+        const bool on = tid < k;
+        const float x = on ? expf(select_value(sel[2 * tid + 1]) - select_value(sel[1])) : 0.f;
+        float sum = x;
 #pragma unroll
-    for (int o = 1; o < MOE_MAX_K; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane < k) {
-        ids[row * k + lane] = my_id;
-        weights[row * k + lane] = x / sum;
+        for (int o = 1; o < MOE_MAX_K; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (on) {
+            ids[row * k + tid] = (int32_t)sel[2 * tid];
+            weights[row * k + tid] = x / sum;
+        }
     }
 }
-static_assert(MOE_MAX_K == 8, "the sum over the selected takes three exchanges");
+static_assert(MOE_MAX_K == 8 && MOE_MAX_E == 256, "three exchanges over the selected, a thread per expert at least");
 #endif
