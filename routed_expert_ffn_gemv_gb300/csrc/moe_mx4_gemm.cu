@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
         // ---------------- producers.  LOCAL: warp 0 the stage's expected bytes, its weights and the even
         // groups of four code rows, warp 1 the odd groups.  Otherwise warp 0 the weights, warp 1
         // the chunk's rows and scales, runs of bytes.
+        const uint64_t once = l2_evict_first();
         int g = 0, st_i = 0;
         uint32_t ph = 1;
         bool ok = true;
@@ -388,7 +389,9 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                 if (warp == 0) {
                     const uint32_t wb = 2 * kc + 1 < KB ? MXG_WBYTES : MX4_TB;
                     mbar_arrive_expect_tx_elect(full, LOCAL ? wb + (uint32_t)npad * 128u : wb);
-                    bulk_g2s_elect(st, w, wb, full);
+                    // few routes read an expert's weights about once, many in several chunks
+                    if (LOCAL) bulk_g2s_elect_hint(st, w, wb, full, once);
+                    else bulk_g2s_elect(st, w, wb, full);
                     w += MXG_WBYTES;
                 } else if (!LOCAL) {
                     // (an arrival of its own: a copy takes its thread about 100 clocks)

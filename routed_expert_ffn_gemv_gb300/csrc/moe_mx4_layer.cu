@@ -517,6 +517,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
         {
             bool ok = true;
             int fills = 0;
+            const uint64_t once = l2_evict_first();
             for (int i = 0; ok; ++i) {
                 const int q = i % MXL_Q, u = __shfl_sync(0xffffffffu, claim, 0);
                 if (i >= MXL_Q && !(ok = mbar_wait_warp(&q_empty[q], ((i / MXL_Q) & 1) ^ 1, p.status, abort_flag))) break;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                     if (fills >= S && !(ok = mbar_wait_warp(&s_empty[s], ph ^ 1u, p.status, abort_flag))) break;
                     const uint32_t wb = 2 * kc + 1 < KB ? MXL_WBYTES : MX4_TB;
                     mbar_arrive_expect_tx_elect(&s_full[s], wb + nb);
-                    bulk_g2s_elect(ring + (size_t)s * STAGE, w, wb, &s_full[s]);
+                    bulk_g2s_elect_hint(ring + (size_t)s * STAGE, w, wb, &s_full[s], once);
                 }
             }
             // never leave with copies in flight: the last fill of every stage
