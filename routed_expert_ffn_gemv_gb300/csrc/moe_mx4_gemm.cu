@@ -39,6 +39,10 @@ namespace {
 
 // ------------------------------------------------------------------ workspace
 
+// Routes that every CTA groups for itself (LOCAL): beyond, its 512 threads take longer than two kernels
+// in front, and four rows to a TMA copy longer than rows laid out.
+#define MX4_LOCAL_R 1024
+
 struct GemmWs {
     int max_chunks;
     size_t o_rows, o_slot, o_pos, o_n, o_hist, ints;  // in ints; [0] is the number of chunks
@@ -267,6 +271,9 @@ struct GemmParams {
     int *status;
 };
 
+// (at most R / NT + E chunks)
+typedef Mx4Chunks<MX4_LOCAL_R, MX4_LOCAL_R / MXG_NT_SMALL + MOE_MAX_E> GemmChunks;
+
 // A ring stage and its scales in tensor memory share their index: a landed stage means that the MMAs
 // that read the scales' previous contents are done, so the scale slots need no wait of their own.
 // A stage lives about 3000 clocks (its copies, its scales, its MMAs): as many stages as fit.  Gate/up
@@ -280,7 +287,7 @@ struct GemmGeom {
     static constexpr int SFCOL = 2 * NT;                     // scales after the two accumulators, 24 columns a stage
     static constexpr int XCH = DOWN ? 8 * 16 * 36 * 4 : 4 * 2 * 2 * 4 * 32 * 4;
     static constexpr int O_XCH = 1024 + MXG_ITEMS * 16, O_ROWS = O_XCH + XCH, O_LOC = O_ROWS + 2 * NT * 8;
-    static constexpr int O_SC = (O_LOC + (int)sizeof(Mx4Chunks) + 15) / 16 * 16;
+    static constexpr int O_SC = (O_LOC + (int)sizeof(GemmChunks) + 15) / 16 * 16;
     static constexpr int O_RING = (O_SC + S * SSTAGE + 1023) / 1024 * 1024;
     static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
     static_assert(SFCOL + S * 24 <= 512 && STAGE % 1024 == 0 && O_LOC % 16 == 0 && SMEM <= 227 * 1024, "budget");
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     Item *items = (Item *)(smem + 1024);                  // [MXG_ITEMS]
     float *xch = (float *)(smem + G::O_XCH);              // gate/up [4 pairs][2][2 ways][4 routes][32], down [8][16][36]
     int2 *e_rows = (int2 *)(smem + G::O_ROWS);            // [2 accumulators][NT]: route, its weight's bits
-    Mx4Chunks &loc = *(Mx4Chunks *)(smem + G::O_LOC);     // LOCAL
+    GemmChunks &loc = *(GemmChunks *)(smem + G::O_LOC);   // LOCAL
     uint8_t *ring = smem + G::O_RING, *sring = smem + G::O_SC;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -344,7 +351,8 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_trigger();
-    if (LOCAL) mx4_local_chunks(loc, p.ids, p.R, p.E, p.table, p.n_slots, NT, p.status);
+    if (LOCAL)
+        mx4_local_chunks<MXG_THREADS>(loc, (uint16_t *)ring, p.ids, p.R, p.E, p.table, p.n_slots, NT, nullptr, p.status);
     const int *rows = LOCAL ? loc.rows : p.rows;
     const int MT = p.MT, n_items = (LOCAL ? loc.nch : p.ints[0]) * MT;
     // this CTA's items are blockIdx.x, + gridDim.x, ..; every role looks them up, and from global memory

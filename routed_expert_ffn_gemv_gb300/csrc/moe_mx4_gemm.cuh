@@ -15,85 +15,90 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 
 // ------------------------------------------------------------------ few routes: chunks by every CTA
 //
-// Up to MX4_LOCAL_R routes are grouped by expert by each CTA for itself in shared memory: thread r
-// compares route r with every other one (its rank among the routes of its expert, their number, the
-// first of them), a block-wide sum gives the experts' positions in the order of their first routes.
-// Everyone arrives at the same tables, without a kernel in front.
-#define MX4_LOCAL_R 256
-
-struct Mx4Chunks {
-    alignas(16) int id[MX4_LOCAL_R];                          // served expert of a route, or -1
-    int slot[MX4_LOCAL_R], pos[MX4_LOCAL_R], n[MX4_LOCAL_R];  // per chunk
-    int rows[MX4_LOCAL_R];                                    // position -> route
-    int base[MX4_LOCAL_R];                                    // of an expert, at its first route
-    int scan[MX4_LOCAL_R / 32];
+// Up to MAXR routes are grouped by expert by each CTA for itself in shared memory: a warp match ranks the
+// routes of each 32 among those of their expert, a thread per expert adds the 32s up, a block-wide sum
+// gives the experts' positions.  No atomics: every CTA arrives at the same tables (they share chunks), and
+// no kernel has to run in front.
+template <int MAXR, int MAXC>
+struct alignas(16) Mx4Chunks {
+    int rows[MAXR];                                           // position -> route
+    int slot[MAXC], pos[MAXC], n[MAXC];                       // per chunk
+    int eslot[MOE_MAX_E], off[MOE_MAX_E];                     // per expert: slot (or -1), first position
+    int sums[32];
     int nch;                                                  // chunks
 };
 
-// Called by every thread of a block of at least MX4_LOCAL_R; syncs the block.  Routes of -1 are not
-// served; ids outside [0, E) and slots outside [0, n_slots) are recorded and not served either.
-// Chunks of at most NR routes.  `table`: global or shared memory, or NULL.
-__device__ __forceinline__ void mx4_local_chunks(Mx4Chunks &c, const int32_t *ids, int R, int E, const int32_t *table,
-                                                 int n_slots, int NR, int *status) {
-    const int r = threadIdx.x, lane = r & 31, warp = r >> 5;
-    int id = -1, slot = -1;
-    if (r < MX4_LOCAL_R) {
-        if (r < R) {
-            id = ids[r];
-            bool bad = id != -1 && (id < 0 || id >= E);
-            if (!bad && id >= 0) {
-                slot = table ? table[id] : id;
-                bad = slot < 0 || slot >= n_slots;
-            }
-            if (bad) {
-                moe_set_status(status, MOE_ERR_INVALID);
-                id = -1;
-            }
+// Called by every thread of a block of NTHR (a multiple of 32, at least MOE_MAX_E and MAXR / 2); syncs the
+// block.  Routes of -1 are not served; ids outside [0, E) and slots outside [0, n_slots) are recorded and
+// not served either.  Chunks of at most NR routes.  `table`: global or shared memory, or NULL.  `scratch`:
+// shared, 2 * E bytes for every 32 of MAXR.  `served`: shared [MAXR], 1 for the routes that are, or NULL.
+template <int NTHR, int MAXR, int MAXC>
+__device__ __forceinline__ void mx4_local_chunks(Mx4Chunks<MAXR, MAXC> &c, uint16_t *scratch, const int32_t *ids, int R,
+                                                 int E, const int32_t *table, int n_slots, int NR, int *served,
+                                                 int *status) {
+    constexpr int PASSES = (MAXR + NTHR - 1) / NTHR;
+    static_assert(PASSES <= 2 && NTHR >= MOE_MAX_E && NTHR % 32 == 0, "threads");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = (R + 31) / 32;
+    int id[PASSES], rank[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int r = tid + i * NTHR;
+        id[i] = r < R ? ids[r] : -1;
+    }
+    if (tid < E) {
+        const int s = table ? table[tid] : tid;
+        c.eslot[tid] = s >= 0 && s < n_slots ? s : -1;
+    }
+    for (int i = tid; i < (groups * E + 1) / 2; i += NTHR) ((uint32_t *)scratch)[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int r = tid + i * NTHR;
+        if (id[i] != -1 && (id[i] < 0 || id[i] >= E || c.eslot[id[i]] < 0)) {
+            moe_set_status(status, MOE_ERR_INVALID);
+            id[i] = -1;
         }
-        c.id[r] = id;
+        const unsigned peers = __match_any_sync(0xffffffffu, id[i]);
+        rank[i] = __popc(peers & ((1u << lane) - 1));
+        if (id[i] >= 0 && rank[i] == 0) scratch[(r >> 5) * E + id[i]] = (uint16_t)__popc(peers);
+        if (served && r < R) served[r] = id[i] >= 0;
     }
     __syncthreads();
-    int cnt = 0, rank = 0, first = MX4_LOCAL_R, pk = 0, incl = 0;
-    if (r < MX4_LOCAL_R) {
-        if (id >= 0)
+    int total = 0;
+    if (tid < E)
 #pragma unroll 4
-            for (int q = 0; q < R; q += 4) {
-                const int4 v = *(const int4 *)&c.id[q];
-                const int w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool eq = w[i] == id;
-                    cnt += eq;
-                    rank += eq && q + i < r;
-                    first = min(first, eq ? q + i : MX4_LOCAL_R);
-                }
-            }
-        if (id >= 0 && rank == 0) pk = cnt | ((cnt + NR - 1) / NR) << 16;
-        incl = pk;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+        for (int g = 0; g < groups; ++g) {
+            const int v = scratch[g * E + tid];
+            scratch[g * E + tid] = (uint16_t)total;
+            total += v;
         }
-        if (lane == 31) c.scan[warp] = incl;
+    const int nc = (total + NR - 1) / NR, pk = total | nc << 16;
+    int incl = pk;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
     }
+    if (lane == 31) c.sums[warp] = incl;
     __syncthreads();
-    if (r < MX4_LOCAL_R) {
-        int b = incl - pk;
-        for (int w = 0; w < warp; ++w) b += c.scan[w];
-        if (r == MX4_LOCAL_R - 1) c.nch = (b + pk) >> 16;
-        if (pk) {
-            c.base[r] = b & 0xFFFF;
-            const int c0 = b >> 16, nc = pk >> 16;
-            for (int i = 0; i < nc; ++i) {  // near-equal chunks
-                const int lo = cnt * i / nc, hi = cnt * (i + 1) / nc;
-                c.slot[c0 + i] = slot;
-                c.pos[c0 + i] = (b & 0xFFFF) + lo;
-                c.n[c0 + i] = hi - lo;
-            }
+    int b = incl - pk;
+    for (int w = 0; w < warp; ++w) b += c.sums[w];
+    if (tid == NTHR - 1) c.nch = (b + pk) >> 16;
+    if (tid < E) {
+        c.off[tid] = b & 0xFFFF;
+        for (int i = 0; i < nc; ++i) {  // near-equal chunks
+            const int lo = total * i / nc, hi = total * (i + 1) / nc;
+            c.slot[(b >> 16) + i] = c.eslot[tid];
+            c.pos[(b >> 16) + i] = (b & 0xFFFF) + lo;
+            c.n[(b >> 16) + i] = hi - lo;
         }
     }
     __syncthreads();
-    if (id >= 0) c.rows[c.base[first] + rank] = r;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int r = tid + i * NTHR;
+        if (id[i] >= 0) c.rows[c.off[id[i]] + scratch[(r >> 5) * E + id[i]] + rank[i]] = r;
+    }
+    fence_proxy_async_smem();  // the scratch becomes part of a copy ring
     __syncthreads();
 }

@@ -47,9 +47,11 @@
 #define MXL_WBYTES (2 * MX4_TB)
 
 static_assert(MXL_PREP_THREADS == MOE_MAX_E, "a thread per expert");
-static_assert(MXL_MAX_R <= MX4_LOCAL_R, "a CTA groups the routes itself");
 
 namespace {
+
+// (a chunk holds a route at least)
+typedef Mx4Chunks<MXL_MAX_R, MXL_MAX_R> LayerChunks;
 
 struct LayerWs {
     size_t ctr, ids, weights, xscale, xq, hq, partial, total;
@@ -323,9 +325,11 @@ struct LayerGeom {
     static constexpr int N = NR * 8;
     static constexpr int SFCOL = 2 * N;      // scales after the two accumulators, 16 columns a stage
     static constexpr int MAXS = 10;
-    static constexpr int CTRL = (1024 + 2 * 4 * NR * 32 * 4 + (int)sizeof(Mx4Chunks) + MXL_MAX_R * 4 +
+    static constexpr int CTRL = (1024 + 2 * 4 * NR * 32 * 4 + (int)sizeof(LayerChunks) + 2 * MXL_MAX_R * 4 +
                                  MOE_DECODE_MAX_T * 8 + MOE_MAX_E * 4 + 1023) / 1024 * 1024;
     static_assert(SFCOL + MAXS * 16 <= 512, "tensor memory");
+    static_assert(sizeof(LayerChunks) % 16 == 0 && 2 * 4 * NR * 32 * 4 % 16 == 0 && MXL_MAX_R * 4 % 16 == 0,
+                  "the control block's arrays follow one another on 16-byte boundaries");
 };
 
 __device__ __forceinline__ int ld_acquire_gpu(const int *a) {
@@ -364,9 +368,9 @@ __device__ __forceinline__ Unit unit_unpack(int v) {
     return v < 0 ? Unit{MXL_NONE, 0, 0} : Unit{v >> 28, (v >> 20) & 0xFF, v & 0xFFFFF};
 }
 
-// y[t][columns of tile m] = extra + the partial rows of token t's routes, in route order (`id` -1: not
-// computed), for eight tokens by 128 threads: four columns of a token to a thread.
-__device__ __forceinline__ void combine_tile(const FfnParams &p, int m, int t0, int thr, const int *id) {
+// y[t][columns of tile m] = extra + the partial rows of token t's routes, in route order (`on`: routes
+// that were computed), for eight tokens by 128 threads: four columns of a token to a thread.
+__device__ __forceinline__ void combine_tile(const FfnParams &p, int m, int t0, int thr, const int *on) {
     const int o = 128 * m + 4 * (thr & 31);
     if (o >= p.H) return;
 #pragma unroll
@@ -376,7 +380,7 @@ __device__ __forceinline__ void combine_tile(const FfnParams &p, int m, int t0, 
         float4 v[MOE_MAX_K];
 #pragma unroll
         for (int j = 0; j < MOE_MAX_K; ++j)
-            v[j] = j < p.k && id[t * p.k + j] >= 0 ? __ldcg((const float4 *)(p.partial + (size_t)(t * p.k + j) * p.H + o))
+            v[j] = j < p.k && on[t * p.k + j] ? __ldcg((const float4 *)(p.partial + (size_t)(t * p.k + j) * p.H + o))
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         const size_t at = (size_t)t * p.H + o;
@@ -429,8 +433,9 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
     volatile int *q_unit = (volatile int *)(tmem_slot + 2);  // [MXL_Q]
     static_assert((3 * G::MAXS + 4 + 2 * MXL_Q + MXL_PUB + 2) * 8 + (2 + MXL_Q) * 4 <= 1024, "barriers");
     float *xch = (float *)(smem + 1024);                     // [2 buffers][2 pairs][gate, up][NR][32]
-    Mx4Chunks &ch = *(Mx4Chunks *)(xch + 2 * 4 * NR * 32);
-    float *s_w = (float *)(&ch + 1);                         // [MXL_MAX_R] router weights
+    LayerChunks &ch = *(LayerChunks *)(xch + 2 * 4 * NR * 32);
+    int *s_on = (int *)(&ch + 1);                            // [MXL_MAX_R] whether a route is computed
+    float *s_w = (float *)(s_on + MXL_MAX_R);                // [MXL_MAX_R] router weights
     float2 *s_xs = (float2 *)(s_w + MXL_MAX_R);              // [MOE_DECODE_MAX_T]
     int *s_table = (int *)(s_xs + MOE_DECODE_MAX_T);         // [MOE_MAX_E]
     uint8_t *xres = smem + G::CTRL;
@@ -480,7 +485,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
     if (tid < R) s_w[tid] = p.weights[tid];
     if (tid < p.T) s_xs[tid] = p.xscale[tid];
     tc_fence_before();
-    mx4_local_chunks(ch, p.ids, R, p.E, p.table ? s_table : nullptr, p.n_slots, NR, p.status);
+    mx4_local_chunks<MXL_THREADS>(ch, (uint16_t *)ring, p.ids, R, p.E, p.table ? s_table : nullptr, p.n_slots, NR, s_on,
+                                  p.status);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int nch = ch.nch;
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
         if (tid == 0 && p.res) mbar_wait_role(x_full, 0, p.status, abort_flag);
         for (int m = blockIdx.x; m < HT; m += gridDim.x)
             if (tid < 128)
-                for (int t = 0; t < p.T; t += 8) combine_tile(p, m, t, tid, ch.id);
+                for (int t = 0; t < p.T; t += 8) combine_tile(p, m, t, tid, s_on);
     } else if (warp == 0) {
         // ---------------- claims and weights; a stage's barrier expects its digits' bytes too
         {
@@ -705,7 +711,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
             else if (un.kind < MXL_COMBINE) ok = mbar_wait_role(&acc_full[i & 1], (i / 2) & 1, p.status, abort_flag);
             if (!bar_and_n(1, 128, ok) || un.kind == MXL_NONE) break;
             if (un.kind == MXL_COMBINE) {
-                combine_tile(p, un.m, 8 * un.c, ew, ch.id);
+                combine_tile(p, un.m, 8 * un.c, ew, s_on);
                 continue;
             }
             tc_fence_after();
