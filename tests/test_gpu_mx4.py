@@ -430,7 +430,8 @@ class Layer:
 
 
 LAYERS = [(1, 32, 32, 1, 1), (1, 256, 512, 8, 2), (2, 96, 160, 5, 3), (8, 288, 192, 16, 8), (9, 128, 64, 3, 2),
-          (32, 160, 96, 40, 4), (32, 64, 32, 2, 2), (17, 256, 128, 256, 8), (1, 2048, 768, 16, 8), (3, 1024, 1408, 4, 2)]
+          (32, 160, 96, 40, 4), (32, 64, 32, 2, 2), (17, 256, 128, 256, 8), (32, 128, 64, 256, 8), (32, 96, 64, 4, 4),
+          (8, 4096, 32, 2, 1), (7, 4096, 160, 3, 2), (1, 2048, 768, 16, 8), (3, 1024, 1408, 4, 2)]
 
 
 @pytest.mark.parametrize("xtype", ["f32", "bf16"])
@@ -453,6 +454,35 @@ def test_layer_optional_arguments_and_aliased_output():
     z = l.extra.clone()
     l.run(y=z, extra=z)
     assert torch.equal(y, z)
+
+
+def test_layer_unaligned_router_and_tokens():
+    """Router weights and tokens on element boundaries only."""
+    l = Layer(5, 160, 96, 16, 3, seed=13, xtype="bf16")
+    y, ids, w = l.run()
+    l.check(y, ids, w)
+    wr, x = l.d_wr, l.x
+    l.d_wr = torch.cat([wr.new_zeros(1), wr.reshape(-1)])[1:]
+    l.x = torch.cat([x.new_zeros(1), x.reshape(-1)])[1:].reshape(x.shape)
+    assert l.d_wr.data_ptr() % 16 and l.x.data_ptr() % 16
+    y2, ids2, w2 = l.run()
+    assert torch.equal(ids, ids2)
+    l.check(y2, ids2, w2)
+
+
+def test_layer_equal_logits_go_to_the_lower_expert():
+    l = Layer(3, 128, 64, 40, 8, seed=14, bias=False, extra=False)
+    l.d_wr.zero_()
+    l.wr = np.zeros_like(l.wr)
+    y, ids, w = l.run()
+    assert ids.tolist() == [list(range(8))] * 3
+    assert torch.allclose(w, torch.full_like(w, 0.125), rtol=2 ** -22, atol=0)
+    l.bias = np.zeros(40, np.float32)
+    l.bias[[39, 7, 20]] = 1.0
+    l.bias[5] = -0.0
+    y, ids, w = l.run()
+    assert ids.tolist() == [[7, 20, 39, 0, 1, 2, 3, 4]] * 3
+    l.check(y, ids, w)
 
 
 @pytest.mark.parametrize("gain", [1e-18, 1e-6, 1e6, 1e18])
