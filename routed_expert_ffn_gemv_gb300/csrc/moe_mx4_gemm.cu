@@ -225,26 +225,34 @@ mx4_place_kernel(const int32_t *__restrict__ ids, int R, int E, const int32_t *_
             s_src[tid] = r / div;
         }
         __syncthreads();
-        // a warp takes eight rows.  Codes: lane l piece l % 8 of a stage of row l / 8 (and + 4)
-        const int j = lane & 7;
+        // a warp takes eight rows.  Codes: lane l piece l % 8 of a stage of rows l / 8 and l / 8 + 4, four
+        // stages at a time, every load before the first store (the copies are all latency)
+        const int j = lane & 7, ka = 8 * warp + (lane >> 3), at[2] = {s_pos[ka], s_pos[ka + 4]};
+        const uint8_t *src[2] = {codes + (size_t)s_src[ka] * (K / 2) + 16 * j, codes + (size_t)s_src[ka + 4] * (K / 2) + 16 * j};
+        const int ks = 8 * warp + (lane >> 2), ats = s_pos[ks];
+        const uint8_t *srcs = scales + (size_t)s_src[ks] * KS;
+#pragma unroll 1
+        for (int q0 = 0; q0 < NKS; q0 += 4) {
+            uint4 v[2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = 8 * warp + 4 * i + (lane >> 3), at = s_pos[k];
-            if (at >= 0) {
-                const uint8_t *src = codes + (size_t)s_src[k] * (K / 2);
-                uint8_t *dst = xg + (size_t)at * 128 + ((j ^ (at & 7)) << 4);
-#pragma unroll 8
-                for (int q = 0; q < NKS; ++q) {
-                    const int col = 128 * q + 16 * j;  // bytes into the code row
-                    *(uint4 *)(dst + (size_t)q * Rp * 128) = col < K / 2 ? *(const uint4 *)(src + col) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[i][q] = make_uint4(0, 0, 0, 0);
+                    if (at[i] >= 0 && 128 * (q0 + q) + 16 * j < K / 2) v[i][q] = *(const uint4 *)(src[i] + 128 * (q0 + q));
                 }
-            }
+            // scales: lane l stage l % 4 of row l / 4
+            const int qs = q0 + (lane & 3);
+            const bool has = ats >= 0 && qs < NKS;
+            const uint2 sc = has ? scale8(srcs, qs, KS) : make_uint2(0, 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (at[i] >= 0 && q0 + q < NKS)
+                        *(uint4 *)(xg + ((size_t)(q0 + q) * Rp + at[i]) * 128 + ((j ^ (at[i] & 7)) << 4)) = v[i][q];
+            if (has) *(uint2 *)(sg + ((size_t)qs * Rp + ats) * 8) = sc;
         }
-        // scales: lane l stages l % 4, + 4, .. of row l / 4
-        const int k = 8 * warp + (lane >> 2), at = s_pos[k];
-        if (at >= 0)
-            for (int q = lane & 3; q < NKS; q += 4)
-                *(uint2 *)(sg + ((size_t)q * Rp + at) * 8) = scale8(scales + (size_t)s_src[k] * KS, q, KS);
         __syncthreads();
     }
 }
