@@ -69,10 +69,16 @@ GemmWs gemm_ws(int T, int H, int F, int E, int k, int NT) {
     return L;
 }
 
-// Most routes of a chunk.
+// Most routes of a chunk: a few where experts have few (more stages in the ring), else as wide as tensor
+// and shared memory allow, which is less beside the tables of LOCAL.  The larger saves passes over the
+// weights: 32768 routes over 128 experts are 241 chunks of at most 176, 227 of at most 192.
 #define MXG_NT_SMALL 32
-#define MXG_NT_LARGE 176
-int chunk_routes(int T, int E, int k) { return (long)T * k <= 16L * E ? MXG_NT_SMALL : MXG_NT_LARGE; }
+#define MXG_NT_LOCAL 176
+#define MXG_NT_LARGE 192
+int chunk_routes(int T, int E, int k) {
+    const long R = (long)T * k;
+    return R <= 16L * E ? MXG_NT_SMALL : R <= MX4_LOCAL_R ? MXG_NT_LOCAL : MXG_NT_LARGE;
+}
 
 // ------------------------------------------------------------------ routes by expert
 
@@ -286,16 +292,16 @@ typedef Mx4Chunks<MX4_LOCAL_R, MX4_LOCAL_R / MXG_NT_SMALL + MOE_MAX_E> GemmChunk
 // that read the scales' previous contents are done, so the scale slots need no wait of their own.
 // A stage lives about 3000 clocks (its copies, its scales, its MMAs): as many stages as fit.  Gate/up
 // exchanges eight routes at a time, down (three stages an item, its epilogue the longer part) 16.
-template <int NT, bool DOWN>
+template <int NT, bool DOWN, bool LOCAL>
 struct GemmGeom {
     static constexpr int NI = (NT + 31) / 32;                // 32-route groups
     static constexpr int STAGE = MXG_WBYTES + NT * 128;      // weights, code rows
     static constexpr int SSTAGE = NI * 256;                  // scales of the rows
-    static constexpr int S = NT == MXG_NT_LARGE ? (DOWN ? 4 : 5) : (DOWN ? 8 : 9);  // ring stages
+    static constexpr int S = NT > MXG_NT_SMALL ? (DOWN ? 4 : 5) : (DOWN ? 8 : 9);  // ring stages
     static constexpr int SFCOL = 2 * NT;                     // scales after the two accumulators, 24 columns a stage
     static constexpr int XCH = DOWN ? 8 * 16 * 36 * 4 : 4 * 2 * 2 * 4 * 32 * 4;
     static constexpr int O_XCH = 1024 + MXG_ITEMS * 16, O_ROWS = O_XCH + XCH, O_LOC = O_ROWS + 2 * NT * 8;
-    static constexpr int O_SC = (O_LOC + (int)sizeof(GemmChunks) + 15) / 16 * 16;
+    static constexpr int O_SC = (O_LOC + (LOCAL ? (int)sizeof(GemmChunks) : 0) + 15) / 16 * 16;
     static constexpr int O_RING = (O_SC + S * SSTAGE + 1023) / 1024 * 1024;
     static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
     static_assert(SFCOL + S * 24 <= 512 && STAGE % 1024 == 0 && O_LOC % 16 == 0 && SMEM <= 227 * 1024, "budget");
@@ -316,7 +322,7 @@ __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, i
 // LOCAL: few routes, grouped by the CTA itself; otherwise mx4_place_kernel's tables.
 template <int NT, bool DOWN, int OT, bool LOCAL>
 __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_constant__ GemmParams p) {
-    using G = GemmGeom<NT, DOWN>;
+    using G = GemmGeom<NT, DOWN, LOCAL>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     uint64_t *s_full = (uint64_t *)smem;
@@ -677,7 +683,7 @@ int encode_codes_map(const uint8_t *codes, long rows, int K, CUtensorMap *map) {
 
 template <int NT, bool DOWN, int OT, bool LOCAL>
 int launch_gemm_t(const GemmParams &p, int max_chunks, cudaStream_t s) {
-    using G = GemmGeom<NT, DOWN>;
+    using G = GemmGeom<NT, DOWN, LOCAL>;
     static std::mutex mu;
     static int sms[64] = {0};
     int dev = -1;
@@ -704,10 +710,10 @@ int launch_gemm_t(const GemmParams &p, int max_chunks, cudaStream_t s) {
 template <bool DOWN, int OT>
 int launch_gemm(const GemmParams &p, int NT, int max_chunks, cudaStream_t s) {
     if (p.R <= MX4_LOCAL_R)
-        return NT == MXG_NT_LARGE ? launch_gemm_t<MXG_NT_LARGE, DOWN, OT, true>(p, max_chunks, s)
-                                  : launch_gemm_t<MXG_NT_SMALL, DOWN, OT, true>(p, max_chunks, s);
-    return NT == MXG_NT_LARGE ? launch_gemm_t<MXG_NT_LARGE, DOWN, OT, false>(p, max_chunks, s)
-                              : launch_gemm_t<MXG_NT_SMALL, DOWN, OT, false>(p, max_chunks, s);
+        return NT == MXG_NT_SMALL ? launch_gemm_t<MXG_NT_SMALL, DOWN, OT, true>(p, max_chunks, s)
+                                  : launch_gemm_t<MXG_NT_LOCAL, DOWN, OT, true>(p, max_chunks, s);
+    return NT == MXG_NT_SMALL ? launch_gemm_t<MXG_NT_SMALL, DOWN, OT, false>(p, max_chunks, s)
+                              : launch_gemm_t<MXG_NT_LARGE, DOWN, OT, false>(p, max_chunks, s);
 }
 
 int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, int H, int F, int E, int k,
