@@ -209,19 +209,17 @@ def _ck(fn: str, rc: int) -> int:
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
     return t.data_ptr()
 
 
 def _stream(s) -> Optional[int]:
+    if s.__class__ is int:
+        return s
     if s is None:
         import torch
         return torch.cuda.current_stream().cuda_stream
-    if isinstance(s, int):
-        return s
     return s.cuda_stream
 
 

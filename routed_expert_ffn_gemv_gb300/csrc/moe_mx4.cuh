@@ -24,17 +24,29 @@ __device__ __forceinline__ int e8m0_of_amax(uint32_t amax_bits) {
 // power of two with an exact product wherever the result is not far below the smallest code).
 __device__ __forceinline__ float e8m0_inverse(int s) { return e8m0_value(254 - s); }
 
-// Two floats to E2M1 codes, nearest even, saturating at 6: lo in the low nibble.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// Eight floats to E2M1 codes, nearest even, saturating at 6: element i at bits 4i.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
     uint32_t r;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
 }
-// Values of the two codes of a byte.
-__device__ __forceinline__ float2 e2m1x2_value(uint32_t codes) {
-    uint32_t h;
-    asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(codes));
-    return __half22float2(*(const __half2 *)&h);
+// Values of eight codes, two to a half2.
+__device__ __forceinline__ void e2m1x8_value(uint32_t codes, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
 }
 
 // Eight consecutive elements as they are stored (wide loads where `wide`), as floats, and back.
@@ -138,16 +150,17 @@ __device__ __forceinline__ uint32_t mx4_quant8(const Raw8<XT> &r, int &scale) {
     const float inv = e8m0_inverse(scale);
     float v[8];
     raw8_floats<XT>(r, v);
-    uint32_t c[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = e2m1x2(v[2 * j] * inv, v[2 * j + 1] * inv);
-    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    for (int j = 0; j < 8; ++j) v[j] *= inv;
+    return e2m1x8(v);
 }
 __device__ __forceinline__ void mx4_dequant8(uint32_t codes, int scale, float (&v)[8]) {
     const float m = e8m0_value(scale);
+    uint32_t h[4];
+    e2m1x8_value(codes, h);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float2 f = e2m1x2_value(codes >> (8 * j));
+        const float2 f = __half22float2(*(const __half2 *)&h[j]);
         v[2 * j] = f.x * m;
         v[2 * j + 1] = f.y * m;
     }

@@ -49,8 +49,41 @@ __device__ __forceinline__ void mx4_local_chunks(Mx4Chunks<MAXR, MAXC> &c, uint1
         const int s = table ? table[tid] : tid;
         c.eslot[tid] = s >= 0 && s < n_slots ? s : -1;
     }
-    for (int i = tid; i < (groups * E + 1) / 2; i += NTHR) ((uint32_t *)scratch)[i] = 0;
+    if (groups > 1)
+        for (int i = tid; i < (groups * E + 1) / 2; i += NTHR) ((uint32_t *)scratch)[i] = 0;
     __syncthreads();
+    if (groups <= 1) {
+        // a warp's worth of routes: its first warp does it all, experts in the order of their first routes
+        if (warp == 0) {
+            if (id[0] != -1 && (id[0] < 0 || id[0] >= E || c.eslot[id[0]] < 0)) {
+                moe_set_status(status, MOE_ERR_INVALID);
+                id[0] = -1;
+            }
+            const unsigned peers = __match_any_sync(0xffffffffu, id[0]);
+            const int cnt = __popc(peers), head = __ffs(peers) - 1, nc = (cnt + NR - 1) / NR;
+            const bool lead = id[0] >= 0 && head == lane;
+            int incl = lead ? cnt | nc << 16 : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const int b = incl - (lead ? cnt | nc << 16 : 0), pos = b & 0xFFFF;
+            if (lead)
+                for (int i = 0; i < nc; ++i) {  // near-equal chunks
+                    const int lo = cnt * i / nc, hi = cnt * (i + 1) / nc;
+                    c.slot[(b >> 16) + i] = c.eslot[id[0]];
+                    c.pos[(b >> 16) + i] = pos + lo;
+                    c.n[(b >> 16) + i] = hi - lo;
+                }
+            const int start = __shfl_sync(0xffffffffu, pos, head);
+            if (id[0] >= 0) c.rows[start + __popc(peers & ((1u << lane) - 1))] = lane;
+            if (served && lane < R) served[lane] = id[0] >= 0;
+            if (lane == 31) c.nch = incl >> 16;
+        }
+        __syncthreads();
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
         const int r = tid + i * NTHR;

@@ -71,7 +71,7 @@ def test_quantise_borders_and_non_finite_blocks(xtype):
 
 @pytest.mark.parametrize("xtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,cols,pad,off", [(1, 32, 0, 0), (3, 96, 8, 0), (17, 160, 5, 0), (5, 2048, 1, 1), (700, 64, 3, 1),
-                                               (257, 224, 32, 8)])
+                                               (257, 224, 32, 8), (2440, 1056, 5, 1)])
 def test_quantise_rows_strides_and_alignment(rows, cols, pad, off, xtype):
     rng = np.random.default_rng(rows + cols)
     ld = cols + pad
@@ -86,6 +86,26 @@ def test_quantise_rows_strides_and_alignment(rows, cols, pad, off, xtype):
     v = back[off:].reshape(rows, ld).double().cpu().numpy()
     np.testing.assert_array_equal(v[:, :cols], ref.values(rc, rs))
     assert (v[:, cols:] == 7.0).all()
+
+
+@pytest.mark.slow
+def test_quantise_past_32_bit_offsets():
+    """2^31 groups of eight columns and some: the same codes as of its two halves."""
+    rows, cols = (1 << 21) + 6, 8192
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    codes, scales = quantise_gpu(x, "bf16")
+    half = rows // 2
+    for part in (slice(0, half), slice(half, rows)):
+        c, s = quantise_gpu(x[part], "bf16")
+        assert torch.equal(codes[part], c) and torch.equal(scales[part], s)
+        del c, s
+    tail = x[-2:].double().cpu().numpy()
+    y = x  # the values take the tokens' place
+    L.moe_mx4_dequantize(codes, scales, rows, cols, y, L.MOE_BF16, cols)
+    np.testing.assert_array_equal(y[-2:].double().cpu().numpy(), ref.values(*ref.quantise(tail)))
+    z = torch.empty(rows - half, cols, dtype=torch.bfloat16, device="cuda")
+    L.moe_mx4_dequantize(codes[half:], scales[half:], rows - half, cols, z, L.MOE_BF16, cols)
+    assert torch.equal(y[half:], z)
 
 
 def quantise_gpu_view(x, cols, ld, xtype):
