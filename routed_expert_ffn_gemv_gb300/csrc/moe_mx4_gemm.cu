@@ -803,6 +803,7 @@ extern "C" int moe_mx4_expert_gateup(const uint8_t *x_codes, const uint8_t *x_sc
     if (T == 0) return MOE_OK;
     MOE_CHECK(x_codes && x_scales && ids && h && workspace && ws_bytes >= need);
     MOE_CHECK(((uintptr_t)x_codes & 15) == 0 && ((uintptr_t)workspace & 255) == 0);
+    MOE_CHECK(((uintptr_t)h & (htype == MOE_BF16 ? 1 : 3)) == 0);
     if ((rc = mx4_pool_check(H, F, n_slots, pool, slot_bytes)) != MOE_OK) return rc;
     return run_product(false, x_codes, x_scales, T, H, F, E, k, ids, nullptr, d_slot_table, n_slots, pool, slot_bytes,
                        h, htype, workspace, moe_cuda_stream(s));

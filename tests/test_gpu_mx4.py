@@ -384,6 +384,16 @@ def test_prompt_chain_and_pool():
     assert torch.allclose(y.double(), want, rtol=(k + 1) * 2 ** -24 * 4, atol=1e-5)
     L.moe_cache_release(cache)
     torch.cuda.synchronize()
+    # a stack's kernels read other images: such a pool is refused
+    wr = torch.zeros(H, E, dtype=torch.float16, device="cuda")
+    wsb = L.moe_stack_workspace(H, F, L.MOE_Q8_0, E, k, 1, 0)
+    sws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    stack = L.StackDesc(qtype=L.MOE_Q8_0, H=H, F=F, E=E, k=k, n_layers=1, n_shared=0,
+                        w_router=(ctypes.c_void_p * 1)(wr.data_ptr()), n_groups=1,
+                        caches=(ctypes.c_void_p * 1)(cache), slot_bytes=1 << 20, max_T=1, workspace=sws.data_ptr(),
+                        ws_bytes=wsb)
+    out = ctypes.c_void_p()
+    assert L.load().moe_stack_create(ctypes.byref(stack), ctypes.byref(out)) == L.MOE_ERR_UNSUPPORTED
     desc.device_managed = 1
     out = ctypes.c_void_p()
     assert L.load().moe_cache_create(ctypes.byref(desc), ctypes.byref(out)) == L.MOE_ERR_UNSUPPORTED

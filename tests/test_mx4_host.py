@@ -123,6 +123,7 @@ def test_product_and_layer_refusals(lib):
         for kw in (dict(xs=None), dict(ids=None), dict(x=p + 8), dict(T=(1 << 23) + 1)):
             assert f(**kw) == bad, (f.__name__, kw)
     assert gu(t=2) == bad and dn(w=None) == bad and dn(h=p + 4) == bad
+    assert gu(h=p + 2) == bad and gu(h=p + 1, t=1) == bad
     assert ly(t=2) == bad and ly(wr=None) == bad and ly(T=33) == bad
     out = ctypes.c_size_t()
     assert lib.moe_mx4_expert_workspace(1, 128, 64, 4, 2, None) == bad
