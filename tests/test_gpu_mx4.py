@@ -527,6 +527,20 @@ def test_layer_scales_of_x(gain):
     l.check(y, ids, w)
 
 
+def test_layer_subnormal_tokens_and_overflowing_h():
+    l = Layer(4, 128, 96, 6, 3, seed=4, extra=True)
+    l.bias = np.arange(6, dtype=np.float32) * 8
+    l.d_wr.zero_()
+    x = l.x.clone()
+    l.x = x * 1e-41
+    y, ids, w = l.run()
+    assert torch.equal(y, l.extra)  # products of two such values are zero
+    l.x = x * 1e30
+    y, ids, w = l.run()
+    assert bool(torch.isnan(y).all())
+    assert L.moe_device_status() == 0
+
+
 def test_layer_zero_and_non_finite_tokens():
     l = Layer(6, 128, 96, 4, 2, seed=6, extra=False)
     ok, ids0, w0 = l.run()
