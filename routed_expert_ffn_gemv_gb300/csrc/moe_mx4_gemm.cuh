@@ -21,14 +21,14 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // no kernel has to run in front.
 template <int MAXR, int MAXC>
 struct alignas(16) Mx4Chunks {
-    int rows[MAXR];                                           // position -> route
+    uint16_t rows[MAXR];                                      // position -> route
     int slot[MAXC], pos[MAXC], n[MAXC];                       // per chunk
     int eslot[MOE_MAX_E], off[MOE_MAX_E];                     // per expert: slot (or -1), first position
     int sums[32];
     int nch;                                                  // chunks
 };
 
-// Called by every thread of a block of NTHR (a multiple of 32, at least MOE_MAX_E and MAXR / 2); syncs the
+// Called by every thread of a block of NTHR (a multiple of 32, at least MOE_MAX_E and MAXR / 4); syncs the
 // block.  Routes of -1 are not served; ids outside [0, E) and slots outside [0, n_slots) are recorded and
 // not served either.  Chunks of at most NR routes.  `table`: global or shared memory, or NULL.  `scratch`:
 // shared, 2 * E bytes for every 32 of MAXR.  `served`: shared [MAXR], 1 for the routes that are, or NULL.
@@ -37,7 +37,7 @@ __device__ __forceinline__ void mx4_local_chunks(Mx4Chunks<MAXR, MAXC> &c, uint1
                                                  int E, const int32_t *table, int n_slots, int NR, int *served,
                                                  int *status) {
     constexpr int PASSES = (MAXR + NTHR - 1) / NTHR;
-    static_assert(PASSES <= 2 && NTHR >= MOE_MAX_E && NTHR % 32 == 0, "threads");
+    static_assert(PASSES <= 4 && NTHR >= MOE_MAX_E && NTHR % 32 == 0, "threads");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, groups = (R + 31) / 32;
     int id[PASSES], rank[PASSES];
 #pragma unroll
@@ -77,7 +77,7 @@ __device__ __forceinline__ void mx4_local_chunks(Mx4Chunks<MAXR, MAXC> &c, uint1
                     c.n[(b >> 16) + i] = hi - lo;
                 }
             const int start = __shfl_sync(0xffffffffu, pos, head);
-            if (id[0] >= 0) c.rows[start + __popc(peers & ((1u << lane) - 1))] = lane;
+            if (id[0] >= 0) c.rows[start + __popc(peers & ((1u << lane) - 1))] = (uint16_t)lane;
             if (served && lane < R) served[lane] = id[0] >= 0;
             if (lane == 31) c.nch = incl >> 16;
         }
@@ -130,7 +130,7 @@ __device__ __forceinline__ void mx4_local_chunks(Mx4Chunks<MAXR, MAXC> &c, uint1
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
         const int r = tid + i * NTHR;
-        if (id[i] >= 0) c.rows[c.off[id[i]] + scratch[(r >> 5) * E + id[i]] + rank[i]] = r;
+        if (id[i] >= 0) c.rows[c.off[id[i]] + scratch[(r >> 5) * E + id[i]] + rank[i]] = (uint16_t)r;
     }
     fence_proxy_async_smem();  // the scratch becomes part of a copy ring
     __syncthreads();

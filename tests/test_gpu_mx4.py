@@ -242,8 +242,8 @@ def test_products_against_64_bits(T, H, F, E, k, htype):
     assert L.moe_device_status() == 0
 
 
-@pytest.mark.parametrize("n", [1, 7, 8, 9, 127, 128, 129, 175, 176, 177, 255, 256, 257, 513, 1000, 1023, 1024, 1025, 1500,
-                               2113])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 127, 128, 129, 175, 176, 177, 255, 256, 257, 513, 1000, 1024, 1025, 2047, 2048,
+                               2049, 2113])
 def test_one_expert_takes_every_route(n):
     """Group lengths around every tile border; the other experts are empty."""
     ids = np.full((n, 1), 2, np.int32)
@@ -269,7 +269,8 @@ def test_dropped_routes_repeats_and_slot_table():
     assert L.moe_device_status() == 0
 
 
-@pytest.mark.parametrize("T,k,E", [(300, 4, 5), (1031, 1, 256), (515, 8, 16), (129, 8, 129)])
+@pytest.mark.parametrize("T,k,E", [(300, 4, 5), (1031, 1, 256), (515, 8, 16), (129, 8, 129), (257, 8, 9),
+                                   (700, 3, 130)])
 def test_many_routes_dropped_and_repeated(T, k, E):
     """More routes than a CTA groups for itself, over few and over many experts, some unused."""
     rng = np.random.default_rng(T)
@@ -281,7 +282,7 @@ def test_many_routes_dropped_and_repeated(T, k, E):
     assert L.moe_device_status() == 0
 
 
-@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("T", [1, 40, 300, 600])
 def test_ids_and_slots_out_of_range_are_reported_and_skipped(T):
     k, E = 4, 6
     ids = np.tile(np.array([[0, E, -7, 3]], np.int32), (T, 1))
