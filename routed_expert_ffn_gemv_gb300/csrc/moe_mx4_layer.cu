@@ -875,6 +875,7 @@ extern "C" int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int 
     MOE_CHECK(xtype == MOE_F32 || xtype == MOE_BF16);
     if (T == 0) return MOE_OK;
     MOE_CHECK(x && w_router && y && workspace && ws_bytes >= need && ((uintptr_t)workspace & 255) == 0);
+    MOE_CHECK(((uintptr_t)x & (xtype == MOE_BF16 ? 1 : 3)) == 0);
     if ((rc = mx4_pool_check(H, F, n_slots, pool, slot_bytes)) != MOE_OK) return rc;
     const LayerWs L = layer_ws(T, H, F, k);
     uint8_t *w = (uint8_t *)workspace;

@@ -129,3 +129,12 @@ def test_product_and_layer_refusals(lib):
     assert lib.moe_mx4_expert_workspace(1, 128, 64, 4, 2, None) == bad
     assert lib.moe_mx4_layer_workspace(33, 128, 64, 4, 2, ctypes.byref(out)) == bad
     assert lib.moe_mx4_layer_workspace(32, 128, 64, 4, 2, ctypes.byref(out)) == L.MOE_OK and out.value > 0
+
+
+def test_layer_refuses_tokens_off_their_elements(lib):
+    b = aligned(4096)
+    p = b.ctypes.data
+    sb = ref.slot_bytes(128, 64)
+    for t, x in ((L.MOE_F32, p + 2), (L.MOE_F32, p + 1), (L.MOE_BF16, p + 1)):
+        assert lib.moe_mx4_layer(x, t, 1, 128, 64, 4, 2, p, None, None, 4, p, sb, None, p, None, None, p, 1 << 40,
+                                 None) == L.MOE_ERR_INVALID, (t, x - p)
