@@ -877,6 +877,8 @@ extern "C" int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int 
     MOE_CHECK(x && w_router && y && workspace && ws_bytes >= need && ((uintptr_t)workspace & 255) == 0);
     MOE_CHECK(((uintptr_t)x & (xtype == MOE_BF16 ? 1 : 3)) == 0);
     if ((rc = mx4_pool_check(H, F, n_slots, pool, slot_bytes)) != MOE_OK) return rc;
+    // a unit travels in a word with 20 bits for its tile (H stays far below by the router's shared memory)
+    if ((F + 63L) / 64 > 1 << 20) return MOE_ERR_UNSUPPORTED;
     const LayerWs L = layer_ws(T, H, F, k);
     uint8_t *w = (uint8_t *)workspace;
     cudaStream_t st = moe_cuda_stream(s);

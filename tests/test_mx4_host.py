@@ -138,3 +138,12 @@ def test_layer_refuses_tokens_off_their_elements(lib):
     for t, x in ((L.MOE_F32, p + 2), (L.MOE_F32, p + 1), (L.MOE_BF16, p + 1)):
         assert lib.moe_mx4_layer(x, t, 1, 128, 64, 4, 2, p, None, None, 4, p, sb, None, p, None, None, p, 1 << 40,
                                  None) == L.MOE_ERR_INVALID, (t, x - p)
+
+
+def test_layer_refuses_more_tiles_than_a_unit_numbers(lib):
+    b = aligned(4096)
+    p = b.ctypes.data
+    F = (1 << 26) + 32
+    sb = (ref.slot_bytes(32, F) + 255) // 256 * 256
+    assert lib.moe_mx4_layer(p, L.MOE_F32, 1, 32, F, 4, 2, p, None, None, 4, p, sb, None, p, None, None, p, 1 << 40,
+                             None) == L.MOE_ERR_UNSUPPORTED
