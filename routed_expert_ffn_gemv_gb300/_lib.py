@@ -211,7 +211,7 @@ def _ck(fn: str, rc: int) -> int:
 def _ptr(t) -> Optional[int]:
     if t is None or t.__class__ is int:
         return t
-    return t.data_ptr()
+    return int(t) if isinstance(t, int) else t.data_ptr()
 
 
 def _stream(s) -> Optional[int]:
@@ -220,7 +220,7 @@ def _stream(s) -> Optional[int]:
     if s is None:
         import torch
         return torch.cuda.current_stream().cuda_stream
-    return s.cuda_stream
+    return int(s) if isinstance(s, int) else s.cuda_stream
 
 
 # ------------------------------------------------------------------------------ entry points
