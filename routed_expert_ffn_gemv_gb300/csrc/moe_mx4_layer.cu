@@ -588,8 +588,12 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                     if (!(ok = __all_sync(0xffffffffu, !*abort_flag))) break;
                 }
                 if (!ok) break;
-                // the rows were written as ordinary stores; from here on they are read by bulk copies
-                if (looked) fence_proxy_async_all();
+                // the rows were written as ordinary stores; from here on they are read by bulk copies, by
+                // whichever lane is elected (hence the warp's barrier after the looking lane's acquire)
+                if (looked) {
+                    __syncwarp();
+                    fence_proxy_async_all();
+                }
             }
             const int tok = !down && lane < n ? ch.rows[pos + lane] / p.k : 0;
             for (int kc = 0; kc < NKS; ++kc, advance(), ++fills) {
