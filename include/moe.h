@@ -437,7 +437,7 @@ int moe_combine_rmsnorm(const float *partial, int T, int k, int H, const float *
  * cols a positive multiple of 32; rows >= 0 (0: no-op); codes 16-byte aligned.
  *
  * moe_mx4_dequantize — the inverse: y[r][c] = 2^(s-127) * e2m1 (device [rows][ld], ytype; exact in
- * both types).  Columns cols .. ld-1 of y are left as they were.
+ * both types, an infinity beyond their range, which scales of 253 and 254 reach).  Columns cols .. ld-1 of y are left as they were.
  */
 int moe_mx4_quantize(const void *x, int xtype, int rows, int cols, size_t ld, uint8_t *codes,
                      uint8_t *scales, moe_stream_t s);
@@ -477,7 +477,7 @@ int moe_mx4_dequantize_experts(const void *pool, size_t slot_bytes, const int32_
  *                      16-byte aligned.
  *   workspace          device, moe_mx4_expert_workspace() bytes, 256-byte aligned; needs no
  *                      initial contents; one per call in flight.
- * H, F multiples of 32; T >= 0 (0: no-op), E <= MOE_MAX_E, k <= MOE_MAX_K, T*k <= 2^24.
+ * H, F multiples of 32; T >= 0 (0: no-op), E <= MOE_MAX_E, k <= MOE_MAX_K, k <= E, T*k <= 2^24.
  */
 int moe_mx4_expert_workspace(int T, int H, int F, int E, int k, size_t *bytes);
 int moe_mx4_expert_gateup(const uint8_t *x_codes, const uint8_t *x_scales, int T, int H, int F, int E, int k,
@@ -495,6 +495,7 @@ int moe_mx4_expert_down(const uint8_t *h_codes, const uint8_t *h_scales, int T, 
  *   y[t] = extra[t] + sum_{j=0..k-1} weights[t][j] * Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),
  * with x and h kept at fp32 accuracy (24-bit fixed point under one scale per token, per 32
  * columns of h), summed over j in the order 0..k-1 after extra.  The same bits for the same input.
+ * (Logits are fp32 sums, as moe_router_topk's, in an order of their own.)
  *   x, w_router, bias  as in moe_router_topk; extra device [T][H] fp32 or NULL; y device [T][H]
  *                      fp32 out, may alias extra.
  *   ids, weights       device [T][k] out, or NULL.

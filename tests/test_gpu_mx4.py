@@ -70,6 +70,18 @@ def test_quantise_borders_and_non_finite_blocks(xtype):
 
 
 @pytest.mark.parametrize("xtype", ["f32", "bf16"])
+def test_dequantise_every_scale(xtype):
+    """2^(s-127) * e2m1 exactly for every scale byte; an infinity of its sign past the type's range."""
+    scales = np.arange(256, dtype=np.uint8)[:, None]
+    codes = np.tile(np.arange(16, dtype=np.uint8), 2)[None, :].repeat(256, 0)
+    y = torch.zeros(256, 32, dtype=DT[xtype], device="cuda")
+    L.moe_mx4_dequantize(dev(ref.pack(codes)), dev(scales), 256, 32, y, XT[xtype], 32)
+    want = ref.values(codes, scales)  # 64 bits: nothing overflows there
+    want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(np.inf, want), want)
+    np.testing.assert_array_equal(y.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("xtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,cols,pad,off", [(1, 32, 0, 0), (3, 96, 8, 0), (17, 160, 5, 0), (5, 2048, 1, 1), (700, 64, 3, 1),
                                                (257, 224, 32, 8), (2440, 1056, 5, 1)])
 def test_quantise_rows_strides_and_alignment(rows, cols, pad, off, xtype):
