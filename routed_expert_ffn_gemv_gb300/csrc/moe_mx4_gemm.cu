@@ -16,7 +16,7 @@
 //                  bulk copy: the slot image is in operand order) and the chunk's code rows, as runs
 //                  of mx4_place_kernel's output, or, for few routes, four rows to a TMA gather
 //                  straight into the 128-byte-swizzled operand layout;
-//      warp 2      one thread issues the four MMAs of a stage and one commit;
+//      warp 2      the four MMAs of a stage and one commit, by an elected thread;
 //      warps 4-7   the stage's scales into tensor memory.  Each warp writes its own
 //                  lane quarter (the tensor core reads a copy in each);
 //      warps 8-15  the epilogue of the previous item from the other accumulator.
@@ -305,7 +305,7 @@ struct GemmGeom {
     static constexpr int O_SC = (O_LOC + (LOCAL ? (int)sizeof(GemmChunks) : 0) + 15) / 16 * 16;
     static constexpr int O_RING = (O_SC + S * SSTAGE + 1023) / 1024 * 1024;
     static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
-    static_assert(SFCOL + S * 24 <= 512 && STAGE % 1024 == 0 && O_LOC % 16 == 0 && SMEM <= 227 * 1024, "budget");
+    static_assert(SFCOL + S * 24 <= 512 && STAGE % 1024 == 0 && O_LOC % 16 == 0 && SMEM <= 227 * 1024, "tensor and shared memory");
 };
 
 // A work item: slot (-1: none), first position and number of its routes, weight tile.
@@ -543,6 +543,9 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
         // warps of a quarter take alternate groups of routes.  The next item's routes and weights are
         // read while this one is worked on.  Gate/up: lanes 0-63 hold gate rows, 64-127 the same up
         // rows; a gate warp and its up warp trade halves of the group, so that both work on SwiGLU.
+        // (Measured, 32768 routes, gate/up 82.5 us and down 78.7: the warps as two groups on alternate items
+        // 86.6 and 79.3, tensor memory read a group ahead 85.3 and 79.9, the accumulator released after its
+        // last load instead of its last store 83.6 and 78.3.)
         const int q = warp & 3, ew = warp - 8, half = ew >> 2, et = ew * 32 + lane;
         int jl = 0, xs = 0;
         auto next_item = [&](int i, Item &it) {  // the first item from i on that has a slot
