@@ -157,11 +157,14 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid
             }
         }
     };
-    uint4 wa[PRE], wb[PRE];
-    load_rows(hsub, wa);  // the router's weights do not come from the kernel before
-    load_rows(hsub + PRE * NH, wb);
+    // the router's weights, too, may come from the kernel before: ahead of the wait they are only brought to L2
+    // (this CTA's rows are one run of bytes)
+    if (p.wide_w && tid == 0 && blockIdx.y == 0) bulk_prefetch_l2(p.w_router + (size_t)h0 * p.E, (uint32_t)HS * p.E * 2u);
     pdl_wait();
     pdl_trigger();  // not before: the next kernel reads its slot table before its own wait
+    uint4 wa[PRE], wb[PRE];
+    load_rows(hsub, wa);
+    load_rows(hsub + PRE * NH, wb);
     // this CTA's eighth of the tokens, and their largest magnitudes (as bits: NaN sorts above all)
     {
         uint32_t m[TT] = {};

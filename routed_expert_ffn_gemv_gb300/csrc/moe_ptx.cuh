@@ -98,6 +98,12 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t by
         : "memory");
 }
 
+// Brings a run of global memory to L2 and nothing else: no register or shared memory holds it, so it may
+// run ahead of the kernel that writes that memory.  src 16-byte aligned; bytes a multiple of 16.
+__device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // ------------------------------------------------------------------ packed fp32x2
 
 __device__ __forceinline__ unsigned long long f2_pack(float lo, float hi) {
