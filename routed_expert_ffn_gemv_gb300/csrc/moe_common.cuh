@@ -182,6 +182,12 @@ static inline void moe_pdl_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *
     cfg->numAttrs = 1;
 }
 
+// moe_router_topk_threshold.  w_ready: w_router and bias were complete before the launch preceding this call
+// started (the decode kernel then reads them before its dependency wait).
+int moe_router_topk_impl(const void *x, int xtype, int T, int H, const uint16_t *w_router, const float *bias, int E,
+                         int k, float min_weight, int32_t *ids, float *weights, float *logits, cudaStream_t s,
+                         bool w_ready);
+
 // Writes up to three small int32 arrays (<= 256 values each) on stream s with one launch
 // (values travel as kernel parameters, so no host staging buffer outlives the call).
 int moe_write_ints(int32_t *const dst[3], const int n[3], const int32_t *const src[3], cudaStream_t s);

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS)
 router_topk_kernel(const void *__restrict__ x, int T, int H, const uint16_t *__restrict__ w_router,
                    const float *__restrict__ bias, int E, int k, int32_t *__restrict__ ids,
                    float *__restrict__ weights, float *__restrict__ logits_out, int use_bulk,
-                   int *status, float min_w) {
+                   int *status, float min_w, int w_ready) {
     extern __shared__ __align__(128) unsigned char smem[];
     const RouterSmem L = router_smem_layout(H, E);
     const uint16_t *w_s = (const uint16_t *)(smem + L.w);
@@ -74,6 +74,12 @@ router_topk_kernel(const void *__restrict__ x, int T, int H, const uint16_t *__r
     const int tid = threadIdx.x;
     const size_t wbytes = (size_t)HS * E * 2;
 
+    // The weights and the bias, too, may come from the kernel before, unless the caller knows better
+    // (w_ready): then only L2 gets them ahead of the dependency wait.
+    if (!w_ready) {
+        if (use_bulk && tid == 0 && blockIdx.y == 0) bulk_prefetch_l2(w_router + (size_t)h0 * E, (uint32_t)wbytes);
+        pdl_wait();
+    }
     // ---- W_r slice -> shared memory (bulk copy when aligned, else plain loads)
     bool w_ok = true;
     if (use_bulk) {
@@ -91,7 +97,7 @@ router_topk_kernel(const void *__restrict__ x, int T, int H, const uint16_t *__r
     __shared__ float bias_s[MOE_MAX_E];
     if (rank == 0)
         for (int e = tid; e < E; e += MOE_ROUTER_THREADS) bias_s[e] = bias ? bias[e] : 0.f;
-    pdl_wait();  // x comes from the previous kernel (the weights and the bias do not)
+    if (w_ready) pdl_wait();  // x comes from the previous kernel
     pdl_trigger();
     // ---- x slice of this cluster's tokens
     for (int i = tid; i < TT * HS; i += MOE_ROUTER_THREADS) {
@@ -619,6 +625,13 @@ extern "C" int moe_router_topk(const void *x, int xtype, int T, int H, const uin
 extern "C" int moe_router_topk_threshold(const void *x, int xtype, int T, int H, const uint16_t *w_router,
                                          const float *bias, int E, int k, float min_weight, int32_t *ids,
                                          float *weights, float *logits, moe_stream_t s) {
+    return moe_router_topk_impl(x, xtype, T, H, w_router, bias, E, k, min_weight, ids, weights, logits,
+                                moe_cuda_stream(s), false);
+}
+
+int moe_router_topk_impl(const void *x, int xtype, int T, int H, const uint16_t *w_router, const float *bias, int E,
+                         int k, float min_weight, int32_t *ids, float *weights, float *logits, cudaStream_t s,
+                         bool w_ready) {
     MOE_CHECK(T >= 0);
     MOE_CHECK(min_weight >= 0.0f && min_weight <= 1.0f);
     MOE_CHECK(xtype == MOE_F32 || xtype == MOE_BF16);
@@ -628,10 +641,8 @@ extern "C" int moe_router_topk_threshold(const void *x, int xtype, int T, int H,
     MOE_CHECK(x && w_router && ids && weights);
     if (T > MOE_DECODE_MAX_T && ((uintptr_t)x & 15) == 0 && ((uintptr_t)w_router & 15) == 0) {
         if (router_mma_eligible(xtype, H, E))
-            return router_mma_launch(x, T, H, w_router, bias, E, k, ids, weights, logits, min_weight,
-                                     moe_cuda_stream(s));
-        return router_tiled_launch(x, xtype, T, H, w_router, bias, E, k, ids, weights, logits, min_weight,
-                                   moe_cuda_stream(s));
+            return router_mma_launch(x, T, H, w_router, bias, E, k, ids, weights, logits, min_weight, s);
+        return router_tiled_launch(x, xtype, T, H, w_router, bias, E, k, ids, weights, logits, min_weight, s);
     }
     const RouterSmem L = router_smem_layout(H, E);
     if (L.total > 200 * 1024) return MOE_ERR_UNSUPPORTED;
@@ -645,7 +656,7 @@ extern "C" int moe_router_topk_threshold(const void *x, int xtype, int T, int H,
     cfg.gridDim = dim3(MOE_ROUTER_CLUSTER, (T + MOE_ROUTER_TOKENS - 1) / MOE_ROUTER_TOKENS, 1);
     cfg.blockDim = dim3(MOE_ROUTER_THREADS, 1, 1);
     cfg.dynamicSmemBytes = L.total;
-    cfg.stream = moe_cuda_stream(s);
+    cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = MOE_ROUTER_CLUSTER;
@@ -659,12 +670,12 @@ extern "C" int moe_router_topk_threshold(const void *x, int xtype, int T, int H,
         MOE_TRY_CUDA(cudaFuncSetAttribute(router_topk_kernel<MOE_F32>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.total));
         MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, router_topk_kernel<MOE_F32>, x, T, H, w_router, bias, E,
-                                        k, ids, weights, logits, use_bulk, status, min_weight));
+                                        k, ids, weights, logits, use_bulk, status, min_weight, (int)w_ready));
     } else {
         MOE_TRY_CUDA(cudaFuncSetAttribute(router_topk_kernel<MOE_BF16>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.total));
         MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, router_topk_kernel<MOE_BF16>, x, T, H, w_router, bias,
-                                        E, k, ids, weights, logits, use_bulk, status, min_weight));
+                                        E, k, ids, weights, logits, use_bulk, status, min_weight, (int)w_ready));
     }
     return MOE_OK;
 }

@@ -240,10 +240,10 @@ int prefetch_fork(moe_stack *st, int layer, const float *x, int T, cudaStream_t 
     MOE_TRY_CUDA(cudaEventRecord(st->pf_fork, s));
     MOE_TRY_CUDA(cudaStreamWaitEvent(ps, st->pf_fork, 0));
     int rc;
+    // (the fork's event, then a router, precede: the weights are complete)
     for (int i = 0; i < n; ++i)
-        if ((rc = moe_router_topk_threshold(x, MOE_F32, T, d.H, st->w_router[targets[i]], st->bias[targets[i]], d.E,
-                                            d.k, d.load_threshold, pids + i * R, pw + i * R, nullptr,
-                                            (moe_stream_t)ps)))
+        if ((rc = moe_router_topk_impl(x, MOE_F32, T, d.H, st->w_router[targets[i]], st->bias[targets[i]], d.E, d.k,
+                                       d.load_threshold, pids + i * R, pw + i * R, nullptr, ps, true)))
             return rc;
     MOE_TRY_CUDA(cudaEventRecord(st->pf_rdone, ps));
     for (int i = 0; i < n; ++i)
@@ -283,8 +283,10 @@ int layer_step(moe_stack *st, int layer, const float *h, float *y, int T, int32_
         st->prof.kernel_launches += 1;
     }
     if ((rc = begin_timed(st, s, &ep))) return rc;
-    if ((rc = moe_router_topk_threshold(x, MOE_F32, T, d.H, st->w_router[layer], st->bias[layer], d.E, d.k,
-                                        d.load_threshold, ids_d, w_d, nullptr, (moe_stream_t)s)))
+    // a norm or combine kernel of the step precedes: it started its dependents after its own wait, so whatever
+    // wrote the weights is complete
+    if ((rc = moe_router_topk_impl(x, MOE_F32, T, d.H, st->w_router[layer], st->bias[layer], d.E, d.k,
+                                   d.load_threshold, ids_d, w_d, nullptr, s, true)))
         return rc;
     st->prof.kernel_launches += 1;
     if ((rc = end_timed(st, s, K_ROUTER, ep))) return rc;
