@@ -422,8 +422,8 @@ int moe_combine_rmsnorm(const float *partial, int T, int k, int H, const float *
 
 /*
  * The MXFP4 operators: activations and weights to 4 bits, the routed experts' products with
- * both sides in 4 bits (prompts), and a whole MoE layer over 4-bit experts with activations kept
- * at fp32 accuracy (decode).  Page 5, section 1.2, keeps quantised blocks as they are on the GPU
+ * both sides in 4 bits (prompts), and a whole MoE layer over 4-bit experts with 23-bit activations
+ * (decode).  Page 5, section 1.2, keeps quantised blocks as they are on the GPU
  * and multiplies them there; the format is the Open Compute microscaling one (32 elements of E2M1
  * under one E8M0 scale).
  *
@@ -493,8 +493,9 @@ int moe_mx4_expert_down(const uint8_t *h_codes, const uint8_t *h_scales, int T, 
  * moe_mx4_layer — a whole MoE layer for a few tokens (T <= MOE_DECODE_MAX_T) over resident MXFP4
  * experts: moe_router_topk's routing, the routed FFNs and the combine,
  *   y[t] = extra[t] + sum_{j=0..k-1} weights[t][j] * Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),
- * with x and h kept at fp32 accuracy (24-bit fixed point under one scale per token, per 32
- * columns of h), summed over j in the order 0..k-1 after extra.  The same bits for the same input.
+ * with x and h as fixed-point numbers under one power of two per 32 columns (each element off by at most
+ * 2^-22 of the largest magnitude of its 32, or by 2^-128), sums in fp32, added over j in the order 0..k-1 after
+ * extra.  The same bits for the same input.
  * (Logits are fp32 sums, as moe_router_topk's, in an order of their own.)
  *   x, w_router, bias  as in moe_router_topk; extra device [T][H] fp32 or NULL; y device [T][H]
  *                      fp32 out, may alias extra.

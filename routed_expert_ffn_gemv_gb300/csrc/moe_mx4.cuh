@@ -107,10 +107,6 @@ __device__ __forceinline__ uint32_t raw8_amax(const Raw8<XT> &r) {
     return a;
 }
 template <int XT>
-__device__ __forceinline__ void load8(const void *p, size_t i, bool wide, float (&v)[8]) {
-    raw8_floats<XT>(load_raw8<XT>(p, i, wide), v);
-}
-template <int XT>
 __device__ __forceinline__ void store8(void *p, size_t i, bool wide, const float (&v)[8]) {
     if (XT == MOE_BF16) {
         __nv_bfloat16 *b = (__nv_bfloat16 *)p + i;

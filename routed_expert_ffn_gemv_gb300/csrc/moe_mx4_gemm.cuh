@@ -7,12 +7,6 @@
 int mx4_ffn_check(int T, int H, int F, int E, int k);
 int mx4_pool_check(int H, int F, int n_slots, const void *pool, size_t slot_bytes);
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 // ------------------------------------------------------------------ few routes: chunks by every CTA
 //
 // Up to MAXR routes are grouped by expert by each CTA for itself in shared memory: a warp match ranks the

@@ -1,18 +1,19 @@
 // A whole MoE layer for a few tokens over resident MXFP4 experts (moe_mx4_layer): two kernels.
 //
-// The 4-bit tensor cores multiply E2M1 by E2M1.  To keep the activations at fp32 accuracy they are
+// The 4-bit tensor cores multiply E2M1 by E2M1.  To keep 23 bits of the activations they are
 // written in radix 8: an activation is a 24-bit fixed-point number under a common scale, and its
 // eight digits -4 .. 3 are all E2M1 values, so a token becomes eight exact 4-bit columns and
 //     w . x = scale * sum_p 8^p (w . digit_p),
 // each term an exact product of 4-bit operands summed in fp32 by the MMA.  Eight columns are the
 // narrowest MMA there is, so one token's digits cost nothing over a single 4-bit column, the weights
 // go from HBM through shared memory to the tensor core untouched, and no thread dequantises.
-//   x: one scale per token (largest magnitude to 7190000, the largest symmetric 8-digit number);
-//   h: one power of two per 32 columns, the MMA's own E8M0 scale (largest magnitude below 2^22).
+// x and h have one power of two per 32 columns, the MMA's own E8M0 scale: the largest magnitude of the 32
+// becomes a number of 1.71 * 2^21 to 1.71 * 2^22 (the largest symmetric 8-digit one), so that an element is off
+// by at most 2^-22.7 of it, and columns of another block by nothing.
 //
 //  * mx4_prep_kernel, 8-CTA clusters of 1 or 2 tokens: the router (a CTA sums its eighth of H, the
-//    partial logits meet over distributed shared memory, one warp selects), the tokens' digits in
-//    operand order, and the counters of the second kernel.
+//    partial logits meet over distributed shared memory, one CTA per token ranks the experts), the tokens'
+//    digits and scales in operand order, and the counters of the second kernel.
 //  * mx4_layer_kernel: persistent.  Units: (chunk of at most NR routes of one expert, 128-row weight
 //    tile) of gate/up, then of down, then (tile of H, eight tokens) of the combine.  CTAs take units in order from a counter, so a down unit only
 //    ever waits for gate/up units that running CTAs hold: no co-residency is needed, and other work
@@ -42,8 +43,9 @@
 #define MXL_Q 4               // claimed units in flight in a CTA
 #define MXL_PUB (2 * MXL_Q)   // the epilogue may be MXL_Q units ahead of warp 3 and of a queue slot's reuse
 #define MXL_MAX_R (MOE_DECODE_MAX_T * MOE_MAX_K)
-#define MXL_XMAX 7190000.0f   // <= 3 (8^8 - 1) / 7
 #define MXL_BIAS 9586980u     // 4 (8^8 - 1) / 7: turns digits -4 .. 3 into 0 .. 7
+#define MXL_SC 16             // bytes of a row's scales in a stage: a word for each 128 columns, and padding
+#define MXL_ROW (1024 + MXL_SC)  // a row's digits and scales
 #define MXL_WBYTES (2 * MX4_TB)
 
 static_assert(MXL_PREP_THREADS == MOE_MAX_E, "a thread per expert");
@@ -53,8 +55,11 @@ namespace {
 // (a chunk holds a route at least)
 typedef Mx4Chunks<MXL_MAX_R, MXL_MAX_R> LayerChunks;
 
+// Most routes of a chunk (NR of the second kernel).
+int chunk_routes(int T) { return T <= 8 ? 8 : 16; }
+
 struct LayerWs {
-    size_t ctr, ids, weights, xscale, xq, hq, partial, total;
+    size_t ctr, ids, weights, xq, hq, partial, total;
     size_t ctr_ints;
 };
 
@@ -71,9 +76,8 @@ LayerWs layer_ws(int T, int H, int F, int k) {
     L.ctr = take(L.ctr_ints * 4);
     L.ids = take(R * 4);
     L.weights = take(R * 4);
-    L.xscale = take((size_t)T * 8);
-    L.xq = take((HB + 1) / 2 * T * 1024);
-    L.hq = take(R * ((FB + 1) / 2) * (1024 + 128));  // (at most a chunk per route)
+    L.xq = take((HB + 1) / 2 * T * MXL_ROW);  // every stage's digits, then every stage's scales
+    L.hq = take(R * ((FB + 1) / 2) * (1024 + chunk_routes(T) * MXL_SC));  // (at most a chunk per route)
     L.partial = take(R * H * 4);
     L.total = o;
     return L;
@@ -82,17 +86,38 @@ LayerWs layer_ws(int T, int H, int F, int k) {
 // Code of the radix-8 digit d (0 .. 7 for -4 .. 3).
 __device__ __forceinline__ uint32_t digit_code(uint32_t d) { return (0x5420ACDEu >> (4 * d)) & 15u; }
 
+// The scale byte of a block whose largest magnitude has these bits: the power of two that makes it a number
+// of at most 7190000 < 3 (8^8 - 1) / 7 = 1.7142.. * 2^22, the largest symmetric one of eight digits; at least
+// 2^-127 (blocks below 2^-105 keep fewer digits); 255 for an infinity or a NaN.  A mantissa beyond
+// 7190000 / 2^22 (0x5B6BE0 steps above 1) carries into the exponent.
+__device__ __forceinline__ int digit_scale(uint32_t amax_bits) {
+    return amax_bits >= 0x7F800000u ? 255 : max(0, (int)((amax_bits + 0x24941Fu) >> 23) - 22);
+}
+// A block's digits under that scale, a column's value to a lane, transposed: lane 8a + b gets digit b of columns
+// 8a .. 8a + 7 (zeros under 255).
+__device__ __forceinline__ uint32_t digit_word(float v, int scale, int lane) {
+    uint32_t u = MXL_BIAS, w = 0;
+    if (scale != 255) u += (uint32_t)__float2int_rn(v * e8m0_inverse(scale));
+#pragma unroll
+    for (int p = 0; p < 8; ++p) w |= digit_code((u >> (3 * p)) & 7u) << (4 * p);
+    uint32_t y = __shfl_xor_sync(0xffffffffu, w, 4);
+    w = lane & 4 ? (w & 0xFFFF0000u) | (y >> 16) : (w & 0x0000FFFFu) | (y << 16);
+    y = __shfl_xor_sync(0xffffffffu, w, 2);
+    w = lane & 2 ? (w & 0xFF00FF00u) | ((y >> 8) & 0x00FF00FFu) : (w & 0x00FF00FFu) | ((y & 0x00FF00FFu) << 8);
+    y = __shfl_xor_sync(0xffffffffu, w, 1);
+    return lane & 1 ? (w & 0xF0F0F0F0u) | ((y >> 4) & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | ((y & 0x0F0F0F0Fu) << 4);
+}
+
 // ------------------------------------------------------------------ router, digits of x
 
 struct PrepParams {
     const void *x;
     const uint16_t *w_router;
     const float *bias;
-    int T, H, E, k, wide_w, wide_x;
+    int T, H, E, k, wide_w;
     int32_t *ids;
     float *weights;
-    float2 *xscale;
-    uint8_t *xq;
+    uint8_t *xq, *xsc;  // [stage][token] of 1024, of MXL_SC bytes
     int *ctr;
     int n_ctr;
 };
@@ -118,7 +143,6 @@ __device__ __forceinline__ void half8(const uint4 &u, float (&w)[8]) {
 template <int XT, int TT>
 __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid_constant__ PrepParams p) {
     extern __shared__ __align__(16) float sm[];
-    __shared__ uint32_t mx_w[TT][MXL_PREP_THREADS / 32], mx[TT], gmx[TT];
     __shared__ __align__(16) uint32_t key[MOE_MAX_E];
     __shared__ uint32_t sel[2 * MOE_MAX_K];
     constexpr int NW = MXL_PREP_THREADS / 32, PRE = 8;  // rows of w_router a thread reads at a time
@@ -165,35 +189,21 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid
     uint4 wa[PRE], wb[PRE];
     load_rows(hsub, wa);
     load_rows(hsub + PRE * NH, wb);
-    // this CTA's eighth of the tokens, and their largest magnitudes (as bits: NaN sorts above all)
-    {
-        uint32_t m[TT] = {};
-        for (int h = tid; h < HS; h += MXL_PREP_THREADS)
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                float v = 0.f;
-                if (t < nt) {
-                    const size_t at = (size_t)(t0 + t) * p.H + h0 + h;
-                    v = XT == MOE_BF16 ? __bfloat162float(((const __nv_bfloat16 *)p.x)[at]) : ((const float *)p.x)[at];
-                }
-                xs[h * TT + t] = v;
-                m[t] = max(m[t], __float_as_uint(v) & 0x7FFFFFFFu);
-            }
+    // this CTA's eighth of the tokens
+    for (int h = tid; h < HS; h += MXL_PREP_THREADS)
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            m[t] = __reduce_max_sync(0xffffffffu, m[t]);
-            if (lane == 0) mx_w[t][warp] = m[t];
+            float v = 0.f;
+            if (t < nt) {
+                const size_t at = (size_t)(t0 + t) * p.H + h0 + h;
+                v = XT == MOE_BF16 ? __bfloat162float(((const __nv_bfloat16 *)p.x)[at]) : ((const float *)p.x)[at];
+            }
+            xs[h * TT + t] = v;
         }
-    }
     const float bias = p.bias && tid < p.E ? p.bias[tid] : 0.f;
     if (blockIdx.y == 0)
         for (int i = rank * MXL_PREP_THREADS + tid; i < p.n_ctr; i += MXL_CLUSTER * MXL_PREP_THREADS) p.ctr[i] = 0;
     __syncthreads();
-    if (tid < TT) {
-        uint32_t m = 0;
-        for (int w = 0; w < NW; ++w) m = max(m, mx_w[tid][w]);
-        mx[tid] = m;
-    }
     float acc[TT][8];
 #pragma unroll
     for (int t = 0; t < TT; ++t)
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid
         part[i] = s;
     }
     cluster_sync_all();
-    // a thread per expert sums token t0 + rank's logit; the last warp fetches the tokens' maxima
+    // a thread per expert sums token t0 + rank's logit
     if (rank < nt && tid < p.E) {
         float s = 0.f;
 #pragma unroll
@@ -244,57 +254,32 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid
     } else {
         key[tid] = 0;
     }
-    if (warp == NW - 1) {
-        uint32_t m = lane < TT * MXL_CLUSTER ? ld_cluster_u32(cluster_map(&mx[lane / MXL_CLUSTER], lane % MXL_CLUSTER)) : 0;
-#pragma unroll
-        for (int o = 1; o < MXL_CLUSTER; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane < TT * MXL_CLUSTER && lane % MXL_CLUSTER == 0) gmx[lane / MXL_CLUSTER] = m;
-    }
     __syncthreads();
     // nothing of another CTA is read after this; a CTA's own shared memory stays until all have come here
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (rank < nt) select_topk_block(key, p.E, p.k, sel, (size_t)(t0 + rank), p.ids, p.weights);
     if (warp > 0) {
-        // digits, by the other warps: eight columns of one token per thread, of this CTA's eighth of H where
-        // it is whole groups of eight columns, else of the tokens' groups in turn
-        const bool own = HS % 8 == 0;
-        const int per = own ? HS / 8 : p.H / 8, step = (MXL_PREP_THREADS - 32) * (own ? 1 : MXL_CLUSTER);
+        // digits and scales, by the other warps: a block of 32 columns of one token to a warp; of this CTA's eighth
+        // of H where it is whole blocks, else of the tokens' blocks in turn
+        const bool own = HS % 32 == 0;
+        const int per = (own ? HS : p.H) / 32, step = (NW - 1) * (own ? 1 : MXL_CLUSTER);
+        const int d = lane & 7;  // this lane's digit after the transpose
 #pragma unroll 1
-        for (int i = own ? tid - 32 : (tid - 32) * MXL_CLUSTER + rank; i < nt * per; i += step) {
-            const int t = i / per, col = (i - t * per) * 8 + (own ? h0 : 0);
-            float v[8];
-            if (own) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = xs[(col - h0 + j) * TT + t];
-            } else {
-                load8<XT>(p.x, (size_t)(t0 + t) * p.H + col, p.wide_x, v);
+        for (int i = own ? warp - 1 : (warp - 1) * MXL_CLUSTER + rank; i < nt * per; i += step) {
+            const int t = i / per, col = (i - t * per) * 32 + (own ? h0 : 0), c = (col >> 5) & 3;
+            const size_t in = (size_t)(t0 + t) * p.H + col + lane;
+            const float v = own ? xs[(col - h0 + lane) * TT + t]
+                          : XT == MOE_BF16 ? __bfloat162float(((const __nv_bfloat16 *)p.x)[in]) : ((const float *)p.x)[in];
+            const int sc = digit_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
+            const size_t at = (size_t)(col >> 8) * p.T + t0 + t;
+            uint8_t *atom = p.xq + at * 1024 + ((col >> 7) & 1) * 512;
+            *(uint32_t *)(atom + d * 64 + ((c ^ ((d >> 1) & 3)) << 4) + 4 * (lane >> 3)) = digit_word(v, sc, lane);
+            if (lane == 0) {
+                uint8_t *dst = p.xsc + at * MXL_SC + ((col >> 7) & 1) * 4 + c;
+                dst[0] = (uint8_t)sc;
+                // the MMA's last 64 columns may be 32 columns and 32 past H, against weights of zero: any scale but NaN
+                if (col + 32 == p.H && (c & 1) == 0) dst[1] = 0;
             }
-            // largest magnitude = norm * pw, norm in [1, 2), pw a power of two (possibly subnormal)
-            const uint32_t m = gmx[t];
-            const int e = (int)(m >> 23);
-            float norm = __uint_as_float((m & 0x7FFFFFu) | 0x3F800000u), pw = __uint_as_float((uint32_t)e << 23);
-            if (m == 0 || e == 255) {
-                norm = m == 0 ? 1.f : __uint_as_float(0x7FC00000u);
-                pw = 1.f;
-            } else if (e == 0) {
-                const int top = 31 - __clz(m);
-                norm = (float)m / (float)(1u << top);
-                pw = __uint_as_float(1u << top);
-            }
-            if (col == 0) p.xscale[t0 + t] = make_float2(norm / MXL_XMAX, pw);
-            // x / pw in (-2, 2): by two exact factors where 1 / pw would overflow
-            const float f = MXL_XMAX / norm, i1 = pw < 1e-30f ? 1.2676506e30f : 1.f, i2 = 1.f / (pw * i1);
-            uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t u = (uint32_t)(__float2int_rn(v[j] * i1 * i2 * f)) + MXL_BIAS;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) w[q] |= digit_code((u >> (3 * q)) & 7u) << (4 * j);
-            }
-            uint8_t *atom = p.xq + ((size_t)(col >> 8) * p.T + t0 + t) * 1024 + ((col >> 7) & 1) * 512;
-            const int c = (col >> 5) & 3, o = 4 * ((col >> 3) & 3);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) *(uint32_t *)(atom + q * 64 + ((c ^ ((q >> 1) & 3)) << 4) + o) = w[q];
         }
     }
     __syncwarp();
@@ -310,26 +295,25 @@ struct FfnParams {
     int n_slots;
     const uint8_t *pool;
     size_t slot_bytes;
-    const float2 *xscale;
-    const uint8_t *xq;
+    const uint8_t *xq, *xsc;
     uint8_t *hq;
     float *partial, *y;
     int *ticket, *ready, *done;
     int *status;
-    int res;      // bytes of resident digits (0: copied by stage)
+    int res;      // bytes of resident digits and scales (0: copied by stage)
     int S, stage; // ring stages, bytes of one
 };
 
-// Shared memory: control, the tokens' digits (resident: T <= NR = 8, and enough of the ring left),
+// Shared memory: control, the tokens' digits and scales (resident: T <= NR = 8, and enough of the ring left),
 // then S stages of two weight blocks and `cap` routes' digits (1024 bytes each: two 512-byte atoms of 8
-// rows x 128 columns), for down followed by 128 bytes of h scales ([2 blocks][16 routes] words).
+// rows x 128 columns) followed by their scales.
 template <int NR>
 struct LayerGeom {
     static constexpr int N = NR * 8;
     static constexpr int SFCOL = 2 * N;      // scales after the two accumulators, 16 columns a stage
     static constexpr int MAXS = 10;
     static constexpr int CTRL = (1024 + 2 * 4 * NR * 32 * 4 + (int)sizeof(LayerChunks) + 2 * MXL_MAX_R * 4 +
-                                 MOE_DECODE_MAX_T * 8 + MOE_MAX_E * 4 + 1023) / 1024 * 1024;
+                                 MOE_MAX_E * 4 + 1023) / 1024 * 1024;
     static_assert(SFCOL + MAXS * 16 <= 512, "tensor memory");
     static_assert(sizeof(LayerChunks) % 16 == 0 && 2 * 4 * NR * 32 * 4 % 16 == 0 && MXL_MAX_R * 4 % 16 == 0,
                   "the control block's arrays follow one another on 16-byte boundaries");
@@ -345,9 +329,10 @@ __device__ __forceinline__ void red_release_gpu(int *a) {
 }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// Digits of h of stage kc of a chunk of n routes (n * 1024 bytes, then its scales).
+// Digits of h of stage kc of a chunk of n routes (n * 1024 bytes, then its scales; on 128-byte boundaries).
+template <int NR>
 __device__ __forceinline__ size_t hq_offset(int chunk, int pos, int n, int stages, int kc) {
-    return (size_t)stages * (pos * 1024 + chunk * 128) + (size_t)kc * (n * 1024 + 128);
+    return (size_t)stages * (pos * 1024 + chunk * NR * MXL_SC) + (size_t)kc * (n * 1024 + NR * MXL_SC);
 }
 
 // A unit: gate/up or down tile m of a chunk, or (last) tile m of y for tokens 8 c .. 8 c + 7.
@@ -430,19 +415,19 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
     uint64_t *q_empty = q_full + MXL_Q;
     uint64_t *pub = q_empty + MXL_Q;           // a unit's outputs are written (4 epilogue warps)
     uint64_t *x_full = pub + MXL_PUB;          // resident digits
-    uint64_t *mma_done = x_full + 1;
+    uint64_t *xs_full = x_full + 1;            // and their scales
+    uint64_t *mma_done = xs_full + 1;
     uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *q_unit = (volatile int *)(tmem_slot + 2);  // [MXL_Q]
-    static_assert((3 * G::MAXS + 4 + 2 * MXL_Q + MXL_PUB + 2) * 8 + (2 + MXL_Q) * 4 <= 1024, "barriers");
+    static_assert((3 * G::MAXS + 4 + 2 * MXL_Q + MXL_PUB + 3) * 8 + (2 + MXL_Q) * 4 <= 1024, "barriers");
     float *xch = (float *)(smem + 1024);                     // [2 buffers][2 pairs][gate, up][NR][32]
     LayerChunks &ch = *(LayerChunks *)(xch + 2 * 4 * NR * 32);
     int *s_on = (int *)(&ch + 1);                            // [MXL_MAX_R] whether a route is computed
     float *s_w = (float *)(s_on + MXL_MAX_R);                // [MXL_MAX_R] router weights
-    float2 *s_xs = (float2 *)(s_w + MXL_MAX_R);              // [MOE_DECODE_MAX_T]
-    int *s_table = (int *)(s_xs + MOE_DECODE_MAX_T);         // [MOE_MAX_E]
+    int *s_table = (int *)(s_w + MXL_MAX_R);                 // [MOE_MAX_E]
     uint8_t *xres = smem + G::CTRL;
-    uint8_t *ring = xres + p.res;
+    uint8_t *ring = xres + (p.res + 511) / 512 * 512;
     const int S = p.S, STAGE = p.stage;
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -462,6 +447,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
         }
         for (int q = 0; q < MXL_PUB; ++q) mbar_init(&pub[q], 4);
         mbar_init(x_full, 1);
+        mbar_init(xs_full, 1);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -480,13 +466,16 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
     if (tid == 0) {
         claim = atomicAdd(p.ticket, 1);
         if (p.res) {
-            mbar_arrive_expect_tx(x_full, (uint32_t)p.res);
-            bulk_g2s(xres, p.xq, (uint32_t)p.res, x_full);
+            // (the scales by themselves: they are a few bytes, and their warps come first)
+            const uint32_t sb = (uint32_t)p.res / MXL_ROW * MXL_SC, xb = (uint32_t)p.res - sb;
+            mbar_arrive_expect_tx(xs_full, sb);
+            bulk_g2s(xres + xb, p.xsc, sb, xs_full);
+            mbar_arrive_expect_tx(x_full, xb);
+            bulk_g2s(xres, p.xq, xb, x_full);
         }
     }
     const int R = p.T * p.k;
     if (tid < R) s_w[tid] = p.weights[tid];
-    if (tid < p.T) s_xs[tid] = p.xscale[tid];
     tc_fence_before();
     mx4_local_chunks<MXL_THREADS>(ch, (uint16_t *)ring, p.ids, R, p.E, p.table ? s_table : nullptr, p.n_slots, NR, s_on,
                                   p.status);
@@ -517,7 +506,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
 
     if (nch == 0) {
         // no expert is resident: the layer is its extra
-        if (tid == 0 && p.res) mbar_wait_role(x_full, 0, p.status, abort_flag);
+        if (tid == 0 && p.res && mbar_wait_role(xs_full, 0, p.status, abort_flag))
+            mbar_wait_role(x_full, 0, p.status, abort_flag);
         for (int m = blockIdx.x; m < HT; m += gridDim.x)
             if (tid < 128)
                 for (int t = 0; t < p.T; t += 8) combine_tile(p, m, t, tid, s_on);
@@ -540,7 +530,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                 if (un.kind == MXL_COMBINE) continue;
                 const bool down = un.kind == MXL_DOWN;
                 const int KB = down ? FB : HB, NKS = (KB + 1) / 2, n = __shfl_sync(0xffffffffu, ch.n[un.c], 0);
-                const uint32_t nb = down ? (uint32_t)n * 1024u + 128u : p.res ? 0u : (uint32_t)n * 1024u;
+                const uint32_t nb = down || !p.res ? (uint32_t)n * MXL_ROW : 0u;
                 const uint8_t *w = p.pool + (size_t)__shfl_sync(0xffffffffu, ch.slot[un.c], 0) * p.slot_bytes +
                                    (down ? down_off : 0) + (size_t)un.m * KB * MX4_TB;
                 for (int kc = 0; kc < NKS; ++kc, advance(), ++fills, w += MXL_WBYTES) {
@@ -551,7 +541,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                 }
             }
             // never leave with copies in flight: the last fill of every stage
-            if (ok && p.res) ok = mbar_wait_role(x_full, 0, p.status, abort_flag);
+            if (ok && p.res)
+                ok = mbar_wait_role(xs_full, 0, p.status, abort_flag) && mbar_wait_role(x_full, 0, p.status, abort_flag);
             for (int i = 0; ok && i < S && i < fills; ++i) {
                 if (--s < 0) {
                     s = S - 1;
@@ -603,10 +594,11 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                 if (fills >= S && !(ok = mbar_wait_warp(&s_empty[s], ph ^ 1u, p.status, abort_flag))) break;
                 uint8_t *st = ring + (size_t)s * STAGE;
                 if (down) {
-                    bulk_g2s_elect(st + MXL_WBYTES, p.hq + hq_offset(un.c, pos, n, NKS, kc),
-                                   (uint32_t)n * 1024u + 128u, &s_full[s]);
+                    bulk_g2s_elect(st + MXL_WBYTES, p.hq + hq_offset<NR>(un.c, pos, n, NKS, kc), (uint32_t)n * MXL_ROW, &s_full[s]);
                 } else if (!p.res && lane < n) {
-                    bulk_g2s(st + MXL_WBYTES + lane * 1024, p.xq + ((size_t)kc * p.T + tok) * 1024, 1024, &s_full[s]);
+                    const size_t at = (size_t)kc * p.T + tok;
+                    bulk_g2s(st + MXL_WBYTES + lane * 1024, p.xq + at * 1024, 1024, &s_full[s]);
+                    bulk_g2s(st + MXL_WBYTES + n * 1024 + lane * MXL_SC, p.xsc + at * MXL_SC, MXL_SC, &s_full[s]);
                 }
                 __syncwarp();
             }
@@ -666,31 +658,41 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
             __syncwarp();
         }
     } else if (warp >= 4 && warp < 8) {
-        // ---------------- scales: the weights' rows lane, lane + 32, ..; a route's for its 8 columns (1 for
-        // x, whose scale is applied at the end)
+        // ---------------- scales: the weights' rows lane, lane + 32, ..; a route's (a resident token's) for its 8
+        // columns
         const uint32_t t0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::SFCOL;
-        bool ok = true;
+        const int HK = (HB + 1) / 2;
+        bool ok = true, xok = !p.res;
         for (int i = 0; ok; ++i) {
             const Unit un = next_unit(i);
             if (un.kind == MXL_COMBINE) continue;
             if (un.kind > MXL_COMBINE) break;
             const bool down = un.kind == MXL_DOWN;
-            const int KB = down ? FB : HB, NKS = (KB + 1) / 2, hs_off = MXL_WBYTES + ch.n[un.c] * 1024;
+            const int KB = down ? FB : HB, NKS = (KB + 1) / 2, n = ch.n[un.c];
+            const bool all = !down && p.res;
+            if (all && !xok && !(ok = xok = mbar_wait_warp(xs_full, 0, p.status, abort_flag))) break;
             for (int kc = 0; kc < NKS; ++kc, advance()) {
+                const uint8_t *st = ring + (size_t)s * STAGE;
+                // (rows past the chunk's or the tokens read whatever follows in shared memory: unused columns)
+                uint2 w[NR / 4];
+                auto row_scales = [&](const uint8_t *rs) {
+#pragma unroll
+                    for (int c = 0; c < NR / 4; ++c) w[c] = *(const uint2 *)(rs + (4 * c + (lane >> 3)) * MXL_SC);
+                };
+                if (all) row_scales(xres + (HK * 1024 + kc * MXL_SC) * p.T);
                 if (!(ok = mbar_wait_warp(&s_full[s], ph, p.status, abort_flag))) break;
                 tc_fence_after();
-                const uint8_t *st = ring + (size_t)s * STAGE;
+                if (!all) row_scales(st + MXL_WBYTES + n * 1024);
                 const bool two = 2 * kc + 1 < KB;
                 const uint4 a = *(const uint4 *)(st + 8192 + 16 * lane);
                 uint4 b = make_uint4(0, 0, 0, 0);
                 if (two) b = *(const uint4 *)(st + MX4_TB + 8192 + 16 * lane);
                 const uint32_t va[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                uint32_t vb[8];
-                const uint32_t *hs = (const uint32_t *)(st + hs_off) + (lane >> 3);
+                uint32_t vb[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    vb[c] = down ? hs[4 * c] : 0x7F7F7F7Fu;
-                    vb[4 + c] = down ? hs[16 + 4 * c] : 0x7F7F7F7Fu;
+                for (int c = 0; c < NR / 4; ++c) {
+                    vb[c] = w[c].x;
+                    vb[4 + c] = w[c].y;
                 }
                 tmem_st8(t0 + 16 * s, va);
                 tmem_st8(t0 + 16 * s + 8, vb);
@@ -742,30 +744,16 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                 if (lane == 0) mbar_arrive1(&acc_empty[buf]);
                 bar_sync_n(2 + (q & 1), 64);
                 const int f0 = 64 * un.m + 32 * (q & 1), kb = f0 >> 7, cb = (f0 >> 5) & 3;
-                uint8_t *hq = p.hq + hq_offset(un.c, pos, n, (FB + 1) / 2, kb >> 1);
+                uint8_t *hq = p.hq + hq_offset<NR>(un.c, pos, n, (FB + 1) / 2, kb >> 1);
                 const int d = lane & 7;  // this lane's digit after the transpose
                 uint8_t *dst = hq + (kb & 1) * 512 + d * 64 + ((cb ^ ((d >> 1) & 3)) << 4) + 4 * (lane >> 3);
 #pragma unroll 1
                 for (int r = q >> 1; r < n; r += 2) {
-                    const float2 xs = s_xs[ch.rows[pos + r] / p.k];
-                    const float gv = xg[32 * r] * xs.x * xs.y, uv = xu[32 * r] * xs.x * xs.y;
+                    const float gv = xg[32 * r], uv = xu[32 * r];
                     const float h = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
-                    const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu) >> 23);
-                    const int sc = e == 255 ? 255 : max(0, e - 21);
-                    uint32_t dg = MXL_BIAS;
-                    if (e != 255) dg += (uint32_t)__float2int_rn(h * e8m0_inverse(sc));
-                    uint32_t w = 0;
-#pragma unroll
-                    for (int i8 = 0; i8 < 8; ++i8) w |= digit_code((dg >> (3 * i8)) & 7u) << (4 * i8);
-                    // lane 8a + b: digit b of columns 8a .. 8a + 7
-                    uint32_t y = __shfl_xor_sync(0xffffffffu, w, 4);
-                    w = lane & 4 ? (w & 0xFFFF0000u) | (y >> 16) : (w & 0x0000FFFFu) | (y << 16);
-                    y = __shfl_xor_sync(0xffffffffu, w, 2);
-                    w = lane & 2 ? (w & 0xFF00FF00u) | ((y >> 8) & 0x00FF00FFu) : (w & 0x00FF00FFu) | ((y & 0x00FF00FFu) << 8);
-                    y = __shfl_xor_sync(0xffffffffu, w, 1);
-                    w = lane & 1 ? (w & 0xF0F0F0F0u) | ((y >> 4) & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | ((y & 0x0F0F0F0Fu) << 4);
-                    *(uint32_t *)(dst + r * 1024) = w;
-                    if (lane == 0) hq[n * 1024 + (kb & 1) * 64 + 4 * r + cb] = (uint8_t)sc;
+                    const int sc = digit_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu));
+                    *(uint32_t *)(dst + r * 1024) = digit_word(h, sc, lane);
+                    if (lane == 0) hq[n * 1024 + r * MXL_SC + (kb & 1) * 4 + cb] = (uint8_t)sc;
                 }
             } else {
                 const int o = 128 * un.m + 32 * q + lane;
@@ -832,10 +820,14 @@ int launch_layer_t(FfnParams &p, cudaStream_t s) {
     using G = LayerGeom<NR>;
     // digits stay resident where four ring stages remain beside them
     const int HK = ((p.H + 127) / 128 + 1) / 2, cap = std::min(p.T, NR);
-    p.stage = (MXL_WBYTES + cap * 1024 + 128 + 511) / 512 * 512;
-    p.res = p.T <= 8 ? HK * p.T * 1024 : 0;
-    if (p.res && G::CTRL + p.res + 4 * p.stage > MXL_SMEM) p.res = 0;
-    p.S = std::min<int>(G::MAXS, (MXL_SMEM - G::CTRL - p.res) / p.stage);
+    p.stage = (MXL_WBYTES + cap * MXL_ROW + 511) / 512 * 512;
+    p.res = p.T <= 8 ? HK * p.T * MXL_ROW : 0;
+    int front = G::CTRL + (p.res + 511) / 512 * 512;
+    if (p.res && front + 4 * p.stage > MXL_SMEM) {
+        p.res = 0;
+        front = G::CTRL;
+    }
+    p.S = std::min<int>(G::MAXS, (MXL_SMEM - front) / p.stage);
     if (p.S < 2) return MOE_ERR_UNSUPPORTED;
     static std::mutex mu;
     static int sms[64] = {0};
@@ -856,7 +848,7 @@ int launch_layer_t(FfnParams &p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<long>(units, n)), dim3(MXL_THREADS),
-                   1024 + G::CTRL + p.res + (size_t)p.S * p.stage, s);
+                   1024 + front + (size_t)p.S * p.stage, s);
     MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_layer_kernel<NR>, p));
     return MOE_OK;
 }
@@ -895,11 +887,10 @@ extern "C" int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int 
     a.bias = bias;
     a.T = T; a.H = H; a.E = E; a.k = k;
     a.wide_w = E % 8 == 0 && ((uintptr_t)w_router & 15) == 0;
-    a.wide_x = ((uintptr_t)x & 15) == 0;
     a.ids = ids ? ids : (int32_t *)(w + L.ids);
     a.weights = weights ? weights : (float *)(w + L.weights);
-    a.xscale = (float2 *)(w + L.xscale);
     a.xq = w + L.xq;
+    a.xsc = a.xq + (size_t)((H + 127) / 128 + 1) / 2 * T * 1024;
     a.ctr = (int *)(w + L.ctr);
     a.n_ctr = (int)L.ctr_ints;
     FfnParams b;
@@ -911,8 +902,8 @@ extern "C" int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int 
     b.n_slots = n_slots;
     b.pool = (const uint8_t *)pool;
     b.slot_bytes = slot_bytes;
-    b.xscale = a.xscale;
     b.xq = a.xq;
+    b.xsc = a.xsc;
     b.hq = w + L.hq;
     b.partial = (float *)(w + L.partial);
     b.y = y;
@@ -922,5 +913,5 @@ extern "C" int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int 
     b.status = moe_status_word_device_ptr();
     rc = xtype == MOE_BF16 ? launch_prep<MOE_BF16>(a, st) : launch_prep<MOE_F32>(a, st);
     if (rc != MOE_OK) return rc;
-    return T <= 8 ? launch_layer_t<8>(b, st) : launch_layer_t<16>(b, st);
+    return chunk_routes(T) == 8 ? launch_layer_t<8>(b, st) : launch_layer_t<16>(b, st);
 }

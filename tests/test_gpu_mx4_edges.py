@@ -12,6 +12,14 @@ torch = pytest.importorskip("torch")
 from test_gpu_mx4 import DT, XT, Layer, clean_status, dev  # noqa: E402,F401
 
 
+def experts_of(E, H, F, parts):
+    """ref.Experts of given (codes, scales) triples, one per expert."""
+    e = ref.Experts.__new__(ref.Experts)
+    e.E, e.H, e.F, e.parts = E, H, F, parts
+    e.vals = [[ref.values(*m) for m in p] for p in parts]
+    return e
+
+
 # ------------------------------------------------------------------ stream order
 
 @pytest.mark.parametrize("E", [256, 20])
@@ -29,3 +37,56 @@ def test_layer_router_weights_of_the_kernel_before(E):
         L.moe_mx4_layer(l.x, L.MOE_F32, l.T, l.H, l.F, E, l.k, l.d_wr, None, l.table, l.n_slots, l.pool, l.sb, None, y,
                         ids2, w2, l.ws, l.ws.numel())
         assert torch.equal(ids2, ids) and torch.equal(w2, w) and torch.equal(y, want), i
+
+
+# ------------------------------------------------------------------ precision of the layer's tokens
+
+@pytest.mark.parametrize("xtype", ["f32", "bf16"])
+@pytest.mark.parametrize("ratio", [1.0, 45.0, 1e4, 1e6])
+@pytest.mark.parametrize("T,H", [(1, 2048), (5, 288), (8, 4096), (12, 1056)])
+def test_layer_token_with_a_large_channel(T, H, ratio, xtype):
+    """A channel `ratio` times the others, in a block of 32 columns whose weights are zero: the other
+    columns keep their 22 bits (of their own block's largest magnitude)."""
+    E, F, k = 2, 96, 1
+    rng = np.random.default_rng(T + H)
+    l = Layer(T, H, F, E, k, seed=T + H, xtype=xtype, extra=False)
+    for p in l.ex.parts:
+        for m in (0, 1):
+            p[m][0][:, 64:96] = 0
+    l.ex = experts_of(E, H, F, l.ex.parts)
+    pool, l.sb = l.ex.pool(l.table.cpu().numpy(), l.n_slots)
+    l.pool = dev(pool.reshape(-1))
+    x = l.x.float()
+    x[:, 71] = 3.0 * ratio
+    l.x = x.to(DT[xtype])
+    l.d_wr.zero_()
+    l.bias = np.array([0.0, 1.0], np.float32)
+    y, ids, w = l.run()
+    assert ids.reshape(-1).tolist() == [1] * T
+    xs, y = l.x.double().cpu().numpy(), y.double().cpu().numpy()
+    g, u, d = l.ex.vals[1]
+    for t in range(T):
+        h, th = ref.gateup(xs[t], g, u)
+        # half a step: a number of 1.71 * 2^21 steps or more stands for the block's largest magnitude
+        q = np.abs(xs[t]).reshape(-1, 32).max(1).repeat(32) * 2.0 ** -22
+        q[64:96] = 0
+        eg, eu = np.abs(g) @ q, np.abs(u) @ q
+        th = th + 1.1 * (np.abs(u @ xs[t]) * eg + np.abs(g @ xs[t]) * eu + eg * eu)
+        hb = np.abs(h).reshape(-1, 32).max(1).repeat(32) + th
+        want = d @ h
+        tol = np.abs(d) @ (th + 2.0 ** -22 * hb) + ref.accumulation(F) * (np.abs(d) @ np.abs(h)) + 4 * ref.F32_STEP * np.abs(want)
+        err = np.abs(y[t] - want)
+        assert (err <= tol).all(), (t, (err / tol).max())
+        assert np.linalg.norm(err) <= 2e-6 * np.linalg.norm(want), np.linalg.norm(err) / np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("T,H,F", [(1, 32, 32), (3, 96, 160), (8, 288, 96), (12, 160, 224), (20, 416, 32)])
+def test_layer_takes_any_workspace_contents(T, H, F):
+    """Columns past H and F meet weights of zero: what the workspace held before (a NaN scale is 255) must not."""
+    l = Layer(T, H, F, 4, 2, seed=H, extra=False)
+    y = []
+    for fill in (0, 0xFF, 0x7F):
+        l.ws.fill_(fill)
+        y.append(l.run()[0])
+    assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
+    assert not bool(torch.isnan(y[0]).any())
