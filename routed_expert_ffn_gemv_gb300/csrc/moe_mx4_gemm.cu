@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(MXG_THREADS, 1) mx4_gemm_kernel(const __grid_c
                         const float other = xb[128 * (1 - up) + 32 * k];
                         const float gv = up ? other : __uint_as_float(v[k]);
                         const float uv = up ? __uint_as_float(v[4 + k]) : other;
-                        h[k] = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
+                        h[k] = mx4_swiglu<OT == MOE_F32>(gv, uv);
                     }
                     auto put = [&](int k) {
                         if (OT == MOE_BF16) *(__nv_bfloat16 *)o[k] = __float2bfloat16(h[k]);

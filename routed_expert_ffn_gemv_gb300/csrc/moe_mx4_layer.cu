@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
 #pragma unroll 1
                 for (int r = q >> 1; r < n; r += 2) {
                     const float gv = xg[32 * r], uv = xu[32 * r];
-                    const float h = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
+                    const float h = mx4_swiglu<true>(gv, uv);
                     const int sc = digit_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu));
                     *(uint32_t *)(dst + r * 1024) = digit_word(h, sc, lane);
                     if (lane == 0) hq[n * 1024 + r * MXL_SC + (kb & 1) * 4 + cb] = (uint8_t)sc;

@@ -90,3 +90,86 @@ def test_layer_takes_any_workspace_contents(T, H, F):
         y.append(l.run()[0])
     assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
     assert not bool(torch.isnan(y[0]).any())
+
+
+# ------------------------------------------------------------------ SwiGLU of large negative gates
+
+def gate_experts(H, F, gates, up):
+    """One expert whose gate rows give gates[f] and up rows `up` for a token of ten ones: sums of a few
+    small integers (a power of two), exact in any order; down takes h's column 32 b into row b."""
+    gc, gs = np.zeros((F, H), np.uint8), np.full((F, H // 32), 127, np.uint8)
+    left = np.abs(gates).astype(np.int64).copy()
+    for c in range(10):
+        for code, v in ((7, 12), (6, 8), (5, 6), (4, 4), (3, 3), (2, 2), (1, 1)):
+            take = (left >= v) & (gc[:, c] == 0)
+            gc[take, c] = code
+            left[take] -= v
+    assert not left.any()
+    gc[np.sign(gates) < 0] |= 8 * (gc[np.sign(gates) < 0] > 0).astype(np.uint8)
+    gs[:] = 128  # codes times two
+    uc, us = np.zeros((F, H), np.uint8), np.full((F, H // 32), 127, np.uint8)
+    uc[:, 0] = 2
+    us[:, 0] = 127 + up
+    dc, ds = np.zeros((H, F), np.uint8), np.full((H, F // 32), 127, np.uint8)
+    for b in range(F // 32):
+        dc[b, 32 * b] = 2
+    return experts_of(1, H, F, [[(gc, gs), (uc, us), (dc, ds)]])
+
+
+def silu_bound(g, u, htype="f32"):
+    """h and the bound of its fp32 evaluation, in half steps (2^-24) of h: exp(-|g| / 2) by a power of two
+    good to 2^-22 (4) and its correction (1), squared; a sum (1); a reciprocal good to 2^-23 (2); four products.
+    The bf16 form leaves the correction out: the argument's rounding, |g| / 2 log2(e) half steps, and its
+    constant's, another half step of it, come to |g| 2^-24 each, twice; then h is rounded to bf16."""
+    h = g * (1.0 / (1.0 + np.exp(-g))) * u
+    tol = 17 * ref.F32_STEP * np.abs(h)
+    if htype == "bf16":
+        tol = tol + 4 * np.abs(g) * ref.F32_STEP * np.abs(h)
+        tol = tol + ref.BF16_STEP * (np.abs(h) + tol)
+    return h, tol
+
+
+@pytest.mark.parametrize("htype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 2100])
+def test_product_swiglu_of_every_gate(T, htype):
+    H, F = 64, 192
+    gates = np.arange(-96, 96).astype(np.float64)
+    ex = gate_experts(H, F, gates, 60)
+    pool, sb = ex.pool()
+    pool = dev(pool.reshape(-1))
+    x = np.zeros((T, H))
+    x[:, :10] = 1.0
+    codes, scales = (np.repeat(a, T, 0) for a in ref.quantise(x[:1]))
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(L.moe_mx4_expert_workspace(T, H, F, 1, 1), dtype=torch.uint8, device="cuda")
+    h = torch.full((T, F), 7.0, dtype=DT[htype], device="cuda")
+    L.moe_mx4_expert_gateup(dev(ref.pack(codes)), dev(scales), T, H, F, 1, 1, ids, None, 1, pool, sb, h, XT[htype], ws,
+                            ws.numel())
+    want, tol = silu_bound(gates, 2.0 ** 60, htype)
+    got = h.double().cpu().numpy()
+    assert (got == got[0]).all()
+    err = np.abs(got[0] - want)
+    assert (err <= tol).all(), (gates[err > tol], (err / np.maximum(np.abs(want), 1e-300))[err > tol])
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_layer_swiglu_of_every_gate(T):
+    """A gate to each block of 32 columns of h, so that its digits add 2^-22 of itself at most."""
+    gates = np.arange(-96, 32).astype(np.float64)
+    H, F = 128, 32 * gates.size
+    ex = gate_experts(H, F, gates.repeat(32), 60)
+    l = Layer(T, H, 32, 1, 1, seed=1, bias=False, extra=False)
+    l.ex, l.F = ex, F
+    pool, l.sb = ex.pool(l.table.cpu().numpy(), l.n_slots)
+    l.pool = dev(pool.reshape(-1))
+    l.x = torch.zeros_like(l.x)
+    l.x[:, :10] = 1.0
+    l.ws = torch.full((L.moe_mx4_layer_workspace(T, H, F, 1, 1),), 0xC3, dtype=torch.uint8, device="cuda")
+    y, _, w = l.run()
+    assert bool((w == 1.0).all())
+    want, tol = silu_bound(gates, 2.0 ** 60)
+    tol = tol + 2.0 ** -22 * np.abs(want)
+    got = y.double().cpu().numpy()
+    assert (got == got[0]).all()
+    err = np.abs(got[0] - want)
+    assert (err <= tol).all(), (gates[err > tol], (err / np.maximum(np.abs(want), 1e-300))[err > tol])
