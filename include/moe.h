@@ -504,8 +504,9 @@ int moe_mx4_expert_down(const uint8_t *h_codes, const uint8_t *h_scales, int T, 
  *                      [0, n_slots) is recorded in the device status word and its routes add nothing.
  *   workspace          device, moe_mx4_layer_workspace() bytes, 256-byte aligned; needs no initial
  *                      contents; one per call in flight.
- * A token with an infinity or a NaN has NaN outputs, as has one whose h overflows.  MOE_ERR_UNSUPPORTED
- * where H is too large for the shared memory of a block (beyond about 100,000), or F beyond 2^26.
+ * A token with an infinity or a NaN has NaN outputs, as has one whose h overflows.  MOE_ERR_UNSUPPORTED, with
+ * nothing launched, where H is too large for the router's shared memory (E8 = E rounded up to a multiple of 8:
+ * H + 72 E8 > 409,600 with T <= 16; H + 72 E8 > 204,800 with more), or F beyond 2^26.
  */
 int moe_mx4_layer_workspace(int T, int H, int F, int E, int k, size_t *bytes);
 int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int E, int k, const uint16_t *w_router,

@@ -786,13 +786,26 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
 
 // ------------------------------------------------------------------ host
 
+// Most dynamic shared memory of the first kernel (its static arrays, about 1 KB, come on top).
+#define MXL_PREP_SMEM (200 * 1024)
+
 template <int XT, int TT>
 int launch_prep_t(const PrepParams &p, cudaStream_t s) {
     const size_t smem = prep_smem(p.H, p.E, TT);
-    if (smem > 200 * 1024) return MOE_ERR_UNSUPPORTED;
-    if (smem > 48 * 1024)
-        MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_prep_kernel<XT, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)smem));
+    // the limit is raised once, to the most: another thread's call may come between this and the launch
+    static std::mutex mu;
+    static bool raised[64] = {false};
+    int dev = -1;
+    MOE_TRY_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!raised[dev]) {
+            MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_prep_kernel<XT, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              MXL_PREP_SMEM));
+            raised[dev] = true;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     moe_pdl_config(&cfg, attr, dim3(MXL_CLUSTER, (p.T + TT - 1) / TT), dim3(MXL_PREP_THREADS), smem, s);
@@ -805,11 +818,11 @@ int launch_prep_t(const PrepParams &p, cudaStream_t s) {
 }
 
 static_assert(MOE_DECODE_MAX_T <= 2 * MXL_MAX_CLUSTERS, "two tokens a cluster at most");
+int cluster_tokens(int T) { return T <= MXL_MAX_CLUSTERS ? 1 : 2; }
 
 template <int XT>
 int launch_prep(const PrepParams &p, cudaStream_t s) {
-    if (p.T <= MXL_MAX_CLUSTERS) return launch_prep_t<XT, 1>(p, s);
-    return launch_prep_t<XT, 2>(p, s);
+    return cluster_tokens(p.T) == 1 ? launch_prep_t<XT, 1>(p, s) : launch_prep_t<XT, 2>(p, s);
 }
 
 // Shared memory of a block, less the alignment of its start.
@@ -828,7 +841,7 @@ int launch_layer_t(FfnParams &p, cudaStream_t s) {
         front = G::CTRL;
     }
     p.S = std::min<int>(G::MAXS, (MXL_SMEM - front) / p.stage);
-    if (p.S < 2) return MOE_ERR_UNSUPPORTED;
+    static_assert((MXL_SMEM - G::CTRL) / (MXL_WBYTES + NR * MXL_ROW + 511) >= 4, "a ring");
     static std::mutex mu;
     static int sms[64] = {0};
     int dev = -1, n = 0;
@@ -878,6 +891,7 @@ extern "C" int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int 
     if ((rc = mx4_pool_check(H, F, n_slots, pool, slot_bytes)) != MOE_OK) return rc;
     // a unit travels in a word with 20 bits for its tile (H stays far below by the router's shared memory)
     if ((F + 63L) / 64 > 1 << 20) return MOE_ERR_UNSUPPORTED;
+    if (prep_smem(H, E, cluster_tokens(T)) > MXL_PREP_SMEM) return MOE_ERR_UNSUPPORTED;
     const LayerWs L = layer_ws(T, H, F, k);
     uint8_t *w = (uint8_t *)workspace;
     cudaStream_t st = moe_cuda_stream(s);

@@ -173,3 +173,14 @@ def test_layer_swiglu_of_every_gate(T):
     assert (got == got[0]).all()
     err = np.abs(got[0] - want)
     assert (err <= tol).all(), (gates[err > tol], (err / np.maximum(np.abs(want), 1e-300))[err > tol])
+
+
+# ------------------------------------------------------------------ long rows
+
+@pytest.mark.parametrize("T,H,E", [(32, 48000, 8), (17, 204224, 1), (2, 96000, 3)])
+def test_layer_long_router_rows(T, H, E):
+    """The first: a little less than 48 KB of shared memory, beside what the kernel declares; the second: the
+    longest rows of more than 16 tokens."""
+    l = Layer(T, H, 32, E, 1, seed=5, extra=False)
+    l.check(*l.run(), tokens=[0, T // 2, T - 1])
+    assert L.moe_device_status() == 0

@@ -1,0 +1,34 @@
+"""MXFP4 on the host: limits of sizes (no GPU)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import mx4_reference as ref
+from routed_expert_ffn_gemv_gb300 import _build, _lib as L
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return L.load()
+
+
+@pytest.fixture(scope="module")
+def ptr():
+    a = np.zeros(4096 + 256, np.uint8)
+    ptr.keep = a
+    return a.ctypes.data + (-a.ctypes.data) % 256
+
+
+def layer(lib, p, T, H, F, E, k=1):
+    """A layer call whose sizes are refused before anything is read."""
+    return lib.moe_mx4_layer(p, L.MOE_F32, T, H, F, E, k, p, None, None, 1, p, ref.slot_bytes(H, F), None, p, None, None, p,
+                             1 << 50, None)
+
+
+@pytest.mark.parametrize("T,E", [(1, 1), (16, 8), (16, 256), (17, 1), (32, 8), (32, 250)])
+def test_layer_refuses_rows_past_the_routers_shared_memory(lib, ptr, T, E):
+    most = (409600 if T <= 16 else 204800) - 72 * ((E + 7) // 8 * 8)
+    H = most // 32 * 32 + 32
+    assert layer(lib, ptr, T, H, 32, E) == L.MOE_ERR_UNSUPPORTED
