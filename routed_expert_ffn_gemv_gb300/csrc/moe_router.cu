@@ -645,7 +645,9 @@ int moe_router_topk_impl(const void *x, int xtype, int T, int H, const uint16_t 
         return router_tiled_launch(x, xtype, T, H, w_router, bias, E, k, ids, weights, logits, min_weight, s);
     }
     const RouterSmem L = router_smem_layout(H, E);
-    if (L.total > 200 * 1024) return MOE_ERR_UNSUPPORTED;
+    // every call sets the same limit: with its own size, a thread could lower it between another's set and launch
+    constexpr int most = 200 * 1024;
+    if (L.total > most) return MOE_ERR_UNSUPPORTED;
     const int HS = H / MOE_ROUTER_CLUSTER;
     const size_t wbytes = (size_t)HS * E * 2;
     const int use_bulk = ((uintptr_t)w_router % 16 == 0) && (wbytes % 16 == 0) &&
@@ -668,12 +670,12 @@ int moe_router_topk_impl(const void *x, int xtype, int T, int H, const uint16_t 
     cfg.numAttrs = 2;
     if (xtype == MOE_F32) {
         MOE_TRY_CUDA(cudaFuncSetAttribute(router_topk_kernel<MOE_F32>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.total));
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, most));
         MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, router_topk_kernel<MOE_F32>, x, T, H, w_router, bias, E,
                                         k, ids, weights, logits, use_bulk, status, min_weight, (int)w_ready));
     } else {
         MOE_TRY_CUDA(cudaFuncSetAttribute(router_topk_kernel<MOE_BF16>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.total));
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, most));
         MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, router_topk_kernel<MOE_BF16>, x, T, H, w_router, bias,
                                         E, k, ids, weights, logits, use_bulk, status, min_weight, (int)w_ready));
     }

@@ -42,3 +42,34 @@ def test_router_inputs_of_the_kernel_before(T, H, E, off, last):
             b.add_(bf)
         call(1)
         assert torch.equal(ids[1], ids[0]) and torch.equal(wt[1], wt[0]) and torch.equal(logits[1], logits[0]), i
+
+
+def test_router_calls_of_two_threads():
+    """Two host threads with routers of different sizes, a stream each."""
+    import threading
+    errors = []
+
+    def work(H, E, seed):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                g = torch.Generator(device="cuda")
+                g.manual_seed(seed)
+                x = torch.randn(4, H, generator=g, device="cuda")
+                w = (torch.randn(H, E, generator=g, device="cuda") / H ** 0.5).half()
+                ids, wt = torch.zeros(4, 2, dtype=torch.int32, device="cuda"), torch.zeros(4, 2, device="cuda")
+                for _ in range(500):
+                    L.moe_router_topk(x, L.MOE_F32, 4, H, w, None, E, 2, ids, wt, None, s)
+                logits = x.double() @ w.double()
+            s.synchronize()
+            if not torch.equal(torch.topk(logits, 2).indices.int(), ids):
+                errors.append("ids")
+        except Exception as e:  # handed to the main thread
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=a) for a in ((2048, 128, 1), (256, 8, 2), (1024, 128, 3))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
