@@ -475,8 +475,8 @@ int moe_mx4_dequantize_experts(const void *pool, size_t slot_bytes, const int32_
  *                      slot_bytes 256-byte aligned.
  *   h                  device [T*k][F] out, htype MOE_F32 or MOE_BF16; partial device [T][k][H] fp32,
  *                      16-byte aligned.
- *   workspace          device, moe_mx4_expert_workspace() bytes, 256-byte aligned; needs no
- *                      initial contents; one per call in flight.
+ *   workspace          device, moe_mx4_expert_workspace() bytes (no fewer for more tokens, or a larger H or
+ *                      F), 256-byte aligned; needs no initial contents; one per call in flight.
  * H, F multiples of 32; T >= 0 (0: no-op), E <= MOE_MAX_E, k <= MOE_MAX_K, k <= E, T*k <= 2^24.
  */
 int moe_mx4_expert_workspace(int T, int H, int F, int E, int k, size_t *bytes);

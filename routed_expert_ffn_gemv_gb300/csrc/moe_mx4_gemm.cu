@@ -44,32 +44,6 @@ namespace {
 // 11.7 against 14.2, over 8 (four rows to a TMA copy, 128 rows a chunk) 19.9 against 20.3.
 #define MX4_LOCAL_R 2048
 
-struct GemmWs {
-    int max_chunks;
-    size_t o_rows, o_slot, o_pos, o_n, o_hist, ints;  // in ints; [0] is the number of chunks
-    size_t Rp;                                // positions: every expert's start at a multiple of 8
-    size_t codes, scales, total;              // in bytes
-};
-
-GemmWs gemm_ws(int T, int H, int F, int E, int k, int NT) {
-    GemmWs L;
-    const long R = (long)T * k;
-    L.max_chunks = (int)(R / NT + std::min<long>(E, R));
-    L.Rp = (size_t)(R + 7 * std::min<long>(E, R) + 7) / 8 * 8;
-    size_t o = 16;
-    L.o_rows = o; o += L.Rp;
-    L.o_slot = o; o += L.max_chunks;
-    L.o_pos = o;  o += L.max_chunks;
-    L.o_n = o;    o += L.max_chunks;
-    L.o_hist = o; o += (size_t)MXG_ROUTE_BLOCKS * E;
-    L.ints = o;
-    L.codes = (o * 4 + 1023) / 1024 * 1024;
-    const size_t stages = (std::max(H, F) + 255) / 256, rows = R > MX4_LOCAL_R ? stages * L.Rp : 0;
-    L.scales = L.codes + rows * 128;
-    L.total = L.scales + rows * 8;
-    return L;
-}
-
 // Most routes of a chunk: a few where experts have few (more stages in the ring), else as wide as tensor
 // and shared memory allow, which is less beside the tables of LOCAL.  The larger saves passes over the
 // weights: 32768 routes over 128 experts are 241 chunks of at most 176, 227 of at most 192.
@@ -79,6 +53,35 @@ GemmWs gemm_ws(int T, int H, int F, int E, int k, int NT) {
 int chunk_routes(int T, int E, int k) {
     const long R = (long)T * k;
     return R <= 16L * E ? MXG_NT_SMALL : R <= MX4_LOCAL_R ? MXG_NT_LOCAL : MXG_NT_LARGE;
+}
+
+struct GemmWs {
+    size_t o_rows, o_slot, o_pos, o_n, o_hist, ints;  // in ints; [0] is the number of chunks
+    size_t Rp;                                // positions: every expert's start at a multiple of 8
+    size_t codes, scales, total;              // in bytes
+};
+
+// Chunks of at most NT routes that R routes can make.
+int most_chunks(long R, int E, int NT) { return (int)(R / NT + std::min<long>(E, R)); }
+
+// (the tables hold the chunks of the smallest kind, so that the size grows with T whatever kind a call takes)
+GemmWs gemm_ws(int T, int H, int F, int E, int k) {
+    GemmWs L;
+    const long R = (long)T * k;
+    const int max_chunks = most_chunks(R, E, MXG_NT_SMALL);
+    L.Rp = (size_t)(R + 7 * std::min<long>(E, R) + 7) / 8 * 8;
+    size_t o = 16;
+    L.o_rows = o; o += L.Rp;
+    L.o_slot = o; o += max_chunks;
+    L.o_pos = o;  o += max_chunks;
+    L.o_n = o;    o += max_chunks;
+    L.o_hist = o; o += (size_t)MXG_ROUTE_BLOCKS * E;
+    L.ints = o;
+    L.codes = (o * 4 + 1023) / 1024 * 1024;
+    const size_t stages = (std::max(H, F) + 255) / 256, rows = R > MX4_LOCAL_R ? stages * L.Rp : 0;
+    L.scales = L.codes + rows * 128;
+    L.total = L.scales + rows * 8;
+    return L;
 }
 
 // ------------------------------------------------------------------ routes by expert
@@ -724,7 +727,7 @@ int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, i
                 const int32_t *ids, const float *weights, const int32_t *table, int n_slots, const void *pool,
                 size_t slot_bytes, void *out, int otype, void *workspace, cudaStream_t s) {
     const int NT = chunk_routes(T, E, k);
-    const GemmWs L = gemm_ws(T, H, F, E, k, NT);
+    const GemmWs L = gemm_ws(T, H, F, E, k);
     int32_t *w = (int32_t *)workspace;
     GemmParams p;
     p.K = down ? F : H;
@@ -756,6 +759,7 @@ int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, i
     p.MT = down ? (H + 127) / 128 : (F + 63) / 64;
     p.mat = down ? mx4_gu_bytes(H, F) : 0;
     p.status = moe_status_word_device_ptr();
+    const int max_chunks = most_chunks(p.R, E, NT);
 
     if (p.R > MX4_LOCAL_R) {
         cudaLaunchConfig_t cfg = {};
@@ -768,9 +772,9 @@ int run_product(bool down, const uint8_t *codes, const uint8_t *scales, int T, i
                                         (const int32_t *)(w + L.o_hist), codes, scales, p.K, p.div, L.Rp, w,
                                         w + L.o_rows, w + L.o_slot, w + L.o_pos, w + L.o_n, xg, sg, p.status));
     }
-    if (down) return launch_gemm<true, MOE_F32>(p, NT, L.max_chunks, s);
-    return otype == MOE_BF16 ? launch_gemm<false, MOE_BF16>(p, NT, L.max_chunks, s)
-                             : launch_gemm<false, MOE_F32>(p, NT, L.max_chunks, s);
+    if (down) return launch_gemm<true, MOE_F32>(p, NT, max_chunks, s);
+    return otype == MOE_BF16 ? launch_gemm<false, MOE_BF16>(p, NT, max_chunks, s)
+                             : launch_gemm<false, MOE_F32>(p, NT, max_chunks, s);
 }
 
 }  // namespace
@@ -792,7 +796,7 @@ extern "C" int moe_mx4_expert_workspace(int T, int H, int F, int E, int k, size_
     MOE_CHECK(bytes);
     const int rc = mx4_ffn_check(T, H, F, E, k);
     if (rc != MOE_OK) return rc;
-    *bytes = (gemm_ws(T, H, F, E, k, chunk_routes(T, E, k)).total + 255) / 256 * 256;
+    *bytes = (gemm_ws(T, H, F, E, k).total + 255) / 256 * 256;
     return MOE_OK;
 }
 

@@ -32,3 +32,20 @@ def test_layer_refuses_rows_past_the_routers_shared_memory(lib, ptr, T, E):
     most = (409600 if T <= 16 else 204800) - 72 * ((E + 7) // 8 * 8)
     H = most // 32 * 32 + 32
     assert layer(lib, ptr, T, H, 32, E) == L.MOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 8), (96, 8), (128, 1), (129, 8), (256, 3), (256, 8)])
+def test_workspaces_grow_with_the_call(lib, E, k):
+    """A workspace of a larger call serves every smaller one of the same experts."""
+    most = 0
+    for T in list(range(1, 700)) + [1000, 1023, 1024, 2047, 2048, 2049, 4095, 4096, 20000]:
+        n = L.moe_mx4_expert_workspace(T, 160, 96, E, k)
+        assert n >= most, T
+        most = n
+    for H, F in ((32, 32), (128, 96), (160, 64)):
+        assert L.moe_mx4_expert_workspace(20000, H, F, E, k) <= most
+    most = 0
+    for T in range(1, L.MOE_DECODE_MAX_T + 1):
+        n = L.moe_mx4_layer_workspace(T, 160, 96, E, k)
+        assert n >= most, T
+        most = n
