@@ -190,7 +190,8 @@ typedef struct {
      *   one access per distinct (layer, expert); a miss whose count, this access included,
      *   is below admit_after takes no slot and changes no LRU state ("bypassed": its slot
      *   is reported as -1 and its weights are read from its pinned host image, see
-     *   moe_expert_ffn_fill); it still counts as a miss.  Values 0 and 1 mean plain LRU.
+     *   moe_expert_ffn_fill); it still counts as a miss.  Values 0 and 1 mean plain LRU, and
+ *   are the only ones for MOE_MXFP4 pools (MOE_ERR_UNSUPPORTED: their products read slots).
      * lru_window: W tokens (page 1, section 4.3, --moe-lru-window: an expert not used within
      *   the last W tokens is unloaded).  The pool's token clock advances by the ubatch's
      *   token count at every request for the group's first layer; before each request every

@@ -519,8 +519,9 @@ extern "C" int moe_cache_create(const moe_cache_desc *desc, moe_cache **out) {
     MOE_CHECK(d.n_slots >= 1);
     MOE_CHECK(d.admit_after >= 0 && d.lru_window >= 0);
     if (d.device_managed && d.lru_window > 0) return MOE_ERR_UNSUPPORTED;
-    // the kernels that fill a device-managed pool read q8_0 and 4-bit images only
-    if (d.device_managed && d.qtype == MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
+    // the kernels that fill a device-managed pool, or read a bypassed expert's host image, take q8_0 and 4-bit
+    // images only
+    if ((d.device_managed || d.admit_after > 1) && d.qtype == MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
     const size_t img = moe_expert_image_bytes(d.qtype, d.H, d.F);
     MOE_CHECK(d.slot_bytes >= img && d.slot_bytes % 256 == 0);
     MOE_CHECK(d.device_pool && ((uintptr_t)d.device_pool % 256) == 0);

@@ -49,3 +49,22 @@ def test_workspaces_grow_with_the_call(lib, E, k):
         n = L.moe_mx4_layer_workspace(T, 160, 96, E, k)
         assert n >= most, T
         most = n
+
+
+def cache_desc(ptr, **kw):
+    images = (ctypes.c_void_p * 4)(*[ptr] * 4)
+    d = L.CacheDesc(qtype=L.MOE_MXFP4, H=128, F=64, n_layers=1, n_experts=4, first_layer=0, n_slots=4,
+                    slot_bytes=ref.slot_bytes(128, 64), device_pool=ptr, host_images=images)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    d.keep = images
+    return d
+
+
+@pytest.mark.parametrize("admit_after", [2, 7])
+def test_pool_refuses_admission_of_experts_that_only_stay_on_the_host(lib, ptr, admit_after):
+    """A bypassed expert would be read from its pinned image, which no MXFP4 call does."""
+    out = ctypes.c_void_p()
+    d = cache_desc(ptr, admit_after=admit_after)
+    assert lib.moe_cache_create(ctypes.byref(d), ctypes.byref(out)) == L.MOE_ERR_UNSUPPORTED
+    assert not out.value
