@@ -478,7 +478,8 @@ int moe_mx4_dequantize_experts(const void *pool, size_t slot_bytes, const int32_
  *                      16-byte aligned.
  *   workspace          device, moe_mx4_expert_workspace() bytes (no fewer for more tokens, or a larger H or
  *                      F), 256-byte aligned; needs no initial contents; one per call in flight.
- * H, F multiples of 32; T >= 0 (0: no-op), E <= MOE_MAX_E, k <= MOE_MAX_K, k <= E, T*k <= 2^24.
+ * H, F multiples of 32; T >= 0 (0: no-op), E <= MOE_MAX_E, k <= MOE_MAX_K, k <= E, T*k <= 2^24;
+ * MOE_ERR_UNSUPPORTED for H or F beyond 2^28.
  */
 int moe_mx4_expert_workspace(int T, int H, int F, int E, int k, size_t *bytes);
 int moe_mx4_expert_gateup(const uint8_t *x_codes, const uint8_t *x_scales, int T, int H, int F, int E, int k,

@@ -783,6 +783,8 @@ int mx4_ffn_check(int T, int H, int F, int E, int k) {
     MOE_CHECK(T >= 0 && H > 0 && F > 0 && H % 32 == 0 && F % 32 == 0);
     MOE_CHECK(E >= 1 && E <= MOE_MAX_E && k >= 1 && k <= MOE_MAX_K && k <= E);
     MOE_CHECK((long long)T * k <= 1 << 24);
+    // a row of h in bytes, a tile's columns and the number of work items are ints in the kernels
+    if (H > 1 << 28 || F > 1 << 28) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

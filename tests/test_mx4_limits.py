@@ -68,3 +68,18 @@ def test_pool_refuses_admission_of_experts_that_only_stay_on_the_host(lib, ptr, 
     d = cache_desc(ptr, admit_after=admit_after)
     assert lib.moe_cache_create(ctypes.byref(d), ctypes.byref(out)) == L.MOE_ERR_UNSUPPORTED
     assert not out.value
+
+
+@pytest.mark.parametrize("H,F", [(32, (1 << 28) + 32), ((1 << 28) + 32, 32), (32, (1 << 31) - 32), ((1 << 31) - 32, 64)])
+def test_calls_refuse_rows_past_their_offsets(lib, ptr, H, F):
+    """A row of h of 2^29 fp32 elements has more bytes than the kernels' row offsets, and (2^31 rounded up to a
+    tile) is no int."""
+    out, sb = ctypes.c_size_t(), 1 << 46
+    un = L.MOE_ERR_UNSUPPORTED
+    assert lib.moe_mx4_expert_workspace(4, H, F, 4, 2, ctypes.byref(out)) == un
+    assert lib.moe_mx4_layer_workspace(4, H, F, 4, 2, ctypes.byref(out)) == un
+    assert lib.moe_mx4_expert_gateup(ptr, ptr, 4, H, F, 4, 2, ptr, None, 4, ptr, sb, ptr, L.MOE_F32, ptr, sb, None) == un
+    assert lib.moe_mx4_expert_down(ptr, ptr, 4, H, F, 4, 2, ptr, ptr, None, 4, ptr, sb, ptr, ptr, sb, None) == un
+    assert lib.moe_mx4_layer(ptr, L.MOE_F32, 4, H, F, 4, 2, ptr, None, None, 4, ptr, sb, None, ptr, None, None, ptr, sb,
+                             None) == un
+    assert lib.moe_mx4_expert_workspace(4, 32, 1 << 28, 4, 2, ctypes.byref(out)) == L.MOE_OK
