@@ -77,10 +77,10 @@ __host__ __device__ static inline int moe_scale_in_block(int qtype, int lane) {
 // (see moe_pack_expert in moe.h).
 #define MX4_TB 8704
 __host__ __device__ static inline size_t mx4_gu_bytes(int H, int F) {
-    return (size_t)((F + 63) / 64) * ((H + 127) / 128) * MX4_TB;
+    return (size_t)((F - 1) / 64 + 1) * ((H - 1) / 128 + 1) * MX4_TB;  // (no sum past an int)
 }
 __host__ __device__ static inline size_t mx4_down_bytes(int H, int F) {
-    return (size_t)((H + 127) / 128) * ((F + 127) / 128) * MX4_TB;
+    return (size_t)((H - 1) / 128 + 1) * ((F - 1) / 128 + 1) * MX4_TB;
 }
 // byte offsets in a matrix of B column blocks: the code byte of (tile row, column), and its scale
 __host__ __device__ static inline size_t mx4_tile_offset(int B, int row, int col) {

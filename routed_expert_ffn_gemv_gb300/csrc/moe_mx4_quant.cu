@@ -89,7 +89,7 @@ template <int XT>
 __device__ __forceinline__ Mx4Tile mx4_tile_of(const void *gate, const void *up, const void *down, int i, int H, int F,
                                                int tile) {
     const size_t es = XT == MOE_BF16 ? 2 : 4;
-    const int HB = (H + 127) / 128, FB = (F + 127) / 128, gu = (F + 63) / 64 * HB;
+    const int HB = (H - 1) / 128 + 1, FB = (F - 1) / 128 + 1, gu = ((F - 1) / 64 + 1) * HB;
     Mx4Tile t;
     const size_t base = (size_t)i * H * F * es;
     if (tile < gu) {

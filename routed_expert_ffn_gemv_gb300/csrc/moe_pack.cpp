@@ -72,7 +72,7 @@ void mx4_rows(uint8_t *tiles, int B, int tile_row, int NB, uint8_t *aos_row) {
 
 template <bool PACK>
 void mx4_expert(int H, int F, uint8_t *image, uint8_t *gate, uint8_t *up, uint8_t *down) {
-    const int HB = (H + 127) / 128, FB = (F + 127) / 128;
+    const int HB = (H - 1) / 128 + 1, FB = (F - 1) / 128 + 1;
     const size_t gu_row = (size_t)H / 32 * 17, down_row = (size_t)F / 32 * 17;
     if (PACK) memset(image, 0, moe_expert_image_bytes(MOE_MXFP4, H, F));
     for (int f = 0; f < F; ++f) {

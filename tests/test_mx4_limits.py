@@ -83,3 +83,10 @@ def test_calls_refuse_rows_past_their_offsets(lib, ptr, H, F):
     assert lib.moe_mx4_layer(ptr, L.MOE_F32, 4, H, F, 4, 2, ptr, None, None, 4, ptr, sb, None, ptr, None, None, ptr, sb,
                              None) == un
     assert lib.moe_mx4_expert_workspace(4, 32, 1 << 28, 4, 2, ctypes.byref(out)) == L.MOE_OK
+
+
+def test_image_size_of_the_longest_rows(lib):
+    """Rows rounded up to a tile do not wrap."""
+    n = (1 << 31) - 32
+    assert L.moe_slot_image_bytes(L.MOE_MXFP4, 32, n) == ((1 << 25) + (1 << 24)) * 8704
+    assert L.moe_slot_image_bytes(L.MOE_MXFP4, n, 32) == ((1 << 24) + (1 << 24)) * 8704
