@@ -114,7 +114,7 @@ struct PrepParams {
     const void *x;
     const uint16_t *w_router;
     const float *bias;
-    int T, H, E, k, wide_w;
+    int T, H, E, k;
     int32_t *ids;
     float *weights;
     uint8_t *xq, *xsc;  // [stage][token] of 1024, of MXL_SC bytes
@@ -139,8 +139,9 @@ __device__ __forceinline__ void half8(const uint4 &u, float (&w)[8]) {
 
 // TT: tokens of a cluster (the last one may hold fewer).  Few tokens to a cluster and up to 16 clusters:
 // the router's sums, not its reads of w_router from L2, take the time.  The kernel is a chain of
-// latencies, instruction fetches among them: loops are kept rolled.
-template <int XT, int TT>
+// latencies, instruction fetches among them: loops are kept rolled.  WIDE: rows of w_router in 16-byte loads
+// (E a multiple of 8, 16-byte aligned); otherwise element by element, every load of a row before its first use.
+template <int XT, int TT, bool WIDE>
 __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid_constant__ PrepParams p) {
     extern __shared__ __align__(16) float sm[];
     __shared__ __align__(16) uint32_t key[MOE_MAX_E];
@@ -164,26 +165,24 @@ __global__ void __launch_bounds__(MXL_PREP_THREADS) mx4_prep_kernel(const __grid
             a[i] = make_uint4(0, 0, 0, 0);
             if (h < HS && ne > 0) {
                 const uint16_t *src = wr + (size_t)h * p.E;
-                if (p.wide_w) {
+                if (WIDE) {
                     a[i] = *(const uint4 *)src;
                 } else {
-                    uint32_t q[4] = {0, 0, 0, 0};
-#pragma unroll 1
-                    for (int j = 0; j < min(8, ne); ++j) {
-                        const uint32_t v = (uint32_t)src[j] << (16 * (j & 1));
-                        if (j < 2) q[0] |= v;
-                        else if (j < 4) q[1] |= v;
-                        else if (j < 6) q[2] |= v;
-                        else q[3] |= v;
-                    }
-                    a[i] = make_uint4(q[0], q[1], q[2], q[3]);
+                    uint32_t v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = j < ne ? src[j] : 0;
+                    a[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
                 }
             }
         }
     };
     // the router's weights, too, may come from the kernel before: ahead of the wait they are only brought to L2
     // (this CTA's rows are one run of bytes)
-    if (p.wide_w && tid == 0 && blockIdx.y == 0) bulk_prefetch_l2(p.w_router + (size_t)h0 * p.E, (uint32_t)HS * p.E * 2u);
+    if (tid == 0 && blockIdx.y == 0) {
+        const uintptr_t w0 = (uintptr_t)(p.w_router + (size_t)h0 * p.E), w1 = w0 + (size_t)HS * p.E * 2;
+        const uintptr_t a0 = (w0 + 15) & ~(uintptr_t)15, a1 = w1 & ~(uintptr_t)15;
+        if (a1 > a0) bulk_prefetch_l2((const void *)a0, (uint32_t)(a1 - a0));
+    }
     pdl_wait();
     pdl_trigger();  // not before: the next kernel reads its slot table before its own wait
     uint4 wa[PRE], wb[PRE];
@@ -300,13 +299,14 @@ struct FfnParams {
     float *partial, *y;
     int *ticket, *ready, *done;
     int *status;
-    int res;      // bytes of resident digits and scales (0: copied by stage)
+    int res, xsr; // bytes of resident digits and of x's resident scales (0: copied by stage)
     int S, stage; // ring stages, bytes of one
 };
 
-// Shared memory: control, the tokens' digits and scales (resident: T <= NR = 8, and enough of the ring left),
-// then S stages of two weight blocks and `cap` routes' digits (1024 bytes each: two 512-byte atoms of 8
-// rows x 128 columns) followed by their scales.
+// Shared memory: control, the tokens' digits (resident: T <= NR = 8) and their scales (resident where, like the
+// digits, they leave four stages of the ring), then S stages of two weight blocks and `cap` routes' digits (1024
+// bytes each: two 512-byte atoms of 8 rows x 128 columns) followed by their scales.  (Scales copied a row at a
+// time with each stage: 32 tokens, Qwen-shaped, 61.7 us against 59.8.)
 template <int NR>
 struct LayerGeom {
     static constexpr int N = NR * 8;
@@ -427,7 +427,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
     float *s_w = (float *)(s_on + MXL_MAX_R);                // [MXL_MAX_R] router weights
     int *s_table = (int *)(s_w + MXL_MAX_R);                 // [MOE_MAX_E]
     uint8_t *xres = smem + G::CTRL;
-    uint8_t *ring = xres + (p.res + 511) / 512 * 512;
+    const uint8_t *xsres = xres + p.res;
+    uint8_t *ring = xres + p.res + (p.xsr + 511) / 512 * 512;
     const int S = p.S, STAGE = p.stage;
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -465,13 +466,13 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
     int claim = 0;
     if (tid == 0) {
         claim = atomicAdd(p.ticket, 1);
+        if (p.xsr) {
+            mbar_arrive_expect_tx(xs_full, (uint32_t)p.xsr);
+            bulk_g2s(xres + p.res, p.xsc, (uint32_t)p.xsr, xs_full);
+        }
         if (p.res) {
-            // (the scales by themselves: they are a few bytes, and their warps come first)
-            const uint32_t sb = (uint32_t)p.res / MXL_ROW * MXL_SC, xb = (uint32_t)p.res - sb;
-            mbar_arrive_expect_tx(xs_full, sb);
-            bulk_g2s(xres + xb, p.xsc, sb, xs_full);
-            mbar_arrive_expect_tx(x_full, xb);
-            bulk_g2s(xres, p.xq, xb, x_full);
+            mbar_arrive_expect_tx(x_full, (uint32_t)p.res);
+            bulk_g2s(xres, p.xq, (uint32_t)p.res, x_full);
         }
     }
     const int R = p.T * p.k;
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
 
     if (nch == 0) {
         // no expert is resident: the layer is its extra
-        if (tid == 0 && p.res && mbar_wait_role(xs_full, 0, p.status, abort_flag))
+        if (tid == 0 && (!p.xsr || mbar_wait_role(xs_full, 0, p.status, abort_flag)) && p.res)
             mbar_wait_role(x_full, 0, p.status, abort_flag);
         for (int m = blockIdx.x; m < HT; m += gridDim.x)
             if (tid < 128)
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                 if (un.kind == MXL_COMBINE) continue;
                 const bool down = un.kind == MXL_DOWN;
                 const int KB = down ? FB : HB, NKS = (KB + 1) / 2, n = __shfl_sync(0xffffffffu, ch.n[un.c], 0);
-                const uint32_t nb = down || !p.res ? (uint32_t)n * MXL_ROW : 0u;
+                const uint32_t nb = (uint32_t)n * (down ? MXL_ROW : (p.res ? 0 : 1024) + (p.xsr ? 0 : MXL_SC));
                 const uint8_t *w = p.pool + (size_t)__shfl_sync(0xffffffffu, ch.slot[un.c], 0) * p.slot_bytes +
                                    (down ? down_off : 0) + (size_t)un.m * KB * MX4_TB;
                 for (int kc = 0; kc < NKS; ++kc, advance(), ++fills, w += MXL_WBYTES) {
@@ -541,8 +542,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                 }
             }
             // never leave with copies in flight: the last fill of every stage
-            if (ok && p.res)
-                ok = mbar_wait_role(xs_full, 0, p.status, abort_flag) && mbar_wait_role(x_full, 0, p.status, abort_flag);
+            if (ok && p.xsr) ok = mbar_wait_role(xs_full, 0, p.status, abort_flag);
+            if (ok && p.res) ok = mbar_wait_role(x_full, 0, p.status, abort_flag);
             for (int i = 0; ok && i < S && i < fills; ++i) {
                 if (--s < 0) {
                     s = S - 1;
@@ -598,7 +599,8 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
                 } else if (!p.res && lane < n) {
                     const size_t at = (size_t)kc * p.T + tok;
                     bulk_g2s(st + MXL_WBYTES + lane * 1024, p.xq + at * 1024, 1024, &s_full[s]);
-                    bulk_g2s(st + MXL_WBYTES + n * 1024 + lane * MXL_SC, p.xsc + at * MXL_SC, MXL_SC, &s_full[s]);
+                    if (!p.xsr)
+                        bulk_g2s(st + MXL_WBYTES + n * 1024 + lane * MXL_SC, p.xsc + at * MXL_SC, MXL_SC, &s_full[s]);
                 }
                 __syncwarp();
             }
@@ -661,28 +663,33 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
         // ---------------- scales: the weights' rows lane, lane + 32, ..; a route's (a resident token's) for its 8
         // columns
         const uint32_t t0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::SFCOL;
-        const int HK = (HB + 1) / 2;
-        bool ok = true, xok = !p.res;
+        bool ok = true, xok = false;
         for (int i = 0; ok; ++i) {
             const Unit un = next_unit(i);
             if (un.kind == MXL_COMBINE) continue;
             if (un.kind > MXL_COMBINE) break;
             const bool down = un.kind == MXL_DOWN;
             const int KB = down ? FB : HB, NKS = (KB + 1) / 2, n = ch.n[un.c];
-            const bool all = !down && p.res;
-            if (all && !xok && !(ok = xok = mbar_wait_warp(xs_full, 0, p.status, abort_flag))) break;
+            const bool resident = !down && p.xsr;
+            if (resident && !xok && !(ok = xok = mbar_wait_warp(xs_full, 0, p.status, abort_flag))) break;
+            // (rows past the chunk's or the tokens: unused columns, any scale)
+            int row[NR / 4];
+#pragma unroll
+            for (int c = 0; c < NR / 4; ++c) {
+                const int r = 4 * c + (lane >> 3);
+                row[c] = MXL_SC * (!resident ? r : p.res ? min(r, p.T - 1) : r < n ? ch.rows[ch.pos[un.c] + r] / p.k : 0);
+            }
             for (int kc = 0; kc < NKS; ++kc, advance()) {
                 const uint8_t *st = ring + (size_t)s * STAGE;
-                // (rows past the chunk's or the tokens read whatever follows in shared memory: unused columns)
                 uint2 w[NR / 4];
                 auto row_scales = [&](const uint8_t *rs) {
 #pragma unroll
-                    for (int c = 0; c < NR / 4; ++c) w[c] = *(const uint2 *)(rs + (4 * c + (lane >> 3)) * MXL_SC);
+                    for (int c = 0; c < NR / 4; ++c) w[c] = *(const uint2 *)(rs + row[c]);
                 };
-                if (all) row_scales(xres + (HK * 1024 + kc * MXL_SC) * p.T);
+                if (resident) row_scales(xsres + kc * p.T * MXL_SC);
                 if (!(ok = mbar_wait_warp(&s_full[s], ph, p.status, abort_flag))) break;
                 tc_fence_after();
-                if (!all) row_scales(st + MXL_WBYTES + n * 1024);
+                if (!resident) row_scales(st + MXL_WBYTES + n * 1024);
                 const bool two = 2 * kc + 1 < KB;
                 const uint4 a = *(const uint4 *)(st + 8192 + 16 * lane);
                 uint4 b = make_uint4(0, 0, 0, 0);
@@ -789,7 +796,7 @@ __global__ void __launch_bounds__(MXL_THREADS, 1) mx4_layer_kernel(const __grid_
 // Most dynamic shared memory of the first kernel (its static arrays, about 1 KB, come on top).
 #define MXL_PREP_SMEM (200 * 1024)
 
-template <int XT, int TT>
+template <int XT, int TT, bool WIDE>
 int launch_prep_t(const PrepParams &p, cudaStream_t s) {
     const size_t smem = prep_smem(p.H, p.E, TT);
     // the limit is raised once, to the most: another thread's call may come between this and the launch
@@ -801,7 +808,7 @@ int launch_prep_t(const PrepParams &p, cudaStream_t s) {
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!raised[dev]) {
-            MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_prep_kernel<XT, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            MOE_TRY_CUDA(cudaFuncSetAttribute(mx4_prep_kernel<XT, TT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               MXL_PREP_SMEM));
             raised[dev] = true;
         }
@@ -813,7 +820,7 @@ int launch_prep_t(const PrepParams &p, cudaStream_t s) {
     attr[1].val.clusterDim.x = MXL_CLUSTER;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
-    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_prep_kernel<XT, TT>, p));
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, mx4_prep_kernel<XT, TT, WIDE>, p));
     return MOE_OK;
 }
 
@@ -822,7 +829,9 @@ int cluster_tokens(int T) { return T <= MXL_MAX_CLUSTERS ? 1 : 2; }
 
 template <int XT>
 int launch_prep(const PrepParams &p, cudaStream_t s) {
-    return cluster_tokens(p.T) == 1 ? launch_prep_t<XT, 1>(p, s) : launch_prep_t<XT, 2>(p, s);
+    const bool wide = p.E % 8 == 0 && ((uintptr_t)p.w_router & 15) == 0;
+    if (cluster_tokens(p.T) == 1) return wide ? launch_prep_t<XT, 1, true>(p, s) : launch_prep_t<XT, 1, false>(p, s);
+    return wide ? launch_prep_t<XT, 2, true>(p, s) : launch_prep_t<XT, 2, false>(p, s);
 }
 
 // Shared memory of a block, less the alignment of its start.
@@ -831,14 +840,15 @@ int launch_prep(const PrepParams &p, cudaStream_t s) {
 template <int NR>
 int launch_layer_t(FfnParams &p, cudaStream_t s) {
     using G = LayerGeom<NR>;
-    // digits stay resident where four ring stages remain beside them
     const int HK = ((p.H + 127) / 128 + 1) / 2, cap = std::min(p.T, NR);
     p.stage = (MXL_WBYTES + cap * MXL_ROW + 511) / 512 * 512;
-    p.res = p.T <= 8 ? HK * p.T * MXL_ROW : 0;
-    int front = G::CTRL + (p.res + 511) / 512 * 512;
-    if (p.res && front + 4 * p.stage > MXL_SMEM) {
-        p.res = 0;
-        front = G::CTRL;
+    // what stays resident leaves four ring stages: digits and scales, else the scales alone, else nothing
+    int front = 0;
+    for (int what = p.T <= 8 ? 2 : 1; what >= 0; --what) {
+        p.res = what == 2 ? HK * p.T * 1024 : 0;
+        p.xsr = what >= 1 ? HK * p.T * MXL_SC : 0;
+        front = G::CTRL + p.res + (p.xsr + 511) / 512 * 512;
+        if (front + 4 * p.stage <= MXL_SMEM) break;
     }
     p.S = std::min<int>(G::MAXS, (MXL_SMEM - front) / p.stage);
     static_assert((MXL_SMEM - G::CTRL) / (MXL_WBYTES + NR * MXL_ROW + 511) >= 4, "a ring");
@@ -900,7 +910,6 @@ extern "C" int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int 
     a.w_router = w_router;
     a.bias = bias;
     a.T = T; a.H = H; a.E = E; a.k = k;
-    a.wide_w = E % 8 == 0 && ((uintptr_t)w_router & 15) == 0;
     a.ids = ids ? ids : (int32_t *)(w + L.ids);
     a.weights = weights ? weights : (float *)(w + L.weights);
     a.xq = w + L.xq;
