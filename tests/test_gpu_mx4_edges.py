@@ -184,3 +184,15 @@ def test_layer_long_router_rows(T, H, E):
     l = Layer(T, H, 32, E, 1, seed=5, extra=False)
     l.check(*l.run(), tokens=[0, T // 2, T - 1])
     assert L.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("T,H,E,off", [(1, 4096, 250, 0), (3, 4128, 249, 3), (20, 5120, 251, 1), (16, 1472, 73, 5),
+                                       (17, 8192, 130, 2), (4, 32, 1, 1), (2, 64, 7, 7), (32, 30048, 9, 4), (9, 256, 256, 1)])
+def test_layer_router_weights_in_several_passes(T, H, E, off):
+    """Router rows that are not 16-byte pieces, from any element on: more of them than shared memory holds at a
+    time, a few, and fewer than a piece."""
+    l = Layer(T, H, 32, E, 1, seed=E, extra=False)
+    l.d_wr = torch.cat([l.d_wr.new_zeros(off), l.d_wr.reshape(-1)])[off:]
+    assert l.d_wr.data_ptr() % 16 == 2 * off % 16
+    l.check(*l.run(), tokens=[0, T - 1])
+    assert L.moe_device_status() == 0
