@@ -497,13 +497,14 @@ int moe_mx4_expert_down(const uint8_t *h_codes, const uint8_t *h_scales, int T, 
  *   y[t] = extra[t] + sum_{j=0..k-1} weights[t][j] * Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),
  * with x and h as fixed-point numbers under one power of two per 32 columns (each element off by at most
  * 2^-22 of the largest magnitude of its 32, or by 2^-128), sums in fp32, added over j in the order 0..k-1 after
- * extra.  The same bits for the same input.
+ * extra.  The same bits for the same input (and alignment of w_router).
  * (Logits are fp32 sums, as moe_router_topk's, in an order of their own.)
  *   x, w_router, bias  as in moe_router_topk; extra device [T][H] fp32 or NULL; y device [T][H]
  *                      fp32 out, may alias extra.
  *   ids, weights       device [T][k] out, or NULL.
  *   d_slot_table .. slot_bytes  as in moe_mx4_expert_gateup; an expert whose slot is outside
- *                      [0, n_slots) is recorded in the device status word and its routes add nothing.
+ *                      [0, n_slots) is recorded in the device status word and its routes add nothing: the
+ *                      routing is the call's own, so a pool has to hold every expert of the layer.
  *   workspace          device, moe_mx4_layer_workspace() bytes, 256-byte aligned; needs no initial
  *                      contents; one per call in flight.
  * A token with an infinity or a NaN has NaN outputs, as has one whose h overflows.  MOE_ERR_UNSUPPORTED, with

@@ -7,9 +7,9 @@
 // The weights are the M side, so that an expert's few routes cost only as wide an MMA as they are.
 //
 //  * few routes (MX4_LOCAL_R): each CTA groups them by expert itself; otherwise mx4_count_kernel and
-//    mx4_place_kernel sort them and lay their rows out.  Chunks are at most NT routes of one expert,
-//    experts with the most routes first.  The order of the routes inside an expert is not fixed; a
-//    route's result does not depend on it.
+//    mx4_place_kernel sort them, experts with the most routes first, and lay their rows out.  Chunks are at
+//    most NT routes of one expert.  The order of the routes inside an expert is not fixed; a route's result
+//    does not depend on it.
 //  * mx4_gemm_kernel: persistent, one CTA per SM; a work item is (chunk, 128-row weight tile).
 //    Warp roles, mbarrier rings that run on across items:
 //      warps 0, 1  a stage of 256 columns: the tile's two 8704-byte blocks (codes and scales, one
@@ -46,7 +46,8 @@ namespace {
 
 // Most routes of a chunk: a few where experts have few (more stages in the ring), else as wide as tensor
 // and shared memory allow, which is less beside the tables of LOCAL.  The larger saves passes over the
-// weights: 32768 routes over 128 experts are 241 chunks of at most 176, 227 of at most 192.
+// weights: 32768 routes over 128 experts of uneven popularity (one draw) are 241 chunks of at most 176, 227
+// of at most 192.
 #define MXG_NT_SMALL 32
 #define MXG_NT_LOCAL 176
 #define MXG_NT_LARGE 192
