@@ -84,8 +84,8 @@ enum moe_qtype {
                       images, host-managed pools and the moe_mx4_* calls below; moe_expert_ffn*
                       and the stacks refuse it */
 };
-/* Activation element types. */
-enum moe_xtype { MOE_F32 = 0, MOE_BF16 = 1 };
+/* Activation element types.  MOE_F16 is taken by the 16-bit products below (moe_grouped_*, moe_lora_matmul) only. */
+enum moe_xtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 };
 
 /* --------------------------------------------------------------- router (a1, a2) */
 
@@ -516,6 +516,103 @@ int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int E, int k, c
                   const float *bias, const int32_t *d_slot_table, int n_slots, const void *pool,
                   size_t slot_bytes, const float *extra, float *y, int32_t *ids, float *weights,
                   void *workspace, size_t ws_bytes, moe_stream_t s);
+
+/* --------------------------- products whose rows choose their matrix (16 bit) */
+
+/*
+ * The products of experts that are held in bf16 or fp16, forward and backward, and of low-rank adapters beside a
+ * projection that all tokens share.  Page 1, section 3.1: the experts that the gating chose work on their tokens and
+ * the results are added up.  The rows of a group (an expert's routes) stand one after another; a table of first positions
+ * says where each group begins, so groups may be as uneven as the routing makes them, or empty.  A 16-bit MoE
+ * layer is
+ *   moe_router_topk -> ids, weights [T][k]
+ *   moe_group_rows(ids)                                             -> offsets, rows
+ *   moe_grouped_matmul(x, x_index = rows, x_share = k, MOE_ACT_SWIGLU)       -> h, one row per position
+ *   moe_grouped_matmul(h, scale = weights, y_index = rows)          -> partial [T][k][H]
+ *   moe_combine(partial).
+ */
+#define MOE_MAX_GROUPS 1024 /* groups of a call */
+#define MOE_MAX_RANK 256    /* ranks of an adapter */
+
+/* Order of a matrix of N outputs by K inputs. */
+enum moe_order { MOE_ORDER_NK = 0, MOE_ORDER_KN = 1 }; /* [N][K]: an output's weights together; [K][N] */
+/* What is done to a product's rows. */
+enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SWIGLU = 1 /* the matrix has 2N outputs, N gate rows then N up rows: silu(gate) * up */
+};
+
+/*
+ * moe_group_rows - the positions 0 .. n-1 in the order of their groups.
+ *   ids      device [n], group of each position; -1: none; other values outside [0, G) are recorded in the
+ *            device status word and treated as -1.
+ *   offsets  device [G + 1] out: group g is rows[offsets[g]] .. rows[offsets[g + 1] - 1]; offsets[0] = 0.
+ *   rows     device [n] out: the positions of each group, ascending; -1 from offsets[G] on.
+ *   workspace  device, moe_group_rows_workspace() bytes (0 for most calls: then NULL will do), 4-byte
+ *            aligned; needs no initial contents; one per call in flight.
+ * 0 <= n <= 2^24 (0: offsets are zeroed), 1 <= G <= MOE_MAX_GROUPS.  ids may not overlap the outputs.
+ */
+int moe_group_rows_workspace(int n, int G, size_t *bytes);
+int moe_group_rows(const int32_t *ids, int n, int G, int32_t *offsets, int32_t *rows, void *workspace,
+                   size_t ws_bytes, moe_stream_t s);
+
+/*
+ * moe_grouped_matmul - for every group g and position i in [offsets[g], offsets[g + 1]):
+ *   y[dst] = scale[dst] * act(W_g x[src]),   src = x_index ? x_index[i] / x_share : i,   dst = y_index ? y_index[i] : i.
+ * Products of 16-bit operands are exact, sums fp32; y is rounded once.
+ *   x        device [x_rows][ldx], type MOE_BF16 or MOE_F16; 16-byte aligned, ldx >= K a multiple of 8.
+ *   x_index  device [R] or NULL; x_share >= 1 positions share a row of x (the k routes of a token).
+ *   offsets  device [G + 1], not descending, within [0, R]; a group whose two offsets are no such range is
+ *            recorded in the device status word and skipped.  R: the length of the index arrays, at most 2^24
+ *            (positions from offsets[G] on are not looked at).
+ *   w        device [G] matrices of w_order, of type's elements, contiguous, 16-byte aligned.
+ *            MOE_ORDER_KN is the order that the gradient of x needs: dx = dy W is this call with dy as x and the forward
+ *            call's N and K exchanged.
+ *   act      MOE_ACT_SWIGLU with MOE_ORDER_NK only (MOE_ERR_UNSUPPORTED otherwise).
+ *   scale    device [y_rows] fp32 or NULL (1).
+ *   y        device [y_rows][ldy], ytype MOE_F32, MOE_BF16 or MOE_F16; 16-byte aligned, ldy >= N a multiple
+ *            of 8; rows that no position names, and columns from N on, are left as they were.  y may not overlap x.
+ * A position whose src or dst is outside its matrix is recorded in the device status word and skipped.  No two positions may
+ * have the same dst.  N and K multiples of 8 up to 65536 (MOE_ERR_UNSUPPORTED otherwise), R = 0: no-op.
+ */
+int moe_grouped_matmul(const void *x, int type, int x_rows, size_t ldx, const int32_t *x_index, int x_share,
+                       const int32_t *offsets, int G, int R, const void *w, int w_order, int N, int K, int act,
+                       const float *scale, const int32_t *y_index, void *y, int ytype, int y_rows, size_t ldy,
+                       moe_stream_t s);
+
+/*
+ * moe_grouped_weight_grad - the gradient of the groups' matrices:
+ *   dw[g][n][k] = (accumulate ? dw[g][n][k] : 0) + sum_{i in group g} dy[dyr][n] * x[src][k],
+ *   src as above, dyr = dy_index ? dy_index[i] : i.
+ * x, dy as x of moe_grouped_matmul (dy: N columns); dw device [G][N][K] contiguous, wtype MOE_F32, MOE_BF16 or MOE_F16,
+ * 16-byte aligned (for matrices in MOE_ORDER_KN exchange x and dy, and N and K).  An empty group's dw is zeroed, or left by
+ * accumulate.  Sums fp32, rounded once, in an order that depends on the sizes alone.  A position whose src or dyr is outside
+ * its matrix is recorded in the device status word and adds nothing.  R = 0: dw is zeroed, or left.
+ */
+int moe_grouped_weight_grad(const void *x, int type, int x_rows, size_t ldx, const int32_t *x_index, int x_share,
+                            const void *dy, int dy_rows, size_t lddy, const int32_t *dy_index,
+                            const int32_t *offsets, int G, int R, int N, int K, int accumulate, void *dw, int wtype,
+                            moe_stream_t s);
+
+/*
+ * moe_lora_matmul - a projection that all tokens share plus, for each token, the adapter of its request:
+ *   y[t] = W x_t + scale[a] * B_a (A_a x_t),   a = adapter[t] (-1: W x_t alone).
+ *   x        device [T][ldx], type MOE_BF16 or MOE_F16; 16-byte aligned, ldx >= K a multiple of 8.
+ *   w        device [N][K]; a device [n_adapters][rank][K]; b device [n_adapters][N][rank]; all of type's
+ *            elements, contiguous, 16-byte aligned.
+ *   adapter  device [T]; values outside [-1, n_adapters) are recorded in the device status word and treated as -1.
+ *   scale    device [n_adapters] fp32 or NULL (1).
+ *   y        device [T][ldy] out, ytype MOE_F32, MOE_BF16 or MOE_F16; 16-byte aligned, ldy >= N a multiple of 8;
+ *            columns from N on are left as they were.
+ *   workspace  device, moe_lora_workspace() bytes, 256-byte aligned; needs no initial contents; one per call in flight.
+ * Sums fp32; scale[a] A_a x_t is kept to 16 bits of mantissa (bf16: two bf16; fp16: 22 bits, and beyond 65504 an
+ * infinity); y is rounded once.  N and K multiples of 8 up to 65536, rank a multiple of 8 up to MOE_MAX_RANK
+ * (MOE_ERR_UNSUPPORTED otherwise), T <= 2^24 (0: no-op).
+ */
+int moe_lora_workspace(int T, int rank, size_t *bytes);
+int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const void *w, int N, int K, const int32_t *adapter,
+                    int n_adapters, const void *a, const void *b, int rank, const float *scale, void *y, int ytype,
+                    size_t ldy, void *workspace, size_t ws_bytes, moe_stream_t s);
 
 /* ------------------------------------------------------------ device status */
 

@@ -26,6 +26,13 @@ MOE_Q4_SM = 1
 MOE_MXFP4 = 2
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_F16 = 2
+MOE_ORDER_NK = 0
+MOE_ORDER_KN = 1
+MOE_ACT_NONE = 0
+MOE_ACT_SWIGLU = 1
+MOE_MAX_GROUPS = 1024
+MOE_MAX_RANK = 256
 MOE_MAX_K = 8
 MOE_MAX_E = 256
 MOE_DECODE_MAX_T = 32
@@ -45,6 +52,8 @@ EXPORTED = [
     "moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_quantize_experts", "moe_mx4_dequantize_experts",
     "moe_mx4_expert_workspace", "moe_mx4_expert_gateup", "moe_mx4_expert_down",
     "moe_mx4_layer_workspace", "moe_mx4_layer",
+    "moe_group_rows_workspace", "moe_group_rows", "moe_grouped_matmul", "moe_grouped_weight_grad",
+    "moe_lora_workspace", "moe_lora_matmul",
 ]
 MOE_NOALLOC_SCRATCH_MAX = 8 << 20
 
@@ -189,6 +198,15 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "moe_mx4_layer_workspace": ([_i, _i, _i, _i, _i, P(_sz)], _i),
         "moe_mx4_layer": ([_vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _sz,
                            _vp], _i),
+        "moe_group_rows_workspace": ([_i, _i, P(_sz)], _i),
+        "moe_group_rows": ([_vp, _i, _i, _vp, _vp, _vp, _sz, _vp], _i),
+        "moe_grouped_matmul": ([_vp, _i, _i, _sz, _vp, _i, _vp, _i, _i, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i,
+                                _sz, _vp], _i),
+        "moe_grouped_weight_grad": ([_vp, _i, _i, _sz, _vp, _i, _vp, _i, _sz, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i,
+                                     _vp], _i),
+        "moe_lora_workspace": ([_i, _i, P(_sz)], _i),
+        "moe_lora_matmul": ([_vp, _i, _i, _sz, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _i, _sz, _vp, _sz, _vp],
+                            _i),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -505,3 +523,45 @@ def moe_mx4_layer(x, xtype: int, T: int, H: int, F: int, E: int, k: int, w_route
         load().moe_mx4_layer(_ptr(x), xtype, T, H, F, E, k, _ptr(w_router), _ptr(bias), _ptr(d_slot_table), n_slots,
                              _ptr(pool), slot_bytes, _ptr(extra), _ptr(y), _ptr(ids), _ptr(weights),
                              _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def moe_group_rows_workspace(n: int, G: int) -> int:
+    out = _sz()
+    _ck("moe_group_rows_workspace", load().moe_group_rows_workspace(n, G, ctypes.byref(out)))
+    return out.value
+
+
+def moe_group_rows(ids, n: int, G: int, offsets, rows, workspace, ws_bytes: int, stream=None) -> None:
+    _ck("moe_group_rows", load().moe_group_rows(_ptr(ids), n, G, _ptr(offsets), _ptr(rows), _ptr(workspace), ws_bytes,
+                                                _stream(stream)))
+
+
+def moe_grouped_matmul(x, type: int, x_rows: int, ldx: int, x_index, x_share: int, offsets, G: int, R: int, w,
+                       w_order: int, N: int, K: int, act: int, scale, y_index, y, ytype: int, y_rows: int, ldy: int,
+                       stream=None) -> None:
+    _ck("moe_grouped_matmul",
+        load().moe_grouped_matmul(_ptr(x), type, x_rows, ldx, _ptr(x_index), x_share, _ptr(offsets), G, R, _ptr(w),
+                                  w_order, N, K, act, _ptr(scale), _ptr(y_index), _ptr(y), ytype, y_rows, ldy,
+                                  _stream(stream)))
+
+
+def moe_grouped_weight_grad(x, type: int, x_rows: int, ldx: int, x_index, x_share: int, dy, dy_rows: int, lddy: int,
+                            dy_index, offsets, G: int, R: int, N: int, K: int, accumulate: int, dw, wtype: int,
+                            stream=None) -> None:
+    _ck("moe_grouped_weight_grad",
+        load().moe_grouped_weight_grad(_ptr(x), type, x_rows, ldx, _ptr(x_index), x_share, _ptr(dy), dy_rows, lddy,
+                                       _ptr(dy_index), _ptr(offsets), G, R, N, K, accumulate, _ptr(dw), wtype,
+                                       _stream(stream)))
+
+
+def moe_lora_workspace(T: int, rank: int) -> int:
+    out = _sz()
+    _ck("moe_lora_workspace", load().moe_lora_workspace(T, rank, ctypes.byref(out)))
+    return out.value
+
+
+def moe_lora_matmul(x, type: int, T: int, ldx: int, w, N: int, K: int, adapter, n_adapters: int, a, b, rank: int, scale,
+                    y, ytype: int, ldy: int, workspace, ws_bytes: int, stream=None) -> None:
+    _ck("moe_lora_matmul",
+        load().moe_lora_matmul(_ptr(x), type, T, ldx, _ptr(w), N, K, _ptr(adapter), n_adapters, _ptr(a), _ptr(b), rank,
+                               _ptr(scale), _ptr(y), ytype, ldy, _ptr(workspace), ws_bytes, _stream(stream)))

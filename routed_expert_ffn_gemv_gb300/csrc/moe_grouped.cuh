@@ -1,0 +1,580 @@
+// The tensor-core kernel of the 16-bit products whose rows choose their matrix: moe_grouped_matmul,
+// moe_grouped_weight_grad (moe_grouped.cu) and moe_lora_matmul (moe_lora.cu).
+//
+//   D[m][c] = sum_k A[m][k] B[c][k],  tcgen05.mma kind::f16, fp32 sums in tensor memory.
+// The matrix is always the M side (128 rows a CTA) and the rows of the group the N side, up to NT of them: an MMA is
+// only as wide as the group's rows are, so ragged groups waste at most GP_GRAN - 1 columns.
+//
+//              A (M side)                       B (N side)                     reduction
+//   GP_NK      W_g[n][k], K-major               rows x[i][k]                   K
+//   GP_KN      W_g[k][n], MN-major              rows x[i][k]                   K
+//   GP_SWIGLU  16 gate and 16 up rows of W_g    rows x[i][k]                   K
+//              in each 32 lanes
+//   GP_GRAD    columns of x, MN-major           columns of dy, MN-major        the group's rows
+//   GP_LORA    W[n][k], then the adapters'      rows x[t][k], then the rows    K, then 32 ranks of each
+//              B_a[n][r]                        u[t] of the adapter's tokens   adapter in the tile
+//
+// Persistent; a work item is (group, NT-row tile, 128-row tile of the matrix).  Warp roles over rings of mbarriers that
+// run on across items:
+//   warp 0      the stage's expected bytes and its A tile (TMA);
+//   warp 1      its B tile: boxes of 16 rows, or rows picked four at a time (TMA gather);
+//   warp 2      the MMAs, by an elected thread;
+//   warps 4-11  the epilogue of the previous item from the other accumulator: two warps to a lane quarter.
+// CG = 2: two CTAs share each MMA (M = 256), every CTA loads half of A and half of B.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "moe_mx4.cuh"
+#include "moe_tc.cuh"
+
+enum { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_GRAD = 3, GP_LORA = 4 };
+
+#define GP_THREADS 384
+#define GP_ABYTES 16384   // 128 rows of 64 reduction steps
+#define GP_UBYTES 8192    // GP_LORA: 128 rows of 32 ranks
+
+struct GroupedParams {
+    CUtensorMap a, b;         // GP_GRAD: x and dy by rows
+    CUtensorMap ab, u;        // GP_LORA: the adapters' B; u by rows
+    const int32_t *offsets;   // [G + 1], or NULL: one group of R rows
+    int G, R;
+    const int32_t *x_index;   // B's rows (GP_GRAD: A's): row i is x_index[i] / x_share, NULL: i
+    int x_share, x_rows;
+    const int32_t *y_index;   // output rows (GP_GRAD: B's rows), NULL: i
+    int y_rows;
+    const float *scale;       // [y_rows] or NULL
+    void *y;
+    size_t ldy;               // GP_GRAD: M
+    int ytype;
+    int M, K, N;              // columns of an output row; reduction (not GP_GRAD); GP_GRAD: output rows of a group
+    int accumulate;           // GP_GRAD
+    const int32_t *adapter;   // GP_LORA, [R]
+    int n_adapters, rank;
+    int fmt;                  // 0 fp16, 1 bf16
+    int *status;
+};
+
+template <int CG, int NT>
+struct GroupedGeom {
+    static constexpr int GRAN = 16 * CG;                     // rows an MMA's width is rounded up to
+    static constexpr int BBYTES = NT / CG * 128;
+    static constexpr int STAGE = GP_ABYTES + BBYTES;
+    static constexpr int TCOLS = 2 * NT < 32 ? 32 : 2 * NT;  // two accumulators
+    static constexpr int O_OFF = 1024, O_FIRST = O_OFF + (MOE_MAX_GROUPS + 4) * 4;
+    static constexpr int O_ROWS = O_FIRST + (MOE_MAX_GROUPS + 4) * 4;
+    static constexpr int O_XCH = O_ROWS + 2 * NT * 8;
+    static constexpr int XCH = 16 * 36;                      // floats of a warp: 16 rows x 32 (padded)
+    static constexpr int O_RING = (O_XCH + 8 * XCH * 4 + 1023) / 1024 * 1024;
+    static constexpr int S = (227 * 1024 - 1024 - O_RING) / STAGE > 12 ? 12 : (227 * 1024 - 1024 - O_RING) / STAGE;
+    static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
+    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (2 * S + 5) * 8 + 16 + 48 <= 1024 && S >= 3, "");
+};
+
+struct GroupedItem {
+    int g, m, row0, n, npad;  // group, M tile, first row (GP_GRAD: first output row), rows, rows rounded up
+    int r0, cnt, steps;       // GP_GRAD: the group's first row and rows; stages of the reduction
+};
+
+__device__ __forceinline__ void grouped_store4(void *y, int ytype, size_t i, float4 v, bool accumulate) {
+    if (ytype == MOE_F32) {
+        float4 *o = (float4 *)((float *)y + i);
+        if (accumulate) {
+            const float4 w = *o;
+            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+        }
+        *o = v;
+    } else if (ytype == MOE_BF16) {
+        uint2 *o = (uint2 *)((__nv_bfloat16 *)y + i);
+        if (accumulate) {
+            const uint2 w = *o;
+            v.x += __uint_as_float(w.x << 16);
+            v.y += __uint_as_float(w.x & 0xFFFF0000u);
+            v.z += __uint_as_float(w.y << 16);
+            v.w += __uint_as_float(w.y & 0xFFFF0000u);
+        }
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *o = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
+    } else {
+        uint2 *o = (uint2 *)((__half *)y + i);
+        if (accumulate) {
+            const uint2 w = *o;
+            const float2 a = __half22float2(*(const __half2 *)&w.x), b = __half22float2(*(const __half2 *)&w.y);
+            v = make_float4(v.x + a.x, v.y + a.y, v.z + b.x, v.w + b.y);
+        }
+        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+        *o = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
+    }
+}
+
+// The smallest of a tile's adapters above `last` (-1 to begin with); INT_MAX: none.  ids: this lane's share of the
+// tile's tokens; every lane gets the same answer.
+__device__ __forceinline__ int grouped_next_adapter(const int (&ids)[8], int last) {
+    unsigned best = 0x7FFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (ids[i] > last) best = min(best, (unsigned)ids[i]);
+    return (int)__reduce_min_sync(0xffffffffu, best);
+}
+
+template <int CG, int NT, int MODE>
+__global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
+    using G_ = GroupedGeom<CG, NT>;
+    constexpr int S = G_::S;
+    constexpr bool GRAD = MODE == GP_GRAD, A_MN = GRAD || MODE == GP_KN, B_MN = GRAD;
+    constexpr int MROWS = MODE == GP_SWIGLU ? 64 : 128;  // output columns of a CTA's tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_smem_1024(smem_raw);
+    uint64_t *full = (uint64_t *)smem;
+    uint64_t *empty = full + S;
+    uint64_t *acc_full = empty + S;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *mma_done = acc_empty + 2;
+    uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
+    volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
+    int *sums = (int *)(tmem_slot + 4);                       // [12]
+    int *off = (int *)(smem + G_::O_OFF);                     // [G + 1]
+    int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before a group's
+    int2 *e_rows = (int2 *)(smem + G_::O_ROWS);               // [2][NT] output row (-1: none), scale
+    uint8_t *ring = smem + G_::O_RING;
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 8 * CG);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 2) tmem_alloc_group<CG>(tmem_slot, G_::TCOLS);
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // (GP_LORA: the kernel in front computes u and nothing else; it starts this one when everything before it is
+    // complete, and only u is waited for, by the warp that loads it)
+    if (MODE != GP_LORA) pdl_wait();
+    pdl_trigger();
+
+    // ---------------- items: tiles of the M side, inner, by tiles of each group's rows
+    const int mt = (p.M + MROWS * CG - 1) / (MROWS * CG);
+    const int gran = GRAD ? 64 * CG : G_::GRAN;
+    const int gt = GRAD ? (p.N + NT - 1) / NT : 0;  // GP_GRAD: tiles of N
+    for (int i = tid; i <= p.G; i += GP_THREADS) off[i] = p.offsets ? p.offsets[i] : i * p.R;
+    __syncthreads();
+    auto rows_of = [&](int g) -> int {  // rows of a group; none where the offsets are no range of rows
+        const int a = off[g], b = off[g + 1];
+        return a >= 0 && b >= a && b <= p.R ? b - a : 0;
+    };
+    constexpr int PER = (MOE_MAX_GROUPS + GP_THREADS - 1) / GP_THREADS;
+    {
+        int c[PER], t = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int g = tid * PER + i;
+            c[i] = t;
+            if (g < p.G) {
+                const int n = rows_of(g);
+                if (!n && off[g + 1] != off[g]) moe_set_status(p.status, MOE_ERR_INVALID);
+                t += mt * (GRAD ? gt : (n + NT - 1) / NT);
+            }
+        }
+        int inc = t;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += v;
+        }
+        if (lane == 31) sums[warp] = inc;
+        __syncthreads();
+        int before = inc - t;
+        for (int w = 0; w < warp; ++w) before += sums[w];
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (tid * PER + i < p.G) first[tid * PER + i] = before + c[i];
+        if (tid == GP_THREADS - 1) first[p.G] = before + t;
+    }
+    __syncthreads();
+    const int n_items = first[p.G], stride = (int)gridDim.x / CG, item0 = (int)blockIdx.x / CG;
+    auto item_at = [&](int j) -> GroupedItem {
+        GroupedItem it;
+        int lo = 0, hi = p.G;  // the last group whose first item is not after j
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (first[mid] <= j) lo = mid;
+            else hi = mid;
+        }
+        it.g = lo;
+        const int r = j - first[lo], t = r / mt;
+        it.m = r - t * mt;
+        it.r0 = off[lo];
+        it.cnt = rows_of(lo);
+        // near-equal tiles: none is empty, as size <= NT
+        const int all = GRAD ? p.N : it.cnt, nt = (all + NT - 1) / NT;
+        const int size = ((all + nt - 1) / nt + gran - 1) / gran * gran;
+        it.n = min(size, all - t * size);
+        it.npad = (it.n + gran - 1) / gran * gran;
+        it.row0 = (GRAD ? 0 : it.r0) + t * size;
+        it.steps = ((GRAD ? it.cnt : p.K) + 63) / 64;
+        return it;
+    };
+    // GP_LORA: this lane's share of the tile's adapters (-1: none)
+    auto tile_adapters = [&](const GroupedItem &it, int (&ids)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = lane + 32 * i;
+            const int a = c < it.n ? p.adapter[it.row0 + c] : -1;
+            if (a >= p.n_adapters || a < -1) moe_set_status(p.status, MOE_ERR_INVALID);
+            ids[i] = a < p.n_adapters ? a : -1;
+        }
+    };
+    const int chunks = MODE == GP_LORA ? (p.rank + 31) / 32 : 0;
+    auto source = [&](int i) -> int {  // x's row of position i, -1: none
+        if (!p.x_index) return i < p.x_rows ? i : -1;
+        const int v = p.x_index[i], r = v / p.x_share;
+        return v >= 0 && r < p.x_rows ? r : -1;
+    };
+    auto target = [&](int i) -> int {
+        const int v = p.y_index ? p.y_index[i] : i;
+        return v >= 0 && v < p.y_rows ? v : -1;
+    };
+    // GP_GRAD: the four rows of x (or dy) of reduction step q's lane; past the group's end, or where either side has no
+    // row, one outside the tensor, which reads 0
+    auto grad_rows = [&](const GroupedItem &it, int kb, bool dy, int (&r4)[4]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int q = kb * 64 + 4 * (lane & 15) + k;
+            int a = -1, b = -1;
+            if (q < it.cnt) {
+                a = source(it.r0 + q);
+                b = target(it.r0 + q);
+            }
+            const bool both = a >= 0 && b >= 0;
+            if (q < it.cnt && !both && !dy) moe_set_status(p.status, MOE_ERR_INVALID);
+            r4[k] = both ? (dy ? b : a) : (dy ? p.y_rows : p.x_rows);
+        }
+    };
+
+    if (warp == 0) {
+        // ---------------- A
+        int gs = 0, st = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        for (int j = item0; j < n_items && ok; j += stride) {
+            const GroupedItem it = item_at(j);
+            const int nb = it.npad / CG;
+            const uint32_t bytes = (uint32_t)CG * (GP_ABYTES + (uint32_t)nb * 128u);
+            const int m0 = (it.m * CG + rank) * MROWS;
+            int r4[4] = {0, 0, 0, 0};
+            if (GRAD && it.steps) grad_rows(it, 0, false, r4);
+            for (int kb = 0; kb < it.steps; ++kb, ++gs) {
+                if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
+                uint8_t *dst = ring + (size_t)st * G_::STAGE;
+                const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
+                if (rank == 0) mbar_arrive_expect_tx_elect(&full[st], bytes);
+                if (MODE == GP_NK || MODE == GP_LORA) {
+                    if (lane == 0) tma_tile_3d<CG>(dst, &p.a, kb * 64, m0, MODE == GP_LORA ? 0 : it.g, bar);
+                } else if (MODE == GP_KN) {
+                    if (lane < 2) tma_tile_3d<CG>(dst + lane * 8192, &p.a, m0 + 64 * lane, kb * 64, it.g, bar);
+                } else if (MODE == GP_SWIGLU) {
+                    if (lane < 4) tma_tile_4d<CG>(dst + lane * 4096, &p.a, kb * 64, m0 + 16 * lane, 0, it.g, bar);
+                } else {
+                    tma_rows4<CG>(dst + (lane >> 4) * 8192 + (lane & 15) * 512, &p.a, m0 + 64 * (lane >> 4), r4, bar);
+                    if (kb + 1 < it.steps) grad_rows(it, kb + 1, false, r4);
+                }
+                __syncwarp();
+                if (++st == S) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (MODE == GP_LORA && ok) {
+                int ids[8];
+                tile_adapters(it, ids);
+                for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a))
+                    for (int c = 0; c < chunks; ++c, ++gs) {
+                        if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
+                        uint8_t *dst = ring + (size_t)st * G_::STAGE;
+                        const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
+                        if (rank == 0)
+                            mbar_arrive_expect_tx_elect(&full[st], (uint32_t)CG * (GP_UBYTES + (uint32_t)nb * 128u));
+                        if (lane == 0) tma_tile_3d<CG>(dst, &p.ab, c * 32, m0, a, bar);
+                        __syncwarp();
+                        if (++st == S) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    }
+            }
+        }
+        // never leave with copies in flight (a pair: the leader's barriers count both CTAs' copies)
+        if (lane == 0 && rank == 0)
+            for (int s = 0; s < S && s < gs; ++s) {
+                const int last = s + ((gs - 1 - s) / S) * S;
+                mbar_wait_bounded(&full[s], (last / S) & 1, p.status);
+            }
+        if (!ok) settle_after_abort();
+    } else if (warp == 1) {
+        // ---------------- B
+        int gs = 0, st = 0;
+        uint32_t ph = 1;
+        bool ok = true, waited = false;
+        for (int j = item0; j < n_items && ok; j += stride) {
+            const GroupedItem it = item_at(j);
+            const int nb = it.npad / CG, c0 = rank * nb;
+            constexpr int Q = (NT / CG + 127) / 128;  // gathers of a lane
+            int r4[Q][4];
+            if (GRAD) {
+                if (it.steps) grad_rows(it, 0, true, r4[0]);
+            } else if (p.x_index) {
+#pragma unroll
+                for (int i = 0; i < Q; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = c0 + 4 * (lane + 32 * i) + k;
+                        r4[i][k] = max(0, source(it.row0 + (c < it.n ? c : 0)));  // (columns that are not stored)
+                    }
+            }
+            for (int kb = 0; kb < it.steps; ++kb, ++gs) {
+                if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
+                uint8_t *dst = ring + (size_t)st * G_::STAGE + GP_ABYTES;
+                const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
+                if (GRAD) {
+#pragma unroll
+                    for (int i = 0; i < (NT / CG + 127) / 128; ++i) {
+                        const int q = lane + 32 * i;
+                        if (4 * q < nb) tma_rows4<CG>(dst + q * 512, &p.b, it.row0 + c0 + 64 * (q >> 4), r4[0], bar);
+                    }
+                    if (kb + 1 < it.steps) grad_rows(it, kb + 1, true, r4[0]);
+                } else if (p.x_index) {
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        const int q = lane + 32 * i;
+                        if (4 * q < nb) tma_rows4<CG>(dst + q * 512, &p.b, kb * 64, r4[i], bar);
+                    }
+                } else if (16 * lane < nb) {
+                    tma_tile_2d<CG>(dst + lane * 2048, &p.b, kb * 64, it.row0 + c0 + 16 * lane, bar);
+                }
+                __syncwarp();
+                if (++st == S) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (MODE == GP_LORA && ok) {
+                if (!waited) {
+                    pdl_wait();
+                    waited = true;
+                }
+                int ids[8], mine[Q][4];
+                tile_adapters(it, ids);
+#pragma unroll
+                for (int i = 0; i < Q; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = c0 + 4 * (lane + 32 * i) + k;
+                        mine[i][k] = c < it.n ? p.adapter[it.row0 + c] : -1;
+                    }
+                for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a)) {
+                    // u's rows of the adapter's tokens; for the others its row R, which is zero
+#pragma unroll
+                    for (int i = 0; i < Q; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            r4[i][k] = mine[i][k] == a ? it.row0 + c0 + 4 * (lane + 32 * i) + k : p.R;
+                    for (int c = 0; c < chunks; ++c, ++gs) {
+                        if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
+                        uint8_t *dst = ring + (size_t)st * G_::STAGE + GP_ABYTES;
+                        const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
+#pragma unroll
+                        for (int i = 0; i < Q; ++i) {
+                            const int q = lane + 32 * i;
+                            if (4 * q < nb) tma_rows4<CG>(dst + q * 512, &p.u, c * 64, r4[i], bar);
+                        }
+                        __syncwarp();
+                        if (++st == S) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+            }
+        }
+        if (MODE == GP_LORA && !waited) pdl_wait();
+        if (!ok) settle_after_abort();
+    } else if (warp == 2 && rank == 0) {
+        // ---------------- MMA issuer
+        int jl = 0, st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int j = item0; j < n_items && ok; j += stride, ++jl) {
+            const GroupedItem it = item_at(j);
+            const uint32_t idesc = umma_idesc_16(p.fmt, A_MN, B_MN, 128 * CG, it.npad);
+            const int buf = jl & 1;
+            int extra = 0;
+            if (MODE == GP_LORA) {
+                int ids[8];
+                tile_adapters(it, ids);
+                for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a)) extra += chunks;
+            }
+            if (jl >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((jl / 2) - 1) & 1, p.status, abort_flag))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + buf * NT;
+            const int len = GRAD ? it.cnt : p.K;
+            for (int kb = 0; kb < it.steps; ++kb) {
+                if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
+                const uint64_t a = A_MN ? umma_desc_mn_sw128(sa, 8192) : umma_desc_sw128(sa);
+                const uint64_t b = B_MN ? umma_desc_mn_sw128(sa + GP_ABYTES, 8192) : umma_desc_sw128(sa + GP_ABYTES);
+                const int steps = min(4, (len - 64 * kb + 15) / 16);
+                for (int q = 0; q < steps; ++q)
+                    umma_f16_elect<CG>(d, a + (uint64_t)(q * (A_MN ? 128 : 2)), b + (uint64_t)(q * (B_MN ? 128 : 2)), idesc,
+                                       kb > 0 || q > 0);
+                umma_commit_group_elect<CG>(&empty[st]);
+                if (++st == S) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            for (int e = 0, c = 0; e < extra && ok; ++e) {
+                if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
+                tc_fence_after();
+                // 32 ranks: u's upper halves in the first 64 bytes of a row, the rest of u in the second, both by the same B_a
+                const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
+                const uint64_t a = umma_desc_sw64(sa), b = umma_desc_sw128(sa + GP_ABYTES);
+                const bool two = p.rank - 32 * c > 16;
+                umma_f16_elect<CG>(d, a, b, idesc, 1);
+                umma_f16_elect<CG>(d, a, b + 4, idesc, 1);
+                if (two) {
+                    umma_f16_elect<CG>(d, a + 2, b + 2, idesc, 1);
+                    umma_f16_elect<CG>(d, a + 2, b + 6, idesc, 1);
+                }
+                umma_commit_group_elect<CG>(&empty[st]);
+                if (++c == chunks) c = 0;
+                if (++st == S) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (ok) umma_commit_group_elect<CG>(&acc_full[buf]);
+        }
+        umma_commit_group_elect<CG>(mma_done);  // every MMA has completed before tensor memory is released
+        mbar_wait_bounded(mma_done, 0, p.status);
+    } else if (warp >= 4) {
+        // ---------------- epilogue: lane = row of the M side; 32 of them x 16 rows of the group at a time by way of
+        // shared memory, so that a store covers 32 consecutive elements of an output row
+        const int q = warp & 3, ew = warp - 4, half = ew >> 2, et = ew * 32 + lane;
+        float *xb = (float *)(smem + G_::O_XCH) + ew * G_::XCH;
+        int jl = 0;
+        for (int j = item0; j < n_items; j += stride, ++jl) {
+            const GroupedItem it = item_at(j);
+            const int buf = jl & 1;
+            if (et < NT && et < it.n) {
+                int dst = -1;
+                float s = 1.f;
+                if (GRAD) {
+                    dst = it.row0 + et;
+                } else {
+                    dst = target(it.row0 + et);
+                    if (source(it.row0 + et) < 0) dst = -1;
+                    if (dst < 0) moe_set_status(p.status, MOE_ERR_INVALID);
+                    else if (p.scale) s = p.scale[dst];
+                }
+                e_rows[buf * NT + et] = make_int2(dst, __float_as_int(s));
+            }
+            const bool w = mbar_wait_role(&acc_full[buf], (jl / 2) & 1, p.status, abort_flag);
+            if (!bar_and_n(1, 256, w)) break;
+            tc_fence_after();
+            const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * NT;
+            const int2 *rows = e_rows + buf * NT;
+            const size_t base = GRAD ? (size_t)it.g * p.N * p.M : 0;
+            if (MODE != GP_SWIGLU) {
+                const int o = (it.m * CG + rank) * 128 + 32 * q + 4 * (lane & 7);
+                for (int c0 = 16 * half; c0 < it.n; c0 += 32) {
+                    uint32_t v[16];
+                    tmem_ld16(tb + c0, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) xb[36 * k + lane] = GRAD && !it.steps ? 0.f : __uint_as_float(v[k]);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = 4 * k + (lane >> 3);
+                        float4 a = *(const float4 *)(xb + 36 * c + 4 * (lane & 7));
+                        if (c0 + c < it.n && o < p.M) {
+                            const int2 r = rows[c0 + c];
+                            if (!GRAD) {
+                                const float s = __int_as_float(r.y);
+                                a = make_float4(s * a.x, s * a.y, s * a.z, s * a.w);
+                            }
+                            if (r.x >= 0) grouped_store4(p.y, p.ytype, base + (size_t)r.x * p.ldy + o, a, GRAD && p.accumulate);
+                        }
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // lanes 0-15 hold gate rows, 16-31 the same up rows: they trade eight of 16 rows of the group
+                const int f0 = (it.m * CG + rank) * 64 + 16 * q, o = f0 + 4 * (lane & 3);
+                const bool up = lane >= 16;
+                for (int c0 = 16 * half; c0 < it.n; c0 += 32) {
+                    uint32_t v[16];
+                    tmem_ld16(tb + c0, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, up ? v[k] : v[8 + k], 16));
+                        const float gv = up ? other : __uint_as_float(v[k]), uv = up ? __uint_as_float(v[8 + k]) : other;
+                        // (16 floats further for the second eight rows: no bank conflicts)
+                        xb[20 * (k + (up ? 8 : 0)) + (up ? 16 : 0) + (lane & 15)] = mx4_swiglu<true>(gv, uv);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int c = 8 * k + (lane >> 2);
+                        float4 a = *(const float4 *)(xb + 20 * c + 16 * k + 4 * (lane & 3));
+                        if (c0 + c < it.n && o < p.M) {
+                            const int2 r = rows[c0 + c];
+                            const float s = __int_as_float(r.y);
+                            a = make_float4(s * a.x, s * a.y, s * a.z, s * a.w);
+                            if (r.x >= 0) grouped_store4(p.y, p.ytype, (size_t)r.x * p.ldy + o, a, false);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 1) mbar_arrive1(&acc_empty[buf]);
+                else mbar_arrive_cluster(cluster_map(&acc_empty[buf], 0));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();
+    if (warp == 2) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_group<CG>(tmem, G_::TCOLS);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+// Launches the kernel on the current device with one CTA (or pair) an SM (or two), at most `items` of them.
+int grouped_launch(const GroupedParams &p, int mode, bool wide, long long items, cudaStream_t s);
+// Tensor map of 16-bit elements: `rank` dimensions and box extents innermost first, strides in bytes from the second on.
+int grouped_map(CUtensorMap *map, int type, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                const uint32_t *box, int swizzle_bytes);
