@@ -587,7 +587,7 @@ int moe_grouped_matmul(const void *x, int type, int x_rows, size_t ldx, const in
  * x, dy as x of moe_grouped_matmul (dy: N columns); dw device [G][N][K] contiguous, wtype MOE_F32, MOE_BF16 or MOE_F16,
  * 16-byte aligned (for matrices in MOE_ORDER_KN exchange x and dy, and N and K).  An empty group's dw is zeroed, or left by
  * accumulate.  Sums fp32, rounded once, in an order that depends on the sizes alone.  A position whose src or dyr is outside
- * its matrix is recorded in the device status word and adds nothing.  R = 0: dw is zeroed, or left.
+ * its matrix is recorded in the device status word and adds zero times its other row.  R = 0: dw is zeroed, or left.
  */
 int moe_grouped_weight_grad(const void *x, int type, int x_rows, size_t ldx, const int32_t *x_index, int x_share,
                             const void *dy, int dy_rows, size_t lddy, const int32_t *dy_index,

@@ -7,7 +7,7 @@
 #include "moe_grouped.cuh"
 
 #ifndef GP_WIDE_CG
-#define GP_WIDE_CG 1
+#define GP_WIDE_CG 2
 #endif
 
 namespace {
@@ -79,7 +79,7 @@ int check_rows(int rows, int cols, size_t ld) {
     return MOE_OK;
 }
 
-// Rows of 64-element pieces: boxes of `box` rows.
+// Rows in boxes of 64 elements of `box` rows.
 int rows_map(CUtensorMap *map, int type, const void *x, int rows, int cols, size_t ld, int box) {
     const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)ld * 2};
     const uint32_t b[2] = {64, (uint32_t)box};
@@ -147,7 +147,10 @@ extern "C" int moe_grouped_matmul(const void *x, int type, int x_rows, size_t ld
         const uint32_t box[3] = {64, mode == GP_NK ? 128u : 64u, 1};
         rc = grouped_map(&p.a, type, 3, w, dims, strides, box, 128);
     }
-    if (rc != MOE_OK || (rc = rows_map(&p.b, type, x, x_rows, K, ldx, x_index ? 1 : 16)) != MOE_OK) return rc;
+    if (rc != MOE_OK || (rc = rows_map(&p.b, type, x, x_rows, K, ldx, 16)) != MOE_OK) return rc;
+    if ((rc = rows_map(&p.b64, type, x, x_rows, K, ldx, 64)) != MOE_OK) return rc;
+    p.rows = (const uint16_t *)x;
+    p.ld = ldx;
     p.offsets = offsets;
     p.G = G;
     p.R = R;
@@ -190,8 +193,12 @@ extern "C" int moe_grouped_weight_grad(const void *x, int type, int x_rows, size
     MOE_CHECK(x && dy && offsets && x_rows >= 1 && dy_rows >= 1 && aligned16(x) && aligned16(dy));
 
     GroupedParams p = {};
-    if ((rc = rows_map(&p.a, type, x, x_rows, K, ldx, 1)) != MOE_OK) return rc;
-    if ((rc = rows_map(&p.b, type, dy, dy_rows, N, lddy, 1)) != MOE_OK) return rc;
+    if ((rc = rows_map(&p.a, type, x, x_rows, K, ldx, 64)) != MOE_OK) return rc;
+    if ((rc = rows_map(&p.b, type, dy, dy_rows, N, lddy, 64)) != MOE_OK) return rc;
+    p.rows = (const uint16_t *)x;
+    p.ld = ldx;
+    p.dy = (const uint16_t *)dy;
+    p.lddy = lddy;
     p.offsets = offsets;
     p.G = G;
     p.R = R;

@@ -16,10 +16,15 @@
 //
 // Persistent; a work item is (group, NT-row tile, 128-row tile of the matrix).  Warp roles over rings of mbarriers that
 // run on across items:
-//   warp 0      the stage's expected bytes and its A tile (TMA);
-//   warp 1      its B tile: boxes of 16 rows, or rows picked four at a time (TMA gather);
-//   warp 2      the MMAs, by an elected thread;
-//   warps 4-11  the epilogue of the previous item from the other accumulator: two warps to a lane quarter.
+//   warp 0       the stage's expected bytes and its A tile (TMA boxes);
+//   warp 1       its B tile (TMA boxes of 64 and 16 rows);
+//   warp 2       the MMAs, by an elected thread;
+//   warps 4-11   the epilogue of the previous item from the other accumulator: two warps to a lane quarter;
+//   warps 12-19  rows that are no box: picked by an index, u's rows of one adapter, a group's last rows (GP_GRAD).
+//                16-byte asynchronous copies, zeros where there is no row;
+//   warp 3       hands their stages over once they have landed.  (TMA gathers, four rows an instruction,
+//                take about 40 ns each however many are in flight: 32768 rows of 2048 gathered for 1536
+//                outputs took 510 us.)
 // CG = 2: two CTAs share each MMA (M = 256), every CTA loads half of A and half of B.
 #pragma once
 
@@ -32,13 +37,16 @@
 
 enum { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_GRAD = 3, GP_LORA = 4 };
 
-#define GP_THREADS 384
+#define GP_THREADS 640
 #define GP_ABYTES 16384   // 128 rows of 64 reduction steps
 #define GP_UBYTES 8192    // GP_LORA: 128 rows of 32 ranks
 
 struct GroupedParams {
-    CUtensorMap a, b;         // GP_GRAD: x and dy by rows
-    CUtensorMap ab, u;        // GP_LORA: the adapters' B; u by rows
+    CUtensorMap a, b, b64;    // GP_GRAD: x and dy
+    CUtensorMap ab;           // GP_LORA: the adapters' B
+    const uint16_t *rows;     // x; GP_LORA: u
+    const uint16_t *dy;       // GP_GRAD
+    size_t ld, lddy;
     const int32_t *offsets;   // [G + 1], or NULL: one group of R rows
     int G, R;
     const int32_t *x_index;   // B's rows (GP_GRAD: A's): row i is x_index[i] / x_share, NULL: i
@@ -68,9 +76,9 @@ struct GroupedGeom {
     static constexpr int O_XCH = O_ROWS + 2 * NT * 8;
     static constexpr int XCH = 16 * 36;                      // floats of a warp: 16 rows x 32 (padded)
     static constexpr int O_RING = (O_XCH + 8 * XCH * 4 + 1023) / 1024 * 1024;
-    static constexpr int S = (227 * 1024 - 1024 - O_RING) / STAGE > 12 ? 12 : (227 * 1024 - 1024 - O_RING) / STAGE;
+    static constexpr int S = (227 * 1024 - 1024 - O_RING) / STAGE / 2 * 2;  // (even: see the loaders)
     static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
-    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (2 * S + 5) * 8 + 16 + 48 <= 1024 && S >= 3, "");
+    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 5) * 8 + 16 + 80 <= 1024 && S >= 3, "");
 };
 
 struct GroupedItem {
@@ -109,6 +117,16 @@ __device__ __forceinline__ void grouped_store4(void *y, int ytype, size_t i, flo
     }
 }
 
+// 16 bytes global -> shared (bytes = 16), or zeros (0).
+__device__ __forceinline__ void cp_async_16_or_0(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// An arrival (one of the barrier's count) once every copy this thread has issued has landed.
+__device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // The smallest of a tile's adapters above `last` (-1 to begin with); INT_MAX: none.  ids: this lane's share of the
 // tile's tokens; every lane gets the same answer.
 __device__ __forceinline__ int grouped_next_adapter(const int (&ids)[8], int last) {
@@ -125,16 +143,18 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     constexpr int S = G_::S;
     constexpr bool GRAD = MODE == GP_GRAD, A_MN = GRAD || MODE == GP_KN, B_MN = GRAD;
     constexpr int MROWS = MODE == GP_SWIGLU ? 64 : 128;  // output columns of a CTA's tile
+    static_assert(!GRAD || NT / CG == 128, "sixteen pieces of eight columns");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     uint64_t *full = (uint64_t *)smem;
     uint64_t *empty = full + S;
-    uint64_t *acc_full = empty + S;
+    uint64_t *landed = empty + S;
+    uint64_t *acc_full = landed + S;
     uint64_t *acc_empty = acc_full + 2;
     uint64_t *mma_done = acc_empty + 2;
     uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
-    int *sums = (int *)(tmem_slot + 4);                       // [12]
+    int *sums = (int *)(tmem_slot + 4);                       // [20]
     int *off = (int *)(smem + G_::O_OFF);                     // [G + 1]
     int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before a group's
     int2 *e_rows = (int2 *)(smem + G_::O_ROWS);               // [2][NT] output row (-1: none), scale
@@ -142,9 +162,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
+    const bool loaders = GRAD || MODE == GP_LORA || p.x_index;
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + (loaders ? CG : 0));
+            mbar_init(&landed[s], 128);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -239,6 +261,15 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         }
     };
     const int chunks = MODE == GP_LORA ? (p.rank + 31) / 32 : 0;
+    auto extra_stages = [&](const GroupedItem &it) -> int {
+        int n = 0;
+        if (MODE == GP_LORA) {
+            int ids[8];
+            tile_adapters(it, ids);
+            for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a)) n += chunks;
+        }
+        return n;
+    };
     auto source = [&](int i) -> int {  // x's row of position i, -1: none
         if (!p.x_index) return i < p.x_rows ? i : -1;
         const int v = p.x_index[i], r = v / p.x_share;
@@ -248,49 +279,30 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         const int v = p.y_index ? p.y_index[i] : i;
         return v >= 0 && v < p.y_rows ? v : -1;
     };
-    // GP_GRAD: the four rows of x (or dy) of reduction step q's lane; past the group's end, or where either side has no
-    // row, one outside the tensor, which reads 0
-    auto grad_rows = [&](const GroupedItem &it, int kb, bool dy, int (&r4)[4]) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int q = kb * 64 + 4 * (lane & 15) + k;
-            int a = -1, b = -1;
-            if (q < it.cnt) {
-                a = source(it.r0 + q);
-                b = target(it.r0 + q);
-            }
-            const bool both = a >= 0 && b >= 0;
-            if (q < it.cnt && !both && !dy) moe_set_status(p.status, MOE_ERR_INVALID);
-            r4[k] = both ? (dy ? b : a) : (dy ? p.y_rows : p.x_rows);
-        }
-    };
-
     if (warp == 0) {
-        // ---------------- A
+        // ---------------- A, and what a stage's copies bring
         int gs = 0, st = 0;
         uint32_t ph = 1;
         bool ok = true;
         for (int j = item0; j < n_items && ok; j += stride) {
             const GroupedItem it = item_at(j);
-            const int nb = it.npad / CG;
-            const uint32_t bytes = (uint32_t)CG * (GP_ABYTES + (uint32_t)nb * 128u);
-            const int m0 = (it.m * CG + rank) * MROWS;
-            int r4[4] = {0, 0, 0, 0};
-            if (GRAD && it.steps) grad_rows(it, 0, false, r4);
+            const int nb = it.npad / CG, m0 = (it.m * CG + rank) * MROWS;
             for (int kb = 0; kb < it.steps; ++kb, ++gs) {
                 if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
                 uint8_t *dst = ring + (size_t)st * G_::STAGE;
                 const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
-                if (rank == 0) mbar_arrive_expect_tx_elect(&full[st], bytes);
+                const bool whole = !GRAD || 64 * kb + 64 <= it.cnt;  // (else by the loaders)
+                const bool box_a = GRAD ? whole && !p.x_index : true, box_b = GRAD ? whole && !p.y_index : !p.x_index;
+                if (rank == 0)
+                    mbar_arrive_expect_tx_elect(&full[st], CG * ((box_a ? GP_ABYTES : 0u) + (box_b ? nb * 128u : 0u)));
                 if (MODE == GP_NK || MODE == GP_LORA) {
                     if (lane == 0) tma_tile_3d<CG>(dst, &p.a, kb * 64, m0, MODE == GP_LORA ? 0 : it.g, bar);
                 } else if (MODE == GP_KN) {
                     if (lane < 2) tma_tile_3d<CG>(dst + lane * 8192, &p.a, m0 + 64 * lane, kb * 64, it.g, bar);
                 } else if (MODE == GP_SWIGLU) {
                     if (lane < 4) tma_tile_4d<CG>(dst + lane * 4096, &p.a, kb * 64, m0 + 16 * lane, 0, it.g, bar);
-                } else {
-                    tma_rows4<CG>(dst + (lane >> 4) * 8192 + (lane & 15) * 512, &p.a, m0 + 64 * (lane >> 4), r4, bar);
-                    if (kb + 1 < it.steps) grad_rows(it, kb + 1, false, r4);
+                } else if (box_a) {
+                    if (lane < 2) tma_tile_2d<CG>(dst + lane * 8192, &p.a, m0 + 64 * lane, it.r0 + 64 * kb, bar);
                 }
                 __syncwarp();
                 if (++st == S) {
@@ -306,8 +318,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
                         uint8_t *dst = ring + (size_t)st * G_::STAGE;
                         const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
-                        if (rank == 0)
-                            mbar_arrive_expect_tx_elect(&full[st], (uint32_t)CG * (GP_UBYTES + (uint32_t)nb * 128u));
+                        if (rank == 0) mbar_arrive_expect_tx_elect(&full[st], CG * GP_UBYTES);
                         if (lane == 0) tma_tile_3d<CG>(dst, &p.ab, c * 32, m0, a, bar);
                         __syncwarp();
                         if (++st == S) {
@@ -324,46 +335,26 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 mbar_wait_bounded(&full[s], (last / S) & 1, p.status);
             }
         if (!ok) settle_after_abort();
-    } else if (warp == 1) {
+    } else if (warp == 1 && (GRAD ? !p.y_index : !p.x_index)) {
         // ---------------- B
         int gs = 0, st = 0;
         uint32_t ph = 1;
-        bool ok = true, waited = false;
+        bool ok = true;
         for (int j = item0; j < n_items && ok; j += stride) {
             const GroupedItem it = item_at(j);
-            const int nb = it.npad / CG, c0 = rank * nb;
-            constexpr int Q = (NT / CG + 127) / 128;  // gathers of a lane
-            int r4[Q][4];
-            if (GRAD) {
-                if (it.steps) grad_rows(it, 0, true, r4[0]);
-            } else if (p.x_index) {
-#pragma unroll
-                for (int i = 0; i < Q; ++i)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = c0 + 4 * (lane + 32 * i) + k;
-                        r4[i][k] = max(0, source(it.row0 + (c < it.n ? c : 0)));  // (columns that are not stored)
-                    }
-            }
-            for (int kb = 0; kb < it.steps; ++kb, ++gs) {
+            const int nb = it.npad / CG, c0 = it.row0 + rank * nb;
+            const int extra = extra_stages(it);
+            for (int kb = 0; kb < it.steps + extra; ++kb, ++gs) {
                 if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
                 uint8_t *dst = ring + (size_t)st * G_::STAGE + GP_ABYTES;
                 const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
                 if (GRAD) {
-#pragma unroll
-                    for (int i = 0; i < (NT / CG + 127) / 128; ++i) {
-                        const int q = lane + 32 * i;
-                        if (4 * q < nb) tma_rows4<CG>(dst + q * 512, &p.b, it.row0 + c0 + 64 * (q >> 4), r4[0], bar);
-                    }
-                    if (kb + 1 < it.steps) grad_rows(it, kb + 1, true, r4[0]);
-                } else if (p.x_index) {
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) {
-                        const int q = lane + 32 * i;
-                        if (4 * q < nb) tma_rows4<CG>(dst + q * 512, &p.b, kb * 64, r4[i], bar);
-                    }
-                } else if (16 * lane < nb) {
-                    tma_tile_2d<CG>(dst + lane * 2048, &p.b, kb * 64, it.row0 + c0 + 16 * lane, bar);
+                    if (64 * lane < nb && 64 * kb + 64 <= it.cnt)
+                        tma_tile_2d<CG>(dst + lane * 8192, &p.b, c0 + 64 * lane, it.r0 + 64 * kb, bar);
+                } else if (kb < it.steps) {
+                    // 64 rows a box, the rest by 16
+                    const int big = nb / 64, r = lane < big ? 64 * lane : 64 * big + 16 * (lane - big);
+                    if (r < nb) tma_tile_2d<CG>(dst + r * 128, lane < big ? &p.b64 : &p.b, kb * 64, c0 + r, bar);
                 }
                 __syncwarp();
                 if (++st == S) {
@@ -371,47 +362,144 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     ph ^= 1u;
                 }
             }
-            if (MODE == GP_LORA && ok) {
-                if (!waited) {
-                    pdl_wait();
-                    waited = true;
+        }
+        if (!ok) settle_after_abort();
+    } else if (warp >= 12 && loaders) {
+        // ---------------- rows that are no box
+        // Two teams of four warps take alternate stages (the ring is an even number of stages: a team sees every phase of the
+        // barriers that it waits for).  A copy costs its warp a few instructions one after another, which is what bounds
+        // this: 8192^3, every row by index: one team of four warps 921 us, two of two 1442.
+        const int team = (warp - 12) >> 2, lt = (tid - 384) & 127;
+        int gs = 0, st = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        auto begin = [&]() -> bool { return gs < S || (ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag)); };
+        auto next = [&]() {
+            ++gs;
+            if (++st == S) {
+                st = 0;
+                ph ^= 1u;
+            }
+        };
+        for (int j = item0; j < n_items && ok; j += stride) {
+            const GroupedItem it = item_at(j);
+            const int nb = it.npad / CG;
+            if (!GRAD) {
+                // eight threads a row: piece lt % 8 of rows lt / 8 + 16 i
+                constexpr int RI = NT / CG / 16;
+                const int piece = lt & 7, r0 = lt >> 3, rows = min(nb, it.n - rank * nb);
+                const uint32_t at = smem_u32(ring) + GP_ABYTES + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
+                const uint16_t *src[RI];
+                int who[RI];  // bytes to copy; GP_LORA: the token's adapter
+#pragma unroll
+                for (int i = 0; i < RI; ++i) {
+                    const int c = r0 + 16 * i;
+                    const int r = c >= rows ? -1 : MODE == GP_LORA ? it.row0 + rank * nb + c : source(it.row0 + rank * nb + c);
+                    who[i] = MODE != GP_LORA ? (r >= 0 ? 16 : 0) : r >= 0 ? p.adapter[r] : -1;
+                    src[i] = p.rows + (size_t)max(r, 0) * p.ld + 8 * piece + (team == (gs & 1) ? 0 : 64);
                 }
-                int ids[8], mine[Q][4];
-                tile_adapters(it, ids);
+                for (int kb = 0; kb < it.steps; ++kb, next()) {
+                    if ((gs & 1) != team) continue;
+                    if (!begin()) break;
+                    if (MODE != GP_LORA) {
+                        const uint32_t d = at + (uint32_t)st * G_::STAGE;
+                        const int most = kb * 64 + 8 * piece < p.K ? 16 : 0;
 #pragma unroll
-                for (int i = 0; i < Q; ++i)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = c0 + 4 * (lane + 32 * i) + k;
-                        mine[i][k] = c < it.n ? p.adapter[it.row0 + c] : -1;
-                    }
-                for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a)) {
-                    // u's rows of the adapter's tokens; for the others its row R, which is zero
-#pragma unroll
-                    for (int i = 0; i < Q; ++i)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            r4[i][k] = mine[i][k] == a ? it.row0 + c0 + 4 * (lane + 32 * i) + k : p.R;
-                    for (int c = 0; c < chunks; ++c, ++gs) {
-                        if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
-                        uint8_t *dst = ring + (size_t)st * G_::STAGE + GP_ABYTES;
-                        const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
-#pragma unroll
-                        for (int i = 0; i < Q; ++i) {
-                            const int q = lane + 32 * i;
-                            if (4 * q < nb) tma_rows4<CG>(dst + q * 512, &p.u, c * 64, r4[i], bar);
-                        }
-                        __syncwarp();
-                        if (++st == S) {
-                            st = 0;
-                            ph ^= 1u;
+                        for (int i = 0; i < RI; ++i) {
+                            if (16 * i < rows) cp_async_16_or_0(d + i * 2048, src[i], min(most, who[i]));
+                            src[i] += kb + 3 > it.steps ? 0 : 128;
                         }
                     }
+                    cp_async_mbar_arrive_noinc(&landed[st]);
+                }
+                if (MODE == GP_LORA && ok) {
+                    if (j == item0) pdl_wait();  // u
+                    int ids[8];
+                    tile_adapters(it, ids);
+                    const uint16_t *u = p.rows + (size_t)(it.row0 + rank * nb + r0) * p.ld + 8 * piece;
+                    for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a))
+                        for (int c = 0; c < chunks; ++c, next()) {
+                            if ((gs & 1) != team) continue;
+                            if (!begin()) break;
+                            const uint32_t d = at + (uint32_t)st * G_::STAGE;
+#pragma unroll
+                            for (int i = 0; i < RI; ++i)
+                                if (16 * i < nb) {
+                                    const bool some = who[i] == a;
+                                    cp_async_16_or_0(d + i * 2048, some ? u + (size_t)16 * i * p.ld + c * 64 : p.rows,
+                                                     some ? 16 : 0);
+                                }
+                            cp_async_mbar_arrive_noinc(&landed[st]);
+                        }
+                }
+            } else {
+                // sixteen threads a row (128 columns): piece lt % 16 of rows lt / 16 + 8 i.  A warp's sixteen rows are looked up
+                // by its lanes 0-15, for the team's next stage while this one is copied.
+                const int piece = lt & 15, r0 = lt >> 4;
+                const int ca = (it.m * CG + rank) * 128 + 8 * piece, cb = rank * nb + 8 * piece;
+                const int in_a = ca < p.M ? 16 : 0, in_b = it.row0 + cb < p.N ? 16 : 0;
+                const uint16_t *a = p.rows + (in_a ? ca : 0), *b = p.dy + (in_b ? it.row0 + cb : 0);
+                const uint32_t at = smem_u32(ring) + (piece >> 3) * 8192 + r0 * 128 + (((piece ^ r0) & 7) << 4);
+                int xr = -1, yr = -1;
+                auto look_up = [&](int kb) {
+                    const int q = kb * 64 + (lt >> 5) * 2 + (lane & 1) + 8 * ((lane >> 1) & 7);
+                    xr = yr = -1;
+                    if (kb < it.steps && q < it.cnt) {
+                        xr = source(it.r0 + q);
+                        yr = target(it.r0 + q);
+                        if (xr < 0 || yr < 0) {
+                            moe_set_status(p.status, MOE_ERR_INVALID);
+                            xr = yr = -1;
+                        }
+                    }
+                };
+                look_up((gs & 1) != team);
+                for (int kb = 0; kb < it.steps; ++kb, next()) {
+                    if ((gs & 1) != team) continue;
+                    if (!begin()) break;
+                    const bool whole = 64 * kb + 64 <= it.cnt;
+                    const uint32_t d = at + (uint32_t)st * G_::STAGE;
+                    if (p.x_index || !whole)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = __shfl_sync(0xffffffffu, xr, 2 * i + (lane >> 4));
+                            cp_async_16_or_0(d + i * 1024, a + (size_t)max(r, 0) * p.ld, r >= 0 ? in_a : 0);
+                        }
+                    if (p.y_index || !whole)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = __shfl_sync(0xffffffffu, yr, 2 * i + (lane >> 4));
+                            if (cb < (rank + 1) * nb)
+                                cp_async_16_or_0(d + GP_ABYTES + i * 1024, b + (size_t)max(r, 0) * p.lddy, r >= 0 ? in_b : 0);
+                        }
+                    look_up(kb + 2);
+                    cp_async_mbar_arrive_noinc(&landed[st]);
                 }
             }
         }
-        if (MODE == GP_LORA && !waited) pdl_wait();
-        if (!ok) settle_after_abort();
+        cp_async_wait_all();
+        if (MODE == GP_LORA) pdl_wait();
+    } else if (warp == 3 && loaders) {
+        // ---------------- the loaders' stages: their copies have landed; the tensor cores may read them
+        int st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int j = item0; j < n_items && ok; j += stride) {
+            const GroupedItem it = item_at(j);
+            const int n = it.steps + extra_stages(it);
+            for (int kb = 0; kb < n; ++kb) {
+                if (!(ok = mbar_wait_warp(&landed[st], ph, p.status, abort_flag))) break;
+                fence_proxy_async_smem();
+                if (lane == 0) {
+                    if (CG == 1) mbar_arrive1(&full[st]);
+                    else mbar_arrive_cluster(cluster_map(&full[st], 0));
+                }
+                if (++st == S) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
     } else if (warp == 2 && rank == 0) {
         // ---------------- MMA issuer
         int jl = 0, st = 0;
@@ -421,12 +509,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             const GroupedItem it = item_at(j);
             const uint32_t idesc = umma_idesc_16(p.fmt, A_MN, B_MN, 128 * CG, it.npad);
             const int buf = jl & 1;
-            int extra = 0;
-            if (MODE == GP_LORA) {
-                int ids[8];
-                tile_adapters(it, ids);
-                for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a)) extra += chunks;
-            }
+            const int extra = extra_stages(it);
             if (jl >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((jl / 2) - 1) & 1, p.status, abort_flag))) break;
             tc_fence_after();
             const uint32_t d = tmem + buf * NT;
@@ -471,7 +554,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         }
         umma_commit_group_elect<CG>(mma_done);  // every MMA has completed before tensor memory is released
         mbar_wait_bounded(mma_done, 0, p.status);
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 12) {
         // ---------------- epilogue: lane = row of the M side; 32 of them x 16 rows of the group at a time by way of
         // shared memory, so that a store covers 32 consecutive elements of an output row
         const int q = warp & 3, ew = warp - 4, half = ew >> 2, et = ew * 32 + lane;

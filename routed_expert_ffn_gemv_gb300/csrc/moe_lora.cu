@@ -2,9 +2,8 @@
 //
 //   y[t] = W x_t + B_a u_t,   u_t = scale[a] A_a x_t,   a = adapter[t]
 // Two kernels.  lora_shrink_kernel computes u in fp32 and leaves it as two 16-bit halves (the nearest, and the nearest of what
-// is left: 16 bits of bf16, 22 of fp16), 32 ranks to a 128-byte row piece, upper halves first, and a row of zeros behind the
-// last token's.  The product's kernel (moe_grouped.cuh, GP_LORA) runs K on into the ranks: for each adapter that has tokens in
-// its tile, 32 ranks at a time, B_a's tile against the tokens' rows of u, the zero row for the tokens of other adapters.  So y
+// is left: 16 bits of bf16, 22 of fp16), 32 ranks to a 128-byte row piece, upper halves first.  The product's kernel (moe_grouped.cuh, GP_LORA) runs K on into the ranks: for each adapter that has tokens in
+// its tile, 32 ranks at a time, B_a's tile against the tokens' rows of u, zeros for the tokens of other adapters.  So y
 // is rounded once and W's part and the adapters' share an accumulator.  The product starts beside the first kernel and waits
 // for u only where it loads it.
 #include "moe_grouped.cuh"
@@ -31,7 +30,7 @@ __device__ __forceinline__ void split16(float v, uint16_t &hi, uint16_t &lo) {
     }
 }
 
-// A warp: LS_RANKS ranks of one token.  u: [T + 1][chunks][64].
+// A warp: LS_RANKS ranks of one token.  u: [T][chunks][64].
 template <bool BF>
 __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, size_t ldx, int T, int K, const int32_t *adapter,
                                                           int n_adapters, const uint16_t *a, int rank, const float *scale,
@@ -41,11 +40,11 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
     const int lane = threadIdx.x % 32, chunks = (rank + 31) / 32, groups = chunks * 32 / LS_RANKS;
     const long long job = (long long)blockIdx.x * 8 + threadIdx.x / 32;
     const int t = (int)(job / groups), j0 = (int)(job % groups) * LS_RANKS;
-    if (t > T) return;
-    const int ad = t < T ? adapter[t] : 0;
+    if (t >= T) return;
+    const int ad = adapter[t];
     if (ad < 0 || ad >= n_adapters) return;  // (no product reads this row)
     float v[LS_RANKS] = {};
-    if (t < T && j0 < rank) {
+    if (j0 < rank) {
         const uint16_t *xr = x + (size_t)t * ldx, *ar = a + ((size_t)ad * rank + j0) * K;
         for (int k = 8 * lane; k < K; k += 256) {
             const uint4 xv = *(const uint4 *)(xr + k);
@@ -72,8 +71,8 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
 #pragma unroll
         for (int j = 0; j < LS_RANKS; ++j)
             if (j == lane) r = v[j];
-        if (scale && t < T) r *= scale[ad];
-        if (t == T || j0 >= rank) r = 0.f;
+        if (scale) r *= scale[ad];
+        if (j0 >= rank) r = 0.f;
         uint16_t hi, lo;
         split16<BF>(r, hi, lo);
         const int j = j0 + lane;
@@ -95,7 +94,7 @@ extern "C" int moe_lora_workspace(int T, int rank, size_t *bytes) {
     MOE_CHECK(bytes);
     const int rc = check(T, rank);
     if (rc != MOE_OK) return rc;
-    *bytes = ((size_t)T + 1) * ((rank + 31) / 32) * 128;
+    *bytes = (size_t)T * ((rank + 31) / 32) * 128;
     return MOE_OK;
 }
 
@@ -124,8 +123,9 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     }
     {
         const uint64_t dims[2] = {(uint64_t)K, (uint64_t)T}, strides[1] = {(uint64_t)ldx * 2};
-        const uint32_t box[2] = {64, 16};
+        const uint32_t box[2] = {64, 16}, box64[2] = {64, 64};
         if ((rc = grouped_map(&p.b, type, 2, x, dims, strides, box, 128)) != MOE_OK) return rc;
+        if ((rc = grouped_map(&p.b64, type, 2, x, dims, strides, box64, 128)) != MOE_OK) return rc;
     }
     {
         const uint64_t dims[3] = {(uint64_t)rank, (uint64_t)N, (uint64_t)n_adapters};
@@ -133,11 +133,8 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
         const uint32_t box[3] = {32, 128, 1};
         if ((rc = grouped_map(&p.ab, type, 3, b, dims, strides, box, 64)) != MOE_OK) return rc;
     }
-    {
-        const uint64_t dims[2] = {(uint64_t)chunks * 64, (uint64_t)T + 1}, strides[1] = {(uint64_t)chunks * 128};
-        const uint32_t box[2] = {64, 1};
-        if ((rc = grouped_map(&p.u, type, 2, workspace, dims, strides, box, 128)) != MOE_OK) return rc;
-    }
+    p.rows = (const uint16_t *)workspace;
+    p.ld = (size_t)chunks * 64;
     p.G = 1;
     p.R = T;
     p.x_rows = T;
@@ -156,7 +153,7 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
 
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    const long long jobs = ((long long)T + 1) * (chunks * 32 / LS_RANKS);
+    const long long jobs = (long long)T * (chunks * 32 / LS_RANKS);
     moe_pdl_config(&cfg, attr, dim3((unsigned)((jobs + 7) / 8)), dim3(256), 0, moe_cuda_stream(s));
     const uint16_t *xa = (const uint16_t *)x, *aa = (const uint16_t *)a;
     MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, type == MOE_BF16 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>, xa, ldx, T,
