@@ -531,7 +531,7 @@ int moe_mx4_layer(const void *x, int xtype, int T, int H, int F, int E, int k, c
  *   moe_grouped_matmul(h, scale = weights, y_index = rows)          -> partial [T][k][H]
  *   moe_combine(partial).
  */
-#define MOE_MAX_GROUPS 1024 /* groups of a call */
+#define MOE_MAX_GROUPS 512  /* groups of a call */
 #define MOE_MAX_RANK 256    /* ranks of an adapter */
 
 /* Order of a matrix of N outputs by K inputs. */

@@ -31,7 +31,7 @@ MOE_ORDER_NK = 0
 MOE_ORDER_KN = 1
 MOE_ACT_NONE = 0
 MOE_ACT_SWIGLU = 1
-MOE_MAX_GROUPS = 1024
+MOE_MAX_GROUPS = 512
 MOE_MAX_RANK = 256
 MOE_MAX_K = 8
 MOE_MAX_E = 256

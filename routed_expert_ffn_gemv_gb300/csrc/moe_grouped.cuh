@@ -73,48 +73,36 @@ struct GroupedGeom {
     static constexpr int TCOLS = 2 * NT < 32 ? 32 : 2 * NT;  // two accumulators
     static constexpr int O_OFF = 1024, O_FIRST = O_OFF + (MOE_MAX_GROUPS + 4) * 4;
     static constexpr int O_ROWS = O_FIRST + (MOE_MAX_GROUPS + 4) * 4;
-    static constexpr int O_XCH = O_ROWS + 2 * NT * 8;
-    static constexpr int XCH = 16 * 36;                      // floats of a warp: 16 rows x 32 (padded)
-    static constexpr int O_RING = (O_XCH + 8 * XCH * 4 + 1023) / 1024 * 1024;
+    static constexpr int O_XCH = O_ROWS + 2 * NT * 16;
+    static constexpr int XCH = 2 * 16 * 80;                  // bytes of an epilogue warp: two chunks
+    static constexpr int O_RING = (O_XCH + 8 * XCH + 1023) / 1024 * 1024;
     static constexpr int S = (227 * 1024 - 1024 - O_RING) / STAGE / 2 * 2;  // (even: see the loaders)
     static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
     static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 5) * 8 + 16 + 80 <= 1024 && S >= 3, "");
 };
 
+struct alignas(16) GroupedRow {
+    uint8_t *y;  // the output row (NULL: none)
+    float scale;
+    int pad;
+};
 struct GroupedItem {
     int g, m, row0, n, npad;  // group, M tile, first row (GP_GRAD: first output row), rows, rows rounded up
     int r0, cnt, steps;       // GP_GRAD: the group's first row and rows; stages of the reduction
 };
 
-__device__ __forceinline__ void grouped_store4(void *y, int ytype, size_t i, float4 v, bool accumulate) {
-    if (ytype == MOE_F32) {
-        float4 *o = (float4 *)((float *)y + i);
-        if (accumulate) {
-            const float4 w = *o;
-            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-        }
-        *o = v;
-    } else if (ytype == MOE_BF16) {
-        uint2 *o = (uint2 *)((__nv_bfloat16 *)y + i);
-        if (accumulate) {
-            const uint2 w = *o;
-            v.x += __uint_as_float(w.x << 16);
-            v.y += __uint_as_float(w.x & 0xFFFF0000u);
-            v.z += __uint_as_float(w.y << 16);
-            v.w += __uint_as_float(w.y & 0xFFFF0000u);
-        }
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-        *o = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
-    } else {
-        uint2 *o = (uint2 *)((__half *)y + i);
-        if (accumulate) {
-            const uint2 w = *o;
-            const float2 a = __half22float2(*(const __half2 *)&w.x), b = __half22float2(*(const __half2 *)&w.y);
-            v = make_float4(v.x + a.x, v.y + a.y, v.z + b.x, v.w + b.y);
-        }
-        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-        *o = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
+// Two results to the two 16-bit halves of a word and back.
+__device__ __forceinline__ uint32_t grouped_pack(float lo, float hi, bool bf) {
+    if (bf) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *(const uint32_t *)&v;
     }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *(const uint32_t *)&v;
+}
+__device__ __forceinline__ float2 grouped_unpack(uint32_t w, bool bf) {
+    if (bf) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*(const __half2 *)&w);
 }
 
 // 16 bytes global -> shared (bytes = 16), or zeros (0).
@@ -157,7 +145,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     int *sums = (int *)(tmem_slot + 4);                       // [20]
     int *off = (int *)(smem + G_::O_OFF);                     // [G + 1]
     int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before a group's
-    int2 *e_rows = (int2 *)(smem + G_::O_ROWS);               // [2][NT] output row (-1: none), scale
+    GroupedRow *e_rows = (GroupedRow *)(smem + G_::O_ROWS);   // [2][NT]
     uint8_t *ring = smem + G_::O_RING;
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -381,8 +369,33 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 ph ^= 1u;
             }
         };
+        // GP_GRAD: a warp's sixteen rows of a stage, looked up by its lanes 0-15 for the team's next stage (of this item or the
+        // next) while this one is copied
+        int xr = -1, yr = -1;
+        auto look_up = [&](const GroupedItem &it, int kb) {
+            const int q = kb * 64 + (lt >> 5) * 2 + (lane & 1) + 8 * ((lane >> 1) & 7);
+            xr = yr = -1;
+            if (kb < it.steps && q < it.cnt) {
+                xr = source(it.r0 + q);
+                yr = target(it.r0 + q);
+                if (xr < 0 || yr < 0) {
+                    moe_set_status(p.status, MOE_ERR_INVALID);
+                    xr = yr = -1;
+                }
+            }
+        };
+        GroupedItem it = {}, after = {};
+        if (GRAD && item0 < n_items) {
+            after = item_at(item0);
+            look_up(after, team);
+        }
         for (int j = item0; j < n_items && ok; j += stride) {
-            const GroupedItem it = item_at(j);
+            if (GRAD) {
+                it = after;
+                if (j + stride < n_items) after = item_at(j + stride);
+            } else {
+                it = item_at(j);
+            }
             const int nb = it.npad / CG;
             if (!GRAD) {
                 // eight threads a row: piece lt % 8 of rows lt / 8 + 16 i
@@ -433,27 +446,15 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         }
                 }
             } else {
-                // sixteen threads a row (128 columns): piece lt % 16 of rows lt / 16 + 8 i.  A warp's sixteen rows are looked up
-                // by its lanes 0-15, for the team's next stage while this one is copied.
+                // sixteen threads a row (128 columns): piece lt % 16 of rows lt / 16 + 8 i
+                const int end = gs + it.steps;  // the next item's first stage
+                const bool more = j + stride < n_items, any = it.steps > ((gs & 1) != team);
+                if (!any && more) look_up(after, (end & 1) != team);
                 const int piece = lt & 15, r0 = lt >> 4;
                 const int ca = (it.m * CG + rank) * 128 + 8 * piece, cb = rank * nb + 8 * piece;
                 const int in_a = ca < p.M ? 16 : 0, in_b = it.row0 + cb < p.N ? 16 : 0;
                 const uint16_t *a = p.rows + (in_a ? ca : 0), *b = p.dy + (in_b ? it.row0 + cb : 0);
                 const uint32_t at = smem_u32(ring) + (piece >> 3) * 8192 + r0 * 128 + (((piece ^ r0) & 7) << 4);
-                int xr = -1, yr = -1;
-                auto look_up = [&](int kb) {
-                    const int q = kb * 64 + (lt >> 5) * 2 + (lane & 1) + 8 * ((lane >> 1) & 7);
-                    xr = yr = -1;
-                    if (kb < it.steps && q < it.cnt) {
-                        xr = source(it.r0 + q);
-                        yr = target(it.r0 + q);
-                        if (xr < 0 || yr < 0) {
-                            moe_set_status(p.status, MOE_ERR_INVALID);
-                            xr = yr = -1;
-                        }
-                    }
-                };
-                look_up((gs & 1) != team);
                 for (int kb = 0; kb < it.steps; ++kb, next()) {
                     if ((gs & 1) != team) continue;
                     if (!begin()) break;
@@ -472,7 +473,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                             if (cb < (rank + 1) * nb)
                                 cp_async_16_or_0(d + GP_ABYTES + i * 1024, b + (size_t)max(r, 0) * p.lddy, r >= 0 ? in_b : 0);
                         }
-                    look_up(kb + 2);
+                    if (kb + 2 < it.steps) look_up(it, kb + 2);
+                    else if (more) look_up(after, (end & 1) != team);
                     cp_async_mbar_arrive_noinc(&landed[st]);
                 }
             }
@@ -507,23 +509,35 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         bool ok = true;
         for (int j = item0; j < n_items && ok; j += stride, ++jl) {
             const GroupedItem it = item_at(j);
-            const uint32_t idesc = umma_idesc_16(p.fmt, A_MN, B_MN, 128 * CG, it.npad);
+            // (a value that a shuffle hands out is known to be the same in every lane: it stays in a uniform register, where
+            // the MMA wants its operands)
+            const uint32_t idesc = umma_idesc_16(p.fmt, A_MN, B_MN, 128 * CG, __shfl_sync(0xffffffffu, it.npad, 0));
             const int buf = jl & 1;
             const int extra = extra_stages(it);
             if (jl >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((jl / 2) - 1) & 1, p.status, abort_flag))) break;
             tc_fence_after();
-            const uint32_t d = tmem + buf * NT;
-            const int len = GRAD ? it.cnt : p.K;
-            for (int kb = 0; kb < it.steps; ++kb) {
+            const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + buf * NT;
+            const int len = GRAD ? __shfl_sync(0xffffffffu, it.cnt, 0) : p.K, n_steps = __shfl_sync(0xffffffffu, it.steps, 0);
+            for (int kb = 0; kb < n_steps; ++kb) {
                 if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
                 tc_fence_after();
                 const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
                 const uint64_t a = A_MN ? umma_desc_mn_sw128(sa, 8192) : umma_desc_sw128(sa);
                 const uint64_t b = B_MN ? umma_desc_mn_sw128(sa + GP_ABYTES, 8192) : umma_desc_sw128(sa + GP_ABYTES);
-                const int steps = min(4, (len - 64 * kb + 15) / 16);
-                for (int q = 0; q < steps; ++q)
+                const int left = len - 64 * kb;
+                auto step = [&](int q) {
                     umma_f16_elect<CG>(d, a + (uint64_t)(q * (A_MN ? 128 : 2)), b + (uint64_t)(q * (B_MN ? 128 : 2)), idesc,
-                                       kb > 0 || q > 0);
+                                       q > 0 || kb > 0);
+                };
+                step(0);
+                if (left > 48) {  // (no branch between the MMAs)
+                    step(1);
+                    step(2);
+                    step(3);
+                } else {
+                    if (left > 16) step(1);
+                    if (left > 32) step(2);
+                }
                 umma_commit_group_elect<CG>(&empty[st]);
                 if (++st == S) {
                     st = 0;
@@ -555,85 +569,161 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         umma_commit_group_elect<CG>(mma_done);  // every MMA has completed before tensor memory is released
         mbar_wait_bounded(mma_done, 0, p.status);
     } else if (warp >= 4 && warp < 12) {
-        // ---------------- epilogue: lane = row of the M side; 32 of them x 16 rows of the group at a time by way of
-        // shared memory, so that a store covers 32 consecutive elements of an output row
+        // ---------------- epilogue: an accumulator column is an output row.  16-bit results: fragments of 16 lanes x 8 columns,
+        // each pair of columns packed, transposed by way of shared memory (stmatrix), so that a lane stores eight
+        // consecutive elements of an output row; fp32 results transposed a word at a time, four consecutive elements a store.
+        // (Stored straight from the registers, 128 bytes of one output row an instruction: 4864 x 4096 x 512 31.4 us,
+        // this way 24.8.)
         const int q = warp & 3, ew = warp - 4, half = ew >> 2, et = ew * 32 + lane;
-        float *xb = (float *)(smem + G_::O_XCH) + ew * G_::XCH;
+        const bool bf = p.ytype == MOE_BF16, f32 = p.ytype == MOE_F32;
+        const uint32_t xb = smem_u32(smem + G_::O_XCH) + ew * G_::XCH;
+        const int size = f32 ? 4 : 2;
+        // stmatrix: the address of row lane % 8 of 8 x 8 matrix lane / 8.  Matrices 0, 1: output rows 0-7, elements 0-7 and 8-15;
+        // 2, 3: output rows 8-15
+        constexpr int PITCH = MODE == GP_SWIGLU ? 48 : 80;  // (no bank conflicts)
+        const uint32_t xm = xb + ((lane & 7) + 8 * (lane >> 4)) * PITCH + ((lane >> 3) & 1) * 16;
         int jl = 0;
         for (int j = item0; j < n_items; j += stride, ++jl) {
             const GroupedItem it = item_at(j);
             const int buf = jl & 1;
             if (et < NT && et < it.n) {
-                int dst = -1;
-                float s = 1.f;
+                GroupedRow r;
+                r.y = nullptr;
+                r.scale = 1.f;
                 if (GRAD) {
-                    dst = it.row0 + et;
+                    r.y = (uint8_t *)p.y + ((size_t)it.g * p.N + it.row0 + et) * p.M * size;
                 } else {
-                    dst = target(it.row0 + et);
-                    if (source(it.row0 + et) < 0) dst = -1;
-                    if (dst < 0) moe_set_status(p.status, MOE_ERR_INVALID);
-                    else if (p.scale) s = p.scale[dst];
+                    const int dst = source(it.row0 + et) < 0 ? -1 : target(it.row0 + et);
+                    if (dst < 0) {
+                        moe_set_status(p.status, MOE_ERR_INVALID);
+                    } else {
+                        r.y = (uint8_t *)p.y + (size_t)dst * p.ldy * size;
+                        if (p.scale) r.scale = p.scale[dst];
+                    }
                 }
-                e_rows[buf * NT + et] = make_int2(dst, __float_as_int(s));
+                e_rows[buf * NT + et] = r;
             }
             const bool w = mbar_wait_role(&acc_full[buf], (jl / 2) & 1, p.status, abort_flag);
             if (!bar_and_n(1, 256, w)) break;
             tc_fence_after();
             const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * NT;
-            const int2 *rows = e_rows + buf * NT;
-            const size_t base = GRAD ? (size_t)it.g * p.N * p.M : 0;
-            if (MODE != GP_SWIGLU) {
-                const int o = (it.m * CG + rank) * 128 + 32 * q + 4 * (lane & 7);
-                for (int c0 = 16 * half; c0 < it.n; c0 += 32) {
-                    uint32_t v[16];
+            const GroupedRow *rows = e_rows + buf * NT;
+            const bool none = GRAD && !it.steps;
+            const int m0 = (it.m * CG + rank) * MROWS + MROWS / 4 * q;  // the warp's first element
+            // 16 columns: 32x32b, or in fragments the first 16 lanes' registers, then the others'
+            auto load = [&](uint32_t (&v)[16], int c0) {
+                if (MODE != GP_SWIGLU && f32) {
                     tmem_ld16(tb + c0, v);
-                    tmem_ld_wait();
+                } else {
+                    tmem_ld_16x256b_x2(tb + c0, reinterpret_cast<uint32_t(&)[8]>(v[0]));
+                    tmem_ld_16x256b_x2(tb + (16u << 16) + c0, reinterpret_cast<uint32_t(&)[8]>(v[8]));
+                }
+            };
+            auto process = [&](uint32_t (&v)[16], int c0, int odd) {
+                if (none)
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) xb[36 * k + lane] = GRAD && !it.steps ? 0.f : __uint_as_float(v[k]);
+                    for (int k = 0; k < 16; ++k) v[k] = 0u;
+                if (MODE != GP_SWIGLU && f32) {
+                    float *x = (float *)(smem + G_::O_XCH + ew * G_::XCH);  // padded to 36: no bank conflicts
+                    const int m = m0 + 4 * (lane & 7);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[36 * k + lane] = __uint_as_float(v[k]);
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int c = 4 * k + (lane >> 3);
-                        float4 a = *(const float4 *)(xb + 36 * c + 4 * (lane & 7));
-                        if (c0 + c < it.n && o < p.M) {
-                            const int2 r = rows[c0 + c];
-                            if (!GRAD) {
-                                const float s = __int_as_float(r.y);
-                                a = make_float4(s * a.x, s * a.y, s * a.z, s * a.w);
+                        float4 a = *(const float4 *)(x + 36 * c + 4 * (lane & 7));
+                        if (c0 + c < it.n && m < p.M) {
+                            const GroupedRow r = rows[c0 + c];
+                            float4 *o = (float4 *)((float *)r.y + m);
+                            if (!GRAD) a = make_float4(r.scale * a.x, r.scale * a.y, r.scale * a.z, r.scale * a.w);
+                            if (GRAD && p.accumulate) {
+                                const float4 b = *o;
+                                a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
                             }
-                            if (r.x >= 0) grouped_store4(p.y, p.ytype, base + (size_t)r.x * p.ldy + o, a, GRAD && p.accumulate);
+                            if (GRAD || r.y) *o = a;
                         }
                     }
                     __syncwarp();
+                    return;
                 }
-            } else {
-                // lanes 0-15 hold gate rows, 16-31 the same up rows: they trade eight of 16 rows of the group
-                const int f0 = (it.m * CG + rank) * 64 + 16 * q, o = f0 + 4 * (lane & 3);
-                const bool up = lane >= 16;
-                for (int c0 = 16 * half; c0 < it.n; c0 += 32) {
-                    uint32_t v[16];
-                    tmem_ld16(tb + c0, v);
-                    tmem_ld_wait();
+                // registers 4 b + {0, 1}: row lane / 4, columns 8 b + 2 (lane % 4) + {0, 1}; + {2, 3}: row lane / 4 + 8
+                uint32_t(&lo)[8] = reinterpret_cast<uint32_t(&)[8]>(v[0]);
+                uint32_t(&hi)[8] = reinterpret_cast<uint32_t(&)[8]>(v[8]);
+                const int cq = c0 + 2 * (lane & 3);
+                const uint32_t to = xm + odd * (G_::XCH / 2), from = xb + odd * (G_::XCH / 2);
+                if (MODE == GP_SWIGLU) {
+                    float h[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, up ? v[k] : v[8 + k], 16));
-                        const float gv = up ? other : __uint_as_float(v[k]), uv = up ? __uint_as_float(v[8 + k]) : other;
-                        // (16 floats further for the second eight rows: no bank conflicts)
-                        xb[20 * (k + (up ? 8 : 0)) + (up ? 16 : 0) + (lane & 15)] = mx4_swiglu<true>(gv, uv);
+                    for (int k = 0; k < 8; ++k) h[k] = mx4_swiglu<true>(__uint_as_float(lo[k]), __uint_as_float(hi[k]));
+                    if (p.scale || f32) {
+                        // (e_rows past the last row may hold anything: not stored)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int c = cq + 8 * (k >> 2) + (k & 1), m = m0 + (lane >> 2) + 4 * (k & 2);
+                            if (c < it.n) {
+                                const GroupedRow r = rows[c];
+                                h[k] *= r.scale;
+                                if (f32 && r.y && m < p.M) ((float *)r.y)[m] = h[k];
+                            }
+                        }
+                        if (f32) return;
                     }
+                    stmatrix_x4_trans(to, grouped_pack(h[0], h[1], bf), grouped_pack(h[2], h[3], bf),
+                                      grouped_pack(h[4], h[5], bf), grouped_pack(h[6], h[7], bf));
+                    __syncwarp();
+                    const int c = lane >> 1, m = m0 + 8 * (lane & 1);
+                    const uint4 a = ld_shared_16(from + c * PITCH + 16 * (lane & 1));
+                    if (c0 + c < it.n && m < p.M && rows[c0 + c].y) *(uint4 *)(rows[c0 + c].y + 2 * m) = a;
+                } else {
+                    uint32_t old[8] = {};
+                    if (GRAD && p.accumulate) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int c = 8 * k + (lane >> 2), m = m0 + 8 * (lane & 3);
+                            if (c0 + c < it.n && m < p.M)
+                                st_shared_16(from + c * PITCH + 16 * (lane & 3), *(const uint4 *)(rows[c0 + c].y + 2 * m));
+                        }
+                        __syncwarp();
+                        ldmatrix_x4_trans(to, old[0], old[1], old[2], old[3]);
+                        ldmatrix_x4_trans(to + 32, old[4], old[5], old[6], old[7]);
+                        __syncwarp();
+                    }
+                    float s[4] = {1.f, 1.f, 1.f, 1.f};
+                    if (!GRAD && p.scale)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (cq + 8 * (k >> 1) + (k & 1) < it.n) s[k] = rows[cq + 8 * (k >> 1) + (k & 1)].scale;
+                    auto pack = [&](const uint32_t (&v)[8], int k, uint32_t before) -> uint32_t {
+                        float2 o = make_float2(0.f, 0.f);
+                        if (GRAD && p.accumulate) o = grouped_unpack(before, bf);
+                        return grouped_pack(fmaf(s[k >> 2 << 1], __uint_as_float(v[k]), o.x),
+                                            fmaf(s[(k >> 2 << 1) + 1], __uint_as_float(v[k + 1]), o.y), bf);
+                    };
+                    stmatrix_x4_trans(to, pack(lo, 0, old[0]), pack(lo, 2, old[1]), pack(lo, 4, old[2]), pack(lo, 6, old[3]));
+                    stmatrix_x4_trans(to + 32, pack(hi, 0, old[4]), pack(hi, 2, old[5]), pack(hi, 4, old[6]), pack(hi, 6, old[7]));
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int c = 8 * k + (lane >> 2);
-                        float4 a = *(const float4 *)(xb + 20 * c + 16 * k + 4 * (lane & 3));
-                        if (c0 + c < it.n && o < p.M) {
-                            const int2 r = rows[c0 + c];
-                            const float s = __int_as_float(r.y);
-                            a = make_float4(s * a.x, s * a.y, s * a.z, s * a.w);
-                            if (r.x >= 0) grouped_store4(p.y, p.ytype, (size_t)r.x * p.ldy + o, a, false);
-                        }
+                        const int c = 8 * k + (lane >> 2), m = m0 + 8 * (lane & 3);
+                        const uint4 a = ld_shared_16(from + c * PITCH + 16 * (lane & 3));
+                        if (c0 + c < it.n && m < p.M && rows[c0 + c].y) *(uint4 *)(rows[c0 + c].y + 2 * m) = a;
                     }
-                    __syncwarp();
+                }
+            };
+            // a chunk of 16 columns is read from tensor memory while the one before it is worked on (two buffers each: a
+            // warp barrier lies between two uses of one)
+            uint32_t v0[16], v1[16];
+            int c0 = 16 * half;
+            if (c0 < it.n) load(v0, c0);
+            for (; c0 < it.n; c0 += 64) {
+                tmem_ld_wait();
+                if (c0 + 32 < it.n) load(v1, c0 + 32);
+                process(v0, c0, 0);
+                if (c0 + 32 < it.n) {
+                    tmem_ld_wait();
+                    if (c0 + 64 < it.n) load(v0, c0 + 64);
+                    process(v1, c0 + 32, 1);
                 }
             }
             tc_fence_before();
