@@ -6,10 +6,6 @@
 
 #include "moe_grouped.cuh"
 
-#ifndef GP_WIDE_CG
-#define GP_WIDE_CG 2
-#endif
-
 namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -24,40 +20,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
             fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
     });
     return fn;
-}
-
-template <int CG, int NT, int MODE>
-int launch(const GroupedParams &p, long long items, cudaStream_t s) {
-    using G = GroupedGeom<CG, NT>;
-    static std::mutex mu;
-    static int sms[64] = {0};
-    int dev = -1;
-    MOE_TRY_CUDA(cudaGetDevice(&dev));
-    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
-    int n = 0;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!sms[dev]) {
-            int count = 0;
-            MOE_TRY_CUDA(cudaFuncSetAttribute(grouped_kernel<CG, NT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              (int)G::SMEM));
-            MOE_TRY_CUDA(cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev));
-            sms[dev] = count;
-        }
-        n = sms[dev];
-    }
-    const long long groups = std::max(1LL, std::min<long long>(items, n / CG));
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    moe_pdl_config(&cfg, attr, dim3((unsigned)(groups * CG)), dim3(GP_THREADS), G::SMEM, s);
-    if (CG > 1) {
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = CG;
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.numAttrs = 2;
-    }
-    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, grouped_kernel<CG, NT, MODE>, p));
-    return MOE_OK;
 }
 
 bool type16(int t) { return t == MOE_BF16 || t == MOE_F16; }
@@ -107,17 +69,6 @@ int grouped_map(CUtensorMap *map, int type, int rank, const void *base, const ui
     return MOE_OK;
 }
 
-int grouped_launch(const GroupedParams &p, int mode, bool wide, long long items, cudaStream_t s) {
-    switch (mode) {
-        case GP_NK: return wide ? launch<GP_WIDE_CG, 256, GP_NK>(p, items, s) : launch<1, 32, GP_NK>(p, items, s);
-        case GP_KN: return wide ? launch<GP_WIDE_CG, 256, GP_KN>(p, items, s) : launch<1, 32, GP_KN>(p, items, s);
-        case GP_SWIGLU:
-            return wide ? launch<GP_WIDE_CG, 256, GP_SWIGLU>(p, items, s) : launch<1, 32, GP_SWIGLU>(p, items, s);
-        case GP_LORA: return wide ? launch<GP_WIDE_CG, 256, GP_LORA>(p, items, s) : launch<1, 32, GP_LORA>(p, items, s);
-        default: return launch<GP_WIDE_CG, 256, GP_GRAD>(p, items, s);
-    }
-}
-
 extern "C" int moe_grouped_matmul(const void *x, int type, int x_rows, size_t ldx, const int32_t *x_index, int x_share,
                                   const int32_t *offsets, int G, int R, const void *w, int w_order, int N, int K, int act,
                                   const float *scale, const int32_t *y_index, void *y, int ytype, int y_rows, size_t ldy,
@@ -162,16 +113,15 @@ extern "C" int moe_grouped_matmul(const void *x, int type, int x_rows, size_t ld
     p.scale = scale;
     p.y = y;
     p.ldy = ldy;
-    p.ytype = ytype;
     p.M = N;
     p.K = K;
     p.fmt = type == MOE_BF16;
     p.status = moe_status_word_device_ptr();
     // few rows to a group: narrow tiles, one CTA each
     const bool wide = R > 16LL * G;
-    const int nt = wide ? 256 : 32, mrows = (swiglu ? 64 : 128) * (wide ? GP_WIDE_CG : 1);
+    const int nt = wide ? 256 : 32, mrows = (swiglu ? 64 : 128) * (wide ? 2 : 1);
     const long long row_tiles = (long long)R / nt + std::min(G, R);
-    return grouped_launch(p, mode, wide, row_tiles * ((N + mrows - 1) / mrows), moe_cuda_stream(s));
+    return grouped_launch(p, ytype, mode, wide, row_tiles * ((N + mrows - 1) / mrows), (K + 63) / 64, moe_cuda_stream(s));
 }
 
 extern "C" int moe_grouped_weight_grad(const void *x, int type, int x_rows, size_t ldx, const int32_t *x_index,
@@ -209,12 +159,11 @@ extern "C" int moe_grouped_weight_grad(const void *x, int type, int x_rows, size
     p.y_rows = dy_rows;
     p.y = dw;
     p.ldy = K;
-    p.ytype = wtype;
     p.M = K;
     p.N = N;
     p.accumulate = accumulate;
     p.fmt = type == MOE_BF16;
     p.status = moe_status_word_device_ptr();
-    const long long items = (long long)G * ((N + 255) / 256) * ((K + 128 * GP_WIDE_CG - 1) / (128 * GP_WIDE_CG));
-    return grouped_launch(p, GP_GRAD, true, items, moe_cuda_stream(s));
+    const long long items = (long long)G * ((N + 255) / 256) * ((K + 255) / 256);
+    return grouped_launch(p, wtype, GP_GRAD, true, items, 0, moe_cuda_stream(s));
 }

@@ -25,6 +25,8 @@
 //   warp 3       hands their stages over once they have landed.  (TMA gathers, four rows an instruction,
 //                take about 40 ns each however many are in flight: 32768 rows of 2048 gathered for 1536
 //                outputs took 510 us.)
+// CG = 1: where items are few, the CTAs of a cluster share an item's reduction and add their sums up over distributed shared
+// memory, in the order of their ranks.
 // CG = 2: two CTAs share each MMA (M = 256), every CTA loads half of A and half of B.
 #pragma once
 
@@ -56,7 +58,6 @@ struct GroupedParams {
     const float *scale;       // [y_rows] or NULL
     void *y;
     size_t ldy;               // GP_GRAD: M
-    int ytype;
     int M, K, N;              // columns of an output row; reduction (not GP_GRAD); GP_GRAD: output rows of a group
     int accumulate;           // GP_GRAD
     const int32_t *adapter;   // GP_LORA, [R]
@@ -65,44 +66,61 @@ struct GroupedParams {
     int *status;
 };
 
+#define GP_ITEMS 96       // items of a CTA that are worked out ahead, in shared memory
+#define GP_MAX_SPLIT 8    // CTAs that share an item's reduction
+
 template <int CG, int NT>
 struct GroupedGeom {
     static constexpr int GRAN = 16 * CG;                     // rows an MMA's width is rounded up to
     static constexpr int BBYTES = NT / CG * 128;
     static constexpr int STAGE = GP_ABYTES + BBYTES;
     static constexpr int TCOLS = 2 * NT < 32 ? 32 : 2 * NT;  // two accumulators
-    static constexpr int O_OFF = 1024, O_FIRST = O_OFF + (MOE_MAX_GROUPS + 4) * 4;
+    static constexpr int CH = NT >= 64 ? 32 : 16;            // columns of an epilogue warp's chunk
+    static constexpr int XCH = CH * 80 < 2304 ? 2304 : CH * 80;  // bytes of an epilogue warp
+    // CG = 1: partial sums of up to GP_MAX_SPLIT CTAs, for this CTA's share of the rows
+    static constexpr int RED = CG == 1 ? (NT + GP_MAX_SPLIT - 1) * 512 : 0;
+    static constexpr int O_ITEMS = 1024, O_OFF = O_ITEMS + GP_ITEMS * 16;
+    static constexpr int O_FIRST = O_OFF + (MOE_MAX_GROUPS + 4) * 4;
     static constexpr int O_ROWS = O_FIRST + (MOE_MAX_GROUPS + 4) * 4;
-    static constexpr int O_XCH = O_ROWS + 2 * NT * 16;
-    static constexpr int XCH = 2 * 16 * 80;                  // bytes of an epilogue warp: two chunks
-    static constexpr int O_RING = (O_XCH + 8 * XCH + 1023) / 1024 * 1024;
+    static constexpr int O_XCH = O_ROWS + 2 * NT * 12;
+    static constexpr int O_RED = O_XCH + 8 * XCH;
+    static constexpr int O_RING = (O_RED + RED + 1023) / 1024 * 1024;
     static constexpr int S = (227 * 1024 - 1024 - O_RING) / STAGE / 2 * 2;  // (even: see the loaders)
     static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
-    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 5) * 8 + 16 + 80 <= 1024 && S >= 3, "");
+    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 6) * 8 + 16 + 80 <= 1024 && S >= 6, "");
 };
 
-struct alignas(16) GroupedRow {
-    uint8_t *y;  // the output row (NULL: none)
-    float scale;
-    int pad;
-};
 struct GroupedItem {
     int g, m, row0, n, npad;  // group, M tile, first row (GP_GRAD: first output row), rows, rows rounded up
     int r0, cnt, steps;       // GP_GRAD: the group's first row and rows; stages of the reduction
 };
 
-// Two results to the two 16-bit halves of a word and back.
-__device__ __forceinline__ uint32_t grouped_pack(float lo, float hi, bool bf) {
-    if (bf) {
+// Two results to the two halves of a word and back.
+template <int OT>
+__device__ __forceinline__ uint32_t grouped_pack(float lo, float hi) {
+    if (OT == MOE_BF16) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         return *(const uint32_t *)&v;
     }
     const __half2 v = __floats2half2_rn(lo, hi);
     return *(const uint32_t *)&v;
 }
-__device__ __forceinline__ float2 grouped_unpack(uint32_t w, bool bf) {
-    if (bf) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+template <int OT>
+__device__ __forceinline__ float2 grouped_unpack(uint32_t w) {
+    if (OT == MOE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     return __half22float2(*(const __half2 *)&w);
+}
+// Four results to consecutive elements of a row.
+template <int OT>
+__device__ __forceinline__ void grouped_store4(uint8_t *row, int i, float4 a) {
+    if (OT == MOE_F32) *(float4 *)(row + 4 * (size_t)i) = a;
+    else *(uint2 *)(row + 2 * (size_t)i) = make_uint2(grouped_pack<OT>(a.x, a.y), grouped_pack<OT>(a.z, a.w));
+}
+
+// A word to shared memory of the cluster, counted by a barrier there.
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr), "f"(v), "r"(bar)
+                 : "memory");
 }
 
 // 16 bytes global -> shared (bytes = 16), or zeros (0).
@@ -125,7 +143,8 @@ __device__ __forceinline__ int grouped_next_adapter(const int (&ids)[8], int las
     return (int)__reduce_min_sync(0xffffffffu, best);
 }
 
-template <int CG, int NT, int MODE>
+// OT: y's type
+template <int CG, int NT, int MODE, int OT>
 __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
     using G_ = GroupedGeom<CG, NT>;
     constexpr int S = G_::S;
@@ -140,16 +159,21 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     uint64_t *acc_full = landed + S;
     uint64_t *acc_empty = acc_full + 2;
     uint64_t *mma_done = acc_empty + 2;
-    uint32_t *tmem_slot = (uint32_t *)(mma_done + 1);
+    uint64_t *red_full = mma_done + 1;
+    uint32_t *tmem_slot = (uint32_t *)(red_full + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     int *sums = (int *)(tmem_slot + 4);                       // [20]
     int *off = (int *)(smem + G_::O_OFF);                     // [G + 1]
     int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before a group's
-    GroupedRow *e_rows = (GroupedRow *)(smem + G_::O_ROWS);   // [2][NT]
+    uint8_t **e_y = (uint8_t **)(smem + G_::O_ROWS);          // [2][NT] the output rows of an accumulator's columns (NULL: none)
+    float *e_s = (float *)(e_y + 2 * NT);                     // [2][NT] and their scale
+    int4 *items = (int4 *)(smem + G_::O_ITEMS);
     uint8_t *ring = smem + G_::O_RING;
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
+    // CG = 1: the CTAs of a cluster share their item's reduction
+    const int ks = CG == 1 ? (int)cluster_nctarank() : 1, kr = CG == 1 ? (int)cluster_ctarank() : 0;
     const bool loaders = GRAD || MODE == GP_LORA || p.x_index;
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
@@ -162,13 +186,14 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             mbar_init(&acc_empty[b], 8 * CG);
         }
         mbar_init(mma_done, 1);
+        mbar_init(red_full, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 2) tmem_alloc_group<CG>(tmem_slot, G_::TCOLS);
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();
+    if (CG == 2 || ks > 1) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     // (GP_LORA: the kernel in front computes u and nothing else; it starts this one when everything before it is
@@ -215,27 +240,37 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         if (tid == GP_THREADS - 1) first[p.G] = before + t;
     }
     __syncthreads();
-    const int n_items = first[p.G], stride = (int)gridDim.x / CG, item0 = (int)blockIdx.x / CG;
-    auto item_at = [&](int j) -> GroupedItem {
-        GroupedItem it;
+    // this CTA's items: unit, unit + units, ..
+    const int n_items = first[p.G], units = (int)gridDim.x / (CG * ks), unit = (int)blockIdx.x / (CG * ks);
+    const int n_mine = unit < n_items ? (n_items - unit - 1) / units + 1 : 0;
+    auto look_up_item = [&](int i) -> int4 {  // group and M tile, first row, rows, the group's rows
+        const int j = unit + i * units;
         int lo = 0, hi = p.G;  // the last group whose first item is not after j
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (first[mid] <= j) lo = mid;
             else hi = mid;
         }
-        it.g = lo;
-        const int r = j - first[lo], t = r / mt;
-        it.m = r - t * mt;
-        it.r0 = off[lo];
-        it.cnt = rows_of(lo);
+        const int r = j - first[lo], t = r / mt, cnt = rows_of(lo);
         // near-equal tiles: none is empty, as size <= NT
-        const int all = GRAD ? p.N : it.cnt, nt = (all + NT - 1) / NT;
+        const int all = GRAD ? p.N : cnt, nt = (all + NT - 1) / NT;
         const int size = ((all + nt - 1) / nt + gran - 1) / gran * gran;
-        it.n = min(size, all - t * size);
-        it.npad = (it.n + gran - 1) / gran * gran;
-        it.row0 = (GRAD ? 0 : it.r0) + t * size;
-        it.steps = ((GRAD ? it.cnt : p.K) + 63) / 64;
+        return make_int4(lo | (r - t * mt) << 10, (GRAD ? 0 : off[lo]) + t * size, min(size, all - t * size), cnt);
+    };
+    static_assert(MOE_MAX_GROUPS <= 1024, "ten bits of a group");
+    for (int i = tid; i < min(n_mine, GP_ITEMS); i += GP_THREADS) items[i] = look_up_item(i);
+    __syncthreads();
+    auto item_at = [&](int i) -> GroupedItem {
+        const int4 v = i < GP_ITEMS ? items[i] : look_up_item(i);
+        GroupedItem it;
+        it.g = v.x & 1023;
+        it.m = v.x >> 10;
+        it.row0 = v.y;
+        it.n = v.z;
+        it.npad = (v.z + gran - 1) / gran * gran;
+        it.r0 = GRAD ? off[it.g] : 0;
+        it.cnt = v.w;
+        it.steps = ((GRAD ? v.w : p.K) + 63) / 64;
         return it;
     };
     // GP_LORA: this lane's share of the tile's adapters (-1: none)
@@ -248,7 +283,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             ids[i] = a < p.n_adapters ? a : -1;
         }
     };
-    const int chunks = MODE == GP_LORA ? (p.rank + 31) / 32 : 0;
+    const int chunks = MODE == GP_LORA ? (p.rank + 31) / 32 : 1;
     auto extra_stages = [&](const GroupedItem &it) -> int {
         int n = 0;
         if (MODE == GP_LORA) {
@@ -257,6 +292,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a)) n += chunks;
         }
         return n;
+    };
+    // the stages [lo, hi) of an item that are this CTA's, its `extra` last ones those of GP_LORA
+    auto stage_range = [&](const GroupedItem &it, int extra, int &lo, int &hi) {
+        const int all = it.steps + extra;
+        lo = CG == 1 ? all * kr / ks : 0;
+        hi = CG == 1 ? all * (kr + 1) / ks : all;
     };
     auto source = [&](int i) -> int {  // x's row of position i, -1: none
         if (!p.x_index) return i < p.x_rows ? i : -1;
@@ -272,10 +313,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         int gs = 0, st = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (int j = item0; j < n_items && ok; j += stride) {
+        for (int j = 0; j < n_mine && ok; ++j) {
             const GroupedItem it = item_at(j);
             const int nb = it.npad / CG, m0 = (it.m * CG + rank) * MROWS;
-            for (int kb = 0; kb < it.steps; ++kb, ++gs) {
+            int lo, hi;
+            stage_range(it, extra_stages(it), lo, hi);
+            for (int kb = lo; kb < min(hi, it.steps); ++kb, ++gs) {
                 if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
                 uint8_t *dst = ring + (size_t)st * G_::STAGE;
                 const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
@@ -301,14 +344,17 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             if (MODE == GP_LORA && ok) {
                 int ids[8];
                 tile_adapters(it, ids);
+                int e = it.steps;
                 for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a))
-                    for (int c = 0; c < chunks; ++c, ++gs) {
+                    for (int c = 0; c < chunks; ++c, ++e) {
+                        if (e < lo || e >= hi) continue;
                         if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
                         uint8_t *dst = ring + (size_t)st * G_::STAGE;
                         const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
                         if (rank == 0) mbar_arrive_expect_tx_elect(&full[st], CG * GP_UBYTES);
                         if (lane == 0) tma_tile_3d<CG>(dst, &p.ab, c * 32, m0, a, bar);
                         __syncwarp();
+                        ++gs;
                         if (++st == S) {
                             st = 0;
                             ph ^= 1u;
@@ -328,11 +374,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         int gs = 0, st = 0;
         uint32_t ph = 1;
         bool ok = true;
-        for (int j = item0; j < n_items && ok; j += stride) {
+        for (int j = 0; j < n_mine && ok; ++j) {
             const GroupedItem it = item_at(j);
             const int nb = it.npad / CG, c0 = it.row0 + rank * nb;
-            const int extra = extra_stages(it);
-            for (int kb = 0; kb < it.steps + extra; ++kb, ++gs) {
+            int lo, hi;
+            stage_range(it, extra_stages(it), lo, hi);
+            for (int kb = lo; kb < hi; ++kb, ++gs) {
                 if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
                 uint8_t *dst = ring + (size_t)st * G_::STAGE + GP_ABYTES;
                 const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
@@ -385,18 +432,20 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             }
         };
         GroupedItem it = {}, after = {};
-        if (GRAD && item0 < n_items) {
-            after = item_at(item0);
+        if (GRAD && n_mine) {
+            after = item_at(0);
             look_up(after, team);
         }
-        for (int j = item0; j < n_items && ok; j += stride) {
+        for (int j = 0; j < n_mine && ok; ++j) {
             if (GRAD) {
                 it = after;
-                if (j + stride < n_items) after = item_at(j + stride);
+                if (j + 1 < n_mine) after = item_at(j + 1);
             } else {
                 it = item_at(j);
             }
             const int nb = it.npad / CG;
+            int lo, hi;
+            stage_range(it, extra_stages(it), lo, hi);
             if (!GRAD) {
                 // eight threads a row: piece lt % 8 of rows lt / 8 + 16 i
                 constexpr int RI = NT / CG / 16;
@@ -409,9 +458,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     const int c = r0 + 16 * i;
                     const int r = c >= rows ? -1 : MODE == GP_LORA ? it.row0 + rank * nb + c : source(it.row0 + rank * nb + c);
                     who[i] = MODE != GP_LORA ? (r >= 0 ? 16 : 0) : r >= 0 ? p.adapter[r] : -1;
-                    src[i] = p.rows + (size_t)max(r, 0) * p.ld + 8 * piece + (team == (gs & 1) ? 0 : 64);
+                    src[i] = p.rows + (size_t)max(r, 0) * p.ld + 8 * piece + 64 * (lo + (team != (gs & 1)));
                 }
-                for (int kb = 0; kb < it.steps; ++kb, next()) {
+                for (int kb = lo; kb < min(hi, it.steps); ++kb, next()) {
                     if ((gs & 1) != team) continue;
                     if (!begin()) break;
                     if (MODE != GP_LORA) {
@@ -420,19 +469,24 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
 #pragma unroll
                         for (int i = 0; i < RI; ++i) {
                             if (16 * i < rows) cp_async_16_or_0(d + i * 2048, src[i], min(most, who[i]));
-                            src[i] += kb + 3 > it.steps ? 0 : 128;
+                            src[i] += kb + 3 > hi ? 0 : 128;
                         }
                     }
                     cp_async_mbar_arrive_noinc(&landed[st]);
                 }
                 if (MODE == GP_LORA && ok) {
-                    if (j == item0) pdl_wait();  // u
+                    if (j == 0) pdl_wait();  // u
                     int ids[8];
                     tile_adapters(it, ids);
                     const uint16_t *u = p.rows + (size_t)(it.row0 + rank * nb + r0) * p.ld + 8 * piece;
+                    int e = it.steps;
                     for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a))
-                        for (int c = 0; c < chunks; ++c, next()) {
-                            if ((gs & 1) != team) continue;
+                        for (int c = 0; c < chunks; ++c, ++e) {
+                            if (e < lo || e >= hi) continue;
+                            if ((gs & 1) != team) {
+                                next();
+                                continue;
+                            }
                             if (!begin()) break;
                             const uint32_t d = at + (uint32_t)st * G_::STAGE;
 #pragma unroll
@@ -443,12 +497,13 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                                                      some ? 16 : 0);
                                 }
                             cp_async_mbar_arrive_noinc(&landed[st]);
+                            next();
                         }
                 }
             } else {
                 // sixteen threads a row (128 columns): piece lt % 16 of rows lt / 16 + 8 i
                 const int end = gs + it.steps;  // the next item's first stage
-                const bool more = j + stride < n_items, any = it.steps > ((gs & 1) != team);
+                const bool more = j + 1 < n_mine, any = it.steps > ((gs & 1) != team);
                 if (!any && more) look_up(after, (end & 1) != team);
                 const int piece = lt & 15, r0 = lt >> 4;
                 const int ca = (it.m * CG + rank) * 128 + 8 * piece, cb = rank * nb + 8 * piece;
@@ -486,10 +541,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int j = item0; j < n_items && ok; j += stride) {
+        for (int j = 0; j < n_mine && ok; ++j) {
             const GroupedItem it = item_at(j);
-            const int n = it.steps + extra_stages(it);
-            for (int kb = 0; kb < n; ++kb) {
+            int lo, hi;
+            stage_range(it, extra_stages(it), lo, hi);
+            for (int kb = lo; kb < hi; ++kb) {
                 if (!(ok = mbar_wait_warp(&landed[st], ph, p.status, abort_flag))) break;
                 fence_proxy_async_smem();
                 if (lane == 0) {
@@ -504,21 +560,24 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         }
     } else if (warp == 2 && rank == 0) {
         // ---------------- MMA issuer
-        int jl = 0, st = 0;
+        int st = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int j = item0; j < n_items && ok; j += stride, ++jl) {
+        for (int j = 0; j < n_mine && ok; ++j) {
             const GroupedItem it = item_at(j);
             // (a value that a shuffle hands out is known to be the same in every lane: it stays in a uniform register, where
             // the MMA wants its operands)
             const uint32_t idesc = umma_idesc_16(p.fmt, A_MN, B_MN, 128 * CG, __shfl_sync(0xffffffffu, it.npad, 0));
-            const int buf = jl & 1;
-            const int extra = extra_stages(it);
-            if (jl >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((jl / 2) - 1) & 1, p.status, abort_flag))) break;
+            const int buf = j & 1;
+            int lo, hi;
+            stage_range(it, extra_stages(it), lo, hi);
+            lo = __shfl_sync(0xffffffffu, lo, 0);
+            hi = __shfl_sync(0xffffffffu, hi, 0);
+            if (j >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((j / 2) - 1) & 1, p.status, abort_flag))) break;
             tc_fence_after();
             const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + buf * NT;
             const int len = GRAD ? __shfl_sync(0xffffffffu, it.cnt, 0) : p.K, n_steps = __shfl_sync(0xffffffffu, it.steps, 0);
-            for (int kb = 0; kb < n_steps; ++kb) {
+            for (int kb = lo; kb < min(hi, n_steps); ++kb) {
                 if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
                 tc_fence_after();
                 const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
@@ -527,7 +586,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 const int left = len - 64 * kb;
                 auto step = [&](int q) {
                     umma_f16_elect<CG>(d, a + (uint64_t)(q * (A_MN ? 128 : 2)), b + (uint64_t)(q * (B_MN ? 128 : 2)), idesc,
-                                       q > 0 || kb > 0);
+                                       q > 0 || kb > lo);
                 };
                 step(0);
                 if (left > 48) {  // (no branch between the MMAs)
@@ -544,21 +603,19 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     ph ^= 1u;
                 }
             }
-            for (int e = 0, c = 0; e < extra && ok; ++e) {
+            for (int e = max(lo, n_steps); MODE == GP_LORA && e < hi && ok; ++e) {
                 if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
                 tc_fence_after();
                 // 32 ranks: u's upper halves in the first 64 bytes of a row, the rest of u in the second, both by the same B_a
                 const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
                 const uint64_t a = umma_desc_sw64(sa), b = umma_desc_sw128(sa + GP_ABYTES);
-                const bool two = p.rank - 32 * c > 16;
-                umma_f16_elect<CG>(d, a, b, idesc, 1);
+                umma_f16_elect<CG>(d, a, b, idesc, e > lo);
                 umma_f16_elect<CG>(d, a, b + 4, idesc, 1);
-                if (two) {
+                if (p.rank - 32 * ((e - n_steps) % chunks) > 16) {
                     umma_f16_elect<CG>(d, a + 2, b + 2, idesc, 1);
                     umma_f16_elect<CG>(d, a + 2, b + 6, idesc, 1);
                 }
                 umma_commit_group_elect<CG>(&empty[st]);
-                if (++c == chunks) c = 0;
                 if (++st == S) {
                     st = 0;
                     ph ^= 1u;
@@ -574,156 +631,221 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         // consecutive elements of an output row; fp32 results transposed a word at a time, four consecutive elements a store.
         // (Stored straight from the registers, 128 bytes of one output row an instruction: 4864 x 4096 x 512 31.4 us,
         // this way 24.8.)
+        constexpr bool F32 = OT == MOE_F32;
+        constexpr int CH = G_::CH, NB = CH / 8, SIZE = F32 ? 4 : 2;
         const int q = warp & 3, ew = warp - 4, half = ew >> 2, et = ew * 32 + lane;
-        const bool bf = p.ytype == MOE_BF16, f32 = p.ytype == MOE_F32;
         const uint32_t xb = smem_u32(smem + G_::O_XCH) + ew * G_::XCH;
-        const int size = f32 ? 4 : 2;
         // stmatrix: the address of row lane % 8 of 8 x 8 matrix lane / 8.  Matrices 0, 1: output rows 0-7, elements 0-7 and 8-15;
         // 2, 3: output rows 8-15
         constexpr int PITCH = MODE == GP_SWIGLU ? 48 : 80;  // (no bank conflicts)
         const uint32_t xm = xb + ((lane & 7) + 8 * (lane >> 4)) * PITCH + ((lane >> 3) & 1) * 16;
-        int jl = 0;
-        for (int j = item0; j < n_items; j += stride, ++jl) {
-            const GroupedItem it = item_at(j);
-            const int buf = jl & 1;
-            if (et < NT && et < it.n) {
-                GroupedRow r;
-                r.y = nullptr;
-                r.scale = 1.f;
-                if (GRAD) {
-                    r.y = (uint8_t *)p.y + ((size_t)it.g * p.N + it.row0 + et) * p.M * size;
-                } else {
-                    const int dst = source(it.row0 + et) < 0 ? -1 : target(it.row0 + et);
-                    if (dst < 0) {
-                        moe_set_status(p.status, MOE_ERR_INVALID);
-                    } else {
-                        r.y = (uint8_t *)p.y + (size_t)dst * p.ldy * size;
-                        if (p.scale) r.scale = p.scale[dst];
-                    }
-                }
-                e_rows[buf * NT + et] = r;
+        // this thread's row of an item, read an item ahead: its indexes, then (once they are there) its output row and scale
+        int ix = 0, iy = 0;
+        uint8_t *row = nullptr;
+        float scale = 1.f;
+        auto fetch = [&](const GroupedItem &it) {
+            if (GRAD || et >= it.n) return;
+            ix = p.x_index ? p.x_index[it.row0 + et] : it.row0 + et;
+            iy = p.y_index ? p.y_index[it.row0 + et] : it.row0 + et;
+        };
+        auto resolve = [&](const GroupedItem &it) {
+            row = nullptr;
+            scale = 1.f;
+            if (et >= it.n) return;
+            if (GRAD) {
+                row = (uint8_t *)p.y + ((size_t)it.g * p.N + it.row0 + et) * p.M * SIZE;
+            } else if (ix >= 0 && ix / (p.x_index ? p.x_share : 1) < p.x_rows && iy >= 0 && iy < p.y_rows) {
+                row = (uint8_t *)p.y + (size_t)iy * p.ldy * SIZE;
+                if (p.scale) scale = p.scale[iy];
+            } else {
+                moe_set_status(p.status, MOE_ERR_INVALID);
             }
-            const bool w = mbar_wait_role(&acc_full[buf], (jl / 2) & 1, p.status, abort_flag);
+        };
+        GroupedItem it = {};
+        if (n_mine) {
+            it = item_at(0);
+            fetch(it);
+            resolve(it);
+        }
+        for (int j = 0; j < n_mine; ++j) {
+            const int buf = j & 1;
+            if (et < NT) {
+                e_y[buf * NT + et] = row;
+                e_s[buf * NT + et] = scale;
+            }
+            GroupedItem nx = {};
+            if (j + 1 < n_mine) {
+                nx = item_at(j + 1);
+                fetch(nx);
+            }
+            const bool w = mbar_wait_role(&acc_full[buf], (j / 2) & 1, p.status, abort_flag);
             if (!bar_and_n(1, 256, w)) break;
+            if (j + 1 < n_mine) resolve(nx);
             tc_fence_after();
             const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * NT;
-            const GroupedRow *rows = e_rows + buf * NT;
+            uint8_t *const *ys = e_y + buf * NT;
+            const float *ss = e_s + buf * NT;
             const bool none = GRAD && !it.steps;
             const int m0 = (it.m * CG + rank) * MROWS + MROWS / 4 * q;  // the warp's first element
-            // 16 columns: 32x32b, or in fragments the first 16 lanes' registers, then the others'
-            auto load = [&](uint32_t (&v)[16], int c0) {
-                if (MODE != GP_SWIGLU && f32) {
+            if (CG == 1 && ks > 1) {
+                // the item's only CTA but for the others of the cluster: each adds up the rows c with c % ks = its rank
+                // (and has one item: nothing is left in the buffers by an earlier one)
+                const uint32_t bar = smem_u32(red_full), red = smem_u32(smem + G_::O_RED);
+                const int per = (NT + ks - 1) / ks, own = it.n > kr ? (it.n - kr - 1) / ks + 1 : 0;
+                if (et == 0 && own) mbar_arrive_expect_tx(red_full, (uint32_t)(own * ks) * 512u);
+                int lo, hi;
+                stage_range(it, extra_stages(it), lo, hi);
+                for (int c0 = 16 * half; c0 < it.n; c0 += 32) {
+                    uint32_t v[16];
                     tmem_ld16(tb + c0, v);
-                } else {
-                    tmem_ld_16x256b_x2(tb + c0, reinterpret_cast<uint32_t(&)[8]>(v[0]));
-                    tmem_ld_16x256b_x2(tb + (16u << 16) + c0, reinterpret_cast<uint32_t(&)[8]>(v[8]));
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const int c = c0 + k;
+                        if (c < it.n) {
+                            uint32_t to, tobar;
+                            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(red), "r"(c % ks));
+                            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(tobar) : "r"(bar), "r"(c % ks));
+                            st_async_f32(to + ((kr * per + c / ks) * 128 + 32 * q + lane) * 4, lo < hi ? __uint_as_float(v[k]) : 0.f,
+                                         tobar);
+                        }
+                    }
                 }
-            };
-            auto process = [&](uint32_t (&v)[16], int c0, int odd) {
-                if (none)
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = 0u;
-                if (MODE != GP_SWIGLU && f32) {
-                    float *x = (float *)(smem + G_::O_XCH + ew * G_::XCH);  // padded to 36: no bank conflicts
-                    const int m = m0 + 4 * (lane & 7);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) x[36 * k + lane] = __uint_as_float(v[k]);
-                    __syncwarp();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = 4 * k + (lane >> 3);
-                        float4 a = *(const float4 *)(x + 36 * c + 4 * (lane & 7));
-                        if (c0 + c < it.n && m < p.M) {
-                            const GroupedRow r = rows[c0 + c];
-                            float4 *o = (float4 *)((float *)r.y + m);
-                            if (!GRAD) a = make_float4(r.scale * a.x, r.scale * a.y, r.scale * a.z, r.scale * a.w);
-                            if (GRAD && p.accumulate) {
-                                const float4 b = *o;
-                                a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-                            }
-                            if (GRAD || r.y) *o = a;
+                if (own) {
+                    const bool there = mbar_wait_role(red_full, 0, p.status, abort_flag);
+                    if (!bar_and_n(1, 256, there)) break;
+                    const float *sum = (const float *)(smem + G_::O_RED);
+                    auto total = [&](int r, int m) -> float4 {  // in the order of the CTAs
+                        float4 a = *(const float4 *)(sum + r * 128 + m);
+                        for (int k = 1; k < ks; ++k) {
+                            const float4 b = *(const float4 *)(sum + (k * per + r) * 128 + m);
+                            a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
                         }
+                        return a;
+                    };
+                    constexpr int QUADS = MROWS / 4;
+                    for (int i = et; i < own * QUADS; i += 256) {
+                        const int r = i / QUADS, c = r * ks + kr, m = 4 * (i % QUADS), mg = it.m * MROWS + m;
+                        float4 a;
+                        if (MODE == GP_SWIGLU) {
+                            const int at = 2 * (m & ~15) + (m & 15);
+                            const float4 g = total(r, at), u = total(r, at + 16);
+                            a = make_float4(mx4_swiglu<F32>(g.x, u.x), mx4_swiglu<F32>(g.y, u.y), mx4_swiglu<F32>(g.z, u.z),
+                                            mx4_swiglu<F32>(g.w, u.w));
+                        } else {
+                            a = total(r, m);
+                        }
+                        const float s = ss[c];
+                        if (mg < p.M && ys[c]) grouped_store4<OT>(ys[c], mg, make_float4(s * a.x, s * a.y, s * a.z, s * a.w));
                     }
-                    __syncwarp();
-                    return;
                 }
-                // registers 4 b + {0, 1}: row lane / 4, columns 8 b + 2 (lane % 4) + {0, 1}; + {2, 3}: row lane / 4 + 8
-                uint32_t(&lo)[8] = reinterpret_cast<uint32_t(&)[8]>(v[0]);
-                uint32_t(&hi)[8] = reinterpret_cast<uint32_t(&)[8]>(v[8]);
-                const int cq = c0 + 2 * (lane & 3);
-                const uint32_t to = xm + odd * (G_::XCH / 2), from = xb + odd * (G_::XCH / 2);
-                if (MODE == GP_SWIGLU) {
-                    float h[8];
+            } else {
+                for (int c0 = CH * half; c0 < it.n; c0 += 2 * CH) {
+                    if (F32 && MODE != GP_SWIGLU) {
+                        uint32_t v[CH / 16][16];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) h[k] = mx4_swiglu<true>(__uint_as_float(lo[k]), __uint_as_float(hi[k]));
-                    if (p.scale || f32) {
-                        // (e_rows past the last row may hold anything: not stored)
+                        for (int h = 0; h < CH / 16; ++h) tmem_ld16(tb + c0 + 16 * h, v[h]);
+                        tmem_ld_wait();
+                        float *x = (float *)(smem + G_::O_XCH + ew * G_::XCH);  // padded to 36: no bank conflicts
+                        const int m = m0 + 4 * (lane & 7);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int c = cq + 8 * (k >> 2) + (k & 1), m = m0 + (lane >> 2) + 4 * (k & 2);
-                            if (c < it.n) {
-                                const GroupedRow r = rows[c];
-                                h[k] *= r.scale;
-                                if (f32 && r.y && m < p.M) ((float *)r.y)[m] = h[k];
+                        for (int h = 0; h < CH / 16; ++h) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) x[36 * k + lane] = none ? 0.f : __uint_as_float(v[h][k]);
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int r = 4 * k + (lane >> 3), c = c0 + 16 * h + r;
+                                float4 a = *(const float4 *)(x + 36 * r + 4 * (lane & 7));
+                                if (c < it.n && m < p.M && ys[c]) {
+                                    const float s = ss[c];
+                                    a = make_float4(s * a.x, s * a.y, s * a.z, s * a.w);
+                                    if (GRAD && p.accumulate) {
+                                        const float4 b = *(const float4 *)(ys[c] + 4 * (size_t)m);
+                                        a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+                                    }
+                                    grouped_store4<OT>(ys[c], m, a);
+                                }
                             }
+                            __syncwarp();
                         }
-                        if (f32) return;
+                        continue;
                     }
-                    stmatrix_x4_trans(to, grouped_pack(h[0], h[1], bf), grouped_pack(h[2], h[3], bf),
-                                      grouped_pack(h[4], h[5], bf), grouped_pack(h[6], h[7], bf));
-                    __syncwarp();
-                    const int c = lane >> 1, m = m0 + 8 * (lane & 1);
-                    const uint4 a = ld_shared_16(from + c * PITCH + 16 * (lane & 1));
-                    if (c0 + c < it.n && m < p.M && rows[c0 + c].y) *(uint4 *)(rows[c0 + c].y + 2 * m) = a;
-                } else {
-                    uint32_t old[8] = {};
-                    if (GRAD && p.accumulate) {
+                    // registers 4 b + {0, 1}: row lane / 4, columns 8 b + 2 (lane % 4) + {0, 1}; + {2, 3}: row lane / 4 + 8
+                    uint32_t lo[4 * NB], hi[4 * NB];  // (GP_SWIGLU: gate and up)
+                    tmem_ld_16x256b(tb + c0, lo);
+                    tmem_ld_16x256b(tb + (16u << 16) + c0, hi);
+                    tmem_ld_wait();
+                    const int cq = c0 + 2 * (lane & 3);
+                    if (none)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int c = 8 * k + (lane >> 2), m = m0 + 8 * (lane & 3);
-                            if (c0 + c < it.n && m < p.M)
-                                st_shared_16(from + c * PITCH + 16 * (lane & 3), *(const uint4 *)(rows[c0 + c].y + 2 * m));
-                        }
-                        __syncwarp();
-                        ldmatrix_x4_trans(to, old[0], old[1], old[2], old[3]);
-                        ldmatrix_x4_trans(to + 32, old[4], old[5], old[6], old[7]);
-                        __syncwarp();
-                    }
-                    float s[4] = {1.f, 1.f, 1.f, 1.f};
+                        for (int k = 0; k < 4 * NB; ++k) lo[k] = hi[k] = 0u;
+                    if (MODE == GP_SWIGLU)
+#pragma unroll
+                        for (int k = 0; k < 4 * NB; ++k)
+                            lo[k] = __float_as_uint(mx4_swiglu<F32>(__uint_as_float(lo[k]), __uint_as_float(hi[k])));
                     if (!GRAD && p.scale)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (cq + 8 * (k >> 1) + (k & 1) < it.n) s[k] = rows[cq + 8 * (k >> 1) + (k & 1)].scale;
-                    auto pack = [&](const uint32_t (&v)[8], int k, uint32_t before) -> uint32_t {
-                        float2 o = make_float2(0.f, 0.f);
-                        if (GRAD && p.accumulate) o = grouped_unpack(before, bf);
-                        return grouped_pack(fmaf(s[k >> 2 << 1], __uint_as_float(v[k]), o.x),
-                                            fmaf(s[(k >> 2 << 1) + 1], __uint_as_float(v[k + 1]), o.y), bf);
+                        for (int k = 0; k < 2 * NB; ++k) {  // (rows past the last one are not stored)
+                            const int c = cq + 8 * (k >> 1) + (k & 1), r = 4 * (k >> 1) + (k & 1);
+                            const float s = c < it.n ? ss[c] : 0.f;
+#pragma unroll
+                            for (int h = 0; h < 4; h += 2) {
+                                lo[r + h] = __float_as_uint(s * __uint_as_float(lo[r + h]));
+                                if (MODE != GP_SWIGLU) hi[r + h] = __float_as_uint(s * __uint_as_float(hi[r + h]));
+                            }
+                        }
+                    if (F32) {  // GP_SWIGLU: 32 bytes of four output rows an instruction
+#pragma unroll
+                        for (int k = 0; k < 4 * NB; ++k) {
+                            const int c = cq + 8 * (k >> 2) + (k & 1), m = m0 + (lane >> 2) + 4 * (k & 2);
+                            if (c < it.n && m < p.M && ys[c]) ((float *)ys[c])[m] = __uint_as_float(lo[k]);
+                        }
+                        continue;
+                    }
+                    constexpr int PARTS = MODE == GP_SWIGLU ? 2 : 4, LINES = 32 / PARTS;  // 16-byte pieces of an output row
+                    const int part = lane % PARTS, m = m0 + 8 * part;
+                    if (GRAD && p.accumulate) {
+#pragma unroll
+                        for (int k = 0; k < CH / LINES; ++k) {
+                            const int c = LINES * k + lane / PARTS;
+                            if (c0 + c < it.n && m < p.M)
+                                st_shared_16(xb + c * PITCH + 16 * part, *(const uint4 *)(ys[c0 + c] + 2 * (size_t)m));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int b = 0; b < NB / 2; ++b)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t old[4];
+                                ldmatrix_x4_trans(xm + 16 * b * PITCH + 32 * h, old[0], old[1], old[2], old[3]);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    uint32_t *v = (h ? hi : lo) + 8 * b + 2 * k;
+                                    const float2 o = grouped_unpack<OT>(old[k]);
+                                    v[0] = __float_as_uint(__uint_as_float(v[0]) + o.x);
+                                    v[1] = __float_as_uint(__uint_as_float(v[1]) + o.y);
+                                }
+                            }
+                        __syncwarp();
+                    }
+                    auto pack = [&](const uint32_t *v) -> uint32_t {
+                        return grouped_pack<OT>(__uint_as_float(v[0]), __uint_as_float(v[1]));
                     };
-                    stmatrix_x4_trans(to, pack(lo, 0, old[0]), pack(lo, 2, old[1]), pack(lo, 4, old[2]), pack(lo, 6, old[3]));
-                    stmatrix_x4_trans(to + 32, pack(hi, 0, old[4]), pack(hi, 2, old[5]), pack(hi, 4, old[6]), pack(hi, 6, old[7]));
+#pragma unroll
+                    for (int b = 0; b < NB / 2; ++b) {
+                        const uint32_t *l = lo + 8 * b, *h = hi + 8 * b;
+                        stmatrix_x4_trans(xm + 16 * b * PITCH, pack(l), pack(l + 2), pack(l + 4), pack(l + 6));
+                        if (MODE != GP_SWIGLU) stmatrix_x4_trans(xm + 16 * b * PITCH + 32, pack(h), pack(h + 2), pack(h + 4), pack(h + 6));
+                    }
                     __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int c = 8 * k + (lane >> 2), m = m0 + 8 * (lane & 3);
-                        const uint4 a = ld_shared_16(from + c * PITCH + 16 * (lane & 3));
-                        if (c0 + c < it.n && m < p.M && rows[c0 + c].y) *(uint4 *)(rows[c0 + c].y + 2 * m) = a;
+                    for (int k = 0; k < CH / LINES; ++k) {
+                        const int c = LINES * k + lane / PARTS;
+                        const uint4 a = ld_shared_16(xb + c * PITCH + 16 * part);
+                        if (c0 + c < it.n && m < p.M && ys[c0 + c]) *(uint4 *)(ys[c0 + c] + 2 * (size_t)m) = a;
                     }
-                }
-            };
-            // a chunk of 16 columns is read from tensor memory while the one before it is worked on (two buffers each: a
-            // warp barrier lies between two uses of one)
-            uint32_t v0[16], v1[16];
-            int c0 = 16 * half;
-            if (c0 < it.n) load(v0, c0);
-            for (; c0 < it.n; c0 += 64) {
-                tmem_ld_wait();
-                if (c0 + 32 < it.n) load(v1, c0 + 32);
-                process(v0, c0, 0);
-                if (c0 + 32 < it.n) {
-                    tmem_ld_wait();
-                    if (c0 + 64 < it.n) load(v0, c0 + 64);
-                    process(v1, c0 + 32, 1);
+                    __syncwarp();
                 }
             }
             tc_fence_before();
@@ -732,11 +854,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 if (CG == 1) mbar_arrive1(&acc_empty[buf]);
                 else mbar_arrive_cluster(cluster_map(&acc_empty[buf], 0));
             }
+            it = nx;
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();
+    if (CG == 2 || ks > 1) cluster_sync_all();
     if (warp == 2) {
         __syncwarp();
         tc_fence_after();
@@ -746,8 +869,17 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
 
 // ------------------------------------------------------------------ host
 
-// Launches the kernel on the current device with one CTA (or pair) an SM (or two), at most `items` of them.
-int grouped_launch(const GroupedParams &p, int mode, bool wide, long long items, cudaStream_t s);
+// Launches the kernel on the current device: one CTA (or pair) an SM (or two), at most as many as `items`; where there are few
+// of them (not wide), clusters share one item's reduction of `stages` stages.  One translation unit for each y type.
+int grouped_launch_f32(const GroupedParams &p, int mode, bool wide, long long items, int stages, cudaStream_t s);
+int grouped_launch_bf16(const GroupedParams &p, int mode, bool wide, long long items, int stages, cudaStream_t s);
+int grouped_launch_f16(const GroupedParams &p, int mode, bool wide, long long items, int stages, cudaStream_t s);
+static inline int grouped_launch(const GroupedParams &p, int ytype, int mode, bool wide, long long items, int stages,
+                                 cudaStream_t s) {
+    return ytype == MOE_F32    ? grouped_launch_f32(p, mode, wide, items, stages, s)
+           : ytype == MOE_BF16 ? grouped_launch_bf16(p, mode, wide, items, stages, s)
+                               : grouped_launch_f16(p, mode, wide, items, stages, s);
+}
 // Tensor map of 16-bit elements: `rank` dimensions and box extents innermost first, strides in bytes from the second on.
 int grouped_map(CUtensorMap *map, int type, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
                 const uint32_t *box, int swizzle_bytes);

@@ -1,0 +1,63 @@
+// Launches of the kernel in moe_grouped.cuh, for the translation units of its three y types.
+#pragma once
+
+#include <algorithm>
+#include <mutex>
+
+#include "moe_grouped.cuh"
+
+template <int CG, int NT, int MODE, int OT>
+static int grouped_launch_t(const GroupedParams &p, long long items, int stages, cudaStream_t s) {
+    using G = GroupedGeom<CG, NT>;
+    static std::mutex mu;
+    static int sms[64] = {0};
+    int dev = -1;
+    MOE_TRY_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    int n = 0;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!sms[dev]) {
+            int count = 0;
+            MOE_TRY_CUDA(cudaFuncSetAttribute(grouped_kernel<CG, NT, MODE, OT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              (int)G::SMEM));
+            MOE_TRY_CUDA(cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev));
+            sms[dev] = count;
+        }
+        n = sms[dev];
+    }
+    items = std::max(1LL, items);
+    int cluster = CG;
+    // CG = 1: as many CTAs to an item as there are SMs for, each with four stages of the reduction at least
+    if (CG == 1)
+        while (cluster < GP_MAX_SPLIT && items * (cluster + 1) <= n && (cluster + 1) * 4 <= stages) ++cluster;
+    const long long units = std::min<long long>(items, n / cluster);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    moe_pdl_config(&cfg, attr, dim3((unsigned)(units * cluster)), dim3(GP_THREADS), G::SMEM, s);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, grouped_kernel<CG, NT, MODE, OT>, p));
+    return MOE_OK;
+}
+
+template <int OT>
+static int grouped_launch_modes(const GroupedParams &p, int mode, bool wide, long long items, int stages, cudaStream_t s) {
+    switch (mode) {
+        case GP_NK:
+            return wide ? grouped_launch_t<2, 256, GP_NK, OT>(p, items, stages, s)
+                        : grouped_launch_t<1, 32, GP_NK, OT>(p, items, stages, s);
+        case GP_KN:
+            return wide ? grouped_launch_t<2, 256, GP_KN, OT>(p, items, stages, s)
+                        : grouped_launch_t<1, 32, GP_KN, OT>(p, items, stages, s);
+        case GP_SWIGLU:
+            return wide ? grouped_launch_t<2, 256, GP_SWIGLU, OT>(p, items, stages, s)
+                        : grouped_launch_t<1, 32, GP_SWIGLU, OT>(p, items, stages, s);
+        case GP_LORA:
+            return wide ? grouped_launch_t<2, 256, GP_LORA, OT>(p, items, stages, s)
+                        : grouped_launch_t<1, 32, GP_LORA, OT>(p, items, stages, s);
+        default: return grouped_launch_t<2, 256, GP_GRAD, OT>(p, items, stages, s);
+    }
+}

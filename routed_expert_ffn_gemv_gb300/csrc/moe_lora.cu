@@ -6,6 +6,8 @@
 // its tile, 32 ranks at a time, B_a's tile against the tokens' rows of u, zeros for the tokens of other adapters.  So y
 // is rounded once and W's part and the adapters' share an accumulator.  The product starts beside the first kernel and waits
 // for u only where it loads it.
+#include <algorithm>
+
 #include "moe_grouped.cuh"
 
 namespace {
@@ -142,7 +144,6 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     p.x_share = 1;
     p.y = y;
     p.ldy = ldy;
-    p.ytype = ytype;
     p.M = N;
     p.K = K;
     p.adapter = adapter;
@@ -160,5 +161,6 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
                                     K, adapter, n_adapters, aa, rank, scale, (uint16_t *)workspace));
     const bool wide = T > 32;
     const long long tiles = wide ? (T + 255) / 256 : (T + 31) / 32;
-    return grouped_launch(p, GP_LORA, wide, tiles * ((N + 127) / 128), moe_cuda_stream(s));
+    return grouped_launch(p, ytype, GP_LORA, wide, tiles * ((N + 127) / 128), (K + 63) / 64 + std::min(T, n_adapters) * chunks,
+                          moe_cuda_stream(s));
 }

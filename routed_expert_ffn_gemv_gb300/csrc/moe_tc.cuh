@@ -395,13 +395,21 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 TMEM lanes x 16 columns in fragments: registers 4 b + {0, 1} are lane (base + laneid / 4), columns 8 b + 2 (laneid % 4) + {0, 1},
+// 16 TMEM lanes x 16 (or 32) columns in fragments: registers 4 b + {0, 1} are lane (base + laneid / 4), columns 8 b + 2 (laneid % 4) + {0, 1},
 // 4 b + {2, 3} the same eight lanes further.  base: 0 or 16 of the warp's lane quarter.
-__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr)
                  : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 // Four 8 x 8 matrices of 16-bit elements to and from shared memory, transposed: a thread's word of a matrix is its row
 // laneid / 4, columns 2 (laneid % 4) + {0, 1}; a line of shared memory (16 bytes, its address by lane: line lane % 8 of matrix
