@@ -7,12 +7,14 @@
 // is rounded once and W's part and the adapters' share an accumulator.  The product starts beside the first kernel and waits
 // for u only where it loads it.
 #include <algorithm>
+#include <mutex>
 
 #include "moe_grouped.cuh"
 
 namespace {
 
-#define LS_RANKS 4  // ranks of a warp
+#define LS_RANKS 4         // few tokens: ranks of a warp
+#define LS_FEW 64          // tokens
 
 template <bool BF>
 __device__ __forceinline__ float2 pair_value(uint32_t w) {
@@ -32,7 +34,7 @@ __device__ __forceinline__ void split16(float v, uint16_t &hi, uint16_t &lo) {
     }
 }
 
-// A warp: LS_RANKS ranks of one token.  u: [T][chunks][64].
+// Few tokens: a warp for LS_RANKS ranks of one token.  No shared memory: it runs beside the product.  u: [T][chunks][64].
 template <bool BF>
 __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, size_t ldx, int T, int K, const int32_t *adapter,
                                                           int n_adapters, const uint16_t *a, int rank, const float *scale,
@@ -84,9 +86,289 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
     }
 }
 
+#define LS_TOKENS 128      // tokens of a tile: the M side of the MMA
+#define LS_COLS 256        // most ranks of a pass, of one adapter or several: its N side
+#define LS_STAGES 4
+#define LS_STAGE (LS_TOKENS * 128 + LS_COLS * 128)  // 64 columns of x and of A
+#define LS_THREADS 256
+#define LS_HEADER 3072
+#define LS_MAX_SPLIT 8     // CTAs (a cluster) that share a tile's K
+#define LS_SMEM (1024 + LS_HEADER + LS_STAGES * LS_STAGE)
+
+struct ShrinkParams {
+    CUtensorMap x, a;  // x by boxes of 128 rows, A by adapters
+    int T, K, rank, n_adapters, per_pass, fmt;  // per_pass: adapters of a pass
+    const int32_t *adapter;
+    const float *scale;
+    uint16_t *u;       // [T][chunks][64]
+    int *status;
+};
+
+struct ShrinkSmem {
+    uint64_t full[LS_STAGES], empty[LS_STAGES], done;
+    uint32_t tmem;
+    int abort;
+    int count[LS_TOKENS / 32];
+    alignas(16) int ids[LS_TOKENS];  // adapter of each token, -1: none
+    int place[LS_TOKENS];            // of a token that is its adapter's first: the adapter's place among the tile's
+    int list[LS_TOKENS];             // adapter of each place
+    int mine[LS_TOKENS];             // place of each token's adapter in this pass, -1: not in it
+};
+static_assert(sizeof(ShrinkSmem) <= LS_HEADER, "");
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Many tokens.  A cluster: a tile of 128 tokens, one pass over some of its adapters (blockIdx.y); its CTAs share K.
+// D[token][rank] on the tensor cores, x the M side, the rows of the pass's A_a one after another the N side; a token keeps
+// its own adapter's columns.  The CTAs' sums are added up in the order of their ranks, each CTA for its share of the tokens.
+template <bool BF>
+__global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __grid_constant__ ShrinkParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_smem_1024(smem_raw), *ring = smem + LS_HEADER;
+    ShrinkSmem &s = *(ShrinkSmem *)smem;
+    static_assert(LS_TOKENS * (MOE_MAX_RANK + 4) * 4 <= LS_STAGES * LS_STAGE, "sums in the ring's place");
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int ctas = (int)cluster_nctarank(), me = (int)cluster_ctarank();
+    const int t0 = (int)blockIdx.x / ctas * LS_TOKENS, n = min(LS_TOKENS, p.T - t0), chunks = (p.rank + 31) / 32;
+    if (tid == 0) {
+        for (int i = 0; i < LS_STAGES; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        mbar_init(&s.done, 1);
+        s.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc_group<1>(&s.tmem, LS_COLS);
+    pdl_wait();
+    pdl_trigger();
+    // ---------------- the tile's adapters, in the order of their first tokens
+    if (tid < LS_TOKENS) {
+        const int a = tid < n ? p.adapter[t0 + tid] : -1;
+        s.ids[tid] = a >= 0 && a < p.n_adapters ? a : -1;  // (others: recorded by the product)
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int head = -1;  // the first token of this token's adapter
+    if (tid < LS_TOKENS) {
+        const int a = s.ids[tid];
+        if (a >= 0)
+#pragma unroll 8
+            for (int i = LS_TOKENS - 4; i >= 0; i -= 4) {
+                const int4 v = *(const int4 *)&s.ids[i];
+                head = v.w == a ? i + 3 : head;
+                head = v.z == a ? i + 2 : head;
+                head = v.y == a ? i + 1 : head;
+                head = v.x == a ? i : head;
+            }
+        const unsigned heads = __ballot_sync(0xffffffffu, head == tid);
+        if (head == tid) s.place[tid] = __popc(heads & ((1u << lane) - 1u));
+        if (lane == 0) s.count[warp] = __popc(heads);
+    }
+    __syncthreads();
+    int all = 0, base = 0;
+    for (int w = 0; w < LS_TOKENS / 32; ++w) {
+        base += w < warp ? s.count[w] : 0;
+        all += s.count[w];
+    }
+    if (tid < LS_TOKENS && head == tid) {
+        s.place[tid] += base;
+        s.list[s.place[tid]] = s.ids[tid];
+    }
+    __syncthreads();
+    const int first = (int)blockIdx.y * p.per_pass, used = min(p.per_pass, all - first);
+    const bool work = used > 0;  // (the same for the whole cluster)
+    if (work) {
+        int mine = -1;
+        if (tid < LS_TOKENS) {
+            if (head >= 0) mine = s.place[head] - first;
+            if (mine >= used) mine = -1;
+            s.mine[tid] = max(mine, -1);
+        }
+        const int KB = (p.K + 63) / 64, kb0 = KB * me / ctas, kb1 = KB * (me + 1) / ctas;
+        if (warp == 4) {
+            // ---------------- copies
+            int st = 0;
+            uint32_t ph = 1;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (kb - kb0 >= LS_STAGES && !(ok = mbar_wait_warp(&s.empty[st], ph, p.status, &s.abort))) break;
+                uint8_t *dst = ring + (size_t)st * LS_STAGE;
+                const uint32_t bar = smem_u32(&s.full[st]);
+                mbar_arrive_expect_tx_elect(&s.full[st], (uint32_t)(LS_TOKENS + used * p.rank) * 128u);
+                if (lane == 0) tma_tile_2d<1>(dst, &p.x, kb * 64, t0, bar);
+                if (lane < used)  // (at most 256 / 8)
+                    tma_tile_3d<1>(dst + (LS_TOKENS + lane * p.rank) * 128, &p.a, kb * 64, 0, s.list[first + lane], bar);
+                __syncwarp();
+                if (++st == LS_STAGES) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (!ok) settle_after_abort();
+        } else if (warp == 5) {
+            // ---------------- MMAs
+            int st = 0;
+            uint32_t ph = 0;
+            const uint32_t d = __shfl_sync(0xffffffffu, s.tmem, 0);
+            const uint32_t idesc = umma_idesc_16(p.fmt, false, false, 128, __shfl_sync(0xffffffffu, (used * p.rank + 15) & ~15, 0));
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_warp(&s.full[st], ph, p.status, &s.abort)) break;
+                tc_fence_after();
+                const uint32_t sa = smem_u32(ring) + (uint32_t)st * LS_STAGE;
+                const uint64_t a = umma_desc_sw128(sa), b = umma_desc_sw128(sa + LS_TOKENS * 128);
+                const int left = p.K - 64 * kb;
+                umma_f16_elect<1>(d, a, b, idesc, kb > kb0);
+                if (left > 16) umma_f16_elect<1>(d, a + 2, b + 2, idesc, 1);
+                if (left > 32) umma_f16_elect<1>(d, a + 4, b + 4, idesc, 1);
+                if (left > 48) umma_f16_elect<1>(d, a + 6, b + 6, idesc, 1);
+                umma_commit_elect(&s.empty[st]);
+                if (++st == LS_STAGES) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            umma_commit_elect(&s.done);  // every copy has been consumed, every MMA has completed
+        }
+        __syncwarp();
+        const bool ok = mbar_wait_role(&s.done, 0, p.status, &s.abort);
+        const bool fine = __syncthreads_and(ok);
+        tc_fence_after();
+        // ---------------- this CTA's sums: a token's own adapter's columns
+        float *part = (float *)ring;  // [LS_TOKENS][rank + 4]
+        const int pitch = p.rank + 4;
+        if (fine && warp < 4) {
+            const uint32_t tb = s.tmem + ((uint32_t)(32 * warp) << 16);
+            float *o = part + (size_t)tid * pitch;
+            for (int i = 0; i < used; ++i) {
+                if (!__any_sync(0xffffffffu, mine == i)) continue;
+                for (int c = 0; c < p.rank; c += 8) {
+                    uint32_t v[8];
+                    tmem_ld8(tb + i * p.rank + c, v);
+                    tmem_ld_wait();
+                    if (mine == i) {
+                        if (kb0 == kb1)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[k] = 0u;
+                        *(float4 *)(o + c) = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
+                                                         __uint_as_float(v[3]));
+                        *(float4 *)(o + c + 4) = make_float4(__uint_as_float(v[4]), __uint_as_float(v[5]), __uint_as_float(v[6]),
+                                                             __uint_as_float(v[7]));
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+        cluster_sync_all();
+        // ---------------- the cluster's
+        const int ta = LS_TOKENS * me / ctas, tb = LS_TOKENS * (me + 1) / ctas, quads = chunks * 8;
+        for (int i = tid; i < (tb - ta) * quads; i += LS_THREADS) {
+            const int t = ta + i / quads, j = 4 * (i % quads);
+            if (s.mine[t] < 0) continue;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < p.rank) {
+                for (int c = 0; c < ctas; ++c) {
+                    const float4 w = ld_cluster_f32x4(cluster_map(part + (size_t)t * pitch + j, c));
+                    v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+                }
+                const float sc = p.scale ? p.scale[s.ids[t]] : 1.f;
+                v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
+            }
+            uint16_t hi[4], lo[4];
+            split16<BF>(v.x, hi[0], lo[0]);
+            split16<BF>(v.y, hi[1], lo[1]);
+            split16<BF>(v.z, hi[2], lo[2]);
+            split16<BF>(v.w, hi[3], lo[3]);
+            uint16_t *row = p.u + ((size_t)(t0 + t) * chunks + j / 32) * 64 + j % 32;
+            *(uint2 *)row = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
+            *(uint2 *)(row + 32) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
+        }
+        cluster_sync_all();  // (no CTA leaves while its sums are read)
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_group<1>(s.tmem, LS_COLS);
+    }
+}
+
 int check(int T, int rank) {
     MOE_CHECK(T >= 0 && T <= 1 << 24 && rank >= 1);
     if (rank % 8 || rank > MOE_MAX_RANK) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+int shrink_few(const void *x, size_t ldx, int T, int K, int type, const int32_t *adapter, int n_adapters, const void *a,
+               int rank, const float *scale, void *u, moe_stream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    const long long jobs = (long long)T * ((rank + 31) / 32 * 32 / LS_RANKS);
+    moe_pdl_config(&cfg, attr, dim3((unsigned)((jobs + 7) / 8)), dim3(256), 0, moe_cuda_stream(s));
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, type == MOE_BF16 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>,
+                                    (const uint16_t *)x, ldx, T, K, adapter, n_adapters, (const uint16_t *)a, rank, scale,
+                                    (uint16_t *)u));
+    return MOE_OK;
+}
+
+int shrink_many(const void *x, size_t ldx, int T, int K, int type, const int32_t *adapter, int n_adapters, const void *a,
+                int rank, const float *scale, void *u, int *status, moe_stream_t s) {
+    static std::mutex mu;
+    static int sms[64] = {0};
+    int dev = -1, n = 0, rc;
+    MOE_TRY_CUDA(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!sms[dev]) {
+            int count = 0;
+            MOE_TRY_CUDA(cudaFuncSetAttribute(lora_shrink_mma_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, LS_SMEM));
+            MOE_TRY_CUDA(cudaFuncSetAttribute(lora_shrink_mma_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, LS_SMEM));
+            MOE_TRY_CUDA(cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev));
+            sms[dev] = count;
+        }
+        n = sms[dev];
+    }
+    ShrinkParams p = {};
+    {
+        const uint64_t dims[2] = {(uint64_t)K, (uint64_t)T}, strides[1] = {(uint64_t)ldx * 2};
+        const uint32_t box[2] = {64, LS_TOKENS};
+        if ((rc = grouped_map(&p.x, type, 2, x, dims, strides, box, 128)) != MOE_OK) return rc;
+    }
+    {
+        const uint64_t dims[3] = {(uint64_t)K, (uint64_t)rank, (uint64_t)n_adapters};
+        const uint64_t strides[2] = {(uint64_t)K * 2, (uint64_t)K * rank * 2};
+        const uint32_t box[3] = {64, (uint32_t)rank, 1};
+        if ((rc = grouped_map(&p.a, type, 3, a, dims, strides, box, 128)) != MOE_OK) return rc;
+    }
+    p.T = T;
+    p.K = K;
+    p.rank = rank;
+    p.n_adapters = n_adapters;
+    p.per_pass = LS_COLS / rank;
+    p.fmt = type == MOE_BF16;
+    p.adapter = adapter;
+    p.scale = scale;
+    p.u = (uint16_t *)u;
+    p.status = status;
+    const int tiles = (T + LS_TOKENS - 1) / LS_TOKENS, most = std::min(n_adapters, LS_TOKENS);
+    const int passes = (most + p.per_pass - 1) / p.per_pass;
+    int ctas = 1;
+    while (ctas < LS_MAX_SPLIT && tiles * ctas * 2 <= n && ctas * 2 * 64 <= K) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    moe_pdl_config(&cfg, attr, dim3((unsigned)(tiles * ctas), (unsigned)passes), dim3(LS_THREADS), LS_SMEM, moe_cuda_stream(s));
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, type == MOE_BF16 ? lora_shrink_mma_kernel<true> : lora_shrink_mma_kernel<false>, p));
     return MOE_OK;
 }
 
@@ -152,13 +434,9 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     p.fmt = type == MOE_BF16;
     p.status = moe_status_word_device_ptr();
 
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    const long long jobs = (long long)T * (chunks * 32 / LS_RANKS);
-    moe_pdl_config(&cfg, attr, dim3((unsigned)((jobs + 7) / 8)), dim3(256), 0, moe_cuda_stream(s));
-    const uint16_t *xa = (const uint16_t *)x, *aa = (const uint16_t *)a;
-    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, type == MOE_BF16 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>, xa, ldx, T,
-                                    K, adapter, n_adapters, aa, rank, scale, (uint16_t *)workspace));
+    rc = T <= LS_FEW ? shrink_few(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, s)
+                     : shrink_many(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, p.status, s);
+    if (rc != MOE_OK) return rc;
     const bool wide = T > 32;
     const long long tiles = wide ? (T + 255) / 256 : (T + 31) / 32;
     return grouped_launch(p, ytype, GP_LORA, wide, tiles * ((N + 127) / 128), (K + 63) / 64 + std::min(T, n_adapters) * chunks,
