@@ -117,9 +117,10 @@ __device__ __forceinline__ void grouped_store4(uint8_t *row, int i, float4 a) {
     else *(uint2 *)(row + 2 * (size_t)i) = make_uint2(grouped_pack<OT>(a.x, a.y), grouped_pack<OT>(a.z, a.w));
 }
 
-// A word to shared memory of the cluster, counted by a barrier there.
-__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr), "f"(v), "r"(bar)
+// Shared memory to shared memory of the cluster, counted by a barrier there (shared::cluster addresses).
+__device__ __forceinline__ void bulk_s2cluster(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(smem_u32(src)), "r"(bytes), "r"(bar)
                  : "memory");
 }
 
@@ -205,26 +206,29 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     const int mt = (p.M + MROWS * CG - 1) / (MROWS * CG);
     const int gran = GRAD ? 64 * CG : G_::GRAN;
     const int gt = GRAD ? (p.N + NT - 1) / NT : 0;  // GP_GRAD: tiles of N
-    for (int i = tid; i <= p.G; i += GP_THREADS) off[i] = p.offsets ? p.offsets[i] : i * p.R;
-    __syncthreads();
-    auto rows_of = [&](int g) -> int {  // rows of a group; none where the offsets are no range of rows
-        const int a = off[g], b = off[g + 1];
+    // this CTA's items: unit, unit + units, ..
+    const int units = (int)gridDim.x / (CG * ks), unit = (int)blockIdx.x / (CG * ks);
+    auto rows_of = [&](int a, int b) -> int {  // rows of a group; none where the offsets are no range of rows
         return a >= 0 && b >= a && b <= p.R ? b - a : 0;
     };
-    constexpr int PER = (MOE_MAX_GROUPS + GP_THREADS - 1) / GP_THREADS;
+    // item `r` of group g: group and M tile, first row, rows, the group's rows
+    auto make_item = [&](int g, int r, int begin, int cnt) -> int4 {
+        const int t = r / mt;
+        // near-equal tiles: none is empty, as size <= NT
+        const int all = GRAD ? p.N : cnt, nt = (all + NT - 1) / NT;
+        const int size = nt == 1 ? NT : ((all + nt - 1) / nt + gran - 1) / gran * gran;
+        return make_int4(g | (r - t * mt) << 10, (GRAD ? 0 : begin) + t * size, min(size, all - t * size), cnt);
+    };
+    static_assert(MOE_MAX_GROUPS <= 1024 && MOE_MAX_GROUPS <= GP_THREADS, "ten bits of a group, a thread each");
     {
-        int c[PER], t = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int g = tid * PER + i;
-            c[i] = t;
-            if (g < p.G) {
-                const int n = rows_of(g);
-                if (!n && off[g + 1] != off[g]) moe_set_status(p.status, MOE_ERR_INVALID);
-                t += mt * (GRAD ? gt : (n + NT - 1) / NT);
-            }
-        }
-        int inc = t;
+        // a thread per group: its items behind those of the groups before it, and of them this CTA's to the table
+        const int begin = tid > p.G ? 0 : p.offsets ? p.offsets[tid] : tid * p.R;
+        const int next = tid >= p.G ? 0 : p.offsets ? p.offsets[tid + 1] : p.R;
+        const int cnt = tid < p.G ? rows_of(begin, next) : 0;
+        if (tid <= p.G) off[tid] = begin;
+        if (tid < p.G && !cnt && next != begin) moe_set_status(p.status, MOE_ERR_INVALID);
+        const int mine = tid < p.G ? mt * (GRAD ? gt : (cnt + NT - 1) / NT) : 0;
+        int inc = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int v = __shfl_up_sync(0xffffffffu, inc, d);
@@ -232,34 +236,26 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         }
         if (lane == 31) sums[warp] = inc;
         __syncthreads();
-        int before = inc - t;
-        for (int w = 0; w < warp; ++w) before += sums[w];
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (tid * PER + i < p.G) first[tid * PER + i] = before + c[i];
-        if (tid == GP_THREADS - 1) first[p.G] = before + t;
+        const int begins = __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0) + inc - mine;
+        if (tid <= p.G) first[tid] = begins;
+        if (mine) {
+            int i = begins <= unit ? 0 : (begins - unit + units - 1) / units;
+            for (int at = unit + i * units; at < begins + mine && i < GP_ITEMS; ++i, at += units)
+                items[i] = make_item(tid, at - begins, begin, cnt);
+        }
     }
     __syncthreads();
-    // this CTA's items: unit, unit + units, ..
-    const int n_items = first[p.G], units = (int)gridDim.x / (CG * ks), unit = (int)blockIdx.x / (CG * ks);
-    const int n_mine = unit < n_items ? (n_items - unit - 1) / units + 1 : 0;
-    auto look_up_item = [&](int i) -> int4 {  // group and M tile, first row, rows, the group's rows
-        const int j = unit + i * units;
-        int lo = 0, hi = p.G;  // the last group whose first item is not after j
+    const int n_items = first[p.G], n_mine = unit < n_items ? (n_items - unit - 1) / units + 1 : 0;
+    auto look_up_item = [&](int i) -> int4 {  // (past the table)
+        const int at = unit + i * units;
+        int lo = 0, hi = p.G;  // the last group whose first item is not after this one
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (first[mid] <= j) lo = mid;
+            if (first[mid] <= at) lo = mid;
             else hi = mid;
         }
-        const int r = j - first[lo], t = r / mt, cnt = rows_of(lo);
-        // near-equal tiles: none is empty, as size <= NT
-        const int all = GRAD ? p.N : cnt, nt = (all + NT - 1) / NT;
-        const int size = ((all + nt - 1) / nt + gran - 1) / gran * gran;
-        return make_int4(lo | (r - t * mt) << 10, (GRAD ? 0 : off[lo]) + t * size, min(size, all - t * size), cnt);
+        return make_item(lo, at - first[lo], off[lo], rows_of(off[lo], off[lo + 1]));
     };
-    static_assert(MOE_MAX_GROUPS <= 1024, "ten bits of a group");
-    for (int i = tid; i < min(n_mine, GP_ITEMS); i += GP_THREADS) items[i] = look_up_item(i);
-    __syncthreads();
     auto item_at = [&](int i) -> GroupedItem {
         const int4 v = i < GP_ITEMS ? items[i] : look_up_item(i);
         GroupedItem it;
@@ -284,20 +280,15 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         }
     };
     const int chunks = MODE == GP_LORA ? (p.rank + 31) / 32 : 1;
-    auto extra_stages = [&](const GroupedItem &it) -> int {
+    auto extra_stages = [&](const int (&ids)[8]) -> int {
         int n = 0;
-        if (MODE == GP_LORA) {
-            int ids[8];
-            tile_adapters(it, ids);
-            for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a)) n += chunks;
-        }
+        for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a)) n += chunks;
         return n;
     };
-    // the stages [lo, hi) of an item that are this CTA's, its `extra` last ones those of GP_LORA
-    auto stage_range = [&](const GroupedItem &it, int extra, int &lo, int &hi) {
-        const int all = it.steps + extra;
-        lo = CG == 1 ? all * kr / ks : 0;
-        hi = CG == 1 ? all * (kr + 1) / ks : all;
+    // of n stages (those of the matrix, then GP_LORA's extra ones) this CTA's [lo, hi)
+    auto share = [&](int n, int &lo, int &hi) {
+        lo = CG == 1 ? n * kr / ks : 0;
+        hi = CG == 1 ? n * (kr + 1) / ks : n;
     };
     auto source = [&](int i) -> int {  // x's row of position i, -1: none
         if (!p.x_index) return i < p.x_rows ? i : -1;
@@ -317,8 +308,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             const GroupedItem it = item_at(j);
             const int nb = it.npad / CG, m0 = (it.m * CG + rank) * MROWS;
             int lo, hi;
-            stage_range(it, extra_stages(it), lo, hi);
-            for (int kb = lo; kb < min(hi, it.steps); ++kb, ++gs) {
+            share(it.steps, lo, hi);
+            for (int kb = lo; kb < hi; ++kb, ++gs) {
                 if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
                 uint8_t *dst = ring + (size_t)st * G_::STAGE;
                 const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
@@ -342,9 +333,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 }
             }
             if (MODE == GP_LORA && ok) {
-                int ids[8];
+                int ids[8], e = 0;
                 tile_adapters(it, ids);
-                int e = it.steps;
+                share(extra_stages(ids), lo, hi);
                 for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a))
                     for (int c = 0; c < chunks; ++c, ++e) {
                         if (e < lo || e >= hi) continue;
@@ -377,8 +368,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         for (int j = 0; j < n_mine && ok; ++j) {
             const GroupedItem it = item_at(j);
             const int nb = it.npad / CG, c0 = it.row0 + rank * nb;
-            int lo, hi;
-            stage_range(it, extra_stages(it), lo, hi);
+            int lo, hi, elo, ehi;
+            share(it.steps, lo, hi);
             for (int kb = lo; kb < hi; ++kb, ++gs) {
                 if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
                 uint8_t *dst = ring + (size_t)st * G_::STAGE + GP_ABYTES;
@@ -386,7 +377,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 if (GRAD) {
                     if (64 * lane < nb && 64 * kb + 64 <= it.cnt)
                         tma_tile_2d<CG>(dst + lane * 8192, &p.b, c0 + 64 * lane, it.r0 + 64 * kb, bar);
-                } else if (kb < it.steps) {
+                } else {
                     // 64 rows a box, the rest by 16
                     const int big = nb / 64, r = lane < big ? 64 * lane : 64 * big + 16 * (lane - big);
                     if (r < nb) tma_tile_2d<CG>(dst + r * 128, lane < big ? &p.b64 : &p.b, kb * 64, c0 + r, bar);
@@ -395,6 +386,18 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 if (++st == S) {
                     st = 0;
                     ph ^= 1u;
+                }
+            }
+            if (MODE == GP_LORA) {  // (the loaders' stages)
+                int ids[8];
+                tile_adapters(it, ids);
+                share(extra_stages(ids), elo, ehi);
+                for (int e = elo; e < ehi; ++e, ++gs) {
+                    if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
+                    if (++st == S) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
         }
@@ -445,7 +448,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             }
             const int nb = it.npad / CG;
             int lo, hi;
-            stage_range(it, extra_stages(it), lo, hi);
+            share(it.steps, lo, hi);
             if (!GRAD) {
                 // eight threads a row: piece lt % 8 of rows lt / 8 + 16 i
                 constexpr int RI = NT / CG / 16;
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     who[i] = MODE != GP_LORA ? (r >= 0 ? 16 : 0) : r >= 0 ? p.adapter[r] : -1;
                     src[i] = p.rows + (size_t)max(r, 0) * p.ld + 8 * piece + 64 * (lo + (team != (gs & 1)));
                 }
-                for (int kb = lo; kb < min(hi, it.steps); ++kb, next()) {
+                for (int kb = lo; kb < hi; ++kb, next()) {
                     if ((gs & 1) != team) continue;
                     if (!begin()) break;
                     if (MODE != GP_LORA) {
@@ -476,10 +479,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 }
                 if (MODE == GP_LORA && ok) {
                     if (j == 0) pdl_wait();  // u
-                    int ids[8];
+                    int ids[8], e = 0;
                     tile_adapters(it, ids);
+                    share(extra_stages(ids), lo, hi);
                     const uint16_t *u = p.rows + (size_t)(it.row0 + rank * nb + r0) * p.ld + 8 * piece;
-                    int e = it.steps;
                     for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a))
                         for (int c = 0; c < chunks; ++c, ++e) {
                             if (e < lo || e >= hi) continue;
@@ -543,9 +546,16 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         bool ok = true;
         for (int j = 0; j < n_mine && ok; ++j) {
             const GroupedItem it = item_at(j);
-            int lo, hi;
-            stage_range(it, extra_stages(it), lo, hi);
-            for (int kb = lo; kb < hi; ++kb) {
+            int lo, hi, n = 0;
+            share(it.steps, lo, hi);
+            n = hi - lo;
+            if (MODE == GP_LORA) {
+                int ids[8];
+                tile_adapters(it, ids);
+                share(extra_stages(ids), lo, hi);
+                n += hi - lo;
+            }
+            for (int kb = 0; kb < n; ++kb) {
                 if (!(ok = mbar_wait_warp(&landed[st], ph, p.status, abort_flag))) break;
                 fence_proxy_async_smem();
                 if (lane == 0) {
@@ -570,14 +580,13 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             const uint32_t idesc = umma_idesc_16(p.fmt, A_MN, B_MN, 128 * CG, __shfl_sync(0xffffffffu, it.npad, 0));
             const int buf = j & 1;
             int lo, hi;
-            stage_range(it, extra_stages(it), lo, hi);
-            lo = __shfl_sync(0xffffffffu, lo, 0);
-            hi = __shfl_sync(0xffffffffu, hi, 0);
+            share(__shfl_sync(0xffffffffu, it.steps, 0), lo, hi);
+            bool fresh = true;  // nothing summed yet
             if (j >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((j / 2) - 1) & 1, p.status, abort_flag))) break;
             tc_fence_after();
             const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + buf * NT;
-            const int len = GRAD ? __shfl_sync(0xffffffffu, it.cnt, 0) : p.K, n_steps = __shfl_sync(0xffffffffu, it.steps, 0);
-            for (int kb = lo; kb < min(hi, n_steps); ++kb) {
+            const int len = GRAD ? __shfl_sync(0xffffffffu, it.cnt, 0) : p.K;
+            for (int kb = lo; kb < hi; ++kb) {
                 if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
                 tc_fence_after();
                 const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
@@ -586,7 +595,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 const int left = len - 64 * kb;
                 auto step = [&](int q) {
                     umma_f16_elect<CG>(d, a + (uint64_t)(q * (A_MN ? 128 : 2)), b + (uint64_t)(q * (B_MN ? 128 : 2)), idesc,
-                                       q > 0 || kb > lo);
+                                       q > 0 || !fresh);
                 };
                 step(0);
                 if (left > 48) {  // (no branch between the MMAs)
@@ -597,24 +606,32 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     if (left > 16) step(1);
                     if (left > 32) step(2);
                 }
+                fresh = false;
                 umma_commit_group_elect<CG>(&empty[st]);
                 if (++st == S) {
                     st = 0;
                     ph ^= 1u;
                 }
             }
-            for (int e = max(lo, n_steps); MODE == GP_LORA && e < hi && ok; ++e) {
+            if (MODE == GP_LORA) {
+                int ids[8];
+                tile_adapters(it, ids);
+                share(__shfl_sync(0xffffffffu, extra_stages(ids), 0), lo, hi);
+            }
+            for (int e = lo, c = MODE == GP_LORA ? lo % chunks : 0; MODE == GP_LORA && e < hi && ok; ++e) {
                 if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
                 tc_fence_after();
                 // 32 ranks: u's upper halves in the first 64 bytes of a row, the rest of u in the second, both by the same B_a
                 const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
                 const uint64_t a = umma_desc_sw64(sa), b = umma_desc_sw128(sa + GP_ABYTES);
-                umma_f16_elect<CG>(d, a, b, idesc, e > lo);
+                umma_f16_elect<CG>(d, a, b, idesc, !fresh);
                 umma_f16_elect<CG>(d, a, b + 4, idesc, 1);
-                if (p.rank - 32 * ((e - n_steps) % chunks) > 16) {
+                if (p.rank - 32 * c > 16) {
                     umma_f16_elect<CG>(d, a + 2, b + 2, idesc, 1);
                     umma_f16_elect<CG>(d, a + 2, b + 6, idesc, 1);
                 }
+                fresh = false;
+                if (++c == chunks) c = 0;
                 umma_commit_group_elect<CG>(&empty[st]);
                 if (++st == S) {
                     st = 0;
@@ -688,32 +705,37 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             const bool none = GRAD && !it.steps;
             const int m0 = (it.m * CG + rank) * MROWS + MROWS / 4 * q;  // the warp's first element
             if (CG == 1 && ks > 1) {
-                // the item's only CTA but for the others of the cluster: each adds up the rows c with c % ks = its rank
-                // (and has one item: nothing is left in the buffers by an earlier one)
-                const uint32_t bar = smem_u32(red_full), red = smem_u32(smem + G_::O_RED);
-                const int per = (NT + ks - 1) / ks, own = it.n > kr ? (it.n - kr - 1) / ks + 1 : 0;
-                if (et == 0 && own) mbar_arrive_expect_tx(red_full, (uint32_t)(own * ks) * 512u);
-                int lo, hi;
-                stage_range(it, extra_stages(it), lo, hi);
-                for (int c0 = 16 * half; c0 < it.n; c0 += 32) {
+                // the cluster's only item: each CTA adds up its share of the rows, `per` of them (the last ones fewer)
+                const int per = (it.n + ks - 1) / ks, own = max(0, min(per, it.n - kr * per));
+                int lo, hi, n;
+                share(it.steps, lo, hi);
+                n = hi - lo;
+                if (MODE == GP_LORA) {
+                    int ids[8];
+                    tile_adapters(it, ids);
+                    share(extra_stages(ids), lo, hi);
+                    n += hi - lo;
+                }
+                float *x = (float *)(smem + G_::O_XCH);  // [NT][128]
+                static_assert(CG == 2 || NT * 512 <= 8 * G_::XCH, "sums of an item");
+                if (16 * half < it.n) {
                     uint32_t v[16];
-                    tmem_ld16(tb + c0, v);
+                    tmem_ld16(tb + 16 * half, v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int c = c0 + k;
-                        if (c < it.n) {
-                            uint32_t to, tobar;
-                            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(red), "r"(c % ks));
-                            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(tobar) : "r"(bar), "r"(c % ks));
-                            st_async_f32(to + ((kr * per + c / ks) * 128 + 32 * q + lane) * 4, lo < hi ? __uint_as_float(v[k]) : 0.f,
-                                         tobar);
-                        }
-                    }
+                    for (int k = 0; k < 16; ++k) x[(16 * half + k) * 128 + 32 * q + lane] = n ? __uint_as_float(v[k]) : 0.f;
                 }
+                fence_proxy_async_smem();
+                if (et == 0 && own) mbar_arrive_expect_tx(red_full, (uint32_t)(own * ks) * 512u);
+                bar_sync_n(2, 256);
+                // to each CTA its rows, in one copy
+                const int rows = max(0, min(per, it.n - et * per));
+                if (et < ks && rows)
+                    bulk_s2cluster(cluster_map(smem + G_::O_RED + kr * per * 512, et), x + et * per * 128, rows * 512u,
+                                   cluster_map(red_full, et));
                 if (own) {
                     const bool there = mbar_wait_role(red_full, 0, p.status, abort_flag);
-                    if (!bar_and_n(1, 256, there)) break;
+                    if (!bar_and_n(3, 256, there)) break;
                     const float *sum = (const float *)(smem + G_::O_RED);
                     auto total = [&](int r, int m) -> float4 {  // in the order of the CTAs
                         float4 a = *(const float4 *)(sum + r * 128 + m);
@@ -725,7 +747,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     };
                     constexpr int QUADS = MROWS / 4;
                     for (int i = et; i < own * QUADS; i += 256) {
-                        const int r = i / QUADS, c = r * ks + kr, m = 4 * (i % QUADS), mg = it.m * MROWS + m;
+                        const int r = i / QUADS, c = kr * per + r, m = 4 * (i % QUADS), mg = it.m * MROWS + m;
                         float4 a;
                         if (MODE == GP_SWIGLU) {
                             const int at = 2 * (m & ~15) + (m & 15);
