@@ -2,6 +2,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "moe_grouped.cuh"
@@ -49,6 +50,15 @@ int rows_map(CUtensorMap *map, int type, const void *x, int rows, int cols, size
 }
 
 }  // namespace
+
+int grouped_sms() {
+    static std::atomic<int> sms[64];
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = sms[dev].load();
+    if (!n && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) sms[dev].store(n);
+    return n;
+}
 
 int grouped_map(CUtensorMap *map, int type, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
                 const uint32_t *box, int swizzle_bytes) {

@@ -81,7 +81,8 @@ struct GroupedGeom {
     static constexpr int RED = CG == 1 ? (NT + GP_MAX_SPLIT - 1) * 512 : 0;
     static constexpr int O_ITEMS = 1024, O_OFF = O_ITEMS + GP_ITEMS * 16;
     static constexpr int O_FIRST = O_OFF + (MOE_MAX_GROUPS + 4) * 4;
-    static constexpr int O_ROWS = O_FIRST + (MOE_MAX_GROUPS + 4) * 4;
+    static constexpr int O_ORDER = O_FIRST + (MOE_MAX_GROUPS + 4) * 4;
+    static constexpr int O_ROWS = O_ORDER + MOE_MAX_GROUPS * 2;
     static constexpr int O_XCH = O_ROWS + 2 * NT * 12;
     static constexpr int O_RED = O_XCH + 8 * XCH;
     static constexpr int O_RING = (O_RED + RED + 1023) / 1024 * 1024;
@@ -165,7 +166,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     int *sums = (int *)(tmem_slot + 4);                       // [20]
     int *off = (int *)(smem + G_::O_OFF);                     // [G + 1]
-    int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before a group's
+    int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before those of the i-th group ..
+    uint16_t *order = (uint16_t *)(smem + G_::O_ORDER);       // [G] .. and which group that is (pairs)
     uint8_t **e_y = (uint8_t **)(smem + G_::O_ROWS);          // [2][NT] the output rows of an accumulator's columns (NULL: none)
     float *e_s = (float *)(e_y + 2 * NT);                     // [2][NT] and their scale
     int4 *items = (int4 *)(smem + G_::O_ITEMS);
@@ -221,12 +223,37 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     };
     static_assert(MOE_MAX_GROUPS <= 1024 && MOE_MAX_GROUPS <= GP_THREADS, "ten bits of a group, a thread each");
     {
-        // a thread per group: its items behind those of the groups before it, and of them this CTA's to the table
-        const int begin = tid > p.G ? 0 : p.offsets ? p.offsets[tid] : tid * p.R;
+        // A thread per group: its items behind those of the groups before it, and of them this CTA's to the table.  Pairs:
+        // the groups with the most rows first, so that the last round's items are narrow ones (32768 routes over 128
+        // experts of uneven popularity, gate/up 198 -> 192 us).  Not GP_GRAD, whose long and short items, bound by the MMAs
+        // and by the stores, had better be mixed.
+        int g = tid, begin = tid > p.G ? 0 : p.offsets ? p.offsets[tid] : tid * p.R;
         const int next = tid >= p.G ? 0 : p.offsets ? p.offsets[tid + 1] : p.R;
-        const int cnt = tid < p.G ? rows_of(begin, next) : 0;
+        int cnt = tid < p.G ? rows_of(begin, next) : 0;
         if (tid <= p.G) off[tid] = begin;
         if (tid < p.G && !cnt && next != begin) moe_set_status(p.status, MOE_ERR_INVALID);
+        if (CG == 2 && !GRAD && p.G > 1) {
+            int *rows = first;
+            if (tid < (p.G + 3) / 4 * 4) rows[tid] = cnt;
+            __syncthreads();
+            if (tid < p.G) {
+                int before = 0;
+#pragma unroll 4
+                for (int i = 0; i < p.G; i += 4) {  // (past the last group: no rows, and behind this one)
+                    const int4 v = *(const int4 *)&rows[i];
+                    before += (v.x > cnt || (v.x == cnt && i < tid)) + (v.y > cnt || (v.y == cnt && i + 1 < tid)) +
+                              (v.z > cnt || (v.z == cnt && i + 2 < tid)) + (v.w > cnt || (v.w == cnt && i + 3 < tid));
+                }
+                order[before] = (uint16_t)tid;
+            }
+            __syncthreads();
+            if (tid < p.G) {
+                g = order[tid];
+                cnt = rows[g];
+                begin = off[g];
+            }
+            __syncthreads();
+        }
         const int mine = tid < p.G ? mt * (GRAD ? gt : (cnt + NT - 1) / NT) : 0;
         int inc = mine;
 #pragma unroll
@@ -241,20 +268,21 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         if (mine) {
             int i = begins <= unit ? 0 : (begins - unit + units - 1) / units;
             for (int at = unit + i * units; at < begins + mine && i < GP_ITEMS; ++i, at += units)
-                items[i] = make_item(tid, at - begins, begin, cnt);
+                items[i] = make_item(g, at - begins, begin, cnt);
         }
     }
     __syncthreads();
     const int n_items = first[p.G], n_mine = unit < n_items ? (n_items - unit - 1) / units + 1 : 0;
     auto look_up_item = [&](int i) -> int4 {  // (past the table)
         const int at = unit + i * units;
-        int lo = 0, hi = p.G;  // the last group whose first item is not after this one
+        int lo = 0, hi = p.G;  // the last one whose first item is not after this one
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (first[mid] <= at) lo = mid;
             else hi = mid;
         }
-        return make_item(lo, at - first[lo], off[lo], rows_of(off[lo], off[lo + 1]));
+        const int g = CG == 2 && !GRAD && p.G > 1 ? order[lo] : lo;
+        return make_item(g, at - first[lo], off[g], rows_of(off[g], off[g + 1]));
     };
     auto item_at = [&](int i) -> GroupedItem {
         const int4 v = i < GP_ITEMS ? items[i] : look_up_item(i);
@@ -455,12 +483,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 const int piece = lt & 7, r0 = lt >> 3, rows = min(nb, it.n - rank * nb);
                 const uint32_t at = smem_u32(ring) + GP_ABYTES + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
                 const uint16_t *src[RI];
-                int who[RI];  // bytes to copy; GP_LORA: the token's adapter
+                int who[RI];  // bytes to copy; GP_LORA, later: the token's adapter
 #pragma unroll
                 for (int i = 0; i < RI; ++i) {
                     const int c = r0 + 16 * i;
-                    const int r = c >= rows ? -1 : MODE == GP_LORA ? it.row0 + rank * nb + c : source(it.row0 + rank * nb + c);
-                    who[i] = MODE != GP_LORA ? (r >= 0 ? 16 : 0) : r >= 0 ? p.adapter[r] : -1;
+                    const int r = c >= rows || MODE == GP_LORA ? -1 : source(it.row0 + rank * nb + c);
+                    who[i] = r >= 0 ? 16 : 0;
                     src[i] = p.rows + (size_t)max(r, 0) * p.ld + 8 * piece + 64 * (lo + (team != (gs & 1)));
                 }
                 for (int kb = lo; kb < hi; ++kb, next()) {
@@ -482,6 +510,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     int ids[8], e = 0;
                     tile_adapters(it, ids);
                     share(extra_stages(ids), lo, hi);
+#pragma unroll
+                    for (int i = 0; i < RI; ++i)
+                        who[i] = r0 + 16 * i < rows ? p.adapter[it.row0 + rank * nb + r0 + 16 * i] : -1;
                     const uint16_t *u = p.rows + (size_t)(it.row0 + rank * nb + r0) * p.ld + 8 * piece;
                     for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a))
                         for (int c = 0; c < chunks; ++c, ++e) {
@@ -902,6 +933,8 @@ static inline int grouped_launch(const GroupedParams &p, int ytype, int mode, bo
            : ytype == MOE_BF16 ? grouped_launch_bf16(p, mode, wide, items, stages, s)
                                : grouped_launch_f16(p, mode, wide, items, stages, s);
 }
+// SMs of the current device (0: none).
+int grouped_sms();
 // Tensor map of 16-bit elements: `rank` dimensions and box extents innermost first, strides in bytes from the second on.
 int grouped_map(CUtensorMap *map, int type, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
                 const uint32_t *box, int swizzle_bytes);

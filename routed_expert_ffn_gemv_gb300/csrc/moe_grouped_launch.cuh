@@ -10,22 +10,19 @@ template <int CG, int NT, int MODE, int OT>
 static int grouped_launch_t(const GroupedParams &p, long long items, int stages, cudaStream_t s) {
     using G = GroupedGeom<CG, NT>;
     static std::mutex mu;
-    static int sms[64] = {0};
+    static bool ready[64] = {false};
     int dev = -1;
     MOE_TRY_CUDA(cudaGetDevice(&dev));
     if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
-    int n = 0;
     {
         std::lock_guard<std::mutex> lock(mu);
-        if (!sms[dev]) {
-            int count = 0;
+        if (!ready[dev]) {
             MOE_TRY_CUDA(cudaFuncSetAttribute(grouped_kernel<CG, NT, MODE, OT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               (int)G::SMEM));
-            MOE_TRY_CUDA(cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev));
-            sms[dev] = count;
+            ready[dev] = true;
         }
-        n = sms[dev];
     }
+    const int n = std::max(CG, grouped_sms());
     items = std::max(1LL, items);
     int cluster = CG;
     // CG = 1: as many CTAs to an item as there are SMs for, each with four stages of the reduction at least

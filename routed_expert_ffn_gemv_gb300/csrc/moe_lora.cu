@@ -320,20 +320,18 @@ int shrink_few(const void *x, size_t ldx, int T, int K, int type, const int32_t 
 int shrink_many(const void *x, size_t ldx, int T, int K, int type, const int32_t *adapter, int n_adapters, const void *a,
                 int rank, const float *scale, void *u, int *status, moe_stream_t s) {
     static std::mutex mu;
-    static int sms[64] = {0};
-    int dev = -1, n = 0, rc;
+    static bool ready[64] = {false};
+    int dev = -1, rc;
+    const int n = grouped_sms();
     MOE_TRY_CUDA(cudaGetDevice(&dev));
     if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
     {
         std::lock_guard<std::mutex> lock(mu);
-        if (!sms[dev]) {
-            int count = 0;
+        if (!ready[dev]) {
             MOE_TRY_CUDA(cudaFuncSetAttribute(lora_shrink_mma_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, LS_SMEM));
             MOE_TRY_CUDA(cudaFuncSetAttribute(lora_shrink_mma_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, LS_SMEM));
-            MOE_TRY_CUDA(cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev));
-            sms[dev] = count;
+            ready[dev] = true;
         }
-        n = sms[dev];
     }
     ShrinkParams p = {};
     {
