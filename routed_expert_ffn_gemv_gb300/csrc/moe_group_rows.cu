@@ -11,9 +11,10 @@
 
 #define GR_WARPS 32
 #define GR_THREADS (32 * GR_WARPS)
-#define GR_CTA_IDS 4096                    // ids of a CTA of the cluster, while there are few
-#define GR_MAX_CTAS 8
-#define GR_CLUSTER_IDS (1 << 17)           // most ids that one cluster takes
+#define GR_CTA_IDS 2048                    // ids of a CTA of the cluster, while there are few
+#define GR_MAX_CTAS 16
+#define GR_LANE_IDS 8                      // most ids of a thread
+#define GR_CLUSTER_IDS (GR_MAX_CTAS * GR_THREADS * GR_LANE_IDS)  // most ids that one cluster takes
 #define GR_BLOCKS 148
 
 namespace {
@@ -82,30 +83,52 @@ __device__ __forceinline__ int group_starts(const int *total, int *first, int G,
 }
 
 size_t table_bytes(int G) { return (size_t)(GR_WARPS + 2) * G * 4; }
+size_t cluster_bytes(int G) { return (size_t)(GR_WARPS + 1 + 3) * G * 4; }
 
+// A thread keeps its ids and their ranks among the warp's ids of the same group between the count and the placement.
 __global__ void __launch_bounds__(GR_THREADS, 1)
     group_cluster_kernel(const int32_t *ids, int n, int G, int32_t *offsets, int32_t *rows, int *status) {
     extern __shared__ int sm[];
     __shared__ int sums[GR_WARPS + 1];
-    int *count = sm, *total = sm + GR_WARPS * G, *first = total + G;  // [warps][G], this CTA's, all CTAs'
-    const int tid = threadIdx.x, warp = tid / 32;
+    constexpr int P = GR_WARPS + 1;  // (padded: no bank conflicts)
+    int *count = sm, *total = sm + P * G, *first = total + G, *start = first + G;  // [G][warps], this CTA's, all, and where it begins
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int ctas = (int)cluster_nctarank(), me = (int)cluster_ctarank();
-    for (int i = tid; i < GR_WARPS * G; i += GR_THREADS) count[i] = 0;
+    for (int i = tid; i < P * G; i += GR_THREADS) count[i] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const int seg = ((n + ctas * GR_WARPS - 1) / (ctas * GR_WARPS) + 31) / 32 * 32;  // ids of a warp
-    const int i0 = min(n, (me * GR_WARPS + warp) * seg), i1 = min(n, i0 + seg);
-    warp_pass(ids, i0, i1, G, count + warp * G, nullptr, status);
-    __syncthreads();
-    for (int g = tid; g < G; g += GR_THREADS) {
-        int t = 0;
-        for (int w = 0; w < GR_WARPS; ++w) {  // counts -> the warp's place among the CTA's ids of the group
-            const int c = count[w * G + g];
-            count[w * G + g] = t;
-            t += c;
+    const int turns = (n + ctas * GR_THREADS - 1) / (ctas * GR_THREADS);  // of 32 ids a warp
+    const int i0 = (me * GR_WARPS + warp) * turns * 32 + lane;
+    int id[GR_LANE_IDS], rank[GR_LANE_IDS];
+#pragma unroll
+    for (int t = 0; t < GR_LANE_IDS; ++t) id[t] = t < turns && i0 + 32 * t < n ? ids[i0 + 32 * t] : -1;
+#pragma unroll
+    for (int t = 0; t < GR_LANE_IDS; ++t) {
+        if (t >= turns) break;
+        if (id[t] < -1 || id[t] >= G) {
+            moe_set_status(status, MOE_ERR_INVALID);
+            id[t] = -1;
         }
-        total[g] = t;
+        const unsigned peers = __match_any_sync(0xffffffffu, id[t]);
+        const int before = __popc(peers & ((1u << lane) - 1u));
+        int *c = &count[max(id[t], 0) * P + warp];
+        rank[t] = id[t] >= 0 ? *c + before : 0;
+        __syncwarp();
+        if (id[t] >= 0 && before == 0) *c = rank[t] + __popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int g = warp; g < G; g += GR_WARPS) {  // counts -> the warps' places among the CTA's ids of the group
+        const int c = count[g * P + lane];
+        int inc = c;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += v;
+        }
+        count[g * P + lane] = inc - c;
+        if (lane == 31) total[g] = inc;
     }
     if (ctas > 1) cluster_sync_all();
     else __syncthreads();
@@ -114,18 +137,19 @@ __global__ void __launch_bounds__(GR_THREADS, 1)
         int t = 0, before = 0;
         for (int c = 0; c < ctas; ++c) {
             const int v = ctas > 1 ? __float_as_int(ld_cluster_f32(cluster_map(&total[g], c))) : total[g];
-            if (c == me) before = t;
+            if (c < me) before += v;
             t += v;
         }
         first[g] = t;
-        for (int w = 0; w < GR_WARPS; ++w) count[w * G + g] += before;
+        start[g] = before;
     }
     __syncthreads();
     const int all = group_starts(first, first, G, me == 0 ? offsets : nullptr, sums);
+    for (int g = tid; g < G; g += GR_THREADS) start[g] += first[g];
     __syncthreads();
-    for (int i = tid; i < GR_WARPS * G; i += GR_THREADS) count[i] += first[i % G];
-    __syncthreads();
-    warp_pass(ids, i0, i1, G, count + warp * G, rows, status);
+#pragma unroll
+    for (int t = 0; t < GR_LANE_IDS; ++t)
+        if (id[t] >= 0 && t < turns) rows[start[id[t]] + count[id[t] * P + warp] + rank[t]] = i0 + 32 * t;
     for (int i = all + me * GR_THREADS + tid; i < n; i += ctas * GR_THREADS) rows[i] = -1;
     if (ctas > 1) cluster_sync_all();  // (no CTA leaves while its counts are read)
 }
@@ -196,7 +220,9 @@ int prepare_device() {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
         const int most = (int)table_bytes(MOE_MAX_GROUPS);
-        MOE_TRY_CUDA(cudaFuncSetAttribute(group_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+        MOE_TRY_CUDA(cudaFuncSetAttribute(group_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          (int)cluster_bytes(MOE_MAX_GROUPS)));
+        MOE_TRY_CUDA(cudaFuncSetAttribute(group_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
         MOE_TRY_CUDA(cudaFuncSetAttribute(group_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
         MOE_TRY_CUDA(cudaFuncSetAttribute(group_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
         done[dev] = true;
@@ -233,7 +259,7 @@ extern "C" int moe_group_rows(const int32_t *ids, int n, int G, int32_t *offsets
     if (!need) {
         int ctas = 1;
         while (ctas < GR_MAX_CTAS && (long long)ctas * GR_CTA_IDS < n) ctas *= 2;
-        moe_pdl_config(&cfg, attr, dim3(ctas), dim3(GR_THREADS), table_bytes(G), moe_cuda_stream(s));
+        moe_pdl_config(&cfg, attr, dim3(ctas), dim3(GR_THREADS), cluster_bytes(G), moe_cuda_stream(s));
         attr[1].id = cudaLaunchAttributeClusterDimension;
         attr[1].val.clusterDim.x = ctas;
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;

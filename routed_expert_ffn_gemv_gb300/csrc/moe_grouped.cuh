@@ -938,3 +938,29 @@ int grouped_sms();
 // Tensor map of 16-bit elements: `rank` dimensions and box extents innermost first, strides in bytes from the second on.
 int grouped_map(CUtensorMap *map, int type, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
                 const uint32_t *box, int swizzle_bytes);
+
+// ------------------------------------------------------------------ few rows (moe_grouped_few.cu)
+
+#define GF_MAX_R 32                      // rows of a call
+#define GF_MAX_TILES GF_MAX_R
+
+struct GroupedFewParams {
+    const uint16_t *x, *w;
+    size_t ldx;
+    const int32_t *offsets;  // as in GroupedParams
+    int G, R;
+    const int32_t *x_index;
+    int x_share, x_rows;
+    const int32_t *y_index;
+    int y_rows;
+    const float *scale;
+    void *y;
+    size_t ldy;
+    int ytype, M, K;
+    const int32_t *adapter;  // GP_LORA
+    const uint16_t *b, *u;
+    int n_adapters, rank;
+    int *status;
+};
+// GP_NK, GP_SWIGLU, GP_LORA with R <= GF_MAX_R.
+int grouped_few_launch(const GroupedFewParams &p, int mode, bool bf, cudaStream_t s);

@@ -1,0 +1,261 @@
+// The products of moe_grouped.cuh for few rows (GP_NK, GP_SWIGLU, GP_LORA): decode.
+//
+// What such a call waits for is latency: a tile of the tensor-core kernel passes its prologue, a ring of copies, 4 MMAs a
+// stage of at least 80 clocks each and an epilogue.  Here nothing is staged: a warp loads 16 rows of the matrix straight into
+// the fragments of mma.sync m16n8k16 (the reduction's order is free: a lane's 16 bytes of a row, eight consecutive
+// elements, are its share of two steps, and the same eight of its token's row the other side's), for up to 32 rows of the
+// group.  A CTA's eight warps share the reduction in turns of 32 elements and add their sums up in shared memory in
+// the order of the warps.  HBM bounds it: every matrix element is read once, coalesced in 64-byte pieces, 16 rows of them
+// in flight per warp and instruction.
+#include <algorithm>
+
+#include "moe_grouped.cuh"
+
+#define GF_WARPS 8
+#define GF_THREADS (32 * GF_WARPS)
+#define GF_ROWS 16                       // of the matrix: M of the MMA
+#define GF_PITCH 18                      // floats of a token's sums (padded)
+
+namespace {
+
+// Sixteen bytes that are read once.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+template <bool BF>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if (BF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 32 elements of the reduction: rows g and g + 8 of the matrix (lo, hi) by the token's row.
+template <bool BF>
+__device__ __forceinline__ void mma32(float (&c)[4], const uint4 &lo, const uint4 &hi, const uint4 &x) {
+    mma16<BF>(c, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+    mma16<BF>(c, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+}
+
+struct FewTile {
+    int g, row0, n;
+};
+
+// NB: blocks of eight rows of the group in a tile
+template <int MODE, bool BF, int NB>
+__global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid_constant__ GroupedFewParams p) {
+    constexpr int MATS = MODE == GP_SWIGLU ? 2 : 1, NT = 8 * NB;
+    __shared__ FewTile tiles[GF_MAX_TILES];
+    __shared__ int sums[GF_WARPS], n_tiles_s;
+    __shared__ alignas(16) float red[GF_WARPS][MATS][NT][GF_PITCH];  // (read two at a time)
+    __shared__ uint8_t *s_y[NT];
+    __shared__ float s_scale[NT];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t4 = lane & 3;
+    // (GP_LORA: see grouped_kernel)
+    if (MODE != GP_LORA) pdl_wait();
+    pdl_trigger();
+    // ---------------- tiles of at most NT rows of a group
+    {
+        int base = 0;
+        for (int g0 = 0; g0 < p.G; g0 += GF_THREADS) {
+            const int i = g0 + tid;
+            int begin = 0, cnt = 0;
+            if (i < p.G) {
+                begin = p.offsets ? p.offsets[i] : 0;
+                const int end = p.offsets ? p.offsets[i + 1] : p.R;
+                if (begin >= 0 && end >= begin && end <= p.R) cnt = end - begin;
+                else moe_set_status(p.status, MOE_ERR_INVALID);
+            }
+            const int mine = (cnt + NT - 1) / NT;
+            int inc = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += v;
+            }
+            if (lane == 31) sums[warp] = inc;
+            __syncthreads();
+            const int before = base + __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0) + inc - mine;
+            base += __reduce_add_sync(0xffffffffu, lane < GF_WARPS ? sums[lane] : 0);
+            for (int t = 0; t < mine; ++t)
+                if (before + t < GF_MAX_TILES) tiles[before + t] = FewTile{i, begin + t * NT, min(NT, cnt - t * NT)};
+            __syncthreads();
+        }
+        if (tid == 0) n_tiles_s = min(base, GF_MAX_TILES);  // (the host's bound holds for offsets that do not descend)
+    }
+    __syncthreads();
+    const int blocks = (p.M + GF_ROWS - 1) / GF_ROWS, n_items = n_tiles_s * blocks;
+    // the matrix, PF turns of the warp ahead and across items: rows m0 + g and m0 + g + 8 (past the last one: that one again, not
+    // stored), elements 32 (warp + 8 i) + 8 t4 .. + 7 of turn i
+    constexpr int PF = NB > 1 ? 4 : MATS == 2 ? 5 : 8;
+    uint4 a[PF][MATS][2];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint16_t *w[MATS][2];
+    auto aim = [&](int item) {
+        const int g0 = tiles[item / blocks].g, m0 = item % blocks * GF_ROWS;
+#pragma unroll
+        for (int m = 0; m < MATS; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w[m][h] = p.w + ((size_t)g0 * MATS * p.M + (size_t)m * p.M + min(m0 + g + 8 * h, p.M - 1)) * p.K + 32 * warp + 8 * t4;
+    };
+    auto fetch = [&](uint4 (&v)[MATS][2], int turn) {
+        const int k = 32 * GF_WARPS * turn;
+        const bool in = 32 * warp + 8 * t4 + k < p.K;
+#pragma unroll
+        for (int m = 0; m < MATS; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[m][h] = in ? ld_once(w[m][h] + k) : zero;
+    };
+    const int turns = max(0, (p.K - 32 * warp + 32 * GF_WARPS - 1) / (32 * GF_WARPS));
+    if ((int)blockIdx.x < n_items) {
+        aim(blockIdx.x);
+#pragma unroll
+        for (int i = 0; i < PF; ++i) fetch(a[i], i);
+    }
+    bool waited = false;
+    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+        const FewTile tile = tiles[item / blocks];
+        const int m0 = item % blocks * GF_ROWS;
+        // the tile's rows: this lane's of each block, and (threads 0 .. NT-1) where they go
+        const uint16_t *x[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int c = 8 * b + g;
+            int r = -1;
+            if (c < tile.n) {
+                r = tile.row0 + c;
+                if (p.x_index) {
+                    const int v = p.x_index[r];
+                    r = v < 0 ? -1 : v / p.x_share;
+                }
+            }
+            x[b] = r >= 0 && r < p.x_rows ? p.x + (size_t)r * p.ldx : nullptr;
+        }
+        if (tid < NT) {
+            uint8_t *y = nullptr;
+            float scale = 1.f;
+            if (tid < tile.n) {
+                const int i = tile.row0 + tid;
+                const int s = p.x_index ? p.x_index[i] : i, d = p.y_index ? p.y_index[i] : i;
+                if (s >= 0 && s / (p.x_index ? p.x_share : 1) < p.x_rows && d >= 0 && d < p.y_rows) {
+                    y = (uint8_t *)p.y + (size_t)d * p.ldy * (p.ytype == MOE_F32 ? 4 : 2);
+                    if (p.scale) scale = p.scale[d];
+                } else {
+                    moe_set_status(p.status, MOE_ERR_INVALID);
+                }
+            }
+            s_y[tid] = y;
+            s_scale[tid] = scale;
+        }
+        float acc[MATS][NB][4] = {};
+        // ---------------- the matrix by the tile's rows
+        for (int i0 = 0; i0 < turns; i0 += PF) {
+#pragma unroll
+            for (int i = 0; i < PF; ++i) {
+                const int k = 32 * (warp + GF_WARPS * (i0 + i)) + 8 * t4;  // (turns past the last one: zeros)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint4 v = k < p.K && x[b] ? *(const uint4 *)(x[b] + k) : zero;
+#pragma unroll
+                    for (int m = 0; m < MATS; ++m) mma32<BF>(acc[m][b], a[i][m][0], a[i][m][1], v);
+                }
+                if (i0 + PF < turns) fetch(a[i], i0 + PF + i);
+            }
+        }
+        if (item + (int)gridDim.x < n_items) {
+            aim(item + gridDim.x);
+#pragma unroll
+            for (int i = 0; i < PF; ++i) fetch(a[i], i);
+        }
+        if (MODE == GP_LORA) {
+            // ---------------- the adapters of the tile's tokens, the warps in turns; u's upper halves, then the rest of u
+            if (!waited) pdl_wait();
+            waited = true;
+            int id = lane < tile.n ? p.adapter[tile.row0 + lane] : -1;  // token `lane` of the tile
+            if (id < -1 || id >= p.n_adapters) {
+                moe_set_status(p.status, MOE_ERR_INVALID);
+                id = -1;
+            }
+            const int chunks = (p.rank + 31) / 32;
+            int turn = 0;
+            for (int last = -1;; ++turn) {
+                const unsigned left = __reduce_min_sync(0xffffffffu, id > last ? (unsigned)id : 0x7FFFFFFFu);
+                if (left == 0x7FFFFFFFu) break;
+                const int ad = last = (int)left;
+                if (turn % GF_WARPS != warp) continue;
+                const unsigned who = __ballot_sync(0xffffffffu, id == ad);
+                const uint16_t *w0 = p.b + ((size_t)ad * p.M + min(m0 + g, p.M - 1)) * p.rank;
+                const uint16_t *w1 = p.b + ((size_t)ad * p.M + min(m0 + g + 8, p.M - 1)) * p.rank;
+                for (int c = 0; c < chunks; ++c) {
+                    const int k = 32 * c + 8 * t4;
+                    const bool in = k < p.rank;
+                    const uint4 lo = in ? ld_once(w0 + k) : zero, hi = in ? ld_once(w1 + k) : zero;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        if (!(who >> (8 * b) & 0xFF)) continue;
+                        const bool mine = who >> (8 * b + g) & 1;
+                        const uint16_t *u = p.u + ((size_t)(tile.row0 + 8 * b + g) * chunks + c) * 64 + 8 * t4;
+                        mma32<BF>(acc[0][b], lo, hi, mine ? *(const uint4 *)u : zero);
+                        mma32<BF>(acc[0][b], lo, hi, mine ? *(const uint4 *)(u + 32) : zero);
+                    }
+                }
+            }
+        }
+        // ---------------- the warps' sums
+#pragma unroll
+        for (int m = 0; m < MATS; ++m)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) red[warp][m][8 * b + 2 * t4 + (i & 1)][g + 4 * (i & 2)] = acc[m][b][i];
+        __syncthreads();
+        for (int i = tid; i < tile.n * 8; i += GF_THREADS) {
+            const int c = i >> 3, r = 2 * (i & 7), o = m0 + r;
+            float2 v[MATS];
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) {
+                v[m] = *(const float2 *)&red[0][m][c][r];
+#pragma unroll
+                for (int k = 1; k < GF_WARPS; ++k) {
+                    const float2 a = *(const float2 *)&red[k][m][c][r];
+                    v[m] = make_float2(v[m].x + a.x, v[m].y + a.y);
+                }
+            }
+            float2 z = v[0];
+            if (MODE == GP_SWIGLU) z = make_float2(mx4_swiglu<true>(v[0].x, v[MATS - 1].x), mx4_swiglu<true>(v[0].y, v[MATS - 1].y));
+            z = make_float2(s_scale[c] * z.x, s_scale[c] * z.y);
+            if (o < p.M && s_y[c]) {
+                if (p.ytype == MOE_F32) *(float2 *)(s_y[c] + 4 * (size_t)o) = z;
+                else if (p.ytype == MOE_BF16) *(uint32_t *)(s_y[c] + 2 * (size_t)o) = grouped_pack<MOE_BF16>(z.x, z.y);
+                else *(uint32_t *)(s_y[c] + 2 * (size_t)o) = grouped_pack<MOE_F16>(z.x, z.y);
+            }
+        }
+        __syncthreads();
+    }
+    if (MODE == GP_LORA && !waited) pdl_wait();
+}
+
+template <int MODE, bool BF, int NB>
+int launch(const GroupedFewParams &p, cudaStream_t s) {
+    const long long tiles = (long long)p.R / (8 * NB) + std::min(p.G, p.R), items = tiles * ((p.M + GF_ROWS - 1) / GF_ROWS);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    moe_pdl_config(&cfg, attr, dim3((unsigned)std::min<long long>(items, 2LL * std::max(1, grouped_sms()))), dim3(GF_THREADS), 0, s);
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, grouped_few_kernel<MODE, BF, NB>, p));
+    return MOE_OK;
+}
+
+}  // namespace
+
+int grouped_few_launch(const GroupedFewParams &p, int mode, bool bf, cudaStream_t s) {
+    if (mode == GP_NK) return bf ? launch<GP_NK, true, 1>(p, s) : launch<GP_NK, false, 1>(p, s);
+    if (mode == GP_SWIGLU) return bf ? launch<GP_SWIGLU, true, 1>(p, s) : launch<GP_SWIGLU, false, 1>(p, s);
+    if (p.R <= 8) return bf ? launch<GP_LORA, true, 1>(p, s) : launch<GP_LORA, false, 1>(p, s);
+    return bf ? launch<GP_LORA, true, 4>(p, s) : launch<GP_LORA, false, 4>(p, s);
+}

@@ -396,6 +396,36 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     MOE_CHECK((((uintptr_t)x | (uintptr_t)w | (uintptr_t)a | (uintptr_t)b | (uintptr_t)y) & 15) == 0);
     MOE_CHECK(((uintptr_t)workspace & 255) == 0);
 
+    int *status = moe_status_word_device_ptr();
+    rc = T <= LS_FEW ? shrink_few(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, s)
+                     : shrink_many(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, status, s);
+    if (rc != MOE_OK) return rc;
+    // few tokens, and no more rows of W than CTAs run at once (N = 2816: 1 token 12.1 -> 8.4 us, 32 tokens 20.2 -> 12.4 by the
+    // kernel for few rows; N = 11264: 15.1 -> 14.9 and 21.1 -> 29.9)
+    const bool few = T <= GF_MAX_R && (N + 15) / 16 <= 2 * grouped_sms();
+    if (few) {
+        GroupedFewParams f = {};
+        f.x = (const uint16_t *)x;
+        f.w = (const uint16_t *)w;
+        f.ldx = ldx;
+        f.G = 1;
+        f.R = T;
+        f.x_share = 1;
+        f.x_rows = T;
+        f.y_rows = T;
+        f.y = y;
+        f.ldy = ldy;
+        f.ytype = ytype;
+        f.M = N;
+        f.K = K;
+        f.adapter = adapter;
+        f.b = (const uint16_t *)b;
+        f.u = (const uint16_t *)workspace;
+        f.n_adapters = n_adapters;
+        f.rank = rank;
+        f.status = status;
+        return grouped_few_launch(f, GP_LORA, type == MOE_BF16, moe_cuda_stream(s));
+    }
     const int chunks = (rank + 31) / 32;
     GroupedParams p = {};
     {
@@ -430,11 +460,8 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     p.n_adapters = n_adapters;
     p.rank = rank;
     p.fmt = type == MOE_BF16;
-    p.status = moe_status_word_device_ptr();
+    p.status = status;
 
-    rc = T <= LS_FEW ? shrink_few(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, s)
-                     : shrink_many(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, p.status, s);
-    if (rc != MOE_OK) return rc;
     const bool wide = T > 32;
     const long long tiles = wide ? (T + 255) / 256 : (T + 31) / 32;
     return grouped_launch(p, ytype, GP_LORA, wide, tiles * ((N + 127) / 128), (K + 63) / 64 + std::min(T, n_adapters) * chunks,
