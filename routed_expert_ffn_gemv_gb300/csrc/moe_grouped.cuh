@@ -297,14 +297,20 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         it.steps = ((GRAD ? v.w : p.K) + 63) / 64;
         return it;
     };
-    // GP_LORA: this lane's share of the tile's adapters (-1: none)
-    auto tile_adapters = [&](const GroupedItem &it, int (&ids)[8]) {
+    // GP_LORA: this lane's share of the tile's adapters (-1: none).  Read before an item's stages, looked at behind them.
+    auto read_adapters = [&](const GroupedItem &it, int (&ids)[8]) {
+        if (MODE == GP_LORA)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = lane + 32 * i;
+                ids[i] = c < it.n ? p.adapter[it.row0 + c] : -1;
+            }
+    };
+    auto check_adapters = [&](int (&ids)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int c = lane + 32 * i;
-            const int a = c < it.n ? p.adapter[it.row0 + c] : -1;
-            if (a >= p.n_adapters || a < -1) moe_set_status(p.status, MOE_ERR_INVALID);
-            ids[i] = a < p.n_adapters ? a : -1;
+            if (ids[i] >= p.n_adapters || ids[i] < -1) moe_set_status(p.status, MOE_ERR_INVALID);
+            if (ids[i] >= p.n_adapters) ids[i] = -1;
         }
     };
     const int chunks = MODE == GP_LORA ? (p.rank + 31) / 32 : 1;
@@ -335,7 +341,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         for (int j = 0; j < n_mine && ok; ++j) {
             const GroupedItem it = item_at(j);
             const int nb = it.npad / CG, m0 = (it.m * CG + rank) * MROWS;
-            int lo, hi;
+            int lo, hi, ids[8];
+            read_adapters(it, ids);
             share(it.steps, lo, hi);
             for (int kb = lo; kb < hi; ++kb, ++gs) {
                 if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
@@ -361,8 +368,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 }
             }
             if (MODE == GP_LORA && ok) {
-                int ids[8], e = 0;
-                tile_adapters(it, ids);
+                int e = 0;
+                check_adapters(ids);
                 share(extra_stages(ids), lo, hi);
                 for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a))
                     for (int c = 0; c < chunks; ++c, ++e) {
@@ -396,7 +403,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         for (int j = 0; j < n_mine && ok; ++j) {
             const GroupedItem it = item_at(j);
             const int nb = it.npad / CG, c0 = it.row0 + rank * nb;
-            int lo, hi, elo, ehi;
+            int lo, hi, elo, ehi, ids[8];
+            read_adapters(it, ids);
             share(it.steps, lo, hi);
             for (int kb = lo; kb < hi; ++kb, ++gs) {
                 if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
@@ -417,8 +425,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 }
             }
             if (MODE == GP_LORA) {  // (the loaders' stages)
-                int ids[8];
-                tile_adapters(it, ids);
+                check_adapters(ids);
                 share(extra_stages(ids), elo, ehi);
                 for (int e = elo; e < ehi; ++e, ++gs) {
                     if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
@@ -475,7 +482,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 it = item_at(j);
             }
             const int nb = it.npad / CG;
-            int lo, hi;
+            int lo, hi, ids[8];
+            read_adapters(it, ids);
             share(it.steps, lo, hi);
             if (!GRAD) {
                 // eight threads a row: piece lt % 8 of rows lt / 8 + 16 i
@@ -483,12 +491,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 const int piece = lt & 7, r0 = lt >> 3, rows = min(nb, it.n - rank * nb);
                 const uint32_t at = smem_u32(ring) + GP_ABYTES + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
                 const uint16_t *src[RI];
-                int who[RI];  // bytes to copy; GP_LORA, later: the token's adapter
+                int who[RI];  // bytes to copy; GP_LORA: the token's adapter
 #pragma unroll
                 for (int i = 0; i < RI; ++i) {
                     const int c = r0 + 16 * i;
                     const int r = c >= rows || MODE == GP_LORA ? -1 : source(it.row0 + rank * nb + c);
-                    who[i] = r >= 0 ? 16 : 0;
+                    who[i] = MODE == GP_LORA ? (c < rows ? p.adapter[it.row0 + rank * nb + c] : -1) : r >= 0 ? 16 : 0;
                     src[i] = p.rows + (size_t)max(r, 0) * p.ld + 8 * piece + 64 * (lo + (team != (gs & 1)));
                 }
                 for (int kb = lo; kb < hi; ++kb, next()) {
@@ -507,12 +515,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 }
                 if (MODE == GP_LORA && ok) {
                     if (j == 0) pdl_wait();  // u
-                    int ids[8], e = 0;
-                    tile_adapters(it, ids);
+                    int e = 0;
+                    check_adapters(ids);
                     share(extra_stages(ids), lo, hi);
-#pragma unroll
-                    for (int i = 0; i < RI; ++i)
-                        who[i] = r0 + 16 * i < rows ? p.adapter[it.row0 + rank * nb + r0 + 16 * i] : -1;
                     const uint16_t *u = p.rows + (size_t)(it.row0 + rank * nb + r0) * p.ld + 8 * piece;
                     for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF && ok; a = grouped_next_adapter(ids, a))
                         for (int c = 0; c < chunks; ++c, ++e) {
@@ -577,16 +582,19 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         bool ok = true;
         for (int j = 0; j < n_mine && ok; ++j) {
             const GroupedItem it = item_at(j);
-            int lo, hi, n = 0;
+            int lo, hi, ids[8];
+            read_adapters(it, ids);
             share(it.steps, lo, hi);
-            n = hi - lo;
-            if (MODE == GP_LORA) {
-                int ids[8];
-                tile_adapters(it, ids);
-                share(extra_stages(ids), lo, hi);
-                n += hi - lo;
-            }
-            for (int kb = 0; kb < n; ++kb) {
+            bool extra = MODE != GP_LORA;
+            for (int kb = lo;; ++kb) {
+                if (kb >= hi) {
+                    if (extra) break;
+                    extra = true;
+                    check_adapters(ids);
+                    share(extra_stages(ids), lo, hi);
+                    kb = lo;
+                    if (kb >= hi) break;
+                }
                 if (!(ok = mbar_wait_warp(&landed[st], ph, p.status, abort_flag))) break;
                 fence_proxy_async_smem();
                 if (lane == 0) {
@@ -610,7 +618,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             // the MMA wants its operands)
             const uint32_t idesc = umma_idesc_16(p.fmt, A_MN, B_MN, 128 * CG, __shfl_sync(0xffffffffu, it.npad, 0));
             const int buf = j & 1;
-            int lo, hi;
+            int lo, hi, ids[8];
+            read_adapters(it, ids);
             share(__shfl_sync(0xffffffffu, it.steps, 0), lo, hi);
             bool fresh = true;  // nothing summed yet
             if (j >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((j / 2) - 1) & 1, p.status, abort_flag))) break;
@@ -645,8 +654,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 }
             }
             if (MODE == GP_LORA) {
-                int ids[8];
-                tile_adapters(it, ids);
+                check_adapters(ids);
                 share(__shfl_sync(0xffffffffu, extra_stages(ids), 0), lo, hi);
             }
             for (int e = lo, c = MODE == GP_LORA ? lo % chunks : 0; MODE == GP_LORA && e < hi && ok; ++e) {
@@ -743,7 +751,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 n = hi - lo;
                 if (MODE == GP_LORA) {
                     int ids[8];
-                    tile_adapters(it, ids);
+                    read_adapters(it, ids);
+                    check_adapters(ids);
                     share(extra_stages(ids), lo, hi);
                     n += hi - lo;
                 }
