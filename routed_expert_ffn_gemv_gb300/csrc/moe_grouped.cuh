@@ -48,6 +48,7 @@ struct GroupedParams {
     CUtensorMap ab;           // GP_LORA: the adapters' B
     const uint16_t *rows;     // x; GP_LORA: u
     const uint16_t *dy;       // GP_GRAD
+    const uint16_t *lora_b;   // GP_LORA: the adapters' B
     size_t ld, lddy;
     const int32_t *offsets;   // [G + 1], or NULL: one group of R rows
     int G, R;
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     uint64_t *red_full = mma_done + 1;
     uint32_t *tmem_slot = (uint32_t *)(red_full + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
+    volatile int *bad_item = (volatile int *)(tmem_slot + 2);  // GP_LORA: 1 + the last item with a b that is not finite
     int *sums = (int *)(tmem_slot + 4);                       // [20]
     int *off = (int *)(smem + G_::O_OFF);                     // [G + 1]
     int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before those of the i-th group ..
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1 + (loaders ? CG : 0));
-            mbar_init(&landed[s], 128);
+            mbar_init(&landed[s], 128 + (MODE == GP_LORA));
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -191,6 +193,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         mbar_init(mma_done, 1);
         mbar_init(red_full, 1);
         *abort_flag = 0;
+        *bad_item = 0;
         fence_mbar_init();
     }
     if (warp == 2) tmem_alloc_group<CG>(tmem_slot, G_::TCOLS);
@@ -352,6 +355,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 const bool box_a = GRAD ? whole && !p.x_index : true, box_b = GRAD ? whole && !p.y_index : !p.x_index;
                 if (rank == 0)
                     mbar_arrive_expect_tx_elect(&full[st], CG * ((box_a ? GP_ABYTES : 0u) + (box_b ? nb * 128u : 0u)));
+                if (MODE == GP_LORA && lane == 0) mbar_arrive1(&landed[st]);
                 if (MODE == GP_NK || MODE == GP_LORA) {
                     if (lane == 0) tma_tile_3d<CG>(dst, &p.a, kb * 64, m0, MODE == GP_LORA ? 0 : it.g, bar);
                 } else if (MODE == GP_KN) {
@@ -375,10 +379,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     for (int c = 0; c < chunks; ++c, ++e) {
                         if (e < lo || e >= hi) continue;
                         if (gs >= S && !(ok = mbar_wait_warp(&empty[st], ph, p.status, abort_flag))) break;
-                        uint8_t *dst = ring + (size_t)st * G_::STAGE;
-                        const uint32_t bar = CG == 1 ? smem_u32(&full[st]) : cluster_map(&full[st], 0);
-                        if (rank == 0) mbar_arrive_expect_tx_elect(&full[st], CG * GP_UBYTES);
-                        if (lane == 0) tma_tile_3d<CG>(dst, &p.ab, c * 32, m0, a, bar);
+                        // (the adapter's B goes through the hands of warp 3, as u does: the leader's barrier counts no bytes)
+                        if (rank == 0 && lane == 0) mbar_arrive1(&full[st]);
+                        mbar_arrive_expect_tx_elect(&landed[st], GP_UBYTES);
+                        if (lane == 0)
+                            tma_tile_3d<CG>(ring + (size_t)st * G_::STAGE, &p.ab, c * 32, m0, a, smem_u32(&landed[st]));
                         __syncwarp();
                         ++gs;
                         if (++st == S) {
@@ -596,7 +601,32 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     if (kb >= hi) break;
                 }
                 if (!(ok = mbar_wait_warp(&landed[st], ph, p.status, abort_flag))) break;
+                if (MODE == GP_LORA && extra) {
+                    // The tile's other tokens have zeros for u here, which an infinity or a NaN in b would turn to NaN: rows of
+                    // 32 ranks with one of them become zeros, and the epilogue adds them to this adapter's tokens
+                    const uint32_t most = p.fmt ? 0x7F807F80u : 0x7C007C00u, at = smem_u32(ring) + (uint32_t)st * G_::STAGE;
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t row = at + (lane + 32 * i) * 64;
+                        uint32_t bad = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint4 v = ld_shared_16(row + (((k + (lane >> 1)) & 3) << 4));
+                            bad |= __vcmpeq2(v.x & most, most) | __vcmpeq2(v.y & most, most) | __vcmpeq2(v.z & most, most) |
+                                   __vcmpeq2(v.w & most, most);
+                        }
+                        if (bad) {
+                            any = true;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) st_shared_16(row + 16 * k, make_uint4(0, 0, 0, 0));
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, any) && lane == 0) *bad_item = j + 1;
+                    __syncwarp();
+                }
                 fence_proxy_async_smem();
+                __syncwarp();
                 if (lane == 0) {
                     if (CG == 1) mbar_arrive1(&full[st]);
                     else mbar_arrive_cluster(cluster_map(&full[st], 0));
@@ -717,6 +747,21 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 moe_set_status(p.status, MOE_ERR_INVALID);
             }
         };
+        // GP_LORA: 32 ranks (chunk c) of adapter a for output o of token t, where b is not finite among them, else 0
+        auto not_finite = [&](int a, int c, int o, int t) -> float {
+            const uint16_t *b = p.lora_b + ((size_t)a * p.M + o) * p.rank, *u = p.rows + (size_t)t * p.ld + c * 64;
+            auto value = [&](uint16_t h) -> float {
+                return p.fmt ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+            };
+            float s = 0.f;
+            bool bad = false;
+            for (int k = 0; k < 32 && 32 * c + k < p.rank; ++k) {
+                const float v = value(b[32 * c + k]);
+                bad |= !(fabsf(v) <= 3.4028235e38f);
+                s = fmaf(v, value(u[k]) + value(u[32 + k]), s);
+            }
+            return bad ? s : 0.f;
+        };
         GroupedItem it = {};
         if (n_mine) {
             it = item_at(0);
@@ -746,11 +791,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             if (CG == 1 && ks > 1) {
                 // the cluster's only item: each CTA adds up its share of the rows, `per` of them (the last ones fewer)
                 const int per = (it.n + ks - 1) / ks, own = max(0, min(per, it.n - kr * per));
-                int lo, hi, n;
+                int lo, hi, n, ids[8];
                 share(it.steps, lo, hi);
                 n = hi - lo;
                 if (MODE == GP_LORA) {
-                    int ids[8];
                     read_adapters(it, ids);
                     check_adapters(ids);
                     share(extra_stages(ids), lo, hi);
@@ -764,6 +808,15 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 16; ++k) x[(16 * half + k) * 128 + 32 * q + lane] = n ? __uint_as_float(v[k]) : 0.f;
+                }
+                if (MODE == GP_LORA && *bad_item > j) {
+                    int e = 0;
+                    for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a))
+                        for (int c = 0; c < chunks; ++c, ++e)
+                            if (e >= lo && e < hi && m0 + lane < p.M)
+                                for (int k = 16 * half; k < min(it.n, 16 * half + 16); ++k)
+                                    if (p.adapter[it.row0 + k] == a)
+                                        x[k * 128 + 32 * q + lane] += not_finite(a, c, m0 + lane, it.row0 + k);
                 }
                 fence_proxy_async_smem();
                 if (et == 0 && own) mbar_arrive_expect_tx(red_full, (uint32_t)(own * ks) * 512u);
@@ -908,6 +961,21 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         if (c0 + c < it.n && m < p.M && ys[c0 + c]) *(uint4 *)(ys[c0 + c] + 2 * (size_t)m) = a;
                     }
                     __syncwarp();
+                }
+                if (MODE == GP_LORA && *bad_item > j) {
+                    __syncwarp();
+                    for (int c0 = CH * half; c0 < it.n; c0 += 2 * CH)
+                        for (int c = c0; c < min(it.n, c0 + CH); ++c) {
+                            const int a = p.adapter[it.row0 + c];
+                            if (a < 0 || a >= p.n_adapters || m0 + lane >= p.M || !ys[c]) continue;
+                            float s = 0.f;
+                            for (int k = 0; k < chunks; ++k) s += not_finite(a, k, m0 + lane, it.row0 + c);
+                            if (s != 0.f) {  // (or NaN)
+                                uint8_t *o = ys[c] + (size_t)SIZE * (m0 + lane);
+                                if (F32) *(float *)o += s;
+                                else *(uint16_t *)o = (uint16_t)grouped_pack<OT>(grouped_unpack<OT>(*(uint16_t *)o).x + s, 0.f);
+                            }
+                        }
                 }
             }
             tc_fence_before();

@@ -192,6 +192,8 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
                 const unsigned who = __ballot_sync(0xffffffffu, id == ad);
                 const uint16_t *w0 = p.b + ((size_t)ad * p.M + min(m0 + g, p.M - 1)) * p.rank;
                 const uint16_t *w1 = p.b + ((size_t)ad * p.M + min(m0 + g + 8, p.M - 1)) * p.rank;
+                // sums of their own: an infinity or a NaN in b, times the zeros of the other tokens, stays out of theirs
+                float part[NB][4] = {};
                 for (int c = 0; c < chunks; ++c) {
                     const int k = 32 * c + 8 * t4;
                     const bool in = k < p.rank;
@@ -201,10 +203,15 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
                         if (!(who >> (8 * b) & 0xFF)) continue;
                         const bool mine = who >> (8 * b + g) & 1;
                         const uint16_t *u = p.u + ((size_t)(tile.row0 + 8 * b + g) * chunks + c) * 64 + 8 * t4;
-                        mma32<BF>(acc[0][b], lo, hi, mine ? *(const uint4 *)u : zero);
-                        mma32<BF>(acc[0][b], lo, hi, mine ? *(const uint4 *)(u + 32) : zero);
+                        mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)u : zero);
+                        mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)(u + 32) : zero);
                     }
                 }
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (who >> (8 * b + 2 * t4 + (i & 1)) & 1) acc[0][b][i] += part[b][i];
             }
         }
         // ---------------- the warps' sums

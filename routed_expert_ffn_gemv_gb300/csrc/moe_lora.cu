@@ -21,16 +21,19 @@ __device__ __forceinline__ float2 pair_value(uint32_t w) {
     if (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     return __half22float2(*(const __half2 *)&w);
 }
+// v as two 16-bit numbers (one that overflows: as the infinity alone).
 template <bool BF>
 __device__ __forceinline__ void split16(float v, uint16_t &hi, uint16_t &lo) {
     if (BF) {
-        const __nv_bfloat16 h = __float2bfloat16_rn(v), l = __float2bfloat16_rn(v - __bfloat162float(h));
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        const float f = __bfloat162float(h);
         hi = __bfloat16_as_ushort(h);
-        lo = __bfloat16_as_ushort(l);
+        lo = __bfloat16_as_ushort(__float2bfloat16_rn(isinf(f) ? 0.f : v - f));
     } else {
-        const __half h = __float2half_rn(v), l = __float2half_rn(v - __half2float(h));
+        const __half h = __float2half_rn(v);
+        const float f = __half2float(h);
         hi = __half_as_ushort(h);
-        lo = __half_as_ushort(l);
+        lo = __half_as_ushort(__float2half_rn(isinf(f) ? 0.f : v - f));
     }
 }
 
@@ -447,6 +450,7 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     }
     p.rows = (const uint16_t *)workspace;
     p.ld = (size_t)chunks * 64;
+    p.lora_b = (const uint16_t *)b;
     p.G = 1;
     p.R = T;
     p.x_rows = T;
