@@ -153,7 +153,7 @@ extern "C" int moe_grouped_matmul(const void *x, int type, int x_rows, size_t ld
     p.status = moe_status_word_device_ptr();
     // few rows to a group: narrow tiles, one CTA each
     const bool wide = R > 16LL * G;
-    const int nt = wide ? 256 : 32, mrows = (swiglu ? 64 : 128) * (wide ? 2 : 1);
+    const int nt = !wide ? 32 : ytype == MOE_F32 ? 128 : 256, mrows = (swiglu ? 64 : 128) * (wide ? 2 : 1);
     const long long row_tiles = (long long)R / nt + std::min(G, R);
     return grouped_launch(p, ytype, mode, wide, row_tiles * ((N + mrows - 1) / mrows), (K + 63) / 64, moe_cuda_stream(s));
 }
@@ -198,6 +198,7 @@ extern "C" int moe_grouped_weight_grad(const void *x, int type, int x_rows, size
     p.accumulate = accumulate;
     p.fmt = type == MOE_BF16;
     p.status = moe_status_word_device_ptr();
-    const long long items = (long long)G * ((N + 255) / 256) * ((K + 255) / 256);
+    const int nt = wtype == MOE_F32 ? 128 : 256;
+    const long long items = (long long)G * ((N + nt - 1) / nt) * ((K + 255) / 256);
     return grouped_launch(p, wtype, GP_GRAD, true, items, 0, moe_cuda_stream(s));
 }

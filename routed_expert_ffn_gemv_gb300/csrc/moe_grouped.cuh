@@ -59,6 +59,7 @@ struct GroupedParams {
     const float *scale;       // [y_rows] or NULL
     void *y;
     size_t ldy;               // GP_GRAD: M
+    int accs;                 // fp32 results: most accumulators of an item
     int M, K, N;              // columns of an output row; reduction (not GP_GRAD); GP_GRAD: output rows of a group
     int accumulate;           // GP_GRAD
     const int32_t *adapter;   // GP_LORA, [R]
@@ -70,13 +71,20 @@ struct GroupedParams {
 #define GP_ITEMS 96       // items of a CTA that are worked out ahead, in shared memory
 #define GP_MAX_SPLIT 8    // CTAs that share an item's reduction
 
-template <int CG, int NT>
+// A sum on the tensor cores drops, at each of its steps of 16, what lies below the last bit of the larger term: 128 steps
+// (K = 2048) leave it 1.6e-6 off, relative to the result's norm, which bf16 and fp16 results do not show and fp32 results do
+// (fp32 sums rounded to nearest: 1.5e-7).  For fp32 results the stages are therefore shared out over several accumulators,
+// ACC_STAGES stages or more each, that the epilogue adds up in order (32 steps each: 4.7e-7).
+
+template <int CG, int NT, int OT>
 struct GroupedGeom {
     static constexpr int GRAN = 16 * CG;                     // rows an MMA's width is rounded up to
     static constexpr int BBYTES = NT / CG * 128;
     static constexpr int STAGE = GP_ABYTES + BBYTES;
-    static constexpr int TCOLS = 2 * NT < 32 ? 32 : 2 * NT;  // two accumulators
-    static constexpr int CH = NT >= 64 ? 32 : 16;            // columns of an epilogue warp's chunk
+    static constexpr int SLOTS = OT == MOE_F32 ? 512 / NT : 2;  // accumulators in tensor memory
+    static constexpr int TCOLS = SLOTS * NT;                 // (a power of two from 32 on)
+    static constexpr int ACC_STAGES = NT <= 32 ? 4 : 8;
+    static constexpr int CH = NT >= 64 && OT != MOE_F32 ? 32 : 16;  // columns of an epilogue warp's chunk
     static constexpr int XCH = CH * 80 < 2304 ? 2304 : CH * 80;  // bytes of an epilogue warp
     // CG = 1: partial sums of up to GP_MAX_SPLIT CTAs, for this CTA's share of the rows
     static constexpr int RED = CG == 1 ? (NT + GP_MAX_SPLIT - 1) * 512 : 0;
@@ -149,11 +157,11 @@ __device__ __forceinline__ int grouped_next_adapter(const int (&ids)[8], int las
 // OT: y's type
 template <int CG, int NT, int MODE, int OT>
 __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
-    using G_ = GroupedGeom<CG, NT>;
+    using G_ = GroupedGeom<CG, NT, OT>;
     constexpr int S = G_::S;
     constexpr bool GRAD = MODE == GP_GRAD, A_MN = GRAD || MODE == GP_KN, B_MN = GRAD;
     constexpr int MROWS = MODE == GP_SWIGLU ? 64 : 128;  // output columns of a CTA's tile
-    static_assert(!GRAD || NT / CG == 128, "sixteen pieces of eight columns");
+    static_assert(!GRAD || NT / CG <= 128, "sixteen pieces of eight columns");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     uint64_t *full = (uint64_t *)smem;
@@ -202,6 +210,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     if (CG == 2 || ks > 1) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // accumulators of an item, and items in tensor memory
+    const int accs = OT == MOE_F32 ? min(p.accs, G_::SLOTS) : 1, bufs = 2 * accs <= G_::SLOTS ? 2 : 1;
+    // stages of an accumulator, of n (GP_LORA's extra ones go to the last one)
+    auto acc_stages = [&](int n) -> int { return accs == 1 ? max(n, 1) : max((n + accs - 1) / accs, G_::ACC_STAGES); };
     // (GP_LORA: the kernel in front computes u and nothing else; it starts this one when everything before it is
     // complete, and only u is waited for, by the warp that loads it)
     if (MODE != GP_LORA) pdl_wait();
@@ -647,21 +659,29 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             // (a value that a shuffle hands out is known to be the same in every lane: it stays in a uniform register, where
             // the MMA wants its operands)
             const uint32_t idesc = umma_idesc_16(p.fmt, A_MN, B_MN, 128 * CG, __shfl_sync(0xffffffffu, it.npad, 0));
-            const int buf = j & 1;
+            const int buf = bufs == 2 ? j & 1 : 0, round = bufs == 2 ? j / 2 : j;
             int lo, hi, ids[8];
             read_adapters(it, ids);
             share(__shfl_sync(0xffffffffu, it.steps, 0), lo, hi);
             bool fresh = true;  // nothing summed yet
-            if (j >= 2 && !(ok = mbar_wait_warp(&acc_empty[buf], ((j / 2) - 1) & 1, p.status, abort_flag))) break;
+            if (round >= 1 && !(ok = mbar_wait_warp(&acc_empty[buf], (round - 1) & 1, p.status, abort_flag))) break;
             tc_fence_after();
-            const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + buf * NT;
+            uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + buf * accs * NT;
             const int len = GRAD ? __shfl_sync(0xffffffffu, it.cnt, 0) : p.K;
+            const int per = __shfl_sync(0xffffffffu, acc_stages(hi - lo), 0);
+            int left_in_acc = per;
             for (int kb = lo; kb < hi; ++kb) {
                 if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
                 tc_fence_after();
                 const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
                 const uint64_t a = A_MN ? umma_desc_mn_sw128(sa, 8192) : umma_desc_sw128(sa);
                 const uint64_t b = B_MN ? umma_desc_mn_sw128(sa + GP_ABYTES, 8192) : umma_desc_sw128(sa + GP_ABYTES);
+                if (OT == MOE_F32 && left_in_acc == 0) {
+                    left_in_acc = per;
+                    d += NT;
+                    fresh = true;
+                }
+                --left_in_acc;
                 const int left = len - 64 * kb;
                 auto step = [&](int q) {
                     umma_f16_elect<CG>(d, a + (uint64_t)(q * (A_MN ? 128 : 2)), b + (uint64_t)(q * (B_MN ? 128 : 2)), idesc,
@@ -747,6 +767,13 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 moe_set_status(p.status, MOE_ERR_INVALID);
             }
         };
+        auto add16 = [&](uint32_t (&v)[16], uint32_t at) {  // another accumulator
+            uint32_t u[16];
+            tmem_ld16(at, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(u[k]));
+        };
         // GP_LORA: 32 ranks (chunk c) of adapter a for output o of token t, where b is not finite among them, else 0
         auto not_finite = [&](int a, int c, int o, int t) -> float {
             const uint16_t *b = p.lora_b + ((size_t)a * p.M + o) * p.rank, *u = p.rows + (size_t)t * p.ld + c * 64;
@@ -769,7 +796,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             resolve(it);
         }
         for (int j = 0; j < n_mine; ++j) {
-            const int buf = j & 1;
+            const int buf = j & 1, abuf = bufs == 2 ? buf : 0, round = bufs == 2 ? j / 2 : j;
             if (et < NT) {
                 e_y[buf * NT + et] = row;
                 e_s[buf * NT + et] = scale;
@@ -779,11 +806,18 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 nx = item_at(j + 1);
                 fetch(nx);
             }
-            const bool w = mbar_wait_role(&acc_full[buf], (j / 2) & 1, p.status, abort_flag);
+            const bool w = mbar_wait_role(&acc_full[abuf], round & 1, p.status, abort_flag);
             if (!bar_and_n(1, 256, w)) break;
             if (j + 1 < n_mine) resolve(nx);
             tc_fence_after();
-            const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + buf * NT;
+            const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + abuf * accs * NT;
+            int used = 1;  // accumulators
+            if (OT == MOE_F32) {
+                int lo, hi;
+                share(it.steps, lo, hi);
+                const int per = acc_stages(hi - lo);
+                used = max(1, (hi - lo + per - 1) / per);
+            }
             uint8_t *const *ys = e_y + buf * NT;
             const float *ss = e_s + buf * NT;
             const bool none = GRAD && !it.steps;
@@ -806,6 +840,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     uint32_t v[16];
                     tmem_ld16(tb + 16 * half, v);
                     tmem_ld_wait();
+                    for (int a = 1; a < used; ++a) add16(v, tb + a * NT + 16 * half);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) x[(16 * half + k) * 128 + 32 * q + lane] = n ? __uint_as_float(v[k]) : 0.f;
                 }
@@ -861,6 +896,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
 #pragma unroll
                         for (int h = 0; h < CH / 16; ++h) tmem_ld16(tb + c0 + 16 * h, v[h]);
                         tmem_ld_wait();
+                        for (int a = 1; a < used; ++a)
+#pragma unroll
+                            for (int h = 0; h < CH / 16; ++h) add16(v[h], tb + a * NT + c0 + 16 * h);
                         float *x = (float *)(smem + G_::O_XCH + ew * G_::XCH);  // padded to 36: no bank conflicts
                         const int m = m0 + 4 * (lane & 7);
 #pragma unroll
@@ -891,6 +929,17 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     tmem_ld_16x256b(tb + c0, lo);
                     tmem_ld_16x256b(tb + (16u << 16) + c0, hi);
                     tmem_ld_wait();
+                    for (int a = 1; a < used; ++a) {  // (F32)
+                        uint32_t u[4 * NB];
+                        tmem_ld_16x256b(tb + a * NT + c0, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 4 * NB; ++k) lo[k] = __float_as_uint(__uint_as_float(lo[k]) + __uint_as_float(u[k]));
+                        tmem_ld_16x256b(tb + a * NT + (16u << 16) + c0, u);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 4 * NB; ++k) hi[k] = __float_as_uint(__uint_as_float(hi[k]) + __uint_as_float(u[k]));
+                    }
                     const int cq = c0 + 2 * (lane & 3);
                     if (none)
 #pragma unroll
@@ -981,8 +1030,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (CG == 1) mbar_arrive1(&acc_empty[buf]);
-                else mbar_arrive_cluster(cluster_map(&acc_empty[buf], 0));
+                if (CG == 1) mbar_arrive1(&acc_empty[abuf]);
+                else mbar_arrive_cluster(cluster_map(&acc_empty[abuf], 0));
             }
             it = nx;
         }

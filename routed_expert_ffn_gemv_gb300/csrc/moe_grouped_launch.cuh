@@ -7,8 +7,8 @@
 #include "moe_grouped.cuh"
 
 template <int CG, int NT, int MODE, int OT>
-static int grouped_launch_t(const GroupedParams &p, long long items, int stages, cudaStream_t s) {
-    using G = GroupedGeom<CG, NT>;
+static int grouped_launch_t(GroupedParams p, long long items, int stages, cudaStream_t s) {
+    using G = GroupedGeom<CG, NT, OT>;
     static std::mutex mu;
     static bool ready[64] = {false};
     int dev = -1;
@@ -23,6 +23,13 @@ static int grouped_launch_t(const GroupedParams &p, long long items, int stages,
         }
     }
     const int n = std::max(CG, grouped_sms());
+    // fp32 results: as many accumulators as the reduction has use for, all of tensor memory for one item if it is long (GP_GRAD,
+    // whose reductions differ by group: if they are over 512 rows on average)
+    p.accs = 1;
+    if (OT == MOE_F32) {
+        const long long length = MODE == GP_GRAD ? std::max<long long>(G::ACC_STAGES * 64 + 1, 2LL * p.R / p.G) : p.K;
+        while (p.accs < G::SLOTS && p.accs * G::ACC_STAGES * 64 < length) p.accs *= 2;
+    }
     items = std::max(1LL, items);
     int cluster = CG;
     // CG = 1: as many CTAs to an item as there are SMs for, each with four stages of the reduction at least
@@ -40,21 +47,23 @@ static int grouped_launch_t(const GroupedParams &p, long long items, int stages,
     return MOE_OK;
 }
 
+// Pairs: tiles of 256 rows; of 128 with fp32 results, so that tensor memory holds four accumulators.
 template <int OT>
 static int grouped_launch_modes(const GroupedParams &p, int mode, bool wide, long long items, int stages, cudaStream_t s) {
+    constexpr int WIDE = OT == MOE_F32 ? 128 : 256;
     switch (mode) {
         case GP_NK:
-            return wide ? grouped_launch_t<2, 256, GP_NK, OT>(p, items, stages, s)
+            return wide ? grouped_launch_t<2, WIDE, GP_NK, OT>(p, items, stages, s)
                         : grouped_launch_t<1, 32, GP_NK, OT>(p, items, stages, s);
         case GP_KN:
-            return wide ? grouped_launch_t<2, 256, GP_KN, OT>(p, items, stages, s)
+            return wide ? grouped_launch_t<2, WIDE, GP_KN, OT>(p, items, stages, s)
                         : grouped_launch_t<1, 32, GP_KN, OT>(p, items, stages, s);
         case GP_SWIGLU:
-            return wide ? grouped_launch_t<2, 256, GP_SWIGLU, OT>(p, items, stages, s)
+            return wide ? grouped_launch_t<2, WIDE, GP_SWIGLU, OT>(p, items, stages, s)
                         : grouped_launch_t<1, 32, GP_SWIGLU, OT>(p, items, stages, s);
         case GP_LORA:
-            return wide ? grouped_launch_t<2, 256, GP_LORA, OT>(p, items, stages, s)
+            return wide ? grouped_launch_t<2, WIDE, GP_LORA, OT>(p, items, stages, s)
                         : grouped_launch_t<1, 32, GP_LORA, OT>(p, items, stages, s);
-        default: return grouped_launch_t<2, 256, GP_GRAD, OT>(p, items, stages, s);
+        default: return grouped_launch_t<2, WIDE, GP_GRAD, OT>(p, items, stages, s);
     }
 }

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
         s.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 0) tmem_alloc_group<1>(&s.tmem, LS_COLS);
+    if (warp == 0) tmem_alloc_group<1>(&s.tmem, 2 * LS_COLS);  // two accumulators: see moe_grouped.cuh
     pdl_wait();
     pdl_trigger();
     // ---------------- the tile's adapters, in the order of their first tokens
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
             if (mine >= used) mine = -1;
             s.mine[tid] = max(mine, -1);
         }
-        const int KB = (p.K + 63) / 64, kb0 = KB * me / ctas, kb1 = KB * (me + 1) / ctas;
+        const int KB = (p.K + 63) / 64, kb0 = KB * me / ctas, kb1 = KB * (me + 1) / ctas, second = (kb0 + kb1 + 1) / 2;
         if (warp == 4) {
             // ---------------- copies
             int st = 0;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
             // ---------------- MMAs
             int st = 0;
             uint32_t ph = 0;
-            const uint32_t d = __shfl_sync(0xffffffffu, s.tmem, 0);
+            const uint32_t d0 = __shfl_sync(0xffffffffu, s.tmem, 0);
             const uint32_t idesc = umma_idesc_16(p.fmt, false, false, 128, __shfl_sync(0xffffffffu, (used * p.rank + 15) & ~15, 0));
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait_warp(&s.full[st], ph, p.status, &s.abort)) break;
@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
                 const uint32_t sa = smem_u32(ring) + (uint32_t)st * LS_STAGE;
                 const uint64_t a = umma_desc_sw128(sa), b = umma_desc_sw128(sa + LS_TOKENS * 128);
                 const int left = p.K - 64 * kb;
-                umma_f16_elect<1>(d, a, b, idesc, kb > kb0);
+                const uint32_t d = d0 + (kb >= second ? LS_COLS : 0);
+                umma_f16_elect<1>(d, a, b, idesc, kb > kb0 && kb != second);
                 if (left > 16) umma_f16_elect<1>(d, a + 2, b + 2, idesc, 1);
                 if (left > 32) umma_f16_elect<1>(d, a + 4, b + 4, idesc, 1);
                 if (left > 48) umma_f16_elect<1>(d, a + 6, b + 6, idesc, 1);
@@ -254,6 +255,13 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
                     uint32_t v[8];
                     tmem_ld8(tb + i * p.rank + c, v);
                     tmem_ld_wait();
+                    if (second < kb1) {
+                        uint32_t w[8];
+                        tmem_ld8(tb + LS_COLS + i * p.rank + c, w);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
+                    }
                     if (mine == i) {
                         if (kb0 == kb1)
 #pragma unroll
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
     if (warp == 0) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc_group<1>(s.tmem, LS_COLS);
+        tmem_dealloc_group<1>(s.tmem, 2 * LS_COLS);
     }
 }
 
@@ -467,7 +475,8 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     p.status = status;
 
     const bool wide = T > 32;
-    const long long tiles = wide ? (T + 255) / 256 : (T + 31) / 32;
+    const int nt = !wide ? 32 : ytype == MOE_F32 ? 128 : 256;
+    const long long tiles = (T + nt - 1) / nt;
     return grouped_launch(p, ytype, GP_LORA, wide, tiles * ((N + 127) / 128), (K + 63) / 64 + std::min(T, n_adapters) * chunks,
                           moe_cuda_stream(s));
 }
