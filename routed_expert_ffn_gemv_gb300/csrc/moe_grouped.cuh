@@ -617,24 +617,26 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     // The tile's other tokens have zeros for u here, which an infinity or a NaN in b would turn to NaN: rows of
                     // 32 ranks with one of them become zeros, and the epilogue adds them to this adapter's tokens
                     const uint32_t most = p.fmt ? 0x7F807F80u : 0x7C007C00u, at = smem_u32(ring) + (uint32_t)st * G_::STAGE;
-                    bool any = false;
+                    uint32_t top = 0;  // the largest exponents
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t row = at + (lane + 32 * i) * 64;
-                        uint32_t bad = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint4 v = ld_shared_16(row + (((k + (lane >> 1)) & 3) << 4));
-                            bad |= __vcmpeq2(v.x & most, most) | __vcmpeq2(v.y & most, most) | __vcmpeq2(v.z & most, most) |
-                                   __vcmpeq2(v.w & most, most);
-                        }
-                        if (bad) {
-                            any = true;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) st_shared_16(row + 16 * k, make_uint4(0, 0, 0, 0));
-                        }
+                    for (int i = 0; i < GP_UBYTES / 512; ++i) {
+                        const uint4 v = ld_shared_16(at + i * 512 + lane * 16);
+                        top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & most, v.y & most)), __vmaxu2(v.z & most, v.w & most));
                     }
-                    if (__any_sync(0xffffffffu, any) && lane == 0) *bad_item = j + 1;
+                    const bool any = __any_sync(0xffffffffu, __vcmpeq2(top, most) != 0);
+                    if (any)
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t row = at + (lane + 32 * i) * 64;
+                            uint32_t bad = 0;
+                            for (int k = 0; k < 4; ++k) {
+                                const uint4 v = ld_shared_16(row + 16 * k);
+                                bad |= __vcmpeq2(v.x & most, most) | __vcmpeq2(v.y & most, most) | __vcmpeq2(v.z & most, most) |
+                                       __vcmpeq2(v.w & most, most);
+                            }
+                            if (bad)
+                                for (int k = 0; k < 4; ++k) st_shared_16(row + 16 * k, make_uint4(0, 0, 0, 0));
+                        }
+                    if (any && lane == 0) *bad_item = j + 1;
                     __syncwarp();
                 }
                 fence_proxy_async_smem();

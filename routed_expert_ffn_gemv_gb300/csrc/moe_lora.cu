@@ -474,7 +474,8 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     p.fmt = type == MOE_BF16;
     p.status = status;
 
-    const bool wide = T > 32;
+    // narrow tiles while they are one round of CTAs (64 tokens, N = 2816: 17.7 us against 25.4; 200 tokens 33.6 against 28.8)
+    const bool wide = (T + 31) / 32 * ((N + 127) / 128) > grouped_sms();
     const int nt = !wide ? 32 : ytype == MOE_F32 ? 128 : 256;
     const long long tiles = (T + nt - 1) / nt;
     return grouped_launch(p, ytype, GP_LORA, wide, tiles * ((N + 127) / 128), (K + 63) / 64 + std::min(T, n_adapters) * chunks,

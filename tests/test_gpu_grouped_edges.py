@@ -22,8 +22,9 @@ def status():
 
 # ------------------------------------------------------------------------------ values that are not finite
 
-# few rows (8, 32), a matrix too large for that (split over a cluster), wide tiles
-LORA_PATHS = [(5, 64, 200), (30, 264, 128), (7, 5128, 72), (31, 6400, 64), (40, 136, 72), (300, 520, 64), (600, 128, 520)]
+# few rows (8, 32), a matrix too large for that (split over a cluster), several narrow tiles, wide ones
+LORA_PATHS = [(5, 64, 200), (30, 264, 128), (7, 5128, 72), (31, 6400, 64), (40, 136, 72), (300, 520, 64), (600, 128, 520),
+              (600, 1032, 520), (40, 9736, 64)]
 
 
 @pytest.mark.parametrize("T,N,K", LORA_PATHS)
@@ -94,6 +95,27 @@ def test_broken_rows_and_matrices_stay_in_their_group(order, G, R):
         v, e = ref.product(x[o[i]:o[i + 1]], w[i])
         ref.check(y[o[i]:o[i + 1]], v, ref.rounded(v, e, "f32"), i)
     assert bool(y[o[1]:o[2]].isnan().all()) and not bool(y[o[3]:].isfinite().any())
+
+
+@pytest.mark.parametrize("T,n,rank,N,K", [(300, 5, 128, 2056, 64), (1030, 7, 32, 1160, 2048), (513, 200, 16, 2048, 200),
+                                          (2000, 1, 256, 512, 64), (40, 3, 24, 12000, 72)])
+@pytest.mark.parametrize("t,out", [("bf16", "f32"), ("f16", "f16"), ("bf16", "bf16")])
+def test_lora_in_wide_tiles(T, n, rank, N, K, t, out):
+    rng, g = np.random.default_rng(T + n), gen(T + rank)
+    adapter = rng.integers(-1, n, size=T).astype(np.int32)
+    x, w = rand(g, t, T, K), rand(g, t, N, K, scale=K ** -0.5)
+    a, b = rand(g, t, n, rank, K, scale=K ** -0.5), rand(g, t, n, N, rank, scale=rank ** -0.5)
+    scale = torch.randn(n, generator=g, device="cuda")
+    y = lora(x, t, w, torch.from_numpy(adapter).cuda(), a, b, scale, out)
+    for i in range(-1, n):
+        mine = torch.from_numpy((adapter == i).nonzero()[0]).cuda()
+        if mine.numel():
+            if i < 0:
+                v, e = ref.product(x[mine], w)
+                e = ref.rounded(v, e, out)
+            else:
+                v, e = lora_bound(x[mine], t, w, a[i], b[i], float(scale[i]), out)
+            ref.check(y[mine], v, e, i)
 
 
 # ------------------------------------------------------------------------------ indexes and offsets outside
