@@ -71,9 +71,14 @@ int grouped_map(CUtensorMap *map, int type, int rank, const void *base, const ui
         b[i] = box[i];
         if (i + 1 < rank) st[i] = strides[i];
     }
-    if (enc(map, type == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
-            (void *)base, d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+    if (enc(map,
+            type == MOE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+            : type == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            (cuuint32_t)rank, (void *)base, d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+            : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return MOE_ERR_CUDA;
     return MOE_OK;
@@ -179,6 +184,12 @@ extern "C" int moe_grouped_weight_grad(const void *x, int type, int x_rows, size
     GroupedParams p = {};
     if ((rc = rows_map(&p.a, type, x, x_rows, K, ldx, 64)) != MOE_OK) return rc;
     if ((rc = rows_map(&p.b, type, dy, dy_rows, N, lddy, 64)) != MOE_OK) return rc;
+    {
+        const uint64_t size = type_bytes(wtype), dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)G};
+        const uint64_t strides[2] = {K * size, (uint64_t)N * K * size};
+        const uint32_t box[3] = {32, wtype == MOE_F32 ? 16u : 32u, 1};
+        if ((rc = grouped_map(&p.yt, wtype, 3, dw, dims, strides, box, wtype == MOE_F32 ? 0 : 64)) != MOE_OK) return rc;
+    }
     p.rows = (const uint16_t *)x;
     p.ld = ldx;
     p.dy = (const uint16_t *)dy;
@@ -198,7 +209,7 @@ extern "C" int moe_grouped_weight_grad(const void *x, int type, int x_rows, size
     p.accumulate = accumulate;
     p.fmt = type == MOE_BF16;
     p.status = moe_status_word_device_ptr();
-    const int nt = wtype == MOE_F32 ? 128 : 256;
+    const int nt = wtype == MOE_F32 && !grouped_grad_short(R, G) ? 128 : 256;
     const long long items = (long long)G * ((N + nt - 1) / nt) * ((K + 255) / 256);
     return grouped_launch(p, wtype, GP_GRAD, true, items, 0, moe_cuda_stream(s));
 }

@@ -46,6 +46,7 @@ enum { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_GRAD = 3, GP_LORA = 4 };
 struct GroupedParams {
     CUtensorMap a, b, b64;    // GP_GRAD: x and dy
     CUtensorMap ab;           // GP_LORA: the adapters' B
+    CUtensorMap yt;           // GP_GRAD: dw by boxes of 32 x 32 (16 x 32 of fp32)
     const uint16_t *rows;     // x; GP_LORA: u
     const uint16_t *dy;       // GP_GRAD
     const uint16_t *lora_b;   // GP_LORA: the adapters' B
@@ -92,7 +93,7 @@ struct GroupedGeom {
     static constexpr int O_FIRST = O_OFF + (MOE_MAX_GROUPS + 4) * 4;
     static constexpr int O_ORDER = O_FIRST + (MOE_MAX_GROUPS + 4) * 4;
     static constexpr int O_ROWS = O_ORDER + MOE_MAX_GROUPS * 2;
-    static constexpr int O_XCH = O_ROWS + 2 * NT * 12;
+    static constexpr int O_XCH = (O_ROWS + 2 * NT * 12 + 511) / 512 * 512;  // (GP_GRAD's boxes: 64-byte swizzle)
     static constexpr int O_RED = O_XCH + 8 * XCH;
     static constexpr int O_RING = (O_RED + RED + 1023) / 1024 * 1024;
     static constexpr int S = (227 * 1024 - 1024 - O_RING) / STAGE / 2 * 2;  // (even: see the loaders)
@@ -901,7 +902,21 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         for (int a = 1; a < used; ++a)
 #pragma unroll
                             for (int h = 0; h < CH / 16; ++h) add16(v[h], tb + a * NT + c0 + 16 * h);
-                        float *x = (float *)(smem + G_::O_XCH + ew * G_::XCH);  // padded to 36: no bank conflicts
+                        float *x = (float *)(smem + G_::O_XCH + ew * G_::XCH);
+                        if (GRAD) {  // whole boxes by TMA: see below
+                            if (lane == 0) tma_store_wait_read();
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) x[32 * k + lane] = none ? 0.f : __uint_as_float(v[0][k]);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0 && m0 < p.M) {
+                                if (p.accumulate) tma_add_3d(&p.yt, m0, it.row0 + c0, it.g, xb);
+                                else tma_store_3d(&p.yt, m0, it.row0 + c0, it.g, xb);
+                            }
+                            continue;
+                        }
+                        // padded to 36: no bank conflicts
                         const int m = m0 + 4 * (lane & 7);
 #pragma unroll
                         for (int h = 0; h < CH / 16; ++h) {
@@ -915,10 +930,6 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                                 if (c < it.n && m < p.M && ys[c]) {
                                     const float s = ss[c];
                                     a = make_float4(s * a.x, s * a.y, s * a.z, s * a.w);
-                                    if (GRAD && p.accumulate) {
-                                        const float4 b = *(const float4 *)(ys[c] + 4 * (size_t)m);
-                                        a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-                                    }
                                     grouped_store4<OT>(ys[c], m, a);
                                 }
                             }
@@ -998,6 +1009,24 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     auto pack = [&](const uint32_t *v) -> uint32_t {
                         return grouped_pack<OT>(__uint_as_float(v[0]), __uint_as_float(v[1]));
                     };
+                    if (GRAD && CH == 32 && !p.accumulate) {
+                        // whole boxes: stored by TMA (rows past N, and columns past M, are not); 128 groups of 256 rows, 1536 x
+                        // 2048: 215 us by the lanes' own stores, 188 this way
+                        if (lane == 0) tma_store_wait_read();
+                        __syncwarp();
+#pragma unroll
+                        for (int b = 0; b < NB / 2; ++b)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t *v = (h ? hi : lo) + 8 * b;
+                                const int r = (lane & 7) + 8 * (lane >> 4) + 16 * b, piece = ((lane >> 3) & 1) + 2 * h;
+                                stmatrix_x4_trans(xb + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4), pack(v), pack(v + 2), pack(v + 4), pack(v + 6));
+                            }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && m0 < p.M) tma_store_3d(&p.yt, m0, it.row0 + c0, it.g, xb);
+                        continue;
+                    }
 #pragma unroll
                     for (int b = 0; b < NB / 2; ++b) {
                         const uint32_t *l = lo + 8 * b, *h = hi + 8 * b;
@@ -1037,6 +1066,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             }
             it = nx;
         }
+        if (GRAD && lane == 0) tma_store_wait();
     }
     tc_fence_before();
     __syncthreads();
@@ -1061,9 +1091,11 @@ static inline int grouped_launch(const GroupedParams &p, int ytype, int mode, bo
            : ytype == MOE_BF16 ? grouped_launch_bf16(p, mode, wide, items, stages, s)
                                : grouped_launch_f16(p, mode, wide, items, stages, s);
 }
+// GP_GRAD: reductions of at most 512 rows on average.
+static inline bool grouped_grad_short(int R, int G) { return R <= 512LL * G; }
 // SMs of the current device (0: none).
 int grouped_sms();
-// Tensor map of 16-bit elements: `rank` dimensions and box extents innermost first, strides in bytes from the second on.
+// Tensor map of elements of `type`: `rank` dimensions and box extents innermost first, strides in bytes from the second on.
 int grouped_map(CUtensorMap *map, int type, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
                 const uint32_t *box, int swizzle_bytes);
 

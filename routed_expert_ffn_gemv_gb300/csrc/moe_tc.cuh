@@ -388,6 +388,24 @@ __device__ __forceinline__ void tma_tile_4d(void *dst, const void *map, int x, i
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
             : "memory");
 }
+// A box from shared to global memory, by one thread; what lies outside the tensor is not written.  The thread's earlier boxes:
+// all read (their shared memory may be written again), all written.
+__device__ __forceinline__ void tma_store_3d(const void *map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+// The same box added to what is there (fp32).
+__device__ __forceinline__ void tma_add_3d(const void *map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // An arrival on a barrier of any CTA of the cluster (shared::cluster address).  Its release is at CTA scope: what it
 // hands over is this CTA's own shared or tensor memory, which the MMA that follows reads on this SM.  (With a release at
 // cluster scope an arrival takes about 1 us: rows of 32768 routes handed over a stage at a time 515 us, this way 275.)
