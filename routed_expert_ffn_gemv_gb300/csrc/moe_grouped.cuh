@@ -3,7 +3,7 @@
 //
 //   D[m][c] = sum_k A[m][k] B[c][k],  tcgen05.mma kind::f16, fp32 sums in tensor memory.
 // The matrix is always the M side (128 rows a CTA) and the rows of the group the N side, up to NT of them: an MMA is
-// only as wide as the group's rows are, so ragged groups waste at most GP_GRAN - 1 columns.
+// only as wide as the group's rows are, so ragged groups waste at most GRAN - 1 columns.
 //
 //              A (M side)                       B (N side)                     reduction
 //   GP_NK      W_g[n][k], K-major               rows x[i][k]                   K
@@ -25,6 +25,10 @@
 //   warp 3       hands their stages over once they have landed.  (TMA gathers, four rows an instruction,
 //                take about 40 ns each however many are in flight: 32768 rows of 2048 gathered for 1536
 //                outputs took 510 us.)
+// Two shapes (see moe_grouped_matmul for the rule): NT = 32, one CTA an item, for few rows, when reading the matrix is
+// the work (77 tokens over 64 experts of 2 x 1408 x 2048: 86 us, HBM's rate); NT = 256 (fp32 results 128) by pairs of CTAs, when it
+// is the MMAs (8192^3: 631 us, 1743 TFLOP/s; by single CTAs, which load twice as much, a prompt's gate/up product took
+// 1.7 times as long).
 // CG = 1: where items are few, the CTAs of a cluster share an item's reduction and add their sums up over distributed shared
 // memory, in the order of their ranks.
 // CG = 2: two CTAs share each MMA (M = 256), every CTA loads half of A and half of B.
@@ -60,7 +64,6 @@ struct GroupedParams {
     const float *scale;       // [y_rows] or NULL
     void *y;
     size_t ldy;               // GP_GRAD: M
-    int accs;                 // fp32 results: most accumulators of an item
     int M, K, N;              // columns of an output row; reduction (not GP_GRAD); GP_GRAD: output rows of a group
     int accumulate;           // GP_GRAD
     const int32_t *adapter;   // GP_LORA, [R]
@@ -82,8 +85,8 @@ struct GroupedGeom {
     static constexpr int GRAN = 16 * CG;                     // rows an MMA's width is rounded up to
     static constexpr int BBYTES = NT / CG * 128;
     static constexpr int STAGE = GP_ABYTES + BBYTES;
-    static constexpr int SLOTS = OT == MOE_F32 ? 512 / NT : 2;  // accumulators in tensor memory
-    static constexpr int TCOLS = SLOTS * NT;                 // (a power of two from 32 on)
+    static constexpr unsigned SLOTS = OT == MOE_F32 ? 512 / NT : 2;  // accumulators in tensor memory
+    static constexpr int TCOLS = (int)SLOTS * NT;                 // (a power of two from 32 on)
     static constexpr int ACC_STAGES = NT <= 32 ? 4 : 8;
     static constexpr int CH = NT >= 64 && OT != MOE_F32 ? 32 : 16;  // columns of an epilogue warp's chunk
     static constexpr int XCH = CH * 80 < 2304 ? 2304 : CH * 80;  // bytes of an epilogue warp
@@ -98,7 +101,7 @@ struct GroupedGeom {
     static constexpr int O_RING = (O_RED + RED + 1023) / 1024 * 1024;
     static constexpr int S = (227 * 1024 - 1024 - O_RING) / STAGE / 2 * 2;  // (even: see the loaders)
     static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
-    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 6) * 8 + 16 + 80 <= 1024 && S >= 6, "");
+    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 2 * SLOTS + 2) * 8 + 16 + 80 <= 1024 && S >= 6, "");
 };
 
 struct GroupedItem {
@@ -169,8 +172,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     uint64_t *empty = full + S;
     uint64_t *landed = empty + S;
     uint64_t *acc_full = landed + S;
-    uint64_t *acc_empty = acc_full + 2;
-    uint64_t *mma_done = acc_empty + 2;
+    uint64_t *acc_empty = acc_full + G_::SLOTS;
+    uint64_t *mma_done = acc_empty + G_::SLOTS;
     uint64_t *red_full = mma_done + 1;
     uint32_t *tmem_slot = (uint32_t *)(red_full + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             mbar_init(&landed[s], 128 + (MODE == GP_LORA));
             mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (unsigned b = 0; b < G_::SLOTS; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 8 * CG);
         }
@@ -211,10 +214,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     if (CG == 2 || ks > 1) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // accumulators of an item, and items in tensor memory
-    const int accs = OT == MOE_F32 ? min(p.accs, G_::SLOTS) : 1, bufs = 2 * accs <= G_::SLOTS ? 2 : 1;
-    // stages of an accumulator, of n (GP_LORA's extra ones go to the last one)
-    auto acc_stages = [&](int n) -> int { return accs == 1 ? max(n, 1) : max((n + accs - 1) / accs, G_::ACC_STAGES); };
+    // Accumulators are taken one after another, round tensor memory's slots: an item's one (or, fp32 results, as many as its n
+    // stages have use for; GP_LORA's extra stages go to the last of them), the next item's behind it.
+    auto acc_stages = [&](int n) -> int { return OT == MOE_F32 ? max((n + (int)G_::SLOTS - 1) / (int)G_::SLOTS, G_::ACC_STAGES) : max(n, 1); };
+    auto acc_count = [&](int n) -> int { return OT == MOE_F32 ? max(1, (n + acc_stages(n) - 1) / acc_stages(n)) : 1; };
     // (GP_LORA: the kernel in front computes u and nothing else; it starts this one when everything before it is
     // complete, and only u is waited for, by the warp that loads it)
     if (MODE != GP_LORA) pdl_wait();
@@ -655,6 +658,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     } else if (warp == 2 && rank == 0) {
         // ---------------- MMA issuer
         int st = 0;
+        unsigned seq = 0;  // accumulators taken so far
         uint32_t ph = 0;
         bool ok = true;
         for (int j = 0; j < n_mine && ok; ++j) {
@@ -662,14 +666,22 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             // (a value that a shuffle hands out is known to be the same in every lane: it stays in a uniform register, where
             // the MMA wants its operands)
             const uint32_t idesc = umma_idesc_16(p.fmt, A_MN, B_MN, 128 * CG, __shfl_sync(0xffffffffu, it.npad, 0));
-            const int buf = bufs == 2 ? j & 1 : 0, round = bufs == 2 ? j / 2 : j;
             int lo, hi, ids[8];
             read_adapters(it, ids);
             share(__shfl_sync(0xffffffffu, it.steps, 0), lo, hi);
             bool fresh = true;  // nothing summed yet
-            if (round >= 1 && !(ok = mbar_wait_warp(&acc_empty[buf], (round - 1) & 1, p.status, abort_flag))) break;
-            tc_fence_after();
-            uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + buf * accs * NT;
+            uint32_t d = 0;
+            auto take = [&]() -> bool {  // the next accumulator
+                const unsigned slot = seq % G_::SLOTS, round = seq / G_::SLOTS;
+                if (round >= 1 && !(ok = mbar_wait_warp(&acc_empty[slot], (round - 1) & 1, p.status, abort_flag))) return false;
+                tc_fence_after();
+                d = __shfl_sync(0xffffffffu, tmem, 0) + slot * NT;
+                ++seq;
+                fresh = true;
+                return true;
+            };
+            const unsigned begun = seq;
+            if (!take()) break;
             const int len = GRAD ? __shfl_sync(0xffffffffu, it.cnt, 0) : p.K;
             const int per = __shfl_sync(0xffffffffu, acc_stages(hi - lo), 0);
             int left_in_acc = per;
@@ -681,8 +693,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 const uint64_t b = B_MN ? umma_desc_mn_sw128(sa + GP_ABYTES, 8192) : umma_desc_sw128(sa + GP_ABYTES);
                 if (OT == MOE_F32 && left_in_acc == 0) {
                     left_in_acc = per;
-                    d += NT;
-                    fresh = true;
+                    if (!take()) break;
                 }
                 --left_in_acc;
                 const int left = len - 64 * kb;
@@ -730,7 +741,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     ph ^= 1u;
                 }
             }
-            if (ok) umma_commit_group_elect<CG>(&acc_full[buf]);
+            if (ok)
+                for (unsigned a = begun; a < seq; ++a) umma_commit_group_elect<CG>(&acc_full[a % G_::SLOTS]);
         }
         umma_commit_group_elect<CG>(mma_done);  // every MMA has completed before tensor memory is released
         mbar_wait_bounded(mma_done, 0, p.status);
@@ -792,6 +804,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             }
             return bad ? s : 0.f;
         };
+        unsigned seq = 0;  // accumulators before this item's
         GroupedItem it = {};
         if (n_mine) {
             it = item_at(0);
@@ -799,7 +812,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             resolve(it);
         }
         for (int j = 0; j < n_mine; ++j) {
-            const int buf = j & 1, abuf = bufs == 2 ? buf : 0, round = bufs == 2 ? j / 2 : j;
+            const int buf = j & 1;
             if (et < NT) {
                 e_y[buf * NT + et] = row;
                 e_s[buf * NT + et] = scale;
@@ -809,18 +822,20 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 nx = item_at(j + 1);
                 fetch(nx);
             }
-            const bool w = mbar_wait_role(&acc_full[abuf], round & 1, p.status, abort_flag);
-            if (!bar_and_n(1, 256, w)) break;
-            if (j + 1 < n_mine) resolve(nx);
-            tc_fence_after();
-            const uint32_t tb = tmem + ((uint32_t)(32 * q) << 16) + abuf * accs * NT;
-            int used = 1;  // accumulators
+            unsigned used = 1;  // accumulators
             if (OT == MOE_F32) {
                 int lo, hi;
                 share(it.steps, lo, hi);
-                const int per = acc_stages(hi - lo);
-                used = max(1, (hi - lo + per - 1) / per);
+                used = acc_count(hi - lo);
             }
+            bool w = true;
+            for (unsigned a = seq; a < seq + used && w; ++a)
+                w = mbar_wait_role(&acc_full[a % G_::SLOTS], (a / G_::SLOTS) & 1, p.status, abort_flag);
+            if (!bar_and_n(1, 256, w)) break;
+            if (j + 1 < n_mine) resolve(nx);
+            tc_fence_after();
+            const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16), tb = quarter + seq % G_::SLOTS * NT;
+            auto other = [&](unsigned a) -> uint32_t { return quarter + (seq + a) % G_::SLOTS * NT; };  // the item's a-th accumulator
             uint8_t *const *ys = e_y + buf * NT;
             const float *ss = e_s + buf * NT;
             const bool none = GRAD && !it.steps;
@@ -843,7 +858,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     uint32_t v[16];
                     tmem_ld16(tb + 16 * half, v);
                     tmem_ld_wait();
-                    for (int a = 1; a < used; ++a) add16(v, tb + a * NT + 16 * half);
+                    for (unsigned a = 1; a < used; ++a) add16(v, other(a) + 16 * half);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) x[(16 * half + k) * 128 + 32 * q + lane] = n ? __uint_as_float(v[k]) : 0.f;
                 }
@@ -899,9 +914,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
 #pragma unroll
                         for (int h = 0; h < CH / 16; ++h) tmem_ld16(tb + c0 + 16 * h, v[h]);
                         tmem_ld_wait();
-                        for (int a = 1; a < used; ++a)
+                        for (unsigned a = 1; a < used; ++a)
 #pragma unroll
-                            for (int h = 0; h < CH / 16; ++h) add16(v[h], tb + a * NT + c0 + 16 * h);
+                            for (int h = 0; h < CH / 16; ++h) add16(v[h], other(a) + c0 + 16 * h);
                         float *x = (float *)(smem + G_::O_XCH + ew * G_::XCH);
                         if (GRAD) {  // whole boxes by TMA: see below
                             if (lane == 0) tma_store_wait_read();
@@ -942,13 +957,13 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     tmem_ld_16x256b(tb + c0, lo);
                     tmem_ld_16x256b(tb + (16u << 16) + c0, hi);
                     tmem_ld_wait();
-                    for (int a = 1; a < used; ++a) {  // (F32)
+                    for (unsigned a = 1; a < used; ++a) {  // (F32)
                         uint32_t u[4 * NB];
-                        tmem_ld_16x256b(tb + a * NT + c0, u);
+                        tmem_ld_16x256b(other(a) + c0, u);
                         tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 4 * NB; ++k) lo[k] = __float_as_uint(__uint_as_float(lo[k]) + __uint_as_float(u[k]));
-                        tmem_ld_16x256b(tb + a * NT + (16u << 16) + c0, u);
+                        tmem_ld_16x256b(other(a) + (16u << 16) + c0, u);
                         tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 4 * NB; ++k) hi[k] = __float_as_uint(__uint_as_float(hi[k]) + __uint_as_float(u[k]));
@@ -1060,10 +1075,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                if (CG == 1) mbar_arrive1(&acc_empty[abuf]);
-                else mbar_arrive_cluster(cluster_map(&acc_empty[abuf], 0));
-            }
+            if (lane == 0)
+                for (unsigned a = seq; a < seq + used; ++a) {
+                    if (CG == 1) mbar_arrive1(&acc_empty[a % G_::SLOTS]);
+                    else mbar_arrive_cluster(cluster_map(&acc_empty[a % G_::SLOTS], 0));
+                }
+            seq += used;
             it = nx;
         }
         if (GRAD && lane == 0) tma_store_wait();

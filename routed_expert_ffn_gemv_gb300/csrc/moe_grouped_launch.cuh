@@ -7,7 +7,7 @@
 #include "moe_grouped.cuh"
 
 template <int CG, int NT, int MODE, int OT>
-static int grouped_launch_t(GroupedParams p, long long items, int stages, cudaStream_t s) {
+static int grouped_launch_t(const GroupedParams &p, long long items, int stages, cudaStream_t s) {
     using G = GroupedGeom<CG, NT, OT>;
     static std::mutex mu;
     static bool ready[64] = {false};
@@ -23,11 +23,6 @@ static int grouped_launch_t(GroupedParams p, long long items, int stages, cudaSt
         }
     }
     const int n = std::max(CG, grouped_sms());
-    // fp32 results: as many accumulators as the reduction has use for, all of tensor memory for one item if it is long
-    p.accs = 1;
-    if (OT == MOE_F32 && MODE == GP_GRAD) p.accs = NT == 128 ? G::SLOTS : 1;
-    else if (OT == MOE_F32)
-        while (p.accs < G::SLOTS && p.accs * G::ACC_STAGES * 64 < p.K) p.accs *= 2;
     items = std::max(1LL, items);
     int cluster = CG;
     // CG = 1: as many CTAs to an item as there are SMs for, each with four stages of the reduction at least
@@ -63,7 +58,7 @@ static int grouped_launch_modes(const GroupedParams &p, int mode, bool wide, lon
             return wide ? grouped_launch_t<2, WIDE, GP_LORA, OT>(p, items, stages, s)
                         : grouped_launch_t<1, 32, GP_LORA, OT>(p, items, stages, s);
         default:
-            // fp32: tiles of 128 and four accumulators for long reductions only (128 groups of 256 rows, 1536 x 2048: 403 us
+            // fp32: tiles of 128, for four accumulators instead of two, with long reductions only (128 groups of 256 rows, 1536 x 2048: 403 us
             // against 331)
             if (OT == MOE_F32 && !grouped_grad_short(p.R, p.G)) return grouped_launch_t<2, WIDE, GP_GRAD, OT>(p, items, stages, s);
             return grouped_launch_t<2, 256, GP_GRAD, OT>(p, items, stages, s);

@@ -159,6 +159,22 @@ def test_offsets_that_are_no_range_are_recorded_and_skipped(R):
     assert bool((y[R - 1] == 7.0).all())
 
 
+@pytest.mark.parametrize("T,N", [(3, 32), (30, 64), (30, 5128), (900, 1032)])
+def test_adapters_outside_are_recorded_and_left_out(T, N):
+    g = gen(T)
+    K = 72
+    x, w = rand(g, "f16", T, K), rand(g, "f16", N, K)
+    a, b = rand(g, "f16", 2, 16, K), rand(g, "f16", 2, N, 16)
+    adapter = torch.full((T,), 1, dtype=torch.int32, device="cuda")
+    adapter[0], adapter[T - 1] = 2, -2
+    y = lora(x, "f16", w, adapter, a, b, None, "f32")
+    assert L.moe_device_status(clear=True) == L.MOE_ERR_INVALID
+    v, e = ref.product(x, w)
+    ref.check(y[[0, T - 1]], v[[0, T - 1]], ref.rounded(v, e, "f32")[[0, T - 1]])
+    v, e = lora_bound(x[1:T - 1], "f16", w, a[1], b[1], 1.0, "f32")
+    ref.check(y[1:T - 1], v, e)
+
+
 def test_gradient_of_rows_outside():
     g = gen(4)
     R, N, K = 150, 128, 64
