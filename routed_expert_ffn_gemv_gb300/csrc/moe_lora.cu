@@ -53,12 +53,16 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
     float v[LS_RANKS] = {};
     if (j0 < rank) {
         const uint16_t *xr = x + (size_t)t * ldx, *ar = a + ((size_t)ad * rank + j0) * K;
-        for (int k = 8 * lane; k < K; k += 256) {
-            const uint4 xv = *(const uint4 *)(xr + k);
+#pragma unroll 4
+        for (int k = 8 * lane; k < K; k += 256) {  // (several turns' loads in flight)
+            const uint4 xv = __ldg((const uint4 *)(xr + k));
             const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+            uint4 avs[LS_RANKS];
+#pragma unroll
+            for (int j = 0; j < LS_RANKS; ++j) avs[j] = __ldg((const uint4 *)(ar + (size_t)j * K + k));
 #pragma unroll
             for (int j = 0; j < LS_RANKS; ++j) {  // (the rank is a multiple of 8)
-                const uint4 av = *(const uint4 *)(ar + (size_t)j * K + k);
+                const uint4 av = avs[j];
                 const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
