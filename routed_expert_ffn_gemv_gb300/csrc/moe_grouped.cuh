@@ -67,7 +67,7 @@ struct GroupedParams {
     int M, K, N;              // columns of an output row; reduction (not GP_GRAD); GP_GRAD: output rows of a group
     int accumulate;           // GP_GRAD
     const int32_t *adapter;   // GP_LORA, [R]
-    int n_adapters, rank;
+    int n_adapters, rank, parts;  // parts: 128-byte pieces of u for 32 ranks
     int fmt;                  // 0 fp16, 1 bf16
     int *status;
 };
@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             if (ids[i] >= p.n_adapters) ids[i] = -1;
         }
     };
-    const int chunks = MODE == GP_LORA ? (p.rank + 31) / 32 : 1;
+    const int chunks = MODE == GP_LORA ? (p.rank + 31) / 32 * p.parts : 1;  // pieces of u: p.parts for 32 ranks of B
+    const int shift = MODE == GP_LORA && p.parts == 2;
     auto extra_stages = [&](const int (&ids)[8]) -> int {
         int n = 0;
         for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a)) n += chunks;
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         if (rank == 0 && lane == 0) mbar_arrive1(&full[st]);
                         mbar_arrive_expect_tx_elect(&landed[st], GP_UBYTES);
                         if (lane == 0)
-                            tma_tile_3d<CG>(ring + (size_t)st * G_::STAGE, &p.ab, c * 32, m0, a, smem_u32(&landed[st]));
+                            tma_tile_3d<CG>(ring + (size_t)st * G_::STAGE, &p.ab, (c >> shift) * 32, m0, a, smem_u32(&landed[st]));
                         __syncwarp();
                         ++gs;
                         if (++st == S) {
@@ -729,7 +730,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 const uint64_t a = umma_desc_sw64(sa), b = umma_desc_sw128(sa + GP_ABYTES);
                 umma_f16_elect<CG>(d, a, b, idesc, !fresh);
                 umma_f16_elect<CG>(d, a, b + 4, idesc, 1);
-                if (p.rank - 32 * c > 16) {
+                if (p.rank - 32 * (c >> shift) > 16) {
                     umma_f16_elect<CG>(d, a + 2, b + 2, idesc, 1);
                     umma_f16_elect<CG>(d, a + 2, b + 6, idesc, 1);
                 }
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(u[k]));
         };
-        // GP_LORA: 32 ranks (chunk c) of adapter a for output o of token t, where b is not finite among them, else 0
+        // GP_LORA: 32 ranks (by piece c of u) of adapter a for output o of token t, where b is not finite among them, else 0
         auto not_finite = [&](int a, int c, int o, int t) -> float {
             const uint16_t *b = p.lora_b + ((size_t)a * p.M + o) * p.rank, *u = p.rows + (size_t)t * p.ld + c * 64;
             auto value = [&](uint16_t h) -> float {
@@ -797,8 +798,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             };
             float s = 0.f;
             bool bad = false;
-            for (int k = 0; k < 32 && 32 * c + k < p.rank; ++k) {
-                const float v = value(b[32 * c + k]);
+            const int c0 = 32 * (c >> shift);
+            for (int k = 0; k < 32 && c0 + k < p.rank; ++k) {
+                const float v = value(b[c0 + k]);
                 bad |= !(fabsf(v) <= 3.4028235e38f);
                 s = fmaf(v, value(u[k]) + value(u[32 + k]), s);
             }
@@ -1136,7 +1138,7 @@ struct GroupedFewParams {
     int ytype, M, K;
     const int32_t *adapter;  // GP_LORA
     const uint16_t *b, *u;
-    int n_adapters, rank;
+    int n_adapters, rank, parts;
     int *status;
 };
 // GP_NK, GP_SWIGLU, GP_LORA with R <= GF_MAX_R.

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
             for (int i = 0; i < PF; ++i) fetch(a[i], i);
         }
         if (MODE == GP_LORA) {
-            // ---------------- the adapters of the tile's tokens, the warps in turns; u's upper halves, then the rest of u
+            // ---------------- the adapters of the tile's tokens, the warps in turns; u's upper halves, then the rest of u (its parts)
             if (!waited) pdl_wait();
             waited = true;
             int id = lane < tile.n ? p.adapter[tile.row0 + lane] : -1;  // token `lane` of the tile
@@ -202,9 +202,10 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
                     for (int b = 0; b < NB; ++b) {
                         if (!(who >> (8 * b) & 0xFF)) continue;
                         const bool mine = who >> (8 * b + g) & 1;
-                        const uint16_t *u = p.u + ((size_t)(tile.row0 + 8 * b + g) * chunks + c) * 64 + 8 * t4;
+                        const uint16_t *u = p.u + ((size_t)(tile.row0 + 8 * b + g) * chunks + c) * p.parts * 64 + 8 * t4;
                         mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)u : zero);
                         mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)(u + 32) : zero);
+                        if (BF && p.parts == 2) mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)(u + 64) : zero);
                     }
                 }
 #pragma unroll

@@ -2,7 +2,7 @@
 //
 //   y[t] = W x_t + B_a u_t,   u_t = scale[a] A_a x_t,   a = adapter[t]
 // Two kernels.  lora_shrink_kernel computes u in fp32 and leaves it as two 16-bit halves (the nearest, and the nearest of what
-// is left: 16 bits of bf16, 22 of fp16), 32 ranks to a 128-byte row piece, upper halves first.  The product's kernel (moe_grouped.cuh, GP_LORA) runs K on into the ranks: for each adapter that has tokens in
+// is left: 16 bits of bf16, 22 of fp16), 32 ranks to a 128-byte row piece, upper halves first (and, where a third part is kept, another piece for it).  The product's kernel (moe_grouped.cuh, GP_LORA) runs K on into the ranks: for each adapter that has tokens in
 // its tile, 32 ranks at a time, B_a's tile against the tokens' rows of u, zeros for the tokens of other adapters.  So y
 // is rounded once and W's part and the adapters' share an accumulator.  The product starts beside the first kernel and waits
 // for u only where it loads it.
@@ -22,26 +22,30 @@ __device__ __forceinline__ float2 pair_value(uint32_t w) {
     return __half22float2(*(const __half2 *)&w);
 }
 // v as two 16-bit numbers (one that overflows: as the infinity alone).
+// (rest: what they leave, as a third.)
 template <bool BF>
-__device__ __forceinline__ void split16(float v, uint16_t &hi, uint16_t &lo) {
+__device__ __forceinline__ void split16(float v, uint16_t &hi, uint16_t &lo, uint16_t &rest) {
     if (BF) {
         const __nv_bfloat16 h = __float2bfloat16_rn(v);
-        const float f = __bfloat162float(h);
+        const float f = __bfloat162float(h), left = isinf(f) ? 0.f : v - f;
+        const __nv_bfloat16 l = __float2bfloat16_rn(left);
         hi = __bfloat16_as_ushort(h);
-        lo = __bfloat16_as_ushort(__float2bfloat16_rn(isinf(f) ? 0.f : v - f));
+        lo = __bfloat16_as_ushort(l);
+        rest = __bfloat16_as_ushort(__float2bfloat16_rn(left - __bfloat162float(l)));
     } else {
         const __half h = __float2half_rn(v);
         const float f = __half2float(h);
         hi = __half_as_ushort(h);
         lo = __half_as_ushort(__float2half_rn(isinf(f) ? 0.f : v - f));
+        rest = 0;
     }
 }
 
-// Few tokens: a warp for LS_RANKS ranks of one token.  No shared memory: it runs beside the product.  u: [T][chunks][64].
+// Few tokens: a warp for LS_RANKS ranks of one token.  No shared memory: it runs beside the product.  u: [T][chunks][parts][64].
 template <bool BF>
 __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, size_t ldx, int T, int K, const int32_t *adapter,
                                                           int n_adapters, const uint16_t *a, int rank, const float *scale,
-                                                          uint16_t *u) {
+                                                          uint16_t *u, int parts) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x % 32, chunks = (rank + 31) / 32, groups = chunks * 32 / LS_RANKS;
@@ -84,12 +88,16 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
             if (j == lane) r = v[j];
         if (scale) r *= scale[ad];
         if (j0 >= rank) r = 0.f;
-        uint16_t hi, lo;
-        split16<BF>(r, hi, lo);
+        uint16_t hi, lo, rest;
+        split16<BF>(r, hi, lo, rest);
         const int j = j0 + lane;
-        uint16_t *row = u + ((size_t)t * chunks + j / 32) * 64 + j % 32;
+        uint16_t *row = u + ((size_t)t * chunks + j / 32) * parts * 64 + j % 32;
         row[0] = hi;
         row[32] = lo;
+        if (parts == 2) {
+            row[64] = rest;
+            row[96] = 0;
+        }
     }
 }
 
@@ -104,10 +112,10 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
 
 struct ShrinkParams {
     CUtensorMap x, a;  // x by boxes of 128 rows, A by adapters
-    int T, K, rank, n_adapters, per_pass, fmt;  // per_pass: adapters of a pass
+    int T, K, rank, n_adapters, per_pass, fmt, parts;  // per_pass: adapters of a pass
     const int32_t *adapter;
     const float *scale;
-    uint16_t *u;       // [T][chunks][64]
+    uint16_t *u;       // [T][chunks][parts][64]
     int *status;
 };
 
@@ -294,12 +302,16 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
                 const float sc = p.scale ? p.scale[s.ids[t]] : 1.f;
                 v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
             }
-            uint16_t hi[4], lo[4];
-            split16<BF>(v.x, hi[0], lo[0]);
-            split16<BF>(v.y, hi[1], lo[1]);
-            split16<BF>(v.z, hi[2], lo[2]);
-            split16<BF>(v.w, hi[3], lo[3]);
-            uint16_t *row = p.u + ((size_t)(t0 + t) * chunks + j / 32) * 64 + j % 32;
+            uint16_t hi[4], lo[4], rest[4];
+            split16<BF>(v.x, hi[0], lo[0], rest[0]);
+            split16<BF>(v.y, hi[1], lo[1], rest[1]);
+            split16<BF>(v.z, hi[2], lo[2], rest[2]);
+            split16<BF>(v.w, hi[3], lo[3], rest[3]);
+            uint16_t *row = p.u + ((size_t)(t0 + t) * chunks + j / 32) * p.parts * 64 + j % 32;
+            if (p.parts == 2) {
+                *(uint2 *)(row + 64) = make_uint2(rest[0] | (uint32_t)rest[1] << 16, rest[2] | (uint32_t)rest[3] << 16);
+                *(uint2 *)(row + 96) = make_uint2(0, 0);
+            }
             *(uint2 *)row = make_uint2(hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16);
             *(uint2 *)(row + 32) = make_uint2(lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16);
         }
@@ -321,19 +333,19 @@ int check(int T, int rank) {
 }
 
 int shrink_few(const void *x, size_t ldx, int T, int K, int type, const int32_t *adapter, int n_adapters, const void *a,
-               int rank, const float *scale, void *u, moe_stream_t s) {
+               int rank, const float *scale, void *u, int parts, moe_stream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     const long long jobs = (long long)T * ((rank + 31) / 32 * 32 / LS_RANKS);
     moe_pdl_config(&cfg, attr, dim3((unsigned)((jobs + 7) / 8)), dim3(256), 0, moe_cuda_stream(s));
     MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, type == MOE_BF16 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>,
                                     (const uint16_t *)x, ldx, T, K, adapter, n_adapters, (const uint16_t *)a, rank, scale,
-                                    (uint16_t *)u));
+                                    (uint16_t *)u, parts));
     return MOE_OK;
 }
 
 int shrink_many(const void *x, size_t ldx, int T, int K, int type, const int32_t *adapter, int n_adapters, const void *a,
-                int rank, const float *scale, void *u, int *status, moe_stream_t s) {
+                int rank, const float *scale, void *u, int parts, int *status, moe_stream_t s) {
     static std::mutex mu;
     static bool ready[64] = {false};
     int dev = -1, rc;
@@ -369,6 +381,7 @@ int shrink_many(const void *x, size_t ldx, int T, int K, int type, const int32_t
     p.adapter = adapter;
     p.scale = scale;
     p.u = (uint16_t *)u;
+    p.parts = parts;
     p.status = status;
     const int tiles = (T + LS_TOKENS - 1) / LS_TOKENS, most = std::min(n_adapters, LS_TOKENS);
     const int passes = (most + p.per_pass - 1) / p.per_pass;
@@ -391,7 +404,7 @@ extern "C" int moe_lora_workspace(int T, int rank, size_t *bytes) {
     MOE_CHECK(bytes);
     const int rc = check(T, rank);
     if (rc != MOE_OK) return rc;
-    *bytes = (size_t)T * ((rank + 31) / 32) * 128;
+    *bytes = (size_t)T * ((rank + 31) / 32) * 256;
     return MOE_OK;
 }
 
@@ -412,8 +425,10 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     MOE_CHECK(((uintptr_t)workspace & 255) == 0);
 
     int *status = moe_status_word_device_ptr();
-    rc = T <= LS_FEW ? shrink_few(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, s)
-                     : shrink_many(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, status, s);
+    // bf16 with fp32 results: u in three parts, 24 bits (two leave y 1.8e-6 off, relative to its norm, three 3e-7)
+    const int parts = type == MOE_BF16 && ytype == MOE_F32 ? 2 : 1;
+    rc = T <= LS_FEW ? shrink_few(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, parts, s)
+                     : shrink_many(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, parts, status, s);
     if (rc != MOE_OK) return rc;
     // few tokens, and no more rows of W than CTAs run at once (N = 2816: 1 token 12.1 -> 8.4 us, 32 tokens 20.2 -> 12.4 by the
     // kernel for few rows; N = 11264: 15.1 -> 14.9 and 21.1 -> 29.9)
@@ -438,6 +453,7 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
         f.u = (const uint16_t *)workspace;
         f.n_adapters = n_adapters;
         f.rank = rank;
+        f.parts = parts;
         f.status = status;
         return grouped_few_launch(f, GP_LORA, type == MOE_BF16, moe_cuda_stream(s));
     }
@@ -461,7 +477,8 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
         if ((rc = grouped_map(&p.ab, type, 3, b, dims, strides, box, 64)) != MOE_OK) return rc;
     }
     p.rows = (const uint16_t *)workspace;
-    p.ld = (size_t)chunks * 64;
+    p.ld = (size_t)chunks * parts * 64;
+    p.parts = parts;
     p.lora_b = (const uint16_t *)b;
     p.G = 1;
     p.R = T;
@@ -482,6 +499,6 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     const bool wide = (T + 31) / 32 * ((N + 127) / 128) > grouped_sms();
     const int nt = !wide ? 32 : ytype == MOE_F32 ? 128 : 256;
     const long long tiles = (T + nt - 1) / nt;
-    return grouped_launch(p, ytype, GP_LORA, wide, tiles * ((N + 127) / 128), (K + 63) / 64 + std::min(T, n_adapters) * chunks,
+    return grouped_launch(p, ytype, GP_LORA, wide, tiles * ((N + 127) / 128), (K + 63) / 64 + std::min(T, n_adapters) * chunks * parts,
                           moe_cuda_stream(s));
 }

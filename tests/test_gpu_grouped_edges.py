@@ -118,6 +118,26 @@ def test_lora_in_wide_tiles(T, n, rank, N, K, t, out):
             ref.check(y[mine], v, e, i)
 
 
+@pytest.mark.parametrize("T,N", [(6, 64), (30, 200), (40, 136), (31, 5128), (700, 1032)])
+def test_lora_of_bf16_keeps_24_bits_for_fp32_results(T, N):
+    """u's split adds no more than half a step of bf16 three times over."""
+    rng, g = np.random.default_rng(T), gen(N)
+    K, n, rank = 136, 3, 48
+    adapter = rng.integers(0, n, size=T).astype(np.int32)
+    x, w = rand(g, "bf16", T, K), rand(g, "bf16", N, K, scale=1e-3)
+    a, b = rand(g, "bf16", n, rank, K), rand(g, "bf16", n, N, rank)
+    y = lora(x, "bf16", w, torch.from_numpy(adapter).cuda(), a, b, None, "f32")
+    for i in range(n):
+        mine = torch.from_numpy((adapter == i).nonzero()[0]).cuda()
+        v, _ = ref.product(x[mine], w)
+        u, eu = ref.product(x[mine], a[i])
+        eu = eu + ref.HALF["bf16"] ** 3 * (u.abs() + eu) + ref.TINY["bf16"]
+        m = b[i].double()
+        total = x[mine].double().abs() @ w.double().abs().T + (u.abs() + eu) @ m.abs().T
+        e = ref.rounded(v + u @ m.T, eu @ m.abs().T + (K + 3 * rank + 16) * 2.0 ** -23 * total, "f32")
+        ref.check(y[mine], v + u @ m.T, e, i)
+
+
 # ------------------------------------------------------------------------------ indexes and offsets outside
 
 @pytest.mark.parametrize("R,G", [(6, 3), (60, 4), (900, 4)])
