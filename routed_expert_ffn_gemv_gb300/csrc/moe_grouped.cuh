@@ -26,7 +26,7 @@
 //                take about 40 ns each however many are in flight: 32768 rows of 2048 gathered for 1536
 //                outputs took 510 us.)
 // Two shapes (see moe_grouped_matmul for the rule): NT = 32, one CTA an item, for few rows, when reading the matrix is
-// the work (77 tokens over 64 experts of 2 x 1408 x 2048: 86 us, HBM's rate); NT = 256 (fp32 results 128) by pairs of CTAs, when it
+// the work (77 tokens over 64 experts of 2 x 1408 x 2048: 86 us, HBM's rate); NT = 256 (fp32 results 128 or 64) by pairs of CTAs, when it
 // is the MMAs (8192^3: 631 us, 1743 TFLOP/s; by single CTAs, which load twice as much, a prompt's gate/up product took
 // 1.7 times as long).
 // CG = 1: where items are few, the CTAs of a cluster share an item's reduction and add their sums up over distributed shared
@@ -87,7 +87,6 @@ struct GroupedGeom {
     static constexpr int STAGE = GP_ABYTES + BBYTES;
     static constexpr unsigned SLOTS = OT == MOE_F32 ? 512 / NT : 2;  // accumulators in tensor memory
     static constexpr int TCOLS = (int)SLOTS * NT;                 // (a power of two from 32 on)
-    static constexpr int ACC_STAGES = NT <= 32 ? 4 : 8;
     static constexpr int CH = NT >= 64 && OT != MOE_F32 ? 32 : 16;  // columns of an epilogue warp's chunk
     static constexpr int XCH = CH * 80 < 2304 ? 2304 : CH * 80;  // bytes of an epilogue warp
     // CG = 1: partial sums of up to GP_MAX_SPLIT CTAs, for this CTA's share of the rows
@@ -165,6 +164,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     constexpr int S = G_::S;
     constexpr bool GRAD = MODE == GP_GRAD, A_MN = GRAD || MODE == GP_KN, B_MN = GRAD;
     constexpr int MROWS = MODE == GP_SWIGLU ? 64 : 128;  // output columns of a CTA's tile
+    constexpr int ACC_STAGES = NT <= 64 || MODE == GP_SWIGLU ? 4 : 8;
     static_assert(!GRAD || NT / CG <= 128, "sixteen pieces of eight columns");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     const uint32_t tmem = *tmem_slot;
     // Accumulators are taken one after another, round tensor memory's slots: an item's one (or, fp32 results, as many as its n
     // stages have use for; GP_LORA's extra stages go to the last of them), the next item's behind it.
-    auto acc_stages = [&](int n) -> int { return OT == MOE_F32 ? max((n + (int)G_::SLOTS - 1) / (int)G_::SLOTS, G_::ACC_STAGES) : max(n, 1); };
+    auto acc_stages = [&](int n) -> int { return OT == MOE_F32 ? max((n + (int)G_::SLOTS - 1) / (int)G_::SLOTS, ACC_STAGES) : max(n, 1); };
     auto acc_count = [&](int n) -> int { return OT == MOE_F32 ? max(1, (n + acc_stages(n) - 1) / acc_stages(n)) : 1; };
     // (GP_LORA: the kernel in front computes u and nothing else; it starts this one when everything before it is
     // complete, and only u is waited for, by the warp that loads it)
@@ -1112,6 +1112,8 @@ static inline int grouped_launch(const GroupedParams &p, int ytype, int mode, bo
 }
 // GP_GRAD: reductions of at most 512 rows on average.
 static inline bool grouped_grad_short(int R, int G) { return R <= 512LL * G; }
+// GP_SWIGLU, fp32 results: reductions that four accumulators of 256 do not hold.
+static inline bool grouped_swiglu_long(int K) { return K > 1024; }
 // SMs of the current device (0: none).
 int grouped_sms();
 // Tensor map of elements of `type`: `rank` dimensions and box extents innermost first, strides in bytes from the second on.
