@@ -216,6 +216,26 @@ def test_gradient_of_rows_outside():
 
 # ------------------------------------------------------------------------------ sizes
 
+# few rows, narrow tiles, pairs; reductions of one accumulator and of several
+@pytest.mark.parametrize("G,R,N,K", [(2, 3, 72, 136), (1, 8, 4096, 2048), (8, 60, 264, 2040), (4, 300, 136, 72), (3, 700, 200, 1024),
+                                     (2, 900, 72, 2048), (2, 500, 8, 4104)])
+@pytest.mark.parametrize("t,out", [("bf16", "f32"), ("f16", "f32"), ("f16", "bf16")])
+def test_swiglu_with_results_of_another_type(G, R, N, K, t, out):
+    rng, g = np.random.default_rng(R), gen(K)
+    offsets = uneven(rng, G, R)
+    x, w = rand(g, t, R, K), rand(g, t, G, 2 * N, K, scale=K ** -0.5)
+    scale = torch.randn(R, generator=g, device="cuda")
+    y = matmul(x, t, torch.from_numpy(offsets).cuda(), w, L.MOE_ORDER_NK, N, K, G=G, R=R, act=L.MOE_ACT_SWIGLU, scale=scale,
+               out=out)
+    for i in range(G):
+        a, b = offsets[i], offsets[i + 1]
+        if b > a:
+            p, e = ref.product(x[a:b], w[i])
+            h, eh = ref.swiglu(p[:, :N], e[:, :N], p[:, N:], e[:, N:])
+            s = scale[a:b, None].double()
+            ref.check(y[a:b], h * s, ref.rounded(h * s, eh * s.abs() + 2.0 ** -24 * (h * s).abs(), out), i)
+
+
 @pytest.mark.parametrize("G,R,N,K", [(64, 1100, 32768, 16), (512, 512, 4096, 8)])
 def test_more_items_than_a_ctas_table(G, R, N, K):
     rng, g = np.random.default_rng(G), gen(G)
