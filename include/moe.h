@@ -563,7 +563,8 @@ int moe_group_rows(const int32_t *ids, int n, int G, int32_t *offsets, int32_t *
  *   x        device [x_rows][ldx], type MOE_BF16 or MOE_F16; 16-byte aligned, ldx >= K a multiple of 8.
  *   x_index  device [R] or NULL; x_share >= 1 positions share a row of x (the k routes of a token).
  *   offsets  device [G + 1], not descending, within [0, R]; a group whose two offsets are no such range is
- *            recorded in the device status word and skipped.  R: the length of the index arrays, at most 2^24
+ *            recorded in the device status word and skipped, and positions that an earlier group has are no part
+ *            of a later one.  R: the length of the index arrays, at most 2^24
  *            (positions from offsets[G] on are not looked at).
  *   w        device [G] matrices of w_order, of type's elements, contiguous, 16-byte aligned.
  *            MOE_ORDER_KN is the order that the gradient of x needs: dx = dy W is this call with dy as x and the forward

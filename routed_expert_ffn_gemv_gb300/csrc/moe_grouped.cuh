@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *bad_item = (volatile int *)(tmem_slot + 2);  // GP_LORA: 1 + the last item with a b that is not finite
     int *sums = (int *)(tmem_slot + 4);                       // [20]
-    int *off = (int *)(smem + G_::O_OFF);                     // [G + 1]
+    int *off = (int *)(smem + G_::O_OFF);                     // [G] where a group's rows begin, -1: it has none
     int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before those of the i-th group ..
     uint16_t *order = (uint16_t *)(smem + G_::O_ORDER);       // [G] .. and which group that is (pairs)
     uint8_t **e_y = (uint8_t **)(smem + G_::O_ROWS);          // [2][NT] the output rows of an accumulator's columns (NULL: none)
@@ -229,9 +229,6 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     const int gt = GRAD ? (p.N + NT - 1) / NT : 0;  // GP_GRAD: tiles of N
     // this CTA's items: unit, unit + units, ..
     const int units = (int)gridDim.x / (CG * ks), unit = (int)blockIdx.x / (CG * ks);
-    auto rows_of = [&](int a, int b) -> int {  // rows of a group; none where the offsets are no range of rows
-        return a >= 0 && b >= a && b <= p.R ? b - a : 0;
-    };
     // item `r` of group g: group and M tile, first row, rows, the group's rows
     auto make_item = [&](int g, int r, int begin, int cnt) -> int4 {
         const int t = r / mt;
@@ -240,17 +237,35 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         const int size = nt == 1 ? NT : ((all + nt - 1) / nt + gran - 1) / gran * gran;
         return make_int4(g | (r - t * mt) << 10, (GRAD ? 0 : begin) + t * size, min(size, all - t * size), cnt);
     };
-    static_assert(MOE_MAX_GROUPS <= 1024 && MOE_MAX_GROUPS <= GP_THREADS, "ten bits of a group, a thread each");
+    static_assert(MOE_MAX_GROUPS <= 1024 && MOE_MAX_GROUPS < GP_THREADS, "ten bits of a group, a thread each");
     {
         // A thread per group: its items behind those of the groups before it, and of them this CTA's to the table.  Pairs:
         // the groups with the most rows first, so that the last round's items are narrow ones (32768 routes over 128
         // experts of uneven popularity, gate/up 198 -> 192 us).  Not GP_GRAD, whose long and short items, bound by the MMAs
         // and by the stores, had better be mixed.
-        int g = tid, begin = tid > p.G ? 0 : p.offsets ? p.offsets[tid] : tid * p.R;
+        int g = tid, begin = tid < p.G && p.offsets ? p.offsets[tid] : 0;
         const int next = tid >= p.G ? 0 : p.offsets ? p.offsets[tid + 1] : p.R;
-        int cnt = tid < p.G ? rows_of(begin, next) : 0;
-        if (tid <= p.G) off[tid] = begin;
-        if (tid < p.G && !cnt && next != begin) moe_set_status(p.status, MOE_ERR_INVALID);
+        const bool bad = begin < 0 || next < begin || next > p.R;  // no range of rows
+        int cnt = bad ? 0 : next - begin;
+        if (bad) moe_set_status(p.status, MOE_ERR_INVALID);
+        if (__syncthreads_or(bad)) {
+            // Offsets that descend somewhere: ranges may overlap.  A group's rows begin behind all that earlier groups have,
+            // so that there are R rows at most, and no more items than the host counted on.
+            int taken = cnt ? next : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int v = __shfl_up_sync(0xffffffffu, taken, d);
+                if (lane >= d) taken = max(taken, v);
+            }
+            if (lane == 31) sums[warp] = taken;
+            const int mine = __shfl_up_sync(0xffffffffu, taken, 1);
+            __syncthreads();
+            const int in_front = (int)__reduce_max_sync(0xffffffffu, (unsigned)(lane < warp ? sums[lane] : 0));
+            if (cnt) begin = min(max(begin, max(in_front, lane ? mine : 0)), next);
+            cnt = cnt ? next - begin : 0;
+            __syncthreads();
+        }
+        if (tid < p.G) off[tid] = cnt ? begin : -1;
         if (CG == 2 && !GRAD && p.G > 1) {
             int *rows = first;
             if (tid < (p.G + 3) / 4 * 4) rows[tid] = cnt;
@@ -301,7 +316,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             else hi = mid;
         }
         const int g = CG == 2 && !GRAD && p.G > 1 ? order[lo] : lo;
-        return make_item(g, at - first[lo], off[g], rows_of(off[g], off[g + 1]));
+        const int begin = off[g];
+        return make_item(g, at - first[lo], begin, begin < 0 ? 0 : (p.offsets ? p.offsets[g + 1] : p.R) - begin);
     };
     auto item_at = [&](int i) -> GroupedItem {
         const int4 v = i < GP_ITEMS ? items[i] : look_up_item(i);

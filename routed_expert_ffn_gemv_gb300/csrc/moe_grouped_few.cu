@@ -61,16 +61,35 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
     pdl_trigger();
     // ---------------- tiles of at most NT rows of a group
     {
-        int base = 0;
+        int base = 0, taken = 0;  // tiles so far; where offsets descend: the end of the rows that earlier groups have
+        bool descend = false;
         for (int g0 = 0; g0 < p.G; g0 += GF_THREADS) {
             const int i = g0 + tid;
-            int begin = 0, cnt = 0;
+            int begin = 0, end = 0;
             if (i < p.G) {
                 begin = p.offsets ? p.offsets[i] : 0;
-                const int end = p.offsets ? p.offsets[i + 1] : p.R;
-                if (begin >= 0 && end >= begin && end <= p.R) cnt = end - begin;
-                else moe_set_status(p.status, MOE_ERR_INVALID);
+                end = p.offsets ? p.offsets[i + 1] : p.R;
             }
+            const bool bad = begin < 0 || end < begin || end > p.R;
+            if (bad) moe_set_status(p.status, MOE_ERR_INVALID);
+            if (!descend && g0) taken = p.offsets[g0];
+            descend |= __syncthreads_or(bad) != 0;
+            if (descend) {  // (see grouped_kernel)
+                int top = bad ? 0 : end;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int v = __shfl_up_sync(0xffffffffu, top, d);
+                    if (lane >= d) top = max(top, v);
+                }
+                if (lane == 31) sums[warp] = top;
+                const int before = __shfl_up_sync(0xffffffffu, top, 1);
+                __syncthreads();
+                const int in_front = (int)__reduce_max_sync(0xffffffffu, (unsigned)(lane < warp ? sums[lane] : 0));
+                begin = max(begin, max(max(in_front, taken), lane ? before : 0));
+                taken = max(taken, (int)__reduce_max_sync(0xffffffffu, (unsigned)(lane < GF_WARPS ? sums[lane] : 0)));
+                __syncthreads();
+            }
+            const int cnt = bad ? 0 : max(0, end - begin);
             const int mine = (cnt + NT - 1) / NT;
             int inc = mine;
 #pragma unroll
@@ -86,7 +105,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
                 if (before + t < GF_MAX_TILES) tiles[before + t] = FewTile{i, begin + t * NT, min(NT, cnt - t * NT)};
             __syncthreads();
         }
-        if (tid == 0) n_tiles_s = min(base, GF_MAX_TILES);  // (the host's bound holds for offsets that do not descend)
+        if (tid == 0) n_tiles_s = min(base, GF_MAX_TILES);
     }
     __syncthreads();
     const int blocks = (p.M + GF_ROWS - 1) / GF_ROWS, n_items = n_tiles_s * blocks;
