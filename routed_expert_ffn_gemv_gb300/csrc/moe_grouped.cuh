@@ -806,8 +806,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(u[k]));
         };
-        // GP_LORA: 32 ranks (by piece c of u) of adapter a for output o of token t, where b is not finite among them, else 0
+        // GP_LORA: 32 ranks (those of piece c of u, with their first piece) of adapter a for output o of token t, where b is not
+        // finite among them, else 0.  By the whole u: an infinity times its parts may be infinities of both signs, or of a part
+        // that is 0, NaN.
         auto not_finite = [&](int a, int c, int o, int t) -> float {
+            if (shift && (c & 1)) return 0.f;
             const uint16_t *b = p.lora_b + ((size_t)a * p.M + o) * p.rank, *u = p.rows + (size_t)t * p.ld + c * 64;
             auto value = [&](uint16_t h) -> float {
                 return p.fmt ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
@@ -818,7 +821,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             for (int k = 0; k < 32 && c0 + k < p.rank; ++k) {
                 const float v = value(b[c0 + k]);
                 bad |= !(fabsf(v) <= 3.4028235e38f);
-                s = fmaf(v, value(u[k]) + value(u[32 + k]), s);
+                s = fmaf(v, value(u[k]) + value(u[32 + k]) + (shift ? value(u[64 + k]) : 0.f), s);
             }
             return bad ? s : 0.f;
         };

@@ -8,6 +8,7 @@
 // the order of the warps.  HBM bounds it: every matrix element is read once, coalesced in 64-byte pieces, 16 rows of them
 // in flight per warp and instruction.
 #include <algorithm>
+#include <cfloat>
 
 #include "moe_grouped.cuh"
 
@@ -40,6 +41,11 @@ template <bool BF>
 __device__ __forceinline__ void mma32(float (&c)[4], const uint4 &lo, const uint4 &hi, const uint4 &x) {
     mma16<BF>(c, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
     mma16<BF>(c, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+}
+
+template <bool BF>
+__device__ __forceinline__ float value16(uint16_t h) {
+    return BF ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
 
 struct FewTile {
@@ -227,6 +233,29 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
                         if (BF && p.parts == 2) mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)(u + 64) : zero);
                     }
                 }
+                // this lane's sums 4 b + i: output g or g + 8 (i / 2), token 8 b + 2 t4 or the one behind it
+                bool odd = false;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        odd |= (who >> (8 * b + 2 * t4 + (i & 1)) & 1) && !(fabsf(part[b][i]) <= FLT_MAX);
+                if (odd)  // an infinity of b times u's parts, one of them 0 or of the other sign: NaN, where b u is an infinity
+                    for (int o = 0; o < 4 * NB; ++o) {
+                        const int t = 8 * (o >> 2) + 2 * t4 + (o & 1);
+                        if (!(who >> t & 1)) continue;
+                        const uint16_t *w = o & 2 ? w1 : w0, *u = p.u + (size_t)(tile.row0 + t) * chunks * p.parts * 64;
+                        float s = 0.f;
+                        for (int j = 0; j < p.rank; ++j) {
+                            const uint16_t *v = u + j / 32 * p.parts * 64 + j % 32;
+                            s = fmaf(value16<BF>(w[j]), value16<BF>(v[0]) + value16<BF>(v[32]) + (p.parts == 2 ? value16<BF>(v[64]) : 0.f), s);
+                        }
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)  // (no index but a constant: the sums stay in registers)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (4 * b + i == o && !(fabsf(part[b][i]) <= FLT_MAX)) part[b][i] = s;
+                    }
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll

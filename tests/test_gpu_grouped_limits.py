@@ -1,11 +1,13 @@
-"""The 16-bit products whose rows choose their matrix at their limits: offsets whose ranges overlap (GPU)."""
+"""The 16-bit products whose rows choose their matrix at their limits: offsets whose ranges overlap, infinite weights of
+adapters (GPU)."""
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import grouped_reference as ref
 from routed_expert_ffn_gemv_gb300 import _lib as L
-from test_gpu_grouped import gen, matmul, rand
+from test_gpu_grouped import gen, lora, matmul, rand
+from test_gpu_grouped_edges import LORA_PATHS
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +74,32 @@ def test_gradient_of_ranges_that_overlap(out, form):
             ref.check(dw[i], v, ref.rounded(v, e, out), i)
         else:
             assert bool((dw[i] == 0).all())
+
+
+# ------------------------------------------------------------------------------ infinite weights
+
+@pytest.mark.parametrize("T,N,K", LORA_PATHS)
+@pytest.mark.parametrize("t,out", [("bf16", "f32"), ("bf16", "bf16"), ("f16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("whole", [True, False])
+def test_an_infinite_weight_gives_what_the_formula_gives(T, N, K, t, out, whole):
+    """inf * u is an infinity of u's sign, however u is held (whole: u has the bits of one part, its others are 0); infinities of both
+    signs, and a NaN, give NaN."""
+    g, n, rank, inf = gen(T + N + whole), 3, 40, float("inf")
+    x, w = rand(g, t, T, K), rand(g, t, N, K, scale=K ** -0.5)
+    a, b = rand(g, t, n, rank, K, scale=K ** -0.5), rand(g, t, n, N, rank, scale=rank ** -0.5)
+    if whole:
+        a.zero_()
+        a[:, torch.arange(rank), torch.arange(rank)] = 1.0
+    adapter = torch.arange(T, device="cuda").int() % n
+    put = [(0, 5, inf), (3, 39, -inf), (N - 1, 32, inf)]                      # one
+    put += [(9, 3, inf), (9, 7, inf), (17, 2, inf), (17, 35, -inf), (33, 38, -inf), (33, 39, float("nan"))]  # two
+    for m, r, v in put:
+        b[1, m, r] = v
+    y = lora(x, t, w, adapter, a, b, None, out)
+    mine = adapter == 1
+    u = x[mine].double() @ a[1].double().T
+    for m in {p[0] for p in put}:
+        want = sum(u[:, r] * v for k, r, v in put if k == m)
+        got = y[mine, m].double()
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[~got.isnan()], want[~want.isnan()]), m
+    assert int((~y.isfinite()).sum()) == int(mine.sum()) * len({p[0] for p in put})
