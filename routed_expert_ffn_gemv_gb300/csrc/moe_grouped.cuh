@@ -859,7 +859,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             auto other = [&](unsigned a) -> uint32_t { return quarter + (seq + a) % G_::SLOTS * NT; };  // the item's a-th accumulator
             uint8_t *const *ys = e_y + buf * NT;
             const float *ss = e_s + buf * NT;
-            const bool none = GRAD && !it.steps;
+            const bool none = GRAD && !it.steps, keep = none && p.accumulate;  // (keep: an empty group's matrix is left as it was)
             const int m0 = (it.m * CG + rank) * MROWS + MROWS / 4 * q;  // the warp's first element
             if (CG == 1 && ks > 1) {
                 // the cluster's only item: each CTA adds up its share of the rows, `per` of them (the last ones fewer)
@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     }
                 }
             } else {
-                for (int c0 = CH * half; c0 < it.n; c0 += 2 * CH) {
+                for (int c0 = CH * half; c0 < it.n && !keep; c0 += 2 * CH) {
                     if (F32 && MODE != GP_SWIGLU) {
                         uint32_t v[CH / 16][16];
 #pragma unroll

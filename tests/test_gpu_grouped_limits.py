@@ -1,5 +1,5 @@
 """The 16-bit products whose rows choose their matrix at their limits: offsets whose ranges overlap, infinite weights of
-adapters (GPU)."""
+adapters, empty groups (GPU)."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -103,3 +103,28 @@ def test_an_infinite_weight_gives_what_the_formula_gives(T, N, K, t, out, whole)
         got = y[mine, m].double()
         assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[~got.isnan()], want[~want.isnan()]), m
     assert int((~y.isfinite()).sum()) == int(mine.sum()) * len({p[0] for p in put})
+
+
+# ------------------------------------------------------------------------------ empty groups
+
+@pytest.mark.parametrize("G,R,N,K", [(5, 300, 72, 136), (3, 4000, 520, 64)])
+@pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
+def test_accumulation_leaves_empty_groups_bit_for_bit(G, R, N, K, out):
+    g, bits = gen(R), torch.int32 if out == "f32" else torch.int16
+    x, dy = rand(g, "bf16", R, K), rand(g, "bf16", R, N)
+    dw = torch.randint(-2 ** (31 if out == "f32" else 15), 2 ** (31 if out == "f32" else 15), (G, N, K), generator=g, device="cuda",
+                       dtype=torch.int64).to(bits).view(ref.dtype(out))  # any bits: NaN, subnormal values and both zeros among them
+    dw[:, 0] = -0.0
+    o = [0, 0] + [R // 2] * (G - 2) + [R]
+    dw[1] = dw[G - 1] = 0.25
+    was = dw.clone()
+    L.moe_grouped_weight_grad(x, L.MOE_BF16, R, K, None, 1, dy, R, N, None, torch.tensor(o, dtype=torch.int32, device="cuda"), G, R, N,
+                              K, 1, dw, ref.code(out))
+    torch.cuda.synchronize()
+    for i in range(G):
+        a, b = o[i], o[i + 1]
+        if a == b:
+            assert torch.equal(dw[i].view(bits), was[i].view(bits)), i
+        else:
+            v, e = ref.product(dy[a:b].T, x[a:b].T)
+            ref.check(dw[i], v + 0.25, ref.rounded(v + 0.25, e + 2.0 ** -24 * ((v + 0.25).abs() + e), out), i)
