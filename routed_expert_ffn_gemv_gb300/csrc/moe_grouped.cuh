@@ -77,8 +77,11 @@ struct GroupedParams {
 
 // A sum on the tensor cores drops, at each of its steps of 16, what lies below the last bit of the larger term: 128 steps
 // (K = 2048) leave it 1.6e-6 off, relative to the result's norm, which bf16 and fp16 results do not show and fp32 results do
-// (fp32 sums rounded to nearest: 1.5e-7).  For fp32 results the stages are therefore shared out over several accumulators,
-// ACC_STAGES stages or more each, that the epilogue adds up in order (32 steps each: 4.7e-7).
+// (fp32 sums rounded to nearest: 1.5e-7).  An accumulator therefore takes ACC_STAGES stages at most, and the epilogue adds an
+// item's accumulators up in order: for fp32 results 16 or 32 steps each (2.3e-7, 4.7e-7), for 16-bit ones 512 (6e-6, where
+// fp16's half step is 4.9e-4).  Of more accumulators than tensor memory holds, the epilogue adds the first to the second and
+// hands it back while the others are filled, and so on: the error does not grow with the reduction (K = 65536, pairs:
+// 1.9e-5 off with four accumulators, 5.1e-7 this way).
 
 template <int CG, int NT, int OT>
 struct GroupedGeom {
@@ -100,7 +103,7 @@ struct GroupedGeom {
     static constexpr int O_RING = (O_RED + RED + 1023) / 1024 * 1024;
     static constexpr int S = (227 * 1024 - 1024 - O_RING) / STAGE / 2 * 2;  // (even: see the loaders)
     static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
-    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 2 * SLOTS + 2) * 8 + 16 + 80 <= 1024 && S >= 6, "");
+    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 2 * SLOTS + 2) * 8 + 16 + 80 + 64 <= 1024 && S >= 6, "");
 };
 
 struct GroupedItem {
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     constexpr int S = G_::S;
     constexpr bool GRAD = MODE == GP_GRAD, A_MN = GRAD || MODE == GP_KN, B_MN = GRAD;
     constexpr int MROWS = MODE == GP_SWIGLU ? 64 : 128;  // output columns of a CTA's tile
-    constexpr int ACC_STAGES = NT <= 64 || MODE == GP_SWIGLU ? 4 : 8;
+    constexpr int ACC_STAGES = OT != MOE_F32 ? 128 : NT <= 64 || MODE == GP_SWIGLU ? 4 : 8;
     static_assert(!GRAD || NT / CG <= 128, "sixteen pieces of eight columns");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
@@ -179,6 +182,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *bad_item = (volatile int *)(tmem_slot + 2);  // GP_LORA: 1 + the last item with a b that is not finite
     int *sums = (int *)(tmem_slot + 4);                       // [20]
+    int *has_adapters = sums + 20;                            // GP_LORA: [2][8] for each epilogue warp's columns of an item
     int *off = (int *)(smem + G_::O_OFF);                     // [G] where a group's rows begin, -1: it has none
     int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before those of the i-th group ..
     uint16_t *order = (uint16_t *)(smem + G_::O_ORDER);       // [G] .. and which group that is (pairs)
@@ -214,10 +218,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     if (CG == 2 || ks > 1) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // Accumulators are taken one after another, round tensor memory's slots: an item's one (or, fp32 results, as many as its n
-    // stages have use for; GP_LORA's extra stages go to the last of them), the next item's behind it.
-    auto acc_stages = [&](int n) -> int { return OT == MOE_F32 ? max((n + (int)G_::SLOTS - 1) / (int)G_::SLOTS, ACC_STAGES) : max(n, 1); };
-    auto acc_count = [&](int n) -> int { return OT == MOE_F32 ? max(1, (n + acc_stages(n) - 1) / acc_stages(n)) : 1; };
+    // Accumulators are taken one after another, round tensor memory's slots: an item's (as many as its n stages have use for,
+    // then `apart` for GP_LORA's extra stages; none: those go to the last one), the next item's behind them.
+    // apart: fp32 results, one for the first 128 ranks of every adapter and one for the others (a token has zeros in the stages
+    // of all adapters but one, which lose nothing)
+    const int apart = MODE == GP_LORA && OT == MOE_F32 ? (p.rank > 128 ? 2 : 1) : 0;
+    auto acc_count = [&](int n) -> int { return max(1, (n + ACC_STAGES - 1) / ACC_STAGES); };
     // (GP_LORA: the kernel in front computes u and nothing else; it starts this one when everything before it is
     // complete, and only u is waited for, by the warp that loads it)
     if (MODE != GP_LORA) pdl_wait();
@@ -697,49 +703,59 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 fresh = true;
                 return true;
             };
-            const unsigned begun = seq;
             if (!take()) break;
             const int len = GRAD ? __shfl_sync(0xffffffffu, it.cnt, 0) : p.K;
-            const int per = __shfl_sync(0xffffffffu, acc_stages(hi - lo), 0);
-            int left_in_acc = per;
-            for (int kb = lo; kb < hi; ++kb) {
-                if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
-                tc_fence_after();
-                const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
-                const uint64_t a = A_MN ? umma_desc_mn_sw128(sa, 8192) : umma_desc_sw128(sa);
-                const uint64_t b = B_MN ? umma_desc_mn_sw128(sa + GP_ABYTES, 8192) : umma_desc_sw128(sa + GP_ABYTES);
-                if (OT == MOE_F32 && left_in_acc == 0) {
-                    left_in_acc = per;
-                    if (!take()) break;
+            for (int kb = lo; ok;) {  // (an accumulator's stages by themselves: its address stays in a uniform register)
+                const uint32_t acc = d;
+                for (const int end = min(hi, kb + ACC_STAGES); kb < end; ++kb) {
+                    if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
+                    const uint64_t a = A_MN ? umma_desc_mn_sw128(sa, 8192) : umma_desc_sw128(sa);
+                    const uint64_t b = B_MN ? umma_desc_mn_sw128(sa + GP_ABYTES, 8192) : umma_desc_sw128(sa + GP_ABYTES);
+                    const int left = len - 64 * kb;
+                    auto step = [&](int q) {
+                        umma_f16_elect<CG>(acc, a + (uint64_t)(q * (A_MN ? 128 : 2)), b + (uint64_t)(q * (B_MN ? 128 : 2)), idesc,
+                                           q > 0 || !fresh);
+                    };
+                    step(0);
+                    if (left > 48) {  // (no branch between the MMAs)
+                        step(1);
+                        step(2);
+                        step(3);
+                    } else {
+                        if (left > 16) step(1);
+                        if (left > 32) step(2);
+                    }
+                    fresh = false;
+                    umma_commit_group_elect<CG>(&empty[st]);
+                    if (++st == S) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
-                --left_in_acc;
-                const int left = len - 64 * kb;
-                auto step = [&](int q) {
-                    umma_f16_elect<CG>(d, a + (uint64_t)(q * (A_MN ? 128 : 2)), b + (uint64_t)(q * (B_MN ? 128 : 2)), idesc,
-                                       q > 0 || !fresh);
-                };
-                step(0);
-                if (left > 48) {  // (no branch between the MMAs)
-                    step(1);
-                    step(2);
-                    step(3);
-                } else {
-                    if (left > 16) step(1);
-                    if (left > 32) step(2);
-                }
-                fresh = false;
-                umma_commit_group_elect<CG>(&empty[st]);
-                if (++st == S) {
-                    st = 0;
-                    ph ^= 1u;
-                }
+                if (!ok || kb >= hi) break;
+                umma_commit_group_elect<CG>(&acc_full[(seq - 1) % G_::SLOTS]);
+                if (!take()) break;
             }
+            uint32_t dx[2] = {d, d};
+            bool fresh_x[2] = {fresh, fresh};
             if (MODE == GP_LORA) {
                 check_adapters(ids);
                 share(__shfl_sync(0xffffffffu, extra_stages(ids), 0), lo, hi);
+                if (apart && ok) umma_commit_group_elect<CG>(&acc_full[(seq - 1) % G_::SLOTS]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (x < apart && ok && take()) {
+                        dx[x] = d;
+                        fresh_x[x] = true;
+                    }
             }
             for (int e = lo, c = MODE == GP_LORA ? lo % chunks : 0; MODE == GP_LORA && e < hi && ok; ++e) {
                 if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
+                const bool other = apart == 2 && c >= 4 * p.parts;  // (pieces of 32 ranks)
+                const uint32_t d = other ? dx[1] : dx[0];
+                const bool fresh = other ? fresh_x[1] : fresh_x[0];
                 tc_fence_after();
                 // 32 ranks: u's upper halves in the first 64 bytes of a row, the rest of u in the second, both by the same B_a
                 const uint32_t sa = smem_u32(ring) + (uint32_t)st * G_::STAGE;
@@ -750,7 +766,8 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     umma_f16_elect<CG>(d, a + 2, b + 2, idesc, 1);
                     umma_f16_elect<CG>(d, a + 2, b + 6, idesc, 1);
                 }
-                fresh = false;
+                fresh_x[0] &= other;
+                fresh_x[1] &= !other;
                 if (++c == chunks) c = 0;
                 umma_commit_group_elect<CG>(&empty[st]);
                 if (++st == S) {
@@ -759,7 +776,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 }
             }
             if (ok)
-                for (unsigned a = begun; a < seq; ++a) umma_commit_group_elect<CG>(&acc_full[a % G_::SLOTS]);
+                for (unsigned a = seq - max(apart, 1); a < seq; ++a) umma_commit_group_elect<CG>(&acc_full[a % G_::SLOTS]);
         }
         umma_commit_group_elect<CG>(mma_done);  // every MMA has completed before tensor memory is released
         mbar_wait_bounded(mma_done, 0, p.status);
@@ -781,7 +798,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         int ix = 0, iy = 0;
         uint8_t *row = nullptr;
         float scale = 1.f;
+        int ia = -1;  // GP_LORA: its adapter
         auto fetch = [&](const GroupedItem &it) {
+            if (MODE == GP_LORA) ia = et < it.n ? p.adapter[it.row0 + et] : -1;
             if (GRAD || et >= it.n) return;
             ix = p.x_index ? p.x_index[it.row0 + et] : it.row0 + et;
             iy = p.y_index ? p.y_index[it.row0 + et] : it.row0 + et;
@@ -825,7 +844,13 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             }
             return bad ? s : 0.f;
         };
-        unsigned seq = 0;  // accumulators before this item's
+        unsigned seq = 0;  // accumulators handed back so far
+        auto hand_back = [&](unsigned a) {
+            if (lane == 0) {
+                if (CG == 1) mbar_arrive1(&acc_empty[a % G_::SLOTS]);
+                else mbar_arrive_cluster(cluster_map(&acc_empty[a % G_::SLOTS], 0));
+            }
+        };
         GroupedItem it = {};
         if (n_mine) {
             it = item_at(0);
@@ -838,25 +863,65 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 e_y[buf * NT + et] = row;
                 e_s[buf * NT + et] = scale;
             }
+            if (MODE == GP_LORA && apart) {
+                const bool any = __any_sync(0xffffffffu, ia >= 0 && ia < p.n_adapters);
+                if (lane == 0) has_adapters[buf * 8 + ew] = any;
+            }
             GroupedItem nx = {};
             if (j + 1 < n_mine) {
                 nx = item_at(j + 1);
                 fetch(nx);
             }
-            unsigned used = 1;  // accumulators
-            if (OT == MOE_F32) {
+            unsigned used;  // accumulators
+            {
                 int lo, hi;
                 share(it.steps, lo, hi);
                 used = acc_count(hi - lo);
             }
+            const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16);
             bool w = true;
-            for (unsigned a = seq; a < seq + used && w; ++a)
+            // as many as the last pass adds up: those that tensor memory holds, one for 16-bit results
+            const unsigned held = F32 ? G_::SLOTS - apart : 1;
+            for (; used > held && w; --used, ++seq) {  // the first added to the second (the columns that are this warp's below, too)
+                for (unsigned a = seq; a < seq + 2 && w; ++a)
+                    w = mbar_wait_warp(&acc_full[a % G_::SLOTS], (a / G_::SLOTS) & 1, p.status, abort_flag);
+                if (!w) break;
+                tc_fence_after();
+                const uint32_t from = quarter + seq % G_::SLOTS * NT, to = quarter + (seq + 1) % G_::SLOTS * NT;
+                for (int c0 = CH * half; c0 < it.n; c0 += 2 * CH)
+#pragma unroll
+                    for (int h = 0; h < CH; h += 16) {
+                        uint32_t v[16];
+                        tmem_ld16(from + c0 + h, v);
+                        add16(v, to + c0 + h);
+                        tmem_st16(to + c0 + h, v);
+                    }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                hand_back(seq);
+            }
+            for (unsigned a = seq; a < seq + used + apart && w; ++a)
                 w = mbar_wait_role(&acc_full[a % G_::SLOTS], (a / G_::SLOTS) & 1, p.status, abort_flag);
             if (!bar_and_n(1, 256, w)) break;
             if (j + 1 < n_mine) resolve(nx);
             tc_fence_after();
-            const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16), tb = quarter + seq % G_::SLOTS * NT;
+            const uint32_t tb = quarter + seq % G_::SLOTS * NT;
             auto other = [&](unsigned a) -> uint32_t { return quarter + (seq + a) % G_::SLOTS * NT; };  // the item's a-th accumulator
+            // GP_LORA: of this CTA's extra stages the range; of the accumulators that are apart, those that some of them went to (1 the
+            // first, 2 the second)
+            int elo = 0, ehi = 0, added = 0;
+            if (MODE == GP_LORA && ks > 1) {
+                int ids[8];
+                read_adapters(it, ids);
+                check_adapters(ids);
+                share(extra_stages(ids), elo, ehi);
+                for (int e = elo; e < min(ehi, elo + chunks); ++e) added |= apart == 2 && e % chunks >= 4 * p.parts ? 2 : 1;
+            } else if (MODE == GP_LORA && apart) {
+                const int4 *h = (const int4 *)(has_adapters + buf * 8);
+                const int4 a = h[0], b = h[1];
+                if (a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) added = 3;
+            }
             uint8_t *const *ys = e_y + buf * NT;
             const float *ss = e_s + buf * NT;
             const bool none = GRAD && !it.steps, keep = none && p.accumulate;  // (keep: an empty group's matrix is left as it was)
@@ -864,15 +929,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             if (CG == 1 && ks > 1) {
                 // the cluster's only item: each CTA adds up its share of the rows, `per` of them (the last ones fewer)
                 const int per = (it.n + ks - 1) / ks, own = max(0, min(per, it.n - kr * per));
-                int lo, hi, n, ids[8];
+                int lo, hi;
                 share(it.steps, lo, hi);
-                n = hi - lo;
-                if (MODE == GP_LORA) {
-                    read_adapters(it, ids);
-                    check_adapters(ids);
-                    share(extra_stages(ids), lo, hi);
-                    n += hi - lo;
-                }
+                const bool some = hi > lo || (!apart && ehi > elo);  // (else nothing was summed)
                 float *x = (float *)(smem + G_::O_XCH);  // [NT][128]
                 static_assert(CG == 2 || NT * 512 <= 8 * G_::XCH, "sums of an item");
                 if (16 * half < it.n) {
@@ -880,14 +939,21 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     tmem_ld16(tb + 16 * half, v);
                     tmem_ld_wait();
                     for (unsigned a = 1; a < used; ++a) add16(v, other(a) + 16 * half);
+                    if (!some)
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[(16 * half + k) * 128 + 32 * q + lane] = n ? __uint_as_float(v[k]) : 0.f;
+                        for (int k = 0; k < 16; ++k) v[k] = 0u;
+                    for (int a = 0; a < apart; ++a)
+                        if (added >> a & 1) add16(v, other(used + a) + 16 * half);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[(16 * half + k) * 128 + 32 * q + lane] = __uint_as_float(v[k]);
                 }
                 if (MODE == GP_LORA && *bad_item > j) {
-                    int e = 0;
+                    int e = 0, ids[8];
+                    read_adapters(it, ids);
+                    check_adapters(ids);
                     for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a))
                         for (int c = 0; c < chunks; ++c, ++e)
-                            if (e >= lo && e < hi && m0 + lane < p.M)
+                            if (e >= elo && e < ehi && m0 + lane < p.M)
                                 for (int k = 16 * half; k < min(it.n, 16 * half + 16); ++k)
                                     if (p.adapter[it.row0 + k] == a)
                                         x[k * 128 + 32 * q + lane] += not_finite(a, c, m0 + lane, it.row0 + k);
@@ -938,6 +1004,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         for (unsigned a = 1; a < used; ++a)
 #pragma unroll
                             for (int h = 0; h < CH / 16; ++h) add16(v[h], other(a) + c0 + 16 * h);
+                        for (int a = 0; a < apart; ++a)
+                            if (added >> a & 1)
+#pragma unroll
+                                for (int h = 0; h < CH / 16; ++h) add16(v[h], other(used + a) + c0 + 16 * h);
                         float *x = (float *)(smem + G_::O_XCH + ew * G_::XCH);
                         if (GRAD) {  // whole boxes by TMA: see below
                             if (lane == 0) tma_store_wait_read();
@@ -978,7 +1048,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     tmem_ld_16x256b(tb + c0, lo);
                     tmem_ld_16x256b(tb + (16u << 16) + c0, hi);
                     tmem_ld_wait();
-                    for (unsigned a = 1; a < used; ++a) {  // (F32)
+                    for (unsigned a = 1; F32 && a < used; ++a) {
                         uint32_t u[4 * NB];
                         tmem_ld_16x256b(other(a) + c0, u);
                         tmem_ld_wait();
@@ -1096,12 +1166,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-                for (unsigned a = seq; a < seq + used; ++a) {
-                    if (CG == 1) mbar_arrive1(&acc_empty[a % G_::SLOTS]);
-                    else mbar_arrive_cluster(cluster_map(&acc_empty[a % G_::SLOTS], 0));
-                }
-            seq += used;
+            for (used += apart; used; --used, ++seq) hand_back(seq);
             it = nx;
         }
         if (GRAD && lane == 0) tma_store_wait();

@@ -5,7 +5,7 @@
 // the fragments of mma.sync m16n8k16 (the reduction's order is free: a lane's 16 bytes of a row, eight consecutive
 // elements, are its share of two steps, and the same eight of its token's row the other side's), for up to 32 rows of the
 // group.  A CTA's eight warps share the reduction in turns of 32 elements and add their sums up in shared memory in
-// the order of the warps.  HBM bounds it: every matrix element is read once, coalesced in 64-byte pieces, 16 rows of them
+// the order of the warps (a warp's own of more than eight turns as well: its MMAs' sums truncate, see moe_grouped.cuh).  HBM bounds it: every matrix element is read once, coalesced in 64-byte pieces, 16 rows of them
 // in flight per warp and instruction.
 #include <algorithm>
 #include <cfloat>
@@ -179,6 +179,9 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
             s_scale[tid] = scale;
         }
         float acc[MATS][NB][4] = {};
+        auto sum_at = [&](int m, int b, int i) -> float & { return red[warp][m][8 * b + 2 * t4 + (i & 1)][g + 4 * (i & 2)]; };
+        bool kept = false;  // sums of turns so far are there
+        auto total = [&](int m, int b, int i) -> float { return kept ? sum_at(m, b, i) + acc[m][b][i] : acc[m][b][i]; };
         // ---------------- the matrix by the tile's rows
         for (int i0 = 0; i0 < turns; i0 += PF) {
 #pragma unroll
@@ -191,6 +194,19 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
                     for (int m = 0; m < MATS; ++m) mma32<BF>(acc[m][b], a[i][m][0], a[i][m][1], v);
                 }
                 if (i0 + PF < turns) fetch(a[i], i0 + PF + i);
+            }
+            constexpr int BATCHES = (8 + PF - 1) / PF;
+            if (i0 + PF < turns && i0 / PF % BATCHES == BATCHES - 1) {
+#pragma unroll
+                for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            sum_at(m, b, i) = total(m, b, i);
+                            acc[m][b][i] = 0.f;
+                        }
+                kept = true;
             }
         }
         if (item + (int)gridDim.x < n_items) {
@@ -269,7 +285,7 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) red[warp][m][8 * b + 2 * t4 + (i & 1)][g + 4 * (i & 2)] = acc[m][b][i];
+                for (int i = 0; i < 4; ++i) sum_at(m, b, i) = total(m, b, i);
         __syncthreads();
         for (int i = tid; i < tile.n * 8; i += GF_THREADS) {
             const int c = i >> 3, r = 2 * (i & 7), o = m0 + r;

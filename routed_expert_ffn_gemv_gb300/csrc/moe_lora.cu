@@ -57,24 +57,30 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
     float v[LS_RANKS] = {};
     if (j0 < rank) {
         const uint16_t *xr = x + (size_t)t * ldx, *ar = a + ((size_t)ad * rank + j0) * K;
+        for (int k0 = 0; k0 < K; k0 += 2048) {  // (sums of 64 products a lane, and their sum: K = 65536 in one go 8e-7 off)
+            float part[LS_RANKS] = {};
+            const int end = min(K, k0 + 2048);
 #pragma unroll 4
-        for (int k = 8 * lane; k < K; k += 256) {  // (several turns' loads in flight)
-            const uint4 xv = __ldg((const uint4 *)(xr + k));
-            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-            uint4 avs[LS_RANKS];
+            for (int k = k0 + 8 * lane; k < end; k += 256) {  // (several turns' loads in flight)
+                const uint4 xv = __ldg((const uint4 *)(xr + k));
+                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                uint4 avs[LS_RANKS];
 #pragma unroll
-            for (int j = 0; j < LS_RANKS; ++j) avs[j] = __ldg((const uint4 *)(ar + (size_t)j * K + k));
+                for (int j = 0; j < LS_RANKS; ++j) avs[j] = __ldg((const uint4 *)(ar + (size_t)j * K + k));
 #pragma unroll
-            for (int j = 0; j < LS_RANKS; ++j) {  // (the rank is a multiple of 8)
-                const uint4 av = avs[j];
-                const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
+                for (int j = 0; j < LS_RANKS; ++j) {  // (the rank is a multiple of 8)
+                    const uint4 av = avs[j];
+                    const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 p = pair_value<BF>(xw[i]), q = pair_value<BF>(aw[i]);
-                    v[j] = fmaf(p.x, q.x, v[j]);
-                    v[j] = fmaf(p.y, q.y, v[j]);
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 p = pair_value<BF>(xw[i]), q = pair_value<BF>(aw[i]);
+                        part[j] = fmaf(p.x, q.x, part[j]);
+                        part[j] = fmaf(p.y, q.y, part[j]);
+                    }
                 }
             }
+#pragma unroll
+            for (int j = 0; j < LS_RANKS; ++j) v[j] += part[j];
         }
 #pragma unroll
         for (int j = 0; j < LS_RANKS; ++j)
@@ -113,6 +119,7 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
 struct ShrinkParams {
     CUtensorMap x, a;  // x by boxes of 128 rows, A by adapters
     int T, K, rank, n_adapters, per_pass, fmt, parts;  // per_pass: adapters of a pass
+    int acc_stages;    // most stages of an accumulator
     const int32_t *adapter;
     const float *scale;
     uint16_t *u;       // [T][chunks][parts][64]
@@ -120,7 +127,7 @@ struct ShrinkParams {
 };
 
 struct ShrinkSmem {
-    uint64_t full[LS_STAGES], empty[LS_STAGES], done;
+    uint64_t full[LS_STAGES], empty[LS_STAGES], acc_full[2], acc_empty[2], done;
     uint32_t tmem;
     int abort;
     int count[LS_TOKENS / 32];
@@ -153,6 +160,10 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
         for (int i = 0; i < LS_STAGES; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.acc_full[i], 1);
+            mbar_init(&s.acc_empty[i], LS_TOKENS / 32);
         }
         mbar_init(&s.done, 1);
         s.abort = 0;
@@ -205,7 +216,10 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
             if (mine >= used) mine = -1;
             s.mine[tid] = max(mine, -1);
         }
-        const int KB = (p.K + 63) / 64, kb0 = KB * me / ctas, kb1 = KB * (me + 1) / ctas, second = (kb0 + kb1 + 1) / 2;
+        const int KB = (p.K + 63) / 64, kb0 = KB * me / ctas, kb1 = KB * (me + 1) / ctas;
+        // accumulators of `per` stages, in turn the first and the second half of tensor memory; of more than two, warps 0 to 3 add
+        // each to the next one, and hand it back, while that one is filled (see moe_grouped.cuh)
+        const int per = max(1, min(p.acc_stages, (kb1 - kb0 + 1) / 2)), accs = (kb1 - kb0 + per - 1) / per;
         if (warp == 4) {
             // ---------------- copies
             int st = 0;
@@ -233,23 +247,51 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
             const uint32_t d0 = __shfl_sync(0xffffffffu, s.tmem, 0);
             const uint32_t idesc = umma_idesc_16(p.fmt, false, false, 128, __shfl_sync(0xffffffffu, (used * p.rank + 15) & ~15, 0));
             for (int kb = kb0; kb < kb1; ++kb) {
+                const int acc = (kb - kb0) / per, half = acc & 1;
+                const bool fresh = kb - kb0 == acc * per;
+                if (fresh && acc >= 2 && !mbar_wait_warp(&s.acc_empty[half], (acc / 2 - 1) & 1, p.status, &s.abort)) break;
                 if (!mbar_wait_warp(&s.full[st], ph, p.status, &s.abort)) break;
                 tc_fence_after();
                 const uint32_t sa = smem_u32(ring) + (uint32_t)st * LS_STAGE;
                 const uint64_t a = umma_desc_sw128(sa), b = umma_desc_sw128(sa + LS_TOKENS * 128);
                 const int left = p.K - 64 * kb;
-                const uint32_t d = d0 + (kb >= second ? LS_COLS : 0);
-                umma_f16_elect<1>(d, a, b, idesc, kb > kb0 && kb != second);
+                const uint32_t d = d0 + half * LS_COLS;
+                umma_f16_elect<1>(d, a, b, idesc, !fresh);
                 if (left > 16) umma_f16_elect<1>(d, a + 2, b + 2, idesc, 1);
                 if (left > 32) umma_f16_elect<1>(d, a + 4, b + 4, idesc, 1);
                 if (left > 48) umma_f16_elect<1>(d, a + 6, b + 6, idesc, 1);
                 umma_commit_elect(&s.empty[st]);
+                if (kb + 1 == kb1 || kb + 1 - kb0 == (acc + 1) * per) umma_commit_elect(&s.acc_full[half]);
                 if (++st == LS_STAGES) {
                     st = 0;
                     ph ^= 1u;
                 }
             }
             umma_commit_elect(&s.done);  // every copy has been consumed, every MMA has completed
+        } else if (warp < 4) {
+            const uint32_t tb = s.tmem + ((uint32_t)(32 * warp) << 16);
+            for (int acc = 0; acc + 2 < accs; ++acc) {
+                if (!mbar_wait_warp(&s.acc_full[acc & 1], (acc / 2) & 1, p.status, &s.abort)) break;
+                if (!mbar_wait_warp(&s.acc_full[(acc + 1) & 1], ((acc + 1) / 2) & 1, p.status, &s.abort)) break;
+                tc_fence_after();
+                const uint32_t from = tb + (acc & 1) * LS_COLS, to = tb + ((acc + 1) & 1) * LS_COLS;
+                for (int i = 0; i < used; ++i) {
+                    if (!__any_sync(0xffffffffu, mine == i)) continue;
+                    for (int c = i * p.rank; c < (i + 1) * p.rank; c += 8) {
+                        uint32_t v[8], w[8];
+                        tmem_ld8(from + c, v);
+                        tmem_ld8(to + c, w);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
+                        tmem_st8(to + c, w);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive1(&s.acc_empty[acc & 1]);
+            }
         }
         __syncwarp();
         const bool ok = mbar_wait_role(&s.done, 0, p.status, &s.abort);
@@ -267,7 +309,7 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
                     uint32_t v[8];
                     tmem_ld8(tb + i * p.rank + c, v);
                     tmem_ld_wait();
-                    if (second < kb1) {
+                    if (accs > 1) {
                         uint32_t w[8];
                         tmem_ld8(tb + LS_COLS + i * p.rank + c, w);
                         tmem_ld_wait();
@@ -345,7 +387,7 @@ int shrink_few(const void *x, size_t ldx, int T, int K, int type, const int32_t 
 }
 
 int shrink_many(const void *x, size_t ldx, int T, int K, int type, const int32_t *adapter, int n_adapters, const void *a,
-                int rank, const float *scale, void *u, int parts, int *status, moe_stream_t s) {
+                int rank, const float *scale, void *u, int parts, int acc_stages, int *status, moe_stream_t s) {
     static std::mutex mu;
     static bool ready[64] = {false};
     int dev = -1, rc;
@@ -382,6 +424,7 @@ int shrink_many(const void *x, size_t ldx, int T, int K, int type, const int32_t
     p.scale = scale;
     p.u = (uint16_t *)u;
     p.parts = parts;
+    p.acc_stages = acc_stages;
     p.status = status;
     const int tiles = (T + LS_TOKENS - 1) / LS_TOKENS, most = std::min(n_adapters, LS_TOKENS);
     const int passes = (most + p.per_pass - 1) / p.per_pass;
@@ -427,8 +470,9 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     int *status = moe_status_word_device_ptr();
     // bf16 with fp32 results: u in three parts, 24 bits (two leave y 1.8e-6 off, relative to its norm, three 3e-7)
     const int parts = type == MOE_BF16 && ytype == MOE_F32 ? 2 : 1;
+    const int acc_stages = ytype == MOE_F32 ? 4 : 64;
     rc = T <= LS_FEW ? shrink_few(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, parts, s)
-                     : shrink_many(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, parts, status, s);
+                     : shrink_many(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, parts, acc_stages, status, s);
     if (rc != MOE_OK) return rc;
     // few tokens, and no more rows of W than CTAs run at once (N = 2816: 1 token 12.1 -> 8.4 us, 32 tokens 20.2 -> 12.4 by the
     // kernel for few rows; N = 11264: 15.1 -> 14.9 and 21.1 -> 29.9)

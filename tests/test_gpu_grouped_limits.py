@@ -1,5 +1,5 @@
 """The 16-bit products whose rows choose their matrix at their limits: offsets whose ranges overlap, infinite weights of
-adapters, empty groups (GPU)."""
+adapters, empty groups, long reductions (GPU)."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -128,3 +128,94 @@ def test_accumulation_leaves_empty_groups_bit_for_bit(G, R, N, K, out):
         else:
             v, e = ref.product(dy[a:b].T, x[a:b].T)
             ref.check(dw[i], v + 0.25, ref.rounded(v + 0.25, e + 2.0 ** -24 * ((v + 0.25).abs() + e), out), i)
+
+
+# ------------------------------------------------------------------------------ long reductions
+
+# Relative to the results' norm.  A step of 16 in an MMA drops less than a unit of the sum so far, half of one on average: between
+# 2^-25 and 2^-24 of the sum, 0.72 2^-24 on average, and a sum of independent terms is on its way two thirds of what it ends
+# at.  32 steps: 32 * 0.72 * 2^-24 * 2 / 3 = 0.92e-6, if every loss pointed the same way.  Sums of accumulators, rounded to nearest,
+# add 1.4e-8 sqrt(their number): 0.2e-6 for 256 of them, in quadrature.
+FP32_SUMS = 1e-6
+
+
+def off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+def product_off(g, G, R, N, K, t="bf16", out="f32", order=L.MOE_ORDER_NK, act=L.MOE_ACT_NONE):
+    """How far a product of equal groups is off, and how far the exact one would be once rounded."""
+    x, w = rand(g, t, R, K), rand(g, t, G, 2 * N if act else N, K, scale=K ** -0.5)
+    o = [i * R // G for i in range(G + 1)]
+    y = matmul(x, t, torch.tensor(o, dtype=torch.int32, device="cuda"), w if order == L.MOE_ORDER_NK else w.transpose(1, 2).contiguous(),
+               order, N, K, G=G, R=R, act=act, out=out)
+    want = torch.cat([x[a:b].double() @ w[i].double().T for i, (a, b) in enumerate(zip(o, o[1:]))])
+    if act:
+        want = want[:, :N] * torch.sigmoid(want[:, :N]) * want[:, N:]
+    return off(y, want), off(want.to(y.dtype), want)
+
+
+# few rows, a matrix too large for that, narrow tiles that share their reduction, narrow tiles, pairs
+@pytest.mark.parametrize("G,R,N", [(1, 4, 64), (1, 8, 6400), (4, 40, 256), (16, 200, 1280), (2, 512, 256)])
+@pytest.mark.parametrize("K", [1024, 1032, 2048, 8192, 65536])
+@pytest.mark.parametrize("form", ["nk", "kn", "swiglu"])
+def test_fp32_sums_do_not_lose_with_the_reduction(G, R, N, K, form):
+    if N * K * G > 2 ** 29:
+        N = 2 ** 26 // K
+    e, _ = product_off(gen(K), G, R, N, K, order=L.MOE_ORDER_KN if form == "kn" else L.MOE_ORDER_NK,
+                       act=L.MOE_ACT_SWIGLU if form == "swiglu" else L.MOE_ACT_NONE)
+    assert e <= FP32_SUMS
+
+
+@pytest.mark.parametrize("G,R,N", [(1, 4, 64), (4, 40, 256), (2, 512, 256)])
+@pytest.mark.parametrize("K", [2048, 65536])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("act", [L.MOE_ACT_NONE, L.MOE_ACT_SWIGLU])
+def test_16_bit_results_of_long_reductions(G, R, N, K, t, act):
+    """What the sums lose (at most 2e-5) is not seen beside the rounding (fp16: 2e-4), in quadrature one percent of it."""
+    e, least = product_off(gen(K), G, R, N, K, t=t, out=t, act=act)
+    assert e <= 1.01 * least
+
+
+def gradient_off(g, o, N, K, out, accumulate=False):
+    G, R = len(o) - 1, o[-1]
+    x, dy = rand(g, "f16", R, K), rand(g, "f16", R, N, scale=max(b - a for a, b in zip(o, o[1:])) ** -0.5)
+    dw = torch.zeros(G, N, K, dtype=ref.dtype(out), device="cuda")
+    L.moe_grouped_weight_grad(x, L.MOE_F16, R, K, None, 1, dy, R, N, None, torch.tensor(o, dtype=torch.int32, device="cuda"), G, R, N, K,
+                              accumulate, dw, ref.code(out))
+    torch.cuda.synchronize()
+    want = torch.stack([dy[a:b].double().T @ x[a:b].double() for a, b in zip(o, o[1:])])
+    return off(dw, want), off(want.to(dw.dtype), want)
+
+
+@pytest.mark.parametrize("accumulate", [0, 1])
+@pytest.mark.parametrize("o", [[0, 300, 700], [0, 65536], [0] + [32768 + i for i in range(128)], [0, 100, 4000, 4100] + [4100] * 30])
+def test_gradients_of_long_groups(o, accumulate):
+    """One group, and one of many rows among others that have few."""
+    assert gradient_off(gen(len(o)), o, 200, 264, "f32", accumulate)[0] <= FP32_SUMS
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+def test_16_bit_gradient_of_a_long_group(out):
+    e, least = gradient_off(gen(1), [0, 1 << 20], 64, 64, out)
+    assert e <= 1.01 * least
+
+
+# few rows, narrow tiles, pairs; more tokens than the kernel of u shares K for
+@pytest.mark.parametrize("T,N,K", [(5, 64, 2048), (30, 264, 65536), (7, 6400, 8192), (50, 264, 2048), (300, 264, 65536), (600, 1032, 2048),
+                                   (600, 1032, 65536), (20000, 128, 2048), (20000, 128, 8192)])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("rank", [64, 256])
+@pytest.mark.parametrize("alone", [True, False])
+def test_fp32_sums_of_adapters(T, N, K, t, rank, alone):
+    """alone: the shared projection is zero, so that u's own sums show."""
+    g, n = gen(T + K), 3
+    x, w = rand(g, t, T, K), rand(g, t, N, K, scale=0.0 if alone else K ** -0.5)
+    a, b = rand(g, t, n, rank, K, scale=K ** -0.5), rand(g, t, n, N, rank, scale=rank ** -0.5)
+    adapter = torch.randint(0, n, (T,), generator=g, device="cuda").int()
+    y = lora(x, t, w, adapter, a, b, None, "f32")
+    want = x.double() @ w.double().T
+    for i in range(n):
+        m = adapter == i
+        want[m] += x[m].double() @ a[i].double().T @ b[i].double().T
+    assert off(y, want) <= FP32_SUMS
