@@ -159,7 +159,7 @@ extern "C" int moe_grouped_matmul(const void *x, int type, int x_rows, size_t ld
     // few rows to a group: narrow tiles, one CTA each (gate/up, 32 experts of 2 x 512 x 1024: 8 rows an expert 13.5 us against 15.8
     // by pairs, 32 rows 18.3 against 16.0; 128 experts of 2 x 768 x 2048, 8 rows 126 against 134, 64 rows 233 against 138)
     const bool wide = R > 16LL * G;
-    const int nt = !wide ? 32 : ytype != MOE_F32 ? 256 : swiglu && grouped_swiglu_long(K) ? 64 : 128, mrows = (swiglu ? 64 : 128) * (wide ? 2 : 1);
+    const int nt = !wide ? 32 : ytype != MOE_F32 ? 256 : 128, mrows = (swiglu ? 64 : 128) * (wide ? 2 : 1);
     const long long row_tiles = (long long)R / nt + std::min(G, R);
     return grouped_launch(p, ytype, mode, wide, row_tiles * ((N + mrows - 1) / mrows), (K + 63) / 64, moe_cuda_stream(s));
 }

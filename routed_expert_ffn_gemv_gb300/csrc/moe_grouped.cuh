@@ -1196,8 +1196,6 @@ static inline int grouped_launch(const GroupedParams &p, int ytype, int mode, bo
 }
 // GP_GRAD: reductions of at most 512 rows on average.
 static inline bool grouped_grad_short(int R, int G) { return R <= 512LL * G; }
-// GP_SWIGLU, fp32 results: reductions that four accumulators of 256 do not hold.
-static inline bool grouped_swiglu_long(int K) { return K > 1024; }
 // SMs of the current device (0: none).
 int grouped_sms();
 // Tensor map of elements of `type`: `rank` dimensions and box extents innermost first, strides in bytes from the second on.

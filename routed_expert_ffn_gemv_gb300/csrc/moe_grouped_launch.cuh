@@ -40,9 +40,7 @@ static int grouped_launch_t(const GroupedParams &p, long long items, int stages,
     return MOE_OK;
 }
 
-// Pairs: tiles of 256 rows; of 128 with fp32 results, so that tensor memory holds four accumulators, and of 64 for SwiGLU's of long
-// reductions, whose product doubles what its factors are off, for eight (32768 routes over 64 experts, 2 x 768 x 2048: 9.5e-7 off
-// in 306 us, 4.6e-7 in 545).
+// Pairs: tiles of 256 rows; of 128 with fp32 results, so that tensor memory holds four accumulators.
 template <int OT>
 static int grouped_launch_modes(const GroupedParams &p, int mode, bool wide, long long items, int stages, cudaStream_t s) {
     constexpr int WIDE = OT == MOE_F32 ? 128 : 256;
@@ -54,8 +52,6 @@ static int grouped_launch_modes(const GroupedParams &p, int mode, bool wide, lon
             return wide ? grouped_launch_t<2, WIDE, GP_KN, OT>(p, items, stages, s)
                         : grouped_launch_t<1, 32, GP_KN, OT>(p, items, stages, s);
         case GP_SWIGLU:
-            if (OT == MOE_F32 && wide && grouped_swiglu_long(p.K))
-                return grouped_launch_t<2, OT == MOE_F32 ? 64 : WIDE, GP_SWIGLU, OT>(p, items, stages, s);
             return wide ? grouped_launch_t<2, WIDE, GP_SWIGLU, OT>(p, items, stages, s)
                         : grouped_launch_t<1, 32, GP_SWIGLU, OT>(p, items, stages, s);
         case GP_LORA:
