@@ -606,8 +606,8 @@ int moe_grouped_weight_grad(const void *x, int type, int x_rows, size_t ldx, con
  *   y        device [T][ldy] out, ytype MOE_F32, MOE_BF16 or MOE_F16; 16-byte aligned, ldy >= N a multiple of 8;
  *            columns from N on are left as they were.
  *   workspace  device, moe_lora_workspace() bytes, 256-byte aligned; needs no initial contents; one per call in flight.
- * Sums fp32; scale[a] A_a x_t is kept to 16 bits of mantissa (bf16; 24 for fp32 results) or 22 (fp16; beyond 65504 an
- * infinity); y is rounded once.  N and K multiples of 8 up to 65536, rank a multiple of 8 up to MOE_MAX_RANK
+ * Sums fp32; scale[a] A_a x_t is kept to 16 bits of mantissa (bf16; 24 for fp32 results) or 22 (fp16: or to 2^-22 of its largest
+ * element, 2^-39 of that for fp32 results; an element beyond 65504 counts as an infinity); y is rounded once.  N and K multiples of 8 up to 65536, rank a multiple of 8 up to MOE_MAX_RANK
  * (MOE_ERR_UNSUPPORTED otherwise), T <= 2^24 (0: no-op).  y may not overlap the inputs.  An infinity or a NaN in x, a or b
  * reaches the outputs of its own token, or its own adapter's tokens, only.
  */

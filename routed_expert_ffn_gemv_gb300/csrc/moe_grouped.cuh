@@ -12,7 +12,8 @@
 //              in each 32 lanes
 //   GP_GRAD    columns of x, MN-major           columns of dy, MN-major        the group's rows
 //   GP_LORA    W[n][k], then the adapters'      rows x[t][k], then the rows    K, then 32 ranks of each
-//              B_a[n][r]                        u[t] of the adapter's tokens   adapter in the tile
+//   (bf16),    B_a[n][r]                        u[t] of the adapter's tokens   adapter in the tile
+//   GP_LORA_F16
 //
 // Persistent; a work item is (group, NT-row tile, 128-row tile of the matrix).  Warp roles over rings of mbarriers that
 // run on across items:
@@ -41,7 +42,7 @@
 #include "moe_mx4.cuh"
 #include "moe_tc.cuh"
 
-enum { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_GRAD = 3, GP_LORA = 4 };
+enum { GP_NK = 0, GP_KN = 1, GP_SWIGLU = 2, GP_GRAD = 3, GP_LORA = 4, GP_LORA_F16 = 5 };
 
 #define GP_THREADS 640
 #define GP_ABYTES 16384   // 128 rows of 64 reduction steps
@@ -54,6 +55,8 @@ struct GroupedParams {
     const uint16_t *rows;     // x; GP_LORA: u
     const uint16_t *dy;       // GP_GRAD
     const uint16_t *lora_b;   // GP_LORA: the adapters' B
+    const float *factor;      // GP_LORA, fp16: what each 32 ranks of a token's u are to be multiplied by
+    int factors;              // of a token, that may differ: 1 or all
     size_t ld, lddy;
     const int32_t *offsets;   // [G + 1], or NULL: one group of R rows
     int G, R;
@@ -103,7 +106,7 @@ struct GroupedGeom {
     static constexpr int O_RING = (O_RED + RED + 1023) / 1024 * 1024;
     static constexpr int S = (227 * 1024 - 1024 - O_RING) / STAGE / 2 * 2;  // (even: see the loaders)
     static constexpr size_t SMEM = 1024 + O_RING + (size_t)S * STAGE;
-    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 2 * SLOTS + 2) * 8 + 16 + 80 + 64 <= 1024 && S >= 6, "");
+    static_assert(STAGE % 1024 == 0 && TCOLS <= 512 && (3 * S + 2 * SLOTS + 4) * 8 + 16 + 80 + 64 <= 1024 && S >= 6, "");
 };
 
 struct GroupedItem {
@@ -165,6 +168,7 @@ template <int CG, int NT, int MODE, int OT>
 __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_constant__ GroupedParams p) {
     using G_ = GroupedGeom<CG, NT, OT>;
     constexpr int S = G_::S;
+    constexpr bool LORA = MODE == GP_LORA || MODE == GP_LORA_F16, BY_POWERS = MODE == GP_LORA_F16;  // u by powers of two
     constexpr bool GRAD = MODE == GP_GRAD, A_MN = GRAD || MODE == GP_KN, B_MN = GRAD;
     constexpr int MROWS = MODE == GP_SWIGLU ? 64 : 128;  // output columns of a CTA's tile
     constexpr int ACC_STAGES = OT != MOE_F32 ? 128 : NT <= 64 || MODE == GP_SWIGLU ? 4 : 8;
@@ -178,11 +182,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     uint64_t *acc_empty = acc_full + G_::SLOTS;
     uint64_t *mma_done = acc_empty + G_::SLOTS;
     uint64_t *red_full = mma_done + 1;
-    uint32_t *tmem_slot = (uint32_t *)(red_full + 1);
+    uint64_t *flagged = red_full + 1;  // GP_LORA_F16, 16-bit results: an item's has_adapters is there
+    uint32_t *tmem_slot = (uint32_t *)(flagged + 2);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *bad_item = (volatile int *)(tmem_slot + 2);  // GP_LORA: 1 + the last item with a b that is not finite
     int *sums = (int *)(tmem_slot + 4);                       // [20]
-    int *has_adapters = sums + 20;                            // GP_LORA: [2][8] for each epilogue warp's columns of an item
+    int *has_adapters = sums + 20;                            // GP_LORA: [2][8] for each epilogue warp's columns of an item: some have an adapter (16-bit results: by a power of two)
     int *off = (int *)(smem + G_::O_OFF);                     // [G] where a group's rows begin, -1: it has none
     int *first = (int *)(smem + G_::O_FIRST);                 // [G + 1] items before those of the i-th group ..
     uint16_t *order = (uint16_t *)(smem + G_::O_ORDER);       // [G] .. and which group that is (pairs)
@@ -195,11 +200,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
     // CG = 1: the CTAs of a cluster share their item's reduction
     const int ks = CG == 1 ? (int)cluster_nctarank() : 1, kr = CG == 1 ? (int)cluster_ctarank() : 0;
-    const bool loaders = GRAD || MODE == GP_LORA || p.x_index;
+    const bool loaders = GRAD || LORA || p.x_index;
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1 + (loaders ? CG : 0));
-            mbar_init(&landed[s], 128 + (MODE == GP_LORA));
+            mbar_init(&landed[s], 128 + (LORA));
             mbar_init(&empty[s], 1);
         }
         for (unsigned b = 0; b < G_::SLOTS; ++b) {
@@ -208,6 +213,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         }
         mbar_init(mma_done, 1);
         mbar_init(red_full, 1);
+        mbar_init(flagged, 8);
         *abort_flag = 0;
         *bad_item = 0;
         fence_mbar_init();
@@ -221,12 +227,17 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     // Accumulators are taken one after another, round tensor memory's slots: an item's (as many as its n stages have use for,
     // then `apart` for GP_LORA's extra stages; none: those go to the last one), the next item's behind them.
     // apart: fp32 results, one for the first 128 ranks of every adapter and one for the others (a token has zeros in the stages
-    // of all adapters but one, which lose nothing)
-    const int apart = MODE == GP_LORA && OT == MOE_F32 ? (p.rank > 128 ? 2 : 1) : 0;
+    // of all adapters but one, which lose nothing); fp16, items with a token whose u comes by a power of two, one
+    const int all_apart = LORA && OT == MOE_F32 ? (p.rank > 128 ? 2 : 1) : 0;
+    auto flags = [&](int buf) -> bool {
+        const int4 *h = (const int4 *)(has_adapters + buf * 8);
+        const int4 a = h[0], b = h[1];
+        return (a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) != 0;
+    };
     auto acc_count = [&](int n) -> int { return max(1, (n + ACC_STAGES - 1) / ACC_STAGES); };
     // (GP_LORA: the kernel in front computes u and nothing else; it starts this one when everything before it is
     // complete, and only u is waited for, by the warp that loads it)
-    if (MODE != GP_LORA) pdl_wait();
+    if (!LORA) pdl_wait();
     pdl_trigger();
 
     // ---------------- items: tiles of the M side, inner, by tiles of each group's rows
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
     };
     // GP_LORA: this lane's share of the tile's adapters (-1: none).  Read before an item's stages, looked at behind them.
     auto read_adapters = [&](const GroupedItem &it, int (&ids)[8]) {
-        if (MODE == GP_LORA)
+        if (LORA)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int c = lane + 32 * i;
@@ -354,8 +365,13 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             if (ids[i] >= p.n_adapters) ids[i] = -1;
         }
     };
-    const int chunks = MODE == GP_LORA ? (p.rank + 31) / 32 * p.parts : 1;  // pieces of u: p.parts for 32 ranks of B
-    const int shift = MODE == GP_LORA && p.parts == 2;
+    const int chunks = LORA ? (p.rank + 31) / 32 * p.parts : 1;  // pieces of u: p.parts for 32 ranks of B
+    const int shift = LORA && p.parts == 2;
+    auto token_factor = [&](int t) -> float {  // fp16: of the token's 32 ranks the largest factor, a power of two
+        float f = p.factor[(size_t)t * chunks];
+        for (int c = 1; c < p.factors; ++c) f = fmaxf(f, p.factor[(size_t)t * chunks + c]);
+        return f;
+    };
     auto extra_stages = [&](const int (&ids)[8]) -> int {
         int n = 0;
         for (int a = grouped_next_adapter(ids, -1); a != 0x7FFFFFFF; a = grouped_next_adapter(ids, a)) n += chunks;
@@ -394,9 +410,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 const bool box_a = GRAD ? whole && !p.x_index : true, box_b = GRAD ? whole && !p.y_index : !p.x_index;
                 if (rank == 0)
                     mbar_arrive_expect_tx_elect(&full[st], CG * ((box_a ? GP_ABYTES : 0u) + (box_b ? nb * 128u : 0u)));
-                if (MODE == GP_LORA && lane == 0) mbar_arrive1(&landed[st]);
-                if (MODE == GP_NK || MODE == GP_LORA) {
-                    if (lane == 0) tma_tile_3d<CG>(dst, &p.a, kb * 64, m0, MODE == GP_LORA ? 0 : it.g, bar);
+                if (LORA && lane == 0) mbar_arrive1(&landed[st]);
+                if (MODE == GP_NK || LORA) {
+                    if (lane == 0) tma_tile_3d<CG>(dst, &p.a, kb * 64, m0, LORA ? 0 : it.g, bar);
                 } else if (MODE == GP_KN) {
                     if (lane < 2) tma_tile_3d<CG>(dst + lane * 8192, &p.a, m0 + 64 * lane, kb * 64, it.g, bar);
                 } else if (MODE == GP_SWIGLU) {
@@ -410,7 +426,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     ph ^= 1u;
                 }
             }
-            if (MODE == GP_LORA && ok) {
+            if (LORA && ok) {
                 int e = 0;
                 check_adapters(ids);
                 share(extra_stages(ids), lo, hi);
@@ -468,7 +484,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     ph ^= 1u;
                 }
             }
-            if (MODE == GP_LORA) {  // (the loaders' stages)
+            if (LORA) {  // (the loaders' stages)
                 check_adapters(ids);
                 share(extra_stages(ids), elo, ehi);
                 for (int e = elo; e < ehi; ++e, ++gs) {
@@ -539,14 +555,14 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < RI; ++i) {
                     const int c = r0 + 16 * i;
-                    const int r = c >= rows || MODE == GP_LORA ? -1 : source(it.row0 + rank * nb + c);
-                    who[i] = MODE == GP_LORA ? (c < rows ? p.adapter[it.row0 + rank * nb + c] : -1) : r >= 0 ? 16 : 0;
+                    const int r = c >= rows || LORA ? -1 : source(it.row0 + rank * nb + c);
+                    who[i] = LORA ? (c < rows ? p.adapter[it.row0 + rank * nb + c] : -1) : r >= 0 ? 16 : 0;
                     src[i] = p.rows + (size_t)max(r, 0) * p.ld + 8 * piece + 64 * (lo + (team != (gs & 1)));
                 }
                 for (int kb = lo; kb < hi; ++kb, next()) {
                     if ((gs & 1) != team) continue;
                     if (!begin()) break;
-                    if (MODE != GP_LORA) {
+                    if (!LORA) {
                         const uint32_t d = at + (uint32_t)st * G_::STAGE;
                         const int most = kb * 64 + 8 * piece < p.K ? 16 : 0;
 #pragma unroll
@@ -557,7 +573,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     }
                     cp_async_mbar_arrive_noinc(&landed[st]);
                 }
-                if (MODE == GP_LORA && ok) {
+                if (LORA && ok) {
                     if (j == 0) pdl_wait();  // u
                     int e = 0;
                     check_adapters(ids);
@@ -572,6 +588,29 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                             }
                             if (!begin()) break;
                             const uint32_t d = at + (uint32_t)st * G_::STAGE;
+                            if (BY_POWERS && p.factors > 1) {  // one power of two for the token's whole row: the smaller ones' pieces brought to it
+#pragma unroll
+                                for (int i = 0; i < RI; ++i)
+                                    if (16 * i < nb) {
+                                        uint4 v = make_uint4(0, 0, 0, 0);
+                                        if (who[i] == a) {
+                                            const int t = it.row0 + rank * nb + r0 + 16 * i;
+                                            const float f = p.factor[(size_t)t * chunks + c] / token_factor(t);
+                                            v = *(const uint4 *)(u + (size_t)16 * i * p.ld + c * 64);
+                                            uint32_t *w = (uint32_t *)&v;
+                                            if (f != 1.f)
+#pragma unroll
+                                                for (int k = 0; k < 4; ++k) {
+                                                    const float2 q = grouped_unpack<MOE_F16>(w[k]);
+                                                    w[k] = grouped_pack<MOE_F16>(f * q.x, f * q.y);
+                                                }
+                                        }
+                                        st_shared_16(d + i * 2048, v);
+                                    }
+                                mbar_arrive1(&landed[st]);
+                                next();
+                                continue;
+                            }
 #pragma unroll
                             for (int i = 0; i < RI; ++i)
                                 if (16 * i < nb) {
@@ -618,7 +657,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             }
         }
         cp_async_wait_all();
-        if (MODE == GP_LORA) pdl_wait();
+        if (LORA) pdl_wait();
     } else if (warp == 3 && loaders) {
         // ---------------- the loaders' stages: their copies have landed; the tensor cores may read them
         int st = 0;
@@ -629,7 +668,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             int lo, hi, ids[8];
             read_adapters(it, ids);
             share(it.steps, lo, hi);
-            bool extra = MODE != GP_LORA;
+            bool extra = !LORA;
             for (int kb = lo;; ++kb) {
                 if (kb >= hi) {
                     if (extra) break;
@@ -640,7 +679,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     if (kb >= hi) break;
                 }
                 if (!(ok = mbar_wait_warp(&landed[st], ph, p.status, abort_flag))) break;
-                if (MODE == GP_LORA && extra) {
+                if (LORA && extra) {
                     // The tile's other tokens have zeros for u here, which an infinity or a NaN in b would turn to NaN: rows of
                     // 32 ranks with one of them become zeros, and the epilogue adds them to this adapter's tokens
                     const uint32_t most = p.fmt ? 0x7F807F80u : 0x7C007C00u, at = smem_u32(ring) + (uint32_t)st * G_::STAGE;
@@ -740,8 +779,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             }
             uint32_t dx[2] = {d, d};
             bool fresh_x[2] = {fresh, fresh};
-            if (MODE == GP_LORA) {
+            int apart = all_apart;
+            if (LORA) {
                 check_adapters(ids);
+                if (OT != MOE_F32 && BY_POWERS && ok && (ok = mbar_wait_warp(flagged, j & 1, p.status, abort_flag))) apart = flags(j & 1);
                 share(__shfl_sync(0xffffffffu, extra_stages(ids), 0), lo, hi);
                 if (apart && ok) umma_commit_group_elect<CG>(&acc_full[(seq - 1) % G_::SLOTS]);
 #pragma unroll
@@ -751,9 +792,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         fresh_x[x] = true;
                     }
             }
-            for (int e = lo, c = MODE == GP_LORA ? lo % chunks : 0; MODE == GP_LORA && e < hi && ok; ++e) {
+            for (int e = lo, c = LORA ? lo % chunks : 0; LORA && e < hi && ok; ++e) {
                 if (!(ok = mbar_wait_warp(&full[st], ph, p.status, abort_flag))) break;
-                const bool other = apart == 2 && c >= 4 * p.parts;  // (pieces of 32 ranks)
+                const bool other = OT == MOE_F32 && apart == 2 && c >= 4 * p.parts;  // (pieces of 32 ranks)
                 const uint32_t d = other ? dx[1] : dx[0];
                 const bool fresh = other ? fresh_x[1] : fresh_x[0];
                 tc_fence_after();
@@ -800,7 +841,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         float scale = 1.f;
         int ia = -1;  // GP_LORA: its adapter
         auto fetch = [&](const GroupedItem &it) {
-            if (MODE == GP_LORA) ia = et < it.n ? p.adapter[it.row0 + et] : -1;
+            if (LORA) ia = et < it.n ? p.adapter[it.row0 + et] : -1;
             if (GRAD || et >= it.n) return;
             ix = p.x_index ? p.x_index[it.row0 + et] : it.row0 + et;
             iy = p.y_index ? p.y_index[it.row0 + et] : it.row0 + et;
@@ -813,7 +854,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 row = (uint8_t *)p.y + ((size_t)it.g * p.N + it.row0 + et) * p.M * SIZE;
             } else if (ix >= 0 && ix / (p.x_index ? p.x_share : 1) < p.x_rows && iy >= 0 && iy < p.y_rows) {
                 row = (uint8_t *)p.y + (size_t)iy * p.ldy * SIZE;
-                if (p.scale) scale = p.scale[iy];
+                if (LORA) {  // (the adapter's part alone is multiplied)
+                    if (BY_POWERS && ia >= 0 && ia < p.n_adapters) scale = token_factor(iy);
+                } else if (p.scale) {
+                    scale = p.scale[iy];
+                }
             } else {
                 moe_set_status(p.status, MOE_ERR_INVALID);
             }
@@ -824,6 +869,13 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(u[k]));
+        };
+        auto add16_by = [&](uint32_t (&v)[16], uint32_t at, const float *by) {  // one that is apart, its columns multiplied
+            uint32_t u[16];
+            tmem_ld16(at, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(fmaf(by[k], __uint_as_float(u[k]), __uint_as_float(v[k])));
         };
         // GP_LORA: 32 ranks (those of piece c of u, with their first piece) of adapter a for output o of token t, where b is not
         // finite among them, else 0.  By the whole u: an infinity times its parts may be infinities of both signs, or of a part
@@ -842,7 +894,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 bad |= !(fabsf(v) <= 3.4028235e38f);
                 s = fmaf(v, value(u[k]) + value(u[32 + k]) + (shift ? value(u[64 + k]) : 0.f), s);
             }
-            return bad ? s : 0.f;
+            return bad ? (!BY_POWERS ? s : s * p.factor[(size_t)t * chunks + c]) : 0.f;
         };
         unsigned seq = 0;  // accumulators handed back so far
         auto hand_back = [&](unsigned a) {
@@ -855,6 +907,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
         if (n_mine) {
             it = item_at(0);
             fetch(it);
+            if (BY_POWERS) pdl_wait();  // the factors
             resolve(it);
         }
         for (int j = 0; j < n_mine; ++j) {
@@ -863,9 +916,16 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 e_y[buf * NT + et] = row;
                 e_s[buf * NT + et] = scale;
             }
-            if (MODE == GP_LORA && apart) {
-                const bool any = __any_sync(0xffffffffu, ia >= 0 && ia < p.n_adapters);
+            int apart = all_apart;
+            bool w = true;
+            if (LORA && (F32 || BY_POWERS)) {
+                const bool any = __any_sync(0xffffffffu, ia >= 0 && ia < p.n_adapters && (F32 || scale != 1.f));
                 if (lane == 0) has_adapters[buf * 8 + ew] = any;
+                if (!F32) {
+                    if (lane == 0) mbar_arrive1(flagged);
+                    w = mbar_wait_warp(flagged, buf, p.status, abort_flag);
+                    apart = flags(buf);
+                }
             }
             GroupedItem nx = {};
             if (j + 1 < n_mine) {
@@ -879,7 +939,6 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                 used = acc_count(hi - lo);
             }
             const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16);
-            bool w = true;
             // as many as the last pass adds up: those that tensor memory holds, one for 16-bit results
             const unsigned held = F32 ? G_::SLOTS - apart : 1;
             for (; used > held && w; --used, ++seq) {  // the first added to the second (the columns that are this warp's below, too)
@@ -911,16 +970,14 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
             // GP_LORA: of this CTA's extra stages the range; of the accumulators that are apart, those that some of them went to (1 the
             // first, 2 the second)
             int elo = 0, ehi = 0, added = 0;
-            if (MODE == GP_LORA && ks > 1) {
+            if (LORA && ks > 1) {
                 int ids[8];
                 read_adapters(it, ids);
                 check_adapters(ids);
                 share(extra_stages(ids), elo, ehi);
                 for (int e = elo; e < min(ehi, elo + chunks); ++e) added |= apart == 2 && e % chunks >= 4 * p.parts ? 2 : 1;
-            } else if (MODE == GP_LORA && apart) {
-                const int4 *h = (const int4 *)(has_adapters + buf * 8);
-                const int4 a = h[0], b = h[1];
-                if (a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) added = 3;
+            } else if (LORA && apart && (!F32 || flags(buf))) {
+                added = 3;
             }
             uint8_t *const *ys = e_y + buf * NT;
             const float *ss = e_s + buf * NT;
@@ -943,11 +1000,11 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
 #pragma unroll
                         for (int k = 0; k < 16; ++k) v[k] = 0u;
                     for (int a = 0; a < apart; ++a)
-                        if (added >> a & 1) add16(v, other(used + a) + 16 * half);
+                        if (added >> a & 1) add16_by(v, other(used + a) + 16 * half, ss + 16 * half);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) x[(16 * half + k) * 128 + 32 * q + lane] = __uint_as_float(v[k]);
                 }
-                if (MODE == GP_LORA && *bad_item > j) {
+                if (LORA && *bad_item > j) {
                     int e = 0, ids[8];
                     read_adapters(it, ids);
                     check_adapters(ids);
@@ -990,7 +1047,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         } else {
                             a = total(r, m);
                         }
-                        const float s = ss[c];
+                        const float s = LORA ? 1.f : ss[c];
                         if (mg < p.M && ys[c]) grouped_store4<OT>(ys[c], mg, make_float4(s * a.x, s * a.y, s * a.z, s * a.w));
                     }
                 }
@@ -1007,7 +1064,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         for (int a = 0; a < apart; ++a)
                             if (added >> a & 1)
 #pragma unroll
-                                for (int h = 0; h < CH / 16; ++h) add16(v[h], other(used + a) + c0 + 16 * h);
+                                for (int h = 0; h < CH / 16; ++h) add16_by(v[h], other(used + a) + c0 + 16 * h, ss + c0 + 16 * h);
                         float *x = (float *)(smem + G_::O_XCH + ew * G_::XCH);
                         if (GRAD) {  // whole boxes by TMA: see below
                             if (lane == 0) tma_store_wait_read();
@@ -1034,7 +1091,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                                 const int r = 4 * k + (lane >> 3), c = c0 + 16 * h + r;
                                 float4 a = *(const float4 *)(x + 36 * r + 4 * (lane & 7));
                                 if (c < it.n && m < p.M && ys[c]) {
-                                    const float s = ss[c];
+                                    const float s = LORA ? 1.f : ss[c];
                                     a = make_float4(s * a.x, s * a.y, s * a.z, s * a.w);
                                     grouped_store4<OT>(ys[c], m, a);
                                 }
@@ -1060,6 +1117,17 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                         for (int k = 0; k < 4 * NB; ++k) hi[k] = __float_as_uint(__uint_as_float(hi[k]) + __uint_as_float(u[k]));
                     }
                     const int cq = c0 + 2 * (lane & 3);
+                    if (LORA && (added & 1))  // (fp16)
+#pragma unroll
+                        for (int side = 0; side < 2; ++side) {
+                            uint32_t u[4 * NB];
+                            tmem_ld_16x256b(other(used) + ((uint32_t)(16 * side) << 16) + c0, u);
+                            tmem_ld_wait();
+                            uint32_t *v = side ? hi : lo;
+#pragma unroll
+                            for (int k = 0; k < 4 * NB; ++k)
+                                v[k] = __float_as_uint(fmaf(ss[cq + 8 * (k >> 2) + (k & 1)], __uint_as_float(u[k]), __uint_as_float(v[k])));
+                        }
                     if (none)
 #pragma unroll
                         for (int k = 0; k < 4 * NB; ++k) lo[k] = hi[k] = 0u;
@@ -1148,7 +1216,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1) grouped_kernel(const __grid_con
                     }
                     __syncwarp();
                 }
-                if (MODE == GP_LORA && *bad_item > j) {
+                if (LORA && *bad_item > j) {
                     __syncwarp();
                     for (int c0 = CH * half; c0 < it.n; c0 += 2 * CH)
                         for (int c = c0; c < min(it.n, c0 + CH); ++c) {
@@ -1221,7 +1289,7 @@ struct GroupedFewParams {
     size_t ldy;
     int ytype, M, K;
     const int32_t *adapter;  // GP_LORA
-    const uint16_t *b, *u;
+    const uint16_t *b, *u;   // (fp16: u in fp32, 32 ranks to a piece)
     int n_adapters, rank, parts;
     int *status;
 };

@@ -48,6 +48,49 @@ __device__ __forceinline__ float value16(uint16_t h) {
     return BF ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
 
+// An fp32 number as two of tf32, the nearest and the nearest of what is left (22 bits).
+__device__ __forceinline__ uint32_t nearest_tf32(float v) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 32 elements of the reduction as in mma32, of fp16 (which tf32 holds) by fp32: a lane's eight are its share of four steps.
+__device__ __forceinline__ void mma32_f32(float (&c)[4], const uint4 &lo, const uint4 &hi, const float4 &x, const float4 &y) {
+    const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    float left[4] = {};  // (two short chains of MMAs)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = __half22float2(*(const __half2 *)&l[i]), q = __half22float2(*(const __half2 *)&h[i]);
+        const uint32_t u0 = nearest_tf32(v[2 * i]), u1 = nearest_tf32(v[2 * i + 1]);
+        const uint32_t a0 = __float_as_uint(p.x), a1 = __float_as_uint(q.x), a2 = __float_as_uint(p.y), a3 = __float_as_uint(q.y);
+        mma8(c, a0, a1, a2, a3, u0, u1);
+        mma8(left, a0, a1, a2, a3, nearest_tf32(v[2 * i] - __uint_as_float(u0)), nearest_tf32(v[2 * i + 1] - __uint_as_float(u1)));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] += left[i];
+}
+
+// An output's weights (those of up to 128 ranks from k0 on) by u of token t.
+template <bool BF>
+__device__ __forceinline__ float whole_sum(const uint16_t *w, const GroupedFewParams &p, int t, int k0) {
+    const int chunks = (p.rank + 31) / 32;
+    float s = 0.f;
+    for (int j = k0; j < min(p.rank, k0 + 128); ++j) {
+        const size_t piece = (size_t)t * chunks + j / 32;
+        const uint16_t *u = p.u + piece * p.parts * 64 + j % 32;
+        const float v = BF ? value16<BF>(u[0]) + value16<BF>(u[32]) + (p.parts == 2 ? value16<BF>(u[64]) : 0.f)
+                           : ((const float *)p.u)[piece * 32 + j % 32];
+        s = fmaf(value16<BF>(w[j]), v, s);
+    }
+    return s;
+}
+
 struct FewTile {
     int g, row0, n;
 };
@@ -216,9 +259,9 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
         }
         if (MODE == GP_LORA) {
             // ---------------- the adapters of the tile's tokens, the warps in turns; u's upper halves, then the rest of u (its parts)
+            int id = lane < tile.n ? p.adapter[tile.row0 + lane] : -1;  // token `lane` of the tile
             if (!waited) pdl_wait();
             waited = true;
-            int id = lane < tile.n ? p.adapter[tile.row0 + lane] : -1;  // token `lane` of the tile
             if (id < -1 || id >= p.n_adapters) {
                 moe_set_status(p.status, MOE_ERR_INVALID);
                 id = -1;
@@ -233,50 +276,53 @@ __global__ void __launch_bounds__(GF_THREADS, 2) grouped_few_kernel(const __grid
                 const unsigned who = __ballot_sync(0xffffffffu, id == ad);
                 const uint16_t *w0 = p.b + ((size_t)ad * p.M + min(m0 + g, p.M - 1)) * p.rank;
                 const uint16_t *w1 = p.b + ((size_t)ad * p.M + min(m0 + g + 8, p.M - 1)) * p.rank;
-                // sums of their own: an infinity or a NaN in b, times the zeros of the other tokens, stays out of theirs
-                float part[NB][4] = {};
-                for (int c = 0; c < chunks; ++c) {
-                    const int k = 32 * c + 8 * t4;
-                    const bool in = k < p.rank;
-                    const uint4 lo = in ? ld_once(w0 + k) : zero, hi = in ? ld_once(w1 + k) : zero;
+                for (int c0 = 0; c0 < chunks; c0 += 4) {  // (128 ranks: the MMAs' sums truncate, see moe_grouped.cuh)
+                    // sums of their own: an infinity or a NaN in b, times the zeros of the other tokens, stays out of theirs
+                    float part[NB][4] = {};
+                    for (int c = c0; c < min(chunks, c0 + 4); ++c) {
+                        const int k = 32 * c + 8 * t4;
+                        const bool in = k < p.rank;
+                        const uint4 lo = in ? ld_once(w0 + k) : zero, hi = in ? ld_once(w1 + k) : zero;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        if (!(who >> (8 * b) & 0xFF)) continue;
-                        const bool mine = who >> (8 * b + g) & 1;
-                        const uint16_t *u = p.u + ((size_t)(tile.row0 + 8 * b + g) * chunks + c) * p.parts * 64 + 8 * t4;
-                        mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)u : zero);
-                        mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)(u + 32) : zero);
-                        if (BF && p.parts == 2) mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)(u + 64) : zero);
+                        for (int b = 0; b < NB; ++b) {
+                            if (!(who >> (8 * b) & 0xFF)) continue;
+                            const bool mine = who >> (8 * b + g) & 1;
+                            const uint16_t *u = p.u + ((size_t)(tile.row0 + 8 * b + g) * chunks + c) * p.parts * 64 + 8 * t4;
+                            if (BF) {
+                                mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)u : zero);
+                                mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)(u + 32) : zero);
+                            } else {
+                                const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+                                const float4 *v = (const float4 *)((const float *)p.u + ((size_t)(tile.row0 + 8 * b + g) * chunks + c) * 32 + 8 * t4);
+                                mma32_f32(part[b], lo, hi, mine ? v[0] : none, mine ? v[1] : none);
+                            }
+                            if (BF && p.parts == 2) mma32<BF>(part[b], lo, hi, mine ? *(const uint4 *)(u + 64) : zero);
+                        }
                     }
-                }
-                // this lane's sums 4 b + i: output g or g + 8 (i / 2), token 8 b + 2 t4 or the one behind it
-                bool odd = false;
+                    // this lane's sums 4 b + i: output g or g + 8 (i / 2), token 8 b + 2 t4 or the one behind it
+                    bool odd = false;
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                    for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        odd |= (who >> (8 * b + 2 * t4 + (i & 1)) & 1) && !(fabsf(part[b][i]) <= FLT_MAX);
-                if (odd)  // an infinity of b times u's parts, one of them 0 or of the other sign: NaN, where b u is an infinity
-                    for (int o = 0; o < 4 * NB; ++o) {
-                        const int t = 8 * (o >> 2) + 2 * t4 + (o & 1);
-                        if (!(who >> t & 1)) continue;
-                        const uint16_t *w = o & 2 ? w1 : w0, *u = p.u + (size_t)(tile.row0 + t) * chunks * p.parts * 64;
-                        float s = 0.f;
-                        for (int j = 0; j < p.rank; ++j) {
-                            const uint16_t *v = u + j / 32 * p.parts * 64 + j % 32;
-                            s = fmaf(value16<BF>(w[j]), value16<BF>(v[0]) + value16<BF>(v[32]) + (p.parts == 2 ? value16<BF>(v[64]) : 0.f), s);
+                        for (int i = 0; i < 4; ++i)
+                            odd |= (who >> (8 * b + 2 * t4 + (i & 1)) & 1) && !(fabsf(part[b][i]) <= FLT_MAX);
+                    if (odd)  // an infinity of b times u's parts, one of them 0 or of the other sign: NaN, where b u is an infinity
+                        for (int o = 0; o < 4 * NB; ++o) {
+                            const int t = 8 * (o >> 2) + 2 * t4 + (o & 1);
+                            if (!(who >> t & 1)) continue;
+                            const float s = whole_sum<BF>(o & 2 ? w1 : w0, p, tile.row0 + t, 32 * c0);
+#pragma unroll
+                            for (int b = 0; b < NB; ++b)  // (no index but a constant: the sums stay in registers)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (4 * b + i == o && !(fabsf(part[b][i]) <= FLT_MAX)) part[b][i] = s;
                         }
 #pragma unroll
-                        for (int b = 0; b < NB; ++b)  // (no index but a constant: the sums stay in registers)
+                    for (int b = 0; b < NB; ++b)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (4 * b + i == o && !(fabsf(part[b][i]) <= FLT_MAX)) part[b][i] = s;
-                    }
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (who >> (8 * b + 2 * t4 + (i & 1)) & 1) acc[0][b][i] += part[b][i];
+                        for (int i = 0; i < 4; ++i)
+                            if (who >> (8 * b + 2 * t4 + (i & 1)) & 1) acc[0][b][i] += part[b][i];
+                }
             }
         }
         // ---------------- the warps' sums

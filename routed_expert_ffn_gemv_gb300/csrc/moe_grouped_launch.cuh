@@ -57,6 +57,9 @@ static int grouped_launch_modes(const GroupedParams &p, int mode, bool wide, lon
         case GP_LORA:
             return wide ? grouped_launch_t<2, WIDE, GP_LORA, OT>(p, items, stages, s)
                         : grouped_launch_t<1, 32, GP_LORA, OT>(p, items, stages, s);
+        case GP_LORA_F16:
+            return wide ? grouped_launch_t<2, WIDE, GP_LORA_F16, OT>(p, items, stages, s)
+                        : grouped_launch_t<1, 32, GP_LORA_F16, OT>(p, items, stages, s);
         default:
             // fp32: tiles of 128, for four accumulators instead of two, with long reductions only (128 groups of 256 rows, 1536 x 2048: 403 us
             // against 331)

@@ -2,10 +2,15 @@
 //
 //   y[t] = W x_t + B_a u_t,   u_t = scale[a] A_a x_t,   a = adapter[t]
 // Two kernels.  lora_shrink_kernel computes u in fp32 and leaves it as two 16-bit halves (the nearest, and the nearest of what
-// is left: 16 bits of bf16, 22 of fp16), 32 ranks to a 128-byte row piece, upper halves first (and, where a third part is kept, another piece for it).  The product's kernel (moe_grouped.cuh, GP_LORA) runs K on into the ranks: for each adapter that has tokens in
-// its tile, 32 ranks at a time, B_a's tile against the tokens' rows of u, zeros for the tokens of other adapters.  So y
-// is rounded once and W's part and the adapters' share an accumulator.  The product starts beside the first kernel and waits
-// for u only where it loads it.
+// is left: 16 bits of bf16, 22 of fp16), 32 ranks to a 128-byte row piece, upper halves first (and, where a third part is kept,
+// another piece for it).  fp16 lacks the range for that.  The product of few rows takes u in fp32 instead, as two halves of tf32.  For
+// the other one a token's ranks (T <= LS_FEW: each 32 of them) are first brought to the top of fp16's range by a power of two, whose
+// reciprocal is kept behind u, and the product undoes it.  For 16-bit results only where the largest is below 1/8 (above, its
+// elements are off by 2^-22 of it at most as they are): the adapter's part then wants an accumulator of its own, in which the next
+// item can't begin (4096 tokens, rank 32: 52 us, 58 for small u).  The product's kernel (moe_grouped.cuh, GP_LORA) runs K on into
+// the ranks: for each adapter that has tokens in its tile, 32 ranks at a time, B_a's tile against the tokens' rows of u, zeros for the
+// tokens of other adapters.  So y is rounded once, and W's part and the adapters' share an accumulator or are added before that.
+// The product starts beside the first kernel and waits for u only where it loads it.
 #include <algorithm>
 #include <mutex>
 
@@ -21,10 +26,18 @@ __device__ __forceinline__ float2 pair_value(uint32_t w) {
     if (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     return __half22float2(*(const __half2 *)&w);
 }
-// v as two 16-bit numbers (one that overflows: as the infinity alone).
+// fp16's powers of two: what of v is finite in fp16 counts, and the largest of it, where that is below `below`, comes to 2^14 or
+// more (below 2^-86: to less).
+__device__ __forceinline__ float finite16(float v) { return fabsf(v) < 65520.f ? fabsf(v) : 0.f; }
+__device__ __forceinline__ void power16(float most, float below, float &up, float &down) {
+    const int e = most > 0.f && most < below ? max((int)(__float_as_uint(most) >> 23) - 127 - 14, -100) : 0;
+    up = __uint_as_float((uint32_t)(127 - e) << 23);
+    down = __uint_as_float((uint32_t)(127 + e) << 23);
+}
+// v (fp16: times `up`) as two 16-bit numbers (one that overflows: as the infinity alone).
 // (rest: what they leave, as a third.)
 template <bool BF>
-__device__ __forceinline__ void split16(float v, uint16_t &hi, uint16_t &lo, uint16_t &rest) {
+__device__ __forceinline__ void split16(float v, float up, uint16_t &hi, uint16_t &lo, uint16_t &rest) {
     if (BF) {
         const __nv_bfloat16 h = __float2bfloat16_rn(v);
         const float f = __bfloat162float(h), left = isinf(f) ? 0.f : v - f;
@@ -33,19 +46,21 @@ __device__ __forceinline__ void split16(float v, uint16_t &hi, uint16_t &lo, uin
         lo = __bfloat16_as_ushort(l);
         rest = __bfloat16_as_ushort(__float2bfloat16_rn(left - __bfloat162float(l)));
     } else {
-        const __half h = __float2half_rn(v);
-        const float f = __half2float(h);
+        const bool in = fabsf(v) < 65520.f;
+        const __half h = __float2half_rn(in ? v * up : v);
         hi = __half_as_ushort(h);
-        lo = __half_as_ushort(__float2half_rn(isinf(f) ? 0.f : v - f));
+        lo = __half_as_ushort(__float2half_rn(in ? v * up - __half2float(h) : 0.f));
         rest = 0;
     }
 }
 
-// Few tokens: a warp for LS_RANKS ranks of one token.  No shared memory: it runs beside the product.  u: [T][chunks][parts][64].
-template <bool BF>
+// Few tokens: a warp for LS_RANKS ranks of one token, a CTA for 32 of them.  Next to no shared memory: it runs beside the product.
+// u: [T][chunks][parts][64], fp16: and factor [T][chunks].  F32: u as it is, [T][chunks][32].
+template <bool BF, bool F32>
 __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, size_t ldx, int T, int K, const int32_t *adapter,
                                                           int n_adapters, const uint16_t *a, int rank, const float *scale,
-                                                          uint16_t *u, int parts) {
+                                                          uint16_t *u, float *factor, float below, int parts) {
+    __shared__ float most[8];  // (fp16)
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x % 32, chunks = (rank + 31) / 32, groups = chunks * 32 / LS_RANKS;
@@ -87,6 +102,18 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
 #pragma unroll
             for (int d = 16; d > 0; d /= 2) v[j] += __shfl_xor_sync(0xffffffffu, v[j], d);
     }
+    float up = 1.f, down = 1.f;
+    if (!BF && !F32) {  // (a CTA's warps have the same token)
+        float m = 0.f;
+        const float sc = scale ? scale[ad] : 1.f;
+#pragma unroll
+        for (int j = 0; j < LS_RANKS; ++j) m = fmaxf(m, finite16(v[j] * sc));
+        if (lane == 0) most[threadIdx.x / 32] = m;
+        __syncthreads();
+        for (int w = 0; w < 8; ++w) m = fmaxf(m, most[w]);
+        power16(m, below, up, down);
+        if (threadIdx.x == 0) factor[(size_t)t * chunks + j0 / 32] = down;
+    }
     if (lane < LS_RANKS) {
         float r = 0.f;
 #pragma unroll
@@ -95,8 +122,12 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
         if (scale) r *= scale[ad];
         if (j0 >= rank) r = 0.f;
         uint16_t hi, lo, rest;
-        split16<BF>(r, hi, lo, rest);
+        split16<BF>(r, up, hi, lo, rest);
         const int j = j0 + lane;
+        if (F32) {
+            ((float *)u)[(size_t)t * chunks * 32 + j] = fabsf(r) < 65520.f ? r : __half2float(__float2half_rn(r));
+            return;
+        }
         uint16_t *row = u + ((size_t)t * chunks + j / 32) * parts * 64 + j % 32;
         row[0] = hi;
         row[32] = lo;
@@ -123,6 +154,8 @@ struct ShrinkParams {
     const int32_t *adapter;
     const float *scale;
     uint16_t *u;       // [T][chunks][parts][64]
+    float *factor;     // [T][chunks], fp16
+    float below;       // tokens whose largest is below this come by a power of two (fp16)
     int *status;
 };
 
@@ -134,6 +167,7 @@ struct ShrinkSmem {
     alignas(16) int ids[LS_TOKENS];  // adapter of each token, -1: none
     int place[LS_TOKENS];            // of a token that is its adapter's first: the adapter's place among the tile's
     int list[LS_TOKENS];             // adapter of each place
+    unsigned most[LS_TOKENS];        // fp16: bits of the largest of each token's u
     int mine[LS_TOKENS];             // place of each token's adapter in this pass, -1: not in it
 };
 static_assert(sizeof(ShrinkSmem) <= LS_HEADER, "");
@@ -246,26 +280,28 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
             uint32_t ph = 0;
             const uint32_t d0 = __shfl_sync(0xffffffffu, s.tmem, 0);
             const uint32_t idesc = umma_idesc_16(p.fmt, false, false, 128, __shfl_sync(0xffffffffu, (used * p.rank + 15) & ~15, 0));
-            for (int kb = kb0; kb < kb1; ++kb) {
-                const int acc = (kb - kb0) / per, half = acc & 1;
-                const bool fresh = kb - kb0 == acc * per;
-                if (fresh && acc >= 2 && !mbar_wait_warp(&s.acc_empty[half], (acc / 2 - 1) & 1, p.status, &s.abort)) break;
-                if (!mbar_wait_warp(&s.full[st], ph, p.status, &s.abort)) break;
-                tc_fence_after();
-                const uint32_t sa = smem_u32(ring) + (uint32_t)st * LS_STAGE;
-                const uint64_t a = umma_desc_sw128(sa), b = umma_desc_sw128(sa + LS_TOKENS * 128);
-                const int left = p.K - 64 * kb;
-                const uint32_t d = d0 + half * LS_COLS;
-                umma_f16_elect<1>(d, a, b, idesc, !fresh);
-                if (left > 16) umma_f16_elect<1>(d, a + 2, b + 2, idesc, 1);
-                if (left > 32) umma_f16_elect<1>(d, a + 4, b + 4, idesc, 1);
-                if (left > 48) umma_f16_elect<1>(d, a + 6, b + 6, idesc, 1);
-                umma_commit_elect(&s.empty[st]);
-                if (kb + 1 == kb1 || kb + 1 - kb0 == (acc + 1) * per) umma_commit_elect(&s.acc_full[half]);
-                if (++st == LS_STAGES) {
-                    st = 0;
-                    ph ^= 1u;
+            bool ok = true;
+            for (int acc = 0, kb = kb0; acc < accs && ok; ++acc) {
+                const uint32_t d = d0 + (acc & 1) * LS_COLS;
+                if (acc >= 2 && !(ok = mbar_wait_warp(&s.acc_empty[acc & 1], (acc / 2 - 1) & 1, p.status, &s.abort))) break;
+                const int from = kb;
+                for (const int end = min(kb1, kb + per); kb < end; ++kb) {
+                    if (!(ok = mbar_wait_warp(&s.full[st], ph, p.status, &s.abort))) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(ring) + (uint32_t)st * LS_STAGE;
+                    const uint64_t a = umma_desc_sw128(sa), b = umma_desc_sw128(sa + LS_TOKENS * 128);
+                    const int left = p.K - 64 * kb;
+                    umma_f16_elect<1>(d, a, b, idesc, kb > from);
+                    if (left > 16) umma_f16_elect<1>(d, a + 2, b + 2, idesc, 1);
+                    if (left > 32) umma_f16_elect<1>(d, a + 4, b + 4, idesc, 1);
+                    if (left > 48) umma_f16_elect<1>(d, a + 6, b + 6, idesc, 1);
+                    umma_commit_elect(&s.empty[st]);
+                    if (++st == LS_STAGES) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
+                if (ok && accs > 2) umma_commit_elect(&s.acc_full[acc & 1]);
             }
             umma_commit_elect(&s.done);  // every copy has been consumed, every MMA has completed
         } else if (warp < 4) {
@@ -332,23 +368,43 @@ __global__ void __launch_bounds__(LS_THREADS, 1) lora_shrink_mma_kernel(const __
         cluster_sync_all();
         // ---------------- the cluster's
         const int ta = LS_TOKENS * me / ctas, tb = LS_TOKENS * (me + 1) / ctas, quads = chunks * 8;
+        auto total = [&](int t, int j) -> float4 {  // of ranks j .. j + 3, in the order of the CTAs
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < ctas; ++c) {
+                const float4 w = ld_cluster_f32x4(cluster_map(part + (size_t)t * pitch + j, c));
+                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            }
+            const float sc = p.scale ? p.scale[s.ids[t]] : 1.f;
+            return make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
+        };
+        if (!BF) {  // the largest of each token first; the sums stay in this CTA's own place for its tokens, which no other CTA reads
+            for (int t = tid; t < LS_TOKENS; t += LS_THREADS) s.most[t] = 0u;
+            __syncthreads();
+            for (int i = tid; i < (tb - ta) * quads; i += LS_THREADS) {
+                const int t = ta + i / quads, j = 4 * (i % quads);
+                if (s.mine[t] < 0 || j >= p.rank) continue;
+                const float4 v = total(t, j);
+                *(float4 *)(part + (size_t)t * pitch + j) = v;
+                const float m = fmaxf(fmaxf(finite16(v.x), finite16(v.y)), fmaxf(finite16(v.z), finite16(v.w)));
+                atomicMax(&s.most[t], __float_as_uint(m));  // (no negative numbers: ordered as their bits are)
+            }
+            __syncthreads();
+        }
         for (int i = tid; i < (tb - ta) * quads; i += LS_THREADS) {
             const int t = ta + i / quads, j = 4 * (i % quads);
             if (s.mine[t] < 0) continue;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j < p.rank) {
-                for (int c = 0; c < ctas; ++c) {
-                    const float4 w = ld_cluster_f32x4(cluster_map(part + (size_t)t * pitch + j, c));
-                    v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-                }
-                const float sc = p.scale ? p.scale[s.ids[t]] : 1.f;
-                v = make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
+            if (j < p.rank) v = BF ? total(t, j) : *(const float4 *)(part + (size_t)t * pitch + j);
+            float up = 1.f, down = 1.f;
+            if (!BF) {
+                power16(__uint_as_float(s.most[t]), p.below, up, down);
+                if (j % 32 == 0) p.factor[(size_t)(t0 + t) * chunks + j / 32] = down;
             }
             uint16_t hi[4], lo[4], rest[4];
-            split16<BF>(v.x, hi[0], lo[0], rest[0]);
-            split16<BF>(v.y, hi[1], lo[1], rest[1]);
-            split16<BF>(v.z, hi[2], lo[2], rest[2]);
-            split16<BF>(v.w, hi[3], lo[3], rest[3]);
+            split16<BF>(v.x, up, hi[0], lo[0], rest[0]);
+            split16<BF>(v.y, up, hi[1], lo[1], rest[1]);
+            split16<BF>(v.z, up, hi[2], lo[2], rest[2]);
+            split16<BF>(v.w, up, hi[3], lo[3], rest[3]);
             uint16_t *row = p.u + ((size_t)(t0 + t) * chunks + j / 32) * p.parts * 64 + j % 32;
             if (p.parts == 2) {
                 *(uint2 *)(row + 64) = make_uint2(rest[0] | (uint32_t)rest[1] << 16, rest[2] | (uint32_t)rest[3] << 16);
@@ -375,19 +431,20 @@ int check(int T, int rank) {
 }
 
 int shrink_few(const void *x, size_t ldx, int T, int K, int type, const int32_t *adapter, int n_adapters, const void *a,
-               int rank, const float *scale, void *u, int parts, moe_stream_t s) {
+               int rank, const float *scale, void *u, float *factor, float below, int parts, moe_stream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     const long long jobs = (long long)T * ((rank + 31) / 32 * 32 / LS_RANKS);
     moe_pdl_config(&cfg, attr, dim3((unsigned)((jobs + 7) / 8)), dim3(256), 0, moe_cuda_stream(s));
-    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, type == MOE_BF16 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>,
+    MOE_TRY_CUDA(cudaLaunchKernelEx(&cfg, type == MOE_BF16 ? lora_shrink_kernel<true, false> : factor ? lora_shrink_kernel<false, false> : lora_shrink_kernel<false, true>,
                                     (const uint16_t *)x, ldx, T, K, adapter, n_adapters, (const uint16_t *)a, rank, scale,
-                                    (uint16_t *)u, parts));
+                                    (uint16_t *)u, factor, below, parts));
     return MOE_OK;
 }
 
 int shrink_many(const void *x, size_t ldx, int T, int K, int type, const int32_t *adapter, int n_adapters, const void *a,
-                int rank, const float *scale, void *u, int parts, int acc_stages, int *status, moe_stream_t s) {
+                int rank, const float *scale, void *u, float *factor, float below, int parts, int acc_stages,
+                int *status, moe_stream_t s) {
     static std::mutex mu;
     static bool ready[64] = {false};
     int dev = -1, rc;
@@ -423,6 +480,8 @@ int shrink_many(const void *x, size_t ldx, int T, int K, int type, const int32_t
     p.adapter = adapter;
     p.scale = scale;
     p.u = (uint16_t *)u;
+    p.factor = factor;
+    p.below = below;
     p.parts = parts;
     p.acc_stages = acc_stages;
     p.status = status;
@@ -471,12 +530,15 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     // bf16 with fp32 results: u in three parts, 24 bits (two leave y 1.8e-6 off, relative to its norm, three 3e-7)
     const int parts = type == MOE_BF16 && ytype == MOE_F32 ? 2 : 1;
     const int acc_stages = ytype == MOE_F32 ? 4 : 64;
-    rc = T <= LS_FEW ? shrink_few(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, parts, s)
-                     : shrink_many(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, parts, acc_stages, status, s);
-    if (rc != MOE_OK) return rc;
+    const int chunks = (rank + 31) / 32;
+    float *factor = (float *)((uint8_t *)workspace + (size_t)T * chunks * 128);  // (fp16: one part, half of the workspace)
     // few tokens, and no more rows of W than CTAs run at once (N = 2816: 1 token 12.1 -> 8.4 us, 32 tokens 20.2 -> 12.4 by the
     // kernel for few rows; N = 11264: 15.1 -> 14.9 and 21.1 -> 29.9)
     const bool few = T <= GF_MAX_R && (N + 15) / 16 <= 2 * grouped_sms();
+    const float below = ytype == MOE_F32 ? 65536.f : 0.125f;
+    rc = T <= LS_FEW ? shrink_few(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, few ? nullptr : factor, below, parts, s)
+                     : shrink_many(x, ldx, T, K, type, adapter, n_adapters, a, rank, scale, workspace, factor, below, parts, acc_stages, status, s);
+    if (rc != MOE_OK) return rc;
     if (few) {
         GroupedFewParams f = {};
         f.x = (const uint16_t *)x;
@@ -501,7 +563,6 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
         f.status = status;
         return grouped_few_launch(f, GP_LORA, type == MOE_BF16, moe_cuda_stream(s));
     }
-    const int chunks = (rank + 31) / 32;
     GroupedParams p = {};
     {
         const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, 1}, strides[2] = {(uint64_t)K * 2, (uint64_t)N * K * 2};
@@ -524,6 +585,8 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     p.ld = (size_t)chunks * parts * 64;
     p.parts = parts;
     p.lora_b = (const uint16_t *)b;
+    p.factor = factor;
+    p.factors = T <= LS_FEW ? chunks : 1;
     p.G = 1;
     p.R = T;
     p.x_rows = T;
@@ -543,6 +606,6 @@ extern "C" int moe_lora_matmul(const void *x, int type, int T, size_t ldx, const
     const bool wide = (T + 31) / 32 * ((N + 127) / 128) > grouped_sms();
     const int nt = !wide ? 32 : ytype == MOE_F32 ? 128 : 256;
     const long long tiles = (T + nt - 1) / nt;
-    return grouped_launch(p, ytype, GP_LORA, wide, tiles * ((N + 127) / 128), (K + 63) / 64 + std::min(T, n_adapters) * chunks * parts,
+    return grouped_launch(p, ytype, type == MOE_BF16 ? GP_LORA : GP_LORA_F16, wide, tiles * ((N + 127) / 128), (K + 63) / 64 + std::min(T, n_adapters) * chunks * parts,
                           moe_cuda_stream(s));
 }

@@ -1,5 +1,5 @@
 """The 16-bit products whose rows choose their matrix at their limits: offsets whose ranges overlap, infinite weights of
-adapters, empty groups, long reductions (GPU)."""
+adapters, empty groups, long reductions, small values of fp16 (GPU)."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -219,3 +219,61 @@ def test_fp32_sums_of_adapters(T, N, K, t, rank, alone):
         m = adapter == i
         want[m] += x[m].double() @ a[i].double().T @ b[i].double().T
     assert off(y, want) <= FP32_SUMS
+
+
+# ------------------------------------------------------------------------------ fp16's range between the adapter's two matrices
+
+def adapters_off(g, T, N, K, rank, out, xs=1.0, scale=None, bs=1.0, spread=0):
+    """fp16 adapters alone (the shared projection is zero).  spread: a's ranks and the tokens differ in size by powers of two."""
+    n = 3
+    x, w = rand(g, "f16", T, K, scale=xs), torch.zeros(N, K, dtype=torch.float16, device="cuda")
+    a, b = rand(g, "f16", n, rank, K, scale=K ** -0.5), rand(g, "f16", n, N, rank, scale=bs * rank ** -0.5)
+    if spread:
+        x *= 2.0 ** -(torch.arange(T, device="cuda") % 5)[:, None].half()
+        p = 2.0 ** -(torch.arange(rank, device="cuda") * spread // rank).half()  # ranks from 1 to 2^-spread, weighed back by b
+        a, b = a * p[:, None], b / p
+        assert bool(b.isfinite().all())
+    adapter = torch.arange(T, device="cuda").int() % (n + 1) - 1
+    d_scale = None if scale is None else torch.full((n,), scale, device="cuda")
+    y = lora(x, "f16", w, adapter, a.contiguous(), b.contiguous(), d_scale, out)
+    want = torch.zeros(T, N, dtype=torch.float64, device="cuda")
+    for i in range(n):
+        m = adapter == i
+        want[m] = (scale or 1.0) * (x[m].double() @ a[i].double().T) @ b[i].double().T
+    assert bool((y[adapter < 0] == 0).all())
+    rows = want.norm(dim=1).clamp_min(1e-300)  # every token by its own size
+    return off(y / rows[:, None], want / rows[:, None]), off(want.to(y.dtype) / rows[:, None], want / rows[:, None])
+
+
+FP16_PATHS = [(5, 64, 200), (30, 264, 2048), (7, 6400, 128), (31, 5128, 72), (50, 264, 2048), (300, 264, 520), (600, 1032, 2048),
+              (20000, 128, 2048)]
+
+
+@pytest.mark.parametrize("T,N,K", FP16_PATHS)
+@pytest.mark.parametrize("rank", [24, 64, 256])
+@pytest.mark.parametrize("xs,scale,bs", [(1.0, None, 1.0), (2.0 ** -7, None, 1.0), (2.0 ** -12, 8.0, 64.0), (1.0, 2.0 ** -12, 2.0 ** 10),
+                                         (1.0, 1e-20, 1.0), (8.0, 2.0 ** 9, 2.0 ** -4)])
+def test_fp16_adapters_keep_their_bits_at_every_size(T, N, K, rank, xs, scale, bs):
+    """u from 1e-20 to thousands: 22 bits (2^-23 of a value at most, a fifth of the sums' allowance) and the sums."""
+    assert adapters_off(gen(T + rank), T, N, K, rank, "f32", xs, scale, bs)[0] <= FP32_SUMS
+
+
+@pytest.mark.parametrize("T,N,K", FP16_PATHS)
+@pytest.mark.parametrize("rank", [24, 64, 256])
+@pytest.mark.parametrize("spread", [6, 10])
+def test_fp16_adapters_of_ranks_of_many_sizes(T, N, K, rank, spread):
+    """Ranks whose u differs by 2^10 and counts alike, tokens that differ by 2^4."""
+    assert adapters_off(gen(T + rank), T, N, K, rank, "f32", spread=spread)[0] <= FP32_SUMS
+
+
+@pytest.mark.parametrize("T,N,K", FP16_PATHS)
+@pytest.mark.parametrize("rank", [24, 256])
+@pytest.mark.parametrize("out", ["f16", "bf16"])
+@pytest.mark.parametrize("scale,bs,spread", [(2.0 ** -12, 2.0 ** 10, 0), (None, 1.0, 0), (0.25, 1.0, 10), (2.0 ** -9, 1.0, 10)])
+def test_fp16_adapters_small_between_the_matrices_of_16_bit_results(T, N, K, rank, out, scale, bs, spread):
+    """The sums' 6e-6 (u of long reductions: as much) are not seen beside the rounding (2e-4), nor is what u's smaller ranks lose beside
+    a largest one of 1/8 or more: 2^-25 each at most, 1.7e-8 on average, weighed back by 1 to 2^9, 187 on average: 3.2e-6 over the
+    size of u's first ranks, which is 1/4, 1/8 or 1/16 for three tokens in five (the others come by a power of two): 2.7e-5 on
+    average over the tokens, in quadrature 0.9 percent of the rounding."""
+    e, least = adapters_off(gen(T + rank), T, N, K, rank, out, 1.0, scale, bs, spread)
+    assert e <= 1.01 * least
