@@ -277,3 +277,102 @@ def test_fp16_adapters_small_between_the_matrices_of_16_bit_results(T, N, K, ran
     average over the tokens, in quadrature 0.9 percent of the rounding."""
     e, least = adapters_off(gen(T + rank), T, N, K, rank, out, 1.0, scale, bs, spread)
     assert e <= 1.01 * least
+
+
+# ------------------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("T,N,K", [(20, 64, 16384), (40, 136, 16384), (600, 1032, 16392), (600, 520, 40000)])
+@pytest.mark.parametrize("t,out", [("f16", "f16"), ("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("scale", [None, 2.0 ** -12])
+def test_adapters_of_long_reductions_beside_their_projection(T, N, K, t, out, scale):
+    """More than one accumulator for the projection, with and without the adapters' own, and tokens of zeros."""
+    g, n, rank = gen(T), 3, 72
+    x, w = rand(g, t, T, K), rand(g, t, N, K, scale=K ** -0.5)
+    x[::7] = 0.0
+    a, b = rand(g, t, n, rank, K, scale=K ** -0.5), rand(g, t, n, N, rank, scale=rank ** -0.5 / (scale or 1.0) / 8)
+    adapter = torch.arange(T, device="cuda").int() % (n + 1) - 1
+    y = lora(x, t, w, adapter, a, b, None if scale is None else torch.full((n,), scale, device="cuda"), out)
+    want = x.double() @ w.double().T
+    for i in range(n):
+        m = adapter == i
+        want[m] += (scale or 1.0) * (x[m].double() @ a[i].double().T) @ b[i].double().T
+    assert bool((y[::7] == 0).all())
+    e, least = off(y, want), off(want.to(y.dtype), want)
+    assert e <= (FP32_SUMS if out == "f32" else 1.01 * least)
+
+
+@pytest.mark.parametrize("T,N,K,rank", [(1, 64, 128, 16), (30, 264, 256, 64), (50, 264, 128, 64), (700, 520, 256, 48)])
+@pytest.mark.parametrize("out", ["f16", "f32"])
+def test_fp16_adapters_captured_and_on_two_streams(T, N, K, rank, out):
+    """The same bits again, replayed, and beside another call on another stream, of large and of small u."""
+    calls = []
+    for seed, xs in ((1, 1.0), (2, 2.0 ** -9)):
+        g, n = gen(seed), 3
+        x, w = rand(g, "f16", T, K, scale=xs), rand(g, "f16", N, K, scale=K ** -0.5)
+        a, b = rand(g, "f16", n, rank, K, scale=K ** -0.5), rand(g, "f16", n, N, rank, scale=rank ** -0.5)
+        adapter = torch.randint(-1, n, (T,), generator=g, device="cuda").int()
+        y, ws = torch.zeros(T, N, dtype=ref.dtype(out), device="cuda"), torch.empty(L.moe_lora_workspace(T, rank), dtype=torch.uint8,
+                                                                                 device="cuda")
+
+        def call(stream=None, v=(x, w, adapter, a, b, y, ws)):
+            x, w, adapter, a, b, y, ws = v
+            L.moe_lora_matmul(x, L.MOE_F16, T, K, w, N, K, adapter, 3, a, b, rank, None, y, ref.code(out), N, ws, ws.numel(), stream)
+
+        call()
+        torch.cuda.synchronize()
+        want = y.clone()
+        gr, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(gr, stream=side):
+            call()
+        for _ in range(3):
+            y.zero_()
+            ws.fill_(0xFF)
+            gr.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+        calls.append((call, gr, y, want, torch.cuda.Stream()))
+    for _, _, y, _, _ in calls:
+        y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for call, gr, _, _, st in calls:
+            call(st)
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for _, _, y, want, _ in calls)
+
+
+def test_long_groups_captured_and_on_two_streams():
+    """Accumulators that are folded on the way: the same bits again, replayed and beside another call."""
+    g, o = gen(4), [0, 20000, 20010, 20010, 41000]
+    G, R, N, K = 4, 41000, 264, 136
+    x, dy, w = rand(g, "bf16", R, K), rand(g, "bf16", R, N), rand(g, "bf16", G, K, N, scale=N ** -0.5)
+    xl, wl = rand(g, "bf16", 300, 8200), rand(g, "bf16", G, N, 8200, scale=8200 ** -0.5)
+    d_off, l_off = torch.tensor(o, dtype=torch.int32, device="cuda"), torch.tensor([0, 100, 101, 101, 300], dtype=torch.int32, device="cuda")
+    outs = [torch.zeros(G, N, K, device="cuda"), torch.zeros(G, N, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(300, N, device="cuda"),
+            torch.zeros(300, N // 2 // 8 * 8, device="cuda")]
+    grads = [lambda s=None: L.moe_grouped_weight_grad(x, 1, R, K, None, 1, dy, R, N, None, d_off, G, R, N, K, 0, outs[0], 0, s),
+             lambda s=None: L.moe_grouped_weight_grad(x, 1, R, K, None, 1, dy, R, N, None, d_off, G, R, N, K, 0, outs[1], 1, s)]
+    products = [lambda s=None: L.moe_grouped_matmul(xl, 1, 300, 8200, None, 1, l_off, G, 300, wl, 0, N, 8200, 0, None, None, outs[2], 0, 300, N, s),
+                lambda s=None: L.moe_grouped_matmul(xl, 1, 300, 8200, None, 1, l_off, G, 300, wl, 0, N // 2 // 8 * 8, 8200, 1, None, None, outs[3],
+                                                    0, 300, N // 2 // 8 * 8, s)]
+    for f in grads + products:
+        f()
+    torch.cuda.synchronize()
+    want = [v.clone() for v in outs]
+    gr, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(gr, stream=side):
+        for f in products:
+            f()
+    for v in outs:
+        v.zero_()
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(4):
+        for f in grads:
+            f(one)
+        with torch.cuda.stream(two):
+            gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
