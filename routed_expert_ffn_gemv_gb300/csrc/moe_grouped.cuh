@@ -27,7 +27,8 @@
 //                take about 40 ns each however many are in flight: 32768 rows of 2048 gathered for 1536
 //                outputs took 510 us.)
 // Two shapes (see moe_grouped_matmul for the rule): NT = 32, one CTA an item, for few rows, when reading the matrix is
-// the work (77 tokens over 64 experts of 2 x 1408 x 2048: 86 us, HBM's rate); NT = 256 (fp32 results 128 or 64) by pairs of CTAs, when it
+// the work (77 tokens over 64 experts of 2 x 1408 x 2048: 86 us, HBM's rate); NT = 256 (fp32 results 128, but for the gradient
+// of short groups) by pairs of CTAs, when it
 // is the MMAs (8192^3: 631 us, 1743 TFLOP/s; by single CTAs, which load twice as much, a prompt's gate/up product took
 // 1.7 times as long).
 // CG = 1: where items are few, the CTAs of a cluster share an item's reduction and add their sums up over distributed shared
