@@ -112,7 +112,8 @@ __global__ void __launch_bounds__(256) lora_shrink_kernel(const uint16_t *x, siz
         __syncthreads();
         for (int w = 0; w < 8; ++w) m = fmaxf(m, most[w]);
         power16(m, below, up, down);
-        if (threadIdx.x == 0) factor[(size_t)t * chunks + j0 / 32] = down;
+        // (32 ranks of zeros: the smallest, which is none of the token's other ranks' largest)
+        if (threadIdx.x == 0) factor[(size_t)t * chunks + j0 / 32] = m > 0.f ? down : 0x1p-100f;
     }
     if (lane < LS_RANKS) {
         float r = 0.f;

@@ -267,6 +267,28 @@ def test_fp16_adapters_of_ranks_of_many_sizes(T, N, K, rank, spread):
 
 
 @pytest.mark.parametrize("T,N,K", FP16_PATHS)
+@pytest.mark.parametrize("empty", [[0], [1], [0, 2]])
+@pytest.mark.parametrize("out", ["f32", "f16"])
+def test_fp16_adapters_with_ranks_of_zeros(T, N, K, empty, out):
+    """Adapters of a smaller rank than the table's: 32 ranks of zeros say nothing about the size of the others."""
+    g, n, rank = gen(T), 3, 96
+    x, w = rand(g, "f16", T, K, scale=2.0 ** -9), torch.zeros(N, K, dtype=torch.float16, device="cuda")
+    a, b = rand(g, "f16", n, rank, K, scale=K ** -0.5), rand(g, "f16", n, N, rank, scale=2.0 ** 9 * rank ** -0.5)
+    for c in empty:
+        a[1:, 32 * c:32 * c + 32] = 0.0
+    adapter = torch.arange(T, device="cuda").int() % n
+    d_scale = torch.tensor([1.0, 2.0 ** -8, 1.0], device="cuda")
+    y = lora(x, "f16", w, adapter, a, b, d_scale, out)
+    want = torch.zeros(T, N, dtype=torch.float64, device="cuda")
+    for i in range(n):
+        m = adapter == i
+        want[m] = float(d_scale[i]) * (x[m].double() @ a[i].double().T) @ b[i].double().T
+    rows = want.norm(dim=1, keepdim=True)
+    e, least = off(y / rows, want / rows), off(want.to(y.dtype) / rows, want / rows)
+    assert e <= (FP32_SUMS if out == "f32" else 1.01 * least)
+
+
+@pytest.mark.parametrize("T,N,K", FP16_PATHS)
 @pytest.mark.parametrize("rank", [24, 256])
 @pytest.mark.parametrize("out", ["f16", "bf16"])
 @pytest.mark.parametrize("scale,bs,spread", [(2.0 ** -12, 2.0 ** 10, 0), (None, 1.0, 0), (0.25, 1.0, 10), (2.0 ** -9, 1.0, 10)])
